@@ -20,11 +20,18 @@ runs the chain from them.
 
 ConvBwdData(problem, dtype) is the input gradient of a forward problem,
 ConvBwdWeight(problem) its weight gradient (bf16).
+
+CausalConv(problem, dtype, has_bias, silu) is the short causal depthwise
+convolution of a sequence model and SelectiveScan(problem, dtype) the state
+space scan behind it; both run over prompts (ragged batches, states in and
+out), token by token (.step) and backwards (.backward).
 """
 from . import capi
 from .capi import ConvError  # noqa: F401
+from .sequence import CausalConv, SelectiveScan  # noqa: F401
 
-__all__ = ["ConvFwd", "ConvChain", "ConvBwdData", "ConvBwdWeight", "ConvError", "capi", "desc_from_problem"]
+__all__ = ["ConvFwd", "ConvChain", "ConvBwdData", "ConvBwdWeight", "CausalConv", "SelectiveScan", "ConvError", "capi",
+           "desc_from_problem"]
 
 
 def _ndim(p):

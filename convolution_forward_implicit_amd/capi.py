@@ -36,6 +36,13 @@ EXPORTED = ["conv_fwd_create", "conv_fwd_create_with_config", "conv_fwd_out_dims
             "conv_bwd_weight_describe"]
 
 
+# the sequence operators: the causal convolution and the selective scan
+SEQUENCE_EXPORTED = ["conv_causal_create", "conv_causal_run", "conv_causal_step", "conv_causal_bwd_workspace_bytes",
+                     "conv_causal_bwd_run", "conv_causal_destroy", "conv_causal_describe",
+                     "conv_scan_create", "conv_scan_workspace_bytes", "conv_scan_run", "conv_scan_step",
+                     "conv_scan_bwd_workspace_bytes", "conv_scan_bwd_run", "conv_scan_destroy", "conv_scan_describe"]
+
+
 class conv_fwd_desc_t(ctypes.Structure):
     _fields_ = [("ndim", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("N", ctypes.c_int64), ("G", ctypes.c_int64),
@@ -44,6 +51,40 @@ class conv_fwd_desc_t(ctypes.Structure):
                 ("stride", ctypes.c_int64 * 3), ("pad", ctypes.c_int64 * 3),
                 ("dilation", ctypes.c_int64 * 3),
                 ("has_bias", ctypes.c_int32), ("gelu", ctypes.c_int32)]
+
+
+class conv_causal_desc_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("dtype", "has_bias", "silu", "reserved")] +
+                [(n, ctypes.c_int64) for n in ("N", "L", "C", "F")])
+
+
+class conv_causal_args_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "w", "bias", "state", "lengths", "y", "state_out")] +
+                [(n, ctypes.c_int64) for n in ("x_ld", "y_ld")])
+
+
+class conv_causal_bwd_args_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("dy", "x", "w", "bias", "state", "lengths", "dstate_out",
+                                                  "dx", "dw", "dbias", "dstate")] +
+                [(n, ctypes.c_int64) for n in ("dy_ld", "x_ld", "dx_ld")])
+
+
+class conv_scan_desc_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("dtype", "softplus")] +
+                [(n, ctypes.c_int64) for n in ("N", "L", "H", "P", "G", "S")])
+
+
+class conv_scan_args_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "dt", "a", "b", "c", "d", "dt_bias",
+                                                  "state", "lengths", "y", "state_out")] +
+                [(n, ctypes.c_int64) for n in ("x_ld", "dt_ld", "b_ld", "c_ld", "y_ld")])
+
+
+class conv_scan_bwd_args_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("dy", "x", "dt", "a", "b", "c", "d",
+                                                  "dt_bias", "state", "lengths", "dstate_out", "dx", "ddt", "da",
+                                                  "db", "dc", "dd", "ddt_bias", "dstate")] +
+                [(n, ctypes.c_int64) for n in ("dy_ld", "x_ld", "dt_ld", "b_ld", "c_ld", "dx_ld", "ddt_ld", "db_ld", "dc_ld")])
 
 
 class ConvError(RuntimeError):
@@ -144,6 +185,20 @@ def lib():
         L.conv_bwd_weight_destroy.restype = None
         L.conv_bwd_weight_describe.argtypes = [P]
         L.conv_bwd_weight_describe.restype = ctypes.c_char_p
+        I64 = ctypes.c_int64
+        for name, desc, args, bwd in (("causal", conv_causal_desc_t, conv_causal_args_t, conv_causal_bwd_args_t),
+                                      ("scan", conv_scan_desc_t, conv_scan_args_t, conv_scan_bwd_args_t)):
+            f = lambda what: getattr(L, "conv_%s_%s" % (name, what))
+            f("create").argtypes = [ctypes.POINTER(desc), ctypes.POINTER(P)]
+            f("run").argtypes = [P, ctypes.POINTER(args), P] if name == "causal" else [P, ctypes.POINTER(args), P, I64, P]
+            f("step").argtypes = [P, ctypes.POINTER(args), P]
+            f("bwd_workspace_bytes").argtypes = [P, ctypes.POINTER(I64)]
+            f("bwd_run").argtypes = [P, ctypes.POINTER(bwd), P, I64, P]
+            f("destroy").argtypes = [P]
+            f("destroy").restype = None
+            f("describe").argtypes = [P]
+            f("describe").restype = ctypes.c_char_p
+        L.conv_scan_workspace_bytes.argtypes = [P, ctypes.POINTER(I64)]
         _lib = L
     return _lib
 
@@ -397,3 +452,74 @@ def conv_probe_hbm_read(buf, nbytes, grid, sink, stream=0):
     rc = probe_lib().conv_probe_hbm_read(buf, int(nbytes), int(grid), sink, stream)
     if rc != 0:
         raise RuntimeError("conv_probe_hbm_read failed: hipError %d" % rc)
+
+
+# ---- the sequence operators: args are the ctypes structures above ------------
+def conv_causal_create(desc):
+    plan = ctypes.c_void_p()
+    _check(lib().conv_causal_create(ctypes.byref(desc), ctypes.byref(plan)))
+    return plan.value
+
+
+def conv_causal_run(plan, args, stream=0):
+    _check(lib().conv_causal_run(plan, args, stream))
+
+
+def conv_causal_step(plan, args, stream=0):
+    _check(lib().conv_causal_step(plan, args, stream))
+
+
+def conv_causal_bwd_workspace_bytes(plan):
+    n = ctypes.c_int64()
+    _check(lib().conv_causal_bwd_workspace_bytes(plan, ctypes.byref(n)))
+    return n.value
+
+
+def conv_causal_bwd_run(plan, args, workspace, workspace_bytes, stream=0):
+    _check(lib().conv_causal_bwd_run(plan, args, workspace, workspace_bytes, stream))
+
+
+def conv_causal_destroy(plan):
+    lib().conv_causal_destroy(plan)
+
+
+def conv_causal_describe(plan):
+    return lib().conv_causal_describe(plan).decode()
+
+
+def conv_scan_create(desc):
+    plan = ctypes.c_void_p()
+    _check(lib().conv_scan_create(ctypes.byref(desc), ctypes.byref(plan)))
+    return plan.value
+
+
+def conv_scan_workspace_bytes(plan):
+    n = ctypes.c_int64()
+    _check(lib().conv_scan_workspace_bytes(plan, ctypes.byref(n)))
+    return n.value
+
+
+def conv_scan_run(plan, args, workspace, workspace_bytes, stream=0):
+    _check(lib().conv_scan_run(plan, args, workspace, workspace_bytes, stream))
+
+
+def conv_scan_step(plan, args, stream=0):
+    _check(lib().conv_scan_step(plan, args, stream))
+
+
+def conv_scan_bwd_workspace_bytes(plan):
+    n = ctypes.c_int64()
+    _check(lib().conv_scan_bwd_workspace_bytes(plan, ctypes.byref(n)))
+    return n.value
+
+
+def conv_scan_bwd_run(plan, args, workspace, workspace_bytes, stream=0):
+    _check(lib().conv_scan_bwd_run(plan, args, workspace, workspace_bytes, stream))
+
+
+def conv_scan_destroy(plan):
+    lib().conv_scan_destroy(plan)
+
+
+def conv_scan_describe(plan):
+    return lib().conv_scan_describe(plan).decode()

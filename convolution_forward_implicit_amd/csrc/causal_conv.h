@@ -1,0 +1,296 @@
+// The short causal depthwise convolution over a sequence, its gradient and its
+// single-token step.
+//
+//   v[n,t,c] = b[c] + sum_{k<F} w[c,k] h[n, t-(F-1)+k, c]
+//   y = v (1 / (1 + e^-v)) or v,        h[t] = x[t], and the state's rows for t < 0
+//
+// The work is 2F flop for two elements moved: every kernel is bound by HBM.
+// A thread owns V neighbouring channels (16 bytes) of a run of tokens and
+// keeps the last F - 1 of them in registers, so each input row is fetched once
+// per run and F - 1 rows again at its start; neighbouring threads take
+// neighbouring channels, so a wave's accesses are whole lines.
+#pragma once
+
+#include "seq_common.h"
+
+namespace convfwd {
+
+struct CausalParams {
+    const void *x, *w, *bias, *state;
+    const int32_t *lengths;
+    void *y, *state_out;
+    int64_t x_ld, y_ld;       // elements from one token to the next
+    int N, C, CV;             // CV: channel vectors of a token
+    int64_t L;
+    int64_t blocks;           // token runs of a sequence
+    // gradient
+    const void *dy, *dstate_out;
+    void *dx, *dstate;
+    float *partial;           // [N * groups of runs][F + 1][C]
+    int64_t dy_ld, dx_ld;
+};
+
+constexpr int kConvRun = 8;       // tokens of one thread's run, forward
+constexpr int kConvBwdRun = 16;   // tokens of one thread's run, gradient
+constexpr int kConvBwdCv = 32;    // channel vectors and runs of a gradient workgroup
+constexpr int kConvBwdRuns = 8;
+
+// h[n, t] for V channels: a token inside the sequence, a row of the state, or zero
+template <typename T, int F, int V>
+SEQ_DEV void conv_history(const CausalParams &p, int64_t n, int64_t t, int64_t len, int c, float (&v)[V])
+{
+    if (t >= 0 && t < len) {
+        load_f32<T, V>((const T *)p.x + (n * p.L + t) * p.x_ld + c, v);
+    } else if (t < 0 && p.state) {
+        load_f32<T, V>((const T *)p.state + (n * (F - 1) + (F - 1 + t)) * p.C + c, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = 0.0f;
+    }
+}
+
+template <typename T, int F, int V> SEQ_DEV void conv_weights(const CausalParams &p, int c, float (&w)[F][V])
+{
+    const T *q = (const T *)p.w + (int64_t)c * F;
+    float raw[F * V];
+    if constexpr (V == 1) {
+#pragma unroll
+        for (int k = 0; k < F; ++k) raw[k] = (float)q[k];
+    } else {
+#pragma unroll
+        for (int k = 0; k < F; ++k) {
+            float part[V];
+            load_f32<T, V>(q + k * V, part);
+#pragma unroll
+            for (int i = 0; i < V; ++i) raw[k * V + i] = part[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int k = 0; k < F; ++k) w[k][i] = raw[i * F + k];
+}
+
+// One thread: V channels of kConvRun tokens, or (run == blocks) the state that
+// the sequence leaves behind.
+template <typename T, int F, int V, bool SILU>
+__global__ void __launch_bounds__(256) causal_conv_kernel(CausalParams p)
+{
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t runs = p.blocks + (p.state_out ? 1 : 0);
+    const int64_t row = id / p.CV;
+    if (row >= p.N * runs) return;
+    const int c = (int)(id - row * p.CV) * V;
+    const int64_t n = row / runs, run = row - n * runs;
+    const int64_t len = seq_len(p.lengths, n, p.L);
+    if (run == p.blocks) {
+#pragma unroll
+        for (int j = 0; j < F - 1; ++j) {
+            float v[V];
+            conv_history<T, F, V>(p, n, len - (F - 1) + j, len, c, v);
+            store_f32<T, V>((T *)p.state_out + (n * (F - 1) + j) * p.C + c, v);
+        }
+        return;
+    }
+    const int64_t t0 = run * kConvRun;
+    float h[F - 1 + kConvRun][V];
+#pragma unroll
+    for (int e = 0; e < F - 1 + kConvRun; ++e) conv_history<T, F, V>(p, n, t0 - (F - 1) + e, len, c, h[e]);
+    float w[F][V], b[V];
+    conv_weights<T, F, V>(p, c, w);
+#pragma unroll
+    for (int i = 0; i < V; ++i) b[i] = 0.0f;
+    if (p.bias) load_f32<T, V>((const T *)p.bias + c, b);
+#pragma unroll
+    for (int u = 0; u < kConvRun; ++u) {
+        if (t0 + u >= p.L) break;
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float v = b[i];
+#pragma unroll
+            for (int k = 0; k < F; ++k) v = fmaf(w[k][i], h[u + k][i], v);
+            o[i] = t0 + u < len ? (SILU ? v * sigmoid(v) : v) : 0.0f;
+        }
+        store_f32<T, V>((T *)p.y + (n * p.L + t0 + u) * p.y_ld + c, o);
+    }
+}
+
+// One token of every sequence: y from the state and x, and the state moved on
+// by one row.  A thread owns its channels of the state, so it may be updated
+// in place.
+template <typename T, int F, int V, bool SILU>
+__global__ void __launch_bounds__(256) causal_step_kernel(CausalParams p)
+{
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t n = id / p.CV;
+    if (n >= p.N) return;
+    const int c = (int)(id - n * p.CV) * V;
+    float h[F][V], w[F][V], o[V];
+#pragma unroll
+    for (int j = 0; j < F - 1; ++j) load_f32<T, V>((const T *)p.state + (n * (F - 1) + j) * p.C + c, h[j]);
+    load_f32<T, V>((const T *)p.x + n * p.x_ld + c, h[F - 1]);
+    conv_weights<T, F, V>(p, c, w);
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = 0.0f;
+    if (p.bias) load_f32<T, V>((const T *)p.bias + c, o);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int k = 0; k < F; ++k) o[i] = fmaf(w[k][i], h[k][i], o[i]);
+        if (SILU) o[i] *= sigmoid(o[i]);
+    }
+    store_f32<T, V>((T *)p.y + n * p.y_ld + c, o);
+#pragma unroll
+    for (int j = 0; j < F - 1; ++j) store_f32<T, V>((T *)p.state_out + (n * (F - 1) + j) * p.C + c, h[j + 1]);
+}
+
+// d v[n,t] = dy act'(v), zero outside the sequence
+template <typename T, int F, int V, bool SILU>
+SEQ_DEV void conv_dv(const CausalParams &p, int64_t n, int64_t t, int64_t len, int c, const float (&w)[F][V],
+                     const float (&b)[V], const float (*h)[V], float (&d)[V])
+{
+    if (t < 0 || t >= len) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = 0.0f;
+        return;
+    }
+    load_f32<T, V>((const T *)p.dy + (n * p.L + t) * p.dy_ld + c, d);
+    if (SILU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float v = b[i];
+#pragma unroll
+            for (int k = 0; k < F; ++k) v = fmaf(w[k][i], h[k][i], v);
+            const float s = sigmoid(v);
+            d[i] *= s * (1.0f + v * (1.0f - s));
+        }
+    }
+}
+
+// The gradient: with d = dy act'(v),
+//   dh[s] = sum_k w[k] d[s + (F-1) - k],   dw[k] = sum_t d[t] h[t-(F-1)+k],   db = sum_t d[t].
+// A thread recomputes v for its run and the F - 1 tokens behind it (d of those
+// reaches back into the run), keeps its sums of dw and db in fp32 registers,
+// and the workgroup adds its runs in LDS, in a fixed order; causal_reduce_kernel
+// adds the workgroups' rows, in a fixed order too.
+template <typename T, int F, int V, bool SILU>
+__global__ void __launch_bounds__(256) causal_bwd_kernel(CausalParams p)
+{
+    __shared__ float part[kConvBwdRuns][kConvBwdCv * V];
+    const int cb = (p.CV + kConvBwdCv - 1) / kConvBwdCv;
+    const int64_t blk = blockIdx.x / cb;
+    const int cvi = threadIdx.x & (kConvBwdCv - 1), ri = threadIdx.x / kConvBwdCv;
+    const int cv = (int)(blockIdx.x - blk * cb) * kConvBwdCv + cvi;
+    const int64_t n = blk / p.blocks, run = (blk - n * p.blocks) * kConvBwdRuns + ri;
+    const bool live = cv < p.CV;
+    const int c = cv * V;
+    const int64_t len = seq_len(p.lengths, n, p.L), t0 = run * kConvBwdRun;
+    float w[F][V], b[V], dw[F][V], db[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        db[i] = b[i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < F; ++k) dw[k][i] = w[k][i] = 0.0f;
+    }
+    if (live && (t0 < p.L || t0 == 0)) {
+        conv_weights<T, F, V>(p, c, w);
+        if (p.bias) load_f32<T, V>((const T *)p.bias + c, b);
+        float h[F][V];             // h[t-(F-1)] .. h[t]
+        float d[F][V];             // d[t-(F-1)] .. d[t]
+#pragma unroll
+        for (int k = 0; k < F - 1; ++k) {
+            conv_history<T, F, V>(p, n, t0 - (F - 1) + k, len, c, h[k]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) d[k][i] = 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < kConvBwdRun + F - 1; ++u) {
+            const int64_t t = t0 + u;
+            conv_history<T, F, V>(p, n, t, len, c, h[F - 1]);
+            conv_dv<T, F, V, SILU>(p, n, t, len, c, w, b, h, d[F - 1]);
+            if (u < kConvBwdRun) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    db[i] += d[F - 1][i];
+#pragma unroll
+                    for (int k = 0; k < F; ++k) dw[k][i] = fmaf(d[F - 1][i], h[k][i], dw[k][i]);
+                }
+            }
+            // dh at s = t - (F-1), once d[s .. s+F-1] is known
+            const int64_t s = t - (F - 1);
+            if (u >= F - 1 || (t0 == 0 && p.dstate)) {
+                float g[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    g[i] = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < F; ++k) g[i] = fmaf(w[k][i], d[F - 1 - k][i], g[i]);
+                }
+                const int64_t j = s - (len - (F - 1));     // the row of state_out that h[s] became
+                if (p.dstate_out && j >= 0 && j < F - 1) {
+                    float q[V];
+                    load_f32<T, V>((const T *)p.dstate_out + (n * (F - 1) + j) * p.C + c, q);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) g[i] += q[i];
+                }
+                if (s < 0) {
+                    store_f32<T, V>((T *)p.dstate + (n * (F - 1) + (F - 1 + s)) * p.C + c, g);
+                } else if (s < p.L && u >= F - 1) {
+                    if (s >= len)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) g[i] = 0.0f;
+                    store_f32<T, V>((T *)p.dx + (n * p.L + s) * p.dx_ld + c, g);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < F - 1; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    h[k][i] = h[k + 1][i];
+                    d[k][i] = d[k + 1][i];
+                }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k <= F; ++k) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < V; ++i) part[ri][cvi * V + i] = k < F ? dw[k < F ? k : 0][i] : db[i];
+        __syncthreads();
+        for (int e = threadIdx.x; e < kConvBwdCv * V; e += 256) {
+            const int ch = (int)(blockIdx.x - blk * cb) * kConvBwdCv * V + e;
+            if (ch >= p.C) continue;
+            float sum = 0.0f;
+#pragma unroll
+            for (int r = 0; r < kConvBwdRuns; ++r) sum += part[r][e];
+            p.partial[(blk * (F + 1) + k) * p.C + ch] = sum;
+        }
+    }
+}
+
+// dw[c][k] and db[c] from the workgroups' rows: 64 channels x 4 slices of the rows
+template <typename T>
+__global__ void __launch_bounds__(256) causal_reduce_kernel(const float *partial, T *dw, T *db, int64_t rows, int C,
+                                                            int F)
+{
+    __shared__ float part[4][64];
+    const int cb = (C + 63) / 64;
+    const int k = blockIdx.x / cb, c = (blockIdx.x - k * cb) * 64 + (threadIdx.x & 63), r = threadIdx.x / 64;
+    float s = 0.0f;
+    if (c < C) {
+        const float *q = partial + (int64_t)k * C + c;
+        const int64_t step = (int64_t)(F + 1) * C;
+#pragma unroll 8
+        for (int64_t i = r; i < rows; i += 4) s += q[i * step];
+    }
+    part[r][threadIdx.x & 63] = s;
+    __syncthreads();
+    if (r == 0 && c < C) {
+        s = (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
+        if (k < F) dw[(int64_t)c * F + k] = (T)s;
+        else if (db) db[c] = (T)s;
+    }
+}
+
+}  // namespace convfwd

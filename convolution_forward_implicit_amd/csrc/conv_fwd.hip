@@ -31,11 +31,14 @@
 #include "chain_packed.h"
 #include "bwd_kernels.h"
 #include "weight_pack.h"
+#include "status.h"
 
 namespace convfwd {
 namespace {
 
 thread_local char g_err[512] = "";
+
+}  // namespace
 
 conv_status_t fail(conv_status_t st, const char *fmt, ...)
 {
@@ -45,6 +48,8 @@ conv_status_t fail(conv_status_t st, const char *fmt, ...)
     va_end(ap);
     return st;
 }
+
+namespace {
 
 typedef void (*launch_fn)(const KParams &, uint32_t x_bytes, uint32_t w_bytes, int grid, hipStream_t,
                           hipEvent_t start, hipEvent_t stop);

@@ -1,0 +1,635 @@
+// Host side of the sequence operators (conv_causal_*, conv_scan_*): argument
+// checks, the choice of kernel variants and splits, launches.
+#include <algorithm>
+#include <cstdio>
+#include <cstdlib>
+#include <new>
+
+#include "../../include/convfwd.h"
+#include "causal_conv.h"
+#include "scan_kernels.h"
+#include "status.h"
+
+struct conv_causal_plan {
+    conv_causal_desc_t desc;
+    int64_t esz, ws_bytes, bwd_rows;     // bwd_rows: workgroup rows of partial sums
+    char text[256];
+};
+
+struct conv_scan_plan {
+    conv_scan_desc_t desc;
+    int64_t esz;
+    int SP, Q, K, NPB;                   // padded states, chunk, chunks, channel blocks
+    int64_t units;                       // N * H * NPB
+    int nseg, seg;                       // forward segments and their chunks
+    int bnseg, bseg;                     // the same of the gradient's state passes
+    int slices, heads_per_slice;
+    int64_t ws_bytes, bwd_ws_bytes;
+    int64_t o_log, o_bound, o_ubound, o_head, o_pb, o_pc;   // byte offsets in the gradient's workspace
+    char text[320];
+};
+
+namespace convfwd {
+namespace {
+
+constexpr int64_t kMaxDim = int64_t(1) << 30;
+constexpr double kMaxBytes = 9.0e18;
+
+conv_status_t launched()
+{
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? CONV_OK : fail(CONV_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
+}
+
+// A tensor as `rows` runs of `width` elements, `ld` apart.
+struct Rows {
+    const char *name;
+    const void *p;
+    int64_t rows, width, ld, esz;
+};
+
+bool share_memory(const Rows &a, const Rows &b)
+{
+    if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+    const int64_t a0 = (int64_t)(uintptr_t)a.p, b0 = (int64_t)(uintptr_t)b.p;
+    const int64_t a1 = a0 + ((a.rows - 1) * a.ld + a.width) * a.esz, b1 = b0 + ((b.rows - 1) * b.ld + b.width) * b.esz;
+    if (a1 <= b0 || b1 <= a0) return false;
+    const int64_t step = a.ld * a.esz;
+    if (step != b.ld * b.esz) return true;
+    // equal strides: column ranges of one matrix, disjoint iff the runs are, modulo the stride
+    int64_t d = (b0 - a0) % step;
+    if (d < 0) d += step;
+    return d < a.width * a.esz || d + b.width * b.esz > step;
+}
+
+// Every output against every input and the outputs before it.
+conv_status_t check_overlap(const Rows *out, int nout, const Rows *in, int nin)
+{
+    for (int i = 0; i < nout; ++i) {
+        for (int j = 0; j < nin; ++j)
+            if (share_memory(out[i], in[j])) return fail(CONV_ERR_INVALID_ARG, "%s overlaps %s", out[i].name, in[j].name);
+        for (int j = 0; j < i; ++j)
+            if (share_memory(out[i], out[j]))
+                return fail(CONV_ERR_INVALID_ARG, "%s overlaps %s", out[i].name, out[j].name);
+    }
+    return CONV_OK;
+}
+
+// Alignment of every tensor to its elements, and token strides that hold a row.
+conv_status_t check_rows(const Rows *t, int n)
+{
+    for (int i = 0; i < n; ++i) {
+        if (t[i].p && (uintptr_t)t[i].p % t[i].esz)
+            return fail(CONV_ERR_INVALID_ARG, "%s is not aligned to its elements", t[i].name);
+        if (t[i].ld < t[i].width)
+            return fail(CONV_ERR_INVALID_ARG, "%s: %lld elements from token to token, a row has %lld", t[i].name,
+                        (long long)t[i].ld, (long long)t[i].width);
+        if ((double)t[i].ld * t[i].esz * std::max<int64_t>(1, t[i].rows) > kMaxBytes)
+            return fail(CONV_ERR_UNSUPPORTED, "%s: beyond the address space", t[i].name);
+    }
+    return CONV_OK;
+}
+
+bool vector_rows(const Rows &t) { return !t.p || ((uintptr_t)t.p % 16 == 0 && t.ld * t.esz % 16 == 0); }
+
+int64_t or_packed(int64_t ld, int64_t width) { return ld == 0 ? width : ld; }
+
+conv_status_t check_workspace(const void *ws, int64_t bytes, int64_t need)
+{
+    if (need == 0) return CONV_OK;
+    if (!ws) return fail(CONV_ERR_INVALID_ARG, "workspace is NULL");
+    if (bytes < need)
+        return fail(CONV_ERR_INVALID_ARG, "workspace has %lld bytes, the plan needs %lld", (long long)bytes, (long long)need);
+    if ((uintptr_t)ws % 16) return fail(CONV_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    return CONV_OK;
+}
+
+// ---- causal convolution --------------------------------------------------------
+enum ConvKernel { CONV_RUN, CONV_STEP, CONV_BWD };
+
+template <typename T, int F, int V, bool SILU>
+void launch_causal(ConvKernel which, const CausalParams &p, int64_t grid, hipStream_t s)
+{
+    if (which == CONV_RUN)
+        hipLaunchKernelGGL((causal_conv_kernel<T, F, V, SILU>), dim3((unsigned)grid), dim3(256), 0, s, p);
+    else if (which == CONV_STEP)
+        hipLaunchKernelGGL((causal_step_kernel<T, F, V, SILU>), dim3((unsigned)grid), dim3(256), 0, s, p);
+    else if constexpr (V < 8 || F <= 4)
+        hipLaunchKernelGGL((causal_bwd_kernel<T, F, V, SILU>), dim3((unsigned)grid), dim3(256), 0, s, p);
+}
+
+template <typename T, int F, int V>
+void launch_causal(ConvKernel which, bool silu, const CausalParams &p, int64_t grid, hipStream_t s)
+{
+    if (silu) launch_causal<T, F, V, true>(which, p, grid, s);
+    else launch_causal<T, F, V, false>(which, p, grid, s);
+}
+
+template <typename T, int V>
+void launch_causal(ConvKernel which, int F, bool silu, const CausalParams &p, int64_t grid, hipStream_t s)
+{
+    switch (F) {
+    case 2: return launch_causal<T, 2, V>(which, silu, p, grid, s);
+    case 3: return launch_causal<T, 3, V>(which, silu, p, grid, s);
+    case 4: return launch_causal<T, 4, V>(which, silu, p, grid, s);
+    case 5: return launch_causal<T, 5, V>(which, silu, p, grid, s);
+    case 6: return launch_causal<T, 6, V>(which, silu, p, grid, s);
+    case 7: return launch_causal<T, 7, V>(which, silu, p, grid, s);
+    default: return launch_causal<T, 8, V>(which, silu, p, grid, s);
+    }
+}
+
+// The gradient keeps 4 F V values of a thread in registers; with 8 taps of 8
+// channels they would not fit, so more than 4 taps of bf16 go by 4 channels.
+void launch_causal_bwd4(int F, bool silu, const CausalParams &p, int64_t grid, hipStream_t s)
+{
+    switch (F) {
+    case 5: return launch_causal<bf16_t, 5, 4>(CONV_BWD, silu, p, grid, s);
+    case 6: return launch_causal<bf16_t, 6, 4>(CONV_BWD, silu, p, grid, s);
+    case 7: return launch_causal<bf16_t, 7, 4>(CONV_BWD, silu, p, grid, s);
+    default: return launch_causal<bf16_t, 8, 4>(CONV_BWD, silu, p, grid, s);
+    }
+}
+
+void launch_causal(ConvKernel which, const conv_causal_desc_t &d, int V, const CausalParams &p, int64_t grid, hipStream_t s)
+{
+    if (d.dtype == CONV_DT_BF16) {
+        if (V == 4) launch_causal_bwd4((int)d.F, d.silu, p, grid, s);
+        else if (V > 1) launch_causal<bf16_t, 8>(which, (int)d.F, d.silu, p, grid, s);
+        else launch_causal<bf16_t, 1>(which, (int)d.F, d.silu, p, grid, s);
+    } else {
+        if (V > 1) launch_causal<float, 4>(which, (int)d.F, d.silu, p, grid, s);
+        else launch_causal<float, 1>(which, (int)d.F, d.silu, p, grid, s);
+    }
+}
+
+// channels per access: whole 16-byte vectors where every tensor allows it
+int conv_vector(const conv_causal_desc_t &d, int64_t esz, const Rows *t, int n)
+{
+    bool ok = d.C * esz % 16 == 0;
+    for (int i = 0; i < n; ++i) ok = ok && vector_rows(t[i]);
+    return ok ? (int)(16 / esz) : 1;
+}
+
+int64_t bwd_blocks(const conv_causal_desc_t &d)   // workgroups along a sequence, one at least (dstate)
+{
+    const int64_t per = kConvBwdRun * kConvBwdRuns;
+    return std::max<int64_t>(1, (d.L + per - 1) / per);
+}
+
+// ---- scan ------------------------------------------------------------------------
+template <typename T, int SP> struct ScanLaunch {
+    static void fwd(const ScanParams &p, int64_t units, int64_t, hipStream_t s)
+    {
+        const unsigned blk = SP * kPB / 256;
+        if (p.nseg > 1) {
+            hipLaunchKernelGGL((scan_state_kernel<T, SP, false, false>), dim3((unsigned)(units * (p.nseg - 1))), dim3(256), 0, s, p);
+            hipLaunchKernelGGL((scan_join_kernel<SP, false>), dim3((unsigned)(units * blk)), dim3(256), 0, s, p);
+        }
+        hipLaunchKernelGGL((scan_fwd_kernel<T, SP>), dim3((unsigned)(units * p.nseg)), dim3(256), 0, s, p);
+    }
+    static void bwd(const ScanParams &q, int64_t units, int64_t grid, hipStream_t s)
+    {
+        ScanParams p = q;
+        const unsigned blk = SP * kPB / 256, segs = (unsigned)(units * (p.nseg - 1));
+        if (p.nseg > 1) {
+            hipLaunchKernelGGL((scan_state_kernel<T, SP, false, false>), dim3(segs), dim3(256), 0, s, p);
+            hipLaunchKernelGGL((scan_join_kernel<SP, false>), dim3((unsigned)(units * blk)), dim3(256), 0, s, p);
+        }
+        hipLaunchKernelGGL((scan_state_kernel<T, SP, false, true>), dim3((unsigned)(units * p.nseg)), dim3(256), 0, s, p);
+        p.bound = const_cast<float *>(q.ubound);
+        if (p.nseg > 1) {
+            hipLaunchKernelGGL((scan_state_kernel<T, SP, true, false>), dim3(segs), dim3(256), 0, s, p);
+            hipLaunchKernelGGL((scan_join_kernel<SP, true>), dim3((unsigned)(units * blk)), dim3(256), 0, s, p);
+        }
+        hipLaunchKernelGGL((scan_state_kernel<T, SP, true, true>), dim3((unsigned)(units * p.nseg)), dim3(256), 0, s, p);
+        hipLaunchKernelGGL((scan_bwd_kernel<T, SP>), dim3((unsigned)grid), dim3(256), 0, s, q);
+        if (p.slices > 1 && p.L > 0)
+            hipLaunchKernelGGL((scan_reduce_bc_kernel<T, SP>), dim3((unsigned)(((int64_t)p.N * p.L * p.G * SP + 255) / 256)),
+                               dim3(256), 0, s, q);
+    }
+};
+
+template <typename T> void launch_scan(bool bwd, int SP, const ScanParams &p, int64_t units, int64_t grid, hipStream_t s)
+{
+    auto f = SP == 32 ? (bwd ? ScanLaunch<T, 32>::bwd : ScanLaunch<T, 32>::fwd)
+           : SP == 64 ? (bwd ? ScanLaunch<T, 64>::bwd : ScanLaunch<T, 64>::fwd)
+                      : (bwd ? ScanLaunch<T, 128>::bwd : ScanLaunch<T, 128>::fwd);
+    f(p, units, grid, s);
+}
+
+// Segments of K chunks so that `units` heads give about `want` workgroups.
+void split_segments(int64_t units, int64_t K, int64_t want, int *nseg, int *seg)
+{
+    const int64_t n = std::max<int64_t>(1, std::min(K, want / std::max<int64_t>(1, units)));
+    const int64_t per = (K + n - 1) / n;
+    *seg = (int)per;
+    *nseg = (int)((K + per - 1) / per);
+}
+
+void scan_params(const conv_scan_plan &pl, ScanParams *p)
+{
+    const conv_scan_desc_t &d = pl.desc;
+    *p = ScanParams{};
+    p->N = (int)d.N; p->L = d.L; p->H = (int)d.H; p->P = (int)d.P; p->G = (int)d.G; p->S = (int)d.S;
+    p->NPB = pl.NPB; p->K = pl.K; p->softplus = d.softplus;
+}
+
+}  // namespace
+}  // namespace convfwd
+
+using namespace convfwd;
+
+extern "C" {
+
+conv_status_t conv_causal_create(const conv_causal_desc_t *desc, conv_causal_plan_t **plan)
+{
+    if (!plan) return fail(CONV_ERR_INVALID_ARG, "plan is NULL");
+    *plan = nullptr;
+    if (!desc) return fail(CONV_ERR_INVALID_ARG, "descriptor is NULL");
+    const conv_causal_desc_t &d = *desc;
+    if (d.dtype != CONV_DT_F32 && d.dtype != CONV_DT_BF16) return fail(CONV_ERR_INVALID_ARG, "unknown dtype %d", d.dtype);
+    if (d.has_bias != 0 && d.has_bias != 1) return fail(CONV_ERR_INVALID_ARG, "has_bias must be 0 or 1");
+    if (d.silu != 0 && d.silu != 1) return fail(CONV_ERR_INVALID_ARG, "silu must be 0 or 1");
+    if (d.reserved != 0) return fail(CONV_ERR_INVALID_ARG, "reserved must be 0");
+    if (d.N < 0 || d.L < 0 || d.C < 1 || d.F < 2)
+        return fail(CONV_ERR_INVALID_ARG, "need N >= 0, L >= 0, C >= 1 and F >= 2 (got %lld, %lld, %lld, %lld)",
+                    (long long)d.N, (long long)d.L, (long long)d.C, (long long)d.F);
+    if (d.F > 8) return fail(CONV_ERR_UNSUPPORTED, "more than 8 taps (F = %lld)", (long long)d.F);
+    if (d.N > kMaxDim || d.L > kMaxDim || d.C > kMaxDim) return fail(CONV_ERR_UNSUPPORTED, "N, L or C above 2^30");
+    // one thread per channel and run, 256 to a workgroup
+    const double threads = (double)d.N * (double)((d.L + kConvRun - 1) / kConvRun + 1) * (double)d.C;
+    const double wgs = (double)d.N * (double)bwd_blocks(d) * (double)((d.C + kConvBwdCv - 1) / kConvBwdCv);
+    const double ws = (double)d.N * (double)bwd_blocks(d) * (double)(d.F + 1) * (double)d.C * 4.0;
+    if (threads / 256.0 >= 2147483000.0 || wgs >= 2147483000.0 || ws >= kMaxBytes)
+        return fail(CONV_ERR_UNSUPPORTED, "N x L x C is too large for one launch");
+    conv_causal_plan *pl = new (std::nothrow) conv_causal_plan();
+    if (!pl) return fail(CONV_ERR_NOMEM, "plan allocation failed");
+    pl->desc = d;
+    pl->esz = d.dtype == CONV_DT_BF16 ? 2 : 4;
+    pl->bwd_rows = d.N * bwd_blocks(d);
+    pl->ws_bytes = pl->bwd_rows * (d.F + 1) * d.C * 4;
+    snprintf(pl->text, sizeof(pl->text), "causal %s N=%lld L=%lld C=%lld F=%lld%s%s, %d tokens per thread",
+             d.dtype == CONV_DT_BF16 ? "bf16" : "f32", (long long)d.N, (long long)d.L, (long long)d.C, (long long)d.F,
+             d.has_bias ? " bias" : "", d.silu ? " silu" : "", kConvRun);
+    if (getenv("CONVFWD_LOG")) fprintf(stderr, "convfwd: %s\n", pl->text);
+    *plan = pl;
+    return CONV_OK;
+}
+
+static conv_status_t causal_forward(const conv_causal_plan_t *plan, const conv_causal_args_t *a, bool step, void *stream)
+{
+    if (!plan || !a) return fail(CONV_ERR_INVALID_ARG, "plan or args is NULL");
+    const conv_causal_desc_t &d = plan->desc;
+    const int64_t L = step ? 1 : d.L, e = plan->esz, hist = d.F - 1;
+    if (!a->w) return fail(CONV_ERR_INVALID_ARG, "w is NULL");
+    if ((a->bias != nullptr) != (d.has_bias != 0))
+        return fail(CONV_ERR_INVALID_ARG, d.has_bias ? "bias is NULL" : "this plan has no bias");
+    if (step && a->lengths) return fail(CONV_ERR_INVALID_ARG, "a step takes no lengths");
+    const Rows in[] = {{"x", a->x, d.N * L, d.C, or_packed(a->x_ld, d.C), e},
+                       {"w", a->w, 1, d.C * d.F, d.C * d.F, e},
+                       {"bias", a->bias, 1, d.C, d.C, e},
+                       {"lengths", a->lengths, 1, d.N, std::max<int64_t>(1, d.N), 4},
+                       {"state", a->state, d.N * hist, d.C, d.C, e}};
+    const Rows out[] = {{"y", a->y, d.N * L, d.C, or_packed(a->y_ld, d.C), e},
+                        {"state_out", a->state_out, d.N * hist, d.C, d.C, e}};
+    conv_status_t st = check_rows(in, 5);
+    if (st == CONV_OK) st = check_rows(out, 2);
+    if (st != CONV_OK) return st;
+    if (d.N == 0) return CONV_OK;
+    if (L > 0 && (!a->x || !a->y)) return fail(CONV_ERR_INVALID_ARG, "x or y is NULL");
+    if (step && (!a->state || !a->state_out)) return fail(CONV_ERR_INVALID_ARG, "state or state_out is NULL");
+    // a step may move the state on in place: each thread owns its channels
+    const bool in_place = step && a->state == a->state_out;
+    if ((st = check_overlap(out, 2, in, in_place ? 4 : 5)) != CONV_OK) return st;
+    if (L == 0 && !a->state_out) return CONV_OK;
+    const Rows vec[] = {in[0], in[1], in[2], in[4], out[0], out[1]};
+    const int V = conv_vector(d, e, vec, 6);
+    CausalParams p{};
+    p.x = a->x; p.w = a->w; p.bias = a->bias; p.state = a->state; p.lengths = a->lengths;
+    p.y = a->y; p.state_out = a->state_out;
+    p.x_ld = in[0].ld; p.y_ld = out[0].ld;
+    p.N = (int)d.N; p.C = (int)d.C; p.CV = (int)(d.C / V); p.L = L;
+    p.blocks = (L + kConvRun - 1) / kConvRun;
+    const int64_t threads = step ? d.N * p.CV : d.N * (p.blocks + (a->state_out ? 1 : 0)) * p.CV;
+    (void)hipGetLastError();
+    launch_causal(step ? CONV_STEP : CONV_RUN, d, V, p, (threads + 255) / 256, (hipStream_t)stream);
+    return launched();
+}
+
+conv_status_t conv_causal_run(const conv_causal_plan_t *plan, const conv_causal_args_t *args, void *stream)
+{
+    return causal_forward(plan, args, false, stream);
+}
+
+conv_status_t conv_causal_step(const conv_causal_plan_t *plan, const conv_causal_args_t *args, void *stream)
+{
+    return causal_forward(plan, args, true, stream);
+}
+
+conv_status_t conv_causal_bwd_workspace_bytes(const conv_causal_plan_t *plan, int64_t *bytes)
+{
+    if (!plan || !bytes) return fail(CONV_ERR_INVALID_ARG, "plan or bytes is NULL");
+    *bytes = plan->ws_bytes;
+    return CONV_OK;
+}
+
+conv_status_t conv_causal_bwd_run(const conv_causal_plan_t *plan, const conv_causal_bwd_args_t *a, void *workspace,
+                                  int64_t workspace_bytes, void *stream)
+{
+    if (!plan || !a) return fail(CONV_ERR_INVALID_ARG, "plan or args is NULL");
+    const conv_causal_desc_t &d = plan->desc;
+    const int64_t e = plan->esz, hist = d.F - 1;
+    if (!a->w || !a->dw) return fail(CONV_ERR_INVALID_ARG, "w or dw is NULL");
+    if ((a->bias != nullptr) != (d.has_bias != 0) || (a->dbias != nullptr) != (d.has_bias != 0))
+        return fail(CONV_ERR_INVALID_ARG, d.has_bias ? "bias or dbias is NULL" : "this plan has no bias");
+    if (a->dstate && !a->state) return fail(CONV_ERR_INVALID_ARG, "dstate without a state");
+    const Rows in[] = {{"dy", a->dy, d.N * d.L, d.C, or_packed(a->dy_ld, d.C), e},
+                       {"x", a->x, d.N * d.L, d.C, or_packed(a->x_ld, d.C), e},
+                       {"w", a->w, 1, d.C * d.F, d.C * d.F, e},
+                       {"bias", a->bias, 1, d.C, d.C, e},
+                       {"state", a->state, d.N * hist, d.C, d.C, e},
+                       {"dstate_out", a->dstate_out, d.N * hist, d.C, d.C, e},
+                       {"lengths", a->lengths, 1, d.N, std::max<int64_t>(1, d.N), 4}};
+    const Rows out[] = {{"dx", a->dx, d.N * d.L, d.C, or_packed(a->dx_ld, d.C), e},
+                        {"dw", a->dw, 1, d.C * d.F, d.C * d.F, e},
+                        {"dbias", a->dbias, 1, d.C, d.C, e},
+                        {"dstate", a->dstate, d.N * hist, d.C, d.C, e},
+                        {"workspace", workspace, 1, plan->ws_bytes, std::max<int64_t>(1, plan->ws_bytes), 1}};
+    conv_status_t st = check_rows(in, 7);
+    if (st == CONV_OK) st = check_rows(out, 4);
+    if (st != CONV_OK) return st;
+    if (d.N > 0 && d.L > 0 && (!a->dy || !a->x || !a->dx)) return fail(CONV_ERR_INVALID_ARG, "dy, x or dx is NULL");
+    if ((st = check_workspace(workspace, workspace_bytes, plan->ws_bytes)) != CONV_OK) return st;
+    if ((st = check_overlap(out, 5, in, 7)) != CONV_OK) return st;
+    const Rows vec[] = {in[0], in[1], in[2], in[3], in[4], in[5], out[0], out[3]};
+    int V = conv_vector(d, e, vec, 8);
+    if (V == 8 && d.F > 4) V = 4;
+    CausalParams p{};
+    p.x = a->x; p.w = a->w; p.bias = a->bias; p.state = a->state; p.lengths = a->lengths;
+    p.dy = a->dy; p.dstate_out = a->dstate_out; p.dx = a->dx; p.dstate = a->dstate;
+    p.partial = (float *)workspace;
+    p.x_ld = in[1].ld; p.dy_ld = in[0].ld; p.dx_ld = out[0].ld;
+    p.N = (int)d.N; p.C = (int)d.C; p.CV = (int)(d.C / V); p.L = d.L;
+    p.blocks = bwd_blocks(d);
+    (void)hipGetLastError();
+    hipStream_t s = (hipStream_t)stream;
+    if (d.N > 0)
+        launch_causal(CONV_BWD, d, V, p, plan->bwd_rows * ((p.CV + kConvBwdCv - 1) / kConvBwdCv), s);
+    const dim3 grid((unsigned)((d.F + 1) * ((d.C + 63) / 64)));      // no rows: dw and dbias are zeros
+    if (d.dtype == CONV_DT_BF16)
+        hipLaunchKernelGGL(causal_reduce_kernel<bf16_t>, grid, dim3(256), 0, s, p.partial, (bf16_t *)a->dw,
+                           (bf16_t *)a->dbias, plan->bwd_rows, (int)d.C, (int)d.F);
+    else
+        hipLaunchKernelGGL(causal_reduce_kernel<float>, grid, dim3(256), 0, s, p.partial, (float *)a->dw,
+                           (float *)a->dbias, plan->bwd_rows, (int)d.C, (int)d.F);
+    return launched();
+}
+
+void conv_causal_destroy(conv_causal_plan_t *plan) { delete plan; }
+
+const char *conv_causal_describe(const conv_causal_plan_t *plan) { return plan ? plan->text : ""; }
+
+// ---- scan ------------------------------------------------------------------------
+conv_status_t conv_scan_create(const conv_scan_desc_t *desc, conv_scan_plan_t **plan)
+{
+    if (!plan) return fail(CONV_ERR_INVALID_ARG, "plan is NULL");
+    *plan = nullptr;
+    if (!desc) return fail(CONV_ERR_INVALID_ARG, "descriptor is NULL");
+    const conv_scan_desc_t &d = *desc;
+    if (d.dtype != CONV_DT_F32 && d.dtype != CONV_DT_BF16) return fail(CONV_ERR_INVALID_ARG, "unknown dtype %d", d.dtype);
+    if (d.softplus != 0 && d.softplus != 1) return fail(CONV_ERR_INVALID_ARG, "softplus must be 0 or 1");
+    if (d.N < 0 || d.L < 0 || d.H < 1 || d.P < 1 || d.G < 1 || d.S < 1)
+        return fail(CONV_ERR_INVALID_ARG, "need N, L >= 0 and H, P, G, S >= 1 (got %lld, %lld, %lld, %lld, %lld, %lld)",
+                    (long long)d.N, (long long)d.L, (long long)d.H, (long long)d.P, (long long)d.G, (long long)d.S);
+    if (d.H % d.G != 0)
+        return fail(CONV_ERR_INVALID_ARG, "H = %lld is not a multiple of G = %lld", (long long)d.H, (long long)d.G);
+    if (d.S > 128) return fail(CONV_ERR_UNSUPPORTED, "more than 128 states (S = %lld)", (long long)d.S);
+    if (d.P > 65536) return fail(CONV_ERR_UNSUPPORTED, "more than 65536 channels of a head (P = %lld)", (long long)d.P);
+    if (d.N > kMaxDim || d.L > kMaxDim || d.H > kMaxDim) return fail(CONV_ERR_UNSUPPORTED, "N, L or H above 2^30");
+    conv_scan_plan *pl = new (std::nothrow) conv_scan_plan();
+    if (!pl) return fail(CONV_ERR_NOMEM, "plan allocation failed");
+    pl->desc = d;
+    pl->esz = d.dtype == CONV_DT_BF16 ? 2 : 4;
+    pl->SP = d.S <= 32 ? 32 : d.S <= 64 ? 64 : 128;
+    pl->Q = d.dtype == CONV_DT_BF16 ? Frag<bf16_t>::Q : Frag<float>::Q;
+    pl->K = (int)std::max<int64_t>(1, (d.L + pl->Q - 1) / pl->Q);
+    pl->NPB = (int)((d.P + kPB - 1) / kPB);
+    const double units = (double)d.N * d.H * pl->NPB, tile = (double)pl->SP * kPB * 4;
+    const double grids = std::max(units * std::max<double>(pl->K, 32), (double)d.N * pl->K * d.H);
+    const double rows = (double)d.N * d.L * d.G * pl->SP;
+    // no grid is larger than one workgroup per unit and chunk, or per 256 elements of dB
+    if (grids >= 2147483000.0 || rows / 256.0 >= 2147483000.0 || units * (pl->K + 1) * tile * 3 >= kMaxBytes ||
+        3.0 * d.H >= 2147483000.0) {
+        delete pl;
+        return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
+    }
+    pl->units = d.N * d.H * pl->NPB;
+    // Two forward workgroups fit a compute unit; with fewer heads than half of
+    // those the long axis is split, at the price of a second pass over x and B.
+    const int64_t cus = 256;
+    split_segments(pl->units, pl->K, pl->units >= cus ? 0 : 2 * cus, &pl->nseg, &pl->seg);
+    split_segments(pl->units, pl->K, pl->units >= cus ? 0 : 2 * cus, &pl->bnseg, &pl->bseg);
+    const int64_t chunks = d.N * pl->K * d.G, hpg = d.H / d.G;
+    const int64_t want = std::max<int64_t>(1, std::min(hpg, (2 * cus + chunks - 1) / std::max<int64_t>(1, chunks)));
+    pl->heads_per_slice = (int)((hpg + want - 1) / want);
+    pl->slices = (int)((hpg + pl->heads_per_slice - 1) / pl->heads_per_slice);
+    const int64_t t = (int64_t)pl->SP * kPB * 4;
+    auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
+    pl->ws_bytes = pl->nseg > 1 ? up(pl->units * pl->nseg * t) + up(pl->units * pl->nseg * 4) : 0;
+    int64_t o = pl->bnseg > 1 ? up(pl->units * pl->bnseg * t) : 0;
+    pl->o_log = o;
+    o += pl->bnseg > 1 ? up(pl->units * pl->bnseg * 4) : 0;
+    pl->o_bound = o;
+    o += up(pl->units * pl->K * t);
+    pl->o_ubound = o;
+    o += up(pl->units * pl->K * t);
+    pl->o_head = o;
+    o += up(3 * d.N * pl->K * d.H * 4);
+    pl->o_pb = o;
+    const int64_t part = pl->slices > 1 ? up((int64_t)pl->slices * d.N * d.L * d.G * pl->SP * 4) : 0;
+    pl->o_pc = o + part;
+    pl->bwd_ws_bytes = o + 2 * part;
+    snprintf(pl->text, sizeof(pl->text),
+             "scan %s N=%lld L=%lld H=%lld P=%lld G=%lld S=%lld(%d)%s, %d chunks of %d in %d segments; "
+             "gradient: %d segments, %d slices of %d heads",
+             d.dtype == CONV_DT_BF16 ? "bf16" : "f32", (long long)d.N, (long long)d.L, (long long)d.H, (long long)d.P,
+             (long long)d.G, (long long)d.S, pl->SP, d.softplus ? " softplus" : "", pl->K, pl->Q, pl->nseg, pl->bnseg,
+             pl->slices, pl->heads_per_slice);
+    if (getenv("CONVFWD_LOG")) fprintf(stderr, "convfwd: %s\n", pl->text);
+    *plan = pl;
+    return CONV_OK;
+}
+
+conv_status_t conv_scan_workspace_bytes(const conv_scan_plan_t *plan, int64_t *bytes)
+{
+    if (!plan || !bytes) return fail(CONV_ERR_INVALID_ARG, "plan or bytes is NULL");
+    *bytes = plan->ws_bytes;
+    return CONV_OK;
+}
+
+conv_status_t conv_scan_bwd_workspace_bytes(const conv_scan_plan_t *plan, int64_t *bytes)
+{
+    if (!plan || !bytes) return fail(CONV_ERR_INVALID_ARG, "plan or bytes is NULL");
+    *bytes = plan->bwd_ws_bytes;
+    return CONV_OK;
+}
+
+// 16-byte accesses to heads' channels and groups' states
+static bool scan_vector(const conv_scan_plan &pl, const Rows *t, int n)
+{
+    bool ok = pl.desc.P * pl.esz % 16 == 0 && pl.desc.S * pl.esz % 16 == 0;
+    for (int i = 0; i < n; ++i) ok = ok && vector_rows(t[i]);
+    return ok;
+}
+
+static conv_status_t scan_forward(const conv_scan_plan_t *plan, const conv_scan_args_t *a, bool step, void *ws,
+                                  int64_t ws_bytes, void *stream)
+{
+    if (!plan || !a) return fail(CONV_ERR_INVALID_ARG, "plan or args is NULL");
+    const conv_scan_desc_t &d = plan->desc;
+    const int64_t L = step ? 1 : d.L, e = plan->esz, rows = d.N * L, need = step ? 0 : plan->ws_bytes;
+    if (!a->a) return fail(CONV_ERR_INVALID_ARG, "a is NULL");
+    if (step && a->lengths) return fail(CONV_ERR_INVALID_ARG, "a step takes no lengths");
+    const int64_t hp = d.H * d.P, gs = d.G * d.S;
+    const Rows in[] = {{"x", a->x, rows, hp, or_packed(a->x_ld, hp), e},
+                       {"b", a->b, rows, gs, or_packed(a->b_ld, gs), e},
+                       {"c", a->c, rows, gs, or_packed(a->c_ld, gs), e},
+                       {"dt", a->dt, rows, d.H, or_packed(a->dt_ld, d.H), e},
+                       {"a", a->a, 1, d.H, d.H, 4},
+                       {"d", a->d, 1, d.H, d.H, 4},
+                       {"dt_bias", a->dt_bias, 1, d.H, d.H, 4},
+                       {"lengths", a->lengths, 1, d.N, std::max<int64_t>(1, d.N), 4},
+                       {"state", a->state, d.N * d.H, d.P * d.S, d.P * d.S, 4}};
+    const Rows out[] = {{"y", a->y, rows, hp, or_packed(a->y_ld, hp), e},
+                        {"state_out", a->state_out, d.N * d.H, d.P * d.S, d.P * d.S, 4},
+                        {"workspace", ws, 1, need, std::max<int64_t>(1, need), 1}};
+    conv_status_t st = check_rows(in, 9);
+    if (st == CONV_OK) st = check_rows(out, 2);
+    if (st != CONV_OK) return st;
+    if (d.N == 0) return CONV_OK;
+    if (L > 0 && (!a->x || !a->b || !a->c || !a->dt || !a->y)) return fail(CONV_ERR_INVALID_ARG, "x, b, c, dt or y is NULL");
+    if (step && (!a->state || !a->state_out)) return fail(CONV_ERR_INVALID_ARG, "state or state_out is NULL");
+    if ((st = check_workspace(ws, ws_bytes, need)) != CONV_OK) return st;
+    // a step may update the state in place: each lane owns its part
+    const bool in_place = step && a->state == a->state_out;
+    if ((st = check_overlap(out, 3, in, in_place ? 8 : 9)) != CONV_OK) return st;
+    ScanParams p;
+    scan_params(*plan, &p);
+    p.L = L;
+    p.x = a->x; p.dt = a->dt; p.b = a->b; p.c = a->c; p.a = a->a; p.d = a->d; p.dt_bias = a->dt_bias;
+    p.state = a->state; p.lengths = a->lengths; p.y = a->y; p.state_out = a->state_out;
+    p.x_ld = in[0].ld; p.b_ld = in[1].ld; p.c_ld = in[2].ld; p.dt_ld = in[3].ld; p.y_ld = out[0].ld;
+    hipStream_t s = (hipStream_t)stream;
+    (void)hipGetLastError();
+    if (step) {
+        int lpr = 1;
+        while (lpr * 4 < d.S) lpr *= 2;
+        const int per = 4 * kStepRows * (64 / lpr), blocks = (int)((d.P + per - 1) / per);
+        const bool vec = d.S % 4 == 0 && ((uintptr_t)a->state | (uintptr_t)a->state_out) % 16 == 0;
+        const dim3 grid((unsigned)(d.N * d.H * blocks));
+        if (d.dtype == CONV_DT_BF16) {
+            if (vec) hipLaunchKernelGGL((scan_step_kernel<bf16_t, true>), grid, dim3(256), 0, s, p, lpr, blocks);
+            else hipLaunchKernelGGL((scan_step_kernel<bf16_t, false>), grid, dim3(256), 0, s, p, lpr, blocks);
+        } else {
+            if (vec) hipLaunchKernelGGL((scan_step_kernel<float, true>), grid, dim3(256), 0, s, p, lpr, blocks);
+            else hipLaunchKernelGGL((scan_step_kernel<float, false>), grid, dim3(256), 0, s, p, lpr, blocks);
+        }
+        return launched();
+    }
+    p.nseg = plan->nseg;
+    p.seg = plan->seg;
+    p.seg_state = (float *)ws;
+    p.seg_log = plan->nseg > 1 ? (float *)((char *)ws + plan->ws_bytes - (plan->units * plan->nseg * 4 + 255) / 256 * 256) : nullptr;
+    const Rows vec[] = {in[0], in[1], in[2], out[0]};
+    p.vec = scan_vector(*plan, vec, 4);
+    if (d.dtype == CONV_DT_BF16) launch_scan<bf16_t>(false, plan->SP, p, plan->units, 0, s);
+    else launch_scan<float>(false, plan->SP, p, plan->units, 0, s);
+    return launched();
+}
+
+conv_status_t conv_scan_run(const conv_scan_plan_t *plan, const conv_scan_args_t *args, void *workspace,
+                            int64_t workspace_bytes, void *stream)
+{
+    return scan_forward(plan, args, false, workspace, workspace_bytes, stream);
+}
+
+conv_status_t conv_scan_step(const conv_scan_plan_t *plan, const conv_scan_args_t *args, void *stream)
+{
+    return scan_forward(plan, args, true, nullptr, 0, stream);
+}
+
+conv_status_t conv_scan_bwd_run(const conv_scan_plan_t *plan, const conv_scan_bwd_args_t *a, void *workspace,
+                                int64_t workspace_bytes, void *stream)
+{
+    if (!plan || !a) return fail(CONV_ERR_INVALID_ARG, "plan or args is NULL");
+    const conv_scan_desc_t &d = plan->desc;
+    const int64_t e = plan->esz, rows = d.N * d.L, hp = d.H * d.P, gs = d.G * d.S;
+    if (!a->a || !a->da) return fail(CONV_ERR_INVALID_ARG, "a or da is NULL");
+    if ((a->d != nullptr) != (a->dd != nullptr) || (a->dt_bias != nullptr) != (a->ddt_bias != nullptr))
+        return fail(CONV_ERR_INVALID_ARG, "dd must be NULL iff d is, and ddt_bias iff dt_bias is");
+    const Rows in[] = {{"dy", a->dy, rows, hp, or_packed(a->dy_ld, hp), e},
+                       {"x", a->x, rows, hp, or_packed(a->x_ld, hp), e},
+                       {"b", a->b, rows, gs, or_packed(a->b_ld, gs), e},
+                       {"c", a->c, rows, gs, or_packed(a->c_ld, gs), e},
+                       {"dt", a->dt, rows, d.H, or_packed(a->dt_ld, d.H), e},
+                       {"a", a->a, 1, d.H, d.H, 4},
+                       {"d", a->d, 1, d.H, d.H, 4},
+                       {"dt_bias", a->dt_bias, 1, d.H, d.H, 4},
+                       {"lengths", a->lengths, 1, d.N, std::max<int64_t>(1, d.N), 4},
+                       {"state", a->state, d.N * d.H, d.P * d.S, d.P * d.S, 4},
+                       {"dstate_out", a->dstate_out, d.N * d.H, d.P * d.S, d.P * d.S, 4}};
+    const Rows out[] = {{"dx", a->dx, rows, hp, or_packed(a->dx_ld, hp), e},
+                        {"db", a->db, rows, gs, or_packed(a->db_ld, gs), e},
+                        {"dc", a->dc, rows, gs, or_packed(a->dc_ld, gs), e},
+                        {"ddt", a->ddt, rows, d.H, or_packed(a->ddt_ld, d.H), e},
+                        {"da", a->da, 1, d.H, d.H, 4},
+                        {"dd", a->dd, 1, d.H, d.H, 4},
+                        {"ddt_bias", a->ddt_bias, 1, d.H, d.H, 4},
+                        {"dstate", a->dstate, d.N * d.H, d.P * d.S, d.P * d.S, 4},
+                        {"workspace", workspace, 1, plan->bwd_ws_bytes, std::max<int64_t>(1, plan->bwd_ws_bytes), 1}};
+    conv_status_t st = check_rows(in, 11);
+    if (st == CONV_OK) st = check_rows(out, 8);
+    if (st != CONV_OK) return st;
+    if (rows > 0 && (!a->dy || !a->x || !a->b || !a->c || !a->dt || !a->dx || !a->db || !a->dc || !a->ddt))
+        return fail(CONV_ERR_INVALID_ARG, "dy, x, b, c, dt, dx, db, dc or ddt is NULL");
+    if ((st = check_workspace(workspace, workspace_bytes, plan->bwd_ws_bytes)) != CONV_OK) return st;
+    if ((st = check_overlap(out, 9, in, 11)) != CONV_OK) return st;
+    ScanParams p;
+    scan_params(*plan, &p);
+    p.x = a->x; p.dt = a->dt; p.b = a->b; p.c = a->c; p.a = a->a; p.d = a->d; p.dt_bias = a->dt_bias;
+    p.state = a->state; p.lengths = a->lengths; p.dy = a->dy; p.dstate_out = a->dstate_out;
+    p.dx = a->dx; p.ddt = a->ddt; p.db = a->db; p.dc = a->dc; p.dstate = a->dstate;
+    p.dy_ld = in[0].ld; p.x_ld = in[1].ld; p.b_ld = in[2].ld; p.c_ld = in[3].ld; p.dt_ld = in[4].ld;
+    p.dx_ld = out[0].ld; p.db_ld = out[1].ld; p.dc_ld = out[2].ld; p.ddt_ld = out[3].ld;
+    const Rows vec[] = {in[0], in[1], in[2], in[3], out[0]};
+    p.vec = scan_vector(*plan, vec, 5);
+    char *ws = (char *)workspace;
+    p.nseg = plan->bnseg; p.seg = plan->bseg;
+    p.seg_state = (float *)ws;
+    p.seg_log = (float *)(ws + plan->o_log);
+    p.bound = (float *)(ws + plan->o_bound);
+    p.ubound = (float *)(ws + plan->o_ubound);
+    p.part_head = (float *)(ws + plan->o_head);
+    p.part_b = (float *)(ws + plan->o_pb);
+    p.part_c = (float *)(ws + plan->o_pc);
+    p.slices = plan->slices;
+    p.heads_per_slice = plan->heads_per_slice;
+    hipStream_t s = (hipStream_t)stream;
+    (void)hipGetLastError();
+    const int64_t NK = d.N * plan->K;
+    if (d.N > 0) {
+        const int64_t grid = NK * d.G * plan->slices;
+        if (d.dtype == CONV_DT_BF16) launch_scan<bf16_t>(true, plan->SP, p, plan->units, grid, s);
+        else launch_scan<float>(true, plan->SP, p, plan->units, grid, s);
+    }
+    hipLaunchKernelGGL(scan_reduce_heads_kernel, dim3((unsigned)(3 * d.H)), dim3(256), 0, s, p.part_head, a->da,
+                       a->ddt_bias, a->dd, NK, (int)d.H);      // no sequences: zeros
+    return launched();
+}
+
+void conv_scan_destroy(conv_scan_plan_t *plan) { delete plan; }
+
+const char *conv_scan_describe(const conv_scan_plan_t *plan) { return plan ? plan->text : ""; }
+
+}  // extern "C"

@@ -344,6 +344,163 @@ conv_status_t conv_bwd_weight_run(const conv_bwd_weight_plan_t *plan, const void
 void conv_bwd_weight_destroy(conv_bwd_weight_plan_t *plan);
 const char *conv_bwd_weight_describe(const conv_bwd_weight_plan_t *plan);
 
+/* ---- Causal depthwise convolution over a sequence --------------------------
+ * The short convolution in front of a state space scan: one filter of F taps
+ * per channel, reading the token and the F - 1 before it,
+ *
+ *   v[n,t,c] = bias[c] + sum_{k<F} w[c,k] * h[n, t-(F-1)+k, c]
+ *   y[n,t,c] = v * sigmoid(v)  (silu = 1)   or   v  (silu = 0)
+ *
+ * h[t] = x[t] for t >= 0; the F - 1 tokens before the first are `state`, oldest
+ * first, or zeros without one.  Layouts (row-major, last index fastest):
+ *   x, y   : N x L x C, x_ld / y_ld elements from one token to the next and
+ *            L times that from one sequence to the next (0 = C)
+ *   w      : C x F          bias : C
+ *   state, state_out : N x (F-1) x C
+ * all in the descriptor's dtype; products and sums in fp32, the result rounded
+ * once.  1 <= F - 1 <= 7.
+ *
+ * lengths (optional): int32[N] on the device, the tokens of each sequence that
+ * count (values outside 0..L are taken as the nearer end).  Rows at and behind
+ * a sequence's length are not read; their outputs are written as zeros, and
+ * state_out holds the last F - 1 tokens before the length (of `state`, where
+ * the sequence is shorter).
+ *
+ * Pointers need the alignment of their elements only; 16-byte aligned tensors
+ * whose token strides and channels are whole 16-byte vectors run on vector
+ * accesses.  Outputs must not overlap inputs or each other (they may interleave
+ * as column ranges of one matrix, i.e. with equal token strides).  Ownership,
+ * threading, asynchrony and errors as conv_fwd; the current device is the
+ * stream's and the tensors'. */
+typedef struct {
+    int32_t dtype;         /* conv_dtype_t                                     */
+    int32_t has_bias;      /* 0 or 1                                           */
+    int32_t silu;          /* 0 or 1                                           */
+    int32_t reserved;      /* 0                                                */
+    int64_t N;             /* sequences, >= 0                                  */
+    int64_t L;             /* tokens of a sequence, >= 0                       */
+    int64_t C;             /* channels, >= 1                                   */
+    int64_t F;             /* taps, 2..8                                       */
+} conv_causal_desc_t;
+
+/* Device pointers of a forward pass or step; NULL where optional. */
+typedef struct {
+    const void *x, *w, *bias;     /* bias NULL iff the plan has none           */
+    const void *state;            /* optional                                  */
+    const int32_t *lengths;       /* optional                                  */
+    void *y;
+    void *state_out;              /* optional                                  */
+    int64_t x_ld, y_ld;
+} conv_causal_args_t;
+
+/* Device pointers of the gradient.  dstate NULL unless state is given
+ * (optional then); dstate_out, the gradient of state_out, is optional; dw and
+ * dbias are the sums over all tokens, in the descriptor's dtype. */
+typedef struct {
+    const void *dy, *x, *w, *bias, *state;
+    const int32_t *lengths;
+    const void *dstate_out;
+    void *dx, *dw, *dbias, *dstate;
+    int64_t dy_ld, x_ld, dx_ld;
+} conv_causal_bwd_args_t;
+
+typedef struct conv_causal_plan conv_causal_plan_t;   /* opaque */
+conv_status_t conv_causal_create(const conv_causal_desc_t *desc, conv_causal_plan_t **plan);
+conv_status_t conv_causal_run(const conv_causal_plan_t *plan, const conv_causal_args_t *args, void *stream);
+/* One token of each of the plan's N sequences (the plan's L plays no part): x
+ * and y N x C with x_ld / y_ld elements from row to row.  state and state_out
+ * are required and may be the same buffer; lengths must be NULL. */
+conv_status_t conv_causal_step(const conv_causal_plan_t *plan, const conv_causal_args_t *args, void *stream);
+/* The gradient of <y, dy> + <state_out, dstate_out>.  fp32 partial sums of dw
+ * and dbias go through the workspace and are added in a fixed order, so results
+ * are deterministic. */
+conv_status_t conv_causal_bwd_workspace_bytes(const conv_causal_plan_t *plan, int64_t *bytes);
+conv_status_t conv_causal_bwd_run(const conv_causal_plan_t *plan, const conv_causal_bwd_args_t *args, void *workspace,
+                                  int64_t workspace_bytes, void *stream);
+void conv_causal_destroy(conv_causal_plan_t *plan);
+const char *conv_causal_describe(const conv_causal_plan_t *plan);
+
+/* ---- Selective state space scan --------------------------------------------
+ * The long convolution behind the short one: a filter that decays as fast as
+ * the data say.  H heads of P channels, each head with a state of P x S; the
+ * heads h of group g = h / (H / G) share B and C.  Per token t
+ *
+ *   dt    = softplus(dt_raw[t,h] + dt_bias[h])  (softplus = 1)  or  dt_raw + dt_bias
+ *   state = exp(a[h] * dt) * state + dt * x[t,h,:] (outer) b[t,g,:]
+ *   y[t,h,:] = state . c[t,g,:] + d[h] * x[t,h,:]
+ *
+ *   x, y  : N x L x H x P       dt   : N x L x H
+ *   b, c  : N x L x G x S       a, d, dt_bias : H, float32 whatever the dtype
+ *   state, state_out : N x H x P x S, float32
+ * with *_ld elements from token to token (0 = the packed row) and L times that
+ * from sequence to sequence; x, dt, b, c, y in the descriptor's dtype.  a is
+ * meant to be negative and dt not; nothing checks it, and a decay that exceeds
+ * 1 grows as the formula says.  d, dt_bias, state, lengths and state_out are
+ * optional (NULL: 0, 0, zeros, all L, not written).  lengths as conv_causal:
+ * rows behind a length are not read, their y are zeros and the state stays.
+ * States and sums are fp32.  Tokens are taken in chunks, so a NaN or an
+ * infinity in a token's inputs may reach every y of its chunk (64 tokens in
+ * bf16, 32 in fp32), not only those behind it.  S <= 128, P <= 65536.
+ *
+ * Long sequences of few heads are split into segments whose states go through a
+ * caller-owned device workspace (16-byte aligned; the size may be 0, then it
+ * may be NULL).  Calls that overlap in time need workspaces of their own.
+ * Alignment, overlap, ownership, threading, asynchrony and errors as
+ * conv_causal. */
+typedef struct {
+    int32_t dtype;         /* conv_dtype_t                                     */
+    int32_t softplus;      /* 0 or 1                                           */
+    int64_t N;             /* sequences, >= 0                                  */
+    int64_t L;             /* tokens of a sequence, >= 0                       */
+    int64_t H;             /* heads, a multiple of G                           */
+    int64_t P;             /* channels of a head, >= 1                         */
+    int64_t G;             /* groups, >= 1                                     */
+    int64_t S;             /* states of a channel, 1..128                      */
+} conv_scan_desc_t;
+
+typedef struct {
+    const void *x, *dt;
+    const float *a;
+    const void *b, *c;
+    const float *d, *dt_bias, *state;
+    const int32_t *lengths;
+    void *y;
+    float *state_out;
+    int64_t x_ld, dt_ld, b_ld, c_ld, y_ld;
+} conv_scan_args_t;
+
+/* Gradients of <y, dy> + <state_out, dstate_out> (dstate_out optional).  dd and
+ * ddt_bias are NULL iff d and dt_bias are; dstate is optional.  ddt is that of
+ * dt_raw. */
+typedef struct {
+    const void *dy, *x, *dt;
+    const float *a;
+    const void *b, *c;
+    const float *d, *dt_bias, *state;
+    const int32_t *lengths;
+    const float *dstate_out;
+    void *dx, *ddt;
+    float *da;
+    void *db, *dc;
+    float *dd, *ddt_bias, *dstate;
+    int64_t dy_ld, x_ld, dt_ld, b_ld, c_ld, dx_ld, ddt_ld, db_ld, dc_ld;
+} conv_scan_bwd_args_t;
+
+typedef struct conv_scan_plan conv_scan_plan_t;   /* opaque */
+conv_status_t conv_scan_create(const conv_scan_desc_t *desc, conv_scan_plan_t **plan);
+conv_status_t conv_scan_workspace_bytes(const conv_scan_plan_t *plan, int64_t *bytes);
+conv_status_t conv_scan_run(const conv_scan_plan_t *plan, const conv_scan_args_t *args, void *workspace,
+                            int64_t workspace_bytes, void *stream);
+/* One token of each of the plan's N sequences (the plan's L plays no part):
+ * rows n of x, dt, b, c, y at n times their ld.  state and state_out are
+ * required and may be the same buffer; lengths must be NULL. */
+conv_status_t conv_scan_step(const conv_scan_plan_t *plan, const conv_scan_args_t *args, void *stream);
+conv_status_t conv_scan_bwd_workspace_bytes(const conv_scan_plan_t *plan, int64_t *bytes);
+conv_status_t conv_scan_bwd_run(const conv_scan_plan_t *plan, const conv_scan_bwd_args_t *args, void *workspace,
+                                int64_t workspace_bytes, void *stream);
+void conv_scan_destroy(conv_scan_plan_t *plan);
+const char *conv_scan_describe(const conv_scan_plan_t *plan);
+
 /* Message of the last failed call on this thread ("" if none). */
 const char *conv_fwd_last_error(void);
 
