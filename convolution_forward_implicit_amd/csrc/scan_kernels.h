@@ -29,7 +29,10 @@
 // enters as the sum of two or three bf16 numbers, each the rounding of what
 // the ones before it left, so that 16 or 24 bits of it take part.  fp32 calls
 // run on the fp32 matrix instructions instead.  States, sums and exponents are
-// fp32, the running sums c_i are added in fp64.
+// fp32; the running sums c_i are added in fp64 and used as differences, which
+// are rounded to fp32 only then (c_i itself, up to some hundreds, would be off
+// by 1e-5, and so would every decay): where fp32 results depend on them, two
+// fp32 numbers stand for c_i.
 //
 // Fragments (16x16 blocks, 64 lanes, q = lane / 16): an operand's lane holds 8
 // values of the reduction for row (or column) lane % 16, a result's lane four
@@ -56,15 +59,15 @@ struct ScanParams {
     int K;                      // chunks of a sequence
     int nseg, seg;              // segments of a sequence, chunks of a segment
     int softplus, vec;
-    float *seg_state, *seg_log; // [unit][nseg][SP][64], [unit][nseg]
-    float *bound;               // [unit][K][SP][64]: the state (or its gradient) at every chunk's border
+    int64_t ahead;              // workgroups of the state kernels that run ahead; the others run back
+    float *seg_state[2], *seg_log[2];   // ahead and back: [unit][nseg][SP][64], [unit][nseg]
+    float *bound[2];            // [unit][K][SP][64]: the state and its gradient at every chunk's border
     // gradient
     const void *dy;
     const float *dstate_out;
     void *dx, *ddt, *db, *dc;
     float *dstate;
     int64_t dy_ld, dx_ld, ddt_ld, db_ld, dc_ld;
-    const float *ubound;        // as bound, of the gradient
     float *part_head;           // [3][N * K][H]: dA, ddt_bias, dD
     float *part_b, *part_c;     // [slices][N * L][G][SP]
     int slices, heads_per_slice;
@@ -212,98 +215,162 @@ template <int NS, typename T> SEQ_DEV void write_split4(T *t, int term_stride, f
 }
 
 // ---- tiles -------------------------------------------------------------------
-// ROWS x COLS of a matrix with `ld` elements from row to row, through 256
-// threads' registers into LDS; zeros outside `rows` x `cols`, which are never
-// read (they may hold anything).
-template <typename T, int ROWS, int COLS> struct Tile {
+// ROWS x COLS of a matrix with `ld` elements from row to row, through THREADS
+// threads' registers into LDS and back, by buffer accesses: a lane's offsets
+// are the same for every chunk, and what lies outside `rows` x `cols` comes out
+// as zeros, is never read (it may hold anything) and is not written, without a
+// branch.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+template <typename T, int ROWS, int COLS, int THREADS = 256> struct Tile {
     static constexpr int VE = Frag<T>::VE;
-    static constexpr int NV = ROWS * COLS / VE / 256;
+    static constexpr int NV = ROWS * COLS / VE / THREADS;
     static constexpr int LD = COLS + Frag<T>::PAD;
     static constexpr int CV = COLS / VE;
-    static_assert(ROWS * COLS % (VE * 256) == 0, "whole vectors per thread");
-    typedef typename Pack<T, VE>::type vec_t;
-    vec_t v[NV];
+    static_assert(ROWS * COLS % (VE * THREADS) == 0, "whole vectors per thread");
+    static constexpr uint32_t kOut = 0x80000000u;       // an offset past any buffer
+    u32x4 v[NV];
 
+    // the buffer that ends with the last valid element
+    static SEQ_DEV __amdgpu_buffer_rsrc_t buffer(const T *g, int64_t ld, int rows, int cols)
+    {
+        const int bytes = rows > 0 ? (int)(((rows - 1) * ld + cols) * (int64_t)sizeof(T)) : 0;
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(g), 0, bytes, 0x00020000);
+    }
+    // A thread's k-th vector lies kStep rows behind its first, whose byte offset
+    // and column are these.  opaque() keeps the others from being computed once
+    // and held in registers.
+    static constexpr int kStep = THREADS / CV;
+    static SEQ_DEV int column() { return (int)threadIdx.x % CV * VE; }
+    static SEQ_DEV uint32_t first(int64_t ld, int cols)
+    {
+        const int r = threadIdx.x / CV, c = column();
+        return c < cols ? (uint32_t)(r * (int)ld + c) * (uint32_t)sizeof(T) : kOut;
+    }
+    static SEQ_DEV uint32_t opaque(uint32_t v)
+    {
+        asm volatile("" : "+v"(v));
+        return v;
+    }
     SEQ_DEV void load(const T *g, int64_t ld, int rows, int cols, bool vec)
     {
+        const __amdgpu_buffer_rsrc_t buf = buffer(g, ld, rows, cols);
+        const uint32_t step = (uint32_t)(kStep * (int)ld * (int)sizeof(T));
+        uint32_t o = opaque(first(ld, cols));
+        if (vec) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int e = threadIdx.x + k * 256, r = e / CV, c = (e - r * CV) * VE;
-            vec_t q = {};
-            if (r < rows && c < cols) {
-                const T *p = g + r * ld + c;
-                if (vec) {
-                    q = *reinterpret_cast<const vec_t *>(p);
-                } else {
+            for (int k = 0; k < NV; ++k) v[k] = __builtin_amdgcn_raw_buffer_load_b128(buf, o + k * step, 0, 0);
+        } else {
+            const int left = (int)opaque(cols - column());
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                if constexpr (sizeof(T) == 4) {
 #pragma unroll
                     for (int i = 0; i < VE; ++i)
-                        if (c + i < cols) q[i] = p[i];
+                        v[k][i] = __builtin_amdgcn_raw_buffer_load_b32(buf, i < left ? o + i * 4 : kOut, 0, 0);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VE; i += 2) {
+                        const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b16(buf, i < left ? o + i * 2 : kOut, 0, 0);
+                        const uint32_t hi =
+                            __builtin_amdgcn_raw_buffer_load_b16(buf, i + 1 < left ? o + i * 2 + 2 : kOut, 0, 0);
+                        v[k][i / 2] = (lo & 0xffffu) | (hi << 16);
+                    }
                 }
+                o = opaque(o + step);
             }
-            v[k] = q;
         }
     }
     SEQ_DEV void store(T *lds) const
     {
+        T *p = lds + threadIdx.x / CV * LD + column();
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int e = threadIdx.x + k * 256, r = e / CV, c = (e - r * CV) * VE;
-            *reinterpret_cast<vec_t *>(lds + r * LD + c) = v[k];
-        }
+        for (int k = 0; k < NV; ++k) *reinterpret_cast<u32x4 *>(p + k * kStep * LD) = v[k];
     }
-    // the inverse way, from LDS to memory
+    // from LDS to memory
     static SEQ_DEV void write(const T *lds, T *g, int64_t ld, int rows, int cols, bool vec)
     {
+        Tile t;
+        const T *p = lds + threadIdx.x / CV * LD + column();
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int e = threadIdx.x + k * 256, r = e / CV, c = (e - r * CV) * VE;
-            if (r >= rows || c >= cols) continue;
-            const vec_t q = *reinterpret_cast<const vec_t *>(lds + r * LD + c);
-            T *p = g + r * ld + c;
-            if (vec) {
-                *reinterpret_cast<vec_t *>(p) = q;
-            } else {
-#pragma unroll
-                for (int i = 0; i < VE; ++i)
-                    if (c + i < cols) p[i] = q[i];
-            }
-        }
+        for (int k = 0; k < NV; ++k) t.v[k] = *reinterpret_cast<const u32x4 *>(p + k * kStep * LD);
+        t.put(g, ld, rows, cols, vec);
     }
     static SEQ_DEV void write_zeros(T *g, int64_t ld, int rows, int cols, bool vec)
     {
+        Tile t;
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int e = threadIdx.x + k * 256, r = e / CV, c = (e - r * CV) * VE;
-            if (r >= rows || c >= cols) continue;
-            T *p = g + r * ld + c;
-            if (vec) {
-                *reinterpret_cast<vec_t *>(p) = vec_t{};
-            } else {
+        for (int k = 0; k < NV; ++k) t.v[k] = u32x4{0, 0, 0, 0};
+        t.put(g, ld, rows, cols, vec);
+    }
+    SEQ_DEV void put(T *g, int64_t ld, int rows, int cols, bool vec) const
+    {
+        const __amdgpu_buffer_rsrc_t buf = buffer(g, ld, rows, cols);
+        const uint32_t step = (uint32_t)(kStep * (int)ld * (int)sizeof(T));
+        uint32_t o = opaque(first(ld, cols));
+        if (vec) {
 #pragma unroll
-                for (int i = 0; i < VE; ++i)
-                    if (c + i < cols) p[i] = (T)0.0f;
+            for (int k = 0; k < NV; ++k) __builtin_amdgcn_raw_buffer_store_b128(v[k], buf, o + k * step, 0, 0);
+        } else {
+            const int left = (int)opaque(cols - column());
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+#pragma unroll
+                for (int i = 0; i < VE; ++i) {
+                    const uint32_t at = i < left ? o + i * (uint32_t)sizeof(T) : kOut;
+                    if constexpr (sizeof(T) == 4)
+                        __builtin_amdgcn_raw_buffer_store_b32(v[k][i], buf, at, 0, 0);
+                    else
+                        __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v[k][i / 2] >> (i & 1) * 16), buf, at, 0, 0);
+                }
+                o = opaque(o + step);
             }
         }
     }
 };
 
+// The compiler, left alone, reads one fragment from LDS, waits for it and
+// multiplies, and each wait is a round trip. The kernels read fragments in
+// groups, a group ahead of the products, and keep the order with this.
+SEQ_DEV void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// the wave's number in the workgroup, known to be the same in all its lanes
+SEQ_DEV int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 // ---- wave helpers --------------------------------------------------------------
-// inclusive sums over the 64 lanes
-SEQ_DEV double wave_prefix(double v, int lane)
+// One step of a sum over lanes: v of the lane that DPP control `ctrl` names, or
+// 0 where it names none or the row is masked out.
+template <int CTRL, int ROWS> SEQ_DEV float dpp(float v)
 {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const double u = __shfl_up(v, o);
-        if (lane >= o) v += u;
-    }
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
+}
+template <int CTRL, int ROWS> SEQ_DEV double dpp(double v)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)b, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROWS, 0xf, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// inclusive sums over the 64 lanes: shifts within rows of 16, then row 0's sum
+// into row 1 and 2's into 3, then the first half's into the second
+template <typename V> SEQ_DEV V wave_prefix(V v)
+{
+    v += dpp<0x111, 0xf>(v);
+    v += dpp<0x112, 0xf>(v);
+    v += dpp<0x114, 0xf>(v);
+    v += dpp<0x118, 0xf>(v);
+    v += dpp<0x142, 0xa>(v);
+    v += dpp<0x143, 0xc>(v);
     return v;
 }
-SEQ_DEV float wave_sum(float v)
+SEQ_DEV float wave_last(float v) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63)); }
+SEQ_DEV double wave_last(double v)
 {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)b, 63), hi = __builtin_amdgcn_readlane((int)(b >> 32), 63);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
+SEQ_DEV float wave_sum(float v) { return wave_last(wave_prefix(v)); }
 // the sum over the 16 lanes of a row, in every one of them
 SEQ_DEV float row_sum(float v)
 {
@@ -318,37 +385,43 @@ SEQ_DEV float row_sum(float v)
 }
 
 // Token `lane` of a chunk: the step size dt (0 behind the sequence) and the
-// running sum of log2 of the decays.  The products and the sum are in fp64:
-// the exponents used later are differences of these sums.
-SEQ_DEV void chunk_decay(float raw, bool live, float a, int softplus_on, int lane, float &dt, float &cum)
+// running sum of log2 of the decays, in fp64.
+SEQ_DEV void chunk_decay(float raw, bool live, float a, int softplus_on, float &dt, double &cum)
 {
     dt = live ? (softplus_on ? softplus(raw) : raw) : 0.0f;
-    cum = (float)wave_prefix((double)a * (double)dt * 1.4426950408889634074, lane);
+    cum = wave_prefix((double)a * (double)dt * 1.4426950408889634074);
 }
 
-SEQ_DEV float wave_last(float v) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63)); }
 
 // ---- states at the chunks' borders, and at the segments' ------------------------
 // One workgroup: 64 channels of a head, one segment of chunks, wave w the
 // channels 16w..16w+15 and all of the state (results: rows channels, columns
-// states).  REV runs from the last chunk to the first with dy, C and weights
-// e^{c_i} instead of x, B and e^{c_Q - c_j} dt_j: the state's gradient.  STORE
-// leaves the state at every chunk's near border in `bound` and starts from the
-// segment's own start; without it the segment starts from zero and leaves its
-// last state and the logarithm of its decay.
+// states).  Run back (REV) from the last chunk to the first it takes dy, C and
+// weights e^{c_i} instead of x, B and e^{c_Q - c_j} dt_j: the state's gradient.
+// STORE leaves the state at every chunk's near border in `bound` and starts
+// from the segment's own start; without it the segment starts from zero and
+// leaves its last state and the logarithm of its decay.
+template <typename T, int SP> struct StateShared {
+    static constexpr int Q = Frag<T>::Q;
+    __align__(16) T x[Q * Tile<T, Q, kPB>::LD];
+    __align__(16) T b[Q * Tile<T, Q, SP>::LD];
+    __align__(16) float w[4][Q];        // the weights of four chunks in a row
+    float tot[4];
+};
+
 template <typename T, int SP, bool REV, bool STORE>
-__global__ void __launch_bounds__(256) scan_state_kernel(ScanParams p)
+SEQ_DEV void scan_states(const ScanParams &p, int64_t block, StateShared<T, SP> &sh)
 {
     constexpr int Q = Frag<T>::Q, NT = SP / 16, NS = terms<T, 3>();
     typedef Tile<T, Q, kPB> XT;
     typedef Tile<T, Q, SP> BT;
-    __shared__ __align__(16) T sX[Q * XT::LD];
-    __shared__ __align__(16) T sB[Q * BT::LD];
-    __shared__ float sW[Q], sTot[1];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, q = lane >> 4;
+    T *sX = sh.x, *sB = sh.b;
+    float (*sW)[Q] = sh.w, *sTot = sh.tot;
+    float *seg_state = p.seg_state[REV], *seg_log = p.seg_log[REV];
+    const int lane = threadIdx.x & 63, w = wave_id(), q = lane >> 4;
     const int nseg = STORE ? p.nseg : p.nseg - 1;
-    const int64_t unit = blockIdx.x / nseg;
-    const int s0 = (int)(blockIdx.x - unit * nseg);
+    const int64_t unit = block / nseg;
+    const int s0 = (int)(block - unit * nseg);
     const int seg = STORE ? s0 : REV ? s0 + 1 : s0;      // the last segment of the run is not needed
     const int pb = (int)(unit % p.NPB);
     const int64_t nh = unit / p.NPB, n = nh / p.H;
@@ -370,7 +443,7 @@ __global__ void __launch_bounds__(256) scan_state_kernel(ScanParams p)
     const int ch = w * 16 + q * 4;      // the first of this lane's four channels
     if (STORE) {
         if (p.nseg > 1) {
-            const float *s = p.seg_state + (unit * p.nseg + seg) * (SP * kPB);
+            const float *s = seg_state + (unit * p.nseg + seg) * (SP * kPB);
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[t] = *reinterpret_cast<const f32x4 *>(s + (t * 16 + (lane & 15)) * kPB + ch);
         } else {
@@ -395,51 +468,83 @@ __global__ void __launch_bounds__(256) scan_state_kernel(ScanParams p)
         const int rows = (int)min((int64_t)Q, len - t0);
         xt.load(xg + t0 * x_ld, x_ld, rows, pcols, p.vec);
         bt.load(bg + t0 * b_ld, b_ld, rows, p.S, p.vec);
-        if (w == 0) raw = lane < rows ? (float)dg[(t0 + lane) * p.dt_ld] + bias : 0.0f;
     };
-    if (c_lo < c_live) fetch(REV ? c_live - 1 : c_lo);
+    // The chunks' decays are a long chain of scalar work: each wave does one of
+    // four chunks in a row, all at the same time, with its dt fetched ahead.
+    auto chunk_of = [&](int k) __attribute__((always_inline)) { return REV ? c_live - 1 - (k - c_lo) : k; };
+    auto fetch_dt = [&](int k) __attribute__((always_inline)) {
+        const int64_t t = (int64_t)chunk_of(k) * Q + lane;
+        raw = k < c_live && lane < Q && t < len ? (float)dg[t * p.dt_ld] + bias : 0.0f;
+    };
+    if (c_lo < c_live) {
+        fetch_dt(c_lo + w);
+        fetch(chunk_of(c_lo));
+    }
     for (int k = c_lo; k < c_live; ++k) {
-        const int c = REV ? c_live - 1 - (k - c_lo) : k;
+        const int c = chunk_of(k), slot = (k - c_lo) & 3;
         __syncthreads();
         xt.store(sX);
         bt.store(sB);
-        if (w == 0) {
-            float dt, cum;
-            chunk_decay(raw, (int64_t)c * Q + lane < len && lane < Q, a, p.softplus, lane, dt, cum);
-            const float tot = wave_last(cum);
-            if (lane < Q) sW[lane] = REV ? exp2_fast(cum) : exp2_fast(tot - cum) * dt;
-            if (lane == 0) sTot[0] = tot;
+        if (slot == 0) {
+            float dt;
+            double cum;
+            chunk_decay(raw, k + w < c_live && lane < Q && (int64_t)chunk_of(k + w) * Q + lane < len, a, p.softplus, dt, cum);
+            const double tot = wave_last(cum);
+            if (lane < Q) sW[w][lane] = REV ? exp2_fast((float)cum) : exp2_fast((float)(tot - cum)) * dt;
+            if (lane == 0) sTot[w] = (float)tot;
+            fetch_dt(k + 4 + w);
         }
         __syncthreads();
         if (k + 1 < c_live) fetch(REV ? c - 1 : c + 1);
         if (STORE) {
-            float *s = p.bound + (unit * p.K + c) * (SP * kPB);
+            float *s = p.bound[REV] + (unit * p.K + c) * (SP * kPB);
 #pragma unroll
             for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(s + (t * 16 + (lane & 15)) * kPB + ch) = acc[t];
         }
-        const float tot = sTot[0], dec = exp2_fast(tot);
+        const float tot = sTot[slot], dec = exp2_fast(tot);
         log_dec += tot;
         if (busy) {
+            constexpr int KS = Q / 32;
+            typename Frag<T>::type xf[KS], bf[KS][NT];
+            f32x4 wt[KS][2];
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                xf[ks] = read_cols(sX, XT::LD, ks * 32, w * 16, lane);
+                wt[ks][0] = *reinterpret_cast<const f32x4 *>(&sW[slot][ks * 32 + q * 8]);
+                wt[ks][1] = *reinterpret_cast<const f32x4 *>(&sW[slot][ks * 32 + q * 8 + 4]);
+            }
+            auto read_b = [&](int ks) __attribute__((always_inline)) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) bf[ks][t] = read_cols(sB, BT::LD, ks * 32, t * 16, lane);
+            };
+            read_b(0);
+            in_order();
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[t] *= dec;
+            Split<T, NS> xs[KS];
 #pragma unroll
-            for (int ks = 0; ks < Q / 32; ++ks) {
-                const typename Frag<T>::type xf = read_cols(sX, XT::LD, ks * 32, w * 16, lane);
+            for (int ks = 0; ks < KS; ++ks) {
                 float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = frag_get(xf, e) * sW[ks * 32 + q * 8 + e];
-                Split<T, NS> xs;
-                make_split(v, xs);
+                for (int e = 0; e < 8; ++e) v[e] = frag_get(xf[ks], e) * wt[ks][e / 4][e & 3];
+                make_split(v, xs[ks]);
+            }
 #pragma unroll
-                for (int t = 0; t < NT; ++t) acc[t] = mma_a(xs, read_cols(sB, BT::LD, ks * 32, t * 16, lane), acc[t]);
+            for (int ks = 0; ks < KS; ++ks) {
+                if (ks + 1 < KS) read_b(ks + 1);
+                in_order();
+#pragma unroll
+                for (int m = 0; m < NS; ++m)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) acc[t] = mma(xs[ks].f[m], bf[ks][t], acc[t]);
             }
         }
     }
     if (!STORE) {
-        float *s = p.seg_state + (unit * p.nseg + seg) * (SP * kPB);
+        float *s = seg_state + (unit * p.nseg + seg) * (SP * kPB);
 #pragma unroll
         for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(s + (t * 16 + (lane & 15)) * kPB + ch) = acc[t];
-        if (threadIdx.x == 0) p.seg_log[unit * p.nseg + seg] = log_dec;
+        if (threadIdx.x == 0) seg_log[unit * p.nseg + seg] = log_dec;
     } else if (REV && seg == 0 && p.dstate) {
         float *s = p.dstate + (nh * p.P + pb * kPB) * p.S;
 #pragma unroll
@@ -451,26 +556,43 @@ __global__ void __launch_bounds__(256) scan_state_kernel(ScanParams p)
     }
 }
 
-// Joins the segments: what each left from zero becomes the state it starts
-// from, one thread per element of the state, segments in order.
-template <int SP, bool REV> __global__ void __launch_bounds__(256) scan_join_kernel(ScanParams p)
+template <typename T, int SP, bool STORE> __global__ void __launch_bounds__(256) scan_state_kernel(ScanParams p)
 {
-    constexpr int BLK = SP * kPB / 256;
-    const int64_t unit = blockIdx.x / BLK;
-    const int e = (int)(blockIdx.x - unit * BLK) * 256 + threadIdx.x;
+    __shared__ StateShared<T, SP> sh;
+    if (blockIdx.x < p.ahead) scan_states<T, SP, false, STORE>(p, blockIdx.x, sh);
+    else scan_states<T, SP, true, STORE>(p, blockIdx.x - p.ahead, sh);
+}
+
+// Joins the segments: what each left from zero becomes the state it starts
+// from, one thread per element of the state, segments in order and eight of
+// them fetched at a time.
+template <int SP> __global__ void __launch_bounds__(256) scan_join_kernel(ScanParams p)
+{
+    constexpr int BLK = SP * kPB / 256, AT = 8;
+    const bool rev = blockIdx.x >= p.ahead;
+    const int64_t block = rev ? blockIdx.x - p.ahead : blockIdx.x, unit = block / BLK;
+    const int e = (int)(block - unit * BLK) * 256 + threadIdx.x;
     const int pb = (int)(unit % p.NPB), s = e / kPB, ch = pb * kPB + (e & (kPB - 1));
     const int64_t nh = unit / p.NPB;
-    const float *first = REV ? p.dstate_out : p.state;
+    const float *first = rev ? p.dstate_out : p.state;
     float cur = first && s < p.S && ch < p.P ? first[(nh * p.P + ch) * p.S + s] : 0.0f;
-    float *v = p.seg_state + unit * p.nseg * (SP * kPB) + e;
-    const float *lg = p.seg_log + unit * p.nseg;
-    for (int k = 0; k < p.nseg; ++k) {
-        const int seg = REV ? p.nseg - 1 - k : k;
-        const bool last = k == p.nseg - 1;
-        const float add = last ? 0.0f : v[(int64_t)seg * (SP * kPB)];
-        const float dec = last ? 0.0f : exp2_fast(lg[seg]);
-        v[(int64_t)seg * (SP * kPB)] = cur;
-        cur = fmaf(dec, cur, add);
+    float *v = p.seg_state[rev] + unit * p.nseg * (SP * kPB) + e;
+    const float *lg = p.seg_log[rev] + unit * p.nseg;
+    for (int k0 = 0; k0 < p.nseg; k0 += AT) {
+        float add[AT], dec[AT];
+#pragma unroll
+        for (int i = 0; i < AT; ++i) {
+            const int k = k0 + i, seg = rev ? p.nseg - 1 - k : k;
+            const bool on = k < p.nseg - 1;         // nothing follows the last one
+            add[i] = on ? v[(int64_t)seg * (SP * kPB)] : 0.0f;
+            dec[i] = on ? exp2_fast(lg[seg]) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < AT; ++i) {
+            const int k = k0 + i, seg = rev ? p.nseg - 1 - k : k;
+            if (k < p.nseg) v[(int64_t)seg * (SP * kPB)] = cur;
+            cur = fmaf(dec[i], cur, add[i]);
+        }
     }
 }
 
@@ -493,12 +615,14 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
     constexpr int NM = terms<T, 2>(), NX = terms<T, 3>(), MLD = Q + Frag<T>::PAD;
     typedef Tile<T, Q, kPB> XT;
     typedef Tile<T, Q, SP> BT;
+    typedef typename Frag<T>::type frag;
     __shared__ __align__(16) T sX[Q * XT::LD];
     __shared__ __align__(16) T sB[Q * BT::LD];
     __shared__ __align__(16) T sC[Q * BT::LD];
     __shared__ __align__(16) T sM[NM * Q * MLD];
-    __shared__ __align__(16) float sCum[Q], sDt[Q];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, q = lane >> 4;
+    __shared__ __align__(16) float sCum[4][Q], sLow[4][Q], sDt[4][Q], sW[4][Q], sE[4][Q];     // of four chunks: c_i, its low
+                                                                        // part, dt, e^{c_Q - c_j} dt_j, e^{c_i}
+    const int lane = threadIdx.x & 63, w = wave_id(), q = lane >> 4;
     const int64_t unit = blockIdx.x / p.nseg;
     const int seg = (int)(blockIdx.x - unit * p.nseg);
     const int pb = (int)(unit % p.NPB);
@@ -521,7 +645,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
 #pragma unroll
     for (int t = 0; t < NT; ++t) st[t] = f32x4{0, 0, 0, 0};
     if (p.nseg > 1) {
-        const float *s = p.seg_state + (unit * p.nseg + seg) * (SP * kPB) + col;
+        const float *s = p.seg_state[0] + (unit * p.nseg + seg) * (SP * kPB) + col;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -546,97 +670,154 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
         xt.load(xg + t0 * p.x_ld, p.x_ld, rows, pcols, p.vec);
         bt.load(bg + t0 * p.b_ld, p.b_ld, rows, p.S, p.vec);
         ct.load(cg + t0 * p.c_ld, p.c_ld, rows, p.S, p.vec);
-        if (w == 0) raw = lane < rows ? (float)dg[(t0 + lane) * p.dt_ld] + bias : 0.0f;
     };
-    if (c_lo < c_live) fetch(c_lo);
+    auto fetch_dt = [&](int c) __attribute__((always_inline)) {      // as in scan_state_kernel
+        const int64_t t = (int64_t)c * Q + lane;
+        raw = c < c_live && lane < Q && t < len ? (float)dg[t * p.dt_ld] + bias : 0.0f;
+    };
+    if (c_lo < c_live) {
+        fetch_dt(c_lo + w);
+        fetch(c_lo);
+    }
     for (int c = c_lo; c < c_live; ++c) {
         const int64_t t0 = (int64_t)c * Q;
+        const int slot = (c - c_lo) & 3;
+        const float *cum_ = sCum[slot], *low_ = sLow[slot], *dt_ = sDt[slot], *w_ = sW[slot], *e_ = sE[slot];
         __syncthreads();
         xt.store(sX);
         bt.store(sB);
         ct.store(sC);
-        if (w == 0) {
-            float dt, cum;
-            chunk_decay(raw, t0 + lane < len && lane < Q, a, p.softplus, lane, dt, cum);
+        if (slot == 0) {
+            float dt;
+            double cum;
+            chunk_decay(raw, c + w < c_live && lane < Q && t0 + w * Q + lane < len, a, p.softplus, dt, cum);
+            const double tot = wave_last(cum);
             if (lane < Q) {
-                sDt[lane] = dt;
-                sCum[lane] = cum;
+                sDt[w][lane] = dt;
+                sCum[w][lane] = (float)cum;
+                sLow[w][lane] = (float)(cum - (double)(float)cum);
+                sW[w][lane] = exp2_fast((float)(tot - cum)) * dt;
+                sE[w][lane] = exp2_fast((float)cum);
             }
+            fetch_dt(c + 4 + w);
         }
         __syncthreads();
         if (c + 1 < c_live) fetch(c + 1);
         // M, tile by tile: rows j, column i in a lane, so four neighbours of a row of M
+        {
+            constexpr int KN = SP / 32;
 #pragma unroll
-        for (int k = 0; k < TPW; ++k) {
-            const int t = w + 4 * k;
-            if (t < TRI) {
-                int it, jt;
-                tri_tile(t, it, jt);
-                f32x4 s = {0, 0, 0, 0};
+            for (int k = 0; k < TPW; ++k) {
+                if (w + 4 * k < TRI) {
+                    int it, jt;
+                    tri_tile(w + 4 * k, it, jt);
+                    frag bf[KN], cf[KN];
 #pragma unroll
-                for (int ks = 0; ks < SP / 32; ++ks)
-                    s = mma(read_rows(sB, BT::LD, jt * 16, ks * 32, lane), read_rows(sC, BT::LD, it * 16, ks * 32, lane), s);
-                const int i = it * 16 + (lane & 15), j = jt * 16 + q * 4;
-                const float ci = sCum[i];
-                const f32x4 cj = *reinterpret_cast<const f32x4 *>(sCum + j), dj = *reinterpret_cast<const f32x4 *>(sDt + j);
+                    for (int ks = 0; ks < KN; ++ks) {
+                        bf[ks] = read_rows(sB, BT::LD, jt * 16, ks * 32, lane);
+                        cf[ks] = read_rows(sC, BT::LD, it * 16, ks * 32, lane);
+                    }
+                    const int i = it * 16 + (lane & 15), j = jt * 16 + q * 4;
+                    const f32x4 dj = *reinterpret_cast<const f32x4 *>(dt_ + j);
+                    f32x4 ex = cum_[i] - *reinterpret_cast<const f32x4 *>(cum_ + j);
+                    if (sizeof(T) == 4) ex += low_[i] - *reinterpret_cast<const f32x4 *>(low_ + j);   // y is fp32
+                    in_order();
+                    f32x4 s = {0, 0, 0, 0};
 #pragma unroll
-                for (int r = 0; r < 4; ++r) s[r] = i >= j + r ? s[r] * exp2_fast(ci - cj[r]) * dj[r] : 0.0f;
-                write_split4<NM>(sM + i * MLD + j, Q * MLD, s);
+                    for (int ks = 0; ks < KN; ++ks) s = mma(bf[ks], cf[ks], s);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) s[r] = i >= j + r ? s[r] * exp2_fast(ex[r]) * dj[r] : 0.0f;
+                    write_split4<NM>(sM + i * MLD + j, Q * MLD, s);
+                }
             }
         }
         __syncthreads();
         if (busy) {
+            constexpr int KQ = Q / 32, KN = SP / 32;
+            frag xf[KQ], cf[2][NI], mf[NI][NM], bf[NT];
             f32x4 y[NI];
+            auto read_c = [&](int ks) __attribute__((always_inline)) {
+#pragma unroll
+                for (int it = 0; it < NI; ++it) cf[ks & 1][it] = read_rows_stacked(sC, BT::LD, it * 16, ks * 32, lane);
+            };
+            auto read_m = [&](int ks) __attribute__((always_inline)) {
+#pragma unroll
+                for (int it = 2 * ks; it < NI; ++it)
+#pragma unroll
+                    for (int m = 0; m < NM; ++m) mf[it][m] = read_rows(sM + m * Q * MLD, MLD, it * 16, ks * 32, lane);
+            };
+            auto read_b = [&](int ks) __attribute__((always_inline)) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) bf[t] = read_cols(sB, BT::LD, ks * 32, t * 16, lane);
+            };
 #pragma unroll
             for (int it = 0; it < NI; ++it) y[it] = f32x4{0, 0, 0, 0};
-            // e^{c_i} h_0 C_i
+            read_c(0);
+            // e^{c_i} h_0 C_i, the next fragments on their way
 #pragma unroll
-            for (int ks = 0; ks < SP / 32; ++ks) {
+            for (int ks = 0; ks < KN; ++ks) {
+                if (ks + 1 < KN) {
+                    read_c(ks + 1);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < KQ; ++k) xf[k] = read_cols(sX, XT::LD, k * 32, w * 16, lane);
+                    read_m(0);
+                }
+                in_order();
                 float v[8];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = st[2 * ks][e], v[4 + e] = st[2 * ks + 1][e];
                 Split<T, NM> hs;
                 make_split(v, hs);
 #pragma unroll
-                for (int it = 0; it < NI; ++it)
-                    y[it] = mma_b(read_rows_stacked(sC, BT::LD, it * 16, ks * 32, lane), hs, y[it]);
+                for (int m = 0; m < NM; ++m)
+#pragma unroll
+                    for (int it = 0; it < NI; ++it) y[it] = mma(cf[ks & 1][it], hs.f[m], y[it]);
+                in_order();
             }
 #pragma unroll
-            for (int it = 0; it < NI; ++it) {
-                const f32x4 ci = *reinterpret_cast<const f32x4 *>(sCum + it * 16 + q * 4);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) y[it][r] *= exp2_fast(ci[r]);
-            }
-            const float tot = sCum[Q - 1], dec = exp2_fast(tot);
+            for (int it = 0; it < NI; ++it) y[it] *= *reinterpret_cast<const f32x4 *>(e_ + it * 16 + q * 4);
+            const float dec = e_[Q - 1];
 #pragma unroll
             for (int t = 0; t < NT; ++t) st[t] *= dec;
+            T xr[NI][4];
 #pragma unroll
-            for (int ks = 0; ks < Q / 32; ++ks) {
-                const typename Frag<T>::type xf = read_cols(sX, XT::LD, ks * 32, w * 16, lane);
+            for (int ks = 0; ks < KQ; ++ks) {
+                in_order();
+                read_b(ks);
+                const f32x4 w0 = *reinterpret_cast<const f32x4 *>(w_ + ks * 32 + q * 8);
+                const f32x4 w1 = *reinterpret_cast<const f32x4 *>(w_ + ks * 32 + q * 8 + 4);
+                in_order();
 #pragma unroll
-                for (int it = 2 * ks; it < NI; ++it)
+                for (int m = 0; m < NM; ++m)
 #pragma unroll
-                    for (int m = 0; m < NM; ++m)
-                        y[it] = mma(read_rows(sM + m * Q * MLD, MLD, it * 16, ks * 32, lane), xf, y[it]);
+                    for (int it = 2 * ks; it < NI; ++it) y[it] = mma(mf[it][m], xf[ks], y[it]);
                 float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int j = ks * 32 + q * 8 + e;
-                    v[e] = frag_get(xf, e) * (exp2_fast(tot - sCum[j]) * sDt[j]);
-                }
+                for (int e = 0; e < 8; ++e) v[e] = frag_get(xf[ks], e) * (e < 4 ? w0[e & 3] : w1[e & 3]);
                 Split<T, NX> xs;
                 make_split(v, xs);
+                in_order();
+                if (ks + 1 < KQ) {
+                    read_m(ks + 1);
+                } else {
 #pragma unroll
-                for (int t = 0; t < NT; ++t) st[t] = mma_b(read_cols(sB, BT::LD, ks * 32, t * 16, lane), xs, st[t]);
+                    for (int it = 0; it < NI; ++it)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) xr[it][r] = sX[(it * 16 + q * 4 + r) * XT::LD + col];
+                }
+                in_order();
+#pragma unroll
+                for (int m = 0; m < NX; ++m)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) st[t] = mma(bf[t], xs.f[m], st[t]);
             }
             // y in place of this wave's own columns of x
 #pragma unroll
             for (int it = 0; it < NI; ++it)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    T *o = sX + (it * 16 + q * 4 + r) * XT::LD + col;
-                    *o = (T)fmaf(skip, (float)*o, y[it][r]);
-                }
+                for (int r = 0; r < 4; ++r)
+                    sX[(it * 16 + q * 4 + r) * XT::LD + col] = (T)fmaf(skip, (float)xr[it][r], y[it][r]);
         }
         __syncthreads();
         // rows behind the sequence come out as zeros: x and C are zeros there
@@ -676,9 +857,9 @@ template <typename T, int SP> __global__ void __launch_bounds__(256) scan_bwd_ke
     __shared__ __align__(16) T sB[Q * BT::LD], sC[Q * BT::LD];
     __shared__ __align__(16) T sM[NS * Q * MLD];                      // [term][j][i]
     __shared__ __align__(16) T sU[NS * SP * ULD];                     // [term][state][channel]
-    __shared__ __align__(16) float sCum[Q], sDt[Q];
-    __shared__ float sRow[NI][Q], sCol[NI][Q], sCd[4][Q], sE[4][Q], sDot[4], sDD[4];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, q = lane >> 4, l16 = lane & 15;
+    __shared__ __align__(16) float sCum[Q], sLow[Q], sDt[Q], sW[Q], sE[Q];   // as in the forward, but sW without dt_j
+    __shared__ float sRow[NI][Q], sCol[NI][Q], sCd[4][Q], sXd[4][Q], sDot[4], sDD[4];
+    const int lane = threadIdx.x & 63, w = wave_id(), q = lane >> 4, l16 = lane & 15;
     const int slice = (int)(blockIdx.x % p.slices);
     const int64_t ng = blockIdx.x / p.slices;
     const int g = (int)(ng % p.G);
@@ -731,11 +912,12 @@ template <typename T, int SP> __global__ void __launch_bounds__(256) scan_bwd_ke
     for (int hh = h_lo; hh < h_hi; ++hh) {
         const int h = g * hpg + hh;
         const float a = p.a[h], skip = p.d ? p.d[h] : 0.0f;
-        float raw = 0.0f, dt = 0.0f, cum = 0.0f;
+        float raw = 0.0f, dt = 0.0f;
+        double cum = 0.0;
         float rs = 0.0f, cs = 0.0f, cd = 0.0f, ee = 0.0f, dot = 0.0f, dd = 0.0f;    // wave 0: per token, over the channel blocks
         if (w == 0) {
             if (lane < rows) raw = (float)((const T *)p.dt)[(base + lane) * p.dt_ld + h] + (p.dt_bias ? p.dt_bias[h] : 0.0f);
-            chunk_decay(raw, lane < rows, a, p.softplus, lane, dt, cum);
+            chunk_decay(raw, lane < rows, a, p.softplus, dt, cum);
         }
         for (int pb = 0; pb < p.NPB; ++pb) {
             const int pcols = min(kPB, p.P - pb * kPB);
@@ -753,8 +935,8 @@ template <typename T, int SP> __global__ void __launch_bounds__(256) scan_bwd_ke
                     h0[k][b] = u[k][b] = f32x4{0, 0, 0, 0};
                     if (w + 4 * k < NT && rows > 0) {
                         const int64_t o = bo + ((w + 4 * k) * 16 + l16) * kPB + b * 16 + q * 4;
-                        h0[k][b] = *reinterpret_cast<const f32x4 *>(p.bound + o);
-                        u[k][b] = *reinterpret_cast<const f32x4 *>(p.ubound + o);
+                        h0[k][b] = *reinterpret_cast<const f32x4 *>(p.bound[0] + o);
+                        u[k][b] = *reinterpret_cast<const f32x4 *>(p.bound[1] + o);
                     }
                 }
             float part = 0.0f;
@@ -769,8 +951,12 @@ template <typename T, int SP> __global__ void __launch_bounds__(256) scan_bwd_ke
             xt.store(sX);
             yt.store(sY);
             if (w == 0 && lane < Q) {
+                const double tot = wave_last(cum);
                 sDt[lane] = dt;
-                sCum[lane] = cum;
+                sCum[lane] = (float)cum;
+                sLow[lane] = (float)(cum - (double)(float)cum);
+                sW[lane] = exp2_fast((float)(tot - cum));
+                sE[lane] = exp2_fast((float)cum);
             }
             if (lane == 0) sDot[w] = part;
 #pragma unroll
@@ -780,7 +966,6 @@ template <typename T, int SP> __global__ void __launch_bounds__(256) scan_bwd_ke
                     if (w + 4 * k < NT)
                         write_split4<NS>(sU + ((w + 4 * k) * 16 + l16) * ULD + b * 16 + q * 4, SP * ULD, u[k][b]);
             __syncthreads();
-            const float tot = sCum[Q - 1];
             // dP, M and dS, tile by tile; M goes to LDS transposed (rows j)
             float diag = 0.0f;
 #pragma unroll
@@ -794,13 +979,14 @@ template <typename T, int SP> __global__ void __launch_bounds__(256) scan_bwd_ke
                     for (int ks = 0; ks < 2; ++ks)
                         dp = mma(read_rows(sY, XT::LD, it * 16, ks * 32, lane), read_rows(sX, XT::LD, jt * 16, ks * 32, lane), dp);
                     const int i = it * 16 + q * 4, j = jt * 16 + l16;
-                    const float cj = sCum[j], dj = sDt[j];
-                    const f32x4 ci = *reinterpret_cast<const f32x4 *>(sCum + i);
+                    const float dj = sDt[j];
+                    const f32x4 ex = (*reinterpret_cast<const f32x4 *>(sCum + i) - sCum[j]) +
+                                     (*reinterpret_cast<const f32x4 *>(sLow + i) - sLow[j]);
                     float col = 0.0f;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const bool in = i + r >= j;
-                        const float dec = in ? exp2_fast(ci[r] - cj) : 0.0f;
+                        const float dec = in ? exp2_fast(ex[r]) : 0.0f;
                         if (i + r == j) diag += dp[r];
                         m[r] = in ? sc[k][r] * dec : 0.0f;
                         const float s = in ? dp[r] * dec * dj : 0.0f;
@@ -849,14 +1035,15 @@ template <typename T, int SP> __global__ void __launch_bounds__(256) scan_bwd_ke
                             ac = mma_b(read_rows_stacked(sY, XT::LD, it * 16, ks * 32, lane), hs[ks], ac);
                             ab = mma_b(read_rows_stacked(sX, XT::LD, it * 16, ks * 32, lane), us[ks], ab);
                         }
-                        const f32x4 ci = *reinterpret_cast<const f32x4 *>(sCum + it * 16 + q * 4);
-                        const f32x4 di = *reinterpret_cast<const f32x4 *>(sDt + it * 16 + q * 4);
+                        const f32x4 ei = *reinterpret_cast<const f32x4 *>(sE + it * 16 + q * 4);
+                        const f32x4 wi = *reinterpret_cast<const f32x4 *>(sW + it * 16 + q * 4) *
+                                         *reinterpret_cast<const f32x4 *>(sDt + it * 16 + q * 4);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const float v = ac[r] * exp2_fast(ci[r]);
+                            const float v = ac[r] * ei[r];
                             dC[it][k][r] += v;
                             cdp[it][r] = fmaf(v, cv[it][k][r], cdp[it][r]);
-                            dB[it][k][r] = fmaf(ab[r], exp2_fast(tot - ci[r]) * di[r], dB[it][k][r]);
+                            dB[it][k][r] = fmaf(ab[r], wi[r], dB[it][k][r]);
                         }
                     }
                 }
@@ -887,11 +1074,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(256) scan_bwd_ke
                     }
                 }
 #pragma unroll
-                for (int jt = 0; jt < NI; ++jt) {
-                    const f32x4 cj = *reinterpret_cast<const f32x4 *>(sCum + jt * 16 + q * 4);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) dx[jt][r] *= exp2_fast(tot - cj[r]);
-                }
+                for (int jt = 0; jt < NI; ++jt) dx[jt] *= *reinterpret_cast<const f32x4 *>(sW + jt * 16 + q * 4);
 #pragma unroll
                 for (int ks = 0; ks < Q / 32; ++ks) {
                     const frag yf = read_cols(sY, XT::LD, ks * 32, w * 16, lane);
@@ -908,7 +1091,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(256) scan_bwd_ke
                     for (int r = 0; r < 4; ++r) {
                         const int o = (jt * 16 + q * 4 + r) * XT::LD + w * 16 + l16;
                         const float s = row_sum((float)sX[o] * dx[jt][r]);
-                        if (l16 == 0) sE[w][jt * 16 + q * 4 + r] = s;
+                        if (l16 == 0) sXd[w][jt * 16 + q * 4 + r] = s;
                         sX[o] = (T)fmaf(skip, (float)sY[o], dj[r] * dx[jt][r]);     // this wave's own columns
                     }
                 }
@@ -920,17 +1103,17 @@ template <typename T, int SP> __global__ void __launch_bounds__(256) scan_bwd_ke
 #pragma unroll
                     for (int t = 0; t < NI; ++t) rs += sRow[t][lane], cs += sCol[t][lane];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) cd += sCd[t][lane], ee += sE[t][lane];
+                    for (int t = 0; t < 4; ++t) cd += sCd[t][lane], ee += sXd[t][lane];
                 }
                 dot += (sDot[0] + sDot[1]) + (sDot[2] + sDot[3]);
                 dd += (sDD[0] + sDD[1]) + (sDD[2] + sDD[3]);
             }
         }
         if (w == 0) {
-            const float tot = wave_last(cum);
+            const float tot = (float)wave_last(cum);
             const double before = (double)dt * ee - cs, behind = (double)rs - cs + cd;
-            const double b1 = wave_prefix(before, lane), b2 = wave_prefix(behind, lane);
-            const double all2 = __shfl(b2, 63);
+            const double b1 = wave_prefix(before), b2 = wave_prefix(behind);
+            const double all2 = wave_last(b2);
             const float dl = (float)((b1 - before) + (all2 - b2 + behind) + (double)(exp2_fast(tot) * dot));
             float draw = fmaf(a, dl, ee);
             if (p.softplus) draw *= 1.0f / (1.0f + expf(-raw));
@@ -993,40 +1176,42 @@ template <typename T, int SP> __global__ void __launch_bounds__(256) scan_bwd_ke
     }
 }
 
-// dB and dC from the head slices' parts, in their order
-template <typename T, int SP> __global__ void __launch_bounds__(256) scan_reduce_bc_kernel(ScanParams p)
+// What the chunks and head slices left: the first 3 H workgroups add dA,
+// ddt_bias and dD of a head over the chunks, the others dB and dC over the head
+// slices, all in a fixed order.
+template <typename T, int SP>
+__global__ void __launch_bounds__(256) scan_reduce_kernel(ScanParams p, float *da, float *dbias, float *dd)
 {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, rows = (int64_t)p.N * p.L * p.G;
+    if (blockIdx.x < 3u * p.H) {
+        __shared__ double red[256];
+        const int which = blockIdx.x / p.H, h = blockIdx.x - which * p.H;
+        const int64_t NK = (int64_t)p.N * p.K;
+        float *out = which == 0 ? da : which == 1 ? dbias : dd;
+        if (!out) return;
+        double s = 0.0;
+        for (int64_t i = threadIdx.x; i < NK; i += 256) s += p.part_head[(which * NK + i) * p.H + h];
+        red[threadIdx.x] = s;
+        __syncthreads();
+        for (int o = 128; o > 0; o >>= 1) {
+            if (threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
+            __syncthreads();
+        }
+        if (threadIdx.x == 0) out[h] = (float)red[0];
+        return;
+    }
+    const int64_t id = ((int64_t)blockIdx.x - 3 * p.H) * 256 + threadIdx.x, rows = (int64_t)p.N * p.L * p.G;
     if (id >= rows * SP) return;
     const int64_t rg = id / SP, row = rg / p.G;
     const int s = (int)(id - rg * SP), g = (int)(rg - row * p.G);
     if (s >= p.S) return;
     float b = 0.0f, c = 0.0f;
+#pragma unroll 4
     for (int k = 0; k < p.slices; ++k) {
         b += p.part_b[k * rows * SP + id];
         c += p.part_c[k * rows * SP + id];
     }
     ((T *)p.db)[row * p.db_ld + g * p.S + s] = (T)b;
     ((T *)p.dc)[row * p.dc_ld + g * p.S + s] = (T)c;
-}
-
-// dA, ddt_bias and dD of a head: the chunks' parts in a fixed order
-__global__ void __launch_bounds__(256) scan_reduce_heads_kernel(const float *part, float *da, float *dbias, float *dd,
-                                                                int64_t NK, int H)
-{
-    __shared__ double red[256];
-    const int which = blockIdx.x / H, h = blockIdx.x - which * H;
-    float *out = which == 0 ? da : which == 1 ? dbias : dd;
-    if (!out) return;
-    double s = 0.0;
-    for (int64_t i = threadIdx.x; i < NK; i += 256) s += part[(which * NK + i) * H + h];
-    red[threadIdx.x] = s;
-    __syncthreads();
-    for (int o = 128; o > 0; o >>= 1) {
-        if (threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) out[h] = (float)red[0];
 }
 
 // ---- one token -----------------------------------------------------------------
@@ -1041,7 +1226,7 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p, int lpr, int blocks)
 {
     constexpr int V = 4;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, w = wave_id();
     const int64_t nh = blockIdx.x / blocks, n = nh / p.H;
     const int blk = (int)(blockIdx.x - nh * blocks), h = (int)(nh - n * p.H), g = h / (p.H / p.G);
     const int per = 64 / lpr;                       // channels side by side in a wave

@@ -25,7 +25,8 @@ struct conv_scan_plan {
     int bnseg, bseg;                     // the same of the gradient's state passes
     int slices, heads_per_slice;
     int64_t ws_bytes, bwd_ws_bytes;
-    int64_t o_log, o_bound, o_ubound, o_head, o_pb, o_pc;   // byte offsets in the gradient's workspace
+    int64_t o_fwd_log;                   // byte offsets in the forward's workspace and in the gradient's
+    int64_t o_seg[2], o_log[2], o_bound[2], o_head, o_pb, o_pc;
     char text[320];
 };
 
@@ -84,8 +85,10 @@ conv_status_t check_rows(const Rows *t, int n)
         if (t[i].ld < t[i].width)
             return fail(CONV_ERR_INVALID_ARG, "%s: %lld elements from token to token, a row has %lld", t[i].name,
                         (long long)t[i].ld, (long long)t[i].width);
-        if ((double)t[i].ld * t[i].esz * std::max<int64_t>(1, t[i].rows) > kMaxBytes)
-            return fail(CONV_ERR_UNSUPPORTED, "%s: beyond the address space", t[i].name);
+        // a chunk of 64 tokens is addressed by 32-bit byte offsets
+        if ((double)t[i].ld * t[i].esz * std::max<int64_t>(1, t[i].rows) > kMaxBytes ||
+            (t[i].rows > 1 && t[i].ld * t[i].esz >= int64_t(1) << 25))
+            return fail(CONV_ERR_UNSUPPORTED, "%s: %lld elements from token to token", t[i].name, (long long)t[i].ld);
     }
     return CONV_OK;
 }
@@ -178,44 +181,46 @@ int64_t bwd_blocks(const conv_causal_desc_t &d)   // workgroups along a sequence
 }
 
 // ---- scan ------------------------------------------------------------------------
-template <typename T, int SP> struct ScanLaunch {
-    static void fwd(const ScanParams &p, int64_t units, int64_t, hipStream_t s)
-    {
-        const unsigned blk = SP * kPB / 256;
-        if (p.nseg > 1) {
-            hipLaunchKernelGGL((scan_state_kernel<T, SP, false, false>), dim3((unsigned)(units * (p.nseg - 1))), dim3(256), 0, s, p);
-            hipLaunchKernelGGL((scan_join_kernel<SP, false>), dim3((unsigned)(units * blk)), dim3(256), 0, s, p);
-        }
-        hipLaunchKernelGGL((scan_fwd_kernel<T, SP>), dim3((unsigned)(units * p.nseg)), dim3(256), 0, s, p);
-    }
-    static void bwd(const ScanParams &q, int64_t units, int64_t grid, hipStream_t s)
-    {
-        ScanParams p = q;
-        const unsigned blk = SP * kPB / 256, segs = (unsigned)(units * (p.nseg - 1));
-        if (p.nseg > 1) {
-            hipLaunchKernelGGL((scan_state_kernel<T, SP, false, false>), dim3(segs), dim3(256), 0, s, p);
-            hipLaunchKernelGGL((scan_join_kernel<SP, false>), dim3((unsigned)(units * blk)), dim3(256), 0, s, p);
-        }
-        hipLaunchKernelGGL((scan_state_kernel<T, SP, false, true>), dim3((unsigned)(units * p.nseg)), dim3(256), 0, s, p);
-        p.bound = const_cast<float *>(q.ubound);
-        if (p.nseg > 1) {
-            hipLaunchKernelGGL((scan_state_kernel<T, SP, true, false>), dim3(segs), dim3(256), 0, s, p);
-            hipLaunchKernelGGL((scan_join_kernel<SP, true>), dim3((unsigned)(units * blk)), dim3(256), 0, s, p);
-        }
-        hipLaunchKernelGGL((scan_state_kernel<T, SP, true, true>), dim3((unsigned)(units * p.nseg)), dim3(256), 0, s, p);
-        hipLaunchKernelGGL((scan_bwd_kernel<T, SP>), dim3((unsigned)grid), dim3(256), 0, s, q);
-        if (p.slices > 1 && p.L > 0)
-            hipLaunchKernelGGL((scan_reduce_bc_kernel<T, SP>), dim3((unsigned)(((int64_t)p.N * p.L * p.G * SP + 255) / 256)),
-                               dim3(256), 0, s, q);
-    }
+// Where the gradients of A, dt_bias and D go.
+struct HeadGrads {
+    float *da, *dbias, *dd;
 };
 
-template <typename T> void launch_scan(bool bwd, int SP, const ScanParams &p, int64_t units, int64_t grid, hipStream_t s)
+// The states that the segments start from, in both directions for a gradient.
+template <typename T, int SP> void launch_segments(ScanParams p, int64_t units, int ways, hipStream_t s)
 {
-    auto f = SP == 32 ? (bwd ? ScanLaunch<T, 32>::bwd : ScanLaunch<T, 32>::fwd)
-           : SP == 64 ? (bwd ? ScanLaunch<T, 64>::bwd : ScanLaunch<T, 64>::fwd)
-                      : (bwd ? ScanLaunch<T, 128>::bwd : ScanLaunch<T, 128>::fwd);
-    f(p, units, grid, s);
+    if (p.nseg <= 1) return;
+    p.ahead = units * (p.nseg - 1);
+    hipLaunchKernelGGL((scan_state_kernel<T, SP, false>), dim3((unsigned)(ways * p.ahead)), dim3(256), 0, s, p);
+    p.ahead = units * (SP * kPB / 256);
+    hipLaunchKernelGGL((scan_join_kernel<SP>), dim3((unsigned)(ways * p.ahead)), dim3(256), 0, s, p);
+}
+
+template <typename T, int SP> void launch_fwd(const ScanParams &p, int64_t units, hipStream_t s)
+{
+    launch_segments<T, SP>(p, units, 1, s);
+    hipLaunchKernelGGL((scan_fwd_kernel<T, SP>), dim3((unsigned)(units * p.nseg)), dim3(256), 0, s, p);
+}
+
+template <typename T, int SP> void launch_bwd(ScanParams p, int64_t units, HeadGrads g, hipStream_t s)
+{
+    if (p.N > 0) {
+        launch_segments<T, SP>(p, units, 2, s);
+        p.ahead = units * p.nseg;
+        hipLaunchKernelGGL((scan_state_kernel<T, SP, true>), dim3((unsigned)(2 * p.ahead)), dim3(256), 0, s, p);
+        const int64_t grid = (int64_t)p.N * p.K * p.G * p.slices;
+        hipLaunchKernelGGL((scan_bwd_kernel<T, SP>), dim3((unsigned)grid), dim3(256), 0, s, p);
+    }
+    const int64_t elems = p.slices > 1 ? (int64_t)p.N * p.L * p.G * SP : 0;
+    hipLaunchKernelGGL((scan_reduce_kernel<T, SP>), dim3((unsigned)(3 * p.H + (elems + 255) / 256)), dim3(256), 0, s, p,
+                       g.da, g.dbias, g.dd);       // no sequences: zeros
+}
+
+template <typename T> void launch_scan(int SP, const ScanParams &p, int64_t units, const HeadGrads *g, hipStream_t s)
+{
+    if (SP == 32) return g ? launch_bwd<T, 32>(p, units, *g, s) : launch_fwd<T, 32>(p, units, s);
+    if (SP == 64) return g ? launch_bwd<T, 64>(p, units, *g, s) : launch_fwd<T, 64>(p, units, s);
+    return g ? launch_bwd<T, 128>(p, units, *g, s) : launch_fwd<T, 128>(p, units, s);
 }
 
 // Segments of K chunks so that `units` heads give about `want` workgroups.
@@ -416,10 +421,10 @@ conv_status_t conv_scan_create(const conv_scan_desc_t *desc, conv_scan_plan_t **
     pl->K = (int)std::max<int64_t>(1, (d.L + pl->Q - 1) / pl->Q);
     pl->NPB = (int)((d.P + kPB - 1) / kPB);
     const double units = (double)d.N * d.H * pl->NPB, tile = (double)pl->SP * kPB * 4;
-    const double grids = std::max(units * std::max<double>(pl->K, 32), (double)d.N * pl->K * d.H);
+    const double grids = std::max(2 * units * std::max<double>(pl->K, 32), (double)d.N * pl->K * d.H);
     const double rows = (double)d.N * d.L * d.G * pl->SP;
     // no grid is larger than one workgroup per unit and chunk, or per 256 elements of dB
-    if (grids >= 2147483000.0 || rows / 256.0 >= 2147483000.0 || units * (pl->K + 1) * tile * 3 >= kMaxBytes ||
+    if (grids >= 2147483000.0 || rows / 256.0 + 3.0 * d.H >= 2147483000.0 || units * (pl->K + 1) * tile * 4 >= kMaxBytes ||
         3.0 * d.H >= 2147483000.0) {
         delete pl;
         return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
@@ -436,14 +441,17 @@ conv_status_t conv_scan_create(const conv_scan_desc_t *desc, conv_scan_plan_t **
     pl->slices = (int)((hpg + pl->heads_per_slice - 1) / pl->heads_per_slice);
     const int64_t t = (int64_t)pl->SP * kPB * 4;
     auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
-    pl->ws_bytes = pl->nseg > 1 ? up(pl->units * pl->nseg * t) + up(pl->units * pl->nseg * 4) : 0;
-    int64_t o = pl->bnseg > 1 ? up(pl->units * pl->bnseg * t) : 0;
-    pl->o_log = o;
-    o += pl->bnseg > 1 ? up(pl->units * pl->bnseg * 4) : 0;
-    pl->o_bound = o;
-    o += up(pl->units * pl->K * t);
-    pl->o_ubound = o;
-    o += up(pl->units * pl->K * t);
+    pl->o_fwd_log = pl->nseg > 1 ? up(pl->units * pl->nseg * t) : 0;
+    pl->ws_bytes = pl->o_fwd_log + (pl->nseg > 1 ? up(pl->units * pl->nseg * 4) : 0);
+    int64_t o = 0;
+    for (int k = 0; k < 2; ++k) {
+        pl->o_seg[k] = o;
+        o += pl->bnseg > 1 ? up(pl->units * pl->bnseg * t) : 0;
+        pl->o_log[k] = o;
+        o += pl->bnseg > 1 ? up(pl->units * pl->bnseg * 4) : 0;
+        pl->o_bound[k] = o;
+        o += up(pl->units * pl->K * t);
+    }
     pl->o_head = o;
     o += up(3 * d.N * pl->K * d.H * 4);
     pl->o_pb = o;
@@ -539,12 +547,14 @@ static conv_status_t scan_forward(const conv_scan_plan_t *plan, const conv_scan_
     }
     p.nseg = plan->nseg;
     p.seg = plan->seg;
-    p.seg_state = (float *)ws;
-    p.seg_log = plan->nseg > 1 ? (float *)((char *)ws + plan->ws_bytes - (plan->units * plan->nseg * 4 + 255) / 256 * 256) : nullptr;
+    if (plan->nseg > 1) {
+        p.seg_state[0] = (float *)ws;
+        p.seg_log[0] = (float *)((char *)ws + plan->o_fwd_log);
+    }
     const Rows vec[] = {in[0], in[1], in[2], out[0]};
     p.vec = scan_vector(*plan, vec, 4);
-    if (d.dtype == CONV_DT_BF16) launch_scan<bf16_t>(false, plan->SP, p, plan->units, 0, s);
-    else launch_scan<float>(false, plan->SP, p, plan->units, 0, s);
+    if (d.dtype == CONV_DT_BF16) launch_scan<bf16_t>(plan->SP, p, plan->units, nullptr, s);
+    else launch_scan<float>(plan->SP, p, plan->units, nullptr, s);
     return launched();
 }
 
@@ -606,10 +616,11 @@ conv_status_t conv_scan_bwd_run(const conv_scan_plan_t *plan, const conv_scan_bw
     p.vec = scan_vector(*plan, vec, 5);
     char *ws = (char *)workspace;
     p.nseg = plan->bnseg; p.seg = plan->bseg;
-    p.seg_state = (float *)ws;
-    p.seg_log = (float *)(ws + plan->o_log);
-    p.bound = (float *)(ws + plan->o_bound);
-    p.ubound = (float *)(ws + plan->o_ubound);
+    for (int k = 0; k < 2; ++k) {
+        p.seg_state[k] = (float *)(ws + plan->o_seg[k]);
+        p.seg_log[k] = (float *)(ws + plan->o_log[k]);
+        p.bound[k] = (float *)(ws + plan->o_bound[k]);
+    }
     p.part_head = (float *)(ws + plan->o_head);
     p.part_b = (float *)(ws + plan->o_pb);
     p.part_c = (float *)(ws + plan->o_pc);
@@ -617,14 +628,9 @@ conv_status_t conv_scan_bwd_run(const conv_scan_plan_t *plan, const conv_scan_bw
     p.heads_per_slice = plan->heads_per_slice;
     hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
-    const int64_t NK = d.N * plan->K;
-    if (d.N > 0) {
-        const int64_t grid = NK * d.G * plan->slices;
-        if (d.dtype == CONV_DT_BF16) launch_scan<bf16_t>(true, plan->SP, p, plan->units, grid, s);
-        else launch_scan<float>(true, plan->SP, p, plan->units, grid, s);
-    }
-    hipLaunchKernelGGL(scan_reduce_heads_kernel, dim3((unsigned)(3 * d.H)), dim3(256), 0, s, p.part_head, a->da,
-                       a->ddt_bias, a->dd, NK, (int)d.H);      // no sequences: zeros
+    const HeadGrads g = {a->da, a->ddt_bias, a->dd};
+    if (d.dtype == CONV_DT_BF16) launch_scan<bf16_t>(plan->SP, p, plan->units, &g, s);
+    else launch_scan<float>(plan->SP, p, plan->units, &g, s);
     return launched();
 }
 

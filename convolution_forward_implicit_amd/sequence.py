@@ -33,15 +33,15 @@ class _Plan:
     @staticmethod
     def _dense(t, shape, dtype, dev, name):
         """Address of a contiguous tensor of this shape and type on `dev`."""
+        if t.dtype is dtype and t.is_cuda and t.get_device() == dev.index and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
         if t.device != dev or dev.type != "cuda":
             raise ValueError("%s must be on the cuda device of the other tensors (%s), got %s" % (name, dev, t.device))
         if t.dtype != dtype:
             raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
         if t.shape != shape:
             raise ValueError("%s has shape %r, expected %r" % (name, tuple(t.shape), shape))
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-        return t.data_ptr()
+        raise ValueError("%s must be contiguous" % name)
 
     def _rows(self, t, lead, inner, dtype, dev, name):
         """(address, elements from token to token) of a tensor lead + inner
@@ -74,18 +74,18 @@ class _Plan:
 
     @staticmethod
     def _on(torch, dev, stream):
-        """The stream to use, and the contexts in which to allocate and launch
-        for it: memory that is released when a call returns belongs to the
-        stream that used it."""
+        """(stream handle, context): the stream to use, and, where it is not the
+        current one of the current device, the context to allocate and launch in:
+        memory that is released when a call returns belongs to the stream that
+        used it."""
         if dev.type != "cuda":
             raise ValueError("tensors must be on a cuda device, got %s" % dev)
-        current = torch.cuda.current_stream(dev)
         if stream is None:
-            stream = current
-        away = None
-        if stream != current or torch.cuda.current_device() != dev.index:
-            away = torch.cuda.stream(stream)       # also makes its device the current one
-        return stream, away
+            if torch.cuda.current_device() == dev.index:
+                # the handle alone: building the Stream object takes as long as a launch
+                return torch._C._cuda_getCurrentRawStream(dev.index), None
+            stream = torch.cuda.current_stream(dev)
+        return stream.cuda_stream, torch.cuda.stream(stream)       # also makes its device the current one
 
 
 class CausalConv(_Plan):
@@ -131,10 +131,10 @@ class CausalConv(_Plan):
             None if lengths is None else self._dense(lengths, self.x_shape[:1], torch.int32, dev, "lengths"), yp,
             None if state_out is None else self._dense(state_out, self.state_shape, t, dev, "state_out"), x_ld, y_ld)
         if away is None:
-            capi.conv_causal_run(self._plan, byref(args), stream.cuda_stream)
+            capi.conv_causal_run(self._plan, byref(args), stream)
         else:
             with away:
-                capi.conv_causal_run(self._plan, byref(args), stream.cuda_stream)
+                capi.conv_causal_run(self._plan, byref(args), stream)
         return out
 
     def step(self, x, w, state, bias=None, out=None, stream=None):
@@ -152,10 +152,10 @@ class CausalConv(_Plan):
         args = capi.conv_causal_args_t(xp, self._dense(w, self.w_shape, t, dev, "w"), self._bias(bias, t, dev), sp, None,
                                        yp, sp, x_ld, y_ld)
         if away is None:
-            capi.conv_causal_step(self._plan, byref(args), stream.cuda_stream)
+            capi.conv_causal_step(self._plan, byref(args), stream)
         else:
             with away:
-                capi.conv_causal_step(self._plan, byref(args), stream.cuda_stream)
+                capi.conv_causal_step(self._plan, byref(args), stream)
         return out
 
     def backward(self, dy, x, w, bias=None, state=None, lengths=None, dstate_out=None, out=None, stream=None):
@@ -184,7 +184,7 @@ class CausalConv(_Plan):
             like(dstate_out, self.state_shape, "dstate_out"), dxp, like(got["dw"], self.w_shape, "dw"),
             like(got["dbias"], self.b_shape, "dbias"), like(got["dstate"], self.state_shape, "dstate"), dy_ld, x_ld, dx_ld)
         _with_workspace(torch, self.bwd_workspace_bytes, dev, away, lambda ws, n: capi.conv_causal_bwd_run(
-            self._plan, byref(args), ws, n, stream.cuda_stream))
+            self._plan, byref(args), ws, n, stream))
         return got
 
 
@@ -241,7 +241,7 @@ class SelectiveScan(_Plan):
             None if lengths is None else self._dense(lengths, self.x_shape[:1], torch.int32, dev, "lengths"), yp,
             self._state(state_out, "state_out", torch, dev), x_ld, dt_ld, b_ld, c_ld, y_ld)
         _with_workspace(torch, self.workspace_bytes, dev, away, lambda ws, n: capi.conv_scan_run(
-            self._plan, byref(args), ws, n, stream.cuda_stream))
+            self._plan, byref(args), ws, n, stream))
         return out
 
     def step(self, x, dt, A, B, C, state, D=None, dt_bias=None, out=None, stream=None):
@@ -263,10 +263,10 @@ class SelectiveScan(_Plan):
                                      self._heads(D, "D", torch, dev), self._heads(dt_bias, "dt_bias", torch, dev), sp,
                                      None, yp, sp, x_ld, dt_ld, b_ld, c_ld, y_ld)
         if away is None:
-            capi.conv_scan_step(self._plan, byref(args), stream.cuda_stream)
+            capi.conv_scan_step(self._plan, byref(args), stream)
         else:
             with away:
-                capi.conv_scan_step(self._plan, byref(args), stream.cuda_stream)
+                capi.conv_scan_step(self._plan, byref(args), stream)
         return out
 
     def backward(self, dy, x, dt, A, B, C, D=None, dt_bias=None, state=None, lengths=None, dstate_out=None, out=None,
@@ -300,7 +300,7 @@ class SelectiveScan(_Plan):
             self._heads(got["dD"], "dD", torch, dev), self._heads(got["ddt_bias"], "ddt_bias", torch, dev),
             self._state(got["dstate"], "dstate", torch, dev), *(ld for _, ld in rows))
         _with_workspace(torch, self.bwd_workspace_bytes, dev, away, lambda ws, n: capi.conv_scan_bwd_run(
-            self._plan, byref(args), ws, n, stream.cuda_stream))
+            self._plan, byref(args), ws, n, stream))
         return got
 
 

@@ -104,7 +104,7 @@ def test_causal_calls_refused_before_a_launch():
     _refused(lambda: run(y=M + 32), "y overlaps x")
     _refused(lambda: run(state_out=5 * M), "state_out overlaps state")
     _refused(lambda: run(x_ld=40, y=M + 16, y_ld=40), "y overlaps x")
-    _refused(lambda: run(x_ld=1 << 62), "address space", UNSUPPORTED)
+    _refused(lambda: run(x_ld=1 << 62), "token to token", UNSUPPORTED)
     _refused(lambda: step(state=None), "state")
     _refused(lambda: step(lengths=7 * M), "lengths")
     _refused(lambda: step(state_out=5 * M + 2), "state_out overlaps state")
