@@ -1,0 +1,568 @@
+// The scan's state and forward kernels for bf16 tensors of whole 16-byte rows:
+// the formulas and the fragments of scan_kernels.h, fed by direct-to-LDS loads.
+//
+// scan_kernels.h's forward takes a chunk through one workgroup of four waves:
+// tiles through registers into LDS, scores, a barrier, the products with M.
+// Each wave waits for each of these in turn, and 256 registers leave room for
+// two waves per SIMD (long case, 16384 tokens of 64 heads: 19% of the matrix
+// instructions' time, 200 us).  Here a ring of three stages is filled by loads
+// that need no registers, two chunks ahead, and the waves have two jobs that
+// do not wait for each other within a chunk:
+//
+//   waves 0-3 ("state", 16 channels each):  y' = e^{c_i} h_0 C_i, then the state's update
+//   waves 4-7 ("score", 16 tokens each):    M from C . B, y'' = M x + D x
+//
+// The score waves' products need no LDS for M: the scores' result blocks are
+// the operand of M x as they stand.  y' crosses through LDS, the score waves
+// add y'' and store the rows while the next chunk is under way, so there is one
+// barrier a chunk.
+//
+// LDS tiles hold rows of 16-byte pieces without padding (a load writes 1 KB in
+// lane order); piece c of row r lies at c ^ swz(r), which the loading lane
+// undoes by choosing what it fetches.  With it the 16 rows of a row fragment
+// and the 4 rows x 4 pieces of a transposing read each meet every bank once.
+#pragma once
+
+#include "igemm_dma.h"
+#include "scan_kernels.h"
+
+namespace convfwd {
+
+constexpr int kStages = 3;
+
+// Tiles of 64 tokens x COLS bf16 in that layout
+template <int COLS> struct Ring {
+    static constexpr int CH = COLS / 8;                  // pieces of a row
+    static constexpr int BYTES = 64 * COLS * 2;
+    static constexpr int LOADS = BYTES / 1024;           // wave instructions of a tile
+
+    static SEQ_DEV int swz(int r)
+    {
+        if (CH == 16) return ((r & 3) << 2) | ((r >> 2) & 3);
+        if (CH == 8) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+        return (r >> 2) & 3;
+    }
+    // byte offset into the matrix of what lane `lane` of load `n` fetches
+    static SEQ_DEV uint32_t source(int n, int lane, int ld, int cols)
+    {
+        const int piece = n * 64 + lane, r = piece / CH, c = (piece & (CH - 1)) ^ swz(r);
+        return c * 8 < cols ? (uint32_t)(r * ld + c * 8) * 2 : kOutOfRange;
+    }
+    // row row0 + lane % 16 (row0 a multiple of 16), reduction k0 + 8q ..
+    static SEQ_DEV bf16x8 rows(const bf16_t *t, int row0, int k0, int lane)
+    {
+        const int r = lane & 15, c = (k0 >> 3) + (lane >> 4);
+        return *reinterpret_cast<const bf16x8 *>(t + (row0 + r) * COLS + ((c ^ swz(r)) << 3));
+    }
+    // Transposing reads over the rows k0 + 4q .. +3 and k0 + 16 + 4q .. +3 (the
+    // order of two stacked results): lane % 16 gets column col0 + lane % 16, or,
+    // spread, the column that makes two results (HALF 0 and 1) the operand whose
+    // lane holds k 8q .. 8q + 7: col0 + 8 (m / 4) + 4 HALF + m % 4, m = lane % 16.
+    template <bool SPREAD, int HALF = 0> static SEQ_DEV bf16x8 cols(const bf16_t *t, int k0, int col0, int lane)
+    {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
+        const int i = lane & 15, r = (lane >> 4) * 4 + (i >> 2);
+        const int c = SPREAD ? (col0 >> 3) + (i & 3) : (col0 >> 3) + ((i & 3) >> 1), half = SPREAD ? HALF : i & 1;
+        const bf16_t *p = t + (k0 + r) * COLS + ((c ^ swz(r)) << 3) + half * 4;
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)p);
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 16 * COLS));
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
+
+// the state index of row 4q + r of result t of a spread pair
+SEQ_DEV int spread_state(int t, int q, int r) { return (t >> 1) * 32 + q * 8 + (t & 1) * 4 + r; }
+
+SEQ_DEV uint32_t lds_address(const void *p)
+{
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
+}
+
+// a chunk's rows of a matrix as a buffer that ends with the last valid element
+SEQ_DEV i32x4_t chunk_buffer(const bf16_t *g, int64_t ld, int rows, int cols)
+{
+    return buffer_rsrc(g, rows > 0 ? (uint32_t)(((rows - 1) * ld + cols) * 2) : 0u);
+}
+
+// ---- states ----------------------------------------------------------------------
+template <int SP> struct StateDmaShared {
+    static constexpr int STAGE = Ring<kPB>::BYTES + Ring<SP>::BYTES;
+    __align__(1024) unsigned char ring[kStages * STAGE];
+    __align__(16) float w[8][64];       // the weights of eight chunks, four of them in use
+    float tot[8];
+};
+
+// scan_states of scan_kernels.h
+template <int SP, bool REV, bool STORE>
+SEQ_DEV void scan_states_dma(const ScanParams &p, int64_t block, StateDmaShared<SP> &sh)
+{
+    constexpr int Q = 64, NT = SP / 16, STAGE = StateDmaShared<SP>::STAGE;
+    typedef Ring<kPB> XR;
+    typedef Ring<SP> BR;
+    constexpr int ND = (XR::LOADS + BR::LOADS) / 4;         // loads of a wave and chunk
+    static_assert(XR::LOADS % 4 == 0 && BR::LOADS % 4 == 0, "whole loads per wave");
+    float *seg_state = p.seg_state[REV], *seg_log = p.seg_log[REV];
+    const int lane = threadIdx.x & 63, w = wave_id(), q = lane >> 4, l16 = lane & 15;
+    const int nseg = STORE ? p.nseg : p.nseg - p.sub;
+    const int64_t unit = block / nseg;
+    const int s0 = (int)(block - unit * nseg);
+    const int seg = STORE ? s0 : REV ? s0 + p.sub : s0;
+    const int pb = (int)(unit % p.NPB);
+    const int64_t nh = unit / p.NPB, n = nh / p.H;
+    const int h = (int)(nh - n * p.H), g = h / (p.H / p.G);
+    const int64_t len = seq_len(p.lengths, n, p.L);
+    const int pcols = min(kPB, p.P - pb * kPB);
+    const int64_t x_ld = REV ? p.dy_ld : p.x_ld, b_ld = REV ? p.c_ld : p.b_ld;
+    const bf16_t *xg = (const bf16_t *)(REV ? p.dy : p.x) + n * p.L * x_ld + (int64_t)h * p.P + pb * kPB;
+    const bf16_t *bg = (const bf16_t *)(REV ? p.c : p.b) + n * p.L * b_ld + (int64_t)g * p.S;
+    const bf16_t *dg = (const bf16_t *)p.dt + n * p.L * p.dt_ld + h;
+    const float a = p.a[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
+    const int c_lo = seg * p.seg, c_hi = min(p.K, c_lo + p.seg);
+    const int c_live = (int)min((int64_t)c_hi, (len + Q - 1) / Q);   // chunks behind the sequence change nothing
+    const int steps = max(0, c_live - c_lo);
+    const bool busy = w * 16 < pcols;
+    const int ch = w * 16 + q * 4;
+
+    f32x4 acc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] = f32x4{0, 0, 0, 0};
+    uint32_t src[ND];
+#pragma unroll
+    for (int k = 0; k < ND; ++k)
+        src[k] = k * 4 < XR::LOADS ? XR::source(k * 4 + w, lane, (int)x_ld, pcols)
+                                   : BR::source(k * 4 + w - XR::LOADS, lane, (int)b_ld, p.S);
+    auto chunk_of = [&](int k) __attribute__((always_inline)) { return REV ? c_live - 1 - k : c_lo + k; };
+    auto issue = [&](int k) __attribute__((always_inline)) {
+        const int64_t t0 = (int64_t)chunk_of(k) * Q;
+        const int rows = (int)min((int64_t)Q, len - t0);
+        const i32x4_t xb = chunk_buffer(xg + t0 * x_ld, x_ld, rows, pcols), bb = chunk_buffer(bg + t0 * b_ld, b_ld, rows, p.S);
+        const uint32_t to = lds_address(sh.ring) + (uint32_t)(k % kStages) * STAGE + (uint32_t)w * 1024;
+#pragma unroll
+        for (int i = 0; i < ND; ++i) dma16(i * 4 < XR::LOADS ? xb : bb, src[i], 0, to + i * 4096);
+    };
+    float raw = 0.0f;
+    auto fetch_dt = [&](int k) __attribute__((always_inline)) {
+        const int64_t t = (int64_t)chunk_of(k) * Q + lane;
+        raw = k < steps && t < len ? (float)dg[t * p.dt_ld] + bias : 0.0f;
+    };
+    // the decays of chunk k, into its slot of eight
+    auto decays = [&](int k) __attribute__((always_inline)) {
+        float dt;
+        double cum;
+        chunk_decay(raw, k < steps && (int64_t)chunk_of(k) * Q + lane < len, a, p.softplus, dt, cum);
+        const double tot = wave_last(cum);
+        sh.w[k & 7][lane] = REV ? exp2_fast((float)cum) : exp2_fast((float)(tot - cum)) * dt;
+        if (lane == 0) sh.tot[k & 7] = (float)tot;
+    };
+    if (steps > 0) {
+        fetch_dt(w);
+        issue(0);
+        if (steps > 1) issue(1);
+    }
+    if (STORE) {
+        if (p.nseg > p.sub) {
+            const float *s = seg_state + (unit * p.nseg + seg) * (SP * kPB);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[t] = *reinterpret_cast<const f32x4 *>(s + (t * 16 + l16) * kPB + ch);
+        } else {
+            const float *s = REV ? p.dstate_out : p.state;
+            if (s) {
+                s += (nh * p.P + pb * kPB) * p.S;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (ch + r < pcols && t * 16 + l16 < p.S) acc[t][r] = s[(int64_t)(ch + r) * p.S + t * 16 + l16];
+            }
+        }
+    }
+    float log_dec = 0.0f;
+    if (steps > 0) {
+        decays(w);
+        fetch_dt(4 + w);
+        wait_vmcnt<0>();
+        __syncthreads();
+    }
+    for (int k = 0; k < steps; ++k) {
+        if (k + 2 < steps) issue(k + 2);        // over chunk k - 1, which all waves are done with
+        const bf16_t *sX = (const bf16_t *)(sh.ring + (k % kStages) * STAGE), *sB = sX + XR::BYTES / 2;
+        if (STORE) {
+            float *s = p.bound[REV] + (unit * p.K + chunk_of(k)) * (SP * kPB);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(s + (t * 16 + l16) * kPB + ch) = acc[t];
+        }
+        const float tot = sh.tot[k & 7], dec = exp2_fast(tot);
+        log_dec += tot;
+        if (busy) {
+            bf16x8 xf[2], bf[2][NT];
+            f32x4 wt[2][2];
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                xf[ks] = XR::template cols<false>(sX, ks * 32, w * 16, lane);
+                wt[ks][0] = *reinterpret_cast<const f32x4 *>(&sh.w[k & 7][ks * 32 + q * 4]);
+                wt[ks][1] = *reinterpret_cast<const f32x4 *>(&sh.w[k & 7][ks * 32 + 16 + q * 4]);
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) bf[ks][t] = BR::template cols<false>(sB, ks * 32, t * 16, lane);
+            in_order();
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[t] *= dec;
+            Split<bf16_t, 3> xs[2];
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = (float)xf[ks][e] * wt[ks][e / 4][e & 3];
+                make_split(v, xs[ks]);
+#pragma unroll
+                for (int m = 0; m < 3; ++m)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) acc[t] = mma(xs[ks].f[m], bf[ks][t], acc[t]);
+            }
+        }
+        if ((k & 3) == 2) {         // the next four chunks' decays, into the other half of the slots
+            decays((k & ~3) + 4 + w);
+            fetch_dt((k & ~3) + 8 + w);
+        }
+        if (k + 2 < steps) wait_vmcnt<ND>();        // loads return in order: at most chunk k + 2's are under way
+        else wait_vmcnt<0>();
+        __syncthreads();
+    }
+    if (!STORE) {
+        float *s = seg_state + (unit * p.nseg + seg) * (SP * kPB);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(s + (t * 16 + l16) * kPB + ch) = acc[t];
+        if (threadIdx.x == 0) seg_log[unit * p.nseg + seg] = log_dec;
+    } else if (REV && seg == 0 && p.dstate) {
+        float *s = p.dstate + (nh * p.P + pb * kPB) * p.S;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (ch + r < pcols && t * 16 + l16 < p.S) s[(int64_t)(ch + r) * p.S + t * 16 + l16] = acc[t][r];
+    }
+}
+
+template <int SP, bool STORE> __global__ void __launch_bounds__(256) scan_state_dma_kernel(ScanParams p)
+{
+    __shared__ StateDmaShared<SP> sh;
+    if (blockIdx.x < p.ahead) scan_states_dma<SP, false, STORE>(p, blockIdx.x, sh);
+    else scan_states_dma<SP, true, STORE>(p, blockIdx.x - p.ahead, sh);
+}
+
+// ---- forward -----------------------------------------------------------------------
+template <int SP> struct FwdDmaShared {
+    static constexpr int STAGE = Ring<kPB>::BYTES + 2 * Ring<SP>::BYTES;
+    __align__(1024) unsigned char ring[kStages * STAGE];       // C, B, x of a chunk
+    __align__(16) float y[2][64 * kPB];                         // y' of a chunk: token i, piece c of four channels at c ^ i % 16
+    __align__(16) float cum[8][64], dt[8][64], w[8][64], e[8][64];   // of eight chunks: c_i, dt_i, e^{c_Q - c_i} dt_i, e^{c_i}
+};
+
+// a score wave's chunk: y'' of the tokens 16 IT ..
+template <int SP, int IT>
+SEQ_DEV void score_rows(const bf16_t *sC, const bf16_t *sB, const bf16_t *sX, const float *cum, const float *dt, float skip,
+                        int lane, f32x4 (&y)[4])
+{
+    typedef Ring<SP> BR;
+    typedef Ring<kPB> XR;
+    constexpr int KN = SP / 32, KQ = IT / 2 + 1;
+    const int q = lane >> 4, l16 = lane & 15, i = IT * 16 + l16;
+    bf16x8 cf[KN], xf[KQ][4];
+    f32x4 s[2 * KQ];
+#pragma unroll
+    for (int ks = 0; ks < KN; ++ks) cf[ks] = BR::rows(sC, IT * 16, ks * 32, lane);
+#pragma unroll
+    for (int jt = 0; jt < 2 * KQ; ++jt) s[jt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int jt = 0; jt <= IT; ++jt) {
+        bf16x8 bf[KN];
+#pragma unroll
+        for (int ks = 0; ks < KN; ++ks) bf[ks] = BR::rows(sB, jt * 16, ks * 32, lane);
+        // while these are on their way: the decays of the tile before
+        f32x4 ex = {0, 0, 0, 0}, dj = {0, 0, 0, 0};
+        if (jt > 0) {
+            ex = cum[i] - *reinterpret_cast<const f32x4 *>(cum + (jt - 1) * 16 + q * 4);
+            dj = *reinterpret_cast<const f32x4 *>(dt + (jt - 1) * 16 + q * 4);
+        }
+        in_order();
+        if (jt > 0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[jt - 1][r] *= exp2_fast(ex[r]) * dj[r];
+        }
+#pragma unroll
+        for (int ks = 0; ks < KN; ++ks) s[jt] = mma(bf[ks], cf[ks], s[jt]);
+    }
+#pragma unroll
+    for (int ks = 0; ks < KQ; ++ks)
+#pragma unroll
+        for (int pt = 0; pt < 4; ++pt) xf[ks][pt] = XR::template cols<false>(sX, ks * 32, pt * 16, lane);
+    bf16x4 xr[4];
+#pragma unroll
+    for (int pt = 0; pt < 4; ++pt) {
+        const int c = pt * 2 + (q >> 1);
+        xr[pt] = *reinterpret_cast<const bf16x4 *>(sX + i * kPB + ((c ^ XR::swz(l16)) << 3) + (q & 1) * 4);
+    }
+    const f32x4 ex = cum[i] - *reinterpret_cast<const f32x4 *>(cum + IT * 16 + q * 4);
+    const f32x4 dj = *reinterpret_cast<const f32x4 *>(dt + IT * 16 + q * 4);
+    in_order();
+    // the tile on the diagonal
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[IT][r] = l16 >= q * 4 + r ? s[IT][r] * exp2_fast(ex[r]) * dj[r] : 0.0f;
+#pragma unroll
+    for (int pt = 0; pt < 4; ++pt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[pt][r] = skip * (float)xr[pt][r];
+#pragma unroll
+    for (int ks = 0; ks < KQ; ++ks) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = s[2 * ks][e], v[4 + e] = s[2 * ks + 1][e];
+        Split<bf16_t, 2> ms;
+        make_split(v, ms);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int pt = 0; pt < 4; ++pt) y[pt] = mma(xf[ks][pt], ms.f[m], y[pt]);
+    }
+}
+
+template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(ScanParams p)
+{
+    constexpr int Q = 64, NT = SP / 16, KN = SP / 32, STAGE = FwdDmaShared<SP>::STAGE;
+    typedef Ring<kPB> XR;
+    typedef Ring<SP> BR;
+    constexpr int LOADS = 2 * BR::LOADS + XR::LOADS, ND = LOADS / 8;
+    static_assert(LOADS % 8 == 0, "whole loads per wave");
+    __shared__ FwdDmaShared<SP> sh;
+    const int lane = threadIdx.x & 63, w = wave_id(), q = lane >> 4, l16 = lane & 15;
+    const int nseg = p.nseg / p.sub;
+    const int64_t unit = blockIdx.x / nseg;
+    const int seg = (int)(blockIdx.x - unit * nseg);
+    const int pb = (int)(unit % p.NPB);
+    const int64_t nh = unit / p.NPB, n = nh / p.H;
+    const int h = (int)(nh - n * p.H), g = h / (p.H / p.G);
+    const int64_t len = seq_len(p.lengths, n, p.L);
+    const int pcols = min(kPB, p.P - pb * kPB);
+    const bf16_t *xg = (const bf16_t *)p.x + n * p.L * p.x_ld + (int64_t)h * p.P + pb * kPB;
+    const bf16_t *bg = (const bf16_t *)p.b + n * p.L * p.b_ld + (int64_t)g * p.S;
+    const bf16_t *cg = (const bf16_t *)p.c + n * p.L * p.c_ld + (int64_t)g * p.S;
+    const bf16_t *dg = (const bf16_t *)p.dt + n * p.L * p.dt_ld + h;
+    bf16_t *yg = (bf16_t *)p.y + n * p.L * p.y_ld + (int64_t)h * p.P + pb * kPB;
+    const float a = p.a[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f, skip = p.d ? p.d[h] : 0.0f;
+    const int c_lo = seg * p.seg * p.sub, c_hi = min(p.K, c_lo + p.seg * p.sub);
+    const int c_live = (int)min((int64_t)c_hi, (len + Q - 1) / Q);
+    const int steps = max(0, c_live - c_lo);
+    const int ch = w * 16 + l16;                // a state wave's channel
+    const bool busy = w * 16 < pcols;           // a state wave with channels
+
+    uint32_t src[ND];
+#pragma unroll
+    for (int k = 0; k < ND; ++k) {
+        const int d = k * 8 + w;
+        src[k] = d < BR::LOADS       ? BR::source(d, lane, (int)p.c_ld, p.S)
+                 : d < 2 * BR::LOADS ? BR::source(d - BR::LOADS, lane, (int)p.b_ld, p.S)
+                                     : XR::source(d - 2 * BR::LOADS, lane, (int)p.x_ld, pcols);
+    }
+    auto issue = [&](int k) __attribute__((always_inline)) {
+        const int64_t t0 = (int64_t)(c_lo + k) * Q;
+        const int rows = (int)min((int64_t)Q, len - t0);
+        const i32x4_t xb = chunk_buffer(xg + t0 * p.x_ld, p.x_ld, rows, pcols);
+        const i32x4_t bb = chunk_buffer(bg + t0 * p.b_ld, p.b_ld, rows, p.S);
+        const i32x4_t cb = chunk_buffer(cg + t0 * p.c_ld, p.c_ld, rows, p.S);
+        const uint32_t to = lds_address(sh.ring) + (uint32_t)(k % kStages) * STAGE + (uint32_t)w * 1024;
+#pragma unroll
+        for (int i = 0; i < ND; ++i) {
+            const int d = i * 8 + w;
+            dma16(d < BR::LOADS ? cb : d < 2 * BR::LOADS ? bb : xb, src[i], 0, to + i * 8192);
+        }
+    };
+    float raw = 0.0f;
+    auto fetch_dt = [&](int k) __attribute__((always_inline)) {
+        const int64_t t = (int64_t)(c_lo + k) * Q + lane;
+        raw = k < steps && t < len ? (float)dg[t * p.dt_ld] + bias : 0.0f;
+    };
+    auto decays = [&](int k) __attribute__((always_inline)) {
+        float dt;
+        double cum;
+        chunk_decay(raw, k < steps && (int64_t)(c_lo + k) * Q + lane < len, a, p.softplus, dt, cum);
+        const double tot = wave_last(cum);
+        sh.cum[k & 7][lane] = (float)cum;
+        sh.dt[k & 7][lane] = dt;
+        sh.w[k & 7][lane] = exp2_fast((float)(tot - cum)) * dt;
+        sh.e[k & 7][lane] = exp2_fast((float)cum);
+    };
+    if (steps > 0) {
+        if (w >= 4) fetch_dt(w - 4);
+        issue(0);
+        if (steps > 1) issue(1);
+    }
+    if (w < 4) {
+        f32x4 st[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) st[t] = f32x4{0, 0, 0, 0};
+        if (nseg > 1) {
+            const float *s = p.seg_state[0] + (unit * p.nseg + seg * p.sub) * (SP * kPB) + ch;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) st[t][r] = s[spread_state(t, q, r) * kPB];
+        } else if (p.state && ch < pcols) {
+            const float *s = p.state + (nh * p.P + pb * kPB + ch) * p.S;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (spread_state(t, q, r) < p.S) st[t][r] = s[spread_state(t, q, r)];
+        }
+        if (steps > 0) {
+            wait_vmcnt<0>();
+            __syncthreads();
+        }
+        for (int k = 0; k < steps; ++k) {
+            if (k + 2 < steps) issue(k + 2);
+            if (busy) {
+                const bf16_t *sC = (const bf16_t *)(sh.ring + (k % kStages) * STAGE), *sB = sC + BR::BYTES / 2;
+                const bf16_t *sX = sB + BR::BYTES / 2;
+                bf16x8 cf[2][4], xf[2], bf[NT];
+                f32x4 y[4];
+                float ei[4];
+                auto read_c = [&](int ks) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int it = 0; it < 4; ++it) cf[ks & 1][it] = BR::rows(sC, it * 16, ks * 32, lane);
+                };
+                auto read_b = [&](int ks) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int t = 0; t < NT; t += 2) {
+                        bf[t] = BR::template cols<true, 0>(sB, ks * 32, t * 16, lane);
+                        bf[t + 1] = BR::template cols<true, 1>(sB, ks * 32, t * 16, lane);
+                    }
+                };
+#pragma unroll
+                for (int it = 0; it < 4; ++it) y[it] = f32x4{0, 0, 0, 0};
+                read_c(0);
+#pragma unroll
+                for (int ks = 0; ks < KN; ++ks) {
+                    if (ks + 1 < KN) {
+                        read_c(ks + 1);
+                    } else {
+                        xf[0] = XR::template cols<false>(sX, 0, w * 16, lane);
+                        xf[1] = XR::template cols<false>(sX, 32, w * 16, lane);
+#pragma unroll
+                        for (int it = 0; it < 4; ++it) ei[it] = sh.e[k & 7][it * 16 + l16];
+                        read_b(0);
+                    }
+                    in_order();
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = st[2 * ks][e], v[4 + e] = st[2 * ks + 1][e];
+                    Split<bf16_t, 2> hs;
+                    make_split(v, hs);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int it = 0; it < 4; ++it) y[it] = mma(hs.f[m], cf[ks & 1][it], y[it]);
+                    in_order();
+                }
+                const float dec = sh.e[k & 7][Q - 1];
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&sh.w[k & 7][ks * 32 + q * 4]);
+                    const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&sh.w[k & 7][ks * 32 + 16 + q * 4]);
+                    if (ks == 0) {
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) st[t] *= dec;
+                    }
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = (float)xf[ks][e] * (e < 4 ? w0[e & 3] : w1[e & 3]);
+                    Split<bf16_t, 3> xs;
+                    make_split(v, xs);
+#pragma unroll
+                    for (int m = 0; m < 3; ++m)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) st[t] = mma(bf[t], xs.f[m], st[t]);
+                    in_order();
+                    if (ks == 0) {
+                        read_b(1);
+                        in_order();
+                        // y' goes to the score waves
+#pragma unroll
+                        for (int it = 0; it < 4; ++it)
+                            *reinterpret_cast<f32x4 *>(&sh.y[k & 1][(it * 16 + l16) * kPB + (((w * 4 + q) ^ l16) << 2)]) =
+                                y[it] * ei[it];
+                    }
+                }
+            }
+            if (k + 2 < steps) wait_vmcnt<ND>();
+            else wait_vmcnt<0>();
+            __syncthreads();
+        }
+        if (p.state_out && seg == nseg - 1 && ch < pcols) {
+            float *s = p.state_out + (nh * p.P + pb * kPB + ch) * p.S;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (spread_state(t, q, r) < p.S) s[spread_state(t, q, r)] = st[t][r];
+        }
+    } else {
+        const int it = w - 4, i = it * 16 + l16;
+        f32x4 y[4];
+        // rows behind the sequence come out as zeros: x and C are zeros there
+        auto finish = [&](int k) __attribute__((always_inline)) {
+            const int64_t t0 = (int64_t)(c_lo + k) * Q;
+            const int rows = (int)min((int64_t)Q, p.L - t0);
+            const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(
+                yg + t0 * p.y_ld, 0, (int)(((rows - 1) * p.y_ld + pcols) * 2), 0x00020000);
+#pragma unroll
+            for (int pt = 0; pt < 4; ++pt) {
+                if (pt * 16 >= pcols) continue;
+                const f32x4 v = y[pt] + *reinterpret_cast<const f32x4 *>(&sh.y[k & 1][i * kPB + (((pt * 4 + q) ^ l16) << 2)]);
+                bf16x4 o;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[r] = (bf16_t)v[r];
+                const int col = pt * 16 + q * 4;
+                const uint32_t at = col < pcols ? (uint32_t)(i * (int)p.y_ld + col) * 2 : kOutOfRange;
+                typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), buf, at, 0, 0);
+            }
+        };
+        if (steps > 0) {
+            decays(it);
+            fetch_dt(4 + it);
+            wait_vmcnt<0>();
+            __syncthreads();
+        }
+        for (int k = 0; k < steps; ++k) {
+            if (k > 0) finish(k - 1);
+            if (k + 2 < steps) issue(k + 2);
+            const bf16_t *sC = (const bf16_t *)(sh.ring + (k % kStages) * STAGE), *sB = sC + BR::BYTES / 2;
+            const bf16_t *sX = sB + BR::BYTES / 2;
+            const float *cum = sh.cum[k & 7], *dt = sh.dt[k & 7];
+            if (it == 0) score_rows<SP, 0>(sC, sB, sX, cum, dt, skip, lane, y);
+            else if (it == 1) score_rows<SP, 1>(sC, sB, sX, cum, dt, skip, lane, y);
+            else if (it == 2) score_rows<SP, 2>(sC, sB, sX, cum, dt, skip, lane, y);
+            else score_rows<SP, 3>(sC, sB, sX, cum, dt, skip, lane, y);
+            if ((k & 3) == 2) {
+                decays((k & ~3) + 4 + it);
+                fetch_dt((k & ~3) + 8 + it);
+            }
+            if (k + 2 < steps) wait_vmcnt<ND>();
+            else wait_vmcnt<0>();
+            __syncthreads();
+        }
+        if (steps > 0) finish(steps - 1);
+        // chunks behind the sequence: zeros
+        for (int c = max(c_lo, c_live); c < c_hi; ++c)
+            for (int e = threadIdx.x - 256; e < Q * kPB / 8; e += 256) {
+                const int64_t t = (int64_t)c * Q + e / (kPB / 8);
+                const int col = e % (kPB / 8) * 8;
+                if (t < p.L && col < pcols) *reinterpret_cast<u32x4 *>(yg + t * p.y_ld + col) = u32x4{0, 0, 0, 0};
+            }
+    }
+}
+
+}  // namespace convfwd

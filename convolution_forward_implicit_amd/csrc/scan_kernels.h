@@ -57,7 +57,7 @@ struct ScanParams {
     int64_t L;
     int N, H, P, G, S, NPB;     // NPB: blocks of 64 channels of a head
     int K;                      // chunks of a sequence
-    int nseg, seg;              // segments of a sequence, chunks of a segment
+    int nseg, seg, sub;         // segments of a sequence, chunks of a segment, segments of a forward workgroup
     int softplus, vec;
     int64_t ahead;              // workgroups of the state kernels that run ahead; the others run back
     float *seg_state[2], *seg_log[2];   // ahead and back: [unit][nseg][SP][64], [unit][nseg]
@@ -583,7 +583,7 @@ template <int SP> __global__ void __launch_bounds__(256) scan_join_kernel(ScanPa
 #pragma unroll
         for (int i = 0; i < AT; ++i) {
             const int k = k0 + i, seg = rev ? p.nseg - 1 - k : k;
-            const bool on = k < p.nseg - 1;         // nothing follows the last one
+            const bool on = k < p.nseg - p.sub;     // nothing follows the last ones
             add[i] = on ? v[(int64_t)seg * (SP * kPB)] : 0.0f;
             dec[i] = on ? exp2_fast(lg[seg]) : 0.0f;
         }

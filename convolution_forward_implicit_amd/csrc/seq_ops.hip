@@ -7,6 +7,7 @@
 
 #include "../../include/convfwd.h"
 #include "causal_conv.h"
+#include "scan_dma.h"
 #include "scan_kernels.h"
 #include "status.h"
 
@@ -16,13 +17,17 @@ struct conv_causal_plan {
     char text[256];
 };
 
+// A sequence's chunks in `count` segments of `chunks`, `sub` of which make up what one forward workgroup takes.
+struct Segments {
+    int count, chunks, sub;
+};
+
 struct conv_scan_plan {
     conv_scan_desc_t desc;
     int64_t esz;
     int SP, Q, K, NPB;                   // padded states, chunk, chunks, channel blocks
     int64_t units;                       // N * H * NPB
-    int nseg, seg;                       // forward segments and their chunks
-    int bnseg, bseg;                     // the same of the gradient's state passes
+    Segments fwd, dma, bwd;              // forward, forward of whole bf16 vectors, the gradient's state passes
     int slices, heads_per_slice;
     int64_t ws_bytes, bwd_ws_bytes;
     int64_t o_fwd_log;                   // byte offsets in the forward's workspace and in the gradient's
@@ -186,12 +191,23 @@ struct HeadGrads {
     float *da, *dbias, *dd;
 };
 
+template <typename T, int SP, bool STORE> void launch_states(const ScanParams &p, int64_t grid, hipStream_t s)
+{
+    if constexpr (sizeof(T) == 2) {
+        if (p.vec) {
+            hipLaunchKernelGGL((scan_state_dma_kernel<SP, STORE>), dim3((unsigned)grid), dim3(256), 0, s, p);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((scan_state_kernel<T, SP, STORE>), dim3((unsigned)grid), dim3(256), 0, s, p);
+}
+
 // The states that the segments start from, in both directions for a gradient.
 template <typename T, int SP> void launch_segments(ScanParams p, int64_t units, int ways, hipStream_t s)
 {
-    if (p.nseg <= 1) return;
-    p.ahead = units * (p.nseg - 1);
-    hipLaunchKernelGGL((scan_state_kernel<T, SP, false>), dim3((unsigned)(ways * p.ahead)), dim3(256), 0, s, p);
+    if (p.nseg <= p.sub) return;
+    p.ahead = units * (p.nseg - p.sub);
+    launch_states<T, SP, false>(p, ways * p.ahead, s);
     p.ahead = units * (SP * kPB / 256);
     hipLaunchKernelGGL((scan_join_kernel<SP>), dim3((unsigned)(ways * p.ahead)), dim3(256), 0, s, p);
 }
@@ -199,7 +215,14 @@ template <typename T, int SP> void launch_segments(ScanParams p, int64_t units, 
 template <typename T, int SP> void launch_fwd(const ScanParams &p, int64_t units, hipStream_t s)
 {
     launch_segments<T, SP>(p, units, 1, s);
-    hipLaunchKernelGGL((scan_fwd_kernel<T, SP>), dim3((unsigned)(units * p.nseg)), dim3(256), 0, s, p);
+    const dim3 grid((unsigned)(units * (p.nseg / p.sub)));
+    if constexpr (sizeof(T) == 2) {
+        if (p.vec) {
+            hipLaunchKernelGGL((scan_fwd_dma_kernel<SP>), grid, dim3(512), 0, s, p);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((scan_fwd_kernel<T, SP>), grid, dim3(256), 0, s, p);
 }
 
 template <typename T, int SP> void launch_bwd(ScanParams p, int64_t units, HeadGrads g, hipStream_t s)
@@ -207,7 +230,7 @@ template <typename T, int SP> void launch_bwd(ScanParams p, int64_t units, HeadG
     if (p.N > 0) {
         launch_segments<T, SP>(p, units, 2, s);
         p.ahead = units * p.nseg;
-        hipLaunchKernelGGL((scan_state_kernel<T, SP, true>), dim3((unsigned)(2 * p.ahead)), dim3(256), 0, s, p);
+        launch_states<T, SP, true>(p, 2 * p.ahead, s);
         const int64_t grid = (int64_t)p.N * p.K * p.G * p.slices;
         hipLaunchKernelGGL((scan_bwd_kernel<T, SP>), dim3((unsigned)grid), dim3(256), 0, s, p);
     }
@@ -223,13 +246,14 @@ template <typename T> void launch_scan(int SP, const ScanParams &p, int64_t unit
     return g ? launch_bwd<T, 128>(p, units, *g, s) : launch_fwd<T, 128>(p, units, s);
 }
 
-// Segments of K chunks so that `units` heads give about `want` workgroups.
-void split_segments(int64_t units, int64_t K, int64_t want, int *nseg, int *seg)
+// Segments of K chunks so that `units` heads give about `want` workgroups, each
+// cut into `fine` times as many for the pass over the states.
+Segments split_segments(int64_t units, int64_t K, int64_t want, int64_t fine)
 {
     const int64_t n = std::max<int64_t>(1, std::min(K, want / std::max<int64_t>(1, units)));
-    const int64_t per = (K + n - 1) / n;
-    *seg = (int)per;
-    *nseg = (int)((K + per - 1) / per);
+    const int64_t whole = (K + n - 1) / n, sub = n == 1 ? 1 : std::max<int64_t>(1, std::min(fine, whole / 2));
+    const int64_t chunks = (whole + sub - 1) / sub, count = (K + chunks * sub - 1) / (chunks * sub) * sub;
+    return {(int)count, (int)chunks, (int)sub};
 }
 
 void scan_params(const conv_scan_plan &pl, ScanParams *p)
@@ -238,6 +262,13 @@ void scan_params(const conv_scan_plan &pl, ScanParams *p)
     *p = ScanParams{};
     p->N = (int)d.N; p->L = d.L; p->H = (int)d.H; p->P = (int)d.P; p->G = (int)d.G; p->S = (int)d.S;
     p->NPB = pl.NPB; p->K = pl.K; p->softplus = d.softplus;
+}
+
+void set_segments(ScanParams *p, const Segments &s)
+{
+    p->nseg = s.count;
+    p->seg = s.chunks;
+    p->sub = s.sub;
 }
 
 }  // namespace
@@ -430,25 +461,29 @@ conv_status_t conv_scan_create(const conv_scan_desc_t *desc, conv_scan_plan_t **
         return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
     }
     pl->units = d.N * d.H * pl->NPB;
-    // Two forward workgroups fit a compute unit; with fewer heads than half of
-    // those the long axis is split, at the price of a second pass over x and B.
+    // With fewer heads than compute units the long axis is split, at the price of
+    // a first pass over x and B.  One direct-to-LDS workgroup fits a compute unit
+    // and two of the others; the first pass's are smaller and finer ones fill
+    // the chip.
     const int64_t cus = 256;
-    split_segments(pl->units, pl->K, pl->units >= cus ? 0 : 2 * cus, &pl->nseg, &pl->seg);
-    split_segments(pl->units, pl->K, pl->units >= cus ? 0 : 2 * cus, &pl->bnseg, &pl->bseg);
+    pl->fwd = split_segments(pl->units, pl->K, pl->units >= cus ? 0 : 2 * cus, 1);
+    pl->dma = split_segments(pl->units, pl->K, cus, 2);
+    pl->bwd = split_segments(pl->units, pl->K, cus, 1);
     const int64_t chunks = d.N * pl->K * d.G, hpg = d.H / d.G;
     const int64_t want = std::max<int64_t>(1, std::min(hpg, (2 * cus + chunks - 1) / std::max<int64_t>(1, chunks)));
     pl->heads_per_slice = (int)((hpg + want - 1) / want);
     pl->slices = (int)((hpg + pl->heads_per_slice - 1) / pl->heads_per_slice);
     const int64_t t = (int64_t)pl->SP * kPB * 4;
     auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
-    pl->o_fwd_log = pl->nseg > 1 ? up(pl->units * pl->nseg * t) : 0;
-    pl->ws_bytes = pl->o_fwd_log + (pl->nseg > 1 ? up(pl->units * pl->nseg * 4) : 0);
+    const int64_t most = std::max(pl->fwd.count > pl->fwd.sub ? pl->fwd.count : 0, pl->dma.count > pl->dma.sub ? pl->dma.count : 0);
+    pl->o_fwd_log = up(pl->units * most * t);
+    pl->ws_bytes = pl->o_fwd_log + up(pl->units * most * 4);
     int64_t o = 0;
     for (int k = 0; k < 2; ++k) {
         pl->o_seg[k] = o;
-        o += pl->bnseg > 1 ? up(pl->units * pl->bnseg * t) : 0;
+        o += pl->bwd.count > 1 ? up(pl->units * pl->bwd.count * t) : 0;
         pl->o_log[k] = o;
-        o += pl->bnseg > 1 ? up(pl->units * pl->bnseg * 4) : 0;
+        o += pl->bwd.count > 1 ? up(pl->units * pl->bwd.count * 4) : 0;
         pl->o_bound[k] = o;
         o += up(pl->units * pl->K * t);
     }
@@ -462,7 +497,7 @@ conv_status_t conv_scan_create(const conv_scan_desc_t *desc, conv_scan_plan_t **
              "scan %s N=%lld L=%lld H=%lld P=%lld G=%lld S=%lld(%d)%s, %d chunks of %d in %d segments; "
              "gradient: %d segments, %d slices of %d heads",
              d.dtype == CONV_DT_BF16 ? "bf16" : "f32", (long long)d.N, (long long)d.L, (long long)d.H, (long long)d.P,
-             (long long)d.G, (long long)d.S, pl->SP, d.softplus ? " softplus" : "", pl->K, pl->Q, pl->nseg, pl->bnseg,
+             (long long)d.G, (long long)d.S, pl->SP, d.softplus ? " softplus" : "", pl->K, pl->Q, pl->fwd.count, pl->bwd.count,
              pl->slices, pl->heads_per_slice);
     if (getenv("CONVFWD_LOG")) fprintf(stderr, "convfwd: %s\n", pl->text);
     *plan = pl;
@@ -545,14 +580,13 @@ static conv_status_t scan_forward(const conv_scan_plan_t *plan, const conv_scan_
         }
         return launched();
     }
-    p.nseg = plan->nseg;
-    p.seg = plan->seg;
-    if (plan->nseg > 1) {
+    if (need > 0) {
         p.seg_state[0] = (float *)ws;
         p.seg_log[0] = (float *)((char *)ws + plan->o_fwd_log);
     }
     const Rows vec[] = {in[0], in[1], in[2], out[0]};
     p.vec = scan_vector(*plan, vec, 4);
+    set_segments(&p, p.vec && d.dtype == CONV_DT_BF16 ? plan->dma : plan->fwd);
     if (d.dtype == CONV_DT_BF16) launch_scan<bf16_t>(plan->SP, p, plan->units, nullptr, s);
     else launch_scan<float>(plan->SP, p, plan->units, nullptr, s);
     return launched();
@@ -615,7 +649,7 @@ conv_status_t conv_scan_bwd_run(const conv_scan_plan_t *plan, const conv_scan_bw
     const Rows vec[] = {in[0], in[1], in[2], in[3], out[0]};
     p.vec = scan_vector(*plan, vec, 5);
     char *ws = (char *)workspace;
-    p.nseg = plan->bnseg; p.seg = plan->bseg;
+    set_segments(&p, plan->bwd);
     for (int k = 0; k < 2; ++k) {
         p.seg_state[k] = (float *)(ws + plan->o_seg[k]);
         p.seg_log[k] = (float *)(ws + plan->o_log[k]);

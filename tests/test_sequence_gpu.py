@@ -172,7 +172,8 @@ def _scan_case(N, L, H, P, G, S, dtype, state, lengths, seed, softplus=True):
 SCANS = [(1, 1, 1, 1, 1, 1, True, None), (2, 64, 2, 64, 1, 128, False, None), (2, 65, 4, 64, 2, 128, True, "most"),
          (1, 130, 3, 40, 3, 24, True, None), (3, 33, 2, 130, 1, 17, True, "zero"), (1, 200, 2, 16, 1, 64, False, None),
          (2, 63, 2, 128, 2, 100, True, "one"), (1, 500, 1, 64, 1, 32, True, None), (4, 70, 64, 8, 4, 16, True, "most"),
-         (2, 0, 2, 16, 1, 16, True, None), (0, 9, 2, 16, 1, 16, False, None), (2, 192, 6, 24, 1, 33, True, "zero")]
+         (2, 0, 2, 16, 1, 16, True, None), (0, 9, 2, 16, 1, 16, False, None), (2, 192, 6, 24, 1, 33, True, "zero"),
+         (2, 1030, 64, 8, 2, 16, True, "most"), (1, 900, 3, 72, 1, 40, False, None)]
 
 
 def _around(v):

@@ -168,15 +168,16 @@ def test_python_calls_refuse_tensors():
         rows(torch.zeros(2, 10, 4, 16, dtype=torch.bfloat16), (4, 16))
 
 
-def test_python_rows_accepts_column_ranges_only(monkeypatch):
+def test_python_rows_accepts_column_ranges_only():
     """Strides, with a stand-in for a cuda tensor's device."""
     class Device(str):
-        type = "cuda"
+        type, index = "cuda", 0
 
     class View:
         def __init__(self, t):
             self.t, self.dtype, self.shape, self.device = t, t.dtype, t.shape, Device("cuda:0")
             self.is_contiguous, self.stride, self.data_ptr = t.is_contiguous, t.stride, t.data_ptr
+            self.is_cuda, self.get_device = True, lambda: 0
 
     s = SelectiveScan(SCAN, "f32")
     rows = lambda t, lead, inner: s._rows(View(t), lead, inner, torch.float32, Device("cuda:0"), "x")[1]
