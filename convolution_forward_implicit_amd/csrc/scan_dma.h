@@ -10,17 +10,20 @@
 // do not wait for each other within a chunk:
 //
 //   waves 0-3 ("state", 16 channels each):  y' = e^{c_i} h_0 C_i, then the state's update
-//   waves 4-7 ("score", 16 tokens each):    M from C . B, y'' = M x + D x
+//   waves 4-7 ("score", 16 tokens each):    M from C . B, y'' = (M + D) x
 //
 // The score waves' products need no LDS for M: the scores' result blocks are
 // the operand of M x as they stand.  y' crosses through LDS, the score waves
 // add y'' and store the rows while the next chunk is under way, so there is one
 // barrier a chunk.
 //
-// LDS tiles hold rows of 16-byte pieces without padding (a load writes 1 KB in
-// lane order); piece c of row r lies at c ^ swz(r), which the loading lane
-// undoes by choosing what it fetches.  With it the 16 rows of a row fragment
-// and the 4 rows x 4 pieces of a transposing read each meet every bank once.
+// A load writes 1 KB to LDS in lane order, so rows cannot be padded one by one;
+// but each load's 1 KB may lie anywhere and hold any rows: load g of a tile takes
+// the rows g, g + G, g + 2G .. (G loads to a tile) and its kilobyte starts 32
+// bytes (8 banks) behind the last one's end.  An address is then a lane's
+// constant plus a constant, and reads run at the rate of the banks: measured per
+// wave instruction, 16 rows of 16 bytes 4.0 clocks (8.0 with 16 or 48 bytes
+// between; 8 bytes of each row instead: 16), the transposing read 2.5 (4.0).
 #pragma once
 
 #include "igemm_dma.h"
@@ -32,47 +35,44 @@ constexpr int kStages = 3;
 
 // Tiles of 64 tokens x COLS bf16 in that layout
 template <int COLS> struct Ring {
-    static constexpr int CH = COLS / 8;                  // pieces of a row
-    static constexpr int BYTES = 64 * COLS * 2;
-    static constexpr int LOADS = BYTES / 1024;           // wave instructions of a tile
+    static constexpr int CH = COLS / 8;                  // 16-byte pieces of a row
+    static constexpr int LOADS = 64 * COLS * 2 / 1024;   // wave instructions of a tile
+    static constexpr int GROUP = (1024 + 32) / 2;        // elements from one load's kilobyte to the next
+    static constexpr int BYTES = LOADS * GROUP * 2;
 
-    static SEQ_DEV int swz(int r)
+    static SEQ_DEV constexpr int row(int r) { return r % LOADS * GROUP + r / LOADS * COLS; }
+    // byte offset into the matrix of what lane `lane` of load `g` fetches
+    static SEQ_DEV uint32_t source(int g, int lane, int ld, int cols)
     {
-        if (CH == 16) return ((r & 3) << 2) | ((r >> 2) & 3);
-        if (CH == 8) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
-        return (r >> 2) & 3;
+        const int r = g + lane / CH * LOADS, c = (lane & (CH - 1)) * 8;
+        return c < cols ? (uint32_t)(r * ld + c) * 2 : kOutOfRange;
     }
-    // byte offset into the matrix of what lane `lane` of load `n` fetches
-    static SEQ_DEV uint32_t source(int n, int lane, int ld, int cols)
-    {
-        const int piece = n * 64 + lane, r = piece / CH, c = (piece & (CH - 1)) ^ swz(r);
-        return c * 8 < cols ? (uint32_t)(r * ld + c * 8) * 2 : kOutOfRange;
-    }
-    // row row0 + lane % 16 (row0 a multiple of 16), reduction k0 + 8q ..
+    // Row row0 + lane % 16 (row0 a multiple of 16), reduction k0 + 8q ..
     static SEQ_DEV bf16x8 rows(const bf16_t *t, int row0, int k0, int lane)
     {
-        const int r = lane & 15, c = (k0 >> 3) + (lane >> 4);
-        return *reinterpret_cast<const bf16x8 *>(t + (row0 + r) * COLS + ((c ^ swz(r)) << 3));
+        return *reinterpret_cast<const bf16x8 *>(t + row(lane & 15) + row(row0) + k0 + (lane >> 4) * 8);
     }
-    // Transposing reads over the rows k0 + 4q .. +3 and k0 + 16 + 4q .. +3 (the
-    // order of two stacked results): lane % 16 gets column col0 + lane % 16, or,
-    // spread, the column that makes two results (HALF 0 and 1) the operand whose
-    // lane holds k 8q .. 8q + 7: col0 + 8 (m / 4) + 4 HALF + m % 4, m = lane % 16.
-    template <bool SPREAD, int HALF = 0> static SEQ_DEV bf16x8 cols(const bf16_t *t, int k0, int col0, int lane)
+    // Transposing reads over the rows k0 + 4q .. and k0 + 16 + 4q .. (the order of
+    // two stacked results; k0 a multiple of 32): lane % 16 = m gets column col0 + m
+    // or, spread, the column that makes two results (HALF 0 and 1) an operand whose
+    // lane holds 8q .. 8q + 7: col0 + 8 (m / 4) + 4 HALF + m % 4.
+    template <bool SPREAD = false, int HALF = 0> static SEQ_DEV bf16x8 cols(const bf16_t *t, int k0, int col0, int lane)
     {
         typedef short s16x4 __attribute__((ext_vector_type(4)));
         typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
         const int i = lane & 15, r = (lane >> 4) * 4 + (i >> 2);
-        const int c = SPREAD ? (col0 >> 3) + (i & 3) : (col0 >> 3) + ((i & 3) >> 1), half = SPREAD ? HALF : i & 1;
-        const bf16_t *p = t + (k0 + r) * COLS + ((c ^ swz(r)) << 3) + half * 4;
+        const bf16_t *p = t + row(r) + row(k0) + col0 + (SPREAD ? (i & 3) * 8 + HALF * 4 : (i & 3) * 4);
         const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)p);
-        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 16 * COLS));
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + row(16)));
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     }
 };
 
 // the state index of row 4q + r of result t of a spread pair
 SEQ_DEV int spread_state(int t, int q, int r) { return (t >> 1) * 32 + q * 8 + (t & 1) * 4 + r; }
+
+// the next of the ring's stages
+SEQ_DEV int next_stage(int stage, int bytes) { return stage == (kStages - 1) * bytes ? 0 : stage + bytes; }
 
 SEQ_DEV uint32_t lds_address(const void *p)
 {
@@ -133,13 +133,16 @@ SEQ_DEV void scan_states_dma(const ScanParams &p, int64_t block, StateDmaShared<
         src[k] = k * 4 < XR::LOADS ? XR::source(k * 4 + w, lane, (int)x_ld, pcols)
                                    : BR::source(k * 4 + w - XR::LOADS, lane, (int)b_ld, p.S);
     auto chunk_of = [&](int k) __attribute__((always_inline)) { return REV ? c_live - 1 - k : c_lo + k; };
+    const uint32_t ring = lds_address(sh.ring);
+    int fill = 0, stage = 0;        // the stages that the next chunk goes to and is taken from
     auto issue = [&](int k) __attribute__((always_inline)) {
         const int64_t t0 = (int64_t)chunk_of(k) * Q;
         const int rows = (int)min((int64_t)Q, len - t0);
         const i32x4_t xb = chunk_buffer(xg + t0 * x_ld, x_ld, rows, pcols), bb = chunk_buffer(bg + t0 * b_ld, b_ld, rows, p.S);
-        const uint32_t to = lds_address(sh.ring) + (uint32_t)(k % kStages) * STAGE + (uint32_t)w * 1024;
+        const uint32_t to = ring + fill + (uint32_t)w * (2 * XR::GROUP);
 #pragma unroll
-        for (int i = 0; i < ND; ++i) dma16(i * 4 < XR::LOADS ? xb : bb, src[i], 0, to + i * 4096);
+        for (int i = 0; i < ND; ++i) dma16(i * 4 < XR::LOADS ? xb : bb, src[i], 0, to + i * (8 * XR::GROUP));
+        fill = next_stage(fill, STAGE);
     };
     float raw = 0.0f;
     auto fetch_dt = [&](int k) __attribute__((always_inline)) {
@@ -186,7 +189,8 @@ SEQ_DEV void scan_states_dma(const ScanParams &p, int64_t block, StateDmaShared<
     }
     for (int k = 0; k < steps; ++k) {
         if (k + 2 < steps) issue(k + 2);        // over chunk k - 1, which all waves are done with
-        const bf16_t *sX = (const bf16_t *)(sh.ring + (k % kStages) * STAGE), *sB = sX + XR::BYTES / 2;
+        const bf16_t *sX = (const bf16_t *)(sh.ring + stage), *sB = sX + XR::BYTES / 2;
+        stage = next_stage(stage, STAGE);
         if (STORE) {
             float *s = p.bound[REV] + (unit * p.K + chunk_of(k)) * (SP * kPB);
 #pragma unroll
@@ -199,14 +203,14 @@ SEQ_DEV void scan_states_dma(const ScanParams &p, int64_t block, StateDmaShared<
             f32x4 wt[2][2];
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                xf[ks] = XR::template cols<false>(sX, ks * 32, w * 16, lane);
+                xf[ks] = XR::cols(sX, ks * 32, w * 16, lane);
                 wt[ks][0] = *reinterpret_cast<const f32x4 *>(&sh.w[k & 7][ks * 32 + q * 4]);
                 wt[ks][1] = *reinterpret_cast<const f32x4 *>(&sh.w[k & 7][ks * 32 + 16 + q * 4]);
             }
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) bf[ks][t] = BR::template cols<false>(sB, ks * 32, t * 16, lane);
+                for (int t = 0; t < NT; ++t) bf[ks][t] = BR::cols(sB, ks * 32, t * 16, lane);
             in_order();
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[t] *= dec;
@@ -217,6 +221,9 @@ SEQ_DEV void scan_states_dma(const ScanParams &p, int64_t block, StateDmaShared<
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = (float)xf[ks][e] * wt[ks][e / 4][e & 3];
                 make_split(v, xs[ks]);
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
                 for (int m = 0; m < 3; ++m)
 #pragma unroll
@@ -246,7 +253,7 @@ SEQ_DEV void scan_states_dma(const ScanParams &p, int64_t block, StateDmaShared<
     }
 }
 
-template <int SP, bool STORE> __global__ void __launch_bounds__(256) scan_state_dma_kernel(ScanParams p)
+template <int SP, bool STORE> __global__ void __launch_bounds__(256, 2) scan_state_dma_kernel(ScanParams p)
 {
     __shared__ StateDmaShared<SP> sh;
     if (blockIdx.x < p.ahead) scan_states_dma<SP, false, STORE>(p, blockIdx.x, sh);
@@ -258,7 +265,7 @@ template <int SP> struct FwdDmaShared {
     static constexpr int STAGE = Ring<kPB>::BYTES + 2 * Ring<SP>::BYTES;
     __align__(1024) unsigned char ring[kStages * STAGE];       // C, B, x of a chunk
     __align__(16) float y[2][64 * kPB];                         // y' of a chunk: token i, piece c of four channels at c ^ i % 16
-    __align__(16) float cum[8][64], dt[8][64], w[8][64], e[8][64];   // of eight chunks: c_i, dt_i, e^{c_Q - c_i} dt_i, e^{c_i}
+    __align__(16) float cum[3][64], dt[3][64], w[3][64];        // of three chunks: c_i, dt_i, e^{c_Q - c_i} dt_i
 };
 
 // a score wave's chunk: y'' of the tokens 16 IT ..
@@ -298,23 +305,18 @@ SEQ_DEV void score_rows(const bf16_t *sC, const bf16_t *sB, const bf16_t *sX, co
 #pragma unroll
     for (int ks = 0; ks < KQ; ++ks)
 #pragma unroll
-        for (int pt = 0; pt < 4; ++pt) xf[ks][pt] = XR::template cols<false>(sX, ks * 32, pt * 16, lane);
-    bf16x4 xr[4];
-#pragma unroll
-    for (int pt = 0; pt < 4; ++pt) {
-        const int c = pt * 2 + (q >> 1);
-        xr[pt] = *reinterpret_cast<const bf16x4 *>(sX + i * kPB + ((c ^ XR::swz(l16)) << 3) + (q & 1) * 4);
-    }
+        for (int pt = 0; pt < 4; ++pt) xf[ks][pt] = XR::cols(sX, ks * 32, pt * 16, lane);
     const f32x4 ex = cum[i] - *reinterpret_cast<const f32x4 *>(cum + IT * 16 + q * 4);
     const f32x4 dj = *reinterpret_cast<const f32x4 *>(dt + IT * 16 + q * 4);
     in_order();
-    // the tile on the diagonal
+    // the tile on the diagonal, with D there
 #pragma unroll
-    for (int r = 0; r < 4; ++r) s[IT][r] = l16 >= q * 4 + r ? s[IT][r] * exp2_fast(ex[r]) * dj[r] : 0.0f;
+    for (int r = 0; r < 4; ++r) {
+        s[IT][r] = l16 >= q * 4 + r ? s[IT][r] * exp2_fast(ex[r]) * dj[r] : 0.0f;
+        if (l16 == q * 4 + r) s[IT][r] += skip;
+    }
 #pragma unroll
-    for (int pt = 0; pt < 4; ++pt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) y[pt][r] = skip * (float)xr[pt][r];
+    for (int pt = 0; pt < 4; ++pt) y[pt] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int ks = 0; ks < KQ; ++ks) {
         float v[8];
@@ -329,7 +331,7 @@ SEQ_DEV void score_rows(const bf16_t *sC, const bf16_t *sB, const bf16_t *sX, co
     }
 }
 
-template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(ScanParams p)
+template <int SP> __global__ void __launch_bounds__(512, 2) scan_fwd_dma_kernel(ScanParams p)
 {
     constexpr int Q = 64, NT = SP / 16, KN = SP / 32, STAGE = FwdDmaShared<SP>::STAGE;
     typedef Ring<kPB> XR;
@@ -366,36 +368,40 @@ template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(Sca
                  : d < 2 * BR::LOADS ? BR::source(d - BR::LOADS, lane, (int)p.b_ld, p.S)
                                      : XR::source(d - 2 * BR::LOADS, lane, (int)p.x_ld, pcols);
     }
+    const uint32_t ring = lds_address(sh.ring);
+    int fill = 0, stage = 0, slot = 0;      // where the next chunk goes to, is taken from, and its decays are
     auto issue = [&](int k) __attribute__((always_inline)) {
         const int64_t t0 = (int64_t)(c_lo + k) * Q;
         const int rows = (int)min((int64_t)Q, len - t0);
         const i32x4_t xb = chunk_buffer(xg + t0 * p.x_ld, p.x_ld, rows, pcols);
         const i32x4_t bb = chunk_buffer(bg + t0 * p.b_ld, p.b_ld, rows, p.S);
         const i32x4_t cb = chunk_buffer(cg + t0 * p.c_ld, p.c_ld, rows, p.S);
-        const uint32_t to = lds_address(sh.ring) + (uint32_t)(k % kStages) * STAGE + (uint32_t)w * 1024;
+        const uint32_t to = ring + fill + (uint32_t)w * (2 * XR::GROUP);
 #pragma unroll
         for (int i = 0; i < ND; ++i) {
             const int d = i * 8 + w;
-            dma16(d < BR::LOADS ? cb : d < 2 * BR::LOADS ? bb : xb, src[i], 0, to + i * 8192);
+            dma16(d < BR::LOADS ? cb : d < 2 * BR::LOADS ? bb : xb, src[i], 0, to + i * (16 * XR::GROUP));
         }
+        fill = next_stage(fill, STAGE);
     };
     float raw = 0.0f;
     auto fetch_dt = [&](int k) __attribute__((always_inline)) {
         const int64_t t = (int64_t)(c_lo + k) * Q + lane;
         raw = k < steps && t < len ? (float)dg[t * p.dt_ld] + bias : 0.0f;
     };
-    auto decays = [&](int k) __attribute__((always_inline)) {
+    // The decays of chunk k, a long chain of scalar work, into slot k % 3: two
+    // score waves do those of the next two chunks at every second one.
+    auto decays = [&](int k, int to) __attribute__((always_inline)) {
         float dt;
         double cum;
         chunk_decay(raw, k < steps && (int64_t)(c_lo + k) * Q + lane < len, a, p.softplus, dt, cum);
         const double tot = wave_last(cum);
-        sh.cum[k & 7][lane] = (float)cum;
-        sh.dt[k & 7][lane] = dt;
-        sh.w[k & 7][lane] = exp2_fast((float)(tot - cum)) * dt;
-        sh.e[k & 7][lane] = exp2_fast((float)cum);
+        sh.cum[to][lane] = (float)cum;
+        sh.dt[to][lane] = dt;
+        sh.w[to][lane] = exp2_fast((float)(tot - cum)) * dt;
     };
     if (steps > 0) {
-        if (w >= 4) fetch_dt(w - 4);
+        if (w == 4 || w == 5) fetch_dt(w - 4);
         issue(0);
         if (steps > 1) issue(1);
     }
@@ -423,12 +429,16 @@ template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(Sca
         }
         for (int k = 0; k < steps; ++k) {
             if (k + 2 < steps) issue(k + 2);
+            const bf16_t *sC = (const bf16_t *)(sh.ring + stage), *sB = sC + BR::BYTES / 2, *sX = sB + BR::BYTES / 2;
+            const float *cum = sh.cum[slot], *wt = sh.w[slot];
+            stage = next_stage(stage, STAGE);
+            slot = slot == 2 ? 0 : slot + 1;
             if (busy) {
-                const bf16_t *sC = (const bf16_t *)(sh.ring + (k % kStages) * STAGE), *sB = sC + BR::BYTES / 2;
-                const bf16_t *sX = sB + BR::BYTES / 2;
                 bf16x8 cf[2][4], xf[2], bf[NT];
-                f32x4 y[4];
+                f32x4 y[4], w0[2], w1[2];
                 float ei[4];
+                Split<bf16_t, 2> hs[2];
+                Split<bf16_t, 3> xs[2];
                 auto read_c = [&](int ks) __attribute__((always_inline)) {
 #pragma unroll
                     for (int it = 0; it < 4; ++it) cf[ks & 1][it] = BR::rows(sC, it * 16, ks * 32, lane);
@@ -440,61 +450,67 @@ template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(Sca
                         bf[t + 1] = BR::template cols<true, 1>(sB, ks * 32, t * 16, lane);
                     }
                 };
+                auto split_h = [&](int ks) __attribute__((always_inline)) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = st[2 * ks][e], v[4 + e] = st[2 * ks + 1][e];
+                    make_split(v, hs[ks & 1]);
+                };
+                auto split_x = [&](int ks) __attribute__((always_inline)) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = (float)xf[ks][e] * (e < 4 ? w0[ks][e & 3] : w1[ks][e & 3]);
+                    make_split(v, xs[ks]);
+                };
 #pragma unroll
                 for (int it = 0; it < 4; ++it) y[it] = f32x4{0, 0, 0, 0};
                 read_c(0);
+                split_h(0);
+                // each step's reads and splits are the next one's operands
 #pragma unroll
                 for (int ks = 0; ks < KN; ++ks) {
                     if (ks + 1 < KN) {
                         read_c(ks + 1);
                     } else {
-                        xf[0] = XR::template cols<false>(sX, 0, w * 16, lane);
-                        xf[1] = XR::template cols<false>(sX, 32, w * 16, lane);
 #pragma unroll
-                        for (int it = 0; it < 4; ++it) ei[it] = sh.e[k & 7][it * 16 + l16];
-                        read_b(0);
+                        for (int k2 = 0; k2 < 2; ++k2) {
+                            xf[k2] = XR::cols(sX, k2 * 32, w * 16, lane);
+                            w0[k2] = *reinterpret_cast<const f32x4 *>(wt + k2 * 32 + q * 4);
+                            w1[k2] = *reinterpret_cast<const f32x4 *>(wt + k2 * 32 + 16 + q * 4);
+                        }
+#pragma unroll
+                        for (int it = 0; it < 4; ++it) ei[it] = cum[it * 16 + l16];
                     }
+                    if (ks == KN - 1) read_b(0);
                     in_order();
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = st[2 * ks][e], v[4 + e] = st[2 * ks + 1][e];
-                    Split<bf16_t, 2> hs;
-                    make_split(v, hs);
+                    if (ks + 1 < KN) split_h(ks + 1);
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int it = 0; it < 4; ++it) y[it] = mma(hs.f[m], cf[ks & 1][it], y[it]);
+                        for (int it = 0; it < 4; ++it) y[it] = mma(hs[ks & 1].f[m], cf[ks & 1][it], y[it]);
                     in_order();
                 }
-                const float dec = sh.e[k & 7][Q - 1];
+                const float dec = exp2_fast(cum[Q - 1]);
+                split_x(0);
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&sh.w[k & 7][ks * 32 + q * 4]);
-                    const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&sh.w[k & 7][ks * 32 + 16 + q * 4]);
-                    if (ks == 0) {
+                for (int t = 0; t < NT; ++t) st[t] *= dec;
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) st[t] *= dec;
-                    }
-                    float v[8];
+                for (int m = 0; m < 3; ++m)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = (float)xf[ks][e] * (e < 4 ? w0[e & 3] : w1[e & 3]);
-                    Split<bf16_t, 3> xs;
-                    make_split(v, xs);
+                    for (int t = 0; t < NT; ++t) st[t] = mma(bf[t], xs[0].f[m], st[t]);
+                split_x(1);
+                in_order();
+                read_b(1);
+                in_order();
+                // y' goes to the score waves
 #pragma unroll
-                    for (int m = 0; m < 3; ++m)
+                for (int it = 0; it < 4; ++it)
+                    *reinterpret_cast<f32x4 *>(&sh.y[k & 1][(it * 16 + l16) * kPB + (((w * 4 + q) ^ l16) << 2)]) =
+                        y[it] * exp2_fast(ei[it]);
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) st[t] = mma(bf[t], xs.f[m], st[t]);
-                    in_order();
-                    if (ks == 0) {
-                        read_b(1);
-                        in_order();
-                        // y' goes to the score waves
+                for (int m = 0; m < 3; ++m)
 #pragma unroll
-                        for (int it = 0; it < 4; ++it)
-                            *reinterpret_cast<f32x4 *>(&sh.y[k & 1][(it * 16 + l16) * kPB + (((w * 4 + q) ^ l16) << 2)]) =
-                                y[it] * ei[it];
-                    }
-                }
+                    for (int t = 0; t < NT; ++t) st[t] = mma(bf[t], xs[1].f[m], st[t]);
             }
             if (k + 2 < steps) wait_vmcnt<ND>();
             else wait_vmcnt<0>();
@@ -531,24 +547,27 @@ template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(Sca
             }
         };
         if (steps > 0) {
-            decays(it);
-            fetch_dt(4 + it);
+            if (it < 2) {
+                decays(it, it);
+                fetch_dt(2 + it);
+            }
             wait_vmcnt<0>();
             __syncthreads();
         }
         for (int k = 0; k < steps; ++k) {
             if (k > 0) finish(k - 1);
             if (k + 2 < steps) issue(k + 2);
-            const bf16_t *sC = (const bf16_t *)(sh.ring + (k % kStages) * STAGE), *sB = sC + BR::BYTES / 2;
-            const bf16_t *sX = sB + BR::BYTES / 2;
-            const float *cum = sh.cum[k & 7], *dt = sh.dt[k & 7];
+            const bf16_t *sC = (const bf16_t *)(sh.ring + stage), *sB = sC + BR::BYTES / 2, *sX = sB + BR::BYTES / 2;
+            const float *cum = sh.cum[slot], *dt = sh.dt[slot];
+            stage = next_stage(stage, STAGE);
+            slot = slot == 2 ? 0 : slot + 1;
             if (it == 0) score_rows<SP, 0>(sC, sB, sX, cum, dt, skip, lane, y);
             else if (it == 1) score_rows<SP, 1>(sC, sB, sX, cum, dt, skip, lane, y);
             else if (it == 2) score_rows<SP, 2>(sC, sB, sX, cum, dt, skip, lane, y);
             else score_rows<SP, 3>(sC, sB, sX, cum, dt, skip, lane, y);
-            if ((k & 3) == 2) {
-                decays((k & ~3) + 4 + it);
-                fetch_dt((k & ~3) + 8 + it);
+            if ((k & 1) && it < 2) {        // chunks k + 1 and k + 2: the slots that are neither k's
+                decays(k + 1 + it, it == 0 ? slot : slot == 2 ? 0 : slot + 1);
+                fetch_dt(k + 3 + it);
             }
             if (k + 2 < steps) wait_vmcnt<ND>();
             else wait_vmcnt<0>();

@@ -102,18 +102,29 @@ SEQ_DEV f32x4 mma(const Frag<float>::type &a, const Frag<float>::type &b, f32x4 
 template <typename T, int NS> struct Split {
     typename Frag<T>::type f[NS];
 };
+// two values rounded to bf16 in one word, and taken off them
+SEQ_DEV uint32_t take_pair(float &a, float &b)
+{
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+    a -= __builtin_bit_cast(float, w << 16);
+    b -= __builtin_bit_cast(float, w & 0xffff0000u);
+    return w;
+}
 template <int NS> SEQ_DEV void make_split(const float (&v)[8], Split<bf16_t, NS> &s)
 {
     float r[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) r[e] = v[e];
 #pragma unroll
-    for (int k = 0; k < NS; ++k)
+    for (int k = 0; k < NS; ++k) {
+        typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+        u32x4_t w;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            s.f[k][e] = (bf16_t)r[e];
-            r[e] -= (float)s.f[k][e];
-        }
+        for (int e = 0; e < 4; ++e) w[e] = take_pair(r[2 * e], r[2 * e + 1]);
+        s.f[k] = __builtin_bit_cast(bf16x8, w);
+    }
 }
 template <int NS> SEQ_DEV void make_split(const float (&v)[8], Split<float, NS> &s)
 {
@@ -203,13 +214,10 @@ template <int NS, typename T> SEQ_DEV void write_split4(T *t, int term_stride, f
     } else {
 #pragma unroll
         for (int k = 0; k < NS; ++k) {
-            bf16x4 h;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                h[e] = (bf16_t)v[e];
-                v[e] -= (float)h[e];
-            }
-            *reinterpret_cast<bf16x4 *>(t + k * term_stride) = h;
+            float a = v[0], b = v[1], c = v[2], d = v[3];
+            const uint32_t lo = take_pair(a, b), hi = take_pair(c, d);
+            v = f32x4{a, b, c, d};
+            *reinterpret_cast<uint64_t *>(t + k * term_stride) = (uint64_t)hi << 32 | lo;
         }
     }
 }

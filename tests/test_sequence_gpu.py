@@ -244,9 +244,18 @@ def test_scan_step(case, dtype):
 
 
 def test_scan_in_column_ranges():
-    """The parts of one activation as inputs, their gradients into one buffer; y into columns of another."""
+    """The parts of one activation as inputs, their gradients into one buffer; y into columns of another.  Odd row
+    lengths run on other kernels, which add the same terms in another order: both results are within half a step and
+    c sum |t_k| of the exact one, so at most a step (of either, 2^-7 of the larger) and 2 c sum |t_k| apart."""
     _, SelectiveScan = _ops()
     N, L, H, P, G, S = 2, 70, 2, 32, 1, 40
+
+    def same(got, want, mag, extra, c, what):
+        if not extra:
+            assert torch.equal(got, want), what
+        else:
+            _near(got, want.cpu(), mag, 2 * HALF["bf16"], 2 * c, what)
+
     for extra in (0, 3):        # whole 16-byte rows, and odd ones
         a, dy, _, _ = _scan_case(N, L, H, P, G, S, "bf16", False, None, 7)
         p = SelectiveScan({"N": N, "L": L, "H": H, "P": P, "G": G, "S": S}, "bf16")
@@ -260,12 +269,14 @@ def test_scan_in_column_ranges():
         wide = torch.full((N, L, H * P + 8 + extra), 3.0, dtype=torch.bfloat16, device=DEV)
         out = wide[..., 8:8 + H * P].unflatten(-1, (H, P))
         w = dict(v, x=x, B=B, C=C)
-        assert torch.equal(p(**w, out=out), want)
+        same(p(**w, out=out), want, seq.scan(**a, magnitude=True)[0], extra, 2.0 ** -14, "y")
         assert (wide[..., :8] == 3).all() and (wide[..., 8 + H * P:] == 3).all()
         du = torch.full_like(u, 5.0)
         dx, dB, dC = cut(du)
         p.backward(dy.to(DEV), **w, out={"dx": dx, "dB": dB, "dC": dC})
-        assert torch.equal(dx, grads["dx"]) and torch.equal(dB, grads["dB"]) and torch.equal(dC, grads["dC"])
+        mag = seq.scan_grad(dy, **a, magnitude=True)
+        for k, t in (("dx", dx), ("dB", dB), ("dC", dC)):
+            same(t, grads[k], mag[k], extra, 2.0 ** -13, k)
         assert (du[..., H * P + 2 * G * S:] == 5).all()
 
 
