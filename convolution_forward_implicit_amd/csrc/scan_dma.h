@@ -6,12 +6,15 @@
 // Each wave waits for each of these in turn, and 256 registers leave room for
 // two waves per SIMD (long case, 16384 tokens of 64 heads: 19% of the matrix
 // instructions' time, 200 us).  Here a ring of three stages is filled by loads
-// that need no registers, two chunks ahead, and the waves have two jobs that
-// do not wait for each other within a chunk:
+// that need no registers, two chunks ahead, and the waves have jobs that do not
+// wait for each other within a chunk:
 //
 //   waves 0-3 ("state", 16 channels each):  y' = e^{c_i} h_0 C_i, then the state's update
 //   waves 4-7 ("score", 16 tokens each):    M from C . B, y'' = (M + D) x
+//   wave 8:                                 the loads
 //
+// (The counter that says when loads have arrived counts stores too, so waves
+// that store y would wait for their stores before each barrier: 30 of 190 us.)
 // The score waves' products need no LDS for M: the scores' result blocks are
 // the operand of M x as they stand.  y' crosses through LDS, the score waves
 // add y'' and store the rows while the next chunk is under way, so there is one
@@ -331,13 +334,13 @@ SEQ_DEV void score_rows(const bf16_t *sC, const bf16_t *sB, const bf16_t *sX, co
     }
 }
 
-template <int SP> __global__ void __launch_bounds__(512, 2) scan_fwd_dma_kernel(ScanParams p)
+template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(ScanParams p)
 {
     constexpr int Q = 64, NT = SP / 16, KN = SP / 32, STAGE = FwdDmaShared<SP>::STAGE;
     typedef Ring<kPB> XR;
     typedef Ring<SP> BR;
-    constexpr int LOADS = 2 * BR::LOADS + XR::LOADS, ND = LOADS / 8;
-    static_assert(LOADS % 8 == 0, "whole loads per wave");
+    constexpr int LOADS = 2 * BR::LOADS + XR::LOADS;
+    static_assert(LOADS < 64, "all of a chunk's loads fit the counter");
     __shared__ FwdDmaShared<SP> sh;
     const int lane = threadIdx.x & 63, w = wave_id(), q = lane >> 4, l16 = lane & 15;
     const int nseg = p.nseg / p.sub;
@@ -360,30 +363,6 @@ template <int SP> __global__ void __launch_bounds__(512, 2) scan_fwd_dma_kernel(
     const int ch = w * 16 + l16;                // a state wave's channel
     const bool busy = w * 16 < pcols;           // a state wave with channels
 
-    uint32_t src[ND];
-#pragma unroll
-    for (int k = 0; k < ND; ++k) {
-        const int d = k * 8 + w;
-        src[k] = d < BR::LOADS       ? BR::source(d, lane, (int)p.c_ld, p.S)
-                 : d < 2 * BR::LOADS ? BR::source(d - BR::LOADS, lane, (int)p.b_ld, p.S)
-                                     : XR::source(d - 2 * BR::LOADS, lane, (int)p.x_ld, pcols);
-    }
-    const uint32_t ring = lds_address(sh.ring);
-    int fill = 0, stage = 0, slot = 0;      // where the next chunk goes to, is taken from, and its decays are
-    auto issue = [&](int k) __attribute__((always_inline)) {
-        const int64_t t0 = (int64_t)(c_lo + k) * Q;
-        const int rows = (int)min((int64_t)Q, len - t0);
-        const i32x4_t xb = chunk_buffer(xg + t0 * p.x_ld, p.x_ld, rows, pcols);
-        const i32x4_t bb = chunk_buffer(bg + t0 * p.b_ld, p.b_ld, rows, p.S);
-        const i32x4_t cb = chunk_buffer(cg + t0 * p.c_ld, p.c_ld, rows, p.S);
-        const uint32_t to = ring + fill + (uint32_t)w * (2 * XR::GROUP);
-#pragma unroll
-        for (int i = 0; i < ND; ++i) {
-            const int d = i * 8 + w;
-            dma16(d < BR::LOADS ? cb : d < 2 * BR::LOADS ? bb : xb, src[i], 0, to + i * (16 * XR::GROUP));
-        }
-        fill = next_stage(fill, STAGE);
-    };
     float raw = 0.0f;
     auto fetch_dt = [&](int k) __attribute__((always_inline)) {
         const int64_t t = (int64_t)(c_lo + k) * Q + lane;
@@ -400,12 +379,47 @@ template <int SP> __global__ void __launch_bounds__(512, 2) scan_fwd_dma_kernel(
         sh.dt[to][lane] = dt;
         sh.w[to][lane] = exp2_fast((float)(tot - cum)) * dt;
     };
-    if (steps > 0) {
-        if (w == 4 || w == 5) fetch_dt(w - 4);
-        issue(0);
-        if (steps > 1) issue(1);
-    }
-    if (w < 4) {
+    int stage = 0, slot = 0;        // where a chunk and its decays are
+    if (w == 8) {
+        const uint32_t ring = lds_address(sh.ring);
+        int fill = 0;
+        // a row group of a tile lies LOADS rows on from the one before it, a load's
+        // rows one row on from the load before: one lane offset per tile
+        auto issue = [&](int k) __attribute__((always_inline)) {
+            const int64_t t0 = (int64_t)(c_lo + k) * Q;
+            const int rows = (int)min((int64_t)Q, len - t0);
+            const i32x4_t xb = chunk_buffer(xg + t0 * p.x_ld, p.x_ld, rows, pcols);
+            const i32x4_t bb = chunk_buffer(bg + t0 * p.b_ld, p.b_ld, rows, p.S);
+            const i32x4_t cb = chunk_buffer(cg + t0 * p.c_ld, p.c_ld, rows, p.S);
+            uint32_t to = ring + fill;
+#pragma unroll
+            for (int g = 0; g < BR::LOADS; ++g, to += 2 * BR::GROUP) dma16(cb, BR::source(g, lane, (int)p.c_ld, p.S), 0, to);
+#pragma unroll
+            for (int g = 0; g < BR::LOADS; ++g, to += 2 * BR::GROUP) dma16(bb, BR::source(g, lane, (int)p.b_ld, p.S), 0, to);
+#pragma unroll
+            for (int g = 0; g < XR::LOADS; ++g, to += 2 * XR::GROUP) dma16(xb, XR::source(g, lane, (int)p.x_ld, pcols), 0, to);
+            fill = next_stage(fill, STAGE);
+        };
+        if (steps > 0) {
+            issue(0);
+            if (steps > 1) {
+                issue(1);
+                wait_vmcnt<LOADS>();
+            } else {
+                wait_vmcnt<0>();
+            }
+            __syncthreads();
+        }
+        for (int k = 0; k < steps; ++k) {
+            if (k + 2 < steps) {
+                issue(k + 2);       // over chunk k - 1, which all waves are done with
+                wait_vmcnt<LOADS>();
+            } else {
+                wait_vmcnt<0>();
+            }
+            __syncthreads();
+        }
+    } else if (w < 4) {
         f32x4 st[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) st[t] = f32x4{0, 0, 0, 0};
@@ -423,12 +437,8 @@ template <int SP> __global__ void __launch_bounds__(512, 2) scan_fwd_dma_kernel(
                 for (int r = 0; r < 4; ++r)
                     if (spread_state(t, q, r) < p.S) st[t][r] = s[spread_state(t, q, r)];
         }
-        if (steps > 0) {
-            wait_vmcnt<0>();
-            __syncthreads();
-        }
+        if (steps > 0) __syncthreads();
         for (int k = 0; k < steps; ++k) {
-            if (k + 2 < steps) issue(k + 2);
             const bf16_t *sC = (const bf16_t *)(sh.ring + stage), *sB = sC + BR::BYTES / 2, *sX = sB + BR::BYTES / 2;
             const float *cum = sh.cum[slot], *wt = sh.w[slot];
             stage = next_stage(stage, STAGE);
@@ -512,8 +522,6 @@ template <int SP> __global__ void __launch_bounds__(512, 2) scan_fwd_dma_kernel(
 #pragma unroll
                     for (int t = 0; t < NT; ++t) st[t] = mma(bf[t], xs[1].f[m], st[t]);
             }
-            if (k + 2 < steps) wait_vmcnt<ND>();
-            else wait_vmcnt<0>();
             __syncthreads();
         }
         if (p.state_out && seg == nseg - 1 && ch < pcols) {
@@ -548,15 +556,14 @@ template <int SP> __global__ void __launch_bounds__(512, 2) scan_fwd_dma_kernel(
         };
         if (steps > 0) {
             if (it < 2) {
+                fetch_dt(it);
                 decays(it, it);
                 fetch_dt(2 + it);
             }
-            wait_vmcnt<0>();
             __syncthreads();
         }
         for (int k = 0; k < steps; ++k) {
             if (k > 0) finish(k - 1);
-            if (k + 2 < steps) issue(k + 2);
             const bf16_t *sC = (const bf16_t *)(sh.ring + stage), *sB = sC + BR::BYTES / 2, *sX = sB + BR::BYTES / 2;
             const float *cum = sh.cum[slot], *dt = sh.dt[slot];
             stage = next_stage(stage, STAGE);
@@ -569,8 +576,6 @@ template <int SP> __global__ void __launch_bounds__(512, 2) scan_fwd_dma_kernel(
                 decays(k + 1 + it, it == 0 ? slot : slot == 2 ? 0 : slot + 1);
                 fetch_dt(k + 3 + it);
             }
-            if (k + 2 < steps) wait_vmcnt<ND>();
-            else wait_vmcnt<0>();
             __syncthreads();
         }
         if (steps > 0) finish(steps - 1);

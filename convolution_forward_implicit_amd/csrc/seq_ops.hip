@@ -218,7 +218,7 @@ template <typename T, int SP> void launch_fwd(const ScanParams &p, int64_t units
     const dim3 grid((unsigned)(units * (p.nseg / p.sub)));
     if constexpr (sizeof(T) == 2) {
         if (p.vec) {
-            hipLaunchKernelGGL((scan_fwd_dma_kernel<SP>), grid, dim3(512), 0, s, p);
+            hipLaunchKernelGGL((scan_fwd_dma_kernel<SP>), grid, dim3(576), 0, s, p);
             return;
         }
     }
