@@ -32,22 +32,43 @@ struct CausalParams {
 
 constexpr int kConvRun = 8;       // tokens of one thread's run, forward
 constexpr int kConvBwdRun = 16;   // tokens of one thread's run, gradient
-constexpr int kConvBwdCv = 32;    // channel vectors and runs of a gradient workgroup
-constexpr int kConvBwdRuns = 8;
+constexpr int kConvBwdCv = 64;    // channel vectors and runs of a gradient workgroup
+constexpr int kConvBwdRuns = 4;
 
-// h[n, t] for V channels: a token inside the sequence, a row of the state, or zero
-template <typename T, int F, int V>
-SEQ_DEV void conv_history(const CausalParams &p, int64_t n, int64_t t, int64_t len, int c, float (&v)[V])
-{
-    if (t >= 0 && t < len) {
-        load_f32<T, V>((const T *)p.x + (n * p.L + t) * p.x_ld + c, v);
-    } else if (t < 0 && p.state) {
-        load_f32<T, V>((const T *)p.state + (n * (F - 1) + (F - 1 + t)) * p.C + c, v);
-    } else {
+// The rows t0 .. t0 + M - 1 of h for V channels, as they lie in memory: a token
+// of the sequence, a row of the state, or zero.  Every row is fetched, where it
+// has none from a token that the sequence's row of L has (its value is dropped):
+// without branches the fetches are all under way before the first is used.
+template <typename T, int F, int V, int M> struct ConvRows {
+    typedef typename Pack<T, V>::type vec_t;
+    vec_t q[M];
+    SEQ_DEV void load(const CausalParams &p, int64_t n, int64_t t0, int64_t len, int c)
+    {
+        const T *x = (const T *)p.x + n * p.L * p.x_ld + c;
+        const T *old = p.state ? (const T *)p.state + n * (F - 1) * p.C + c : nullptr;
+        vec_t zero;
+        __builtin_memset(&zero, 0, sizeof(zero));
+        if (len == 0 && (!old || t0 >= 0)) {        // nothing there (L may be 0)
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = 0.0f;
+            for (int e = 0; e < M; ++e) q[e] = zero;
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < M; ++e) {
+            const int64_t t = t0 + e, last = len - 1 < 0 ? 0 : len - 1;
+            const T *row = x + (t < 0 ? 0 : t > last ? last : t) * p.x_ld;
+            if (t < 0 && old) row = old + (F - 1 + t) * p.C;
+            else if (len == 0) row = old;
+            q[e] = *reinterpret_cast<const vec_t *>(row);
+        }
+#pragma unroll
+        for (int e = 0; e < M; ++e) {
+            const int64_t t = t0 + e;
+            if (!(t < 0 ? old != nullptr : t < len)) q[e] = zero;
+        }
     }
-}
+    SEQ_DEV float get(int e, int i) const { return pack_get<T, V>(q[e], i); }
+};
 
 template <typename T, int F, int V> SEQ_DEV void conv_weights(const CausalParams &p, int c, float (&w)[F][V])
 {
@@ -84,18 +105,16 @@ __global__ void __launch_bounds__(256) causal_conv_kernel(CausalParams p)
     const int64_t n = row / runs, run = row - n * runs;
     const int64_t len = seq_len(p.lengths, n, p.L);
     if (run == p.blocks) {
+        ConvRows<T, F, V, F - 1> h;
+        h.load(p, n, len - (F - 1), len, c);
 #pragma unroll
-        for (int j = 0; j < F - 1; ++j) {
-            float v[V];
-            conv_history<T, F, V>(p, n, len - (F - 1) + j, len, c, v);
-            store_f32<T, V>((T *)p.state_out + (n * (F - 1) + j) * p.C + c, v);
-        }
+        for (int j = 0; j < F - 1; ++j)
+            *reinterpret_cast<typename Pack<T, V>::type *>((T *)p.state_out + (n * (F - 1) + j) * p.C + c) = h.q[j];
         return;
     }
     const int64_t t0 = run * kConvRun;
-    float h[F - 1 + kConvRun][V];
-#pragma unroll
-    for (int e = 0; e < F - 1 + kConvRun; ++e) conv_history<T, F, V>(p, n, t0 - (F - 1) + e, len, c, h[e]);
+    ConvRows<T, F, V, F - 1 + kConvRun> h;
+    h.load(p, n, t0 - (F - 1), len, c);
     float w[F][V], b[V];
     conv_weights<T, F, V>(p, c, w);
 #pragma unroll
@@ -109,7 +128,7 @@ __global__ void __launch_bounds__(256) causal_conv_kernel(CausalParams p)
         for (int i = 0; i < V; ++i) {
             float v = b[i];
 #pragma unroll
-            for (int k = 0; k < F; ++k) v = fmaf(w[k][i], h[u + k][i], v);
+            for (int k = 0; k < F; ++k) v = fmaf(w[k][i], h.get(u + k, i), v);
             o[i] = t0 + u < len ? (SILU ? v * sigmoid(v) : v) : 0.0f;
         }
         store_f32<T, V>((T *)p.y + (n * p.L + t0 + u) * p.y_ld + c, o);
@@ -145,29 +164,6 @@ __global__ void __launch_bounds__(256) causal_step_kernel(CausalParams p)
     for (int j = 0; j < F - 1; ++j) store_f32<T, V>((T *)p.state_out + (n * (F - 1) + j) * p.C + c, h[j + 1]);
 }
 
-// d v[n,t] = dy act'(v), zero outside the sequence
-template <typename T, int F, int V, bool SILU>
-SEQ_DEV void conv_dv(const CausalParams &p, int64_t n, int64_t t, int64_t len, int c, const float (&w)[F][V],
-                     const float (&b)[V], const float (*h)[V], float (&d)[V])
-{
-    if (t < 0 || t >= len) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = 0.0f;
-        return;
-    }
-    load_f32<T, V>((const T *)p.dy + (n * p.L + t) * p.dy_ld + c, d);
-    if (SILU) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float v = b[i];
-#pragma unroll
-            for (int k = 0; k < F; ++k) v = fmaf(w[k][i], h[k][i], v);
-            const float s = sigmoid(v);
-            d[i] *= s * (1.0f + v * (1.0f - s));
-        }
-    }
-}
-
 // The gradient: with d = dy act'(v),
 //   dh[s] = sum_k w[k] d[s + (F-1) - k],   dw[k] = sum_t d[t] h[t-(F-1)+k],   db = sum_t d[t].
 // A thread recomputes v for its run and the F - 1 tokens behind it (d of those
@@ -194,31 +190,47 @@ __global__ void __launch_bounds__(256) causal_bwd_kernel(CausalParams p)
         for (int k = 0; k < F; ++k) dw[k][i] = w[k][i] = 0.0f;
     }
     if (live && (t0 < p.L || t0 == 0)) {
+        typedef typename Pack<T, V>::type vec_t;
+        constexpr int M = kConvBwdRun + F - 1;
+        ConvRows<T, F, V, M + F - 1> h;
+        vec_t dy[M];
+        h.load(p, n, t0 - (F - 1), len, c);
+        if (len > 0) {
+#pragma unroll
+            for (int u = 0; u < M; ++u) {
+                const int64_t t = t0 + u < len ? t0 + u : len - 1;
+                dy[u] = *reinterpret_cast<const vec_t *>((const T *)p.dy + (n * p.L + t) * p.dy_ld + c);
+            }
+        }
         conv_weights<T, F, V>(p, c, w);
         if (p.bias) load_f32<T, V>((const T *)p.bias + c, b);
-        float h[F][V];             // h[t-(F-1)] .. h[t]
         float d[F][V];             // d[t-(F-1)] .. d[t]
 #pragma unroll
-        for (int k = 0; k < F - 1; ++k) {
-            conv_history<T, F, V>(p, n, t0 - (F - 1) + k, len, c, h[k]);
+        for (int k = 0; k < F; ++k)
 #pragma unroll
             for (int i = 0; i < V; ++i) d[k][i] = 0.0f;
-        }
 #pragma unroll
-        for (int u = 0; u < kConvBwdRun + F - 1; ++u) {
-            const int64_t t = t0 + u;
-            conv_history<T, F, V>(p, n, t, len, c, h[F - 1]);
-            conv_dv<T, F, V, SILU>(p, n, t, len, c, w, b, h, d[F - 1]);
-            if (u < kConvBwdRun) {
+        for (int u = 0; u < M; ++u) {
+            const bool in = t0 + u < len;
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    db[i] += d[F - 1][i];
+            for (int i = 0; i < V; ++i) {
+                float g = in ? pack_get<T, V>(dy[u], i) : 0.0f;
+                if (SILU) {
+                    float v = b[i];
 #pragma unroll
-                    for (int k = 0; k < F; ++k) dw[k][i] = fmaf(d[F - 1][i], h[k][i], dw[k][i]);
+                    for (int k = 0; k < F; ++k) v = fmaf(w[k][i], h.get(u + k, i), v);
+                    const float s = sigmoid(v);
+                    g *= s * (1.0f + v * (1.0f - s));
+                }
+                d[F - 1][i] = g;
+                if (u < kConvBwdRun) {
+                    db[i] += g;
+#pragma unroll
+                    for (int k = 0; k < F; ++k) dw[k][i] = fmaf(g, h.get(u + k, i), dw[k][i]);
                 }
             }
             // dh at s = t - (F-1), once d[s .. s+F-1] is known
-            const int64_t s = t - (F - 1);
+            const int64_t s = t0 + u - (F - 1);
             if (u >= F - 1 || (t0 == 0 && p.dstate)) {
                 float g[V];
 #pragma unroll
@@ -237,19 +249,15 @@ __global__ void __launch_bounds__(256) causal_bwd_kernel(CausalParams p)
                 if (s < 0) {
                     store_f32<T, V>((T *)p.dstate + (n * (F - 1) + (F - 1 + s)) * p.C + c, g);
                 } else if (s < p.L && u >= F - 1) {
-                    if (s >= len)
 #pragma unroll
-                        for (int i = 0; i < V; ++i) g[i] = 0.0f;
+                    for (int i = 0; i < V; ++i) g[i] = s < len ? g[i] : 0.0f;
                     store_f32<T, V>((T *)p.dx + (n * p.L + s) * p.dx_ld + c, g);
                 }
             }
 #pragma unroll
             for (int k = 0; k < F - 1; ++k)
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    h[k][i] = h[k + 1][i];
-                    d[k][i] = d[k + 1][i];
-                }
+                for (int i = 0; i < V; ++i) d[k][i] = d[k + 1][i];
         }
     }
 #pragma unroll

@@ -22,6 +22,12 @@ template <typename T> struct Pack<T, 1> {
     typedef T type;
 };
 
+template <typename T, int V> SEQ_DEV float pack_get(const typename Pack<T, V>::type &q, int i)
+{
+    if constexpr (V == 1) return (float)q;
+    else return (float)q[i];
+}
+
 template <typename T, int V> SEQ_DEV void load_f32(const T *p, float (&v)[V])
 {
     if constexpr (V == 1) {

@@ -118,12 +118,17 @@ enum ConvKernel { CONV_RUN, CONV_STEP, CONV_BWD };
 template <typename T, int F, int V, bool SILU>
 void launch_causal(ConvKernel which, const CausalParams &p, int64_t grid, hipStream_t s)
 {
-    if (which == CONV_RUN)
-        hipLaunchKernelGGL((causal_conv_kernel<T, F, V, SILU>), dim3((unsigned)grid), dim3(256), 0, s, p);
-    else if (which == CONV_STEP)
-        hipLaunchKernelGGL((causal_step_kernel<T, F, V, SILU>), dim3((unsigned)grid), dim3(256), 0, s, p);
-    else if constexpr (V < 8 || F <= 4)
-        hipLaunchKernelGGL((causal_bwd_kernel<T, F, V, SILU>), dim3((unsigned)grid), dim3(256), 0, s, p);
+    constexpr bool whole = V * sizeof(T) == 16, half = V * sizeof(T) == 8;
+    if constexpr (whole || V == 1) {
+        if (which == CONV_RUN)
+            hipLaunchKernelGGL((causal_conv_kernel<T, F, V, SILU>), dim3((unsigned)grid), dim3(256), 0, s, p);
+        else if (which == CONV_STEP)
+            hipLaunchKernelGGL((causal_step_kernel<T, F, V, SILU>), dim3((unsigned)grid), dim3(256), 0, s, p);
+    }
+    if constexpr (half || V == 1) {
+        if (which == CONV_BWD)
+            hipLaunchKernelGGL((causal_bwd_kernel<T, F, V, SILU>), dim3((unsigned)grid), dim3(256), 0, s, p);
+    }
 }
 
 template <typename T, int F, int V>
@@ -147,26 +152,15 @@ void launch_causal(ConvKernel which, int F, bool silu, const CausalParams &p, in
     }
 }
 
-// The gradient keeps 4 F V values of a thread in registers; with 8 taps of 8
-// channels they would not fit, so more than 4 taps of bf16 go by 4 channels.
-void launch_causal_bwd4(int F, bool silu, const CausalParams &p, int64_t grid, hipStream_t s)
-{
-    switch (F) {
-    case 5: return launch_causal<bf16_t, 5, 4>(CONV_BWD, silu, p, grid, s);
-    case 6: return launch_causal<bf16_t, 6, 4>(CONV_BWD, silu, p, grid, s);
-    case 7: return launch_causal<bf16_t, 7, 4>(CONV_BWD, silu, p, grid, s);
-    default: return launch_causal<bf16_t, 8, 4>(CONV_BWD, silu, p, grid, s);
-    }
-}
-
 void launch_causal(ConvKernel which, const conv_causal_desc_t &d, int V, const CausalParams &p, int64_t grid, hipStream_t s)
 {
     if (d.dtype == CONV_DT_BF16) {
-        if (V == 4) launch_causal_bwd4((int)d.F, d.silu, p, grid, s);
+        if (V == 4) launch_causal<bf16_t, 4>(which, (int)d.F, d.silu, p, grid, s);
         else if (V > 1) launch_causal<bf16_t, 8>(which, (int)d.F, d.silu, p, grid, s);
         else launch_causal<bf16_t, 1>(which, (int)d.F, d.silu, p, grid, s);
     } else {
-        if (V > 1) launch_causal<float, 4>(which, (int)d.F, d.silu, p, grid, s);
+        if (V == 2) launch_causal<float, 2>(which, (int)d.F, d.silu, p, grid, s);
+        else if (V > 1) launch_causal<float, 4>(which, (int)d.F, d.silu, p, grid, s);
         else launch_causal<float, 1>(which, (int)d.F, d.silu, p, grid, s);
     }
 }
@@ -399,8 +393,9 @@ conv_status_t conv_causal_bwd_run(const conv_causal_plan_t *plan, const conv_cau
     if ((st = check_workspace(workspace, workspace_bytes, plan->ws_bytes)) != CONV_OK) return st;
     if ((st = check_overlap(out, 5, in, 7)) != CONV_OK) return st;
     const Rows vec[] = {in[0], in[1], in[2], in[3], in[4], in[5], out[0], out[3]};
-    int V = conv_vector(d, e, vec, 8);
-    if (V == 8 && d.F > 4) V = 4;
+    // A gradient thread holds its run's rows of x and dy: by 8 bytes they leave
+    // room for two waves more per SIMD than by 16 (training case 74 us with 16).
+    const int V = conv_vector(d, e, vec, 8) == 1 ? 1 : (int)(8 / e);
     CausalParams p{};
     p.x = a->x; p.w = a->w; p.bias = a->bias; p.state = a->state; p.lengths = a->lengths;
     p.dy = a->dy; p.dstate_out = a->dstate_out; p.dx = a->dx; p.dstate = a->dstate;
