@@ -5,10 +5,10 @@
 //   y = v (1 / (1 + e^-v)) or v,        h[t] = x[t], and the state's rows for t < 0
 //
 // The work is 2F flop for two elements moved: every kernel is bound by HBM.
-// A thread owns V neighbouring channels (16 bytes) of a run of tokens and
-// keeps the last F - 1 of them in registers, so each input row is fetched once
-// per run and F - 1 rows again at its start; neighbouring threads take
-// neighbouring channels, so a wave's accesses are whole lines.
+// A wave owns 64 V neighbouring channels (V: 16 bytes, in the gradient 8) of a
+// run of tokens, so its accesses are whole lines and its rows' addresses scalar;
+// all rows of a run, with the F - 1 before it, are fetched before the first is
+// used.
 #pragma once
 
 #include "seq_common.h"
@@ -30,22 +30,29 @@ struct CausalParams {
     int64_t dy_ld, dx_ld;
 };
 
-constexpr int kConvRun = 8;       // tokens of one thread's run, forward
-constexpr int kConvBwdRun = 16;   // tokens of one thread's run, gradient
-constexpr int kConvBwdCv = 64;    // channel vectors and runs of a gradient workgroup
-constexpr int kConvBwdRuns = 4;
+constexpr int kConvRun = 8;       // tokens of one wave's run, forward
+constexpr int kConvBwdRun = 16;   // tokens of one wave's run, gradient
+constexpr int kConvRuns = 4;      // runs (waves) of a workgroup
+
+SEQ_DEV int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+SEQ_DEV int64_t scalar(int64_t v)
+{
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
 
 // The rows t0 .. t0 + M - 1 of h for V channels, as they lie in memory: a token
-// of the sequence, a row of the state, or zero.  Every row is fetched, where it
-// has none from a token that the sequence's row of L has (its value is dropped):
-// without branches the fetches are all under way before the first is used.
+// of the sequence, a row of the state, or zero.  Every row is fetched, one that
+// has none from the nearest that has (and its value dropped): without branches
+// the fetches are all under way before the first is used.  n, t0 and len are the
+// same in the whole wave.
 template <typename T, int F, int V, int M> struct ConvRows {
     typedef typename Pack<T, V>::type vec_t;
     vec_t q[M];
     SEQ_DEV void load(const CausalParams &p, int64_t n, int64_t t0, int64_t len, int c)
     {
-        const T *x = (const T *)p.x + n * p.L * p.x_ld + c;
-        const T *old = p.state ? (const T *)p.state + n * (F - 1) * p.C + c : nullptr;
+        const T *x = (const T *)p.x + n * p.L * p.x_ld;
+        const T *old = p.state ? (const T *)p.state + n * (F - 1) * p.C : nullptr;
         vec_t zero;
         __builtin_memset(&zero, 0, sizeof(zero));
         if (len == 0 && (!old || t0 >= 0)) {        // nothing there (L may be 0)
@@ -55,11 +62,10 @@ template <typename T, int F, int V, int M> struct ConvRows {
         }
 #pragma unroll
         for (int e = 0; e < M; ++e) {
-            const int64_t t = t0 + e, last = len - 1 < 0 ? 0 : len - 1;
-            const T *row = x + (t < 0 ? 0 : t > last ? last : t) * p.x_ld;
-            if (t < 0 && old) row = old + (F - 1 + t) * p.C;
-            else if (len == 0) row = old;
-            q[e] = *reinterpret_cast<const vec_t *>(row);
+            const int64_t t = t0 + e;
+            const T *row = x + (t < 0 ? 0 : t < len ? t : len - 1) * p.x_ld;
+            if (old && (t < 0 || len == 0)) row = old + (t < 0 ? F - 1 + t : 0) * p.C;
+            q[e] = *reinterpret_cast<const vec_t *>(row + c);
         }
 #pragma unroll
         for (int e = 0; e < M; ++e) {
@@ -92,17 +98,17 @@ template <typename T, int F, int V> SEQ_DEV void conv_weights(const CausalParams
         for (int k = 0; k < F; ++k) w[k][i] = raw[i * F + k];
 }
 
-// One thread: V channels of kConvRun tokens, or (run == blocks) the state that
+// One wave: 64 V channels of kConvRun tokens, or (run == blocks) the state that
 // the sequence leaves behind.
 template <typename T, int F, int V, bool SILU>
 __global__ void __launch_bounds__(256) causal_conv_kernel(CausalParams p)
 {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t runs = p.blocks + (p.state_out ? 1 : 0);
-    const int64_t row = id / p.CV;
-    if (row >= p.N * runs) return;
-    const int c = (int)(id - row * p.CV) * V;
-    const int64_t n = row / runs, run = row - n * runs;
+    const int64_t runs = p.blocks + (p.state_out ? 1 : 0), groups = (runs + kConvRuns - 1) / kConvRuns;
+    const int cb = (p.CV + 63) / 64;
+    const int64_t blk = blockIdx.x / cb, n = blk / groups;
+    const int64_t run = scalar((blk - n * groups) * kConvRuns + threadIdx.x / 64);
+    const int cv = (int)(blockIdx.x - blk * cb) * 64 + (threadIdx.x & 63), c = cv * V;
+    if (run >= runs || cv >= p.CV) return;
     const int64_t len = seq_len(p.lengths, n, p.L);
     if (run == p.blocks) {
         ConvRows<T, F, V, F - 1> h;
@@ -131,7 +137,8 @@ __global__ void __launch_bounds__(256) causal_conv_kernel(CausalParams p)
             for (int k = 0; k < F; ++k) v = fmaf(w[k][i], h.get(u + k, i), v);
             o[i] = t0 + u < len ? (SILU ? v * sigmoid(v) : v) : 0.0f;
         }
-        store_f32<T, V>((T *)p.y + (n * p.L + t0 + u) * p.y_ld + c, o);
+        T *row = (T *)p.y + (n * p.L + t0 + u) * p.y_ld;
+        store_f32<T, V>(row + c, o);
     }
 }
 
@@ -166,19 +173,19 @@ __global__ void __launch_bounds__(256) causal_step_kernel(CausalParams p)
 
 // The gradient: with d = dy act'(v),
 //   dh[s] = sum_k w[k] d[s + (F-1) - k],   dw[k] = sum_t d[t] h[t-(F-1)+k],   db = sum_t d[t].
-// A thread recomputes v for its run and the F - 1 tokens behind it (d of those
+// A wave recomputes v for its run and the F - 1 tokens behind it (d of those
 // reaches back into the run), keeps its sums of dw and db in fp32 registers,
 // and the workgroup adds its runs in LDS, in a fixed order; causal_reduce_kernel
 // adds the workgroups' rows, in a fixed order too.
 template <typename T, int F, int V, bool SILU>
 __global__ void __launch_bounds__(256) causal_bwd_kernel(CausalParams p)
 {
-    __shared__ float part[kConvBwdRuns][kConvBwdCv * V];
-    const int cb = (p.CV + kConvBwdCv - 1) / kConvBwdCv;
+    __shared__ float part[kConvRuns][64 * V];
+    const int cb = (p.CV + 63) / 64;
     const int64_t blk = blockIdx.x / cb;
-    const int cvi = threadIdx.x & (kConvBwdCv - 1), ri = threadIdx.x / kConvBwdCv;
-    const int cv = (int)(blockIdx.x - blk * cb) * kConvBwdCv + cvi;
-    const int64_t n = blk / p.blocks, run = (blk - n * p.blocks) * kConvBwdRuns + ri;
+    const int cvi = threadIdx.x & 63, ri = scalar((int)threadIdx.x / 64);
+    const int cv = (int)(blockIdx.x - blk * cb) * 64 + cvi;
+    const int64_t n = blk / p.blocks, run = (blk - n * p.blocks) * kConvRuns + ri;
     const bool live = cv < p.CV;
     const int c = cv * V;
     const int64_t len = seq_len(p.lengths, n, p.L), t0 = run * kConvBwdRun;
@@ -198,8 +205,8 @@ __global__ void __launch_bounds__(256) causal_bwd_kernel(CausalParams p)
         if (len > 0) {
 #pragma unroll
             for (int u = 0; u < M; ++u) {
-                const int64_t t = t0 + u < len ? t0 + u : len - 1;
-                dy[u] = *reinterpret_cast<const vec_t *>((const T *)p.dy + (n * p.L + t) * p.dy_ld + c);
+                const T *row = (const T *)p.dy + (n * p.L + (t0 + u < len ? t0 + u : len - 1)) * p.dy_ld;
+                dy[u] = *reinterpret_cast<const vec_t *>(row + c);
             }
         }
         conv_weights<T, F, V>(p, c, w);
@@ -251,7 +258,8 @@ __global__ void __launch_bounds__(256) causal_bwd_kernel(CausalParams p)
                 } else if (s < p.L && u >= F - 1) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) g[i] = s < len ? g[i] : 0.0f;
-                    store_f32<T, V>((T *)p.dx + (n * p.L + s) * p.dx_ld + c, g);
+                    T *row = (T *)p.dx + (n * p.L + s) * p.dx_ld;
+                    store_f32<T, V>(row + c, g);
                 }
             }
 #pragma unroll
@@ -266,12 +274,12 @@ __global__ void __launch_bounds__(256) causal_bwd_kernel(CausalParams p)
 #pragma unroll
         for (int i = 0; i < V; ++i) part[ri][cvi * V + i] = k < F ? dw[k < F ? k : 0][i] : db[i];
         __syncthreads();
-        for (int e = threadIdx.x; e < kConvBwdCv * V; e += 256) {
-            const int ch = (int)(blockIdx.x - blk * cb) * kConvBwdCv * V + e;
+        for (int e = threadIdx.x; e < 64 * V; e += 256) {
+            const int ch = (int)(blockIdx.x - blk * cb) * 64 * V + e;
             if (ch >= p.C) continue;
             float sum = 0.0f;
 #pragma unroll
-            for (int r = 0; r < kConvBwdRuns; ++r) sum += part[r][e];
+            for (int r = 0; r < kConvRuns; ++r) sum += part[r][e];
             p.partial[(blk * (F + 1) + k) * p.C + ch] = sum;
         }
     }

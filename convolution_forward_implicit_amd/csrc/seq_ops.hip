@@ -175,7 +175,7 @@ int conv_vector(const conv_causal_desc_t &d, int64_t esz, const Rows *t, int n)
 
 int64_t bwd_blocks(const conv_causal_desc_t &d)   // workgroups along a sequence, one at least (dstate)
 {
-    const int64_t per = kConvBwdRun * kConvBwdRuns;
+    const int64_t per = kConvBwdRun * kConvRuns;
     return std::max<int64_t>(1, (d.L + per - 1) / per);
 }
 
@@ -287,11 +287,11 @@ conv_status_t conv_causal_create(const conv_causal_desc_t *desc, conv_causal_pla
                     (long long)d.N, (long long)d.L, (long long)d.C, (long long)d.F);
     if (d.F > 8) return fail(CONV_ERR_UNSUPPORTED, "more than 8 taps (F = %lld)", (long long)d.F);
     if (d.N > kMaxDim || d.L > kMaxDim || d.C > kMaxDim) return fail(CONV_ERR_UNSUPPORTED, "N, L or C above 2^30");
-    // one thread per channel and run, 256 to a workgroup
-    const double threads = (double)d.N * (double)((d.L + kConvRun - 1) / kConvRun + 1) * (double)d.C;
-    const double wgs = (double)d.N * (double)bwd_blocks(d) * (double)((d.C + kConvBwdCv - 1) / kConvBwdCv);
+    // a workgroup: 64 channels at least of four runs; in a step 256 channels
+    const double fwd = (double)d.N * ((double)((d.L + kConvRun - 1) / kConvRun + 1) / kConvRuns + 1) * (double)((d.C + 63) / 64);
+    const double wgs = (double)d.N * (double)bwd_blocks(d) * (double)((d.C + 63) / 64);
     const double ws = (double)d.N * (double)bwd_blocks(d) * (double)(d.F + 1) * (double)d.C * 4.0;
-    if (threads / 256.0 >= 2147483000.0 || wgs >= 2147483000.0 || ws >= kMaxBytes)
+    if (fwd >= 2147483000.0 || wgs >= 2147483000.0 || ws >= kMaxBytes)
         return fail(CONV_ERR_UNSUPPORTED, "N x L x C is too large for one launch");
     conv_causal_plan *pl = new (std::nothrow) conv_causal_plan();
     if (!pl) return fail(CONV_ERR_NOMEM, "plan allocation failed");
@@ -299,7 +299,7 @@ conv_status_t conv_causal_create(const conv_causal_desc_t *desc, conv_causal_pla
     pl->esz = d.dtype == CONV_DT_BF16 ? 2 : 4;
     pl->bwd_rows = d.N * bwd_blocks(d);
     pl->ws_bytes = pl->bwd_rows * (d.F + 1) * d.C * 4;
-    snprintf(pl->text, sizeof(pl->text), "causal %s N=%lld L=%lld C=%lld F=%lld%s%s, %d tokens per thread",
+    snprintf(pl->text, sizeof(pl->text), "causal %s N=%lld L=%lld C=%lld F=%lld%s%s, %d tokens per wave",
              d.dtype == CONV_DT_BF16 ? "bf16" : "f32", (long long)d.N, (long long)d.L, (long long)d.C, (long long)d.F,
              d.has_bias ? " bias" : "", d.silu ? " silu" : "", kConvRun);
     if (getenv("CONVFWD_LOG")) fprintf(stderr, "convfwd: %s\n", pl->text);
@@ -341,9 +341,10 @@ static conv_status_t causal_forward(const conv_causal_plan_t *plan, const conv_c
     p.x_ld = in[0].ld; p.y_ld = out[0].ld;
     p.N = (int)d.N; p.C = (int)d.C; p.CV = (int)(d.C / V); p.L = L;
     p.blocks = (L + kConvRun - 1) / kConvRun;
-    const int64_t threads = step ? d.N * p.CV : d.N * (p.blocks + (a->state_out ? 1 : 0)) * p.CV;
+    const int64_t runs = p.blocks + (a->state_out ? 1 : 0);
+    const int64_t grid = step ? (d.N * p.CV + 255) / 256 : d.N * ((runs + kConvRuns - 1) / kConvRuns) * ((p.CV + 63) / 64);
     (void)hipGetLastError();
-    launch_causal(step ? CONV_STEP : CONV_RUN, d, V, p, (threads + 255) / 256, (hipStream_t)stream);
+    launch_causal(step ? CONV_STEP : CONV_RUN, d, V, p, grid, (hipStream_t)stream);
     return launched();
 }
 
@@ -406,7 +407,7 @@ conv_status_t conv_causal_bwd_run(const conv_causal_plan_t *plan, const conv_cau
     (void)hipGetLastError();
     hipStream_t s = (hipStream_t)stream;
     if (d.N > 0)
-        launch_causal(CONV_BWD, d, V, p, plan->bwd_rows * ((p.CV + kConvBwdCv - 1) / kConvBwdCv), s);
+        launch_causal(CONV_BWD, d, V, p, plan->bwd_rows * ((p.CV + 63) / 64), s);
     const dim3 grid((unsigned)((d.F + 1) * ((d.C + 63) / 64)));      // no rows: dw and dbias are zeros
     if (d.dtype == CONV_DT_BF16)
         hipLaunchKernelGGL(causal_reduce_kernel<bf16_t>, grid, dim3(256), 0, s, p.partial, (bf16_t *)a->dw,
