@@ -80,7 +80,10 @@ template <typename T> struct Frag;
 template <> struct Frag<bf16_t> {
     static constexpr int Q = 64;            // tokens of a chunk
     static constexpr int VE = 8;            // elements of 16 bytes
-    static constexpr int PAD = 8;           // row padding of the LDS tiles, elements: 16 bytes
+    // Row padding of the LDS tiles, elements: 32 bytes.  Rows are 128 or 256 bytes;
+    // with 32 more, the 16 rows of a fragment and the 4 rows of a transposing read
+    // take 4.0 clocks a wave instruction each (16 more: 8.0 and 4.0).
+    static constexpr int PAD = 16;
     typedef bf16x8 type;
 };
 template <> struct Frag<float> {
@@ -232,10 +235,12 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 template <typename T, int ROWS, int COLS, int THREADS = 256> struct Tile {
     static constexpr int VE = Frag<T>::VE;
-    static constexpr int NV = ROWS * COLS / VE / THREADS;
+    static constexpr int ALL = ROWS * COLS / VE;        // vectors of the tile
+    static constexpr int NV = (ALL + THREADS - 1) / THREADS;
     static constexpr int LD = COLS + Frag<T>::PAD;
     static constexpr int CV = COLS / VE;
-    static_assert(ROWS * COLS % (VE * THREADS) == 0, "whole vectors per thread");
+    static_assert(ALL % THREADS == 0 || ALL < THREADS, "whole vectors per thread");
+    static SEQ_DEV bool mine() { return ALL >= THREADS || (int)threadIdx.x < ALL; }
     static constexpr uint32_t kOut = 0x80000000u;       // an offset past any buffer
     u32x4 v[NV];
 
@@ -253,7 +258,7 @@ template <typename T, int ROWS, int COLS, int THREADS = 256> struct Tile {
     static SEQ_DEV uint32_t first(int64_t ld, int cols)
     {
         const int r = threadIdx.x / CV, c = column();
-        return c < cols ? (uint32_t)(r * (int)ld + c) * (uint32_t)sizeof(T) : kOut;
+        return c < cols && mine() ? (uint32_t)(r * (int)ld + c) * (uint32_t)sizeof(T) : kOut;
     }
     static SEQ_DEV uint32_t opaque(uint32_t v)
     {
@@ -269,7 +274,7 @@ template <typename T, int ROWS, int COLS, int THREADS = 256> struct Tile {
 #pragma unroll
             for (int k = 0; k < NV; ++k) v[k] = __builtin_amdgcn_raw_buffer_load_b128(buf, o + k * step, 0, 0);
         } else {
-            const int left = (int)opaque(cols - column());
+            const int left = (int)opaque(mine() ? cols - column() : 0);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 if constexpr (sizeof(T) == 4) {
@@ -293,7 +298,8 @@ template <typename T, int ROWS, int COLS, int THREADS = 256> struct Tile {
     {
         T *p = lds + threadIdx.x / CV * LD + column();
 #pragma unroll
-        for (int k = 0; k < NV; ++k) *reinterpret_cast<u32x4 *>(p + k * kStep * LD) = v[k];
+        for (int k = 0; k < NV; ++k)
+            if (mine()) *reinterpret_cast<u32x4 *>(p + k * kStep * LD) = v[k];
     }
     // from LDS to memory
     static SEQ_DEV void write(const T *lds, T *g, int64_t ld, int rows, int cols, bool vec)
@@ -301,7 +307,7 @@ template <typename T, int ROWS, int COLS, int THREADS = 256> struct Tile {
         Tile t;
         const T *p = lds + threadIdx.x / CV * LD + column();
 #pragma unroll
-        for (int k = 0; k < NV; ++k) t.v[k] = *reinterpret_cast<const u32x4 *>(p + k * kStep * LD);
+        for (int k = 0; k < NV; ++k) t.v[k] = mine() ? *reinterpret_cast<const u32x4 *>(p + k * kStep * LD) : u32x4{0, 0, 0, 0};
         t.put(g, ld, rows, cols, vec);
     }
     static SEQ_DEV void write_zeros(T *g, int64_t ld, int rows, int cols, bool vec)
@@ -320,7 +326,7 @@ template <typename T, int ROWS, int COLS, int THREADS = 256> struct Tile {
 #pragma unroll
             for (int k = 0; k < NV; ++k) __builtin_amdgcn_raw_buffer_store_b128(v[k], buf, o + k * step, 0, 0);
         } else {
-            const int left = (int)opaque(cols - column());
+            const int left = (int)opaque(mine() ? cols - column() : 0);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
 #pragma unroll
@@ -341,6 +347,18 @@ template <typename T, int ROWS, int COLS, int THREADS = 256> struct Tile {
 // multiplies, and each wait is a round trip. The kernels read fragments in
 // groups, a group ahead of the products, and keep the order with this.
 SEQ_DEV void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// a value the compiler cannot know to be the same as before
+SEQ_DEV int fresh_vector(int v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+SEQ_DEV int fresh_scalar(int v)
+{
+    asm volatile("" : "+s"(v));
+    return v;
+}
 
 // the wave's number in the workgroup, known to be the same in all its lanes
 SEQ_DEV int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
@@ -846,27 +864,38 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
 }
 
 // ---- gradient ------------------------------------------------------------------
-// One workgroup: one chunk of one group, a slice of the group's heads one after
-// the other.  C . B is the same for all of them and stays in registers, and so
-// do the sums of dS over the heads, from which dB and dC get their parts inside
-// the chunk by one product each at the end.  The waves share dP's 16x16 tiles
-// as the forward shares its scores; dx goes by channels (wave w: 16w..), dB and
-// dC by states (wave w: the 16-state tiles w, w + 4).  The states at the chunk's
-// borders and their gradients come from memory, where the two runs of
-// scan_state_kernel left them.
-template <typename T, int SP> __global__ void __launch_bounds__(256) scan_bwd_kernel(ScanParams p)
+// One workgroup of eight waves: one chunk of one group, a slice of the group's
+// heads (in blocks of 64 channels) one after the other.  C . B is the same for
+// all of them and stays in registers, and so do the sums of dS over the heads,
+// from which dB and dC get their parts inside the chunk by one product each at
+// the end.  The waves share dP's 16x16 tiles as the forward shares its scores;
+// dB and dC go by states (and tokens, where there are fewer than 8 x 16 states),
+// dx by channels and halves of the tokens.  The states at the chunk's borders and
+// their gradients come from memory, where the two runs of the state kernel left
+// them.  While a head is computed the next one's x, dy and states are on their
+// way into registers, wave 6 does its decays, and wave 7 turns the sums that the
+// head before left in LDS into ddt and its parts of dA, ddt_bias and dD.
+template <typename T, int SP> struct BwdShared {
+    static constexpr int Q = Frag<T>::Q, NI = Q / 16, NS = terms<T, 3>();
+    static constexpr int XLD = kPB + Frag<T>::PAD, BLD = SP + Frag<T>::PAD, MLD = Q + Frag<T>::PAD;
+    __align__(16) T x[Q * XLD], y[Q * XLD];     // x and dy
+    __align__(16) T b[Q * BLD], c[Q * BLD];
+    __align__(16) T m[NS * Q * MLD];            // [term][j][i]
+    __align__(16) T u[NS * SP * XLD];           // [term][state][channel]
+    __align__(16) float dt[2][Q], cum[2][Q], low[2][Q], w[2][Q], e[2][Q], raw[2][Q];   // w: e^{c_Q - c_j}
+    float row[2][NI][Q], col[2][NI][Q], cd[2][8][Q], xd[2][4][Q], dot[2][8], dd[2][8];
+};
+
+template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_kernel(ScanParams p)
 {
-    constexpr int Q = Frag<T>::Q, NT = SP / 16, NI = Q / 16, TRI = NI * (NI + 1) / 2, TPW = (TRI + 3) / 4;
-    constexpr int NS = terms<T, 3>(), MLD = Q + Frag<T>::PAD, NTW = (NT + 3) / 4, ULD = kPB + Frag<T>::PAD;
-    typedef Tile<T, Q, kPB> XT;
-    typedef Tile<T, Q, SP> BT;
+    typedef BwdShared<T, SP> Sh;
+    constexpr int Q = Sh::Q, NI = Sh::NI, NS = Sh::NS, XLD = Sh::XLD, BLD = Sh::BLD, MLD = Sh::MLD;
+    constexpr int NT = SP / 16, TRI = NI * (NI + 1) / 2, TPW = (TRI + 7) / 8;
+    constexpr int WN = NT, WI = 8 / WN, ITW = NI / WI > 0 ? NI / WI : 1, JW = NI / 2;
+    typedef Tile<T, Q, kPB, 512> XT;
+    typedef Tile<T, Q, SP, 512> BT;
     typedef typename Frag<T>::type frag;
-    __shared__ __align__(16) T sX[Q * XT::LD], sY[Q * XT::LD];        // x and dy
-    __shared__ __align__(16) T sB[Q * BT::LD], sC[Q * BT::LD];
-    __shared__ __align__(16) T sM[NS * Q * MLD];                      // [term][j][i]
-    __shared__ __align__(16) T sU[NS * SP * ULD];                     // [term][state][channel]
-    __shared__ __align__(16) float sCum[Q], sLow[Q], sDt[Q], sW[Q], sE[Q];   // as in the forward, but sW without dt_j
-    __shared__ float sRow[NI][Q], sCol[NI][Q], sCd[4][Q], sXd[4][Q], sDot[4], sDD[4];
+    __shared__ Sh sh;
     const int lane = threadIdx.x & 63, w = wave_id(), q = lane >> 4, l16 = lane & 15;
     const int slice = (int)(blockIdx.x % p.slices);
     const int64_t ng = blockIdx.x / p.slices;
@@ -874,314 +903,365 @@ template <typename T, int SP> __global__ void __launch_bounds__(256) scan_bwd_ke
     const int64_t nc = ng / p.G, n = nc / p.K;
     const int c = (int)(nc - n * p.K), hpg = p.H / p.G;
     const int h_lo = slice * p.heads_per_slice, h_hi = min(hpg, h_lo + p.heads_per_slice);
+    const int blocks = (h_hi - h_lo) * p.NPB;           // channel blocks of the slice's heads
     const int64_t len = seq_len(p.lengths, n, p.L), t0 = (int64_t)c * Q;
     const int rows = (int)max((int64_t)0, min((int64_t)Q, len - t0)), all_rows = (int)min((int64_t)Q, p.L - t0);
     const int64_t base = n * p.L + t0;
     const int64_t NK = (int64_t)p.N * p.K;
+    const int nt = w % WN, it0 = w / WN * ITW;          // dB and dC: states 16 nt .., tokens 16 it0 ..
+    const bool on = it0 < NI;
+    const int pt = w & 3, jt0 = (w >> 2) * JW;          // dx: channels 16 pt .., tokens 16 jt0 ..
 
-    f32x4 sc[TPW], ds[TPW], dB[NI][NTW], dC[NI][NTW];
-    float cv[NI][NTW][4];
+    XT xt, yt;
+    float h0[16], u[16];        // state 16 nt + lane % 16, channels 32 ks + 8q + e at 8 ks + e
+    auto head_of = [&](int k) __attribute__((always_inline)) { return g * hpg + h_lo + k / p.NPB; };
+    auto fetch = [&](int k) __attribute__((always_inline)) {
+        const int h = head_of(k), pb = k % p.NPB, pcols = min(kPB, p.P - pb * kPB);
+        const int64_t xo = (int64_t)h * p.P + pb * kPB;
+        xt.load((const T *)p.x + base * p.x_ld + xo, p.x_ld, rows, pcols, p.vec);
+        yt.load((const T *)p.dy + base * p.dy_ld + xo, p.dy_ld, rows, pcols, p.vec);
+    };
+    auto fetch_states = [&](int k) __attribute__((always_inline)) {
+        const int h = head_of(k), pb = k % p.NPB;
+        const int64_t o = (((n * p.H + h) * p.NPB + pb) * p.K + c) * (SP * kPB) + (nt * 16 + l16) * kPB + q * 8;
+        // behind the sequence x, dy and dt are zeros: any finite state will do
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+            if (rows > 0) {
+                a = *reinterpret_cast<const f32x4 *>(p.bound[0] + o + (i >> 1) * 32 + (i & 1) * 4);
+                b = *reinterpret_cast<const f32x4 *>(p.bound[1] + o + (i >> 1) * 32 + (i & 1) * 4);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) h0[i * 4 + r] = a[r], u[i * 4 + r] = b[r];
+        }
+    };
+    auto decays = [&](int k) __attribute__((always_inline)) {       // by one wave
+        const int h = head_of(k), to = (k / p.NPB) & 1;
+        float raw = 0.0f, dt;
+        double cum;
+        if (lane < rows) raw = (float)((const T *)p.dt)[(base + lane) * p.dt_ld + h] + (p.dt_bias ? p.dt_bias[h] : 0.0f);
+        chunk_decay(raw, lane < rows, p.a[h], p.softplus, dt, cum);
+        const double tot = wave_last(cum);
+        if (lane < Q) {
+            sh.raw[to][lane] = raw;
+            sh.dt[to][lane] = dt;
+            sh.cum[to][lane] = (float)cum;
+            sh.low[to][lane] = (float)(cum - (double)(float)cum);
+            sh.w[to][lane] = exp2_fast((float)(tot - cum));
+            sh.e[to][lane] = exp2_fast((float)cum);
+        }
+    };
+    // wave 7, per token: the sums of a head over its channel blocks
+    float rs = 0.0f, cs = 0.0f, cd = 0.0f, ee = 0.0f, dot = 0.0f, dd = 0.0f;
+    auto finish = [&](int k) __attribute__((always_inline)) {
+        const int at = k & 1, d = (k / p.NPB) & 1;
+        if (lane < Q) {
+#pragma unroll
+            for (int t = 0; t < NI; ++t) rs += sh.row[at][t][lane], cs += sh.col[at][t][lane];
+#pragma unroll
+            for (int t = 0; t < WN; ++t) cd += sh.cd[at][t][lane];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) ee += sh.xd[at][t][lane];
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) dot += sh.dot[at][t], dd += sh.dd[at][t];
+        if (k % p.NPB != p.NPB - 1) return;
+        const int h = head_of(k);
+        const float dt = lane < Q ? sh.dt[d][lane] : 0.0f, raw = lane < Q ? sh.raw[d][lane] : 0.0f, dec = sh.e[d][Q - 1];
+        const double before = (double)dt * ee - cs, behind = (double)rs - cs + cd;
+        const double b1 = wave_prefix(before), b2 = wave_prefix(behind);
+        const float dl = (float)((b1 - before) + (wave_last(b2) - b2 + behind) + (double)(dec * dot));
+        float draw = fmaf(p.a[h], dl, ee);
+        if (p.softplus) draw *= 1.0f / (1.0f + expf(-raw));
+        if (lane >= rows) draw = 0.0f;
+        if (lane < all_rows) ((T *)p.ddt)[(base + lane) * p.ddt_ld + h] = (T)draw;
+        const float sa = wave_sum(dl * dt), sb = wave_sum(draw);
+        if (lane == 0) {
+            float *o = p.part_head + nc * p.H + h;
+            o[0] = sa;
+            o[NK * p.H] = sb;
+            o[2 * NK * p.H] = dd;
+        }
+        rs = cs = cd = ee = dot = dd = 0.0f;
+    };
+
+    f32x4 sc[TPW], ds[TPW], dB[ITW], dC[ITW];
 #pragma unroll
     for (int k = 0; k < TPW; ++k) sc[k] = ds[k] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int it = 0; it < NI; ++it)
-#pragma unroll
-        for (int k = 0; k < NTW; ++k) dB[it][k] = dC[it][k] = f32x4{0, 0, 0, 0};
+    for (int k = 0; k < ITW; ++k) dB[k] = dC[k] = f32x4{0, 0, 0, 0};
     {
         BT bt, ct;
         bt.load((const T *)p.b + base * p.b_ld + (int64_t)g * p.S, p.b_ld, rows, p.S, p.vec);
         ct.load((const T *)p.c + base * p.c_ld + (int64_t)g * p.S, p.c_ld, rows, p.S, p.vec);
-        bt.store(sB);
-        ct.store(sC);
-        for (int e = threadIdx.x; e < NS * Q * MLD; e += 256) sM[e] = (T)0.0f;
-        for (int e = threadIdx.x; e < NI * Q; e += 256) sRow[0][e] = sCol[0][e] = 0.0f;
+        fetch(0);
+        fetch_states(0);
+        bt.store(sh.b);
+        ct.store(sh.c);
+        // what is never written: M above its diagonal tiles, the same of the sums
+        for (int e = threadIdx.x; e < NS * Q * MLD; e += 512) sh.m[e] = (T)0.0f;
+        for (int e = threadIdx.x; e < 2 * NI * Q; e += 512) sh.row[0][0][e] = sh.col[0][0][e] = 0.0f;
+        if (w == 6) decays(0);
     }
     __syncthreads();
     // scores: rows i, column j in a lane
 #pragma unroll
     for (int k = 0; k < TPW; ++k) {
-        const int t = w + 4 * k;
+        const int t = w + 8 * k;
         if (t < TRI) {
             int it, jt;
             tri_tile(t, it, jt);
 #pragma unroll
             for (int ks = 0; ks < SP / 32; ++ks)
-                sc[k] = mma(read_rows(sC, BT::LD, it * 16, ks * 32, lane), read_rows(sB, BT::LD, jt * 16, ks * 32, lane), sc[k]);
+                sc[k] = mma(read_rows(sh.c, BLD, it * 16, ks * 32, lane), read_rows(sh.b, BLD, jt * 16, ks * 32, lane), sc[k]);
         }
     }
+    const int lane_ = lane, w_ = w;
+    for (int k = 0; k < blocks; ++k) {
+        // Addresses and masks follow from these two; taken anew each time they are
+        // computed where they are used, or the compiler computes all of them ahead
+        // of the loop and keeps them in memory.
+        const int lane = fresh_vector(lane_), w = fresh_scalar(w_), q = lane >> 4, l16 = lane & 15;
+        const int nt = w % WN, it0 = w / WN * ITW, pt = w & 3, jt0 = (w >> 2) * JW;
+        const bool on = it0 < NI;
+        const int at = k & 1, d = (k / p.NPB) & 1, h = head_of(k), pb = k % p.NPB, pcols = min(kPB, p.P - pb * kPB);
+        const float skip = p.d ? p.d[h] : 0.0f;
+        const float *s_cum = sh.cum[d], *s_low = sh.low[d], *s_dt = sh.dt[d], *s_w = sh.w[d], *s_e = sh.e[d];
+        Split<T, NS> hs[2];
+        float part = 0.0f;
+        make_split(reinterpret_cast<const float (&)[8]>(h0[0]), hs[0]);
+        make_split(reinterpret_cast<const float (&)[8]>(h0[8]), hs[1]);
+        if (it0 == 0) {
 #pragma unroll
-    for (int it = 0; it < NI; ++it)
-#pragma unroll
-        for (int k = 0; k < NTW; ++k)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                cv[it][k][r] = w + 4 * k < NT ? (float)sC[(it * 16 + q * 4 + r) * BT::LD + (w + 4 * k) * 16 + l16] : 0.0f;
-
-    for (int hh = h_lo; hh < h_hi; ++hh) {
-        const int h = g * hpg + hh;
-        const float a = p.a[h], skip = p.d ? p.d[h] : 0.0f;
-        float raw = 0.0f, dt = 0.0f;
-        double cum = 0.0;
-        float rs = 0.0f, cs = 0.0f, cd = 0.0f, ee = 0.0f, dot = 0.0f, dd = 0.0f;    // wave 0: per token, over the channel blocks
-        if (w == 0) {
-            if (lane < rows) raw = (float)((const T *)p.dt)[(base + lane) * p.dt_ld + h] + (p.dt_bias ? p.dt_bias[h] : 0.0f);
-            chunk_decay(raw, lane < rows, a, p.softplus, dt, cum);
+            for (int e = 0; e < 16; ++e) part = fmaf(h0[e], u[e], part);
         }
-        for (int pb = 0; pb < p.NPB; ++pb) {
-            const int pcols = min(kPB, p.P - pb * kPB);
-            const int64_t xo = (int64_t)h * p.P + pb * kPB;
-            XT xt, yt;
-            xt.load((const T *)p.x + base * p.x_ld + xo, p.x_ld, rows, pcols, p.vec);
-            yt.load((const T *)p.dy + base * p.dy_ld + xo, p.dy_ld, rows, pcols, p.vec);
-            f32x4 h0[NTW][4], u[NTW][4];
-            const int64_t bo = (((n * p.H + h) * p.NPB + pb) * p.K + c) * (SP * kPB);
-            // behind the sequence x, dy and dt are zeros: any finite state will do
+        part = wave_sum(part);
+        __syncthreads();        // all waves are done with the block before
+        xt.store(sh.x);
+        yt.store(sh.y);
+        if (lane == 0) sh.dot[at][w] = part;
+        if (it0 == 0) {
 #pragma unroll
-            for (int k = 0; k < NTW; ++k)
+            for (int ks = 0; ks < 2; ++ks) {
+                Split<T, NS> us;
+                make_split(reinterpret_cast<const float (&)[8]>(u[ks * 8]), us);
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    h0[k][b] = u[k][b] = f32x4{0, 0, 0, 0};
-                    if (w + 4 * k < NT && rows > 0) {
-                        const int64_t o = bo + ((w + 4 * k) * 16 + l16) * kPB + b * 16 + q * 4;
-                        h0[k][b] = *reinterpret_cast<const f32x4 *>(p.bound[0] + o);
-                        u[k][b] = *reinterpret_cast<const f32x4 *>(p.bound[1] + o);
-                    }
-                }
-            float part = 0.0f;
-#pragma unroll
-            for (int k = 0; k < NTW; ++k)
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) part = fmaf(h0[k][b][r], u[k][b][r], part);
-            part = wave_sum(part);
-            __syncthreads();
-            xt.store(sX);
-            yt.store(sY);
-            if (w == 0 && lane < Q) {
-                const double tot = wave_last(cum);
-                sDt[lane] = dt;
-                sCum[lane] = (float)cum;
-                sLow[lane] = (float)(cum - (double)(float)cum);
-                sW[lane] = exp2_fast((float)(tot - cum));
-                sE[lane] = exp2_fast((float)cum);
+                for (int m = 0; m < NS; ++m)
+                    *reinterpret_cast<frag *>(sh.u + m * SP * XLD + (nt * 16 + l16) * XLD + ks * 32 + q * 8) = us.f[m];
             }
-            if (lane == 0) sDot[w] = part;
+        }
+        __syncthreads();
+        if (k + 1 < blocks) fetch(k + 1);
+        // dP, M and dS, tile by tile; M goes to LDS transposed (rows j)
+        float diag = 0.0f;
 #pragma unroll
-            for (int k = 0; k < NTW; ++k)
+        for (int t8 = 0; t8 < TPW; ++t8) {
+            const int t = w + 8 * t8;
+            if (t < TRI) {
+                int it, jt;
+                tri_tile(t, it, jt);
+                const int i = it * 16 + q * 4, j = jt * 16 + l16;
+                frag yf[2], xf[2];
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    if (w + 4 * k < NT)
-                        write_split4<NS>(sU + ((w + 4 * k) * 16 + l16) * ULD + b * 16 + q * 4, SP * ULD, u[k][b]);
-            __syncthreads();
-            // dP, M and dS, tile by tile; M goes to LDS transposed (rows j)
-            float diag = 0.0f;
-#pragma unroll
-            for (int k = 0; k < TPW; ++k) {
-                const int t = w + 4 * k;
-                if (t < TRI) {
-                    int it, jt;
-                    tri_tile(t, it, jt);
-                    f32x4 dp = {0, 0, 0, 0}, m, wr;
-#pragma unroll
-                    for (int ks = 0; ks < 2; ++ks)
-                        dp = mma(read_rows(sY, XT::LD, it * 16, ks * 32, lane), read_rows(sX, XT::LD, jt * 16, ks * 32, lane), dp);
-                    const int i = it * 16 + q * 4, j = jt * 16 + l16;
-                    const float dj = sDt[j];
-                    const f32x4 ex = (*reinterpret_cast<const f32x4 *>(sCum + i) - sCum[j]) +
-                                     (*reinterpret_cast<const f32x4 *>(sLow + i) - sLow[j]);
-                    float col = 0.0f;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const bool in = i + r >= j;
-                        const float dec = in ? exp2_fast(ex[r]) : 0.0f;
-                        if (i + r == j) diag += dp[r];
-                        m[r] = in ? sc[k][r] * dec : 0.0f;
-                        const float s = in ? dp[r] * dec * dj : 0.0f;
-                        ds[k][r] += s;
-                        wr[r] = s * sc[k][r];
-                        col += wr[r];
-                    }
-                    write_split4<NS>(sM + j * MLD + i, Q * MLD, m);
-                    col += __shfl_xor(col, 16);
-                    col += __shfl_xor(col, 32);
-                    if (q == 0) sCol[it][j] = col;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float s = row_sum(wr[r]);
-                        if (l16 == 0) sRow[jt][i + r] = s;
-                    }
+                for (int ks = 0; ks < 2; ++ks) {
+                    yf[ks] = read_rows(sh.y, XLD, it * 16, ks * 32, lane);
+                    xf[ks] = read_rows(sh.x, XLD, jt * 16, ks * 32, lane);
                 }
-            }
-            diag = wave_sum(diag);
-            if (lane == 0) sDD[w] = diag;
-            // dC and dB through the states at the borders
-            float cdp[NI][4];
+                const float dj = s_dt[j];
+                const f32x4 ex = (*reinterpret_cast<const f32x4 *>(s_cum + i) - s_cum[j]) +
+                                 (*reinterpret_cast<const f32x4 *>(s_low + i) - s_low[j]);
+                in_order();
+                f32x4 dp = {0, 0, 0, 0}, m, wr;
 #pragma unroll
-            for (int it = 0; it < NI; ++it)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) cdp[it][r] = 0.0f;
-#pragma unroll
-            for (int k = 0; k < NTW; ++k) {
-                if (w + 4 * k < NT) {
-                    Split<T, NS> hs[2], us[2];
-#pragma unroll
-                    for (int ks = 0; ks < 2; ++ks) {
-                        float v[8];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = h0[k][2 * ks][e], v[4 + e] = h0[k][2 * ks + 1][e];
-                        make_split(v, hs[ks]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = u[k][2 * ks][e], v[4 + e] = u[k][2 * ks + 1][e];
-                        make_split(v, us[ks]);
-                    }
-#pragma unroll
-                    for (int it = 0; it < NI; ++it) {
-                        f32x4 ac = {0, 0, 0, 0}, ab = {0, 0, 0, 0};
-#pragma unroll
-                        for (int ks = 0; ks < 2; ++ks) {
-                            ac = mma_b(read_rows_stacked(sY, XT::LD, it * 16, ks * 32, lane), hs[ks], ac);
-                            ab = mma_b(read_rows_stacked(sX, XT::LD, it * 16, ks * 32, lane), us[ks], ab);
-                        }
-                        const f32x4 ei = *reinterpret_cast<const f32x4 *>(sE + it * 16 + q * 4);
-                        const f32x4 wi = *reinterpret_cast<const f32x4 *>(sW + it * 16 + q * 4) *
-                                         *reinterpret_cast<const f32x4 *>(sDt + it * 16 + q * 4);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const float v = ac[r] * ei[r];
-                            dC[it][k][r] += v;
-                            cdp[it][r] = fmaf(v, cv[it][k][r], cdp[it][r]);
-                            dB[it][k][r] = fmaf(ab[r], wi[r], dB[it][k][r]);
-                        }
-                    }
-                }
-            }
-#pragma unroll
-            for (int it = 0; it < NI; ++it)
+                for (int ks = 0; ks < 2; ++ks) dp = mma(yf[ks], xf[ks], dp);
+                float col = 0.0f;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float s = row_sum(cdp[it][r]);
-                    if (l16 == 0) sCd[w][it * 16 + q * 4 + r] = s;
+                    const bool in = i + r >= j;
+                    const float dec = in ? exp2_fast(ex[r]) : 0.0f;
+                    if (i + r == j) diag += dp[r];
+                    m[r] = in ? sc[t8][r] * dec : 0.0f;
+                    const float s = in ? dp[r] * dec * dj : 0.0f;
+                    ds[t8][r] += s;
+                    wr[r] = s * sc[t8][r];
+                    col += wr[r];
                 }
-            __syncthreads();
-            // dx, by channels
-            {
-                f32x4 dx[NI];
+                write_split4<NS>(sh.m + j * MLD + i, Q * MLD, m);
+                col += __shfl_xor(col, 16);
+                col += __shfl_xor(col, 32);
+                if (q == 0) sh.col[at][it][j] = col;
 #pragma unroll
-                for (int jt = 0; jt < NI; ++jt) dx[jt] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int ks = 0; ks < SP / 32; ++ks) {
-                    frag uf[NS];
-#pragma unroll
-                    for (int m = 0; m < NS; ++m) uf[m] = read_cols(sU + m * SP * ULD, ULD, ks * 32, w * 16, lane);
-#pragma unroll
-                    for (int jt = 0; jt < NI; ++jt) {
-                        const frag bf = read_rows(sB, BT::LD, jt * 16, ks * 32, lane);
-#pragma unroll
-                        for (int m = 0; m < NS; ++m) dx[jt] = mma(bf, uf[m], dx[jt]);
-                    }
+                for (int r = 0; r < 4; ++r) {
+                    const float s = row_sum(wr[r]);
+                    if (l16 == 0) sh.row[at][jt][i + r] = s;
                 }
-#pragma unroll
-                for (int jt = 0; jt < NI; ++jt) dx[jt] *= *reinterpret_cast<const f32x4 *>(sW + jt * 16 + q * 4);
-#pragma unroll
-                for (int ks = 0; ks < Q / 32; ++ks) {
-                    const frag yf = read_cols(sY, XT::LD, ks * 32, w * 16, lane);
-#pragma unroll
-                    for (int jt = 0; jt < 2 * ks + 2; ++jt)
-#pragma unroll
-                        for (int m = 0; m < NS; ++m)
-                            dx[jt] = mma(read_rows(sM + m * Q * MLD, MLD, jt * 16, ks * 32, lane), yf, dx[jt]);
-                }
-#pragma unroll
-                for (int jt = 0; jt < NI; ++jt) {
-                    const f32x4 dj = *reinterpret_cast<const f32x4 *>(sDt + jt * 16 + q * 4);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int o = (jt * 16 + q * 4 + r) * XT::LD + w * 16 + l16;
-                        const float s = row_sum((float)sX[o] * dx[jt][r]);
-                        if (l16 == 0) sXd[w][jt * 16 + q * 4 + r] = s;
-                        sX[o] = (T)fmaf(skip, (float)sY[o], dj[r] * dx[jt][r]);     // this wave's own columns
-                    }
-                }
-            }
-            __syncthreads();
-            XT::write(sX, (T *)p.dx + base * p.dx_ld + xo, p.dx_ld, all_rows, pcols, p.vec);
-            if (w == 0) {
-                if (lane < Q) {
-#pragma unroll
-                    for (int t = 0; t < NI; ++t) rs += sRow[t][lane], cs += sCol[t][lane];
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) cd += sCd[t][lane], ee += sXd[t][lane];
-                }
-                dot += (sDot[0] + sDot[1]) + (sDot[2] + sDot[3]);
-                dd += (sDD[0] + sDD[1]) + (sDD[2] + sDD[3]);
             }
         }
-        if (w == 0) {
-            const float tot = (float)wave_last(cum);
-            const double before = (double)dt * ee - cs, behind = (double)rs - cs + cd;
-            const double b1 = wave_prefix(before), b2 = wave_prefix(behind);
-            const double all2 = wave_last(b2);
-            const float dl = (float)((b1 - before) + (all2 - b2 + behind) + (double)(exp2_fast(tot) * dot));
-            float draw = fmaf(a, dl, ee);
-            if (p.softplus) draw *= 1.0f / (1.0f + expf(-raw));
-            if (lane >= rows) draw = 0.0f;
-            if (lane < all_rows) ((T *)p.ddt)[(base + lane) * p.ddt_ld + h] = (T)draw;
-            const float sa = wave_sum(dl * dt), sb = wave_sum(draw);
-            if (lane == 0) {
-                float *o = p.part_head + nc * p.H + h;
-                o[0] = sa;
-                o[NK * p.H] = sb;
-                o[2 * NK * p.H] = dd;
+        diag = wave_sum(diag);
+        if (lane == 0) sh.dd[at][w] = diag;
+        // dC and dB through the states at the borders
+        if (on) {
+            frag yf[2][2], xf[2][2], uf[2][NS];
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int m = 0; m < NS; ++m) uf[ks][m] = read_rows(sh.u + m * SP * XLD, XLD, nt * 16, ks * 32, lane);
+            auto read = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    yf[i & 1][ks] = read_rows(sh.y, XLD, (it0 + i) * 16, ks * 32, lane);
+                    xf[i & 1][ks] = read_rows(sh.x, XLD, (it0 + i) * 16, ks * 32, lane);
+                }
+            };
+            read(0);
+#pragma unroll
+            for (int i = 0; i < ITW; ++i) {
+                const int row = (it0 + i) * 16 + q * 4;
+                const f32x4 ei = *reinterpret_cast<const f32x4 *>(s_e + row);
+                const f32x4 wi = *reinterpret_cast<const f32x4 *>(s_w + row) * *reinterpret_cast<const f32x4 *>(s_dt + row);
+                float cv[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) cv[r] = (float)sh.c[(row + r) * BLD + nt * 16 + l16];
+                if (i + 1 < ITW) read(i + 1);
+                in_order();
+                f32x4 ac = {0, 0, 0, 0}, ab = {0, 0, 0, 0};
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                    for (int m = 0; m < NS; ++m) {
+                        ac = mma(yf[i & 1][ks], hs[ks].f[m], ac);
+                        ab = mma(xf[i & 1][ks], uf[ks][m], ab);
+                    }
+                ac *= ei;
+                dC[i] += ac;
+                dB[i] += ab * wi;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float s = row_sum(ac[r] * cv[r]);
+                    if (l16 == 0) sh.cd[at][nt][row + r] = s;
+                }
             }
         }
+        if (w == 7 && k > 0) finish(k - 1);
+        __syncthreads();
+        if (k + 1 < blocks) fetch_states(k + 1);
+        // dx
+        {
+            f32x4 dx[JW];
+            frag uf[2][NS], bf[2][JW];
+            auto read = [&](int ks) __attribute__((always_inline)) {
+#pragma unroll
+                for (int m = 0; m < NS; ++m) uf[ks & 1][m] = read_cols(sh.u + m * SP * XLD, XLD, ks * 32, pt * 16, lane);
+#pragma unroll
+                for (int j = 0; j < JW; ++j) bf[ks & 1][j] = read_rows(sh.b, BLD, (jt0 + j) * 16, ks * 32, lane);
+            };
+#pragma unroll
+            for (int j = 0; j < JW; ++j) dx[j] = f32x4{0, 0, 0, 0};
+            read(0);
+            frag yf[Q / 32], mf[JW][NS];
+            float xv[JW][4], yv[JW][4];
+#pragma unroll
+            for (int ks = 0; ks < SP / 32; ++ks) {
+                if (ks + 1 < SP / 32) {
+                    read(ks + 1);
+                } else {
+#pragma unroll
+                    for (int s = 0; s < Q / 32; ++s) yf[s] = read_cols(sh.y, XLD, s * 32, pt * 16, lane);
+#pragma unroll
+                    for (int j = 0; j < JW; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int o = ((jt0 + j) * 16 + q * 4 + r) * XLD + pt * 16 + l16;
+                            xv[j][r] = (float)sh.x[o];
+                            yv[j][r] = (float)sh.y[o];
+                        }
+                }
+                in_order();
+#pragma unroll
+                for (int m = 0; m < NS; ++m)
+#pragma unroll
+                    for (int j = 0; j < JW; ++j) dx[j] = mma(bf[ks & 1][j], uf[ks & 1][m], dx[j]);
+                in_order();
+            }
+#pragma unroll
+            for (int j = 0; j < JW; ++j) dx[j] *= *reinterpret_cast<const f32x4 *>(s_w + (jt0 + j) * 16 + q * 4);
+            // M's tiles (i >= j): in the upper half of the tokens only the second 32 meet it
+#pragma unroll
+            for (int ks = 0; ks < Q / 32; ++ks) {
+                if (ks * 2 + 1 < jt0) continue;
+#pragma unroll
+                for (int j = 0; j < JW; ++j)
+#pragma unroll
+                    for (int m = 0; m < NS; ++m)
+                        mf[j][m] = read_rows(sh.m + m * Q * MLD, MLD, (jt0 + j) * 16, ks * 32, lane);
+                in_order();
+#pragma unroll
+                for (int m = 0; m < NS; ++m)
+#pragma unroll
+                    for (int j = 0; j < JW; ++j) dx[j] = mma(mf[j][m], yf[ks], dx[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < JW; ++j) {
+                const f32x4 dj = *reinterpret_cast<const f32x4 *>(s_dt + (jt0 + j) * 16 + q * 4);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = (jt0 + j) * 16 + q * 4 + r;
+                    const float s = row_sum(xv[j][r] * dx[j][r]);
+                    if (l16 == 0) sh.xd[at][pt][row] = s;
+                    // in place of x: nothing reads other waves' columns of it any more
+                    sh.x[row * XLD + pt * 16 + l16] = (T)fmaf(skip, yv[j][r], dj[r] * dx[j][r]);
+                }
+            }
+        }
+        if (w == 6 && k + 1 < blocks && (k + 1) % p.NPB == 0) decays(k + 1);
+        __syncthreads();
+        XT::write(sh.x, (T *)p.dx + base * p.dx_ld + (int64_t)h * p.P + pb * kPB, p.dx_ld, all_rows, pcols, p.vec);
     }
+    if (w == 7) finish(blocks - 1);
     // the parts of dB and dC inside the chunk, from the sum of dS over the heads
-    __syncthreads();
+    // (M's last readers are behind the barrier above)
 #pragma unroll
     for (int k = 0; k < TPW; ++k) {
-        const int t = w + 4 * k;
+        const int t = w + 8 * k;
         if (t < TRI) {
             int it, jt;
             tri_tile(t, it, jt);
-            write_split4<NS>(sM + (jt * 16 + l16) * MLD + it * 16 + q * 4, Q * MLD, ds[k]);
+            write_split4<NS>(sh.m + (jt * 16 + l16) * MLD + it * 16 + q * 4, Q * MLD, ds[k]);
         }
     }
     __syncthreads();
+    if (!on) return;
 #pragma unroll
-    for (int k = 0; k < NTW; ++k) {
-        const int nt = w + 4 * k;
-        if (nt >= NT) continue;
+    for (int ks = 0; ks < Q / 32; ++ks) {
+        const frag bf = read_cols(sh.b, BLD, ks * 32, nt * 16, lane), cf = read_cols(sh.c, BLD, ks * 32, nt * 16, lane);
 #pragma unroll
-        for (int ks = 0; ks < Q / 32; ++ks) {
-            const frag bf = read_cols(sB, BT::LD, ks * 32, nt * 16, lane), cf = read_cols(sC, BT::LD, ks * 32, nt * 16, lane);
+        for (int i = 0; i < ITW; ++i)
 #pragma unroll
-            for (int t = 0; t < NI; ++t)
-#pragma unroll
-                for (int m = 0; m < NS; ++m) {
-                    const T *s = sM + m * Q * MLD;
-                    if (t < 2 * ks + 2) dB[t][k] = mma(read_rows(s, MLD, t * 16, ks * 32, lane), cf, dB[t][k]);
-                    if (t >= 2 * ks) dC[t][k] = mma(read_cols(s, MLD, ks * 32, t * 16, lane), bf, dC[t][k]);
-                }
-        }
-        const int s = nt * 16 + l16;
-        if (s >= p.S) continue;
-#pragma unroll
-        for (int t = 0; t < NI; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = t * 16 + q * 4 + r;
-                if (row >= all_rows) continue;
-                if (p.slices == 1) {
-                    ((T *)p.db)[(base + row) * p.db_ld + g * p.S + s] = (T)dB[t][k][r];
-                    ((T *)p.dc)[(base + row) * p.dc_ld + g * p.S + s] = (T)dC[t][k][r];
-                } else {
-                    const int64_t o = (((int64_t)slice * p.N * p.L + base + row) * p.G + g) * SP + s;
-                    p.part_b[o] = dB[t][k][r];
-                    p.part_c[o] = dC[t][k][r];
-                }
+            for (int m = 0; m < NS; ++m) {
+                const T *s = sh.m + m * Q * MLD;
+                const int t = it0 + i;
+                if (t < 2 * ks + 2) dB[i] = mma(read_rows(s, MLD, t * 16, ks * 32, lane), cf, dB[i]);
+                if (t >= 2 * ks) dC[i] = mma(read_cols(s, MLD, ks * 32, t * 16, lane), bf, dC[i]);
             }
     }
+    const int s = nt * 16 + l16;
+    if (s >= p.S) return;
+#pragma unroll
+    for (int i = 0; i < ITW; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = (it0 + i) * 16 + q * 4 + r;
+            if (row >= all_rows) continue;
+            if (p.slices == 1) {
+                ((T *)p.db)[(base + row) * p.db_ld + g * p.S + s] = (T)dB[i][r];
+                ((T *)p.dc)[(base + row) * p.dc_ld + g * p.S + s] = (T)dC[i][r];
+            } else {
+                const int64_t o = (((int64_t)slice * p.N * p.L + base + row) * p.G + g) * SP + s;
+                p.part_b[o] = dB[i][r];
+                p.part_c[o] = dC[i][r];
+            }
+        }
 }
 
 // What the chunks and head slices left: the first 3 H workgroups add dA,

@@ -226,7 +226,7 @@ template <typename T, int SP> void launch_bwd(ScanParams p, int64_t units, HeadG
         p.ahead = units * p.nseg;
         launch_states<T, SP, true>(p, 2 * p.ahead, s);
         const int64_t grid = (int64_t)p.N * p.K * p.G * p.slices;
-        hipLaunchKernelGGL((scan_bwd_kernel<T, SP>), dim3((unsigned)grid), dim3(256), 0, s, p);
+        hipLaunchKernelGGL((scan_bwd_kernel<T, SP>), dim3((unsigned)grid), dim3(512), 0, s, p);
     }
     const int64_t elems = p.slices > 1 ? (int64_t)p.N * p.L * p.G * SP : 0;
     hipLaunchKernelGGL((scan_reduce_kernel<T, SP>), dim3((unsigned)(3 * p.H + (elems + 255) / 256)), dim3(256), 0, s, p,
