@@ -466,7 +466,8 @@ conv_status_t conv_scan_create(const conv_scan_desc_t *desc, conv_scan_plan_t **
     pl->dma = split_segments(pl->units, pl->K, cus, 2);
     pl->bwd = split_segments(pl->units, pl->K, cus, 1);
     const int64_t chunks = d.N * pl->K * d.G, hpg = d.H / d.G;
-    const int64_t want = std::max<int64_t>(1, std::min(hpg, (2 * cus + chunks - 1) / std::max<int64_t>(1, chunks)));
+    // one gradient workgroup fits a compute unit
+    const int64_t want = std::max<int64_t>(1, std::min(hpg, cus / std::max<int64_t>(1, chunks)));
     pl->heads_per_slice = (int)((hpg + want - 1) / want);
     pl->slices = (int)((hpg + pl->heads_per_slice - 1) / pl->heads_per_slice);
     const int64_t t = (int64_t)pl->SP * kPB * 4;
