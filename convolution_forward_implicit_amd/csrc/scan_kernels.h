@@ -397,17 +397,17 @@ SEQ_DEV double wave_last(double v)
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 SEQ_DEV float wave_sum(float v) { return wave_last(wave_prefix(v)); }
-// the sum over the 16 lanes of a row, in every one of them
-SEQ_DEV float row_sum(float v)
+// The sums of v[0..3] over the 16 lanes of a row, v[r]'s in the lanes 4r..4r+3:
+// two exchanges that halve the values, then two within the four lanes.
+SEQ_DEV float row_sum4(f32x4 v, int lane)
 {
-#define SEQ_ROR(n) \
-    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + n, 0xf, 0xf, true))
-    SEQ_ROR(8);
-    SEQ_ROR(4);
-    SEQ_ROR(2);
-    SEQ_ROR(1);
-#undef SEQ_ROR
-    return v;
+    const bool b3 = lane & 8, b2 = lane & 4;
+    const float a = (b3 ? v[2] : v[0]) + dpp<0x128, 0xf>(b3 ? v[0] : v[2]);     // 8 lanes on
+    const float b = (b3 ? v[3] : v[1]) + dpp<0x128, 0xf>(b3 ? v[1] : v[3]);
+    float s = (b2 ? b : a) + dpp<0x141, 0xf>(b2 ? a : b);                       // mirrored in 8 lanes
+    s += dpp<0xb1, 0xf>(s);
+    s += dpp<0x4e, 0xf>(s);
+    return s;
 }
 
 // Token `lane` of a chunk: the step size dt (0 behind the sequence) and the
@@ -890,7 +890,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
 {
     typedef BwdShared<T, SP> Sh;
     constexpr int Q = Sh::Q, NI = Sh::NI, NS = Sh::NS, XLD = Sh::XLD, BLD = Sh::BLD, MLD = Sh::MLD;
-    constexpr int NT = SP / 16, TRI = NI * (NI + 1) / 2, TPW = (TRI + 7) / 8;
+    constexpr int NT = SP / 16, TRI = NI * (NI + 1) / 2, TW = 6, TPW = (TRI + TW - 1) / TW;    // waves 6 and 7 have other work
     constexpr int WN = NT, WI = 8 / WN, ITW = NI / WI > 0 ? NI / WI : 1, JW = NI / 2;
     typedef Tile<T, Q, kPB, 512> XT;
     typedef Tile<T, Q, SP, 512> BT;
@@ -936,11 +936,15 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
             for (int r = 0; r < 4; ++r) h0[i * 4 + r] = a[r], u[i * 4 + r] = b[r];
         }
     };
-    auto decays = [&](int k) __attribute__((always_inline)) {       // by one wave
+    float raw = 0.0f;       // wave 6: of the head that comes next
+    auto fetch_dt = [&](int k) __attribute__((always_inline)) {
+        const int h = head_of(k);
+        raw = lane < rows ? (float)((const T *)p.dt)[(base + lane) * p.dt_ld + h] + (p.dt_bias ? p.dt_bias[h] : 0.0f) : 0.0f;
+    };
+    auto decays = [&](int k) __attribute__((always_inline)) {
         const int h = head_of(k), to = (k / p.NPB) & 1;
-        float raw = 0.0f, dt;
+        float dt;
         double cum;
-        if (lane < rows) raw = (float)((const T *)p.dt)[(base + lane) * p.dt_ld + h] + (p.dt_bias ? p.dt_bias[h] : 0.0f);
         chunk_decay(raw, lane < rows, p.a[h], p.softplus, dt, cum);
         const double tot = wave_last(cum);
         if (lane < Q) {
@@ -1002,14 +1006,17 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
         // what is never written: M above its diagonal tiles, the same of the sums
         for (int e = threadIdx.x; e < NS * Q * MLD; e += 512) sh.m[e] = (T)0.0f;
         for (int e = threadIdx.x; e < 2 * NI * Q; e += 512) sh.row[0][0][e] = sh.col[0][0][e] = 0.0f;
-        if (w == 6) decays(0);
+        if (w == 6) {
+            fetch_dt(0);
+            decays(0);
+        }
     }
     __syncthreads();
     // scores: rows i, column j in a lane
 #pragma unroll
     for (int k = 0; k < TPW; ++k) {
-        const int t = w + 8 * k;
-        if (t < TRI) {
+        const int t = w + TW * k;
+        if (w < TW && t < TRI) {
             int it, jt;
             tri_tile(t, it, jt);
 #pragma unroll
@@ -1028,19 +1035,9 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
         const int at = k & 1, d = (k / p.NPB) & 1, h = head_of(k), pb = k % p.NPB, pcols = min(kPB, p.P - pb * kPB);
         const float skip = p.d ? p.d[h] : 0.0f;
         const float *s_cum = sh.cum[d], *s_low = sh.low[d], *s_dt = sh.dt[d], *s_w = sh.w[d], *s_e = sh.e[d];
-        Split<T, NS> hs[2];
-        float part = 0.0f;
-        make_split(reinterpret_cast<const float (&)[8]>(h0[0]), hs[0]);
-        make_split(reinterpret_cast<const float (&)[8]>(h0[8]), hs[1]);
-        if (it0 == 0) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) part = fmaf(h0[e], u[e], part);
-        }
-        part = wave_sum(part);
         __syncthreads();        // all waves are done with the block before
         xt.store(sh.x);
         yt.store(sh.y);
-        if (lane == 0) sh.dot[at][w] = part;
         if (it0 == 0) {
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
@@ -1052,13 +1049,16 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
             }
         }
         __syncthreads();
-        if (k + 1 < blocks) fetch(k + 1);
+        if (k + 1 < blocks) {
+            fetch(k + 1);
+            if (w == 6 && (k + 1) % p.NPB == 0) fetch_dt(k + 1);
+        }
         // dP, M and dS, tile by tile; M goes to LDS transposed (rows j)
         float diag = 0.0f;
 #pragma unroll
         for (int t8 = 0; t8 < TPW; ++t8) {
-            const int t = w + 8 * t8;
-            if (t < TRI) {
+            const int t = w + TW * t8;
+            if (w < TW && t < TRI) {
                 int it, jt;
                 tri_tile(t, it, jt);
                 const int i = it * 16 + q * 4, j = jt * 16 + l16;
@@ -1091,15 +1091,24 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
                 col += __shfl_xor(col, 16);
                 col += __shfl_xor(col, 32);
                 if (q == 0) sh.col[at][it][j] = col;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float s = row_sum(wr[r]);
-                    if (l16 == 0) sh.row[at][jt][i + r] = s;
-                }
+                const float row = row_sum4(wr, lane);
+                if ((l16 & 3) == 0) sh.row[at][jt][i + (l16 >> 2)] = row;
             }
         }
+        Split<T, NS> hs[2];
+        float part = 0.0f;
+        if (it0 == 0) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) part = fmaf(h0[e], u[e], part);
+        }
+        make_split(reinterpret_cast<const float (&)[8]>(h0[0]), hs[0]);
+        make_split(reinterpret_cast<const float (&)[8]>(h0[8]), hs[1]);
+        part = wave_sum(part);
         diag = wave_sum(diag);
-        if (lane == 0) sh.dd[at][w] = diag;
+        if (lane == 0) {
+            sh.dot[at][w] = part;
+            sh.dd[at][w] = diag;
+        }
         // dC and dB through the states at the borders
         if (on) {
             frag yf[2][2], xf[2][2], uf[2][NS];
@@ -1120,7 +1129,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
                 const int row = (it0 + i) * 16 + q * 4;
                 const f32x4 ei = *reinterpret_cast<const f32x4 *>(s_e + row);
                 const f32x4 wi = *reinterpret_cast<const f32x4 *>(s_w + row) * *reinterpret_cast<const f32x4 *>(s_dt + row);
-                float cv[4];
+                f32x4 cv;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) cv[r] = (float)sh.c[(row + r) * BLD + nt * 16 + l16];
                 if (i + 1 < ITW) read(i + 1);
@@ -1136,11 +1145,8 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
                 ac *= ei;
                 dC[i] += ac;
                 dB[i] += ab * wi;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float s = row_sum(ac[r] * cv[r]);
-                    if (l16 == 0) sh.cd[at][nt][row + r] = s;
-                }
+                const float s = row_sum4(ac * cv, lane);
+                if ((l16 & 3) == 0) sh.cd[at][nt][row + (l16 >> 2)] = s;
             }
         }
         if (w == 7 && k > 0) finish(k - 1);
@@ -1204,14 +1210,16 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
 #pragma unroll
             for (int j = 0; j < JW; ++j) {
                 const f32x4 dj = *reinterpret_cast<const f32x4 *>(s_dt + (jt0 + j) * 16 + q * 4);
+                f32x4 xd;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int row = (jt0 + j) * 16 + q * 4 + r;
-                    const float s = row_sum(xv[j][r] * dx[j][r]);
-                    if (l16 == 0) sh.xd[at][pt][row] = s;
+                    xd[r] = xv[j][r] * dx[j][r];
                     // in place of x: nothing reads other waves' columns of it any more
                     sh.x[row * XLD + pt * 16 + l16] = (T)fmaf(skip, yv[j][r], dj[r] * dx[j][r]);
                 }
+                const float s = row_sum4(xd, lane);
+                if ((l16 & 3) == 0) sh.xd[at][pt][(jt0 + j) * 16 + q * 4 + (l16 >> 2)] = s;
             }
         }
         if (w == 6 && k + 1 < blocks && (k + 1) % p.NPB == 0) decays(k + 1);
@@ -1223,8 +1231,8 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
     // (M's last readers are behind the barrier above)
 #pragma unroll
     for (int k = 0; k < TPW; ++k) {
-        const int t = w + 8 * k;
-        if (t < TRI) {
+        const int t = w + TW * k;
+        if (w < TW && t < TRI) {
             int it, jt;
             tri_tile(t, it, jt);
             write_split4<NS>(sh.m + (jt * 16 + l16) * MLD + it * 16 + q * 4, Q * MLD, ds[k]);
