@@ -166,23 +166,7 @@ SEQ_DEV void scan_states_dma(const ScanParams &p, int64_t block, StateDmaShared<
         issue(0);
         if (steps > 1) issue(1);
     }
-    if (STORE) {
-        if (p.nseg > p.sub) {
-            const float *s = seg_state + (unit * p.nseg + seg) * (SP * kPB);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) acc[t] = *reinterpret_cast<const f32x4 *>(s + (t * 16 + l16) * kPB + ch);
-        } else {
-            const float *s = REV ? p.dstate_out : p.state;
-            if (s) {
-                s += (nh * p.P + pb * kPB) * p.S;
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (ch + r < pcols && t * 16 + l16 < p.S) acc[t][r] = s[(int64_t)(ch + r) * p.S + t * 16 + l16];
-            }
-        }
-    }
+    if (STORE) start_states<SP, REV>(p, unit, seg, ch, pcols, lane, acc);
     float log_dec = 0.0f;
     if (steps > 0) {
         decays(w);
@@ -242,10 +226,7 @@ SEQ_DEV void scan_states_dma(const ScanParams &p, int64_t block, StateDmaShared<
         __syncthreads();
     }
     if (!STORE) {
-        float *s = seg_state + (unit * p.nseg + seg) * (SP * kPB);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(s + (t * 16 + l16) * kPB + ch) = acc[t];
-        if (threadIdx.x == 0) seg_log[unit * p.nseg + seg] = log_dec;
+        leave_segment<SP>(p, seg_state, seg_log, unit, seg, ch, lane, log_dec, acc);
     } else if (REV && seg == 0 && p.dstate) {
         float *s = p.dstate + (nh * p.P + pb * kPB) * p.S;
 #pragma unroll
@@ -423,13 +404,7 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
         f32x4 st[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) st[t] = f32x4{0, 0, 0, 0};
-        if (nseg > 1) {
-            const float *s = p.seg_state[0] + (unit * p.nseg + seg * p.sub) * (SP * kPB) + ch;
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) st[t][r] = s[spread_state(t, q, r) * kPB];
-        } else if (p.state && ch < pcols) {
+        if (p.state && ch < pcols) {
             const float *s = p.state + (nh * p.P + pb * kPB + ch) * p.S;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -437,6 +412,9 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
                 for (int r = 0; r < 4; ++r)
                     if (spread_state(t, q, r) < p.S) st[t][r] = s[spread_state(t, q, r)];
         }
+        join_segments<SP, false>(p, unit, seg * p.sub, st, [&](const float *v, int t) __attribute__((always_inline)) {
+            return *reinterpret_cast<const f32x4 *>(v + ch * SP + spread_state(t, q, 0));
+        });
         if (steps > 0) __syncthreads();
         for (int k = 0; k < steps; ++k) {
             const bf16_t *sC = (const bf16_t *)(sh.ring + stage), *sB = sC + BR::BYTES / 2, *sX = sB + BR::BYTES / 2;

@@ -60,7 +60,7 @@ struct ScanParams {
     int nseg, seg, sub;         // segments of a sequence, chunks of a segment, segments of a forward workgroup
     int softplus, vec;
     int64_t ahead;              // workgroups of the state kernels that run ahead; the others run back
-    float *seg_state[2], *seg_log[2];   // ahead and back: [unit][nseg][SP][64], [unit][nseg]
+    float *seg_state[2], *seg_log[2];   // ahead and back: [unit][nseg][SP][64] (forward: [64][SP]), [unit][nseg]
     float *bound[2];            // [unit][K][SP][64]: the state and its gradient at every chunk's border
     // gradient
     const void *dy;
@@ -435,6 +435,76 @@ template <typename T, int SP> struct StateShared {
     float tot[4];
 };
 
+// The state that a segment starts from: what came before the sequence, then the
+// states that the segments before left from zero, each decayed by those between.
+// get(s, t) is the lane's four values of result t in a segment's state s; the
+// loads of several segments are under way together.
+template <int SP, bool REV, typename F>
+SEQ_DEV void join_segments(const ScanParams &p, int64_t unit, int seg, f32x4 (&acc)[SP / 16], F &&get)
+{
+    constexpr int NT = SP / 16, AT = SP == 128 ? 3 : 4;
+    const float *s = p.seg_state[REV] + unit * p.nseg * (SP * kPB), *lg = p.seg_log[REV] + unit * p.nseg;
+    const int count = REV ? p.nseg - 1 - seg : seg;
+    for (int k0 = 0; k0 < count; k0 += AT) {
+        f32x4 v[AT][NT];
+        float dec[AT];
+#pragma unroll
+        for (int i = 0; i < AT; ++i) {
+            const int k = min(k0 + i, count - 1), from = REV ? p.nseg - 1 - k : k;
+            dec[i] = lg[from];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) v[i][t] = get(s + (int64_t)from * (SP * kPB), t);
+        }
+        in_order();
+#pragma unroll
+        for (int i = 0; i < AT; ++i) {
+            if (k0 + i >= count) break;
+            const float d = exp2_fast(dec[i]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[t] = acc[t] * d + v[i][t];
+        }
+    }
+}
+
+// ... as rows (channels ch .., four) x columns (states 16 t + lane % 16)
+template <int SP, bool REV>
+SEQ_DEV void start_states(const ScanParams &p, int64_t unit, int seg, int ch, int pcols, int lane, f32x4 (&acc)[SP / 16])
+{
+    constexpr int NT = SP / 16;
+    const float *s = REV ? p.dstate_out : p.state;
+    if (s) {
+        s += (unit / p.NPB * p.P + unit % p.NPB * kPB) * p.S;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (ch + r < pcols && t * 16 + (lane & 15) < p.S) acc[t][r] = s[(int64_t)(ch + r) * p.S + t * 16 + (lane & 15)];
+    }
+    join_segments<SP, REV>(p, unit, seg, acc, [&](const float *v, int t) __attribute__((always_inline)) {
+        return *reinterpret_cast<const f32x4 *>(v + (t * 16 + (lane & 15)) * kPB + ch);
+    });
+}
+
+// What a segment leaves from zero, in the order in which the next kernel takes
+// four neighbours at once: channels for the gradient, states for the forward.
+template <int SP>
+SEQ_DEV void leave_segment(const ScanParams &p, float *seg_state, float *seg_log, int64_t unit, int seg, int ch, int lane,
+                           float log_dec, const f32x4 (&acc)[SP / 16])
+{
+    float *s = seg_state + (unit * p.nseg + seg) * (SP * kPB);
+#pragma unroll
+    for (int t = 0; t < SP / 16; ++t) {
+        const int state = t * 16 + (lane & 15);
+        if (p.y) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[(ch + r) * SP + state] = acc[t][r];
+        } else {
+            *reinterpret_cast<f32x4 *>(s + state * kPB + ch) = acc[t];
+        }
+    }
+    if (threadIdx.x == 0) seg_log[unit * p.nseg + seg] = log_dec;
+}
+
 template <typename T, int SP, bool REV, bool STORE>
 SEQ_DEV void scan_states(const ScanParams &p, int64_t block, StateShared<T, SP> &sh)
 {
@@ -467,24 +537,7 @@ SEQ_DEV void scan_states(const ScanParams &p, int64_t block, StateShared<T, SP> 
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t] = f32x4{0, 0, 0, 0};
     const int ch = w * 16 + q * 4;      // the first of this lane's four channels
-    if (STORE) {
-        if (p.nseg > 1) {
-            const float *s = seg_state + (unit * p.nseg + seg) * (SP * kPB);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) acc[t] = *reinterpret_cast<const f32x4 *>(s + (t * 16 + (lane & 15)) * kPB + ch);
-        } else {
-            const float *s = REV ? p.dstate_out : p.state;
-            if (s) {
-                s += (nh * p.P + pb * kPB) * p.S;
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (ch + r < pcols && t * 16 + (lane & 15) < p.S)
-                            acc[t][r] = s[(int64_t)(ch + r) * p.S + t * 16 + (lane & 15)];
-            }
-        }
-    }
+    if (STORE) start_states<SP, REV>(p, unit, seg, ch, pcols, lane, acc);
 
     XT xt;
     BT bt;
@@ -567,10 +620,7 @@ SEQ_DEV void scan_states(const ScanParams &p, int64_t block, StateShared<T, SP> 
         }
     }
     if (!STORE) {
-        float *s = seg_state + (unit * p.nseg + seg) * (SP * kPB);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(s + (t * 16 + (lane & 15)) * kPB + ch) = acc[t];
-        if (threadIdx.x == 0) seg_log[unit * p.nseg + seg] = log_dec;
+        leave_segment<SP>(p, seg_state, seg_log, unit, seg, ch, lane, log_dec, acc);
     } else if (REV && seg == 0 && p.dstate) {
         float *s = p.dstate + (nh * p.P + pb * kPB) * p.S;
 #pragma unroll
@@ -587,39 +637,6 @@ template <typename T, int SP, bool STORE> __global__ void __launch_bounds__(256)
     __shared__ StateShared<T, SP> sh;
     if (blockIdx.x < p.ahead) scan_states<T, SP, false, STORE>(p, blockIdx.x, sh);
     else scan_states<T, SP, true, STORE>(p, blockIdx.x - p.ahead, sh);
-}
-
-// Joins the segments: what each left from zero becomes the state it starts
-// from, one thread per element of the state, segments in order and eight of
-// them fetched at a time.
-template <int SP> __global__ void __launch_bounds__(256) scan_join_kernel(ScanParams p)
-{
-    constexpr int BLK = SP * kPB / 256, AT = 8;
-    const bool rev = blockIdx.x >= p.ahead;
-    const int64_t block = rev ? blockIdx.x - p.ahead : blockIdx.x, unit = block / BLK;
-    const int e = (int)(block - unit * BLK) * 256 + threadIdx.x;
-    const int pb = (int)(unit % p.NPB), s = e / kPB, ch = pb * kPB + (e & (kPB - 1));
-    const int64_t nh = unit / p.NPB;
-    const float *first = rev ? p.dstate_out : p.state;
-    float cur = first && s < p.S && ch < p.P ? first[(nh * p.P + ch) * p.S + s] : 0.0f;
-    float *v = p.seg_state[rev] + unit * p.nseg * (SP * kPB) + e;
-    const float *lg = p.seg_log[rev] + unit * p.nseg;
-    for (int k0 = 0; k0 < p.nseg; k0 += AT) {
-        float add[AT], dec[AT];
-#pragma unroll
-        for (int i = 0; i < AT; ++i) {
-            const int k = k0 + i, seg = rev ? p.nseg - 1 - k : k;
-            const bool on = k < p.nseg - p.sub;     // nothing follows the last ones
-            add[i] = on ? v[(int64_t)seg * (SP * kPB)] : 0.0f;
-            dec[i] = on ? exp2_fast(lg[seg]) : 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < AT; ++i) {
-            const int k = k0 + i, seg = rev ? p.nseg - 1 - k : k;
-            if (k < p.nseg) v[(int64_t)seg * (SP * kPB)] = cur;
-            cur = fmaf(dec[i], cur, add[i]);
-        }
-    }
 }
 
 // Lower-triangle tile t of the chunk's scores: row it, column jt <= it
@@ -670,13 +687,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
     f32x4 st[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) st[t] = f32x4{0, 0, 0, 0};
-    if (p.nseg > 1) {
-        const float *s = p.seg_state[0] + (unit * p.nseg + seg) * (SP * kPB) + col;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) st[t][r] = s[(t * 16 + q * 4 + r) * kPB];
-    } else if (p.state && col < pcols) {
+    if (p.state && col < pcols) {
         const float *s = p.state + (nh * p.P + pb * kPB + col) * p.S;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -684,6 +695,9 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
             for (int r = 0; r < 4; ++r)
                 if (t * 16 + q * 4 + r < p.S) st[t][r] = s[t * 16 + q * 4 + r];
     }
+    join_segments<SP, false>(p, unit, seg, st, [&](const float *v, int t) __attribute__((always_inline)) {
+        return *reinterpret_cast<const f32x4 *>(v + col * SP + t * 16 + q * 4);
+    });
     // the tiles of M above the diagonal that a reduction over 32 tokens meets
     for (int e = threadIdx.x; e < NM * Q * MLD; e += 256) sM[e] = (T)0.0f;
 

@@ -196,14 +196,12 @@ template <typename T, int SP, bool STORE> void launch_states(const ScanParams &p
     hipLaunchKernelGGL((scan_state_kernel<T, SP, STORE>), dim3((unsigned)grid), dim3(256), 0, s, p);
 }
 
-// The states that the segments start from, in both directions for a gradient.
+// The states that the segments leave from zero, in both directions for a gradient.
 template <typename T, int SP> void launch_segments(ScanParams p, int64_t units, int ways, hipStream_t s)
 {
     if (p.nseg <= p.sub) return;
     p.ahead = units * (p.nseg - p.sub);
     launch_states<T, SP, false>(p, ways * p.ahead, s);
-    p.ahead = units * (SP * kPB / 256);
-    hipLaunchKernelGGL((scan_join_kernel<SP>), dim3((unsigned)(ways * p.ahead)), dim3(256), 0, s, p);
 }
 
 template <typename T, int SP> void launch_fwd(const ScanParams &p, int64_t units, hipStream_t s)
@@ -241,10 +239,12 @@ template <typename T> void launch_scan(int SP, const ScanParams &p, int64_t unit
 }
 
 // Segments of K chunks so that `units` heads give about `want` workgroups, each
-// cut into `fine` times as many for the pass over the states.
+// cut into `fine` times as many for the pass over the states.  A segment's start
+// is joined from all before it by the workgroup itself: 32 are the most that
+// costs less than another launch between the two would.
 Segments split_segments(int64_t units, int64_t K, int64_t want, int64_t fine)
 {
-    const int64_t n = std::max<int64_t>(1, std::min(K, want / std::max<int64_t>(1, units)));
+    const int64_t n = std::max<int64_t>(1, std::min({K, want / std::max<int64_t>(1, units), 32 / fine}));
     const int64_t whole = (K + n - 1) / n, sub = n == 1 ? 1 : std::max<int64_t>(1, std::min(fine, whole / 2));
     const int64_t chunks = (whole + sub - 1) / sub, count = (K + chunks * sub - 1) / (chunks * sub) * sub;
     return {(int)count, (int)chunks, (int)sub};
