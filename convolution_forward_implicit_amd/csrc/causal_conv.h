@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(256) causal_conv_kernel(CausalParams p)
             o[i] = t0 + u < len ? (SILU ? v * sigmoid(v) : v) : 0.0f;
         }
         T *row = (T *)p.y + (n * p.L + t0 + u) * p.y_ld;
-        store_f32<T, V>(row + c, o);
+        stream_f32<T, V>(row + c, o);
     }
 }
 
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(256) causal_bwd_kernel(CausalParams p)
 #pragma unroll
                     for (int i = 0; i < V; ++i) g[i] = s < len ? g[i] : 0.0f;
                     T *row = (T *)p.dx + (n * p.L + s) * p.dx_ld;
-                    store_f32<T, V>(row + c, g);
+                    stream_f32<T, V>(row + c, g);
                 }
             }
 #pragma unroll

@@ -36,6 +36,18 @@ namespace convfwd {
 
 constexpr int kStages = 3;
 
+// MFMAS products of this region with VALUS other vector instructions between
+// each two: a product takes the matrix unit 16 clocks, in which the vector unit
+// is free for the splits of the next operand.
+template <int MFMAS, int VALUS> SEQ_DEV void interleave()
+{
+#pragma unroll
+    for (int i = 0; i < MFMAS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, VALUS, 0);
+    }
+}
+
 // Tiles of 64 tokens x COLS bf16 in that layout
 template <int COLS> struct Ring {
     static constexpr int CH = COLS / 8;                  // 16-byte pieces of a row
@@ -252,7 +264,8 @@ template <int SP> struct FwdDmaShared {
     __align__(16) float cum[3][64], dt[3][64], w[3][64];        // of three chunks: c_i, dt_i, e^{c_Q - c_i} dt_i
 };
 
-// a score wave's chunk: y'' of the tokens 16 IT ..
+// A score wave's chunk: y'' of the tokens 16 IT .., in results of spread channels:
+// y[2h] and y[2h + 1] hold token lane % 16's channels 32h + 8q .. +3 and +4 .. +7.
 template <int SP, int IT>
 SEQ_DEV void score_rows(const bf16_t *sC, const bf16_t *sB, const bf16_t *sX, const float *cum, const float *dt, float skip,
                         int lane, f32x4 (&y)[4])
@@ -261,42 +274,51 @@ SEQ_DEV void score_rows(const bf16_t *sC, const bf16_t *sB, const bf16_t *sX, co
     typedef Ring<kPB> XR;
     constexpr int KN = SP / 32, KQ = IT / 2 + 1;
     const int q = lane >> 4, l16 = lane & 15, i = IT * 16 + l16;
-    bf16x8 cf[KN], xf[KQ][4];
+    bf16x8 cf[KN], bf[2][KN], xf[KQ][4];
     f32x4 s[2 * KQ];
+    auto read_b = [&](int jt) __attribute__((always_inline)) {
+#pragma unroll
+        for (int ks = 0; ks < KN; ++ks) bf[jt & 1][ks] = BR::rows(sB, jt * 16, ks * 32, lane);
+    };
 #pragma unroll
     for (int ks = 0; ks < KN; ++ks) cf[ks] = BR::rows(sC, IT * 16, ks * 32, lane);
+    read_b(0);
+    const float ci = cum[i];
+    f32x4 ex[IT + 1], dj[IT + 1];
+#pragma unroll
+    for (int jt = 0; jt <= IT; ++jt) {
+        ex[jt] = ci - *reinterpret_cast<const f32x4 *>(cum + jt * 16 + q * 4);
+        dj[jt] = *reinterpret_cast<const f32x4 *>(dt + jt * 16 + q * 4);
+    }
 #pragma unroll
     for (int jt = 0; jt < 2 * KQ; ++jt) s[jt] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int jt = 0; jt <= IT; ++jt) {
-        bf16x8 bf[KN];
+        if (jt < IT) {
+            read_b(jt + 1);
+        } else {
 #pragma unroll
-        for (int ks = 0; ks < KN; ++ks) bf[ks] = BR::rows(sB, jt * 16, ks * 32, lane);
-        // while these are on their way: the decays of the tile before
-        f32x4 ex = {0, 0, 0, 0}, dj = {0, 0, 0, 0};
-        if (jt > 0) {
-            ex = cum[i] - *reinterpret_cast<const f32x4 *>(cum + (jt - 1) * 16 + q * 4);
-            dj = *reinterpret_cast<const f32x4 *>(dt + (jt - 1) * 16 + q * 4);
+            for (int ks = 0; ks < KQ; ++ks)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    xf[ks][2 * h] = XR::template cols<true, 0>(sX, ks * 32, h * 32, lane);
+                    xf[ks][2 * h + 1] = XR::template cols<true, 1>(sX, ks * 32, h * 32, lane);
+                }
         }
         in_order();
+        // the decays of the tile before go with the products of this one
         if (jt > 0) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) s[jt - 1][r] *= exp2_fast(ex[r]) * dj[r];
+            for (int r = 0; r < 4; ++r) s[jt - 1][r] *= exp2_fast(ex[jt - 1][r]) * dj[jt - 1][r];
         }
 #pragma unroll
-        for (int ks = 0; ks < KN; ++ks) s[jt] = mma(bf[ks], cf[ks], s[jt]);
+        for (int ks = 0; ks < KN; ++ks) s[jt] = mma(bf[jt & 1][ks], cf[ks], s[jt]);
+        in_order();
     }
-#pragma unroll
-    for (int ks = 0; ks < KQ; ++ks)
-#pragma unroll
-        for (int pt = 0; pt < 4; ++pt) xf[ks][pt] = XR::cols(sX, ks * 32, pt * 16, lane);
-    const f32x4 ex = cum[i] - *reinterpret_cast<const f32x4 *>(cum + IT * 16 + q * 4);
-    const f32x4 dj = *reinterpret_cast<const f32x4 *>(dt + IT * 16 + q * 4);
-    in_order();
     // the tile on the diagonal, with D there
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        s[IT][r] = l16 >= q * 4 + r ? s[IT][r] * exp2_fast(ex[r]) * dj[r] : 0.0f;
+        s[IT][r] = l16 >= q * 4 + r ? s[IT][r] * exp2_fast(ex[IT][r]) * dj[IT][r] : 0.0f;
         if (l16 == q * 4 + r) s[IT][r] += skip;
     }
 #pragma unroll
@@ -422,8 +444,8 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
             stage = next_stage(stage, STAGE);
             slot = slot == 2 ? 0 : slot + 1;
             if (busy) {
-                bf16x8 cf[2][4], xf[2], bf[NT];
-                f32x4 y[4], w0[2], w1[2];
+                bf16x8 cf[2][4], xf, bf[NT];
+                f32x4 y[4], w0, w1;
                 float ei[4];
                 Split<bf16_t, 2> hs[2];
                 Split<bf16_t, 3> xs[2];
@@ -438,6 +460,11 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
                         bf[t + 1] = BR::template cols<true, 1>(sB, ks * 32, t * 16, lane);
                     }
                 };
+                auto read_x = [&](int ks) __attribute__((always_inline)) {
+                    xf = XR::cols(sX, ks * 32, w * 16, lane);
+                    w0 = *reinterpret_cast<const f32x4 *>(wt + ks * 32 + q * 4);
+                    w1 = *reinterpret_cast<const f32x4 *>(wt + ks * 32 + 16 + q * 4);
+                };
                 auto split_h = [&](int ks) __attribute__((always_inline)) {
                     float v[8];
 #pragma unroll
@@ -447,7 +474,7 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
                 auto split_x = [&](int ks) __attribute__((always_inline)) {
                     float v[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = (float)xf[ks][e] * (e < 4 ? w0[ks][e & 3] : w1[ks][e & 3]);
+                    for (int e = 0; e < 8; ++e) v[e] = (float)xf[e] * (e < 4 ? w0[e & 3] : w1[e & 3]);
                     make_split(v, xs[ks]);
                 };
 #pragma unroll
@@ -460,33 +487,35 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
                     if (ks + 1 < KN) {
                         read_c(ks + 1);
                     } else {
-#pragma unroll
-                        for (int k2 = 0; k2 < 2; ++k2) {
-                            xf[k2] = XR::cols(sX, k2 * 32, w * 16, lane);
-                            w0[k2] = *reinterpret_cast<const f32x4 *>(wt + k2 * 32 + q * 4);
-                            w1[k2] = *reinterpret_cast<const f32x4 *>(wt + k2 * 32 + 16 + q * 4);
-                        }
-#pragma unroll
-                        for (int it = 0; it < 4; ++it) ei[it] = cum[it * 16 + l16];
+                        read_x(0);
+                        read_b(0);
                     }
-                    if (ks == KN - 1) read_b(0);
                     in_order();
-                    if (ks + 1 < KN) split_h(ks + 1);
+                    if (ks + 1 < KN) {
+                        split_h(ks + 1);
+                    } else {
+                        const float dec = exp2_fast(cum[Q - 1]);
+                        split_x(0);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) st[t] *= dec;
+                    }
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
                         for (int it = 0; it < 4; ++it) y[it] = mma(hs[ks & 1].f[m], cf[ks & 1][it], y[it]);
+                    interleave<8, 3>();
                     in_order();
                 }
-                const float dec = exp2_fast(cum[Q - 1]);
-                split_x(0);
+                read_x(1);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) st[t] *= dec;
+                for (int it = 0; it < 4; ++it) ei[it] = cum[it * 16 + l16];
+                in_order();
+                split_x(1);
 #pragma unroll
                 for (int m = 0; m < 3; ++m)
 #pragma unroll
                     for (int t = 0; t < NT; ++t) st[t] = mma(bf[t], xs[0].f[m], st[t]);
-                split_x(1);
+                interleave<3 * NT, 3>();
                 in_order();
                 read_b(1);
                 in_order();
@@ -499,6 +528,7 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
                 for (int m = 0; m < 3; ++m)
 #pragma unroll
                     for (int t = 0; t < NT; ++t) st[t] = mma(bf[t], xs[1].f[m], st[t]);
+                interleave<3 * NT, 3>();
             }
             __syncthreads();
         }
@@ -520,16 +550,19 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
             const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(
                 yg + t0 * p.y_ld, 0, (int)(((rows - 1) * p.y_ld + pcols) * 2), 0x00020000);
 #pragma unroll
-            for (int pt = 0; pt < 4; ++pt) {
-                if (pt * 16 >= pcols) continue;
-                const f32x4 v = y[pt] + *reinterpret_cast<const f32x4 *>(&sh.y[k & 1][i * kPB + (((pt * 4 + q) ^ l16) << 2)]);
-                bf16x4 o;
+            for (int h = 0; h < 2; ++h) {
+                const int col = h * 32 + q * 8;
+                if (h * 32 >= pcols) continue;
+                bf16x8 o;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) o[r] = (bf16_t)v[r];
-                const int col = pt * 16 + q * 4;
-                const uint32_t at = col < pcols ? (uint32_t)(i * (int)p.y_ld + col) * 2 : kOutOfRange;
-                typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), buf, at, 0, 0);
+                for (int m = 0; m < 2; ++m) {
+                    const int piece = h * 8 + q * 2 + m;
+                    const f32x4 v = y[2 * h + m] + *reinterpret_cast<const f32x4 *>(&sh.y[k & 1][i * kPB + ((piece ^ l16) << 2)]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[m * 4 + r] = (bf16_t)v[r];
+                }
+                const uint32_t to = col < pcols ? (uint32_t)(i * (int)p.y_ld + col) * 2 : kOutOfRange;
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), buf, to, 0, kStream);
             }
         };
         if (steps > 0) {

@@ -233,6 +233,8 @@ template <int NS, typename T> SEQ_DEV void write_split4(T *t, int term_stride, f
 // branch.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
+constexpr int kStream = 2;      // the non-temporal hint of a buffer access: outputs are not read back
+
 template <typename T, int ROWS, int COLS, int THREADS = 256> struct Tile {
     static constexpr int VE = Frag<T>::VE;
     static constexpr int ALL = ROWS * COLS / VE;        // vectors of the tile
@@ -324,7 +326,7 @@ template <typename T, int ROWS, int COLS, int THREADS = 256> struct Tile {
         uint32_t o = opaque(first(ld, cols));
         if (vec) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k) __builtin_amdgcn_raw_buffer_store_b128(v[k], buf, o + k * step, 0, 0);
+            for (int k = 0; k < NV; ++k) __builtin_amdgcn_raw_buffer_store_b128(v[k], buf, o + k * step, 0, kStream);
         } else {
             const int left = (int)opaque(mine() ? cols - column() : 0);
 #pragma unroll

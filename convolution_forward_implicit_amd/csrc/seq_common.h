@@ -51,6 +51,18 @@ template <typename T, int V> SEQ_DEV void store_f32(T *p, const float (&v)[V])
         *reinterpret_cast<typename Pack<T, V>::type *>(p) = q;
     }
 }
+// ... of an output that no kernel of the call reads back, past the caches
+template <typename T, int V> SEQ_DEV void stream_f32(T *p, const float (&v)[V])
+{
+    if constexpr (V == 1) {
+        __builtin_nontemporal_store((T)v[0], p);
+    } else {
+        typename Pack<T, V>::type q;
+#pragma unroll
+        for (int i = 0; i < V; ++i) q[i] = (T)v[i];
+        __builtin_nontemporal_store(q, reinterpret_cast<typename Pack<T, V>::type *>(p));
+    }
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 
