@@ -438,7 +438,9 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
             return *reinterpret_cast<const f32x4 *>(v + ch * SP + spread_state(t, q, 0));
         });
         if (steps > 0) __syncthreads();
+        const int lane_ = lane;
         for (int k = 0; k < steps; ++k) {
+            const int lane = fresh_vector(lane_), q = lane >> 4, l16 = lane & 15;      // as in scan_bwd_kernel
             const bf16_t *sC = (const bf16_t *)(sh.ring + stage), *sB = sC + BR::BYTES / 2, *sX = sB + BR::BYTES / 2;
             const float *cum = sh.cum[slot], *wt = sh.w[slot];
             stage = next_stage(stage, STAGE);
@@ -541,10 +543,11 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
                     if (spread_state(t, q, r) < p.S) s[spread_state(t, q, r)] = st[t][r];
         }
     } else {
-        const int it = w - 4, i = it * 16 + l16;
+        const int it = w - 4;
         f32x4 y[4];
         // rows behind the sequence come out as zeros: x and C are zeros there
-        auto finish = [&](int k) __attribute__((always_inline)) {
+        auto finish = [&](int k, int lane) __attribute__((always_inline)) {
+            const int q = lane >> 4, l16 = lane & 15, i = it * 16 + l16;
             const int64_t t0 = (int64_t)(c_lo + k) * Q;
             const int rows = (int)min((int64_t)Q, p.L - t0);
             const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(
@@ -573,8 +576,10 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
             }
             __syncthreads();
         }
+        const int lane_ = lane;
         for (int k = 0; k < steps; ++k) {
-            if (k > 0) finish(k - 1);
+            const int lane = fresh_vector(lane_);      // as in scan_bwd_kernel
+            if (k > 0) finish(k - 1, lane);
             const bf16_t *sC = (const bf16_t *)(sh.ring + stage), *sB = sC + BR::BYTES / 2, *sX = sB + BR::BYTES / 2;
             const float *cum = sh.cum[slot], *dt = sh.dt[slot];
             stage = next_stage(stage, STAGE);
@@ -589,7 +594,7 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
             }
             __syncthreads();
         }
-        if (steps > 0) finish(steps - 1);
+        if (steps > 0) finish(steps - 1, lane);
         // chunks behind the sequence: zeros
         for (int c = max(c_lo, c_live); c < c_hi; ++c)
             for (int e = threadIdx.x - 256; e < Q * kPB / 8; e += 256) {
