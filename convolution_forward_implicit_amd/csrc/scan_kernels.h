@@ -444,7 +444,7 @@ template <typename T, int SP> struct StateShared {
 template <int SP, bool REV, typename F>
 SEQ_DEV void join_segments(const ScanParams &p, int64_t unit, int seg, f32x4 (&acc)[SP / 16], F &&get)
 {
-    constexpr int NT = SP / 16, AT = SP == 128 ? 3 : 4;
+    constexpr int NT = SP / 16, AT = 24 / NT;
     const float *s = p.seg_state[REV] + unit * p.nseg * (SP * kPB), *lg = p.seg_log[REV] + unit * p.nseg;
     const int count = REV ? p.nseg - 1 - seg : seg;
     for (int k0 = 0; k0 < count; k0 += AT) {
@@ -460,10 +460,11 @@ SEQ_DEV void join_segments(const ScanParams &p, int64_t unit, int seg, f32x4 (&a
         in_order();
 #pragma unroll
         for (int i = 0; i < AT; ++i) {
-            if (k0 + i >= count) break;
-            const float d = exp2_fast(dec[i]);
+            if (k0 + i < count) {
+                const float d = exp2_fast(dec[i]);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) acc[t] = acc[t] * d + v[i][t];
+                for (int t = 0; t < NT; ++t) acc[t] = acc[t] * d + v[i][t];
+            }
         }
     }
 }

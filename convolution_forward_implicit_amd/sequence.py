@@ -33,7 +33,7 @@ class _Plan:
     @staticmethod
     def _dense(t, shape, dtype, dev, name):
         """Address of a contiguous tensor of this shape and type on `dev`."""
-        if t.dtype is dtype and t.is_cuda and t.get_device() == dev.index and t.shape == shape and t.is_contiguous():
+        if t.dtype is dtype and t.get_device() == dev.index and t.shape == shape and t.is_contiguous():
             return t.data_ptr()
         if t.device != dev or dev.type != "cuda":
             raise ValueError("%s must be on the cuda device of the other tensors (%s), got %s" % (name, dev, t.device))
@@ -48,6 +48,8 @@ class _Plan:
         whose rows are packed and evenly spaced: contiguous, or a range of the
         last dimensions of a contiguous one."""
         if t.is_contiguous():
+            if t.dtype is dtype and t.get_device() == dev.index and t.shape == lead + inner:
+                return t.data_ptr(), 0
             return self._dense(t, lead + inner, dtype, dev, name), 0
         if t.device != dev or dev.type != "cuda":
             raise ValueError("%s must be on the cuda device of the other tensors (%s), got %s" % (name, dev, t.device))
@@ -81,7 +83,7 @@ class _Plan:
         if dev.type != "cuda":
             raise ValueError("tensors must be on a cuda device, got %s" % dev)
         if stream is None:
-            if torch.cuda.current_device() == dev.index:
+            if torch._C._cuda_getDevice() == dev.index:
                 # the handle alone: building the Stream object takes as long as a launch
                 return torch._C._cuda_getCurrentRawStream(dev.index), None
             stream = torch.cuda.current_stream(dev)
@@ -121,7 +123,7 @@ class CausalConv(_Plan):
         t, dev = self._type(torch), x.device
         stream, away = self._on(torch, dev, stream)
         if out is None:
-            out = torch.empty(self.x_shape, dtype=t, device=dev)
+            out = x.new_empty(*self.x_shape)
         lead, inner = self.x_shape[:2], self.x_shape[2:]
         xp, x_ld = self._rows(x, lead, inner, t, dev, "x")
         yp, y_ld = self._rows(out, lead, inner, t, dev, "out")
@@ -145,7 +147,7 @@ class CausalConv(_Plan):
         stream, away = self._on(torch, dev, stream)
         lead, inner = self.x_shape[:1], self.x_shape[2:]
         if out is None:
-            out = torch.empty(lead + inner, dtype=t, device=dev)
+            out = x.new_empty(*lead, *inner)
         xp, x_ld = self._rows(x, lead, inner, t, dev, "x")
         yp, y_ld = self._rows(out, lead, inner, t, dev, "out")
         sp = self._dense(state, self.state_shape, t, dev, "state")
@@ -171,7 +173,7 @@ class CausalConv(_Plan):
         _given(got, out, shapes)
         for k, shape in shapes.items():
             if shape is not None and got[k] is None:
-                got[k] = torch.empty(shape, dtype=t, device=dev)
+                got[k] = x.new_empty(*shape)
         lead, inner = self.x_shape[:2], self.x_shape[2:]
         dyp, dy_ld = self._rows(dy, lead, inner, t, dev, "dy")
         xp, x_ld = self._rows(x, lead, inner, t, dev, "x")
@@ -228,7 +230,7 @@ class SelectiveScan(_Plan):
         t, dev = self._type(torch), x.device
         stream, away = self._on(torch, dev, stream)
         if out is None:
-            out = torch.empty(self.x_shape, dtype=t, device=dev)
+            out = x.new_empty(*self.x_shape)
         lead = self.x_shape[:2]
         xp, x_ld = self._rows(x, lead, self.x_shape[2:], t, dev, "x")
         dp, dt_ld = self._rows(dt, lead, self.dt_shape[2:], t, dev, "dt")
@@ -252,7 +254,7 @@ class SelectiveScan(_Plan):
         stream, away = self._on(torch, dev, stream)
         lead, hp, gs = self.x_shape[:1], self.x_shape[2:], self.b_shape[2:]
         if out is None:
-            out = torch.empty(lead + hp, dtype=t, device=dev)
+            out = x.new_empty(*lead, *hp)
         xp, x_ld = self._rows(x, lead, hp, t, dev, "x")
         dp, dt_ld = self._rows(dt, lead, self.a_shape, t, dev, "dt")
         bp, b_ld = self._rows(B, lead, gs, t, dev, "B")
@@ -286,7 +288,7 @@ class SelectiveScan(_Plan):
         _given(got, out, shapes)
         for k, shape in shapes.items():
             if shape is not None and got[k] is None:
-                got[k] = torch.empty(shape, dtype=t if k in ("dx", "ddt", "dB", "dC") else f32, device=dev)
+                got[k] = (x if k in ("dx", "ddt", "dB", "dC") else A).new_empty(*shape)
         lead, hp, gs, hh = self.x_shape[:2], self.x_shape[2:], self.b_shape[2:], self.dt_shape[2:]
         rows = [self._rows(v, lead, inner, t, dev, name) for v, inner, name in (
             (dy, hp, "dy"), (x, hp, "x"), (dt, hh, "dt"), (B, gs, "B"), (C, gs, "C"),
