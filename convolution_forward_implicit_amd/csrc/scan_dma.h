@@ -11,10 +11,9 @@
 //
 //   waves 0-3 ("state", 16 channels each):  y' = e^{c_i} h_0 C_i, then the state's update
 //   waves 4-7 ("score", 16 tokens each):    M from C . B, y'' = (M + D) x
-//   wave 8:                                 the loads
 //
-// (The counter that says when loads have arrived counts stores too, so waves
-// that store y would wait for their stores before each barrier: 30 of 190 us.)
+// (wave 4, with the least of the scores, also starts the loads, waves 5 and 6 do
+// the decays; eight waves leave each 256 registers to read fragments ahead)
 // The score waves' products need no LDS for M: the scores' result blocks are
 // the operand of M x as they stand.  y' crosses through LDS, the score waves
 // add y'' and store the rows while the next chunk is under way, so there is one
@@ -337,7 +336,7 @@ SEQ_DEV void score_rows(const bf16_t *sC, const bf16_t *sB, const bf16_t *sX, co
     }
 }
 
-template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(ScanParams p)
+template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(ScanParams p)
 {
     constexpr int Q = 64, NT = SP / 16, KN = SP / 32, STAGE = FwdDmaShared<SP>::STAGE;
     typedef Ring<kPB> XR;
@@ -383,46 +382,27 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
         sh.w[to][lane] = exp2_fast((float)(tot - cum)) * dt;
     };
     int stage = 0, slot = 0;        // where a chunk and its decays are
-    if (w == 8) {
-        const uint32_t ring = lds_address(sh.ring);
-        int fill = 0;
-        // a row group of a tile lies LOADS rows on from the one before it, a load's
-        // rows one row on from the load before: one lane offset per tile
-        auto issue = [&](int k) __attribute__((always_inline)) {
-            const int64_t t0 = (int64_t)(c_lo + k) * Q;
-            const int rows = (int)min((int64_t)Q, len - t0);
-            const i32x4_t xb = chunk_buffer(xg + t0 * p.x_ld, p.x_ld, rows, pcols);
-            const i32x4_t bb = chunk_buffer(bg + t0 * p.b_ld, p.b_ld, rows, p.S);
-            const i32x4_t cb = chunk_buffer(cg + t0 * p.c_ld, p.c_ld, rows, p.S);
-            uint32_t to = ring + fill;
+    // wave 4's part of the ring: load g of a tile takes rows one row on from load g - 1
+    const uint32_t ring = lds_address(sh.ring);
+    int fill = 0;
+    auto issue = [&](int k) __attribute__((always_inline)) {
+        const int64_t t0 = (int64_t)(c_lo + k) * Q;
+        const int rows = (int)min((int64_t)Q, len - t0);
+        const i32x4_t xb = chunk_buffer(xg + t0 * p.x_ld, p.x_ld, rows, pcols);
+        const i32x4_t bb = chunk_buffer(bg + t0 * p.b_ld, p.b_ld, rows, p.S);
+        const i32x4_t cb = chunk_buffer(cg + t0 * p.c_ld, p.c_ld, rows, p.S);
+        uint32_t to = ring + fill, from = BR::source(0, lane, (int)p.c_ld, p.S);
 #pragma unroll
-            for (int g = 0; g < BR::LOADS; ++g, to += 2 * BR::GROUP) dma16(cb, BR::source(g, lane, (int)p.c_ld, p.S), 0, to);
+        for (int g = 0; g < BR::LOADS; ++g, to += 2 * BR::GROUP, from += 2 * (uint32_t)p.c_ld) dma16(cb, from, 0, to);
+        from = BR::source(0, lane, (int)p.b_ld, p.S);
 #pragma unroll
-            for (int g = 0; g < BR::LOADS; ++g, to += 2 * BR::GROUP) dma16(bb, BR::source(g, lane, (int)p.b_ld, p.S), 0, to);
+        for (int g = 0; g < BR::LOADS; ++g, to += 2 * BR::GROUP, from += 2 * (uint32_t)p.b_ld) dma16(bb, from, 0, to);
+        from = XR::source(0, lane, (int)p.x_ld, pcols);
 #pragma unroll
-            for (int g = 0; g < XR::LOADS; ++g, to += 2 * XR::GROUP) dma16(xb, XR::source(g, lane, (int)p.x_ld, pcols), 0, to);
-            fill = next_stage(fill, STAGE);
-        };
-        if (steps > 0) {
-            issue(0);
-            if (steps > 1) {
-                issue(1);
-                wait_vmcnt<LOADS>();
-            } else {
-                wait_vmcnt<0>();
-            }
-            __syncthreads();
-        }
-        for (int k = 0; k < steps; ++k) {
-            if (k + 2 < steps) {
-                issue(k + 2);       // over chunk k - 1, which all waves are done with
-                wait_vmcnt<LOADS>();
-            } else {
-                wait_vmcnt<0>();
-            }
-            __syncthreads();
-        }
-    } else if (w < 4) {
+        for (int g = 0; g < XR::LOADS; ++g, to += 2 * XR::GROUP, from += 2 * (uint32_t)p.x_ld) dma16(xb, from, 0, to);
+        fill = next_stage(fill, STAGE);
+    };
+    if (w < 4) {
         f32x4 st[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) st[t] = f32x4{0, 0, 0, 0};
@@ -446,26 +426,17 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
             stage = next_stage(stage, STAGE);
             slot = slot == 2 ? 0 : slot + 1;
             if (busy) {
-                bf16x8 cf[2][4], xf, bf[NT];
-                f32x4 y[4], w0, w1;
+                bf16x8 cf[KN][4], xf[2], bf[NT];
+                f32x4 y[4], w0[2], w1[2];
                 float ei[4];
                 Split<bf16_t, 2> hs[2];
                 Split<bf16_t, 3> xs[2];
-                auto read_c = [&](int ks) __attribute__((always_inline)) {
-#pragma unroll
-                    for (int it = 0; it < 4; ++it) cf[ks & 1][it] = BR::rows(sC, it * 16, ks * 32, lane);
-                };
                 auto read_b = [&](int ks) __attribute__((always_inline)) {
 #pragma unroll
                     for (int t = 0; t < NT; t += 2) {
                         bf[t] = BR::template cols<true, 0>(sB, ks * 32, t * 16, lane);
                         bf[t + 1] = BR::template cols<true, 1>(sB, ks * 32, t * 16, lane);
                     }
-                };
-                auto read_x = [&](int ks) __attribute__((always_inline)) {
-                    xf = XR::cols(sX, ks * 32, w * 16, lane);
-                    w0 = *reinterpret_cast<const f32x4 *>(wt + ks * 32 + q * 4);
-                    w1 = *reinterpret_cast<const f32x4 *>(wt + ks * 32 + 16 + q * 4);
                 };
                 auto split_h = [&](int ks) __attribute__((always_inline)) {
                     float v[8];
@@ -476,42 +447,44 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
                 auto split_x = [&](int ks) __attribute__((always_inline)) {
                     float v[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = (float)xf[e] * (e < 4 ? w0[e & 3] : w1[e & 3]);
+                    for (int e = 0; e < 8; ++e) v[e] = (float)xf[ks][e] * (e < 4 ? w0[ks][e & 3] : w1[ks][e & 3]);
                     make_split(v, xs[ks]);
                 };
 #pragma unroll
+                for (int ks = 0; ks < KN; ++ks)
+#pragma unroll
+                    for (int it = 0; it < 4; ++it) cf[ks][it] = BR::rows(sC, it * 16, ks * 32, lane);
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    xf[ks] = XR::cols(sX, ks * 32, w * 16, lane);
+                    w0[ks] = *reinterpret_cast<const f32x4 *>(wt + ks * 32 + q * 4);
+                    w1[ks] = *reinterpret_cast<const f32x4 *>(wt + ks * 32 + 16 + q * 4);
+                }
+#pragma unroll
+                for (int it = 0; it < 4; ++it) ei[it] = cum[it * 16 + l16];
+                const float dec = exp2_fast(cum[Q - 1]);
+                in_order();
+#pragma unroll
                 for (int it = 0; it < 4; ++it) y[it] = f32x4{0, 0, 0, 0};
-                read_c(0);
                 split_h(0);
-                // each step's reads and splits are the next one's operands
+                // the splits of the next operands go between the products
 #pragma unroll
                 for (int ks = 0; ks < KN; ++ks) {
                     if (ks + 1 < KN) {
-                        read_c(ks + 1);
-                    } else {
-                        read_x(0);
-                        read_b(0);
-                    }
-                    in_order();
-                    if (ks + 1 < KN) {
                         split_h(ks + 1);
                     } else {
-                        const float dec = exp2_fast(cum[Q - 1]);
                         split_x(0);
 #pragma unroll
                         for (int t = 0; t < NT; ++t) st[t] *= dec;
                     }
+                    if (ks == (KN > 1 ? KN - 2 : 0)) read_b(0);
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int it = 0; it < 4; ++it) y[it] = mma(hs[ks & 1].f[m], cf[ks & 1][it], y[it]);
+                        for (int it = 0; it < 4; ++it) y[it] = mma(hs[ks & 1].f[m], cf[ks][it], y[it]);
                     interleave<8, 3>();
                     in_order();
                 }
-                read_x(1);
-#pragma unroll
-                for (int it = 0; it < 4; ++it) ei[it] = cum[it * 16 + l16];
-                in_order();
                 split_x(1);
 #pragma unroll
                 for (int m = 0; m < 3; ++m)
@@ -568,11 +541,21 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
                 __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), buf, to, 0, kStream);
             }
         };
+        const bool decaying = it == 1 || it == 2;
         if (steps > 0) {
-            if (it < 2) {
-                fetch_dt(it);
-                decays(it, it);
-                fetch_dt(2 + it);
+            if (decaying) {
+                fetch_dt(it - 1);
+                decays(it - 1, it - 1);
+                fetch_dt(it + 1);
+            }
+            if (it == 0) {
+                issue(0);
+                if (steps > 1) {
+                    issue(1);
+                    wait_vmcnt<LOADS>();
+                } else {
+                    wait_vmcnt<0>();
+                }
             }
             __syncthreads();
         }
@@ -580,6 +563,7 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
         for (int k = 0; k < steps; ++k) {
             const int lane = fresh_vector(lane_);      // as in scan_bwd_kernel
             if (k > 0) finish(k - 1, lane);
+            if (it == 0 && k + 2 < steps) issue(k + 2);       // over chunk k - 1, which all waves are done with
             const bf16_t *sC = (const bf16_t *)(sh.ring + stage), *sB = sC + BR::BYTES / 2, *sX = sB + BR::BYTES / 2;
             const float *cum = sh.cum[slot], *dt = sh.dt[slot];
             stage = next_stage(stage, STAGE);
@@ -588,9 +572,13 @@ template <int SP> __global__ void __launch_bounds__(576) scan_fwd_dma_kernel(Sca
             else if (it == 1) score_rows<SP, 1>(sC, sB, sX, cum, dt, skip, lane, y);
             else if (it == 2) score_rows<SP, 2>(sC, sB, sX, cum, dt, skip, lane, y);
             else score_rows<SP, 3>(sC, sB, sX, cum, dt, skip, lane, y);
-            if ((k & 1) && it < 2) {        // chunks k + 1 and k + 2: the slots that are neither k's
-                decays(k + 1 + it, it == 0 ? slot : slot == 2 ? 0 : slot + 1);
-                fetch_dt(k + 3 + it);
+            if ((k & 1) && decaying) {      // chunks k + 1 and k + 2: the slots that are neither k's
+                decays(k + it, it == 1 ? slot : slot == 2 ? 0 : slot + 1);
+                fetch_dt(k + 2 + it);
+            }
+            if (it == 0) {      // all but chunk k + 2's have arrived
+                if (k + 2 < steps) wait_vmcnt<LOADS>();
+                else wait_vmcnt<0>();
             }
             __syncthreads();
         }

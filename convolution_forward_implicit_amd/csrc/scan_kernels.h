@@ -927,7 +927,6 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
     const int64_t NK = (int64_t)p.N * p.K;
     const int nt = w % WN, it0 = w / WN * ITW;          // dB and dC: states 16 nt .., tokens 16 it0 ..
     const bool on = it0 < NI;
-    const int pt = w & 3, jt0 = (w >> 2) * JW;          // dx: channels 16 pt .., tokens 16 jt0 ..
 
     XT xt, yt;
     float h0[16], u[16];        // state 16 nt + lane % 16, channels 32 ks + 8q + e at 8 ks + e
@@ -1047,7 +1046,8 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
         // computed where they are used, or the compiler computes all of them ahead
         // of the loop and keeps them in memory.
         const int lane = fresh_vector(lane_), w = fresh_scalar(w_), q = lane >> 4, l16 = lane & 15;
-        const int nt = w % WN, it0 = w / WN * ITW, pt = w & 3, jt0 = (w >> 2) * JW;
+        const int nt = w % WN, it0 = w / WN * ITW;
+        const int pt = w & 3, jt0 = (w >> 2) * JW;      // dx: channels 16 pt .., tokens 16 jt0 ..
         const bool on = it0 < NI;
         const int at = k & 1, d = (k / p.NPB) & 1, h = head_of(k), pb = k % p.NPB, pcols = min(kPB, p.P - pb * kPB);
         const float skip = p.d ? p.d[h] : 0.0f;

@@ -426,6 +426,49 @@ def test_same_bits_every_time_and_on_another_stream():
         assert torch.equal(a, b) and torch.equal(a, c) and torch.equal(a, e)
 
 
+def test_two_streams_at_once():
+    """Calls of the same plans on two streams, on other inputs: each has a workspace of its own."""
+    _, one = _everything(L=200)
+    _, two = _everything(L=130)
+    want = [[t.clone() for t in f()] for f in (one, two)]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = []
+        for f, side in zip((one, two), sides):
+            with torch.cuda.stream(side):
+                got.append(f())
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            for x, y in zip(a, b):
+                assert torch.equal(x, y)
+
+
+def test_offsets_past_32_bits():
+    """Rows a megabyte and more apart: 4.4e9 bytes of x, addressed as the packed rows are."""
+    CausalConv, SelectiveScan = _ops()
+    N, L, H, P, G, S, wide = 2, 1100, 1, 64, 1, 16, 1 << 20
+    g = torch.Generator().manual_seed(12)
+    r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(DEV)
+    x, dt, B, C, w = r(N, L, H, P), r(N, L, H), r(N, L, G, S), r(N, L, G, S), r(P, 4)
+    A = torch.full((H,), -1.0, device=DEV)
+    far = torch.empty(N, L, wide, dtype=torch.bfloat16, device=DEV)
+    fx, fB = far[..., 64:64 + P], far[..., 256:256 + S].unflatten(-1, (G, S))
+    fx.copy_(x[:, :, 0]), fB.copy_(B)
+    p = SelectiveScan({"N": N, "L": L, "H": H, "P": P, "G": G, "S": S}, "bf16")
+    y = far[..., 512:512 + P].unflatten(-1, (H, P))
+    p(fx.unflatten(-1, (H, P)), dt, A, fB, C, out=y)
+    want = p(x, dt, A, B, C)
+    assert torch.equal(y, want)
+    c = CausalConv({"N": N, "L": L, "C": P, "F": 4}, "bf16", silu=True)
+    out = far[..., 1024:1024 + P]
+    c(fx, w, out=out)
+    assert torch.equal(out, c(x[:, :, 0].contiguous(), w))
+    dx = far[..., 2048:2048 + P]
+    c.backward(out, fx, w, out={"dx": dx})
+    assert torch.equal(dx, c.backward(out.contiguous(), x[:, :, 0].contiguous(), w)["dx"])
+
+
 def test_captured_graphs_replay():
     """Two graphs of the whole chain, captured one after the other, replayed in turns with eager work between:
     each gives its own inputs' results every time."""
