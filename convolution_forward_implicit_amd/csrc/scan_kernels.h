@@ -895,18 +895,19 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
 template <typename T, int SP> struct BwdShared {
     static constexpr int Q = Frag<T>::Q, NI = Q / 16, NS = terms<T, 3>();
     static constexpr int XLD = kPB + Frag<T>::PAD, BLD = SP + Frag<T>::PAD, MLD = Q + Frag<T>::PAD;
+    static constexpr int ULD = kPB + 16 / (int)sizeof(T);       // few row fragments are read from u: half the padding
     __align__(16) T x[Q * XLD], y[Q * XLD];     // x and dy
     __align__(16) T b[Q * BLD], c[Q * BLD];
     __align__(16) T m[NS * Q * MLD];            // [term][j][i]
-    __align__(16) T u[NS * SP * XLD];           // [term][state][channel]
+    __align__(16) T u[NS * SP * ULD];           // [term][state][channel]
     __align__(16) float dt[2][Q], cum[2][Q], low[2][Q], w[2][Q], e[2][Q], raw[2][Q];   // w: e^{c_Q - c_j}
-    float row[2][NI][Q], col[2][NI][Q], cd[2][8][Q], xd[2][4][Q], dot[2][8], dd[2][8];
+    float row[2][NI][Q], col[2][NI][Q], cd[2][8][Q], xd[2][4][Q], xi[2][4][Q], dot[2][8], dd[2][8];
 };
 
 template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_kernel(ScanParams p)
 {
     typedef BwdShared<T, SP> Sh;
-    constexpr int Q = Sh::Q, NI = Sh::NI, NS = Sh::NS, XLD = Sh::XLD, BLD = Sh::BLD, MLD = Sh::MLD;
+    constexpr int Q = Sh::Q, NI = Sh::NI, NS = Sh::NS, XLD = Sh::XLD, BLD = Sh::BLD, MLD = Sh::MLD, ULD = Sh::ULD;
     constexpr int NT = SP / 16, TRI = NI * (NI + 1) / 2, TW = 6, TPW = (TRI + TW - 1) / TW;    // waves 6 and 7 have other work
     constexpr int WN = NT, WI = 8 / WN, ITW = NI / WI > 0 ? NI / WI : 1, JW = NI / 2;
     typedef Tile<T, Q, kPB, 512> XT;
@@ -973,7 +974,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
         }
     };
     // wave 7, per token: the sums of a head over its channel blocks
-    float rs = 0.0f, cs = 0.0f, cd = 0.0f, ee = 0.0f, dot = 0.0f, dd = 0.0f;
+    float rs = 0.0f, cs = 0.0f, cd = 0.0f, ee = 0.0f, ei = 0.0f, dot = 0.0f, dd = 0.0f;
     auto finish = [&](int k) __attribute__((always_inline)) {
         const int at = k & 1, d = (k / p.NPB) & 1;
         if (lane < Q) {
@@ -982,14 +983,14 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
 #pragma unroll
             for (int t = 0; t < WN; ++t) cd += sh.cd[at][t][lane];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) ee += sh.xd[at][t][lane];
+            for (int t = 0; t < 4; ++t) ee += sh.xd[at][t][lane], ei += sh.xi[at][t][lane];
         }
 #pragma unroll
         for (int t = 0; t < 8; ++t) dot += sh.dot[at][t], dd += sh.dd[at][t];
         if (k % p.NPB != p.NPB - 1) return;
         const int h = head_of(k);
         const float dt = lane < Q ? sh.dt[d][lane] : 0.0f, raw = lane < Q ? sh.raw[d][lane] : 0.0f, dec = sh.e[d][Q - 1];
-        const double before = (double)dt * ee - cs, behind = (double)rs - cs + cd;
+        const double before = (double)dt * ei, behind = (double)rs - cs + cd;
         const double b1 = wave_prefix(before), b2 = wave_prefix(behind);
         const float dl = (float)((b1 - before) + (wave_last(b2) - b2 + behind) + (double)(dec * dot));
         float draw = fmaf(p.a[h], dl, ee);
@@ -1003,7 +1004,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
             o[NK * p.H] = sb;
             o[2 * NK * p.H] = dd;
         }
-        rs = cs = cd = ee = dot = dd = 0.0f;
+        rs = cs = cd = ee = ei = dot = dd = 0.0f;
     };
 
     f32x4 sc[TPW], ds[TPW], dB[ITW], dC[ITW];
@@ -1062,7 +1063,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
                 make_split(reinterpret_cast<const float (&)[8]>(u[ks * 8]), us);
 #pragma unroll
                 for (int m = 0; m < NS; ++m)
-                    *reinterpret_cast<frag *>(sh.u + m * SP * XLD + (nt * 16 + l16) * XLD + ks * 32 + q * 8) = us.f[m];
+                    *reinterpret_cast<frag *>(sh.u + m * SP * ULD + (nt * 16 + l16) * ULD + ks * 32 + q * 8) = us.f[m];
             }
         }
         __syncthreads();
@@ -1101,7 +1102,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
                     m[r] = in ? sc[t8][r] * dec : 0.0f;
                     const float s = in ? dp[r] * dec * dj : 0.0f;
                     ds[t8][r] += s;
-                    wr[r] = s * sc[t8][r];
+                    wr[r] = i + r == j ? 0.0f : s * sc[t8][r];      // a token's own pair crosses no decay
                     col += wr[r];
                 }
                 write_split4<NS>(sh.m + j * MLD + i, Q * MLD, m);
@@ -1132,7 +1133,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-                for (int m = 0; m < NS; ++m) uf[ks][m] = read_rows(sh.u + m * SP * XLD, XLD, nt * 16, ks * 32, lane);
+                for (int m = 0; m < NS; ++m) uf[ks][m] = read_rows(sh.u + m * SP * ULD, ULD, nt * 16, ks * 32, lane);
             auto read = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
@@ -1175,7 +1176,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
             frag uf[2][NS], bf[2][JW];
             auto read = [&](int ks) __attribute__((always_inline)) {
 #pragma unroll
-                for (int m = 0; m < NS; ++m) uf[ks & 1][m] = read_cols(sh.u + m * SP * XLD, XLD, ks * 32, pt * 16, lane);
+                for (int m = 0; m < NS; ++m) uf[ks & 1][m] = read_cols(sh.u + m * SP * ULD, ULD, ks * 32, pt * 16, lane);
 #pragma unroll
                 for (int j = 0; j < JW; ++j) bf[ks & 1][j] = read_rows(sh.b, BLD, (jt0 + j) * 16, ks * 32, lane);
             };
@@ -1208,7 +1209,14 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
                 in_order();
             }
 #pragma unroll
-            for (int j = 0; j < JW; ++j) dx[j] *= *reinterpret_cast<const f32x4 *>(s_w + (jt0 + j) * 16 + q * 4);
+            for (int j = 0; j < JW; ++j) {
+                dx[j] *= *reinterpret_cast<const f32x4 *>(s_w + (jt0 + j) * 16 + q * 4);
+                // what comes from behind the chunk, for dl: as the whole less the
+                // chunk's own part it would lose the digits that ddt_bias sums up
+                const f32x4 xi = {xv[j][0] * dx[j][0], xv[j][1] * dx[j][1], xv[j][2] * dx[j][2], xv[j][3] * dx[j][3]};
+                const float s = row_sum4(xi, lane);
+                if ((l16 & 3) == 0) sh.xi[at][pt][(jt0 + j) * 16 + q * 4 + (l16 >> 2)] = s;
+            }
             // M's tiles (i >= j): in the upper half of the tokens only the second 32 meet it
 #pragma unroll
             for (int ks = 0; ks < Q / 32; ++ks) {
