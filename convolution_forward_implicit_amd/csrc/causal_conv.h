@@ -8,7 +8,9 @@
 // A wave owns 64 V neighbouring channels (V: 16 bytes, in the gradient 8) of a
 // run of tokens, so its accesses are whole lines and its rows' addresses scalar;
 // all rows of a run, with the F - 1 before it, are fetched before the first is
-// used.
+// used.  bf16, 4 taps, SiLU: 4096 x 2304 (38 MB) 10.2 us, 3.7 TB/s (13.6 with a
+// branch a row, 12.6 with rows in threads, 11.8 without the hint on the stores);
+// 32 single tokens 3.2 us, the launch.
 #pragma once
 
 #include "seq_common.h"
@@ -176,7 +178,10 @@ __global__ void __launch_bounds__(256) causal_step_kernel(CausalParams p)
 // A wave recomputes v for its run and the F - 1 tokens behind it (d of those
 // reaches back into the run), keeps its sums of dw and db in fp32 registers,
 // and the workgroup adds its runs in LDS, in a fixed order; causal_reduce_kernel
-// adds the workgroups' rows, in a fixed order too.
+// adds the workgroups' rows, in a fixed order too.  4 x 2048 x 2304 bf16 (113 MB):
+// 38 + 4 us, 2.7 TB/s: about 35 vector instructions an element, the sigmoid's two
+// at a quarter of the rate, are 22 us of it, at two waves per SIMD (200 registers
+// of fetched rows and sums); 74 us with a branch a row.
 template <typename T, int F, int V, bool SILU>
 __global__ void __launch_bounds__(256) causal_bwd_kernel(CausalParams p)
 {

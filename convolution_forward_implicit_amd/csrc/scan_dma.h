@@ -2,12 +2,9 @@
 // the formulas and the fragments of scan_kernels.h, fed by direct-to-LDS loads.
 //
 // scan_kernels.h's forward takes a chunk through one workgroup of four waves:
-// tiles through registers into LDS, scores, a barrier, the products with M.
-// Each wave waits for each of these in turn, and 256 registers leave room for
-// two waves per SIMD (long case, 16384 tokens of 64 heads: 19% of the matrix
-// instructions' time, 200 us).  Here a ring of three stages is filled by loads
-// that need no registers, two chunks ahead, and the waves have jobs that do not
-// wait for each other within a chunk:
+// tiles through registers into LDS, scores, a barrier, the products with M.  Here
+// a ring of three stages is filled by loads that need no registers, two chunks
+// ahead, and the waves have jobs that do not wait for each other within a chunk:
 //
 //   waves 0-3 ("state", 16 channels each):  y' = e^{c_i} h_0 C_i, then the state's update
 //   waves 4-7 ("score", 16 tokens each):    M from C . B, y'' = (M + D) x
@@ -26,6 +23,14 @@
 // constant plus a constant, and reads run at the rate of the banks: measured per
 // wave instruction, 16 rows of 16 bytes 4.0 clocks (8.0 with 16 or 48 bytes
 // between; 8 bytes of each row instead: 16), the transposing read 2.5 (4.0).
+//
+// What bounds it: 16384 tokens x 64 heads of 64 x 128 (34 Gflop by the recurrence,
+// 107 as the products that the splits make of it) take 172-190 us, 2.6 us a chunk
+// and workgroup: the matrix unit is busy for a third of that and other vector
+// instructions for half, and the two hardly overlap -- a wave of products and a wave
+// of FMAs on one SIMD take as long as one after the other (8 products and 24 FMAs:
+// 227 clocks, 128 and 107 alone).  LDS is busy for a quarter.  The registers' form
+// takes 207 us, the state pass 81 there and 62 here.
 #pragma once
 
 #include "igemm_dma.h"
@@ -34,18 +39,6 @@
 namespace convfwd {
 
 constexpr int kStages = 3;
-
-// MFMAS products of this region with VALUS other vector instructions between
-// each two: a product takes the matrix unit 16 clocks, in which the vector unit
-// is free for the splits of the next operand.
-template <int MFMAS, int VALUS> SEQ_DEV void interleave()
-{
-#pragma unroll
-    for (int i = 0; i < MFMAS; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, VALUS, 0);
-    }
-}
 
 // Tiles of 64 tokens x COLS bf16 in that layout
 template <int COLS> struct Ring {
@@ -152,7 +145,8 @@ SEQ_DEV void scan_states_dma(const ScanParams &p, int64_t block, StateDmaShared<
     auto issue = [&](int k) __attribute__((always_inline)) {
         const int64_t t0 = (int64_t)chunk_of(k) * Q;
         const int rows = (int)min((int64_t)Q, len - t0);
-        const i32x4_t xb = chunk_buffer(xg + t0 * x_ld, x_ld, rows, pcols), bb = chunk_buffer(bg + t0 * b_ld, b_ld, rows, p.S);
+        const i32x4_t xb = chunk_buffer(xg + t0 * x_ld, x_ld, rows, pcols);
+        const i32x4_t bb = chunk_buffer(bg + t0 * b_ld, b_ld, rows, p.S);
         const uint32_t to = ring + fill + (uint32_t)w * (2 * XR::GROUP);
 #pragma unroll
         for (int i = 0; i < ND; ++i) dma16(i * 4 < XR::LOADS ? xb : bb, src[i], 0, to + i * (8 * XR::GROUP));
@@ -259,8 +253,8 @@ template <int SP, bool STORE> __global__ void __launch_bounds__(256, 2) scan_sta
 template <int SP> struct FwdDmaShared {
     static constexpr int STAGE = Ring<kPB>::BYTES + 2 * Ring<SP>::BYTES;
     __align__(1024) unsigned char ring[kStages * STAGE];       // C, B, x of a chunk
-    __align__(16) float y[2][64 * kPB];                         // y' of a chunk: token i, piece c of four channels at c ^ i % 16
-    __align__(16) float cum[3][64], dt[3][64], w[3][64];        // of three chunks: c_i, dt_i, e^{c_Q - c_i} dt_i
+    __align__(16) float y[2][64 * kPB];         // y' of a chunk: token i, piece c of four channels at c ^ i % 16
+    __align__(16) float cum[3][64], dt[3][64], w[3][64];    // of three chunks: c_i, dt_i, e^{c_Q - c_i} dt_i
 };
 
 // A score wave's chunk: y'' of the tokens 16 IT .., in results of spread channels:
@@ -467,7 +461,7 @@ template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(Sca
 #pragma unroll
                 for (int it = 0; it < 4; ++it) y[it] = f32x4{0, 0, 0, 0};
                 split_h(0);
-                // the splits of the next operands go between the products
+                // the splits of the next operands go with the products
 #pragma unroll
                 for (int ks = 0; ks < KN; ++ks) {
                     if (ks + 1 < KN) {
@@ -482,7 +476,6 @@ template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(Sca
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
                         for (int it = 0; it < 4; ++it) y[it] = mma(hs[ks & 1].f[m], cf[ks][it], y[it]);
-                    interleave<8, 3>();
                     in_order();
                 }
                 split_x(1);
@@ -490,7 +483,6 @@ template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(Sca
                 for (int m = 0; m < 3; ++m)
 #pragma unroll
                     for (int t = 0; t < NT; ++t) st[t] = mma(bf[t], xs[0].f[m], st[t]);
-                interleave<3 * NT, 3>();
                 in_order();
                 read_b(1);
                 in_order();
@@ -503,7 +495,6 @@ template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(Sca
                 for (int m = 0; m < 3; ++m)
 #pragma unroll
                     for (int t = 0; t < NT; ++t) st[t] = mma(bf[t], xs[1].f[m], st[t]);
-                interleave<3 * NT, 3>();
             }
             __syncthreads();
         }
@@ -533,7 +524,8 @@ template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(Sca
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     const int piece = h * 8 + q * 2 + m;
-                    const f32x4 v = y[2 * h + m] + *reinterpret_cast<const f32x4 *>(&sh.y[k & 1][i * kPB + ((piece ^ l16) << 2)]);
+                    const float *from = &sh.y[k & 1][i * kPB + ((piece ^ l16) << 2)];
+                    const f32x4 v = y[2 * h + m] + *reinterpret_cast<const f32x4 *>(from);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) o[m * 4 + r] = (bf16_t)v[r];
                 }

@@ -422,6 +422,12 @@ SEQ_DEV void chunk_decay(float raw, bool live, float a, int softplus_on, float &
 
 
 // ---- states at the chunks' borders, and at the segments' ------------------------
+// (fp32 calls and bf16 rows that are no whole vectors; the others are in
+// scan_dma.h.)  The products with B are a quarter of the forward's; what a chunk
+// costs beside them is its way through registers into LDS and the decays' chain,
+// so four chunks' decays are done at once, one by each wave.  16384 tokens x 64
+// heads in bf16: 81 us against scan_dma.h's 62; fp32, 777 tokens x 12 sequences
+// and heads of 40 channels x 24 states: 6.0 us, the launch and three chunks' loads.
 // One workgroup: 64 channels of a head, one segment of chunks, wave w the
 // channels 16w..16w+15 and all of the state (results: rows channels, columns
 // states).  Run back (REV) from the last chunk to the first it takes dy, C and
@@ -650,11 +656,16 @@ SEQ_DEV void tri_tile(int t, int &it, int &jt)
 }
 
 // ---- forward -------------------------------------------------------------------
+// (fp32 calls and bf16 rows that are no whole vectors; the others are in
+// scan_dma.h.)
 // One workgroup: 64 channels of a head, one segment of chunks; wave w keeps the
 // state of channels 16w..16w+15 in registers (results: rows states, columns
 // channels, which makes them the operand of h_0 C as they stand).  The chunk's
 // scores are computed once, their 16x16 tiles dealt to the waves, and pass
-// through LDS as M.
+// through LDS as M.  The workgroup waits at four barriers a chunk; two of them
+// share a compute unit (234 registers).  16384 tokens x 64 heads in bf16 take 207
+// us with this kernel; fp32, 777 tokens x 12 heads of 40 x 24: 13 us, of which the
+// join of up to 9 segments is half.
 template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd_kernel(ScanParams p)
 {
     constexpr int Q = Frag<T>::Q, NT = SP / 16, NI = Q / 16, TRI = NI * (NI + 1) / 2, TPW = (TRI + 3) / 4;
@@ -892,6 +903,12 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
 // them.  While a head is computed the next one's x, dy and states are on their
 // way into registers, wave 6 does its decays, and wave 7 turns the sums that the
 // head before left in LDS into ddt and its parts of dA, ddt_bias and dD.
+// 2 x 2048 tokens, 32 heads of 64 x 128 in bf16: 87 us, 11 a head and chunk for 64
+// + 64 KB of states at its borders (1.5 TB/s); the products are 5 us of them, the
+// other vector instructions (splits, decays, sums over lanes) 30, and the loads of
+// the next states, which 256 registers leave no room to start earlier, most of the
+// rest.  Four waves of 512 registers instead: 138; the sums over lanes one value at
+// a time: 100.
 template <typename T, int SP> struct BwdShared {
     static constexpr int Q = Frag<T>::Q, NI = Q / 16, NS = terms<T, 3>();
     static constexpr int XLD = kPB + Frag<T>::PAD, BLD = SP + Frag<T>::PAD, MLD = Q + Frag<T>::PAD;
@@ -1340,7 +1357,9 @@ __global__ void __launch_bounds__(256) scan_reduce_kernel(ScanParams p, float *d
 // one sequence the launch does.  A wave takes kStepRows groups of channels; in a
 // group 64 / LPR channels lie beside each other, LPR lanes with V neighbouring
 // states each, so a wave's accesses are whole lines and y's sum is a few
-// exchanges between lanes.
+// exchanges between lanes.  64 sequences x 64 heads x 64 x 128 (269 MB): 54 us, 5.0
+// TB/s, the rate of a large copy (5.1); 57 without the hint on the stores, 67 with
+// two rows.  One sequence of 32 heads: 5.7 us.
 constexpr int kStepRows = 4;
 
 template <typename T, bool VEC>
@@ -1398,7 +1417,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p, int lpr, i
         if (ch < p.P) {
             float *s = p.state_out + (nh * p.P + ch) * p.S + s0;
             if (VEC) {
-                if (s0 < p.S) store_f32<float, V>(s, st[k]);
+                if (s0 < p.S) stream_f32<float, V>(s, st[k]);
             } else {
 #pragma unroll
                 for (int i = 0; i < V; ++i)
