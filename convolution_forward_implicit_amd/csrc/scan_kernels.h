@@ -919,6 +919,7 @@ template <typename T, int SP> struct BwdShared {
     __align__(16) T u[NS * SP * ULD];           // [term][state][channel]
     __align__(16) float dt[2][Q], cum[2][Q], low[2][Q], w[2][Q], e[2][Q], raw[2][Q];   // w: e^{c_Q - c_j}
     float row[2][NI][Q], col[2][NI][Q], cd[2][8][Q], xd[2][4][Q], xi[2][4][Q], dot[2][8], dd[2][8];
+    float sums[7][64];                          // wave 7's, from channel block to channel block of a head
 };
 
 template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_kernel(ScanParams p)
@@ -990,10 +991,15 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
             sh.e[to][lane] = exp2_fast((float)cum);
         }
     };
-    // wave 7, per token: the sums of a head over its channel blocks
-    float rs = 0.0f, cs = 0.0f, cd = 0.0f, ee = 0.0f, ei = 0.0f, dot = 0.0f, dd = 0.0f;
+    // Wave 7, per token: the sums of a head over its channel blocks (in LDS from
+    // block to block: as registers they would be everyone's), then what follows.
     auto finish = [&](int k) __attribute__((always_inline)) {
         const int at = k & 1, d = (k / p.NPB) & 1;
+        float rs = 0.0f, cs = 0.0f, cd = 0.0f, ee = 0.0f, ei = 0.0f, dot = 0.0f, dd = 0.0f;
+        if (k % p.NPB != 0) {
+            rs = sh.sums[0][lane], cs = sh.sums[1][lane], cd = sh.sums[2][lane], ee = sh.sums[3][lane];
+            ei = sh.sums[4][lane], dot = sh.sums[5][lane], dd = sh.sums[6][lane];
+        }
         if (lane < Q) {
 #pragma unroll
             for (int t = 0; t < NI; ++t) rs += sh.row[at][t][lane], cs += sh.col[at][t][lane];
@@ -1004,7 +1010,11 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
         }
 #pragma unroll
         for (int t = 0; t < 8; ++t) dot += sh.dot[at][t], dd += sh.dd[at][t];
-        if (k % p.NPB != p.NPB - 1) return;
+        if (k % p.NPB != p.NPB - 1) {
+            sh.sums[0][lane] = rs, sh.sums[1][lane] = cs, sh.sums[2][lane] = cd, sh.sums[3][lane] = ee;
+            sh.sums[4][lane] = ei, sh.sums[5][lane] = dot, sh.sums[6][lane] = dd;
+            return;
+        }
         const int h = head_of(k);
         const float dt = lane < Q ? sh.dt[d][lane] : 0.0f, raw = lane < Q ? sh.raw[d][lane] : 0.0f, dec = sh.e[d][Q - 1];
         const double before = (double)dt * ei, behind = (double)rs - cs + cd;
@@ -1021,7 +1031,6 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
             o[NK * p.H] = sb;
             o[2 * NK * p.H] = dd;
         }
-        rs = cs = cd = ee = ei = dot = dd = 0.0f;
     };
 
     f32x4 sc[TPW], ds[TPW], dB[ITW], dC[ITW];
@@ -1085,7 +1094,6 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
         }
         __syncthreads();
         if (k + 1 < blocks) {
-            fetch(k + 1);
             if (w == 6 && (k + 1) % p.NPB == 0) fetch_dt(k + 1);
         }
         // dP, M and dS, tile by tile; M goes to LDS transposed (rows j)
@@ -1186,7 +1194,10 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
         }
         if (w == 7 && k > 0) finish(k - 1);
         __syncthreads();
-        if (k + 1 < blocks) fetch_states(k + 1);
+        if (k + 1 < blocks) {
+            fetch_states(k + 1);
+            fetch(k + 1);
+        }
         // dx
         {
             f32x4 dx[JW];
