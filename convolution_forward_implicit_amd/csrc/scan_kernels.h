@@ -362,6 +362,12 @@ SEQ_DEV int fresh_scalar(int v)
     return v;
 }
 
+SEQ_DEV int64_t fresh_scalar(int64_t v)
+{
+    asm volatile("" : "+s"(v));
+    return v;
+}
+
 // the wave's number in the workgroup, known to be the same in all its lanes
 SEQ_DEV int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
@@ -903,12 +909,12 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
 // them.  While a head is computed the next one's x, dy and states are on their
 // way into registers, wave 6 does its decays, and wave 7 turns the sums that the
 // head before left in LDS into ddt and its parts of dA, ddt_bias and dD.
-// 2 x 2048 tokens, 32 heads of 64 x 128 in bf16: 87 us, 11 a head and chunk for 64
-// + 64 KB of states at its borders (1.5 TB/s); the products are 5 us of them, the
+// 2 x 2048 tokens, 32 heads of 64 x 128 in bf16: 78 us, 10 a head and chunk for 64
+// + 64 KB of states at its borders (1.7 TB/s); the products are 5 us of them, the
 // other vector instructions (splits, decays, sums over lanes) 30, and the loads of
 // the next states, which 256 registers leave no room to start earlier, most of the
 // rest.  Four waves of 512 registers instead: 138; the sums over lanes one value at
-// a time: 100.
+// a time: 100; the tensors' addresses kept over the heads instead of taken anew: 82.
 template <typename T, int SP> struct BwdShared {
     static constexpr int Q = Frag<T>::Q, NI = Q / 16, NS = terms<T, 3>();
     static constexpr int XLD = kPB + Frag<T>::PAD, BLD = SP + Frag<T>::PAD, MLD = Q + Frag<T>::PAD;
@@ -936,13 +942,14 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
     const int slice = (int)(blockIdx.x % p.slices);
     const int64_t ng = blockIdx.x / p.slices;
     const int g = (int)(ng % p.G);
-    const int64_t nc = ng / p.G, n = nc / p.K;
+    const int64_t nc = ng / p.G, n_ = nc / p.K, n = n_;
     const int c = (int)(nc - n * p.K), hpg = p.H / p.G;
     const int h_lo = slice * p.heads_per_slice, h_hi = min(hpg, h_lo + p.heads_per_slice);
     const int blocks = (h_hi - h_lo) * p.NPB;           // channel blocks of the slice's heads
     const int64_t len = seq_len(p.lengths, n, p.L), t0 = (int64_t)c * Q;
     const int rows = (int)max((int64_t)0, min((int64_t)Q, len - t0)), all_rows = (int)min((int64_t)Q, p.L - t0);
-    const int64_t base = n * p.L + t0;
+    const int64_t base_ = n * p.L + t0;       // the chunk's first row: taken anew where used, or every tensor's
+                                              // address is computed once and kept
     const int64_t NK = (int64_t)p.N * p.K;
     const int nt = w % WN, it0 = w / WN * ITW;          // dB and dC: states 16 nt .., tokens 16 it0 ..
     const bool on = it0 < NI;
@@ -952,12 +959,13 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
     auto head_of = [&](int k) __attribute__((always_inline)) { return g * hpg + h_lo + k / p.NPB; };
     auto fetch = [&](int k) __attribute__((always_inline)) {
         const int h = head_of(k), pb = k % p.NPB, pcols = min(kPB, p.P - pb * kPB);
-        const int64_t xo = (int64_t)h * p.P + pb * kPB;
+        const int64_t xo = (int64_t)h * p.P + pb * kPB, base = fresh_scalar(base_);
         xt.load((const T *)p.x + base * p.x_ld + xo, p.x_ld, rows, pcols, p.vec);
         yt.load((const T *)p.dy + base * p.dy_ld + xo, p.dy_ld, rows, pcols, p.vec);
     };
     auto fetch_states = [&](int k) __attribute__((always_inline)) {
         const int h = head_of(k), pb = k % p.NPB;
+        const int64_t n = fresh_scalar(n_);
         const int64_t o = (((n * p.H + h) * p.NPB + pb) * p.K + c) * (SP * kPB) + (nt * 16 + l16) * kPB + q * 8;
         // behind the sequence x, dy and dt are zeros: any finite state will do
 #pragma unroll
@@ -974,6 +982,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
     float raw = 0.0f;       // wave 6: of the head that comes next
     auto fetch_dt = [&](int k) __attribute__((always_inline)) {
         const int h = head_of(k);
+        const int64_t base = fresh_scalar(base_);
         raw = lane < rows ? (float)((const T *)p.dt)[(base + lane) * p.dt_ld + h] + (p.dt_bias ? p.dt_bias[h] : 0.0f) : 0.0f;
     };
     auto decays = [&](int k) __attribute__((always_inline)) {
@@ -1016,6 +1025,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
             return;
         }
         const int h = head_of(k);
+        const int64_t base = fresh_scalar(base_);
         const float dt = lane < Q ? sh.dt[d][lane] : 0.0f, raw = lane < Q ? sh.raw[d][lane] : 0.0f, dec = sh.e[d][Q - 1];
         const double before = (double)dt * ei, behind = (double)rs - cs + cd;
         const double b1 = wave_prefix(before), b2 = wave_prefix(behind);
@@ -1040,8 +1050,8 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
     for (int k = 0; k < ITW; ++k) dB[k] = dC[k] = f32x4{0, 0, 0, 0};
     {
         BT bt, ct;
-        bt.load((const T *)p.b + base * p.b_ld + (int64_t)g * p.S, p.b_ld, rows, p.S, p.vec);
-        ct.load((const T *)p.c + base * p.c_ld + (int64_t)g * p.S, p.c_ld, rows, p.S, p.vec);
+        bt.load((const T *)p.b + base_ * p.b_ld + (int64_t)g * p.S, p.b_ld, rows, p.S, p.vec);
+        ct.load((const T *)p.c + base_ * p.c_ld + (int64_t)g * p.S, p.c_ld, rows, p.S, p.vec);
         fetch(0);
         fetch_states(0);
         bt.store(sh.b);
@@ -1154,7 +1164,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
         }
         // dC and dB through the states at the borders
         if (on) {
-            frag yf[2][2], xf[2][2], uf[2][NS];
+            frag yf[2], xf[2], uf[2][NS];
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
@@ -1162,8 +1172,8 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
             auto read = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
-                    yf[i & 1][ks] = read_rows(sh.y, XLD, (it0 + i) * 16, ks * 32, lane);
-                    xf[i & 1][ks] = read_rows(sh.x, XLD, (it0 + i) * 16, ks * 32, lane);
+                    yf[ks] = read_rows(sh.y, XLD, (it0 + i) * 16, ks * 32, lane);
+                    xf[ks] = read_rows(sh.x, XLD, (it0 + i) * 16, ks * 32, lane);
                 }
             };
             read(0);
@@ -1175,16 +1185,17 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
                 f32x4 cv;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) cv[r] = (float)sh.c[(row + r) * BLD + nt * 16 + l16];
-                if (i + 1 < ITW) read(i + 1);
                 in_order();
                 f32x4 ac = {0, 0, 0, 0}, ab = {0, 0, 0, 0};
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
                     for (int m = 0; m < NS; ++m) {
-                        ac = mma(yf[i & 1][ks], hs[ks].f[m], ac);
-                        ab = mma(xf[i & 1][ks], uf[ks][m], ab);
+                        ac = mma(yf[ks], hs[ks].f[m], ac);
+                        ab = mma(xf[ks], uf[ks][m], ab);
                     }
+                if (i + 1 < ITW) read(i + 1);       // under way while the sums follow
+                in_order();
                 ac *= ei;
                 dC[i] += ac;
                 dB[i] += ab * wi;
@@ -1277,6 +1288,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
         }
         if (w == 6 && k + 1 < blocks && (k + 1) % p.NPB == 0) decays(k + 1);
         __syncthreads();
+        const int64_t base = fresh_scalar(base_);
         XT::write(sh.x, (T *)p.dx + base * p.dx_ld + (int64_t)h * p.P + pb * kPB, p.dx_ld, all_rows, pcols, p.vec);
     }
     if (w == 7) finish(blocks - 1);
@@ -1315,10 +1327,10 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
             const int row = (it0 + i) * 16 + q * 4 + r;
             if (row >= all_rows) continue;
             if (p.slices == 1) {
-                ((T *)p.db)[(base + row) * p.db_ld + g * p.S + s] = (T)dB[i][r];
-                ((T *)p.dc)[(base + row) * p.dc_ld + g * p.S + s] = (T)dC[i][r];
+                ((T *)p.db)[(base_ + row) * p.db_ld + g * p.S + s] = (T)dB[i][r];
+                ((T *)p.dc)[(base_ + row) * p.dc_ld + g * p.S + s] = (T)dC[i][r];
             } else {
-                const int64_t o = (((int64_t)slice * p.N * p.L + base + row) * p.G + g) * SP + s;
+                const int64_t o = (((int64_t)slice * p.N * p.L + base_ + row) * p.G + g) * SP + s;
                 p.part_b[o] = dB[i][r];
                 p.part_c[o] = dC[i][r];
             }
