@@ -103,6 +103,11 @@ bool vector_rows(const Rows &t) { return !t.p || ((uintptr_t)t.p % 16 == 0 && t.
 
 int64_t or_packed(int64_t ld, int64_t width) { return ld == 0 ? width : ld; }
 
+// What a kernel gets as a tensor's stride.  One row has no next one, and its
+// stride may be any: a small one keeps the 32-bit offsets of the rows that a
+// tile has none of past the tensor's end (64 rows of 2^27 bytes wrap round).
+int64_t stride(const Rows &t) { return t.rows > 1 ? t.ld : std::min<int64_t>(t.ld, 65536); }
+
 conv_status_t check_workspace(const void *ws, int64_t bytes, int64_t need)
 {
     if (need == 0) return CONV_OK;
@@ -344,7 +349,7 @@ static conv_status_t causal_forward(const conv_causal_plan_t *plan, const conv_c
     CausalParams p{};
     p.x = a->x; p.w = a->w; p.bias = a->bias; p.state = a->state; p.lengths = a->lengths;
     p.y = a->y; p.state_out = a->state_out;
-    p.x_ld = in[0].ld; p.y_ld = out[0].ld;
+    p.x_ld = stride(in[0]); p.y_ld = stride(out[0]);
     p.N = (int)d.N; p.C = (int)d.C; p.CV = (int)(d.C / V); p.L = L;
     p.blocks = (L + kConvRun - 1) / kConvRun;
     const int64_t runs = p.blocks + (a->state_out ? 1 : 0);
@@ -407,7 +412,7 @@ conv_status_t conv_causal_bwd_run(const conv_causal_plan_t *plan, const conv_cau
     p.x = a->x; p.w = a->w; p.bias = a->bias; p.state = a->state; p.lengths = a->lengths;
     p.dy = a->dy; p.dstate_out = a->dstate_out; p.dx = a->dx; p.dstate = a->dstate;
     p.partial = (float *)workspace;
-    p.x_ld = in[1].ld; p.dy_ld = in[0].ld; p.dx_ld = out[0].ld;
+    p.x_ld = stride(in[1]); p.dy_ld = stride(in[0]); p.dx_ld = stride(out[0]);
     p.N = (int)d.N; p.C = (int)d.C; p.CV = (int)(d.C / V); p.L = d.L;
     p.blocks = bwd_blocks(d);
     (void)hipGetLastError();
@@ -497,11 +502,11 @@ conv_status_t conv_scan_create(const conv_scan_desc_t *desc, conv_scan_plan_t **
     pl->o_pc = o + part;
     pl->bwd_ws_bytes = o + 2 * part;
     snprintf(pl->text, sizeof(pl->text),
-             "scan %s N=%lld L=%lld H=%lld P=%lld G=%lld S=%lld(%d)%s, %d chunks of %d in %d segments; "
-             "gradient: %d segments, %d slices of %d heads",
+             "scan %s N=%lld L=%lld H=%lld P=%lld G=%lld S=%lld(%d)%s, %d chunks of %d in %d segments "
+             "(%d x %d of whole bf16 vectors); gradient: %d segments, %d slices of %d heads",
              d.dtype == CONV_DT_BF16 ? "bf16" : "f32", (long long)d.N, (long long)d.L, (long long)d.H, (long long)d.P,
-             (long long)d.G, (long long)d.S, pl->SP, d.softplus ? " softplus" : "", pl->K, pl->Q, pl->fwd.count, pl->bwd.count,
-             pl->slices, pl->heads_per_slice);
+             (long long)d.G, (long long)d.S, pl->SP, d.softplus ? " softplus" : "", pl->K, pl->Q, pl->fwd.count,
+             pl->dma.count / pl->dma.sub, pl->dma.sub, pl->bwd.count, pl->slices, pl->heads_per_slice);
     if (getenv("CONVFWD_LOG")) fprintf(stderr, "convfwd: %s\n", pl->text);
     *plan = pl;
     return CONV_OK;
@@ -565,7 +570,7 @@ static conv_status_t scan_forward(const conv_scan_plan_t *plan, const conv_scan_
     p.L = L;
     p.x = a->x; p.dt = a->dt; p.b = a->b; p.c = a->c; p.a = a->a; p.d = a->d; p.dt_bias = a->dt_bias;
     p.state = a->state; p.lengths = a->lengths; p.y = a->y; p.state_out = a->state_out;
-    p.x_ld = in[0].ld; p.b_ld = in[1].ld; p.c_ld = in[2].ld; p.dt_ld = in[3].ld; p.y_ld = out[0].ld;
+    p.x_ld = stride(in[0]); p.b_ld = stride(in[1]); p.c_ld = stride(in[2]); p.dt_ld = stride(in[3]); p.y_ld = stride(out[0]);
     hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
     if (step) {
@@ -647,8 +652,8 @@ conv_status_t conv_scan_bwd_run(const conv_scan_plan_t *plan, const conv_scan_bw
     p.x = a->x; p.dt = a->dt; p.b = a->b; p.c = a->c; p.a = a->a; p.d = a->d; p.dt_bias = a->dt_bias;
     p.state = a->state; p.lengths = a->lengths; p.dy = a->dy; p.dstate_out = a->dstate_out;
     p.dx = a->dx; p.ddt = a->ddt; p.db = a->db; p.dc = a->dc; p.dstate = a->dstate;
-    p.dy_ld = in[0].ld; p.x_ld = in[1].ld; p.b_ld = in[2].ld; p.c_ld = in[3].ld; p.dt_ld = in[4].ld;
-    p.dx_ld = out[0].ld; p.db_ld = out[1].ld; p.dc_ld = out[2].ld; p.ddt_ld = out[3].ld;
+    p.dy_ld = stride(in[0]); p.x_ld = stride(in[1]); p.b_ld = stride(in[2]); p.c_ld = stride(in[3]); p.dt_ld = stride(in[4]);
+    p.dx_ld = stride(out[0]); p.db_ld = stride(out[1]); p.dc_ld = stride(out[2]); p.ddt_ld = stride(out[3]);
     const Rows vec[] = {in[0], in[1], in[2], in[3], out[0]};
     p.vec = scan_vector(*plan, vec, 5);
     char *ws = (char *)workspace;

@@ -444,6 +444,22 @@ def test_two_streams_at_once():
                 assert torch.equal(x, y)
 
 
+def test_one_row_wider_than_32_bit_offsets_of_a_tile():
+    """One token of 2^26 channels: the rows that its tile has none of lie 2^27 bytes apart.  With one token and
+    one state y = (dt B C + D) x; the factor is a sum of two terms of one sign here."""
+    _, SelectiveScan = _ops()
+    H, P = 1024, 65536
+    g = torch.Generator(device=DEV).manual_seed(3)
+    u = lambda *s: (torch.rand(*s, generator=g, device=DEV) + 0.5)
+    x = torch.randn(1, 1, H, P, generator=g, device=DEV, dtype=torch.bfloat16)
+    dt, B, C = (u(*s).to(torch.bfloat16) for s in ((1, 1, H), (1, 1, 1, 1), (1, 1, 1, 1)))
+    A, D = -u(H), u(H)
+    y = SelectiveScan({"N": 1, "L": 1, "H": H, "P": P, "G": 1, "S": 1}, "bf16", softplus=False)(x, dt, A, B, C, D)
+    factor = (dt.double() * B.double()[..., 0] * C.double()[..., 0] + D.double()).float()
+    want = x[0, 0].float() * factor[0, 0, :, None]
+    assert ((y[0, 0].float() - want).abs() <= (HALF["bf16"] * (1 + 2 ** -8) + 2.0 ** -14) * want.abs() + 1e-37).all()
+
+
 def test_offsets_past_32_bits():
     """Rows a megabyte and more apart: 4.4e9 bytes of x, addressed as the packed rows are."""
     CausalConv, SelectiveScan = _ops()
