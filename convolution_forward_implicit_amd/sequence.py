@@ -89,6 +89,17 @@ class _Plan:
             stream = torch.cuda.current_stream(dev)
         return stream.cuda_stream, torch.cuda.stream(stream)       # also makes its device the current one
 
+    @staticmethod
+    def _new(torch, like, shape, away):
+        """An output: of the stream that writes it, whose earlier work alone may
+        still hold its memory, and known to the caller's, which will read it."""
+        if away is None:
+            return like.new_empty(*shape)
+        with away:
+            t = like.new_empty(*shape)
+        t.record_stream(torch.cuda.current_stream(like.device))
+        return t
+
 
 class CausalConv(_Plan):
     """A plan of the causal depthwise convolution.  `problem` is a dict {"N",
@@ -123,7 +134,7 @@ class CausalConv(_Plan):
         t, dev = self._type(torch), x.device
         stream, away = self._on(torch, dev, stream)
         if out is None:
-            out = x.new_empty(*self.x_shape)
+            out = self._new(torch, x, self.x_shape, away)
         lead, inner = self.x_shape[:2], self.x_shape[2:]
         xp, x_ld = self._rows(x, lead, inner, t, dev, "x")
         yp, y_ld = self._rows(out, lead, inner, t, dev, "out")
@@ -147,7 +158,7 @@ class CausalConv(_Plan):
         stream, away = self._on(torch, dev, stream)
         lead, inner = self.x_shape[:1], self.x_shape[2:]
         if out is None:
-            out = x.new_empty(*lead, *inner)
+            out = self._new(torch, x, lead + inner, away)
         xp, x_ld = self._rows(x, lead, inner, t, dev, "x")
         yp, y_ld = self._rows(out, lead, inner, t, dev, "out")
         sp = self._dense(state, self.state_shape, t, dev, "state")
@@ -173,7 +184,7 @@ class CausalConv(_Plan):
         _given(got, out, shapes)
         for k, shape in shapes.items():
             if shape is not None and got[k] is None:
-                got[k] = x.new_empty(*shape)
+                got[k] = self._new(torch, x, shape, away)
         lead, inner = self.x_shape[:2], self.x_shape[2:]
         dyp, dy_ld = self._rows(dy, lead, inner, t, dev, "dy")
         xp, x_ld = self._rows(x, lead, inner, t, dev, "x")
@@ -230,7 +241,7 @@ class SelectiveScan(_Plan):
         t, dev = self._type(torch), x.device
         stream, away = self._on(torch, dev, stream)
         if out is None:
-            out = x.new_empty(*self.x_shape)
+            out = self._new(torch, x, self.x_shape, away)
         lead = self.x_shape[:2]
         xp, x_ld = self._rows(x, lead, self.x_shape[2:], t, dev, "x")
         dp, dt_ld = self._rows(dt, lead, self.dt_shape[2:], t, dev, "dt")
@@ -254,7 +265,7 @@ class SelectiveScan(_Plan):
         stream, away = self._on(torch, dev, stream)
         lead, hp, gs = self.x_shape[:1], self.x_shape[2:], self.b_shape[2:]
         if out is None:
-            out = x.new_empty(*lead, *hp)
+            out = self._new(torch, x, lead + hp, away)
         xp, x_ld = self._rows(x, lead, hp, t, dev, "x")
         dp, dt_ld = self._rows(dt, lead, self.a_shape, t, dev, "dt")
         bp, b_ld = self._rows(B, lead, gs, t, dev, "B")
@@ -288,7 +299,7 @@ class SelectiveScan(_Plan):
         _given(got, out, shapes)
         for k, shape in shapes.items():
             if shape is not None and got[k] is None:
-                got[k] = (x if k in ("dx", "ddt", "dB", "dC") else A).new_empty(*shape)
+                got[k] = self._new(torch, x if k in ("dx", "ddt", "dB", "dC") else A, shape, away)
         lead, hp, gs, hh = self.x_shape[:2], self.x_shape[2:], self.b_shape[2:], self.dt_shape[2:]
         rows = [self._rows(v, lead, inner, t, dev, name) for v, inner, name in (
             (dy, hp, "dy"), (x, hp, "x"), (dt, hh, "dt"), (B, gs, "B"), (C, gs, "C"),

@@ -444,6 +444,25 @@ def test_two_streams_at_once():
                 assert torch.equal(x, y)
 
 
+def test_outputs_belong_to_the_stream_that_writes_them():
+    """Memory that the current stream has still to write to is not what a call on another stream returns."""
+    _, run = _everything(L=200)
+    want = run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    junk = torch.ones(1 << 26, device=DEV)
+    late = [torch.empty_like(t) for t in want]
+    for _ in range(40):
+        junk.mul_(1.0)                  # some milliseconds on the current stream
+    for t in late:
+        t.fill_(-7.0)
+    del late, t
+    got = run(side)[:1]                 # y: allocated by the call
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0])
+
+
 def test_one_row_wider_than_32_bit_offsets_of_a_tile():
     """One token of 2^26 channels: the rows that its tile has none of lie 2^27 bytes apart.  With one token and
     one state y = (dt B C + D) x; the factor is a sum of two terms of one sign here."""
