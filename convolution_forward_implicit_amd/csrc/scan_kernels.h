@@ -150,6 +150,18 @@ template <typename T, int NS> SEQ_DEV f32x4 mma_b(const typename Frag<T>::type &
     return c;
 }
 
+// The bf16 matrix unit rounds its sums down, by a few hundredths of a step on
+// average: where they meet x, B or C of one sign it adds up over the tokens.
+// The gradient takes half of its products of negated operands (`flip`: their
+// sign bits) and negates the sums: the error of ddt_bias halves, for 2 of 80 us.
+SEQ_DEV bf16x8 flipped(bf16x8 f, uint32_t flip)
+{
+    typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4_t, f) ^ (u32x4_t)(flip));
+}
+SEQ_DEV Frag<float>::type flipped(const Frag<float>::type &f, uint32_t) { return f; }
+template <typename T> SEQ_DEV uint32_t flip_of(bool odd) { return sizeof(T) == 2 && odd ? 0x80008000u : 0; }
+
 SEQ_DEV float frag_get(bf16x8 f, int e) { return (float)f[e]; }
 SEQ_DEV float frag_get(const Frag<float>::type &f, int e) { return f.v[e]; }
 
@@ -909,7 +921,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
 // them.  While a head is computed the next one's x, dy and states are on their
 // way into registers, wave 6 does its decays, and wave 7 turns the sums that the
 // head before left in LDS into ddt and its parts of dA, ddt_bias and dD.
-// 2 x 2048 tokens, 32 heads of 64 x 128 in bf16: 78 us, 10 a head and chunk for 64
+// 2 x 2048 tokens, 32 heads of 64 x 128 in bf16: 80 us, 10 a head and chunk for 64
 // + 64 KB of states at its borders (1.7 TB/s); the products are 5 us of them, the
 // other vector instructions (splits, decays, sums over lanes) 30, and the loads of
 // the next states, which 256 registers leave no room to start earlier, most of the
@@ -1115,6 +1127,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
                 int it, jt;
                 tri_tile(t, it, jt);
                 const int i = it * 16 + q * 4, j = jt * 16 + l16;
+                const uint32_t flip = flip_of<T>((it + jt) & 1);
                 frag yf[2], xf[2];
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
@@ -1127,7 +1140,8 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
                 in_order();
                 f32x4 dp = {0, 0, 0, 0}, m, wr;
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks) dp = mma(yf[ks], xf[ks], dp);
+                for (int ks = 0; ks < 2; ++ks) dp = mma(flipped(yf[ks], flip), xf[ks], dp);
+                if (flip) dp = -dp;
                 float col = 0.0f;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -1156,6 +1170,8 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
         }
         make_split(reinterpret_cast<const float (&)[8]>(h0[0]), hs[0]);
         make_split(reinterpret_cast<const float (&)[8]>(h0[8]), hs[1]);
+        const uint32_t flip_s = flip_of<T>(nt & 1);
+        const float sign_s = flip_s ? -1.0f : 1.0f;
         part = wave_sum(part);
         diag = wave_sum(diag);
         if (lane == 0) {
@@ -1191,12 +1207,12 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
                 for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
                     for (int m = 0; m < NS; ++m) {
-                        ac = mma(yf[ks], hs[ks].f[m], ac);
+                        ac = mma(flipped(yf[ks], flip_s), hs[ks].f[m], ac);
                         ab = mma(xf[ks], uf[ks][m], ab);
                     }
                 if (i + 1 < ITW) read(i + 1);       // under way while the sums follow
                 in_order();
-                ac *= ei;
+                ac *= ei * sign_s;
                 dC[i] += ac;
                 dB[i] += ab * wi;
                 const float s = row_sum4(ac * cv, lane);
@@ -1211,6 +1227,8 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
         }
         // dx
         {
+            const uint32_t flip_x = flip_of<T>(pt & 1);
+            const float sign_x = flip_x ? -1.0f : 1.0f;
             f32x4 dx[JW];
             frag uf[2][NS], bf[2][JW];
             auto read = [&](int ks) __attribute__((always_inline)) {
@@ -1244,7 +1262,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
 #pragma unroll
                 for (int m = 0; m < NS; ++m)
 #pragma unroll
-                    for (int j = 0; j < JW; ++j) dx[j] = mma(bf[ks & 1][j], uf[ks & 1][m], dx[j]);
+                    for (int j = 0; j < JW; ++j) dx[j] = mma(flipped(bf[ks & 1][j], flip_x), uf[ks & 1][m], dx[j]);
                 in_order();
             }
 #pragma unroll
@@ -1254,7 +1272,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
                 // chunk's own part it would lose the digits that ddt_bias sums up
                 const f32x4 xi = {xv[j][0] * dx[j][0], xv[j][1] * dx[j][1], xv[j][2] * dx[j][2], xv[j][3] * dx[j][3]};
                 const float s = row_sum4(xi, lane);
-                if ((l16 & 3) == 0) sh.xi[at][pt][(jt0 + j) * 16 + q * 4 + (l16 >> 2)] = s;
+                if ((l16 & 3) == 0) sh.xi[at][pt][(jt0 + j) * 16 + q * 4 + (l16 >> 2)] = s * sign_x;
             }
             // M's tiles (i >= j): in the upper half of the tokens only the second 32 meet it
 #pragma unroll
@@ -1269,12 +1287,13 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
 #pragma unroll
                 for (int m = 0; m < NS; ++m)
 #pragma unroll
-                    for (int j = 0; j < JW; ++j) dx[j] = mma(mf[j][m], yf[ks], dx[j]);
+                    for (int j = 0; j < JW; ++j) dx[j] = mma(mf[j][m], flipped(yf[ks], flip_x), dx[j]);
             }
 #pragma unroll
             for (int j = 0; j < JW; ++j) {
                 const f32x4 dj = *reinterpret_cast<const f32x4 *>(s_dt + (jt0 + j) * 16 + q * 4);
                 f32x4 xd;
+                dx[j] *= sign_x;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int row = (jt0 + j) * 16 + q * 4 + r;
