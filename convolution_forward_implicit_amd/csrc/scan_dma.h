@@ -172,6 +172,11 @@ SEQ_DEV void scan_states_dma(const ScanParams &p, int64_t block, StateDmaShared<
         if (steps > 1) issue(1);
     }
     if (STORE) start_states<SP, REV>(p, unit, seg, ch, pcols, lane, acc);
+    // odd waves carry their states negated: see flipped()
+    const uint32_t flip = flip_of<bf16_t>(w & 1);
+    const float sign = flip ? -1.0f : 1.0f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] *= sign;
     float log_dec = 0.0f;
     if (steps > 0) {
         decays(w);
@@ -186,7 +191,7 @@ SEQ_DEV void scan_states_dma(const ScanParams &p, int64_t block, StateDmaShared<
         if (STORE) {
             float *s = p.bound[REV] + (unit * p.K + chunk_of(k)) * (SP * kPB);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(s + (t * 16 + l16) * kPB + ch) = acc[t];
+            for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4 *>(s + (t * 16 + l16) * kPB + ch) = acc[t] * sign;
         }
         const float tot = sh.tot[k & 7], dec = exp2_fast(tot);
         log_dec += tot;
@@ -195,7 +200,7 @@ SEQ_DEV void scan_states_dma(const ScanParams &p, int64_t block, StateDmaShared<
             f32x4 wt[2][2];
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                xf[ks] = XR::cols(sX, ks * 32, w * 16, lane);
+                xf[ks] = flipped(XR::cols(sX, ks * 32, w * 16, lane), flip);
                 wt[ks][0] = *reinterpret_cast<const f32x4 *>(&sh.w[k & 7][ks * 32 + q * 4]);
                 wt[ks][1] = *reinterpret_cast<const f32x4 *>(&sh.w[k & 7][ks * 32 + 16 + q * 4]);
             }
@@ -230,6 +235,8 @@ SEQ_DEV void scan_states_dma(const ScanParams &p, int64_t block, StateDmaShared<
         else wait_vmcnt<0>();
         __syncthreads();
     }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] *= sign;
     if (!STORE) {
         leave_segment<SP>(p, seg_state, seg_log, unit, seg, ch, lane, log_dec, acc);
     } else if (REV && seg == 0 && p.dstate) {
