@@ -430,7 +430,7 @@ template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(Sca
                 bf16x8 cf[KN][4], xf[2], bf[NT];
                 f32x4 y[4], w0[2], w1[2];
                 float ei[4];
-                Split<bf16_t, 2> hs[2];
+                Split<bf16_t, 3> hs[2];
                 Split<bf16_t, 3> xs[2];
                 auto read_b = [&](int ks) __attribute__((always_inline)) {
 #pragma unroll
@@ -480,7 +480,7 @@ template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(Sca
                     }
                     if (ks == (KN > 1 ? KN - 2 : 0)) read_b(0);
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
+                    for (int m = 0; m < 3; ++m)
 #pragma unroll
                         for (int it = 0; it < 4; ++it) y[it] = mma(hs[ks & 1].f[m], cf[ks][it], y[it]);
                     in_order();

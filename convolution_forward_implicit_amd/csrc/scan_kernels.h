@@ -839,10 +839,10 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
                 float v[8];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = st[2 * ks][e], v[4 + e] = st[2 * ks + 1][e];
-                Split<T, NM> hs;
+                Split<T, NX> hs;
                 make_split(v, hs);
 #pragma unroll
-                for (int m = 0; m < NM; ++m)
+                for (int m = 0; m < NX; ++m)
 #pragma unroll
                     for (int it = 0; it < NI; ++it) y[it] = mma(cf[ks & 1][it], hs.f[m], y[it]);
                 in_order();

@@ -1,0 +1,76 @@
+"""How exactly the selective scan is computed, on inputs of few terms: the
+tolerances are small enough to see an operand or an exponent that is held in
+fewer than fp32's 24 bits.
+
+Tolerances.  A result of type T is rounded once (half a step: 2^-8 in bf16,
+2^-24 in fp32, of its value); before that it is off by c * sum |t_k| over its
+terms, the sum being evaluated by the reference (oracle/seq.py).  dt is used as
+it is (no softplus) and A and dt are exact, so a decay e^(A dt ..) has
+  half a step of the exponent, |e| 2^-24 ln 2 < 2^-22 for |e| <= 6, and the
+  exponential's own step, 2^-23: together under 2^-21.4,
+and a product on its way two roundings of 2^-24.  All but two states and three
+tokens are zeros, which add nothing: a sum has six terms at most, in three
+matrix instructions, each off by a step (2^-23) of what it holds at most.
+  one decay, one sum: 2^-21.4 + 2^-23 + 3 2^-23 < c = 2^-20
+  states over four chunks: a decay (2^-21.4) and a sum (2^-23) each, then the
+    product with C: 4 (2^-21.4 + 2^-23) + 2^-20 < c = 2^-18.2
+  gradients: two such chains, c = 2^-17.2
+An operand of two bf16 terms is off by up to 2^-18 by itself, and of 16 bits by
+2^-17; cancelling sums have it all where half a step of the result is far less.
+"""
+import pytest
+import torch
+
+from oracle import seq
+
+pytestmark = pytest.mark.gpu
+
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+TYPE = {"bf16": torch.bfloat16, "f32": torch.float32}
+DEV = "cuda:0"
+# channels, states: whole 16-byte vectors in bf16 and not, few and many states
+SHAPES = [(64, 8), (64, 5), (64, 128), (72, 100)]
+
+
+def _near(got, want, mag, half, c, what):
+    got, want, mag = got.detach().cpu().double(), want.double(), mag.double().abs()
+    assert torch.isfinite(got).all(), what
+    over = (got - want).abs() - (half * want.abs() * (1 + 2 ** -8) + c * mag + 1e-37)
+    assert (over <= 0).all(), "%s: error %.3g of the terms, %d of %d results over 2^%.1f" % (
+        what, ((got - want).abs() - half * want.abs()).div(mag + 1e-37).max(), (over > 0).sum(), over.numel(),
+        torch.tensor(c).log2())
+
+
+def _gpu(d):
+    return {k: v.to(DEV) if torch.is_tensor(v) else v for k, v in d.items()}
+
+
+def _scan(N, L, H, P, G, S, dtype):
+    from convolution_forward_implicit_amd import SelectiveScan
+    return SelectiveScan({"N": N, "L": L, "H": H, "P": P, "G": G, "S": S}, dtype, softplus=False)
+
+
+def _two_states(g, S, *lead):
+    """Values in two of S states, zeros in the others."""
+    v = torch.zeros(*lead, S)
+    v[..., [S // 3, S - 1]] = torch.randn(*lead, 2, generator=g)
+    return v
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("P,S", SHAPES)
+def test_a_state_enters_y_with_all_its_bits(P, S, dtype):
+    """y = e^(A dt) (h_1 C_1 + h_2 C_2) where the two products cancel to the last bits of h."""
+    g = torch.Generator().manual_seed(1)
+    N, H, t = 8, 16, TYPE[dtype]
+    C = _two_states(g, S, N, 1, 1).to(t)
+    a, b = S // 3, S - 1
+    h = torch.zeros(N, H, P, S)
+    h[..., a] = torch.randn(N, H, P, generator=g)
+    h[..., b] = -(h[..., a].double() * C[:, :, :, a].double() / C[:, :, :, b].double()).float()
+    v = dict(x=torch.zeros(N, 1, H, P, dtype=t), dt=torch.full((N, 1, H), 0.25, dtype=t), A=torch.full((H,), -0.5),
+             B=torch.ones(N, 1, 1, S, dtype=t), C=C, state=h)
+    y, _ = seq.scan(**v, softplus=False)
+    mag, _ = seq.scan(**v, softplus=False, magnitude=True)
+    assert (y.abs() < 2.0 ** -22 * mag).all()
+    _near(_scan(N, 1, H, P, 1, S, dtype)(**_gpu(v)), y, mag, HALF[dtype], 2.0 ** -20, "y")
