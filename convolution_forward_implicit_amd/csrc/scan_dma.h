@@ -328,10 +328,10 @@ SEQ_DEV void score_rows(const bf16_t *sC, const bf16_t *sB, const bf16_t *sX, co
         float v[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = s[2 * ks][e], v[4 + e] = s[2 * ks + 1][e];
-        Split<bf16_t, 2> ms;
+        Split<bf16_t, 3> ms;
         make_split(v, ms);
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int m = 0; m < 3; ++m)
 #pragma unroll
             for (int pt = 0; pt < 4; ++pt) y[pt] = mma(xf[ks][pt], ms.f[m], y[pt]);
     }

@@ -26,9 +26,11 @@
 //
 // Numbers.  The matrix instructions take bf16 operands and add in fp32.  x, B,
 // C and dy are bf16 already; what is computed on the way (M, the states, dS)
-// enters as the sum of two or three bf16 numbers, each the rounding of what
-// the ones before it left, so that 16 or 24 bits of it take part.  fp32 calls
-// run on the fp32 matrix instructions instead.  States, sums and exponents are
+// enters as the sum of three bf16 numbers, each the rounding of what the ones
+// before it left, so that all 24 bits of it take part (with two terms for M and
+// h, 16 bits, y's were bf16 neighbours of what fp32 gives at one place in a
+// thousand; the third costs 1 to 4%).  fp32 calls run on the fp32 matrix
+// instructions instead.  States, sums and exponents are
 // fp32; the running sums c_i are added in fp64 and used as differences, which
 // are rounded to fp32 only then (c_i itself, up to some hundreds, would be off
 // by 1e-5, and so would every decay): where fp32 results depend on them, two
@@ -687,16 +689,16 @@ SEQ_DEV void tri_tile(int t, int &it, int &jt)
 template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd_kernel(ScanParams p)
 {
     constexpr int Q = Frag<T>::Q, NT = SP / 16, NI = Q / 16, TRI = NI * (NI + 1) / 2, TPW = (TRI + 3) / 4;
-    constexpr int NM = terms<T, 2>(), NX = terms<T, 3>(), MLD = Q + Frag<T>::PAD;
+    constexpr int NS = terms<T, 3>(), MLD = Q + Frag<T>::PAD;
     typedef Tile<T, Q, kPB> XT;
     typedef Tile<T, Q, SP> BT;
     typedef typename Frag<T>::type frag;
     __shared__ __align__(16) T sX[Q * XT::LD];
     __shared__ __align__(16) T sB[Q * BT::LD];
     __shared__ __align__(16) T sC[Q * BT::LD];
-    __shared__ __align__(16) T sM[NM * Q * MLD];
-    __shared__ __align__(16) float sCum[4][Q], sLow[4][Q], sDt[4][Q], sW[4][Q], sE[4][Q];     // of four chunks: c_i, its low
-                                                                        // part, dt, e^{c_Q - c_j} dt_j, e^{c_i}
+    __shared__ __align__(16) T sM[NS * Q * MLD];
+    // of four chunks: c_i, its low part, dt, e^{c_Q - c_j} dt_j (e^{c_i} besides would leave room for one workgroup only)
+    __shared__ __align__(16) float sCum[4][Q], sLow[4][Q], sDt[4][Q], sW[4][Q];
     const int lane = threadIdx.x & 63, w = wave_id(), q = lane >> 4;
     const int64_t unit = blockIdx.x / p.nseg;
     const int seg = (int)(blockIdx.x - unit * p.nseg);
@@ -731,7 +733,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
         return *reinterpret_cast<const f32x4 *>(v + col * SP + t * 16 + q * 4);
     });
     // the tiles of M above the diagonal that a reduction over 32 tokens meets
-    for (int e = threadIdx.x; e < NM * Q * MLD; e += 256) sM[e] = (T)0.0f;
+    for (int e = threadIdx.x; e < NS * Q * MLD; e += 256) sM[e] = (T)0.0f;
 
     XT xt;
     BT bt, ct;
@@ -754,7 +756,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
     for (int c = c_lo; c < c_live; ++c) {
         const int64_t t0 = (int64_t)c * Q;
         const int slot = (c - c_lo) & 3;
-        const float *cum_ = sCum[slot], *low_ = sLow[slot], *dt_ = sDt[slot], *w_ = sW[slot], *e_ = sE[slot];
+        const float *cum_ = sCum[slot], *low_ = sLow[slot], *dt_ = sDt[slot], *w_ = sW[slot];
         __syncthreads();
         xt.store(sX);
         bt.store(sB);
@@ -769,7 +771,6 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
                 sCum[w][lane] = (float)cum;
                 sLow[w][lane] = (float)(cum - (double)(float)cum);
                 sW[w][lane] = exp2_fast((float)(tot - cum)) * dt;
-                sE[w][lane] = exp2_fast((float)cum);
             }
             fetch_dt(c + 4 + w);
         }
@@ -799,14 +800,14 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
                     for (int ks = 0; ks < KN; ++ks) s = mma(bf[ks], cf[ks], s);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) s[r] = i >= j + r ? s[r] * exp2_fast(ex[r]) * dj[r] : 0.0f;
-                    write_split4<NM>(sM + i * MLD + j, Q * MLD, s);
+                    write_split4<NS>(sM + i * MLD + j, Q * MLD, s);
                 }
             }
         }
         __syncthreads();
         if (busy) {
             constexpr int KQ = Q / 32, KN = SP / 32;
-            frag xf[KQ], cf[2][NI], mf[NI][NM], bf[NT];
+            frag xf[KQ], cf[2][NI], mf[NI][NS], bf[NT];
             f32x4 y[NI];
             auto read_c = [&](int ks) __attribute__((always_inline)) {
 #pragma unroll
@@ -816,7 +817,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
 #pragma unroll
                 for (int it = 2 * ks; it < NI; ++it)
 #pragma unroll
-                    for (int m = 0; m < NM; ++m) mf[it][m] = read_rows(sM + m * Q * MLD, MLD, it * 16, ks * 32, lane);
+                    for (int m = 0; m < NS; ++m) mf[it][m] = read_rows(sM + m * Q * MLD, MLD, it * 16, ks * 32, lane);
             };
             auto read_b = [&](int ks) __attribute__((always_inline)) {
 #pragma unroll
@@ -839,17 +840,19 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
                 float v[8];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = st[2 * ks][e], v[4 + e] = st[2 * ks + 1][e];
-                Split<T, NX> hs;
+                Split<T, NS> hs;
                 make_split(v, hs);
 #pragma unroll
-                for (int m = 0; m < NX; ++m)
+                for (int m = 0; m < NS; ++m)
 #pragma unroll
                     for (int it = 0; it < NI; ++it) y[it] = mma(cf[ks & 1][it], hs.f[m], y[it]);
                 in_order();
             }
 #pragma unroll
-            for (int it = 0; it < NI; ++it) y[it] *= *reinterpret_cast<const f32x4 *>(e_ + it * 16 + q * 4);
-            const float dec = e_[Q - 1];
+            for (int it = 0; it < NI; ++it)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) y[it][r] *= exp2_fast(cum_[it * 16 + q * 4 + r]);
+            const float dec = exp2_fast(cum_[Q - 1]);
 #pragma unroll
             for (int t = 0; t < NT; ++t) st[t] *= dec;
             T xr[NI][4];
@@ -861,13 +864,13 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
                 const f32x4 w1 = *reinterpret_cast<const f32x4 *>(w_ + ks * 32 + q * 8 + 4);
                 in_order();
 #pragma unroll
-                for (int m = 0; m < NM; ++m)
+                for (int m = 0; m < NS; ++m)
 #pragma unroll
                     for (int it = 2 * ks; it < NI; ++it) y[it] = mma(mf[it][m], xf[ks], y[it]);
                 float v[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = frag_get(xf[ks], e) * (e < 4 ? w0[e & 3] : w1[e & 3]);
-                Split<T, NX> xs;
+                Split<T, NS> xs;
                 make_split(v, xs);
                 in_order();
                 if (ks + 1 < KQ) {
@@ -880,7 +883,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
                 }
                 in_order();
 #pragma unroll
-                for (int m = 0; m < NX; ++m)
+                for (int m = 0; m < NS; ++m)
 #pragma unroll
                     for (int t = 0; t < NT; ++t) st[t] = mma(bf[t], xs.f[m], st[t]);
             }

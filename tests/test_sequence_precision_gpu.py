@@ -74,3 +74,18 @@ def test_a_state_enters_y_with_all_its_bits(P, S, dtype):
     mag, _ = seq.scan(**v, softplus=False, magnitude=True)
     assert (y.abs() < 2.0 ** -22 * mag).all()
     _near(_scan(N, 1, H, P, 1, S, dtype)(**_gpu(v)), y, mag, HALF[dtype], 2.0 ** -20, "y")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("P,S", SHAPES)
+def test_tokens_enter_y_with_all_bits_of_their_weights(P, S, dtype):
+    """y = sum_j (C_i . B_j) e^(c_i - c_j) dt_j x_j over three tokens: of many results some nearly cancel."""
+    g = torch.Generator().manual_seed(2)
+    N, L, H, t = 48, 3, 32, TYPE[dtype]
+    v = dict(x=torch.randn(N, L, H, P, generator=g).to(t), dt=(0.1 + torch.rand(N, L, H, generator=g)).to(t),
+             A=-torch.rand(H, generator=g) - 0.1, B=_two_states(g, S, N, L, 1).to(t), C=_two_states(g, S, N, L, 1).to(t),
+             D=torch.randn(H, generator=g))
+    y, _ = seq.scan(**v, softplus=False)
+    mag, _ = seq.scan(**v, softplus=False, magnitude=True)
+    assert (y.abs() < 2.0 ** -12 * mag).sum() > 10
+    _near(_scan(N, L, H, P, 1, S, dtype)(**_gpu(v)), y, mag, HALF[dtype], 2.0 ** -20, "y")
