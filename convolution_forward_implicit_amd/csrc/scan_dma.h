@@ -261,14 +261,15 @@ template <int SP> struct FwdDmaShared {
     static constexpr int STAGE = Ring<kPB>::BYTES + 2 * Ring<SP>::BYTES;
     __align__(1024) unsigned char ring[kStages * STAGE];       // C, B, x of a chunk
     __align__(16) float y[2][64 * kPB];         // y' of a chunk: token i, piece c of four channels at c ^ i % 16
-    __align__(16) float cum[3][64], dt[3][64], w[3][64];    // of three chunks: c_i, dt_i, e^{c_Q - c_i} dt_i
+    __align__(16) float cum[3][64], low[3][64], dt[3][64], w[3][64];    // of three chunks: c_i, its low part, dt_i,
+                                                                        // e^{c_Q - c_i} dt_i
 };
 
 // A score wave's chunk: y'' of the tokens 16 IT .., in results of spread channels:
 // y[2h] and y[2h + 1] hold token lane % 16's channels 32h + 8q .. +3 and +4 .. +7.
 template <int SP, int IT>
-SEQ_DEV void score_rows(const bf16_t *sC, const bf16_t *sB, const bf16_t *sX, const float *cum, const float *dt, float skip,
-                        int lane, f32x4 (&y)[4])
+SEQ_DEV void score_rows(const bf16_t *sC, const bf16_t *sB, const bf16_t *sX, const float *cum, const float *low,
+                        const float *dt, float skip, int lane, f32x4 (&y)[4])
 {
     typedef Ring<SP> BR;
     typedef Ring<kPB> XR;
@@ -283,11 +284,12 @@ SEQ_DEV void score_rows(const bf16_t *sC, const bf16_t *sB, const bf16_t *sX, co
 #pragma unroll
     for (int ks = 0; ks < KN; ++ks) cf[ks] = BR::rows(sC, IT * 16, ks * 32, lane);
     read_b(0);
-    const float ci = cum[i];
+    const float ci = cum[i], li = low[i];
     f32x4 ex[IT + 1], dj[IT + 1];
 #pragma unroll
     for (int jt = 0; jt <= IT; ++jt) {
-        ex[jt] = ci - *reinterpret_cast<const f32x4 *>(cum + jt * 16 + q * 4);
+        ex[jt] = (ci - *reinterpret_cast<const f32x4 *>(cum + jt * 16 + q * 4)) +
+                 (li - *reinterpret_cast<const f32x4 *>(low + jt * 16 + q * 4));
         dj[jt] = *reinterpret_cast<const f32x4 *>(dt + jt * 16 + q * 4);
     }
 #pragma unroll
@@ -379,6 +381,7 @@ template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(Sca
         chunk_decay(raw, k < steps && (int64_t)(c_lo + k) * Q + lane < len, a, p.softplus, dt, cum);
         const double tot = wave_last(cum);
         sh.cum[to][lane] = (float)cum;
+        sh.low[to][lane] = (float)(cum - (double)(float)cum);
         sh.dt[to][lane] = dt;
         sh.w[to][lane] = exp2_fast((float)(tot - cum)) * dt;
     };
@@ -564,13 +567,13 @@ template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(Sca
             if (k > 0) finish(k - 1, lane);
             if (it == 0 && k + 2 < steps) issue(k + 2);       // over chunk k - 1, which all waves are done with
             const bf16_t *sC = (const bf16_t *)(sh.ring + stage), *sB = sC + BR::BYTES / 2, *sX = sB + BR::BYTES / 2;
-            const float *cum = sh.cum[slot], *dt = sh.dt[slot];
+            const float *cum = sh.cum[slot], *low = sh.low[slot], *dt = sh.dt[slot];
             stage = next_stage(stage, STAGE);
             slot = slot == 2 ? 0 : slot + 1;
-            if (it == 0) score_rows<SP, 0>(sC, sB, sX, cum, dt, skip, lane, y);
-            else if (it == 1) score_rows<SP, 1>(sC, sB, sX, cum, dt, skip, lane, y);
-            else if (it == 2) score_rows<SP, 2>(sC, sB, sX, cum, dt, skip, lane, y);
-            else score_rows<SP, 3>(sC, sB, sX, cum, dt, skip, lane, y);
+            if (it == 0) score_rows<SP, 0>(sC, sB, sX, cum, low, dt, skip, lane, y);
+            else if (it == 1) score_rows<SP, 1>(sC, sB, sX, cum, low, dt, skip, lane, y);
+            else if (it == 2) score_rows<SP, 2>(sC, sB, sX, cum, low, dt, skip, lane, y);
+            else score_rows<SP, 3>(sC, sB, sX, cum, low, dt, skip, lane, y);
             if ((k & 1) && decaying) {      // chunks k + 1 and k + 2: the slots that are neither k's
                 decays(k + it, it == 1 ? slot : slot == 2 ? 0 : slot + 1);
                 fetch_dt(k + 2 + it);

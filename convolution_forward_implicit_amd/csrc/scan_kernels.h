@@ -33,8 +33,8 @@
 // instructions instead.  States, sums and exponents are
 // fp32; the running sums c_i are added in fp64 and used as differences, which
 // are rounded to fp32 only then (c_i itself, up to some hundreds, would be off
-// by 1e-5, and so would every decay): where fp32 results depend on them, two
-// fp32 numbers stand for c_i.
+// by 1e-5, and so would every decay; behind a token whose step clears the state
+// it may be any number): two fp32 numbers stand for c_i.
 //
 // Fragments (16x16 blocks, 64 lanes, q = lane / 16): an operand's lane holds 8
 // values of the reduction for row (or column) lane % 16, a result's lane four
@@ -792,8 +792,8 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
                     }
                     const int i = it * 16 + (lane & 15), j = jt * 16 + q * 4;
                     const f32x4 dj = *reinterpret_cast<const f32x4 *>(dt_ + j);
-                    f32x4 ex = cum_[i] - *reinterpret_cast<const f32x4 *>(cum_ + j);
-                    if (sizeof(T) == 4) ex += low_[i] - *reinterpret_cast<const f32x4 *>(low_ + j);   // y is fp32
+                    const f32x4 ex = (cum_[i] - *reinterpret_cast<const f32x4 *>(cum_ + j)) +
+                                     (low_[i] - *reinterpret_cast<const f32x4 *>(low_ + j));
                     in_order();
                     f32x4 s = {0, 0, 0, 0};
 #pragma unroll

@@ -89,3 +89,22 @@ def test_tokens_enter_y_with_all_bits_of_their_weights(P, S, dtype):
     mag, _ = seq.scan(**v, softplus=False, magnitude=True)
     assert (y.abs() < 2.0 ** -12 * mag).sum() > 10
     _near(_scan(N, L, H, P, 1, S, dtype)(**_gpu(v)), y, mag, HALF[dtype], 2.0 ** -20, "y")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("P,S", SHAPES)
+def test_tokens_behind_one_that_clears_the_state(P, S, dtype):
+    """A step of 2^12 forgets all before it; the decays between the tokens behind it are as exact as without it."""
+    g = torch.Generator().manual_seed(3)
+    N, L, H, t = 4, 6, 8, TYPE[dtype]
+    dt = torch.randint(1, 32, (N, L, H), generator=g) / 64
+    dt[:, 1] = 4096.0
+    v = dict(x=torch.randn(N, L, H, P, generator=g).to(t), dt=dt.to(t), A=-torch.rand(H, generator=g) - 1,
+             B=_two_states(g, S, N, L, 1).to(t), C=_two_states(g, S, N, L, 1).to(t))
+    v["x"][:, 1:3] = 0      # of three tokens, one before the step and two behind it
+    v["x"][:, 5] = 0
+    y, last = seq.scan(**v, softplus=False)
+    mag, top = seq.scan(**v, softplus=False, magnitude=True)
+    out = torch.empty(N, H, P, S, device=DEV)
+    _near(_scan(N, L, H, P, 1, S, dtype)(**_gpu(v), state_out=out), y, mag, HALF[dtype], 2.0 ** -20, "y")
+    _near(out, last, top, HALF["f32"], 2.0 ** -20, "state_out")
