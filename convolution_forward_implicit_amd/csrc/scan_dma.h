@@ -519,7 +519,7 @@ template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(Sca
     } else {
         const int it = w - 4;
         f32x4 y[4];
-        // rows behind the sequence come out as zeros: x and C are zeros there
+        // rows behind the sequence come out as zeros, whatever the state times zero is
         auto finish = [&](int k, int lane) __attribute__((always_inline)) {
             const int q = lane >> 4, l16 = lane & 15, i = it * 16 + l16;
             const int64_t t0 = (int64_t)(c_lo + k) * Q;
@@ -539,6 +539,7 @@ template <int SP> __global__ void __launch_bounds__(512) scan_fwd_dma_kernel(Sca
 #pragma unroll
                     for (int r = 0; r < 4; ++r) o[m * 4 + r] = (bf16_t)v[r];
                 }
+                if (t0 + i >= len) o = bf16x8{0, 0, 0, 0, 0, 0, 0, 0};
                 const uint32_t to = col < pcols ? (uint32_t)(i * (int)p.y_ld + col) * 2 : kOutOfRange;
                 __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), buf, to, 0, kStream);
             }

@@ -317,13 +317,18 @@ template <typename T, int ROWS, int COLS, int THREADS = 256> struct Tile {
         for (int k = 0; k < NV; ++k)
             if (mine()) *reinterpret_cast<u32x4 *>(p + k * kStep * LD) = v[k];
     }
-    // from LDS to memory
-    static SEQ_DEV void write(const T *lds, T *g, int64_t ld, int rows, int cols, bool vec)
+    // from LDS to memory, zeros in the rows from `live` on (what was computed there
+    // is zero times a state, which need not be finite)
+    static SEQ_DEV void write(const T *lds, T *g, int64_t ld, int live, int rows, int cols, bool vec)
     {
         Tile t;
-        const T *p = lds + threadIdx.x / CV * LD + column();
+        const int r = threadIdx.x / CV;
+        const T *p = lds + r * LD + column();
 #pragma unroll
-        for (int k = 0; k < NV; ++k) t.v[k] = mine() ? *reinterpret_cast<const u32x4 *>(p + k * kStep * LD) : u32x4{0, 0, 0, 0};
+        for (int k = 0; k < NV; ++k) {
+            t.v[k] = u32x4{0, 0, 0, 0};
+            if (mine() && r + k * kStep < live) t.v[k] = *reinterpret_cast<const u32x4 *>(p + k * kStep * LD);
+        }
         t.put(g, ld, rows, cols, vec);
     }
     static SEQ_DEV void write_zeros(T *g, int64_t ld, int rows, int cols, bool vec)
@@ -895,8 +900,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
                     sX[(it * 16 + q * 4 + r) * XT::LD + col] = (T)fmaf(skip, (float)xr[it][r], y[it][r]);
         }
         __syncthreads();
-        // rows behind the sequence come out as zeros: x and C are zeros there
-        XT::write(sX, yg + t0 * p.y_ld, p.y_ld, (int)min((int64_t)Q, p.L - t0), pcols, p.vec);
+        XT::write(sX, yg + t0 * p.y_ld, p.y_ld, (int)min((int64_t)Q, len - t0), (int)min((int64_t)Q, p.L - t0), pcols, p.vec);
     }
     for (int c = max(c_lo, c_live); c < c_hi; ++c) {
         const int64_t t0 = (int64_t)c * Q;
@@ -1311,7 +1315,8 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
         if (w == 6 && k + 1 < blocks && (k + 1) % p.NPB == 0) decays(k + 1);
         __syncthreads();
         const int64_t base = fresh_scalar(base_);
-        XT::write(sh.x, (T *)p.dx + base * p.dx_ld + (int64_t)h * p.P + pb * kPB, p.dx_ld, all_rows, pcols, p.vec);
+        XT::write(sh.x, (T *)p.dx + base * p.dx_ld + (int64_t)h * p.P + pb * kPB, p.dx_ld, rows, all_rows,
+                  pcols, p.vec);
     }
     if (w == 7) finish(blocks - 1);
     // the parts of dB and dC inside the chunk, from the sum of dS over the heads
@@ -1348,6 +1353,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
         for (int r = 0; r < 4; ++r) {
             const int row = (it0 + i) * 16 + q * 4 + r;
             if (row >= all_rows) continue;
+            if (row >= rows) dB[i][r] = dC[i][r] = 0.0f;
             if (p.slices == 1) {
                 ((T *)p.db)[(base_ + row) * p.db_ld + g * p.S + s] = (T)dB[i][r];
                 ((T *)p.dc)[(base_ + row) * p.dc_ld + g * p.S + s] = (T)dC[i][r];

@@ -437,10 +437,12 @@ const char *conv_causal_describe(const conv_causal_plan_t *plan);
  * meant to be negative and dt not; nothing checks it, and a decay that exceeds
  * 1 grows as the formula says.  d, dt_bias, state, lengths and state_out are
  * optional (NULL: 0, 0, zeros, all L, not written).  lengths as conv_causal:
- * rows behind a length are not read, their y are zeros and the state stays.
- * States and sums are fp32.  Tokens are taken in chunks, so a NaN or an
- * infinity in a token's inputs may reach every y of its chunk (64 tokens in
- * bf16, 32 in fp32), not only those behind it.  S <= 128, P <= 65536.
+ * rows behind a length are not read, their y and gradients are zeros and the
+ * state stays.  States and sums are fp32.  Tokens are taken in chunks, so a NaN
+ * or an infinity in a token's inputs may reach the y of all its sequence's
+ * tokens in its chunk (64 tokens in bf16, 32 in fp32), not only those behind
+ * it, and an infinity, of a state too, may come out as a NaN.  S <= 128,
+ * P <= 65536.
  *
  * Long sequences of few heads are split into segments whose states go through a
  * caller-owned device workspace (16-byte aligned; the size may be 0, then it
