@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(256) causal_bwd_kernel(CausalParams p)
             const bool in = t0 + u < len;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                float g = in ? pack_get<T, V>(dy[u], i) : 0.0f;
+                float g = pack_get<T, V>(dy[u], i);
                 if (SILU) {
                     float v = b[i];
 #pragma unroll
@@ -234,11 +234,16 @@ __global__ void __launch_bounds__(256) causal_bwd_kernel(CausalParams p)
                     const float s = sigmoid(v);
                     g *= s * (1.0f + v * (1.0f - s));
                 }
-                d[F - 1][i] = g;
-                if (u < kConvBwdRun) {
-                    db[i] += g;
+                d[F - 1][i] = in ? g : 0.0f;
+            }
+            // no term where there is no token: zero times a row of the state or of the
+            // last tokens is not zero if that is not finite
+            if (u < kConvBwdRun && in) {
 #pragma unroll
-                    for (int k = 0; k < F; ++k) dw[k][i] = fmaf(g, h.get(u + k, i), dw[k][i]);
+                for (int i = 0; i < V; ++i) {
+                    db[i] += d[F - 1][i];
+#pragma unroll
+                    for (int k = 0; k < F; ++k) dw[k][i] = fmaf(d[F - 1][i], h.get(u + k, i), dw[k][i]);
                 }
             }
             // dh at s = t - (F-1), once d[s .. s+F-1] is known

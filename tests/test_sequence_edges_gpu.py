@@ -60,3 +60,41 @@ def test_rows_behind_a_sequence_are_zeros_whatever_comes_before(dims, dtype):
     assert torch.equal(got[1], y[1])
     for k in ("dx", "ddt", "dB", "dC", "dstate"):
         assert torch.equal(gbad[k][1], grads[k][1]), k
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("C", [16, 21])
+def test_an_empty_sequence_adds_nothing_to_the_convolutions_gradient(C, dtype):
+    """... whatever its state holds: no token reads it, and it is handed on."""
+    g = torch.Generator().manual_seed(5)
+    N, L, F, t = 3, 20, 4, TYPE[dtype]
+    r = lambda *s: torch.randn(*s, generator=g).to(t)
+    v = dict(x=r(N, L, C), w=r(C, F), bias=r(C), state=r(N, F - 1, C))
+    dy, dlast = r(N, L, C), r(N, F - 1, C)
+    n = torch.tensor([20, 0, 7], dtype=torch.int32)
+    bad = dict(v, state=v["state"].clone())
+    bad["state"][1] = float("nan")
+    p = _conv(N, L, C, F, dtype, has_bias=True, silu=True)
+    back = lambda a: p.backward(dy.to(DEV), **_gpu(a), lengths=n.to(DEV), dstate_out=dlast.to(DEV))
+    want, got = back(v), back(bad)
+    for k in ("dx", "dw", "dbias", "dstate"):
+        assert torch.equal(got[k], want[k]), k
+    assert torch.equal(got["dstate"][1].cpu(), dlast[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("C", [16, 21])
+def test_a_last_token_reaches_only_the_tap_that_reads_it(C, dtype):
+    """Without an activation: NaN in a sequence's last token meets w[F-1] alone, the tokens behind it are no terms."""
+    g = torch.Generator().manual_seed(6)
+    N, L, F, t = 2, 40, 4, TYPE[dtype]
+    r = lambda *s: torch.randn(*s, generator=g).to(t)
+    v = dict(x=r(N, L, C), w=r(C, F))
+    dy = r(N, L, C).to(DEV)
+    n = torch.tensor([18, 40], dtype=torch.int32, device=DEV)
+    bad = dict(v, x=v["x"].clone())
+    bad["x"][0, 17] = float("nan")
+    p = _conv(N, L, C, F, dtype)
+    want, got = p.backward(dy, **_gpu(v), lengths=n), p.backward(dy, **_gpu(bad), lengths=n)
+    assert torch.equal(got["dx"], want["dx"])
+    assert torch.equal(got["dw"][:, :F - 1], want["dw"][:, :F - 1]) and torch.isnan(got["dw"][:, F - 1]).all()
