@@ -41,6 +41,9 @@ namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 30;
 constexpr double kMaxBytes = 9.0e18;
+constexpr double kMaxThreads = 4294967296.0;     // a launch has fewer threads than this
+
+bool one_launch(double workgroups, int threads) { return workgroups * threads < kMaxThreads; }
 
 conv_status_t launched()
 {
@@ -185,10 +188,13 @@ int64_t bwd_blocks(const conv_causal_desc_t &d)   // workgroups along a sequence
     return std::max<int64_t>(1, (d.L + per - 1) / per);
 }
 
+int64_t channel_blocks(int64_t vectors) { return (vectors + 63) / 64; }   // workgroups across the channels
+
 // ---- scan ------------------------------------------------------------------------
-// Where the gradients of A, dt_bias and D go.
+// Where the gradients of A, dt_bias and D go, and the workgroups that add them up.
 struct HeadGrads {
     float *da, *dbias, *dd;
+    int64_t workgroups;
 };
 
 template <typename T, int SP, bool STORE> void launch_states(const ScanParams &p, int64_t grid, hipStream_t s)
@@ -223,6 +229,13 @@ template <typename T, int SP> void launch_fwd(const ScanParams &p, int64_t units
     hipLaunchKernelGGL((scan_fwd_kernel<T, SP>), grid, dim3(256), 0, s, p);
 }
 
+// of scan_reduce_kernel: three sums of each head, and elements of dB and dC where the heads are sliced
+int64_t scan_reduce_grid(const conv_scan_plan &pl)
+{
+    const conv_scan_desc_t &d = pl.desc;
+    return 3 * d.H + (pl.slices > 1 ? (d.N * d.L * d.G * pl.SP + 255) / 256 : 0);
+}
+
 template <typename T, int SP> void launch_bwd(ScanParams p, int64_t units, HeadGrads g, hipStream_t s)
 {
     if (p.N > 0) {
@@ -232,9 +245,8 @@ template <typename T, int SP> void launch_bwd(ScanParams p, int64_t units, HeadG
         const int64_t grid = (int64_t)p.N * p.K * p.G * p.slices;
         hipLaunchKernelGGL((scan_bwd_kernel<T, SP>), dim3((unsigned)grid), dim3(512), 0, s, p);
     }
-    const int64_t elems = p.slices > 1 ? (int64_t)p.N * p.L * p.G * SP : 0;
-    hipLaunchKernelGGL((scan_reduce_kernel<T, SP>), dim3((unsigned)(3 * p.H + (elems + 255) / 256)), dim3(256), 0, s, p,
-                       g.da, g.dbias, g.dd);       // no sequences: zeros
+    hipLaunchKernelGGL((scan_reduce_kernel<T, SP>), dim3((unsigned)g.workgroups), dim3(256), 0, s, p, g.da, g.dbias,
+                       g.dd);       // no sequences: zeros
 }
 
 template <typename T> void launch_scan(int SP, const ScanParams &p, int64_t units, const HeadGrads *g, hipStream_t s)
@@ -259,6 +271,19 @@ Segments split_segments(int64_t units, int64_t K, int64_t want, int64_t fine)
     const int64_t whole = (K + n - 1) / n, sub = n == 1 ? 1 : std::max<int64_t>(1, std::min(fine, whole / 16));
     const int64_t chunks = (whole + sub - 1) / sub, count = (K + chunks * sub - 1) / (chunks * sub) * sub;
     return {(int)count, (int)chunks, (int)sub};
+}
+
+// A step's lanes for the states of a channel, and workgroups for the channels of a head.
+struct StepShape {
+    int lanes, blocks;
+};
+
+StepShape step_shape(const conv_scan_desc_t &d)
+{
+    int lanes = 1;
+    while (lanes * 4 < d.S) lanes *= 2;
+    const int64_t per = 4 * kStepRows * (64 / lanes);
+    return {lanes, (int)((d.P + per - 1) / per)};
 }
 
 void scan_params(const conv_scan_plan &pl, ScanParams *p)
@@ -298,11 +323,14 @@ conv_status_t conv_causal_create(const conv_causal_desc_t *desc, conv_causal_pla
                     (long long)d.N, (long long)d.L, (long long)d.C, (long long)d.F);
     if (d.F > 8) return fail(CONV_ERR_UNSUPPORTED, "more than 8 taps (F = %lld)", (long long)d.F);
     if (d.N > kMaxDim || d.L > kMaxDim || d.C > kMaxDim) return fail(CONV_ERR_UNSUPPORTED, "N, L or C above 2^30");
-    // a workgroup: 64 channels at least of four runs; in a step 256 channels
-    const double fwd = (double)d.N * ((double)((d.L + kConvRun - 1) / kConvRun + 1) / kConvRuns + 1) * (double)((d.C + 63) / 64);
-    const double wgs = (double)d.N * (double)bwd_blocks(d) * (double)((d.C + 63) / 64);
+    // What neither a prompt nor a step could launch, whole vectors taken where the channels allow them; every call
+    // checks its own form.
+    const int64_t e = d.dtype == CONV_DT_BF16 ? 2 : 4, vectors = d.C * e % 16 == 0 ? d.C * e / 16 : d.C;
+    const int64_t runs = (d.L + kConvRun - 1) / kConvRun;
+    const double fwd = (double)d.N * (double)((runs + kConvRuns - 1) / kConvRuns) * (double)channel_blocks(vectors);
+    const double step = (double)d.N * (double)vectors / 256;
     const double ws = (double)d.N * (double)bwd_blocks(d) * (double)(d.F + 1) * (double)d.C * 4.0;
-    if (fwd >= 2147483000.0 || wgs >= 2147483000.0 || ws >= kMaxBytes)
+    if ((!one_launch(fwd, 256) && !one_launch(step, 256)) || ws >= kMaxBytes)
         return fail(CONV_ERR_UNSUPPORTED, "N x L x C is too large for one launch");
     conv_causal_plan *pl = new (std::nothrow) conv_causal_plan();
     if (!pl) return fail(CONV_ERR_NOMEM, "plan allocation failed");
@@ -353,7 +381,8 @@ static conv_status_t causal_forward(const conv_causal_plan_t *plan, const conv_c
     p.N = (int)d.N; p.C = (int)d.C; p.CV = (int)(d.C / V); p.L = L;
     p.blocks = (L + kConvRun - 1) / kConvRun;
     const int64_t runs = p.blocks + (a->state_out ? 1 : 0);
-    const int64_t grid = step ? (d.N * p.CV + 255) / 256 : d.N * ((runs + kConvRuns - 1) / kConvRuns) * ((p.CV + 63) / 64);
+    const int64_t grid = step ? (d.N * p.CV + 255) / 256 : d.N * ((runs + kConvRuns - 1) / kConvRuns) * channel_blocks(p.CV);
+    if (!one_launch((double)grid, 256)) return fail(CONV_ERR_UNSUPPORTED, "N x L x C is too large for one launch");
     (void)hipGetLastError();
     launch_causal(step ? CONV_STEP : CONV_RUN, d, V, p, grid, (hipStream_t)stream);
     return launched();
@@ -415,11 +444,13 @@ conv_status_t conv_causal_bwd_run(const conv_causal_plan_t *plan, const conv_cau
     p.x_ld = stride(in[1]); p.dy_ld = stride(in[0]); p.dx_ld = stride(out[0]);
     p.N = (int)d.N; p.C = (int)d.C; p.CV = (int)(d.C / V); p.L = d.L;
     p.blocks = bwd_blocks(d);
+    const int64_t wgs = plan->bwd_rows * channel_blocks(p.CV), sums = (d.F + 1) * channel_blocks(d.C);
+    if (!one_launch((double)wgs, 256) || !one_launch((double)sums, 256))
+        return fail(CONV_ERR_UNSUPPORTED, "N x L x C is too large for one launch");
     (void)hipGetLastError();
     hipStream_t s = (hipStream_t)stream;
-    if (d.N > 0)
-        launch_causal(CONV_BWD, d, V, p, plan->bwd_rows * ((p.CV + 63) / 64), s);
-    const dim3 grid((unsigned)((d.F + 1) * ((d.C + 63) / 64)));      // no rows: dw and dbias are zeros
+    if (d.N > 0) launch_causal(CONV_BWD, d, V, p, wgs, s);
+    const dim3 grid((unsigned)sums);      // no rows: dw and dbias are zeros
     if (d.dtype == CONV_DT_BF16)
         hipLaunchKernelGGL(causal_reduce_kernel<bf16_t>, grid, dim3(256), 0, s, p.partial, (bf16_t *)a->dw,
                            (bf16_t *)a->dbias, plan->bwd_rows, (int)d.C, (int)d.F);
@@ -459,11 +490,9 @@ conv_status_t conv_scan_create(const conv_scan_desc_t *desc, conv_scan_plan_t **
     pl->K = (int)std::max<int64_t>(1, (d.L + pl->Q - 1) / pl->Q);
     pl->NPB = (int)((d.P + kPB - 1) / kPB);
     const double units = (double)d.N * d.H * pl->NPB, tile = (double)pl->SP * kPB * 4;
-    const double grids = std::max(2 * units * std::max<double>(pl->K, 32), (double)d.N * pl->K * d.H);
     const double rows = (double)d.N * d.L * d.G * pl->SP;
-    // no grid is larger than one workgroup per unit and chunk, or per 256 elements of dB
-    if (grids >= 2147483000.0 || rows / 256.0 + 3.0 * d.H >= 2147483000.0 || units * (pl->K + 1) * tile * 4 >= kMaxBytes ||
-        3.0 * d.H >= 2147483000.0) {
+    // What neither a prompt (a workgroup of 64 channels at least) nor a step could launch; every call checks its own.
+    if ((!one_launch(units, 256) && !one_launch((double)d.N * d.H * step_shape(d).blocks, 256)) || rows * 4 >= kMaxBytes || units * (pl->K + 1) * tile * 4 >= kMaxBytes) {
         delete pl;
         return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
     }
@@ -574,10 +603,11 @@ static conv_status_t scan_forward(const conv_scan_plan_t *plan, const conv_scan_
     hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
     if (step) {
-        int lpr = 1;
-        while (lpr * 4 < d.S) lpr *= 2;
-        const int per = 4 * kStepRows * (64 / lpr), blocks = (int)((d.P + per - 1) / per);
+        const StepShape shape = step_shape(d);
+        const int lpr = shape.lanes, blocks = shape.blocks;
         const bool vec = d.S % 4 == 0 && ((uintptr_t)a->state | (uintptr_t)a->state_out) % 16 == 0;
+        if (!one_launch((double)(d.N * d.H * blocks), 256))
+            return fail(CONV_ERR_UNSUPPORTED, "N x H x P is too large for one launch");
         const dim3 grid((unsigned)(d.N * d.H * blocks));
         if (d.dtype == CONV_DT_BF16) {
             if (vec) hipLaunchKernelGGL((scan_step_kernel<bf16_t, true>), grid, dim3(256), 0, s, p, lpr, blocks);
@@ -594,7 +624,11 @@ static conv_status_t scan_forward(const conv_scan_plan_t *plan, const conv_scan_
     }
     const Rows vec[] = {in[0], in[1], in[2], out[0]};
     p.vec = scan_vector(*plan, vec, 4);
-    set_segments(&p, p.vec && d.dtype == CONV_DT_BF16 ? plan->dma : plan->fwd);
+    const bool dma = p.vec && d.dtype == CONV_DT_BF16;
+    set_segments(&p, dma ? plan->dma : plan->fwd);
+    if (!one_launch((double)(plan->units * (p.nseg - p.sub)), 256) ||
+        !one_launch((double)(plan->units * (p.nseg / p.sub)), dma ? 512 : 256))
+        return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
     if (d.dtype == CONV_DT_BF16) launch_scan<bf16_t>(plan->SP, p, plan->units, nullptr, s);
     else launch_scan<float>(plan->SP, p, plan->units, nullptr, s);
     return launched();
@@ -658,6 +692,10 @@ conv_status_t conv_scan_bwd_run(const conv_scan_plan_t *plan, const conv_scan_bw
     p.vec = scan_vector(*plan, vec, 5);
     char *ws = (char *)workspace;
     set_segments(&p, plan->bwd);
+    const HeadGrads g = {a->da, a->ddt_bias, a->dd, scan_reduce_grid(*plan)};
+    if (!one_launch((double)(2 * plan->units * p.nseg), 256) || !one_launch((double)(d.N * plan->K * d.G * plan->slices), 512) ||
+        !one_launch((double)g.workgroups, 256))
+        return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
     for (int k = 0; k < 2; ++k) {
         p.seg_state[k] = (float *)(ws + plan->o_seg[k]);
         p.seg_log[k] = (float *)(ws + plan->o_log[k]);
@@ -670,7 +708,6 @@ conv_status_t conv_scan_bwd_run(const conv_scan_plan_t *plan, const conv_scan_bw
     p.heads_per_slice = plan->heads_per_slice;
     hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
-    const HeadGrads g = {a->da, a->ddt_bias, a->dd};
     if (d.dtype == CONV_DT_BF16) launch_scan<bf16_t>(plan->SP, p, plan->units, &g, s);
     else launch_scan<float>(plan->SP, p, plan->units, &g, s);
     return launched();

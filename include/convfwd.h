@@ -371,7 +371,9 @@ const char *conv_bwd_weight_describe(const conv_bwd_weight_plan_t *plan);
  * accesses.  Outputs must not overlap inputs or each other (they may interleave
  * as column ranges of one matrix, i.e. with equal token strides).  Ownership,
  * threading, asynchrony and errors as conv_fwd; the current device is the
- * stream's and the tensors'. */
+ * stream's and the tensors'.  CONV_ERR_UNSUPPORTED, before anything is launched:
+ * rows of 32 MiB and more from token to token, and a call that would need 2^32
+ * threads (64 vectors, or elements, of 32 tokens take 256). */
 typedef struct {
     int32_t dtype;         /* conv_dtype_t                                     */
     int32_t has_bias;      /* 0 or 1                                           */
