@@ -110,10 +110,9 @@ class CausalConv(_Plan):
 
     def __init__(self, problem, dtype, has_bias=False, silu=False):
         self.problem = dict(problem)
-        self.dtype = dtype
+        self.dtype, dt = _dtype(dtype)
         self.has_bias, self.silu = bool(has_bias), bool(silu)
         N, L, C, F = (int(self.problem[k]) for k in ("N", "L", "C", "F"))
-        dt = capi.DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
         self._plan = capi.conv_causal_create(capi.conv_causal_desc_t(dt, self.has_bias, self.silu, 0, N, L, C, F))
         self.x_shape = (N, L, C)
         self.w_shape = (C, F)
@@ -211,10 +210,9 @@ class SelectiveScan(_Plan):
 
     def __init__(self, problem, dtype, softplus=True):
         self.problem = dict(problem)
-        self.dtype = dtype
+        self.dtype, dt = _dtype(dtype)
         self.softplus = bool(softplus)
         N, L, H, P, G, S = (int(self.problem[k]) for k in ("N", "L", "H", "P", "G", "S"))
-        dt = capi.DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
         self._plan = capi.conv_scan_create(capi.conv_scan_desc_t(dt, self.softplus, N, L, H, P, G, S))
         self.x_shape = (N, L, H, P)
         self.dt_shape = (N, L, H)
@@ -315,6 +313,12 @@ class SelectiveScan(_Plan):
         _with_workspace(torch, self.bwd_workspace_bytes, dev, away, lambda ws, n: capi.conv_scan_bwd_run(
             self._plan, byref(args), ws, n, stream))
         return got
+
+
+def _dtype(dtype):
+    """The name and the number of a type given by either; the library refuses a number it does not know."""
+    number = capi.DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
+    return next((k for k, v in capi.DTYPES.items() if v == number), dtype), number
 
 
 def _given(got, out, shapes):
