@@ -87,6 +87,8 @@ class _Plan:
                 # the handle alone: building the Stream object takes as long as a launch
                 return torch._C._cuda_getCurrentRawStream(dev.index), None
             stream = torch.cuda.current_stream(dev)
+        elif stream.device != dev:
+            raise ValueError("stream is of %s, the tensors are on %s" % (stream.device, dev))
         return stream.cuda_stream, torch.cuda.stream(stream)       # also makes its device the current one
 
     @staticmethod

@@ -19,3 +19,13 @@ def test_a_type_by_its_number_is_the_type_by_its_name(plan):
         plan(7)
     with pytest.raises((KeyError, ValueError, TypeError)):
         plan("f16")
+
+
+@pytest.mark.parametrize("plan", PLANS)
+def test_a_stream_of_another_device_is_refused(plan):
+    """... with stand-ins: the kernels would run there on tensors that are here."""
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 0
+
+    with pytest.raises(ValueError, match="cuda:1.*cuda:0"):
+        plan("bf16")._on(torch, torch.device("cuda", 0), Stream())
