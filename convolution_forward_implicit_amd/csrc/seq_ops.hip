@@ -571,7 +571,7 @@ static conv_status_t scan_forward(const conv_scan_plan_t *plan, const conv_scan_
     const int64_t L = step ? 1 : d.L, e = plan->esz, rows = d.N * L, need = step ? 0 : plan->ws_bytes;
     if (!a->a) return fail(CONV_ERR_INVALID_ARG, "a is NULL");
     if (step && a->lengths) return fail(CONV_ERR_INVALID_ARG, "a step takes no lengths");
-    const int64_t hp = d.H * d.P, gs = d.G * d.S;
+    const int64_t hp = d.H * d.P, gs = d.G * d.S, states = d.N * hp * d.S;
     const Rows in[] = {{"x", a->x, rows, hp, or_packed(a->x_ld, hp), e},
                        {"b", a->b, rows, gs, or_packed(a->b_ld, gs), e},
                        {"c", a->c, rows, gs, or_packed(a->c_ld, gs), e},
@@ -580,9 +580,9 @@ static conv_status_t scan_forward(const conv_scan_plan_t *plan, const conv_scan_
                        {"d", a->d, 1, d.H, d.H, 4},
                        {"dt_bias", a->dt_bias, 1, d.H, d.H, 4},
                        {"lengths", a->lengths, 1, d.N, std::max<int64_t>(1, d.N), 4},
-                       {"state", a->state, d.N * d.H, d.P * d.S, d.P * d.S, 4}};
+                       {"state", a->state, 1, states, states, 4}};
     const Rows out[] = {{"y", a->y, rows, hp, or_packed(a->y_ld, hp), e},
-                        {"state_out", a->state_out, d.N * d.H, d.P * d.S, d.P * d.S, 4},
+                        {"state_out", a->state_out, 1, states, states, 4},
                         {"workspace", ws, 1, need, std::max<int64_t>(1, need), 1}};
     conv_status_t st = check_rows(in, 9);
     if (st == CONV_OK) st = check_rows(out, 2);
@@ -650,7 +650,7 @@ conv_status_t conv_scan_bwd_run(const conv_scan_plan_t *plan, const conv_scan_bw
 {
     if (!plan || !a) return fail(CONV_ERR_INVALID_ARG, "plan or args is NULL");
     const conv_scan_desc_t &d = plan->desc;
-    const int64_t e = plan->esz, rows = d.N * d.L, hp = d.H * d.P, gs = d.G * d.S;
+    const int64_t e = plan->esz, rows = d.N * d.L, hp = d.H * d.P, gs = d.G * d.S, states = d.N * hp * d.S;
     if (!a->a || !a->da) return fail(CONV_ERR_INVALID_ARG, "a or da is NULL");
     if ((a->d != nullptr) != (a->dd != nullptr) || (a->dt_bias != nullptr) != (a->ddt_bias != nullptr))
         return fail(CONV_ERR_INVALID_ARG, "dd must be NULL iff d is, and ddt_bias iff dt_bias is");
@@ -663,8 +663,8 @@ conv_status_t conv_scan_bwd_run(const conv_scan_plan_t *plan, const conv_scan_bw
                        {"d", a->d, 1, d.H, d.H, 4},
                        {"dt_bias", a->dt_bias, 1, d.H, d.H, 4},
                        {"lengths", a->lengths, 1, d.N, std::max<int64_t>(1, d.N), 4},
-                       {"state", a->state, d.N * d.H, d.P * d.S, d.P * d.S, 4},
-                       {"dstate_out", a->dstate_out, d.N * d.H, d.P * d.S, d.P * d.S, 4}};
+                       {"state", a->state, 1, states, states, 4},
+                       {"dstate_out", a->dstate_out, 1, states, states, 4}};
     const Rows out[] = {{"dx", a->dx, rows, hp, or_packed(a->dx_ld, hp), e},
                         {"db", a->db, rows, gs, or_packed(a->db_ld, gs), e},
                         {"dc", a->dc, rows, gs, or_packed(a->dc_ld, gs), e},
@@ -672,7 +672,7 @@ conv_status_t conv_scan_bwd_run(const conv_scan_plan_t *plan, const conv_scan_bw
                         {"da", a->da, 1, d.H, d.H, 4},
                         {"dd", a->dd, 1, d.H, d.H, 4},
                         {"ddt_bias", a->ddt_bias, 1, d.H, d.H, 4},
-                        {"dstate", a->dstate, d.N * d.H, d.P * d.S, d.P * d.S, 4},
+                        {"dstate", a->dstate, 1, states, states, 4},
                         {"workspace", workspace, 1, plan->bwd_ws_bytes, std::max<int64_t>(1, plan->bwd_ws_bytes), 1}};
     conv_status_t st = check_rows(in, 11);
     if (st == CONV_OK) st = check_rows(out, 8);

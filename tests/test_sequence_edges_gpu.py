@@ -98,3 +98,38 @@ def test_a_last_token_reaches_only_the_tap_that_reads_it(C, dtype):
     want, got = p.backward(dy, **_gpu(v), lengths=n), p.backward(dy, **_gpu(bad), lengths=n)
     assert torch.equal(got["dx"], want["dx"])
     assert torch.equal(got["dw"][:, :F - 1], want["dw"][:, :F - 1]) and torch.isnan(got["dw"][:, F - 1]).all()
+
+
+def test_the_widest_heads_take_a_state():
+    """65536 channels of 128 states, 32 MiB a head: one token from a state, as a prompt, a step and a gradient, against
+    the definitions in 64 bits on the GPU.  Sums of up to 128 terms and the decay, in fp32: 140 steps of 2^-24 < 2^-16
+    of the terms; dB and dC over 65536 channels in a chain of 16-channel sums: under 2^13 steps of 2^-24, 2^-11."""
+    H, P, S = 2, 65536, 128
+    g = torch.Generator(device=DEV).manual_seed(9)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    x, dt, A, B, C, D, h, dy = (r(1, 1, H, P), r(1, 1, H).abs() * 0.1, -r(H).abs(), r(1, 1, 1, S), r(1, 1, 1, S), r(H),
+                                r(1, H, P, S), r(1, 1, H, P))
+    p = _scan(1, 1, H, P, 1, S, "f32", softplus=False)
+    last = torch.empty_like(h)
+    y = p(x, dt, A, B, C, D, state=h, state_out=last)
+    got = p.backward(dy, x, dt, A, B, C, D, state=h)
+    one = h.clone()
+    y1 = p.step(x[:, 0], dt[:, 0], A, B[:, 0], C[:, 0], one, D)
+    x, dt, A, B, C, D, dy = (v.double() for v in (x[0, 0], dt[0, 0], A, B[0, 0, 0], C[0, 0, 0], D, dy[0, 0]))
+    h = h[0].double()
+    a = torch.exp(A * dt)[:, None]
+
+    def near(got, want, mag, c, what):
+        assert ((got.double() - want).abs() <= 2.0 ** -24 * want.abs() + c * mag).all(), what
+
+    xd = dt[:, None] * x
+    new, top = a[..., None] * h + xd[..., None] * B, a[..., None] * h.abs() + xd.abs()[..., None] * B.abs()
+    for state, out in ((last, y[0, 0]), (one, y1[0])):
+        near(state[0], new, top, 2.0 ** -16, "state")
+        near(out, new @ C + D[:, None] * x, top @ C.abs() + (D[:, None] * x).abs(), 2.0 ** -16, "y")
+    into = dy * (C @ B)
+    near(got["dx"][0, 0], dt[:, None] * into + D[:, None] * dy,
+         dt[:, None] * dy.abs() * (C.abs() @ B.abs()) + (D[:, None] * dy).abs(), 2.0 ** -16, "dx")
+    near(got["dstate"][0], a[..., None] * dy[..., None] * C, a[..., None] * dy.abs()[..., None] * C.abs(), 2.0 ** -16, "dstate")
+    near(got["dC"][0, 0, 0], (dy[..., None] * new).sum((0, 1)), (dy.abs()[..., None] * top).sum((0, 1)), 2.0 ** -11, "dC")
+    near(got["dB"][0, 0, 0], (xd * dy).sum() * C, (xd * dy).abs().sum() * C.abs(), 2.0 ** -11, "dB")
