@@ -155,7 +155,8 @@ template <typename T, int NS> SEQ_DEV f32x4 mma_b(const typename Frag<T>::type &
 // The bf16 matrix unit rounds its sums down, by a few hundredths of a step on
 // average: where they meet x, B or C of one sign it adds up over the tokens.
 // The gradient takes half of its products of negated operands (`flip`: their
-// sign bits) and negates the sums: the error of ddt_bias halves, for 2 of 80 us.
+// sign bits) and negates the sums: ddt_bias of 2 x 2048 tokens is off by 2e-7 of
+// itself instead of 1.4e-6, for 2 of 80 us.
 SEQ_DEV bf16x8 flipped(bf16x8 f, uint32_t flip)
 {
     typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
@@ -426,12 +427,12 @@ SEQ_DEV double wave_last(double v)
 SEQ_DEV float wave_sum(float v) { return wave_last(wave_prefix(v)); }
 // The sums of v[0..3] over the 16 lanes of a row, v[r]'s in the lanes 4r..4r+3:
 // two exchanges that halve the values, then two within the four lanes.
-SEQ_DEV float row_sum4(f32x4 v, int lane)
+template <typename V = float> SEQ_DEV V row_sum4(f32x4 v, int lane)
 {
     const bool b3 = lane & 8, b2 = lane & 4;
-    const float a = (b3 ? v[2] : v[0]) + dpp<0x128, 0xf>(b3 ? v[0] : v[2]);     // 8 lanes on
-    const float b = (b3 ? v[3] : v[1]) + dpp<0x128, 0xf>(b3 ? v[1] : v[3]);
-    float s = (b2 ? b : a) + dpp<0x141, 0xf>(b2 ? a : b);                       // mirrored in 8 lanes
+    const V a = (V)(b3 ? v[2] : v[0]) + (V)dpp<0x128, 0xf>(b3 ? v[0] : v[2]);   // 8 lanes on
+    const V b = (V)(b3 ? v[3] : v[1]) + (V)dpp<0x128, 0xf>(b3 ? v[1] : v[3]);
+    V s = (b2 ? b : a) + dpp<0x141, 0xf>(b2 ? a : b);                           // mirrored in 8 lanes
     s += dpp<0xb1, 0xf>(s);
     s += dpp<0x4e, 0xf>(s);
     return s;
@@ -943,8 +944,10 @@ template <typename T, int SP> struct BwdShared {
     __align__(16) T m[NS * Q * MLD];            // [term][j][i]
     __align__(16) T u[NS * SP * ULD];           // [term][state][channel]
     __align__(16) float dt[2][Q], cum[2][Q], low[2][Q], w[2][Q], e[2][Q], raw[2][Q];   // w: e^{c_Q - c_j}
-    float row[2][NI][Q], col[2][NI][Q], cd[2][8][Q], xd[2][4][Q], xi[2][4][Q], dot[2][8], dd[2][8];
-    float sums[7][64];                          // wave 7's, from channel block to channel block of a head
+    double row[2][NI][Q], col[2][NI][Q];        // of W: see finish()
+    float cd[2][8][Q], xd[4][Q], xi[4][Q], dot[2][8], dd[2][8];
+    double pairs[64];                           // wave 7's, from channel block to channel block of a head
+    float sums[5][64];
 };
 
 template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_kernel(ScanParams p)
@@ -1021,32 +1024,38 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
     };
     // Wave 7, per token: the sums of a head over its channel blocks (in LDS from
     // block to block: as registers they would be everyone's), then what follows.
+    // A pair i > j of W enters the sum over the pairs around each token as row i
+    // less column j, so what a rounding takes from one of the two is left in every
+    // token's sum: rows and columns are added in fp64, where the pair's fp32 value
+    // cancels.  In fp32 ddt_bias was off by 1.0e-6 of itself, now by 2e-7 (the plain
+    // products in fp32, summed in fp64: 4e-7), at the same time.
     auto finish = [&](int k) __attribute__((always_inline)) {
         const int at = k & 1, d = (k / p.NPB) & 1;
-        float rs = 0.0f, cs = 0.0f, cd = 0.0f, ee = 0.0f, ei = 0.0f, dot = 0.0f, dd = 0.0f;
+        double pairs = 0.0;
+        float cd = 0.0f, ee = 0.0f, ei = 0.0f, dot = 0.0f, dd = 0.0f;
         if (k % p.NPB != 0) {
-            rs = sh.sums[0][lane], cs = sh.sums[1][lane], cd = sh.sums[2][lane], ee = sh.sums[3][lane];
-            ei = sh.sums[4][lane], dot = sh.sums[5][lane], dd = sh.sums[6][lane];
+            pairs = sh.pairs[lane], cd = sh.sums[0][lane], ee = sh.sums[1][lane];
+            ei = sh.sums[2][lane], dot = sh.sums[3][lane], dd = sh.sums[4][lane];
         }
         if (lane < Q) {
 #pragma unroll
-            for (int t = 0; t < NI; ++t) rs += sh.row[at][t][lane], cs += sh.col[at][t][lane];
+            for (int t = 0; t < NI; ++t) pairs += sh.row[at][t][lane] - sh.col[at][t][lane];
 #pragma unroll
             for (int t = 0; t < WN; ++t) cd += sh.cd[at][t][lane];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) ee += sh.xd[at][t][lane], ei += sh.xi[at][t][lane];
+            for (int t = 0; t < 4; ++t) ee += sh.xd[t][lane], ei += sh.xi[t][lane];
         }
 #pragma unroll
         for (int t = 0; t < 8; ++t) dot += sh.dot[at][t], dd += sh.dd[at][t];
         if (k % p.NPB != p.NPB - 1) {
-            sh.sums[0][lane] = rs, sh.sums[1][lane] = cs, sh.sums[2][lane] = cd, sh.sums[3][lane] = ee;
-            sh.sums[4][lane] = ei, sh.sums[5][lane] = dot, sh.sums[6][lane] = dd;
+            sh.pairs[lane] = pairs, sh.sums[0][lane] = cd, sh.sums[1][lane] = ee;
+            sh.sums[2][lane] = ei, sh.sums[3][lane] = dot, sh.sums[4][lane] = dd;
             return;
         }
         const int h = head_of(k);
         const int64_t base = fresh_scalar(base_);
         const float dt = lane < Q ? sh.dt[d][lane] : 0.0f, raw = lane < Q ? sh.raw[d][lane] : 0.0f, dec = sh.e[d][Q - 1];
-        const double before = (double)dt * ei, behind = (double)rs - cs + cd;
+        const double before = (double)dt * ei, behind = pairs + cd;
         const double b1 = wave_prefix(before), b2 = wave_prefix(behind);
         const float dl = (float)((b1 - before) + (wave_last(b2) - b2 + behind) + (double)(dec * dot));
         float draw = fmaf(p.a[h], dl, ee);
@@ -1077,7 +1086,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
         ct.store(sh.c);
         // what is never written: M above its diagonal tiles, the same of the sums
         for (int e = threadIdx.x; e < NS * Q * MLD; e += 512) sh.m[e] = (T)0.0f;
-        for (int e = threadIdx.x; e < 2 * NI * Q; e += 512) sh.row[0][0][e] = sh.col[0][0][e] = 0.0f;
+        for (int e = threadIdx.x; e < 2 * NI * Q; e += 512) sh.row[0][0][e] = sh.col[0][0][e] = 0.0;
         if (w == 6) {
             fetch_dt(0);
             decays(0);
@@ -1149,7 +1158,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) dp = mma(flipped(yf[ks], flip), xf[ks], dp);
                 if (flip) dp = -dp;
-                float col = 0.0f;
+                double col = 0.0;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const bool in = i + r >= j;
@@ -1165,7 +1174,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
                 col += __shfl_xor(col, 16);
                 col += __shfl_xor(col, 32);
                 if (q == 0) sh.col[at][it][j] = col;
-                const float row = row_sum4(wr, lane);
+                const double row = row_sum4<double>(wr, lane);
                 if ((l16 & 3) == 0) sh.row[at][jt][i + (l16 >> 2)] = row;
             }
         }
@@ -1279,7 +1288,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
                 // chunk's own part it would lose the digits that ddt_bias sums up
                 const f32x4 xi = {xv[j][0] * dx[j][0], xv[j][1] * dx[j][1], xv[j][2] * dx[j][2], xv[j][3] * dx[j][3]};
                 const float s = row_sum4(xi, lane);
-                if ((l16 & 3) == 0) sh.xi[at][pt][(jt0 + j) * 16 + q * 4 + (l16 >> 2)] = s * sign_x;
+                if ((l16 & 3) == 0) sh.xi[pt][(jt0 + j) * 16 + q * 4 + (l16 >> 2)] = s * sign_x;
             }
             // M's tiles (i >= j): in the upper half of the tokens only the second 32 meet it
 #pragma unroll
@@ -1309,7 +1318,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
                     sh.x[row * XLD + pt * 16 + l16] = (T)fmaf(skip, yv[j][r], dj[r] * dx[j][r]);
                 }
                 const float s = row_sum4(xd, lane);
-                if ((l16 & 3) == 0) sh.xd[at][pt][(jt0 + j) * 16 + q * 4 + (l16 >> 2)] = s;
+                if ((l16 & 3) == 0) sh.xd[pt][(jt0 + j) * 16 + q * 4 + (l16 >> 2)] = s;
             }
         }
         if (w == 6 && k + 1 < blocks && (k + 1) % p.NPB == 0) decays(k + 1);

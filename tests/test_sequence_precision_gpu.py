@@ -108,3 +108,27 @@ def test_tokens_behind_one_that_clears_the_state(P, S, dtype):
     out = torch.empty(N, H, P, S, device=DEV)
     _near(_scan(N, L, H, P, 1, S, dtype)(**_gpu(v), state_out=out), y, mag, HALF[dtype], 2.0 ** -20, "y")
     _near(out, last, top, HALF["f32"], 2.0 ** -20, "state_out")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("P,S", SHAPES)
+def test_one_large_pair_leaves_the_other_tokens_gradients_alone(P, S, dtype):
+    """Token 10's output meets token 9's input 2^30 times as strongly as any other pair, in a channel of its own.  Only
+    the decay of token 10 lies between them; the others' ddt have no such term and must not be rounded as if they had.
+    A term A W of ddt is off by 2^-21 (decay, products), a sum over 30 tokens in fp32 by 30 steps of 2^-24: c = 2^-18
+    of the terms of each token alone."""
+    g = torch.Generator().manual_seed(7)
+    N, L, H, t = 2, 30, 3, TYPE[dtype]
+    v = dict(x=torch.zeros(N, L, H, P), dt=torch.full((N, L, H), 2.0 ** -6), A=-torch.rand(H, generator=g) - 0.5,
+             B=torch.zeros(N, L, 1, S), C=torch.zeros(N, L, 1, S))
+    v["B"][..., S // 2] = v["C"][..., S // 2] = 1
+    dy = torch.zeros(N, L, H, P)
+    v["x"][..., P - 1], dy[..., P - 1] = torch.randn(N, L, H, generator=g), torch.randn(N, L, H, generator=g)
+    v["x"][:, 9, :, 0], dy[:, 10, :, 0] = 2.0 ** 18, 2.0 ** 18
+    for k in ("x", "dt", "B", "C"):
+        v[k] = v[k].to(t)
+    dy = dy.to(t)
+    want = seq.scan_grad(dy, **v, softplus=False)
+    mag = seq.scan_grad(dy, **v, softplus=False, magnitude=True)
+    got = _scan(N, L, H, P, 1, S, dtype).backward(dy.to(DEV), **_gpu(v))
+    _near(got["ddt"], want["ddt"], mag["ddt"], HALF[dtype], 2.0 ** -18, "ddt")
