@@ -133,3 +133,142 @@ def test_the_widest_heads_take_a_state():
     near(got["dstate"][0], a[..., None] * dy[..., None] * C, a[..., None] * dy.abs()[..., None] * C.abs(), 2.0 ** -16, "dstate")
     near(got["dC"][0, 0, 0], (dy[..., None] * new).sum((0, 1)), (dy.abs()[..., None] * top).sum((0, 1)), 2.0 ** -11, "dC")
     near(got["dB"][0, 0, 0], (xd * dy).sum() * C, (xd * dy).abs().sum() * C.abs(), 2.0 ** -11, "dB")
+
+
+# ---- plans of large problems, at small cost -------------------------------------
+# Heads are repeated: the reference computes `heads` of them, the kernels `times` as many in the same groups, whose
+# copies must come out with the same bits.  Bounds as in test_sequence_gpu.py, whose helpers these are.
+def _repeated(N, L, heads, times, P, G, S, dtype, seed):
+    from test_sequence_gpu import _scan_case as case
+    a, dy, dlast, _ = case(N, L, heads, P, G, S, dtype, True, None, seed)
+    # group by group: the heads of a group are its own and their copies
+    more = lambda v, d: v.unflatten(d, (G, heads // G)).repeat_interleave(times, d).flatten(d, d + 1) if v is not None else v
+    wide = dict(a, **{k: more(a[k], {"x": 2, "dt": 2, "state": 1}.get(k, 0)) for k in ("x", "dt", "A", "D", "dt_bias", "state")})
+    return a, wide, dy, more(dy, 2), dlast, more(dlast, 1)
+
+
+def _check_forward(dims, times, dtype, lengths, what):
+    from test_sequence_gpu import _near as near
+    N, L, heads, P, G, S = dims
+    a, wide, *_ = _repeated(N, L, heads, times, P, G, S, dtype, 41)
+    p = _scan(N, L, heads * times, P, G, S, dtype)
+    assert what(p.describe()), p.describe()
+    n = torch.tensor(lengths, dtype=torch.int32)
+    out = torch.full((N, heads * times, P, S), 7.0, device=DEV)
+    y = p(**_gpu(wide), lengths=n.to(DEV), state_out=out)
+    pick = torch.arange(G)[:, None] * (heads // G * times) + torch.arange(heads // G)[None]
+    first = pick.flatten().to(DEV)
+    for k in range(times):
+        at = first + k * (heads // G)
+        assert torch.equal(y[:, :, at], y[:, :, first]) and torch.equal(out[:, at], out[:, first]), k
+    want, last = seq.scan(**a, lengths=n)
+    my, ml = seq.scan(**a, lengths=n, magnitude=True)
+    near(y[:, :, first], want, my, HALF[dtype], 2.0 ** -14, "y")
+    near(out[:, first], last, ml, HALF["f32"], 2.0 ** -15, "state_out")
+
+
+def test_two_state_segments_a_forward_workgroup():
+    """The plan of long sequences of few heads: a workgroup's chunks are two segments of the pass over the states.
+    One sequence ends within the first of the two."""
+    _check_forward((2, 4100, 8, 8, 2, 16), 8, "bf16", [4100, 2500], lambda t: "(2 x 2 of whole bf16 vectors)" in t)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("S", [128, 64])
+def test_many_chunks_of_whole_heads(S, dtype):
+    """Heads of 64 channels over all chunks of the sequence in one workgroup, full and ragged."""
+    one = "in 1 segments (1 x 1" if dtype == "bf16" else "in "
+    _check_forward((2, 330, 5, 64, 1, S), 26, dtype, [330, 170], lambda t: one in t)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dims,times,lengths", [((2, 330, 5, 64, 1, 128), 13, [330, 170]), ((4, 70, 8, 72, 4, 16), 8, [70, 0, 33, 65]),
+                                                ((2, 140, 2, 130, 1, 40), 24, [140, 77])], ids=str)
+def test_gradient_of_several_heads_a_workgroup(dims, times, lengths, dtype):
+    """... of more than 64 states, and of more than one block of 64 channels each."""
+    from test_sequence_gpu import _around, _near as near
+    N, L, heads, P, G, S = dims
+    a, wide, dy, wdy, dlast, wlast = _repeated(N, L, heads, times, P, G, S, dtype, 43)
+    p = _scan(N, L, heads * times, P, G, S, dtype)
+    assert int(p.describe().split("slices of ")[1].split()[0]) > 1, p.describe()
+    n = torch.tensor(lengths, dtype=torch.int32)
+    got = p.backward(wdy.to(DEV), **_gpu(wide), lengths=n.to(DEV), dstate_out=wlast.to(DEV))
+    kw = dict(a, lengths=n, dstate_out=dlast)
+    want, mag = seq.scan_grad(dy, **kw), seq.scan_grad(dy, **kw, magnitude=True)
+    my, _ = seq.scan(**a, lengths=n, magnitude=True)
+    around = _around((dy.double().abs() * my).sum(-1) + mag["step"] * mag["e"]) + mag["dl"]
+    mag["ddt"] = around * a["A"].double().abs() + mag["e"]
+    mag["dA"] = (around * mag["step"]).sum((0, 1))
+    mag["ddt_bias"] = mag["ddt"].sum((0, 1))
+    first = (torch.arange(G)[:, None] * (heads // G * times) + torch.arange(heads // G)[None]).flatten().to(DEV)
+    for k, v in got.items():
+        if k in ("dB", "dC"):       # over the heads: every copy's
+            near(v, want[k] * times, mag[k] * times, HALF[dtype], 2.0 ** -13, k)
+            continue
+        d = {"dx": 2, "ddt": 2, "dstate": 1}.get(k, 0)
+        for i in range(1, times):
+            assert torch.equal(v.index_select(d, first + i * (heads // G)), v.index_select(d, first)), (k, i)
+        near(v.index_select(d, first), want[k], mag[k], HALF[dtype] if k in ("dx", "ddt") else HALF["f32"], 2.0 ** -13, k)
+
+
+# ---- the convolution's forms ------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,C,F,bias,silu,apart", [
+    (1, 1, 2, False, False, False), (3, 64, 4, True, True, True), (5, 37, 4, True, False, False), (2, 520, 8, False, True, True),
+    (4, 24, 3, True, True, False), (7, 130, 5, False, False, True), (1, 2304, 4, True, True, False), (2, 9, 7, True, True, True),
+    (3, 48, 6, False, True, False)])
+def test_convolution_step(N, C, F, bias, silu, apart, dtype):
+    """Every tap count, vectors and single channels, in place and apart, x and y as columns of wider rows.  Bound: F
+    products and sums in fp32 and the sigmoid, 2^-20 of the terms."""
+    import ctypes
+    from convolution_forward_implicit_amd import capi
+    from test_sequence_gpu import _near as near
+    g = torch.Generator().manual_seed(50 + F)
+    t = TYPE[dtype]
+    r = lambda *s: torch.randn(*s, generator=g).to(t)
+    x, w, b, state = r(N, C), r(C, F), r(C) if bias else None, r(N, F - 1, C)
+    p = _conv(N, 1, C, F, dtype, has_bias=bias, silu=silu)
+    want, last, _ = seq.causal(x[:, None], w, b, silu, state)
+    mag = seq.causal(x[:, None].abs(), w.abs(), None if b is None else b.abs(), False, state.abs())[0]
+    for wide, lo in ((C, 0), (2 * C + 16, 8), (2 * C + 5, 3)):
+        rows = torch.full((N, wide), 5.0, dtype=t, device=DEV)
+        rows[:, lo:lo + C] = x.to(DEV)
+        into = torch.full((N, wide), 9.0, dtype=t, device=DEV)
+        v = _gpu(dict(w=w, b=b, state=state))
+        if apart:
+            out = torch.full_like(v["state"], 7.0)
+            e = rows.element_size()
+            args = capi.conv_causal_args_t(rows.data_ptr() + lo * e, v["w"].data_ptr(), v["b"].data_ptr() if bias else None,
+                                           v["state"].data_ptr(), None, into.data_ptr() + lo * e, out.data_ptr(), wide, wide)
+            capi.conv_causal_step(p._plan, ctypes.byref(args), torch.cuda.current_stream().cuda_stream)
+            torch.cuda.synchronize()
+            assert torch.equal(v["state"].cpu(), state)
+        else:
+            out = v["state"]
+            p.step(rows[:, lo:lo + C], v["w"], out, v["b"], out=into[:, lo:lo + C])
+        near(into[:, lo:lo + C], want[:, 0], mag[:, 0], HALF[dtype], 2.0 ** -20, "y")
+        assert torch.equal(out.cpu(), last.to(t))
+        assert (into[:, :lo] == 9).all() and (into[:, lo + C:] == 9).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("C", [40, 19])
+def test_convolution_without_a_bias_and_lengths_out_of_range(C, dtype):
+    """Lengths outside 0..L are the nearer end."""
+    from test_sequence_gpu import _near as near
+    g = torch.Generator().manual_seed(60)
+    N, L, F, t = 3, 30, 4, TYPE[dtype]
+    r = lambda *s: torch.randn(*s, generator=g).to(t)
+    a, dy = dict(x=r(N, L, C), w=r(C, F), bias=None, state=r(N, F - 1, C)), r(N, L, C)
+    n = torch.tensor([-3, L + 5, 11], dtype=torch.int32)
+    p = _conv(N, L, C, F, dtype)
+    out = torch.full((N, F - 1, C), 7.0, dtype=t, device=DEV)
+    y = p(**_gpu(a), lengths=n.to(DEV), state_out=out)
+    want, last, _ = seq.causal(**a, silu=False, lengths=n)
+    near(y, want, seq.causal(a["x"].abs(), a["w"].abs(), None, False, a["state"].abs(), n)[0], HALF[dtype], 2.0 ** -20, "y")
+    assert torch.equal(out.cpu(), last.to(t))
+    got = p.backward(dy.to(DEV), **_gpu(a), lengths=n.to(DEV))
+    assert got["dbias"] is None
+    want, mag = (seq.causal_grad(dy, **a, silu=False, lengths=n, magnitude=m) for m in (False, True))
+    for k in ("dx", "dw", "dstate"):
+        near(got[k], want[k], mag[k], HALF[dtype], 2.0 ** -17, k)
