@@ -139,19 +139,6 @@ template <int NS> SEQ_DEV void make_split(const float (&v)[8], Split<float, NS> 
 // fp32 needs one term only
 template <typename T, int NS> constexpr int terms() { return sizeof(T) == 4 ? 1 : NS; }
 
-template <typename T, int NS> SEQ_DEV f32x4 mma_a(const Split<T, NS> &a, const typename Frag<T>::type &b, f32x4 c)
-{
-#pragma unroll
-    for (int k = 0; k < NS; ++k) c = mma(a.f[k], b, c);
-    return c;
-}
-template <typename T, int NS> SEQ_DEV f32x4 mma_b(const typename Frag<T>::type &a, const Split<T, NS> &b, f32x4 c)
-{
-#pragma unroll
-    for (int k = 0; k < NS; ++k) c = mma(a, b.f[k], c);
-    return c;
-}
-
 // The bf16 matrix unit rounds its sums down, by a few hundredths of a step on
 // average: where they meet x, B or C of one sign it adds up over the tokens.
 // The gradient takes half of its products of negated operands (`flip`: their
