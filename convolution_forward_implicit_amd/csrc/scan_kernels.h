@@ -426,11 +426,14 @@ template <typename V = float> SEQ_DEV V row_sum4(f32x4 v, int lane)
 }
 
 // Token `lane` of a chunk: the step size dt (0 behind the sequence) and the
-// running sum of log2 of the decays, in fp64.
+// running sum of log2 of the decays, in fp64.  A decay under 2^-1024 counts as
+// that, zero in fp32 like whatever it is a factor of: a step that clears the
+// state may be any number and leaves the sums their digits.
 SEQ_DEV void chunk_decay(float raw, bool live, float a, int softplus_on, float &dt, double &cum)
 {
     dt = live ? (softplus_on ? softplus(raw) : raw) : 0.0f;
-    cum = wave_prefix((double)a * (double)dt * 1.4426950408889634074);
+    const double decay = (double)a * (double)dt * 1.4426950408889634074;
+    cum = wave_prefix(decay < -1024.0 ? -1024.0 : decay);
 }
 
 

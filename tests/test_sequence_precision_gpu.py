@@ -132,3 +132,34 @@ def test_one_large_pair_leaves_the_other_tokens_gradients_alone(P, S, dtype):
     mag = seq.scan_grad(dy, **v, softplus=False, magnitude=True)
     got = _scan(N, L, H, P, 1, S, dtype).backward(dy.to(DEV), **_gpu(v))
     _near(got["ddt"], want["ddt"], mag["ddt"], HALF[dtype], 2.0 ** -18, "ddt")
+
+
+@pytest.mark.parametrize("step", [2.0 ** 40, 2.0 ** 100])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("P,S", SHAPES)
+def test_a_step_of_any_size_clears_the_state(P, S, dtype, step):
+    """As above with steps past the digits of fp64 sums, on tokens without an input; the gradients of what follows too."""
+    g = torch.Generator().manual_seed(8)
+    N, L, H, t = 4, 6, 8, TYPE[dtype]
+    dt = torch.randint(1, 32, (N, L, H), generator=g) / 64
+    dt[:, 1] = step
+    v = dict(x=torch.randn(N, L, H, P, generator=g), dt=dt.to(t), A=-torch.rand(H, generator=g) - 1,
+             B=_two_states(g, S, N, L, 1).to(t), C=_two_states(g, S, N, L, 1).to(t), state=_two_states(g, S, N, H, P))
+    v["x"][:, 1:3] = 0
+    v["x"][:, 5] = 0
+    v["x"] = v["x"].to(t)
+    y, last = seq.scan(**v, softplus=False)
+    mag, top = seq.scan(**v, softplus=False, magnitude=True)
+    out = torch.empty(N, H, P, S, device=DEV)
+    p = _scan(N, L, H, P, 1, S, dtype)
+    _near(p(**_gpu(v), state_out=out), y, mag, HALF[dtype], 2.0 ** -20, "y")
+    _near(out, last, top, HALF["f32"], 2.0 ** -20, "state_out")
+    dy = torch.zeros(N, L, H, P)
+    dy[:, 4:, :, P // 3] = torch.randn(N, 2, H, generator=g)
+    dy = dy.to(t)
+    want = seq.scan_grad(dy, **v, softplus=False)
+    mag = seq.scan_grad(dy, **v, softplus=False, magnitude=True)
+    got = p.backward(dy.to(DEV), **_gpu(v))
+    # sums over eight heads of one channel each: as a gradient's two chains, and eight steps of 2^-24
+    for k in ("dx", "dB", "dC", "dstate"):
+        _near(got[k], want[k], mag[k], HALF["f32" if k == "dstate" else dtype], 2.0 ** -17, k)
