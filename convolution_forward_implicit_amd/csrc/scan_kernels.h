@@ -1047,7 +1047,10 @@ template <typename T, int SP> __global__ void __launch_bounds__(512) scan_bwd_ke
         const float dt = lane < Q ? sh.dt[d][lane] : 0.0f, raw = lane < Q ? sh.raw[d][lane] : 0.0f, dec = sh.e[d][Q - 1];
         const double before = (double)dt * ei, behind = pairs + cd;
         const double b1 = wave_prefix(before), b2 = wave_prefix(behind);
-        const float dl = (float)((b1 - before) + (wave_last(b2) - b2 + behind) + (double)(dec * dot));
+        float dl = (float)((b1 - before) + (wave_last(b2) - b2 + behind) + (double)(dec * dot));
+        // every term has the token's decay as a factor; where that is zero, what the
+        // sums leave is a rounding, and dt, which made it zero, may be any number
+        if (p.a[h] * dt * kLog2e < -150.0f) dl = 0.0f;
         float draw = fmaf(p.a[h], dl, ee);
         if (p.softplus) draw *= 1.0f / (1.0f + expf(-raw));
         if (lane >= rows) draw = 0.0f;

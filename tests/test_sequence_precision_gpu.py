@@ -163,3 +163,28 @@ def test_a_step_of_any_size_clears_the_state(P, S, dtype, step):
     # sums over eight heads of one channel each: as a gradient's two chains, and eight steps of 2^-24
     for k in ("dx", "dB", "dC", "dstate"):
         _near(got[k], want[k], mag[k], HALF["f32" if k == "dstate" else dtype], 2.0 ** -17, k)
+
+
+@pytest.mark.parametrize("step", [4096.0, 2.0 ** 40, 2.0 ** 100])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("P,S", SHAPES)
+def test_a_clearing_step_has_no_gradient_by_its_decay(P, S, dtype, step):
+    """Its decay is zero, and so is the gradient of A dt there, however large dt makes what is left of a sum.  The inputs
+    differ by up to 2^16 in size, so that fp64 sums of them leave something.  c = 2^-17.2 as above and 30 steps of
+    2^-24 for the sums over the tokens: 2^-16."""
+    g = torch.Generator().manual_seed(9)
+    N, L, H, t = 3, 30, 4, TYPE[dtype]
+    dt = torch.randint(1, 32, (N, L, H), generator=g) / 64
+    dt[:, 2] = step
+    v = dict(x=torch.zeros(N, L, H, P), dt=dt.to(t), A=-torch.rand(H, generator=g) - 1, B=_two_states(g, S, N, L, 1).to(t),
+             C=_two_states(g, S, N, L, 1).to(t), state=_two_states(g, S, N, H, P))
+    dy = torch.zeros(N, L, H, P)
+    wide = lambda: torch.randn(N, L, H, generator=g) * 2.0 ** torch.randint(-8, 9, (N, L, H), generator=g)
+    v["x"][..., P // 3], dy[..., P // 3] = wide(), wide()
+    v["x"][:, 2] = 0
+    v["x"], dy = v["x"].to(t), dy.to(t)
+    want = seq.scan_grad(dy, **v, softplus=False)
+    mag = seq.scan_grad(dy, **v, softplus=False, magnitude=True)
+    got = _scan(N, L, H, P, 1, S, dtype).backward(dy.to(DEV), **_gpu(v))
+    _near(got["ddt"], want["ddt"], mag["ddt"], HALF[dtype], 2.0 ** -16, "ddt")
+    _near(got["dA"], want["dA"], mag["dA"], HALF["f32"], 2.0 ** -16, "dA")
