@@ -179,9 +179,11 @@ __global__ void __launch_bounds__(256) causal_step_kernel(CausalParams p)
 // reaches back into the run), keeps its sums of dw and db in fp32 registers,
 // and the workgroup adds its runs in LDS, in a fixed order; causal_reduce_kernel
 // adds the workgroups' rows, in a fixed order too.  4 x 2048 x 2304 bf16 (113 MB):
-// 38 + 4 us, 2.7 TB/s: about 35 vector instructions an element, the sigmoid's two
-// at a quarter of the rate, are 22 us of it, at two waves per SIMD (200 registers
-// of fetched rows and sums); 74 us with a branch a row.
+// 34 + 4 us, 3.3 TB/s: about 35 vector instructions an element, the sigmoid's two
+// at a quarter of the rate, are 22 us of it, at three waves per SIMD (149 registers
+// of fetched rows and sums).  Rows fetched one by one took 80 us where 46 was the
+// time; sums that every row enters, tokens behind the sequence as zeros, 41 for 35
+// (199 registers, two waves).
 template <typename T, int F, int V, bool SILU>
 __global__ void __launch_bounds__(256) causal_bwd_kernel(CausalParams p)
 {

@@ -25,12 +25,14 @@
 // between; 8 bytes of each row instead: 16), the transposing read 2.5 (4.0).
 //
 // What bounds it: 16384 tokens x 64 heads of 64 x 128 (34 Gflop by the recurrence,
-// 107 as the products that the splits make of it) take 172-190 us, 2.6 us a chunk
+// 133 as the products that the splits make of it) take 196-218 us, 3.1 us a chunk
 // and workgroup: the matrix unit is busy for a third of that and other vector
 // instructions for half, and the two hardly overlap -- a wave of products and a wave
 // of FMAs on one SIMD take as long as one after the other (8 products and 24 FMAs:
-// 227 clocks, 128 and 107 alone).  LDS is busy for a quarter.  The registers' form
-// takes 207 us, the state pass 81 there and 62 here.
+// 227 clocks, 128 and 107 alone).  LDS is busy for a quarter.  The pass over the
+// states is another 62-70 us; back to back the two take 226 us, the registers' forms
+// 300.  With two terms for M and h and one number for c_i they took 205 and had lost
+// digits: see scan_kernels.h.
 #pragma once
 
 #include "igemm_dma.h"

@@ -28,13 +28,12 @@
 // C and dy are bf16 already; what is computed on the way (M, the states, dS)
 // enters as the sum of three bf16 numbers, each the rounding of what the ones
 // before it left, so that all 24 bits of it take part (with two terms for M and
-// h, 16 bits, y's were bf16 neighbours of what fp32 gives at one place in a
-// thousand; the third costs 1 to 4%).  fp32 calls run on the fp32 matrix
-// instructions instead.  States, sums and exponents are
-// fp32; the running sums c_i are added in fp64 and used as differences, which
-// are rounded to fp32 only then (c_i itself, up to some hundreds, would be off
-// by 1e-5, and so would every decay; behind a token whose step clears the state
-// it may be any number): two fp32 numbers stand for c_i.
+// h, 16 bits, one y in a thousand was a bf16 neighbour of what fp32 gives; the
+// third costs 3 to 8%).  fp32 calls run on the fp32 matrix instructions instead.
+// States, sums and exponents are fp32; the running sums c_i are added in fp64 and
+// used as differences, which are rounded to fp32 only then (c_i itself, up to some
+// hundreds, would be off by 1e-5, and so would every decay; behind a token whose
+// step clears the state it is thousands): two fp32 numbers stand for c_i.
 //
 // Fragments (16x16 blocks, 64 lanes, q = lane / 16): an operand's lane holds 8
 // values of the reduction for row (or column) lane % 16, a result's lane four
@@ -442,7 +441,7 @@ SEQ_DEV void chunk_decay(float raw, bool live, float a, int softplus_on, float &
 // scan_dma.h.)  The products with B are a quarter of the forward's; what a chunk
 // costs beside them is its way through registers into LDS and the decays' chain,
 // so four chunks' decays are done at once, one by each wave.  16384 tokens x 64
-// heads in bf16: 81 us against scan_dma.h's 62; fp32, 777 tokens x 12 sequences
+// heads in bf16: 78 us against scan_dma.h's 62-70; fp32, 777 tokens x 12 sequences
 // and heads of 40 channels x 24 states: 6.0 us, the launch and three chunks' loads.
 // One workgroup: 64 channels of a head, one segment of chunks, wave w the
 // channels 16w..16w+15 and all of the state (results: rows channels, columns
@@ -679,9 +678,10 @@ SEQ_DEV void tri_tile(int t, int &it, int &jt)
 // channels, which makes them the operand of h_0 C as they stand).  The chunk's
 // scores are computed once, their 16x16 tiles dealt to the waves, and pass
 // through LDS as M.  The workgroup waits at four barriers a chunk; two of them
-// share a compute unit (234 registers).  16384 tokens x 64 heads in bf16 take 207
-// us with this kernel; fp32, 777 tokens x 12 heads of 40 x 24: 13 us, of which the
-// join of up to 9 segments is half.
+// share a compute unit (251 registers, 80 KB of LDS).  16384 tokens x 64 heads in
+// bf16 take 300 us with this kernel and the pass before it, 226 with scan_dma.h's;
+// fp32, 777 tokens x 12 heads of 40 x 24: 13 us, of which the join of up to 9
+// segments is half.
 template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd_kernel(ScanParams p)
 {
     constexpr int Q = Frag<T>::Q, NT = SP / 16, NI = Q / 16, TRI = NI * (NI + 1) / 2, TPW = (TRI + 3) / 4;
@@ -919,12 +919,13 @@ template <typename T, int SP> __global__ void __launch_bounds__(256, 2) scan_fwd
 // them.  While a head is computed the next one's x, dy and states are on their
 // way into registers, wave 6 does its decays, and wave 7 turns the sums that the
 // head before left in LDS into ddt and its parts of dA, ddt_bias and dD.
-// 2 x 2048 tokens, 32 heads of 64 x 128 in bf16: 80 us, 10 a head and chunk for 64
-// + 64 KB of states at its borders (1.7 TB/s); the products are 5 us of them, the
+// 2 x 2048 tokens, 32 heads of 64 x 128 in bf16: 83 us, 10 a head and chunk for 32
+// + 32 KB of states at its borders (1.6 TB/s); the products are 5 us of them, the
 // other vector instructions (splits, decays, sums over lanes) 30, and the loads of
 // the next states, which 256 registers leave no room to start earlier, most of the
-// rest.  Four waves of 512 registers instead: 138; the sums over lanes one value at
-// a time: 100; the tensors' addresses kept over the heads instead of taken anew: 82.
+// rest.  Four waves of 512 registers instead: 138 where 87 was the time; the sums
+// over lanes one value at a time: 100; the tensors' addresses kept over the heads
+// instead of taken anew: 82 for 78.
 template <typename T, int SP> struct BwdShared {
     static constexpr int Q = Frag<T>::Q, NI = Q / 16, NS = terms<T, 3>();
     static constexpr int XLD = kPB + Frag<T>::PAD, BLD = SP + Frag<T>::PAD, MLD = Q + Frag<T>::PAD;

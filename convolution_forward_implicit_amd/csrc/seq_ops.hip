@@ -258,10 +258,11 @@ template <typename T> void launch_scan(int SP, const ScanParams &p, int64_t unit
 
 // Segments of K chunks so that `units` heads give about `want` workgroups, each
 // cut into `fine` times as many for the pass over the states.  A segment's start
-// is joined from all before it by the workgroup itself: 32 are the most that
-// costs less than another launch between the two would; finer ones pay where a
-// forward workgroup has 16 chunks and more (16384 tokens x 64 heads 253 -> 235 us
-// with two; 4096 x 32, 8 chunks: 53 -> 59).
+// is joined from all before it by the workgroup itself, up to 32; against a launch
+// between the two that joins them the gradient of 2 x 2048 x 32 heads went from 160
+// to 150 us and 16384 x 64 heads from 255 to 248, 4096 x 32 from 55 to 59.  Finer
+// segments pay where a forward workgroup has 16 chunks and more (16384 x 64 heads
+// 253 -> 235 us with two; 4096 x 32, 8 chunks: 53 -> 59).
 Segments split_segments(int64_t units, int64_t K, int64_t want, int64_t fine)
 {
     // time goes by K / n chunks and n joins, a chunk costing about four joins: the
@@ -435,7 +436,7 @@ conv_status_t conv_causal_bwd_run(const conv_causal_plan_t *plan, const conv_cau
     if ((st = check_overlap(out, 5, in, 7)) != CONV_OK) return st;
     const Rows vec[] = {in[0], in[1], in[2], in[3], in[4], in[5], out[0], out[3]};
     // A gradient thread holds its run's rows of x and dy: by 8 bytes they leave
-    // room for two waves more per SIMD than by 16 (training case 74 us with 16).
+    // room for three waves per SIMD, by 16 for one (training case 35 and 54 us).
     const int V = conv_vector(d, e, vec, 8) == 1 ? 1 : (int)(8 / e);
     CausalParams p{};
     p.x = a->x; p.w = a->w; p.bias = a->bias; p.state = a->state; p.lengths = a->lengths;
