@@ -28,10 +28,10 @@ out), token by token (.step) and backwards (.backward).
 """
 from . import capi
 from .capi import ConvError  # noqa: F401
-from .sequence import CausalConv, SelectiveScan  # noqa: F401
+from .sequence import CausalConv, DeltaRule, SelectiveScan  # noqa: F401
 
-__all__ = ["ConvFwd", "ConvChain", "ConvBwdData", "ConvBwdWeight", "CausalConv", "SelectiveScan", "ConvError", "capi",
-           "desc_from_problem"]
+__all__ = ["ConvFwd", "ConvChain", "ConvBwdData", "ConvBwdWeight", "CausalConv", "SelectiveScan",
+           "DeltaRule", "ConvError", "capi", "desc_from_problem"]
 
 
 def _ndim(p):

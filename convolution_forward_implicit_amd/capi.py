@@ -42,6 +42,10 @@ SEQUENCE_EXPORTED = ["conv_causal_create", "conv_causal_run", "conv_causal_step"
                      "conv_scan_create", "conv_scan_workspace_bytes", "conv_scan_run", "conv_scan_step",
                      "conv_scan_bwd_workspace_bytes", "conv_scan_bwd_run", "conv_scan_destroy", "conv_scan_describe"]
 
+# the gated delta rule
+DELTA_EXPORTED = ["conv_delta_create", "conv_delta_workspace_bytes", "conv_delta_run", "conv_delta_step",
+                  "conv_delta_destroy", "conv_delta_describe"]
+
 
 class conv_fwd_desc_t(ctypes.Structure):
     _fields_ = [("ndim", ctypes.c_int32), ("dtype", ctypes.c_int32),
@@ -85,6 +89,16 @@ class conv_scan_bwd_args_t(ctypes.Structure):
                                                   "dt_bias", "state", "lengths", "dstate_out", "dx", "ddt", "da",
                                                   "db", "dc", "dd", "ddt_bias", "dstate")] +
                 [(n, ctypes.c_int64) for n in ("dy_ld", "x_ld", "dt_ld", "b_ld", "c_ld", "dx_ld", "ddt_ld", "db_ld", "dc_ld")])
+
+
+class conv_delta_desc_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("dtype", "reserved")] +
+                [(n, ctypes.c_int64) for n in ("N", "L", "H", "P", "G", "S")] + [("scale", ctypes.c_double)])
+
+
+class conv_delta_args_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "g", "beta", "state", "lengths", "y", "state_out")] +
+                [(n, ctypes.c_int64) for n in ("q_ld", "k_ld", "v_ld", "g_ld", "beta_ld", "y_ld")])
 
 
 class ConvError(RuntimeError):
@@ -199,6 +213,14 @@ def lib():
             f("describe").argtypes = [P]
             f("describe").restype = ctypes.c_char_p
         L.conv_scan_workspace_bytes.argtypes = [P, ctypes.POINTER(I64)]
+        L.conv_delta_create.argtypes = [ctypes.POINTER(conv_delta_desc_t), ctypes.POINTER(P)]
+        L.conv_delta_workspace_bytes.argtypes = [P, ctypes.POINTER(I64)]
+        L.conv_delta_run.argtypes = [P, ctypes.POINTER(conv_delta_args_t), P, I64, P]
+        L.conv_delta_step.argtypes = [P, ctypes.POINTER(conv_delta_args_t), P]
+        L.conv_delta_destroy.argtypes = [P]
+        L.conv_delta_destroy.restype = None
+        L.conv_delta_describe.argtypes = [P]
+        L.conv_delta_describe.restype = ctypes.c_char_p
         _lib = L
     return _lib
 
@@ -523,3 +545,32 @@ def conv_scan_destroy(plan):
 
 def conv_scan_describe(plan):
     return lib().conv_scan_describe(plan).decode()
+
+
+# ---- the gated delta rule ------------------------------------------------------
+def conv_delta_create(desc):
+    plan = ctypes.c_void_p()
+    _check(lib().conv_delta_create(ctypes.byref(desc), ctypes.byref(plan)))
+    return plan.value
+
+
+def conv_delta_workspace_bytes(plan):
+    n = ctypes.c_int64()
+    _check(lib().conv_delta_workspace_bytes(plan, ctypes.byref(n)))
+    return n.value
+
+
+def conv_delta_run(plan, args, workspace, workspace_bytes, stream=0):
+    _check(lib().conv_delta_run(plan, args, workspace, workspace_bytes, stream))
+
+
+def conv_delta_step(plan, args, stream=0):
+    _check(lib().conv_delta_step(plan, args, stream))
+
+
+def conv_delta_destroy(plan):
+    lib().conv_delta_destroy(plan)
+
+
+def conv_delta_describe(plan):
+    return lib().conv_delta_describe(plan).decode()

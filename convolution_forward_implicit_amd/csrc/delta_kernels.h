@@ -1,0 +1,568 @@
+// The gated delta rule, its gradient and its single-token step.
+//
+//   S' = e^{g_t} S,   y_t = v_t - S' k_t,   S = S' + beta_t y_t k_t^T,   o_t = scale S q_t
+//
+// per head, with a state S of P x S: a step replaces what the state holds under
+// the key k_t by v_t, as far as the rate beta_t says.  Over a chunk of Q = 64
+// tokens with c_i = sum_{j<=i} g_j and Gamma_ij = e^{c_i - c_j} (i >= j), every
+// y depends on those before it by a triangular system, which is solved once
+// for all channels (S_0 the state that the chunk starts from, i, j tokens):
+//
+//   T_ij = Gamma_ij k_i . k_j  (i > j)         N = (1 + T beta)^-1 T, strictly lower
+//   Z = V - e^c K S_0^T                        Y = Z - N (beta Z),      U = beta Y
+//   O = scale e^c Q S_0^T + M U                M_ij = scale Gamma_ij q_i . k_j  (i >= j)
+//   S_Q = e^{c_Q} S_0 + sum_j e^{c_Q - c_j} U_j k_j^T
+//
+// (beta never divides, so it may be 0.)  With dO and the gradient R of S_Q:
+//
+//   dU = M^T dO + e^{c_Q - c} K R^T            E = dU - N^T (beta dU),  dV = beta E,  dbeta = E . Y
+//   dS_0 = e^{c_Q} R + scale (e^c dO)^T Q - (e^c dV)^T K
+//
+// and the rest from S_0, R, Y and E of each chunk by itself (delta_grad_kernel).
+// All exponents are differences of sums, at most 0 for g <= 0.  The sums are
+// added in fp64; a g below -1e5 counts as that.
+//
+// Numbers.  As in the scan, q, k and dO enter the bf16 matrix instructions as
+// they are and what is computed on the way (states, Z, U, N) as the sum of three
+// bf16 numbers: states come out with fp32's digits.  fp32 calls run on the fp32
+// matrix instructions.
+//
+// delta_prepare_kernel does what a chunk can do without its state and leaves the
+// operands of the matrix instructions in the workspace, each as the 64 lanes
+// load it.  delta_state_kernel then carries 16 channels of one head's state
+// through the sequence: one wave, nothing shared, no barrier.  The results of
+// one product are the operand of the next as they stand: two results of 16 rows
+// are an operand of a reduction over 32 (tokens 4q..4q+3 and 16+4q..16+4q+3 of
+// lane group q), and the rows of K^T are taken in such an order that the states
+// come out as 8 consecutive keys, which K's and Q's rows hold.
+#pragma once
+
+#include "seq_frags.h"
+
+namespace convfwd {
+
+constexpr int kDQ = 64;         // tokens of a chunk
+constexpr int kTri = 6;         // operands of a triangular 64 x 64 matrix: 16 rows x 32 columns each
+
+struct DeltaParams {
+    const void *q, *k, *v, *beta;
+    const float *g, *state;
+    const int32_t *lengths;
+    void *y;
+    float *state_out;
+    int64_t q_ld, k_ld, v_ld, g_ld, beta_ld, y_ld;
+    int64_t L;
+    int N, H, P, G, S, K;       // K: chunks of a sequence
+    int vec, slices, heads_per_slice, blocks;   // blocks: of 16 channels of a head
+    float scale;
+    char *keys, *heads;         // workspace: operands of a group's keys and of a head, by chunk
+    // gradient
+    const void *dy;
+    const float *dstate_out;
+    void *dq, *dk, *dv, *dbeta;
+    float *dg, *dstate;
+    int64_t dy_ld, dq_ld, dk_ld, dv_ld, dg_ld, dbeta_ld;
+    int PP;                     // channels of a head in the workspace
+    float *bound[2];            // [n, h][K][PP][SP]: the state in front of every chunk, the gradient of that behind it
+    float *rows[2];             // [n, h][K * 64][PP]: Y and E
+};
+
+// ---- operands in the workspace -------------------------------------------------
+template <typename T> constexpr int kFrag = 64 * 8 * (int)sizeof(T);
+// K (4 x SP/32), Q (the same), K^T and, for the gradient, Q^T (SP/16 x 2)
+template <typename T, int SP> constexpr int64_t keys_bytes(bool grad) { return (int64_t)(grad ? 4 : 3) * (SP / 8) * kFrag<T>; }
+// what a head adds: -N beta of three terms, M of two, c; gradient: -N beta, (-N beta')^T and M^T of three terms
+template <typename T> constexpr int kN = 3;
+template <> constexpr int kN<float> = 1;
+template <typename T> constexpr int kM = 2;
+template <> constexpr int kM<float> = 1;
+struct ChunkScalars {
+    float from_start[kDQ], to_end[kDQ], beta[kDQ];
+    double cum[kDQ];
+};
+template <typename T> constexpr int64_t head_bytes(bool grad)
+{
+    return (int64_t)(grad ? 3 * kN<T> : kN<T> + kM<T>) * kTri * kFrag<T> + (int64_t)sizeof(ChunkScalars);
+}
+
+SEQ_DEV void put_frag(char *at, int lane, bf16x8 f) { reinterpret_cast<bf16x8 *>(at)[lane] = f; }
+SEQ_DEV void put_frag(char *at, int lane, const Frag<float>::type &f)
+{
+    f32x4 *p = reinterpret_cast<f32x4 *>(at) + lane;
+    p[0] = f32x4{f.v[0], f.v[1], f.v[2], f.v[3]};
+    p[64] = f32x4{f.v[4], f.v[5], f.v[6], f.v[7]};
+}
+template <typename T> SEQ_DEV typename Frag<T>::type get_frag(const char *at, int lane)
+{
+    if constexpr (sizeof(T) == 2) {
+        return reinterpret_cast<const bf16x8 *>(at)[lane];
+    } else {
+        const f32x4 *p = reinterpret_cast<const f32x4 *>(at) + lane;
+        const f32x4 a = p[0], b = p[64];
+        Frag<float>::type f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f.v[e] = a[e], f.v[4 + e] = b[e];
+        return f;
+    }
+}
+
+// two results of 16 rows as an operand
+template <typename T, int NS> SEQ_DEV void stack(f32x4 a, f32x4 b, Split<T, NS> &s)
+{
+    const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    make_split(v, s);
+}
+
+// a b of terms, up to those that the last term of the longer one is worth
+template <typename T, int NA, int NB>
+SEQ_DEV f32x4 mma_terms(const Split<T, NA> &a, const Split<T, NB> &b, f32x4 c)
+{
+    constexpr int most = NA > NB ? NA : NB;
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            if (i + j < most) c = mma(a.f[i], b.f[j], c);
+    return c;
+}
+
+// Operand (row tile i, columns 32 p ..) of a lower triangular matrix, and of an
+// upper triangular one, among the six that are not all zeros.
+SEQ_DEV constexpr int lower(int i, int p) { return i < 2 ? i : 2 * i - 2 + p; }
+SEQ_DEV constexpr int upper(int i, int p) { return i < 2 ? 2 * i + p : 2 + i; }
+
+// Columns k0 .. of 64 tokens as rows: tokens t0 + 4q .., t0 + 16 + 4q .. of key
+// 32 s + 8 (r / 4) + 4 a + r % 4 for row r = lane % 16
+SEQ_DEV bf16x8 read_keys(const bf16_t *t, int ld, int t0, int s, int a, int lane)
+{
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
+    const bf16_t *p = t + (t0 + (lane >> 4) * 4 + ((lane & 15) >> 2)) * ld + 32 * s + 8 * (lane & 3) + 4 * a;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 16 * ld));
+    return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+SEQ_DEV Frag<float>::type read_keys(const float *t, int ld, int t0, int s, int a, int lane)
+{
+    const int r = lane & 15;
+    const float *p = t + (t0 + (lane >> 4) * 4) * ld + 32 * s + 8 * (r >> 2) + 4 * a + (r & 3);
+    Frag<float>::type f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f.v[e] = p[e * ld], f.v[4 + e] = p[(16 + e) * ld];
+    return f;
+}
+
+// ---- what a chunk can do without its state ---------------------------------------
+template <typename T, int SP> struct PrepareShared {
+    static constexpr int LD = Tile<T, kDQ, SP>::LD;
+    static constexpr int TL = kDQ + 4;
+    T k[kDQ * LD], q[kDQ * LD];
+    float t[kDQ * TL];          // [j][i]: T transposed; gradient: N and M, transposed, in turn
+    float inv[4][16][20];       // [block][j][m]: the inverse of a block of 1 + beta T on the diagonal, transposed
+    float beta[kDQ];
+    double cum[kDQ];
+};
+
+// One chunk of one group: 4 waves, wave I owns the rows 16 I .. of T, N and M.
+// Everything is formed transposed (result rows j, columns i), so that the rows
+// of the operands come out as they are stored.  The inverse is that of forward
+// substitution by blocks of 16 (stable also where keys repeat): row blocks of N
+// do not depend on each other, N_IJ = (T_IJ - sum_{J<M<=I} N_IM beta T_MJ) (1 +
+// beta T_JJ)^-1, on the fp32 matrix instructions.
+template <typename T, int SP, bool GRAD>
+__global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaParams p)
+{
+    typedef PrepareShared<T, SP> Shared;
+    constexpr int LD = Shared::LD, TL = Shared::TL, KS = SP / 32;
+    __shared__ __align__(16) Shared sh;
+    const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q4 = (lane >> 4) * 4;
+    const int64_t chunk = blockIdx.x / ((int64_t)p.G * p.slices);        // n K + c
+    const int gs = (int)(blockIdx.x - chunk * p.G * p.slices), grp = gs / p.slices, slice = gs - grp * p.slices;
+    const int64_t n = chunk / p.K, t0 = (chunk - n * p.K) * kDQ, len = seq_len(p.lengths, n, p.L);
+    if (t0 >= len) return;
+    const int live = (int)(len - t0 < kDQ ? len - t0 : kDQ);
+    {
+        Tile<T, kDQ, SP> a, b;
+        a.load((const T *)p.k + (n * p.L + t0) * p.k_ld + (int64_t)grp * p.S, p.k_ld, live, p.S, p.vec);
+        b.load((const T *)p.q + (n * p.L + t0) * p.q_ld + (int64_t)grp * p.S, p.q_ld, live, p.S, p.vec);
+        a.store(sh.k);
+        b.store(sh.q);
+    }
+    __syncthreads();
+    if (slice == 0) {
+        char *at = p.keys + (chunk * p.G + grp) * keys_bytes<T, SP>(GRAD);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            put_frag(at + (w * KS + s) * kFrag<T>, lane, read_rows(sh.k, LD, 16 * w, 32 * s, lane));
+            put_frag(at + (4 * KS + w * KS + s) * kFrag<T>, lane, read_rows(sh.q, LD, 16 * w, 32 * s, lane));
+        }
+        at += 8 * KS * kFrag<T>;
+        for (int f = w; f < 4 * KS; f += 4) {       // (s, a, pair of token tiles)
+            put_frag(at + f * kFrag<T>, lane, read_keys(sh.k, LD, 32 * (f & 1), f >> 2, f >> 1 & 1, lane));
+            if (GRAD) put_frag(at + (4 * KS + f) * kFrag<T>, lane, read_keys(sh.q, LD, 32 * (f & 1), f >> 2, f >> 1 & 1, lane));
+        }
+    }
+    // k_j . k_i and k_j . q_i: rows j of tile J, columns i of tile w
+    f32x4 kk[4], kq[4];
+#pragma unroll
+    for (int J = 0; J < 4; ++J) {
+        kk[J] = kq[J] = f32x4{0, 0, 0, 0};
+        if (J > w) continue;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const typename Frag<T>::type a = read_rows(sh.k, LD, 16 * J, 32 * s, lane);
+            kk[J] = mma(a, read_rows(sh.k, LD, 16 * w, 32 * s, lane), kk[J]);
+            kq[J] = mma(a, read_rows(sh.q, LD, 16 * w, 32 * s, lane), kq[J]);
+        }
+    }
+    const int per = p.H / p.G, h0 = grp * per + slice * p.heads_per_slice;
+    const int h1 = min(h0 + p.heads_per_slice, (grp + 1) * per);
+    const int i = 16 * w + l16;
+    for (int h = h0; h < h1; ++h) {
+        char *at = p.heads + (chunk * p.H + h) * head_bytes<T>(GRAD);
+        if (w == 0) {
+            const int64_t row = n * p.L + t0 + lane;
+            const float g = lane < live ? p.g[row * p.g_ld + h] : 0.0f;
+            const float beta = lane < live ? (float)((const T *)p.beta)[row * p.beta_ld + h] : 0.0f;
+            const double cum = wave_prefix((double)(g < -1e5f ? -1e5f : g)), end = wave_last(cum);
+            sh.cum[lane] = cum;
+            sh.beta[lane] = beta;
+            ChunkScalars *cs = reinterpret_cast<ChunkScalars *>(at + head_bytes<T>(GRAD) - sizeof(ChunkScalars));
+            cs->from_start[lane] = expf((float)cum);
+            cs->to_end[lane] = expf((float)(end - cum));
+            cs->beta[lane] = beta;
+            cs->cum[lane] = cum;
+        }
+        __syncthreads();
+        f32x4 tt[4], mm[4], beta[4];
+        const double ci = sh.cum[i];
+#pragma unroll
+        for (int J = 0; J < 4; ++J) {
+            beta[J] = *reinterpret_cast<const f32x4 *>(sh.beta + 16 * J + q4);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int j = 16 * J + q4 + r;
+                const float decay = j <= i ? expf((float)(ci - sh.cum[j])) : 0.0f;
+                tt[J][r] = j < i ? kk[J][r] * decay : 0.0f;
+                mm[J][r] = j <= i ? kq[J][r] * decay * p.scale : 0.0f;
+                sh.t[j * TL + i] = tt[J][r];
+            }
+        }
+        __syncthreads();
+        // column l16 of (1 + beta T_ww)^-1, by forward substitution
+        {
+            float x[16];
+#pragma unroll
+            for (int m = 0; m < 16; ++m) x[m] = m == l16 ? 1.0f : 0.0f;
+#pragma unroll
+            for (int l = 0; l < 15; ++l) {
+#pragma unroll
+                for (int m = l + 1; m < 16; ++m)
+                    x[m] = fmaf(-sh.t[(16 * w + l) * TL + 16 * w + m] * sh.beta[16 * w + m], x[l], x[m]);
+            }
+            if (lane < 16) {
+#pragma unroll
+                for (int m = 0; m < 16; m += 4)
+                    *reinterpret_cast<f32x4 *>(&sh.inv[w][l16][m]) = f32x4{x[m], x[m + 1], x[m + 2], x[m + 3]};
+            }
+        }
+        __syncthreads();
+        f32x4 nn[4], nb[4];     // N, and -beta N, transposed
+#pragma unroll
+        for (int J = 3; J >= 0; --J) {
+            nn[J] = nb[J] = f32x4{0, 0, 0, 0};
+            if (J > w) continue;
+            f32x4 rhs = tt[J];
+#pragma unroll
+            for (int M = 3; M > J; --M) {
+                if (M > w) continue;
+                const f32x4 a = *reinterpret_cast<const f32x4 *>(sh.t + (16 * J + l16) * TL + 16 * M + q4);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) rhs = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], nb[M][r], rhs, 0, 0, 0);
+            }
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(&sh.inv[J][l16][q4]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) nn[J] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], rhs[r], nn[J], 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) nb[J][r] = -beta[J][r] * nn[J][r];
+        }
+#pragma unroll
+        for (int P = 0; P < 2; ++P) {
+            if (2 * P > w) continue;
+            Split<T, kN<T>> s;
+            stack(nb[2 * P], nb[2 * P + 1], s);
+#pragma unroll
+            for (int e = 0; e < kN<T>; ++e) put_frag(at + (lower(w, P) * kN<T> + e) * kFrag<T>, lane, s.f[e]);
+        }
+        at += kTri * kN<T> * kFrag<T>;
+        if constexpr (!GRAD) {
+#pragma unroll
+            for (int P = 0; P < 2; ++P) {
+                if (2 * P > w) continue;
+                Split<T, kM<T>> s;
+                stack(mm[2 * P] * beta[2 * P], mm[2 * P + 1] * beta[2 * P + 1], s);
+#pragma unroll
+                for (int e = 0; e < kM<T>; ++e) put_frag(at + (lower(w, P) * kM<T> + e) * kFrag<T>, lane, s.f[e]);
+            }
+        } else {
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                __syncthreads();
+#pragma unroll
+                for (int J = 0; J < 4; ++J)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) sh.t[(16 * J + q4 + r) * TL + i] = which ? mm[J][r] : nn[J][r];
+                __syncthreads();
+#pragma unroll
+                for (int P = 0; P < 2; ++P) {
+                    if (2 * P + 1 < w) continue;
+                    f32x4 v[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        v[e] = *reinterpret_cast<const f32x4 *>(sh.t + i * TL + 32 * P + 16 * e + q4);
+                        if (!which) v[e] = v[e] * -beta[2 * P + e];
+                    }
+                    Split<T, kN<T>> s;
+                    stack(v[0], v[1], s);
+#pragma unroll
+                    for (int e = 0; e < kN<T>; ++e) put_frag(at + (upper(w, P) * kN<T> + e) * kFrag<T>, lane, s.f[e]);
+                }
+                at += kTri * kN<T> * kFrag<T>;
+            }
+        }
+        __syncthreads();        // cum, beta and t are the next head's
+    }
+}
+
+// ---- the state, chunk by chunk -----------------------------------------------------
+// Workgroups in XCD order: neighbours share operands, and so an L2.
+SEQ_DEV int64_t unit_of(int64_t block, int64_t units)
+{
+    const int64_t per = (units + 7) / 8;
+    return (block & 7) * per + (block >> 3);
+}
+
+// A state tile pair s: key 32 s + 8q + 4a + r in register [2s + a][r] of channel lane % 16
+template <int SP> SEQ_DEV void load_state(const float *state, bool have, int S, int lane, f32x4 (&st)[SP / 16])
+{
+    const int q8 = (lane >> 4) * 8;
+#pragma unroll
+    for (int i = 0; i < SP / 16; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int key = 32 * (i >> 1) + q8 + 4 * (i & 1) + r;
+            st[i][r] = have && key < S ? state[key] : 0.0f;
+        }
+}
+template <int SP> SEQ_DEV void store_state(float *state, bool have, int S, int lane, const f32x4 (&st)[SP / 16])
+{
+    const int q8 = (lane >> 4) * 8;
+#pragma unroll
+    for (int i = 0; i < SP / 16; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int key = 32 * (i >> 1) + q8 + 4 * (i & 1) + r;
+            if (have && key < S) state[key] = st[i][r];
+        }
+}
+
+// The forward pass (OUT: y and the last state) or the gradient's pass over the
+// states (the state in front of every chunk, and Y).
+template <typename T, int SP, bool OUT> SEQ_DEV void delta_forward(const DeltaParams &p, int64_t unit, int lane)
+{
+    constexpr int KS = SP / 32, NT = OUT ? kM<T> : 1;
+    const int l16 = lane & 15, q4 = (lane >> 4) * 4;
+    const int64_t nh = unit / p.blocks, n = nh / p.H;
+    const int h = (int)(nh - n * p.H), grp = h / (p.H / p.G), ch = (int)(unit - nh * p.blocks) * 16 + l16;
+    const bool mine = ch < p.P;
+    const int64_t len = seq_len(p.lengths, n, p.L);
+    const T *vg = (const T *)p.v + n * p.L * p.v_ld + (int64_t)h * p.P + ch;
+    T *yg = (T *)p.y + n * p.L * p.y_ld + (int64_t)h * p.P + ch;
+    f32x4 st[SP / 16];
+    load_state<SP>(p.state + (nh * p.P + ch) * p.S, p.state && mine, p.S, lane, st);
+    const int live = (int)((len + kDQ - 1) / kDQ);
+    for (int c = 0; c < live; ++c) {
+        const char *keys = p.keys + ((n * p.K + c) * p.G + grp) * keys_bytes<T, SP>(!OUT);
+        const char *head = p.heads + ((n * p.K + c) * p.H + h) * head_bytes<T>(!OUT);
+        const ChunkScalars *cs = reinterpret_cast<const ChunkScalars *>(head + head_bytes<T>(!OUT) - sizeof(ChunkScalars));
+        const int64_t t0 = (int64_t)c * kDQ;
+        const int rows = (int)(len - t0 < kDQ ? len - t0 : kDQ);
+        if constexpr (!OUT) {
+            float *b = p.bound[0] + ((nh * p.K + c) * p.PP + ch) * SP + (lane >> 4) * 8;
+#pragma unroll
+            for (int i = 0; i < SP / 16; ++i) *reinterpret_cast<f32x4 *>(b + 32 * (i >> 1) + 4 * (i & 1)) = st[i];
+        }
+        Split<T, kN<T>> sp[KS];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) stack(st[2 * s], st[2 * s + 1], sp[s]);
+        f32x4 z[4], grow[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            grow[t] = *reinterpret_cast<const f32x4 *>(cs->from_start + 16 * t + q4);
+            f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                Split<T, 1> a;
+                a.f[0] = get_frag<T>(keys + (t * KS + s) * kFrag<T>, lane);
+                acc = mma_terms(a, sp[s], acc);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * t + q4 + r;
+                const float v = mine && row < rows ? (float)vg[(t0 + row) * p.v_ld] : 0.0f;
+                z[t][r] = fmaf(-grow[t][r], acc[r], v);
+            }
+        }
+        Split<T, kN<T>> zs[2];
+        stack(z[0], z[1], zs[0]);
+        stack(z[2], z[3], zs[1]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int P = 0; P <= t / 2; ++P) {
+                Split<T, kN<T>> a;
+#pragma unroll
+                for (int e = 0; e < kN<T>; ++e) a.f[e] = get_frag<T>(head + (lower(t, P) * kN<T> + e) * kFrag<T>, lane);
+                z[t] = mma_terms(a, zs[P], z[t]);        // Y
+            }
+        if constexpr (OUT) {
+            Split<T, NT> ys[2];
+            stack(z[0], z[1], ys[0]);
+            stack(z[2], z[3], ys[1]);
+            const char *qs = keys + 4 * KS * kFrag<T>, *ms = head + kTri * kN<T> * kFrag<T>;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    const typename Frag<T>::type a = get_frag<T>(qs + (t * KS + s) * kFrag<T>, lane);
+#pragma unroll
+                    for (int e = 0; e < NT; ++e) acc = mma(a, sp[s].f[e], acc);
+                }
+                acc = acc * (grow[t] * p.scale);
+#pragma unroll
+                for (int P = 0; P <= t / 2; ++P) {
+                    Split<T, NT> a;
+#pragma unroll
+                    for (int e = 0; e < NT; ++e) a.f[e] = get_frag<T>(ms + (lower(t, P) * NT + e) * kFrag<T>, lane);
+                    acc = mma_terms(a, ys[P], acc);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * t + q4 + r;
+                    if (mine && row < rows) yg[(t0 + row) * p.y_ld] = (T)acc[r];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    p.rows[0][((nh * p.K + c) * kDQ + 16 * t + q4 + r) * p.PP + ch] = z[t][r];
+        }
+        Split<T, kN<T>> us[2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            z[t] = z[t] * (*reinterpret_cast<const f32x4 *>(cs->beta + 16 * t + q4) *
+                           *reinterpret_cast<const f32x4 *>(cs->to_end + 16 * t + q4));
+        stack(z[0], z[1], us[0]);
+        stack(z[2], z[3], us[1]);
+        const float total = cs->from_start[kDQ - 1];
+        const char *kt = keys + 8 * KS * kFrag<T>;
+#pragma unroll
+        for (int i = 0; i < SP / 16; ++i) {
+            st[i] = st[i] * total;
+#pragma unroll
+            for (int P = 0; P < 2; ++P) {
+                Split<T, 1> a;
+                a.f[0] = get_frag<T>(kt + (i * 2 + P) * kFrag<T>, lane);
+                st[i] = mma_terms(a, us[P], st[i]);
+            }
+        }
+    }
+    if constexpr (OUT) {
+        if (mine)
+            for (int64_t t = len + (lane >> 4); t < p.L; t += 4) yg[t * p.y_ld] = (T)0.0f;
+        store_state<SP>(p.state_out + (nh * p.P + ch) * p.S, p.state_out && mine, p.S, lane, st);
+    }
+}
+
+template <typename T, int SP> __global__ void __launch_bounds__(64) delta_fwd_kernel(DeltaParams p)
+{
+    const int64_t units = (int64_t)p.N * p.H * p.blocks, unit = unit_of(blockIdx.x, units);
+    if (unit < units) delta_forward<T, SP, true>(p, unit, threadIdx.x);
+}
+
+// ---- one token -----------------------------------------------------------------------
+// With s = S k, o = S q of the old state and d = k . q, all in one pass over it:
+// y = v - e^g s, the output scale (e^g o + beta d y), the new state e^g S + beta y k^T.
+// A lane holds four keys of kDeltaRows channels; `lpr` lanes share a channel.
+constexpr int kDeltaRows = 4;
+
+template <typename T, bool VEC> __global__ void __launch_bounds__(256) delta_step_kernel(DeltaParams p, int lpr, int blocks)
+{
+    constexpr int V = 4, R = kDeltaRows;
+    const int lane = threadIdx.x & 63, w = wave_id();
+    const int64_t nh = blockIdx.x / blocks, n = nh / p.H;
+    const int blk = (int)(blockIdx.x - nh * blocks), h = (int)(nh - n * p.H), grp = h / (p.H / p.G);
+    const int per = 64 / lpr;                       // channels side by side in a wave
+    const int s0 = (lane & (lpr - 1)) * V;
+    const int ch0 = (blk * 4 + w) * R * per + lane / lpr;
+    const T *kg = (const T *)p.k + n * p.k_ld + (int64_t)grp * p.S, *qg = (const T *)p.q + n * p.q_ld + (int64_t)grp * p.S;
+    const T *vg = (const T *)p.v + n * p.v_ld + (int64_t)h * p.P;
+    T *yg = (T *)p.y + n * p.y_ld + (int64_t)h * p.P;
+    float st[R][V], k[V], q[V], v[R];
+#pragma unroll
+    for (int e = 0; e < R; ++e) {
+        const int ch = ch0 + e * per;
+        const float *s = p.state + (nh * p.P + ch) * p.S + s0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) st[e][i] = 0.0f;
+        if (ch < p.P) {
+            if (VEC) {
+                if (s0 < p.S) load_f32<float, V>(s, st[e]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (s0 + i < p.S) st[e][i] = s[i];
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        k[i] = s0 + i < p.S ? (float)kg[s0 + i] : 0.0f;
+        q[i] = s0 + i < p.S ? (float)qg[s0 + i] : 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < R; ++e) v[e] = ch0 + e * per < p.P ? (float)vg[ch0 + e * per] : 0.0f;
+    const float fade = expf(p.g[n * p.g_ld + h]), beta = (float)((const T *)p.beta)[n * p.beta_ld + h];
+    float d = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) d = fmaf(k[i], q[i], d);
+    for (int o = lpr >> 1; o > 0; o >>= 1) d += __shfl_xor(d, o);
+#pragma unroll
+    for (int e = 0; e < R; ++e) {
+        float a = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) a = fmaf(st[e][i], k[i], a), b = fmaf(st[e][i], q[i], b);
+        for (int o = lpr >> 1; o > 0; o >>= 1) a += __shfl_xor(a, o), b += __shfl_xor(b, o);
+        const int ch = ch0 + e * per;
+        const float u = beta * fmaf(-fade, a, v[e]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) st[e][i] = fmaf(st[e][i], fade, u * k[i]);
+        if (ch < p.P) {
+            float *s = p.state_out + (nh * p.P + ch) * p.S + s0;
+            if (VEC) {
+                if (s0 < p.S) stream_f32<float, V>(s, st[e]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (s0 + i < p.S) s[i] = st[e][i];
+            }
+            if (s0 == 0) yg[ch] = (T)(p.scale * fmaf(fade, b, u * d));
+        }
+    }
+}
+
+}  // namespace convfwd

@@ -1,0 +1,232 @@
+// Host side of the gated delta rule (conv_delta_*): argument checks, workspace
+// layout, launches.
+#include <cmath>
+#include <cstdio>
+#include <cstdlib>
+#include <new>
+
+#include "../../include/convfwd.h"
+#include "delta_kernels.h"
+#include "seq_host.h"
+#include "status.h"
+
+struct conv_delta_plan {
+    conv_delta_desc_t desc;
+    int64_t esz;
+    int SP, K, blocks;                   // padded keys, chunks, blocks of 16 channels of a head
+    int slices, heads_per_slice;         // of a group's heads, for what a chunk does without its state
+    int64_t ws_bytes, o_heads;
+    char text[256];
+};
+
+namespace convfwd {
+namespace {
+
+int64_t up(int64_t v) { return (v + 255) / 256 * 256; }
+
+template <typename T> int64_t keys_of(int SP, bool grad)
+{
+    return SP == 32 ? keys_bytes<T, 32>(grad) : SP == 64 ? keys_bytes<T, 64>(grad)
+         : SP == 128 ? keys_bytes<T, 128>(grad) : keys_bytes<T, 256>(grad);
+}
+int64_t keys_of(const conv_delta_desc_t &d, int SP, bool grad)
+{
+    return d.dtype == CONV_DT_BF16 ? keys_of<bf16_t>(SP, grad) : keys_of<float>(SP, grad);
+}
+int64_t head_of(const conv_delta_desc_t &d, bool grad)
+{
+    return d.dtype == CONV_DT_BF16 ? head_bytes<bf16_t>(grad) : head_bytes<float>(grad);
+}
+
+int64_t state_grid(int64_t units) { return (units + 7) / 8 * 8; }
+
+template <typename T, int SP> void launch_fwd(const DeltaParams &p, int64_t units, hipStream_t s)
+{
+    if (p.K > 0)
+        hipLaunchKernelGGL((delta_prepare_kernel<T, SP, false>), dim3((unsigned)((int64_t)p.N * p.K * p.G * p.slices)), dim3(256),
+                           0, s, p);
+    hipLaunchKernelGGL((delta_fwd_kernel<T, SP>), dim3((unsigned)state_grid(units)), dim3(64), 0, s, p);
+}
+
+template <typename T> void launch_delta(int SP, const DeltaParams &p, int64_t units, hipStream_t s)
+{
+    if (SP == 32) return launch_fwd<T, 32>(p, units, s);
+    if (SP == 64) return launch_fwd<T, 64>(p, units, s);
+    if (SP == 128) return launch_fwd<T, 128>(p, units, s);
+    return launch_fwd<T, 256>(p, units, s);
+}
+
+// A step's lanes for the keys of a channel, and workgroups for the channels of a head.
+struct StepShape {
+    int lanes, blocks;
+};
+
+StepShape step_shape(const conv_delta_desc_t &d)
+{
+    int lanes = 1;
+    while (lanes * 4 < d.S) lanes *= 2;
+    const int64_t per = 4 * kDeltaRows * (64 / lanes);
+    return {lanes, (int)((d.P + per - 1) / per)};
+}
+
+void delta_params(const conv_delta_plan &pl, DeltaParams *p)
+{
+    const conv_delta_desc_t &d = pl.desc;
+    *p = DeltaParams{};
+    p->N = (int)d.N; p->L = d.L; p->H = (int)d.H; p->P = (int)d.P; p->G = (int)d.G; p->S = (int)d.S;
+    p->K = pl.K; p->blocks = pl.blocks; p->slices = pl.slices; p->heads_per_slice = pl.heads_per_slice;
+    p->scale = (float)d.scale;
+}
+
+}  // namespace
+}  // namespace convfwd
+
+using namespace convfwd;
+
+extern "C" {
+
+conv_status_t conv_delta_create(const conv_delta_desc_t *desc, conv_delta_plan_t **plan)
+{
+    if (!plan) return fail(CONV_ERR_INVALID_ARG, "plan is NULL");
+    *plan = nullptr;
+    if (!desc) return fail(CONV_ERR_INVALID_ARG, "descriptor is NULL");
+    const conv_delta_desc_t &d = *desc;
+    if (d.dtype != CONV_DT_F32 && d.dtype != CONV_DT_BF16) return fail(CONV_ERR_INVALID_ARG, "unknown dtype %d", d.dtype);
+    if (d.reserved != 0) return fail(CONV_ERR_INVALID_ARG, "reserved must be 0");
+    if (!std::isfinite((float)d.scale)) return fail(CONV_ERR_INVALID_ARG, "scale must be a finite fp32 number");
+    if (d.N < 0 || d.L < 0 || d.H < 1 || d.P < 1 || d.G < 1 || d.S < 1)
+        return fail(CONV_ERR_INVALID_ARG, "need N, L >= 0 and H, P, G, S >= 1 (got %lld, %lld, %lld, %lld, %lld, %lld)",
+                    (long long)d.N, (long long)d.L, (long long)d.H, (long long)d.P, (long long)d.G, (long long)d.S);
+    if (d.H % d.G != 0)
+        return fail(CONV_ERR_INVALID_ARG, "H = %lld is not a multiple of G = %lld", (long long)d.H, (long long)d.G);
+    if (d.S > 256) return fail(CONV_ERR_UNSUPPORTED, "more than 256 keys (S = %lld)", (long long)d.S);
+    if (d.P > 65536) return fail(CONV_ERR_UNSUPPORTED, "more than 65536 channels of a head (P = %lld)", (long long)d.P);
+    if (d.N > kMaxDim || d.L > kMaxDim || d.H > kMaxDim) return fail(CONV_ERR_UNSUPPORTED, "N, L or H above 2^30");
+    conv_delta_plan *pl = new (std::nothrow) conv_delta_plan();
+    if (!pl) return fail(CONV_ERR_NOMEM, "plan allocation failed");
+    pl->desc = d;
+    pl->esz = d.dtype == CONV_DT_BF16 ? 2 : 4;
+    pl->SP = d.S <= 32 ? 32 : d.S <= 64 ? 64 : d.S <= 128 ? 128 : 256;
+    pl->K = (int)((d.L + kDQ - 1) / kDQ);
+    pl->blocks = (int)((d.P + 15) / 16);
+    // What neither a prompt nor a step could launch; every call checks its own form.
+    const double units = (double)d.N * d.H * pl->blocks, chunks = (double)d.N * pl->K;
+    const double ws = chunks * ((double)d.G * keys_of(d, pl->SP, true) + (double)d.H * head_of(d, true)) +
+                      2.0 * (double)d.N * d.H * pl->K * (d.P + 31.0) * (pl->SP + kDQ) * 4.0;
+    if ((!one_launch(units, 64) && !one_launch((double)d.N * d.H * step_shape(d).blocks, 256)) || ws >= kMaxBytes) {
+        delete pl;
+        return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
+    }
+    const int64_t wgs = std::max<int64_t>(1, d.N * pl->K * d.G), hpg = d.H / d.G;
+    // two workgroups of the preparation fit a compute unit
+    const int64_t want = std::max<int64_t>(1, std::min(hpg, 512 / wgs));
+    pl->heads_per_slice = (int)((hpg + want - 1) / want);
+    pl->slices = (int)((hpg + pl->heads_per_slice - 1) / pl->heads_per_slice);
+    pl->o_heads = up(d.N * pl->K * d.G * keys_of(d, pl->SP, false));
+    pl->ws_bytes = pl->o_heads + up(d.N * pl->K * d.H * head_of(d, false));
+    snprintf(pl->text, sizeof(pl->text),
+             "delta %s N=%lld L=%lld H=%lld P=%lld G=%lld S=%lld(%d), %d chunks of %d, %d slices of %d heads",
+             d.dtype == CONV_DT_BF16 ? "bf16" : "f32", (long long)d.N, (long long)d.L, (long long)d.H, (long long)d.P,
+             (long long)d.G, (long long)d.S, pl->SP, pl->K, kDQ, pl->slices, pl->heads_per_slice);
+    if (getenv("CONVFWD_LOG")) fprintf(stderr, "convfwd: %s\n", pl->text);
+    *plan = pl;
+    return CONV_OK;
+}
+
+conv_status_t conv_delta_workspace_bytes(const conv_delta_plan_t *plan, int64_t *bytes)
+{
+    if (!plan || !bytes) return fail(CONV_ERR_INVALID_ARG, "plan or bytes is NULL");
+    *bytes = plan->ws_bytes;
+    return CONV_OK;
+}
+
+// 16-byte accesses to the keys
+static bool delta_vector(const conv_delta_plan &pl, const Rows *t, int n)
+{
+    bool ok = pl.desc.S * pl.esz % 16 == 0;
+    for (int i = 0; i < n; ++i) ok = ok && vector_rows(t[i]);
+    return ok;
+}
+
+static conv_status_t delta_forward_call(const conv_delta_plan_t *plan, const conv_delta_args_t *a, bool step, void *ws,
+                                        int64_t ws_bytes, void *stream)
+{
+    if (!plan || !a) return fail(CONV_ERR_INVALID_ARG, "plan or args is NULL");
+    const conv_delta_desc_t &d = plan->desc;
+    const int64_t L = step ? 1 : d.L, e = plan->esz, rows = d.N * L, need = step ? 0 : plan->ws_bytes;
+    if (step && a->lengths) return fail(CONV_ERR_INVALID_ARG, "a step takes no lengths");
+    const int64_t hp = d.H * d.P, gs = d.G * d.S, states = d.N * hp * d.S;
+    const Rows in[] = {{"q", a->q, rows, gs, or_packed(a->q_ld, gs), e},
+                       {"k", a->k, rows, gs, or_packed(a->k_ld, gs), e},
+                       {"v", a->v, rows, hp, or_packed(a->v_ld, hp), e},
+                       {"g", a->g, rows, d.H, or_packed(a->g_ld, d.H), 4},
+                       {"beta", a->beta, rows, d.H, or_packed(a->beta_ld, d.H), e},
+                       {"lengths", a->lengths, 1, d.N, std::max<int64_t>(1, d.N), 4},
+                       {"state", a->state, 1, states, states, 4}};
+    const Rows out[] = {{"y", a->y, rows, hp, or_packed(a->y_ld, hp), e},
+                        {"state_out", a->state_out, 1, states, states, 4},
+                        {"workspace", ws, 1, need, std::max<int64_t>(1, need), 1}};
+    conv_status_t st = check_rows(in, 7);
+    if (st == CONV_OK) st = check_rows(out, 2);
+    if (st != CONV_OK) return st;
+    if (d.N == 0) return CONV_OK;
+    if (L > 0 && (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->y))
+        return fail(CONV_ERR_INVALID_ARG, "q, k, v, g, beta or y is NULL");
+    if (step && (!a->state || !a->state_out)) return fail(CONV_ERR_INVALID_ARG, "state or state_out is NULL");
+    if ((st = check_workspace(ws, ws_bytes, need)) != CONV_OK) return st;
+    // a step may update the state in place: each lane owns its part
+    const bool in_place = step && a->state == a->state_out;
+    if ((st = check_overlap(out, 3, in, in_place ? 6 : 7)) != CONV_OK) return st;
+    if (L == 0 && !a->state_out) return CONV_OK;
+    DeltaParams p;
+    delta_params(*plan, &p);
+    p.L = L;
+    p.q = a->q; p.k = a->k; p.v = a->v; p.g = a->g; p.beta = a->beta; p.state = a->state; p.lengths = a->lengths;
+    p.y = a->y; p.state_out = a->state_out;
+    p.q_ld = stride(in[0]); p.k_ld = stride(in[1]); p.v_ld = stride(in[2]); p.g_ld = stride(in[3]);
+    p.beta_ld = stride(in[4]); p.y_ld = stride(out[0]);
+    hipStream_t s = (hipStream_t)stream;
+    (void)hipGetLastError();
+    if (step) {
+        const StepShape shape = step_shape(d);
+        const bool vec = d.S % 4 == 0 && ((uintptr_t)a->state | (uintptr_t)a->state_out) % 16 == 0;
+        if (!one_launch((double)(d.N * d.H) * shape.blocks, 256))
+            return fail(CONV_ERR_UNSUPPORTED, "N x H x P is too large for one launch");
+        const dim3 grid((unsigned)(d.N * d.H * shape.blocks));
+        if (d.dtype == CONV_DT_BF16) {
+            if (vec) hipLaunchKernelGGL((delta_step_kernel<bf16_t, true>), grid, dim3(256), 0, s, p, shape.lanes, shape.blocks);
+            else hipLaunchKernelGGL((delta_step_kernel<bf16_t, false>), grid, dim3(256), 0, s, p, shape.lanes, shape.blocks);
+        } else {
+            if (vec) hipLaunchKernelGGL((delta_step_kernel<float, true>), grid, dim3(256), 0, s, p, shape.lanes, shape.blocks);
+            else hipLaunchKernelGGL((delta_step_kernel<float, false>), grid, dim3(256), 0, s, p, shape.lanes, shape.blocks);
+        }
+        return launched();
+    }
+    p.keys = (char *)ws;
+    p.heads = (char *)ws + plan->o_heads;
+    const Rows vec[] = {in[0], in[1]};
+    p.vec = delta_vector(*plan, vec, 2);
+    const int64_t units = d.N * d.H * plan->blocks;
+    if (!one_launch((double)state_grid(units), 64) || !one_launch((double)d.N * plan->K * d.G * plan->slices, 256))
+        return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
+    if (d.dtype == CONV_DT_BF16) launch_delta<bf16_t>(plan->SP, p, units, s);
+    else launch_delta<float>(plan->SP, p, units, s);
+    return launched();
+}
+
+conv_status_t conv_delta_run(const conv_delta_plan_t *plan, const conv_delta_args_t *args, void *workspace,
+                             int64_t workspace_bytes, void *stream)
+{
+    return delta_forward_call(plan, args, false, workspace, workspace_bytes, stream);
+}
+
+conv_status_t conv_delta_step(const conv_delta_plan_t *plan, const conv_delta_args_t *args, void *stream)
+{
+    return delta_forward_call(plan, args, true, nullptr, 0, stream);
+}
+
+void conv_delta_destroy(conv_delta_plan_t *plan) { delete plan; }
+
+const char *conv_delta_describe(const conv_delta_plan_t *plan) { return plan ? plan->text : ""; }
+
+}  // extern "C"

@@ -1,6 +1,7 @@
 """The sequence operators: the short causal depthwise convolution
-(conv_causal_*) and the selective state space scan (conv_scan_*), each over
-prompts, token by token, and with its gradient.  Argument marshalling only; the
+(conv_causal_*), the selective state space scan (conv_scan_*) and the gated
+delta rule (conv_delta_*), each over prompts, token by token, and with its
+gradient.  Argument marshalling only; the
 computation and its definitions are in include/convfwd.h.
 """
 from ctypes import byref
@@ -9,7 +10,7 @@ from . import capi
 
 
 class _Plan:
-    """What both operators share: the plan's life, tensor checks, the device."""
+    """What the operators share: the plan's life, tensor checks, the device."""
 
     _plan = None
 
@@ -315,6 +316,79 @@ class SelectiveScan(_Plan):
         _with_workspace(torch, self.bwd_workspace_bytes, dev, away, lambda ws, n: capi.conv_scan_bwd_run(
             self._plan, byref(args), ws, n, stream))
         return got
+
+
+class DeltaRule(_Plan):
+    """A plan of the gated delta rule.  `problem` is a dict {"N", "L", "H", "P",
+    "G", "S"}: sequences, tokens, heads, channels of a head, groups of heads with
+    q and k in common, length of a key (up to 256).  scale: of the output, S ** -0.5
+    unless given."""
+
+    _describe = staticmethod(capi.conv_delta_describe)
+    _destroy = staticmethod(capi.conv_delta_destroy)
+
+    def __init__(self, problem, dtype, scale=None):
+        self.problem = dict(problem)
+        self.dtype, dt = _dtype(dtype)
+        N, L, H, P, G, S = (int(self.problem[k]) for k in ("N", "L", "H", "P", "G", "S"))
+        self.scale = max(S, 1) ** -0.5 if scale is None else float(scale)
+        self._plan = capi.conv_delta_create(capi.conv_delta_desc_t(dt, 0, N, L, H, P, G, S, self.scale))
+        self.q_shape = (N, L, G, S)
+        self.v_shape = (N, L, H, P)
+        self.g_shape = (N, L, H)
+        self.state_shape = (N, H, P, S)
+        self.workspace_bytes = capi.conv_delta_workspace_bytes(self._plan)
+
+    def _state(self, v, name, torch, dev):
+        return None if v is None else self._dense(v, self.state_shape, torch.float32, dev, name)
+
+    def _inputs(self, torch, dev, lead, q, k, v, g, beta):
+        """[(address, elements from token to token)] of the five inputs."""
+        t = self._type(torch)
+        gs, hp, hh = self.q_shape[2:], self.v_shape[2:], self.g_shape[2:]
+        return [self._rows(x, lead, inner, dt, dev, name) for x, inner, dt, name in (
+            (q, gs, t, "q"), (k, gs, t, "k"), (v, hp, t, "v"), (g, hh, torch.float32, "g"), (beta, hh, t, "beta"))]
+
+    def __call__(self, q, k, v, g, beta, state=None, lengths=None, out=None, state_out=None, stream=None):
+        """y (N, L, H, P) of q and k (N, L, G, S), v (N, L, H, P) and beta (N, L,
+        H) in the plan's dtype and g (N, L, H), the logarithms of the decays, in
+        float32.  state and state_out: float32 (N, H, P, S), before the first token
+        and, written, behind the last; lengths: int32 (N,).  q, k, v, g, beta and
+        out may be column ranges of wider tensors."""
+        import torch
+        dev = v.device
+        stream, away = self._on(torch, dev, stream)
+        if out is None:
+            out = self._new(torch, v, self.v_shape, away)
+        rows = self._inputs(torch, dev, self.v_shape[:2], q, k, v, g, beta)
+        yp, y_ld = self._rows(out, self.v_shape[:2], self.v_shape[2:], self._type(torch), dev, "out")
+        args = capi.conv_delta_args_t(
+            *(a for a, _ in rows), self._state(state, "state", torch, dev),
+            None if lengths is None else self._dense(lengths, self.v_shape[:1], torch.int32, dev, "lengths"), yp,
+            self._state(state_out, "state_out", torch, dev), *(ld for _, ld in rows), y_ld)
+        _with_workspace(torch, self.workspace_bytes, dev, away, lambda ws, n: capi.conv_delta_run(
+            self._plan, byref(args), ws, n, stream))
+        return out
+
+    def step(self, q, k, v, g, beta, state, out=None, stream=None):
+        """One token of every sequence: q and k (N, G, S), v and the returned y
+        (N, H, P), g and beta (N, H); state (N, H, P, S) is updated in place."""
+        import torch
+        dev = v.device
+        stream, away = self._on(torch, dev, stream)
+        lead = self.v_shape[:1]
+        if out is None:
+            out = self._new(torch, v, lead + self.v_shape[2:], away)
+        rows = self._inputs(torch, dev, lead, q, k, v, g, beta)
+        yp, y_ld = self._rows(out, lead, self.v_shape[2:], self._type(torch), dev, "out")
+        sp = self._dense(state, self.state_shape, torch.float32, dev, "state")
+        args = capi.conv_delta_args_t(*(a for a, _ in rows), sp, None, yp, sp, *(ld for _, ld in rows), y_ld)
+        if away is None:
+            capi.conv_delta_step(self._plan, byref(args), stream)
+        else:
+            with away:
+                capi.conv_delta_step(self._plan, byref(args), stream)
+        return out
 
 
 def _dtype(dtype):

@@ -505,6 +505,69 @@ conv_status_t conv_scan_bwd_run(const conv_scan_plan_t *plan, const conv_scan_bw
 void conv_scan_destroy(conv_scan_plan_t *plan);
 const char *conv_scan_describe(const conv_scan_plan_t *plan);
 
+/* ---- Gated delta rule ------------------------------------------------------
+ * A state that a step does not only fade and add to: what it holds under the
+ * token's key is replaced by the token's value, as far as beta says.  H heads of
+ * P channels, each head with a state of P x S; the heads h of group
+ * g = h / (H / G) share q and k.  Per token t
+ *
+ *   state = exp(g[t,h]) * state
+ *   state = state + beta[t,h] * (v[t,h,:] - state . k[t,g,:]) (outer) k[t,g,:]
+ *   y[t,h,:] = scale * state . q[t,g,:]
+ *
+ *   v, y : N x L x H x P        q, k : N x L x G x S
+ *   g    : N x L x H, float32 whatever the dtype;   beta : N x L x H
+ *   state, state_out : N x H x P x S, float32
+ * with *_ld elements from token to token (0 = the packed row) and L times that
+ * from sequence to sequence; q, k, v, beta, y in the descriptor's dtype.  Keys
+ * are taken as they are: beta times a key's squared length beyond 2 grows as the
+ * formula says, as does a g above 0; a g below -1e5 counts as that.  state, lengths
+ * and state_out are optional (NULL: zeros, all L, not written).  lengths as
+ * conv_causal: rows behind a length are not read, their y and gradients are
+ * zeros and the state stays.  States and sums are fp32.  Tokens are taken in
+ * chunks of 64, so a NaN or an infinity in a token's inputs may reach the y of
+ * all its sequence's tokens in its chunk, not only those behind it, and an
+ * infinity, of a state too, may come out as a NaN.  S <= 256, P <= 65536.
+ *
+ * A prompt goes through a caller-owned device workspace (16-byte aligned; the
+ * size may be 0, then it may be NULL).  Calls that overlap in time need
+ * workspaces of their own.  Alignment, overlap, ownership, threading, asynchrony
+ * and errors as conv_causal. */
+typedef struct {
+    int32_t dtype;         /* conv_dtype_t                                     */
+    int32_t reserved;      /* 0                                                */
+    int64_t N;             /* sequences, >= 0                                  */
+    int64_t L;             /* tokens of a sequence, >= 0                       */
+    int64_t H;             /* heads, a multiple of G                           */
+    int64_t P;             /* channels of a head, >= 1                         */
+    int64_t G;             /* groups, >= 1                                     */
+    int64_t S;             /* keys' length, 1..256                             */
+    double scale;          /* of y, finite in fp32                             */
+} conv_delta_desc_t;
+
+typedef struct {
+    const void *q, *k, *v;
+    const float *g;
+    const void *beta;
+    const float *state;
+    const int32_t *lengths;
+    void *y;
+    float *state_out;
+    int64_t q_ld, k_ld, v_ld, g_ld, beta_ld, y_ld;
+} conv_delta_args_t;
+
+typedef struct conv_delta_plan conv_delta_plan_t;   /* opaque */
+conv_status_t conv_delta_create(const conv_delta_desc_t *desc, conv_delta_plan_t **plan);
+conv_status_t conv_delta_workspace_bytes(const conv_delta_plan_t *plan, int64_t *bytes);
+conv_status_t conv_delta_run(const conv_delta_plan_t *plan, const conv_delta_args_t *args, void *workspace,
+                             int64_t workspace_bytes, void *stream);
+/* One token of each of the plan's N sequences (the plan's L plays no part):
+ * rows n of q, k, v, g, beta, y at n times their ld.  state and state_out are
+ * required and may be the same buffer; lengths must be NULL. */
+conv_status_t conv_delta_step(const conv_delta_plan_t *plan, const conv_delta_args_t *args, void *stream);
+void conv_delta_destroy(conv_delta_plan_t *plan);
+const char *conv_delta_describe(const conv_delta_plan_t *plan);
+
 /* Message of the last failed call on this thread ("" if none). */
 const char *conv_fwd_last_error(void);
 
