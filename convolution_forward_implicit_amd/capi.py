@@ -44,7 +44,7 @@ SEQUENCE_EXPORTED = ["conv_causal_create", "conv_causal_run", "conv_causal_step"
 
 # the gated delta rule
 DELTA_EXPORTED = ["conv_delta_create", "conv_delta_workspace_bytes", "conv_delta_run", "conv_delta_step",
-                  "conv_delta_destroy", "conv_delta_describe"]
+                  "conv_delta_bwd_workspace_bytes", "conv_delta_bwd_run", "conv_delta_destroy", "conv_delta_describe"]
 
 
 class conv_fwd_desc_t(ctypes.Structure):
@@ -99,6 +99,13 @@ class conv_delta_desc_t(ctypes.Structure):
 class conv_delta_args_t(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "g", "beta", "state", "lengths", "y", "state_out")] +
                 [(n, ctypes.c_int64) for n in ("q_ld", "k_ld", "v_ld", "g_ld", "beta_ld", "y_ld")])
+
+
+class conv_delta_bwd_args_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("dy", "q", "k", "v", "g", "beta", "state", "lengths", "dstate_out",
+                                                  "dq", "dk", "dv", "dg", "dbeta", "dstate")] +
+                [(n, ctypes.c_int64) for n in ("dy_ld", "q_ld", "k_ld", "v_ld", "g_ld", "beta_ld",
+                                                 "dq_ld", "dk_ld", "dv_ld", "dg_ld", "dbeta_ld")])
 
 
 class ConvError(RuntimeError):
@@ -217,6 +224,8 @@ def lib():
         L.conv_delta_workspace_bytes.argtypes = [P, ctypes.POINTER(I64)]
         L.conv_delta_run.argtypes = [P, ctypes.POINTER(conv_delta_args_t), P, I64, P]
         L.conv_delta_step.argtypes = [P, ctypes.POINTER(conv_delta_args_t), P]
+        L.conv_delta_bwd_workspace_bytes.argtypes = [P, ctypes.POINTER(I64)]
+        L.conv_delta_bwd_run.argtypes = [P, ctypes.POINTER(conv_delta_bwd_args_t), P, I64, P]
         L.conv_delta_destroy.argtypes = [P]
         L.conv_delta_destroy.restype = None
         L.conv_delta_describe.argtypes = [P]
@@ -566,6 +575,16 @@ def conv_delta_run(plan, args, workspace, workspace_bytes, stream=0):
 
 def conv_delta_step(plan, args, stream=0):
     _check(lib().conv_delta_step(plan, args, stream))
+
+
+def conv_delta_bwd_workspace_bytes(plan):
+    n = ctypes.c_int64()
+    _check(lib().conv_delta_bwd_workspace_bytes(plan, ctypes.byref(n)))
+    return n.value
+
+
+def conv_delta_bwd_run(plan, args, workspace, workspace_bytes, stream=0):
+    _check(lib().conv_delta_bwd_run(plan, args, workspace, workspace_bytes, stream))
 
 
 def conv_delta_destroy(plan):

@@ -65,6 +65,7 @@ struct DeltaParams {
     int PP;                     // channels of a head in the workspace
     float *bound[2];            // [n, h][K][PP][SP]: the state in front of every chunk, the gradient of that behind it
     float *rows[2];             // [n, h][K * 64][PP]: Y and E
+    float *part[2];             // [slice][N L][G][S]: dq and dk of a slice's heads
 };
 
 // ---- operands in the workspace -------------------------------------------------
@@ -492,6 +493,475 @@ template <typename T, int SP> __global__ void __launch_bounds__(64) delta_fwd_ke
 {
     const int64_t units = (int64_t)p.N * p.H * p.blocks, unit = unit_of(blockIdx.x, units);
     if (unit < units) delta_forward<T, SP, true>(p, unit, threadIdx.x);
+}
+
+// The gradient of the state, from the last chunk to the first: that of the state
+// behind every chunk, and E.
+template <typename T, int SP> SEQ_DEV void delta_backward(const DeltaParams &p, int64_t unit, int lane)
+{
+    constexpr int KS = SP / 32;
+    const int l16 = lane & 15, q4 = (lane >> 4) * 4;
+    const int64_t nh = unit / p.blocks, n = nh / p.H;
+    const int h = (int)(nh - n * p.H), grp = h / (p.H / p.G), ch = (int)(unit - nh * p.blocks) * 16 + l16;
+    const bool mine = ch < p.P;
+    const int64_t len = seq_len(p.lengths, n, p.L);
+    const T *dyg = (const T *)p.dy + n * p.L * p.dy_ld + (int64_t)h * p.P + ch;
+    f32x4 st[SP / 16];
+    load_state<SP>(p.dstate_out + (nh * p.P + ch) * p.S, p.dstate_out && mine, p.S, lane, st);
+    for (int c = (int)((len + kDQ - 1) / kDQ) - 1; c >= 0; --c) {
+        const char *keys = p.keys + ((n * p.K + c) * p.G + grp) * keys_bytes<T, SP>(true);
+        const char *head = p.heads + ((n * p.K + c) * p.H + h) * head_bytes<T>(true);
+        const ChunkScalars *cs = reinterpret_cast<const ChunkScalars *>(head + head_bytes<T>(true) - sizeof(ChunkScalars));
+        const int64_t t0 = (int64_t)c * kDQ;
+        const int rows = (int)(len - t0 < kDQ ? len - t0 : kDQ);
+        float *b = p.bound[1] + ((nh * p.K + c) * p.PP + ch) * SP + (lane >> 4) * 8;
+#pragma unroll
+        for (int i = 0; i < SP / 16; ++i) *reinterpret_cast<f32x4 *>(b + 32 * (i >> 1) + 4 * (i & 1)) = st[i];
+        Split<T, kN<T>> sp[KS];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) stack(st[2 * s], st[2 * s + 1], sp[s]);
+        f32x4 z[4], dy[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                Split<T, 1> a;
+                a.f[0] = get_frag<T>(keys + (t * KS + s) * kFrag<T>, lane);
+                acc = mma_terms(a, sp[s], acc);
+            }
+            z[t] = acc * *reinterpret_cast<const f32x4 *>(cs->to_end + 16 * t + q4);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * t + q4 + r;
+                dy[t][r] = mine && row < rows ? (float)dyg[(t0 + row) * p.dy_ld] : 0.0f;
+            }
+        }
+        const char *nt = head + kTri * kN<T> * kFrag<T>, *mt = nt + kTri * kN<T> * kFrag<T>;
+        Split<T, 1> ds[2];
+        stack(dy[0], dy[1], ds[0]);
+        stack(dy[2], dy[3], ds[1]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int P = t / 2; P < 2; ++P) {
+                Split<T, kN<T>> a;
+#pragma unroll
+                for (int e = 0; e < kN<T>; ++e) a.f[e] = get_frag<T>(mt + (upper(t, P) * kN<T> + e) * kFrag<T>, lane);
+                z[t] = mma_terms(a, ds[P], z[t]);        // dU
+            }
+        Split<T, kN<T>> zs[2];
+        stack(z[0], z[1], zs[0]);
+        stack(z[2], z[3], zs[1]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int P = t / 2; P < 2; ++P) {
+                Split<T, kN<T>> a;
+#pragma unroll
+                for (int e = 0; e < kN<T>; ++e) a.f[e] = get_frag<T>(nt + (upper(t, P) * kN<T> + e) * kFrag<T>, lane);
+                z[t] = mma_terms(a, zs[P], z[t]);        // E
+            }
+        Split<T, kN<T>> us[2], xs[2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const f32x4 grow = *reinterpret_cast<const f32x4 *>(cs->from_start + 16 * t + q4);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) p.rows[1][((nh * p.K + c) * kDQ + 16 * t + q4 + r) * p.PP + ch] = z[t][r];
+            z[t] = z[t] * (grow * *reinterpret_cast<const f32x4 *>(cs->beta + 16 * t + q4)) * -1.0f;
+            dy[t] = dy[t] * (grow * p.scale);
+        }
+        stack(z[0], z[1], us[0]);
+        stack(z[2], z[3], us[1]);
+        stack(dy[0], dy[1], xs[0]);
+        stack(dy[2], dy[3], xs[1]);
+        const float total = cs->from_start[kDQ - 1];
+        const char *kt = keys + 8 * KS * kFrag<T>, *qt = kt + 4 * KS * kFrag<T>;
+#pragma unroll
+        for (int i = 0; i < SP / 16; ++i) {
+            st[i] = st[i] * total;
+#pragma unroll
+            for (int P = 0; P < 2; ++P) {
+                Split<T, 1> a, q;
+                a.f[0] = get_frag<T>(kt + (i * 2 + P) * kFrag<T>, lane);
+                q.f[0] = get_frag<T>(qt + (i * 2 + P) * kFrag<T>, lane);
+                st[i] = mma_terms(a, us[P], st[i]);
+                st[i] = mma_terms(q, xs[P], st[i]);
+            }
+        }
+    }
+    store_state<SP>(p.dstate + (nh * p.P + ch) * p.S, p.dstate && mine, p.S, lane, st);
+}
+
+// The two passes over the states of a gradient, which do not depend on each other.
+template <typename T, int SP> __global__ void __launch_bounds__(64) delta_states_kernel(DeltaParams p)
+{
+    const int64_t units = (int64_t)p.N * p.H * p.blocks, half = gridDim.x / 2;
+    const bool back = blockIdx.x < half;
+    const int64_t unit = unit_of(back ? blockIdx.x : blockIdx.x - half, units);
+    if (unit >= units) return;
+    if (back) delta_backward<T, SP>(p, unit, threadIdx.x);
+    else delta_forward<T, SP, false>(p, unit, threadIdx.x);
+}
+
+// ---- the gradient of a chunk ---------------------------------------------------------
+// From the state S in front of the chunk, the gradient R of that behind it, Y and E
+// (U = beta Y, dV = beta E; D and W lower triangular, W strictly):
+//
+//   D = dO U^T,  W = dV U^T,   pair_ij = D_ij M_ij - W_ij T_ij
+//   dq = scale (e^c dO S + (D o Gamma) K)
+//   dk = scale (D o Gamma)^T Q - e^c dV S + e^{c_Q - c} U R - (W o Gamma + its transpose) K
+//   dg_t = sum_{i>=t} (scale e^c dO S . q - e^c dV S . k)_i + sum_{j<t} (e^{c_Q - c} U R . k)_j
+//        + sum_{j<t<=i} pair_ij + e^{c_Q} <S, R>
+//
+// (every path of dg_t crosses the decay of token t; a pair counts as its row less
+// its column, the same number in fp64 twice, so that what cancels leaves nothing).
+// One workgroup takes one chunk of a slice of a group's heads; a wave owns CT
+// blocks of 16 keys, in the order of K^T's operands, and reads S and R itself: no
+// other wave needs them.  dO, dV and U go through LDS, split into their terms once.
+template <typename T, int SP> struct GradShape {
+    static constexpr int NW = SP == 32 ? 2 : SP == 256 ? 8 : 4;      // waves
+    static constexpr int CT = SP / 16 / NW;
+    static constexpr int PB = 64;                                    // channels at a time
+    static constexpr int TT = (10 + NW - 1) / NW;                    // triangular tiles of a wave
+    static constexpr int LD = PB + Frag<T>::PAD, ML = kDQ + Frag<T>::PAD;
+    static constexpr int NL = kM<T>;                                 // terms of D o Gamma and W o Gamma
+};
+template <typename T, int SP> struct GradShared {
+    typedef GradShape<T, SP> G;
+    T dy[kDQ * G::LD], dv[kN<T>][kDQ * G::LD], u[kN<T>][kDQ * G::LD];
+    T low[G::NL][kDQ * G::ML], sym[G::NL][kDQ * G::ML];
+    float from_start[kDQ], to_end[kDQ], beta[kDQ];
+    double cum[kDQ];
+    double row[4][kDQ], col[4][kDQ], front[G::NW][kDQ], behind[G::NW][kDQ], across[G::NW];
+};
+
+// tile t of the ten on and below the diagonal of 4 x 4
+SEQ_DEV void triangle(int t, int &i, int &j)
+{
+    i = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0;
+    j = t - i * (i + 1) / 2;
+}
+
+// Column col0 + lane % 16 of 64 rows, rows k0 + 4q .. and k0 + 16 + 4q ..
+SEQ_DEV bf16x8 read_cols_stacked(const bf16_t *t, int ld, int k0, int col0, int lane)
+{
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
+    const bf16_t *p = t + (k0 + (lane >> 4) * 4 + ((lane & 15) >> 2)) * ld + col0 + (lane & 3) * 4;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 16 * ld));
+    return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+SEQ_DEV Frag<float>::type read_cols_stacked(const float *t, int ld, int k0, int col0, int lane)
+{
+    const float *p = t + (k0 + (lane >> 4) * 4) * ld + col0 + (lane & 15);
+    Frag<float>::type f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f.v[e] = p[e * ld], f.v[4 + e] = p[(16 + e) * ld];
+    return f;
+}
+
+// element (row, col) of a matrix held as terms
+template <typename T, int NS, int ALL> SEQ_DEV void put_terms(T (&m)[NS][ALL], int at, float v)
+{
+#pragma unroll
+    for (int e = 0; e < NS; ++e) {
+        const T t = (T)v;
+        m[e][at] = t;
+        v -= (float)t;
+    }
+}
+
+template <typename T, int SP>
+__global__ void __launch_bounds__(64 * (SP == 32 ? 2 : SP == 256 ? 8 : 4)) delta_grad_kernel(DeltaParams p)
+{
+    typedef GradShape<T, SP> G;
+    constexpr int NW = G::NW, CT = G::CT, PB = G::PB, TT = G::TT, LD = G::LD, ML = G::ML, NL = G::NL, KS = SP / 32;
+    constexpr int kRowsAtOnce = NW * 4, RI = kDQ / kRowsAtOnce;     // 16 threads take a row of PB channels
+    __shared__ __align__(16) GradShared<T, SP> sh;
+    const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4, q4 = q * 4;
+    const int64_t chunk = blockIdx.x / ((int64_t)p.G * p.slices);        // n K + c
+    const int gs = (int)(blockIdx.x - chunk * p.G * p.slices), grp = gs / p.slices, slice = gs - grp * p.slices;
+    const int64_t n = chunk / p.K, c = chunk - n * p.K, t0 = c * kDQ, len = seq_len(p.lengths, n, p.L);
+    const int live = (int)(len - t0 < 0 ? 0 : len - t0 < kDQ ? len - t0 : kDQ);
+    const int all = (int)(p.L - t0 < kDQ ? p.L - t0 : kDQ);              // rows of the outputs
+    const int per = p.H / p.G, h0 = grp * per + slice * p.heads_per_slice;
+    const int h1 = min(h0 + p.heads_per_slice, (grp + 1) * per);
+    const int64_t row0 = n * p.L + t0;
+    const int key0 = 8 * (l16 >> 2) + (l16 & 3);       // key of this lane's column in block (s, a): 32 s + 4 a + key0
+    if (live < all) {           // rows behind the sequence; where none is in front there is nothing else
+        for (int e = threadIdx.x; e < (all - live) * (h1 - h0); e += NW * 64) {
+            const int64_t row = row0 + live + e / (h1 - h0);
+            const int h = h0 + e % (h1 - h0);
+            p.dg[row * p.dg_ld + h] = 0.0f;
+            ((T *)p.dbeta)[row * p.dbeta_ld + h] = (T)0.0f;
+        }
+        const int64_t wide = (int64_t)(h1 - h0) * p.P;
+        for (int64_t e = threadIdx.x; e < (all - live) * wide; e += NW * 64)
+            ((T *)p.dv)[(row0 + live + e / wide) * p.dv_ld + (int64_t)h0 * p.P + e % wide] = (T)0.0f;
+    }
+    f32x4 dq[CT][4], dk[CT][4];
+#pragma unroll
+    for (int x = 0; x < CT; ++x)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) dq[x][t] = dk[x][t] = f32x4{0, 0, 0, 0};
+    const char *keys = p.keys + (chunk * p.G + grp) * keys_bytes<T, SP>(true);
+    const char *kt = keys + 8 * KS * kFrag<T>, *qt = kt + 4 * KS * kFrag<T>;
+    // the upper triangles stay zero
+    for (int e = threadIdx.x; e < kDQ * ML; e += NW * 64)
+#pragma unroll
+        for (int x = 0; x < NL; ++x) sh.low[x][e] = (T)0.0f;
+    for (int h = h0; h < (live > 0 ? h1 : h0); ++h) {
+        const int64_t nh = n * p.H + h;
+        const char *head = p.heads + (chunk * p.H + h) * head_bytes<T>(true);
+        const ChunkScalars *cs = reinterpret_cast<const ChunkScalars *>(head + head_bytes<T>(true) - sizeof(ChunkScalars));
+        __syncthreads();
+        if (w == 0) {
+            sh.from_start[lane] = cs->from_start[lane];
+            sh.to_end[lane] = cs->to_end[lane];
+            sh.beta[lane] = cs->beta[lane];
+            sh.cum[lane] = cs->cum[lane];
+        }
+        f32x4 by[CT][4], old[CT][4], nw[CT][4], dm[TT], wm[TT];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int x = 0; x < CT; ++x) by[x][t] = old[x][t] = nw[x][t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int t = 0; t < TT; ++t) dm[t] = wm[t] = f32x4{0, 0, 0, 0};
+        float db[RI];
+#pragma unroll
+        for (int e = 0; e < RI; ++e) db[e] = 0.0f;
+        double across = 0.0;
+        for (int p0 = 0; p0 < p.PP; p0 += PB) {
+            __syncthreads();
+            const int pc = p0 + 4 * (threadIdx.x & 15);
+#pragma unroll
+            for (int e = 0; e < RI; ++e) {
+                const int row = (threadIdx.x >> 4) + e * kRowsAtOnce;
+                f32x4 y = {0, 0, 0, 0}, ee = {0, 0, 0, 0}, dy = {0, 0, 0, 0};
+                if (row < live && pc < p.PP) {
+                    const int64_t at = ((nh * p.K + c) * kDQ + row) * p.PP + pc;
+                    y = *reinterpret_cast<const f32x4 *>(p.rows[0] + at);
+                    ee = *reinterpret_cast<const f32x4 *>(p.rows[1] + at);
+                    const T *g = (const T *)p.dy + (row0 + row) * p.dy_ld + (int64_t)h * p.P + pc;
+                    T *d = (T *)p.dv + (row0 + row) * p.dv_ld + (int64_t)h * p.P + pc;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        db[e] = fmaf(ee[i], y[i], db[e]);
+                        if (pc + i < p.P) {
+                            dy[i] = (float)g[i];
+                            d[i] = (T)(sh.beta[row] * ee[i]);
+                        }
+                    }
+                    ee = ee * sh.beta[row];
+                    y = y * sh.beta[row];
+                }
+                const int at = row * LD + 4 * (threadIdx.x & 15);
+                write_split4<1>(sh.dy + at, 0, dy);
+                write_split4<kN<T>>(sh.dv[0] + at, kDQ * LD, ee);
+                write_split4<kN<T>>(sh.u[0] + at, kDQ * LD, y);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int s = 0; s < PB / 32; ++s) {
+                if (p0 + 32 * s >= p.PP) break;
+                Split<T, kN<T>> ss[CT], rs[CT];
+#pragma unroll
+                for (int x = 0; x < CT; ++x) {
+                    const int b = w * CT + x;
+                    const int64_t at = ((nh * p.K + c) * p.PP + p0 + 32 * s + 8 * q) * SP + 32 * (b >> 1) + 4 * (b & 1) + key0;
+                    float sv[8], rv[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sv[i] = p.bound[0][at + i * SP], rv[i] = p.bound[1][at + i * SP];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) across = fma((double)sv[i], (double)rv[i], across);
+                    make_split(sv, ss[x]);
+                    make_split(rv, rs[x]);
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    Split<T, 1> a;
+                    Split<T, kN<T>> d, u;
+                    a.f[0] = read_rows(sh.dy, LD, 16 * t, 32 * s, lane);
+#pragma unroll
+                    for (int e = 0; e < kN<T>; ++e) {
+                        d.f[e] = read_rows(sh.dv[e], LD, 16 * t, 32 * s, lane);
+                        u.f[e] = read_rows(sh.u[e], LD, 16 * t, 32 * s, lane);
+                    }
+#pragma unroll
+                    for (int x = 0; x < CT; ++x) {
+                        by[x][t] = mma_terms(a, ss[x], by[x][t]);
+                        old[x][t] = mma_terms(d, ss[x], old[x][t]);
+                        nw[x][t] = mma_terms(u, rs[x], nw[x][t]);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    if (w + t * NW >= 10) continue;
+                    int it, jt;
+                    triangle(w + t * NW, it, jt);
+                    Split<T, 1> a;
+                    Split<T, kN<T>> d, u;
+                    a.f[0] = read_rows(sh.dy, LD, 16 * it, 32 * s, lane);
+#pragma unroll
+                    for (int e = 0; e < kN<T>; ++e) {
+                        d.f[e] = read_rows(sh.dv[e], LD, 16 * it, 32 * s, lane);
+                        u.f[e] = read_rows(sh.u[e], LD, 16 * jt, 32 * s, lane);
+                    }
+                    dm[t] = mma_terms(a, u, dm[t]);
+                    wm[t] = mma_terms(d, u, wm[t]);
+                }
+            }
+        }
+        // dbeta: the 16 threads of a row
+#pragma unroll
+        for (int e = 0; e < RI; ++e) {
+            float v = db[e];
+            for (int o = 8; o > 0; o >>= 1) v += __shfl_xor(v, o);
+            const int row = (threadIdx.x >> 4) + e * kRowsAtOnce;
+            if (l16 == 0 && row < live) ((T *)p.dbeta)[(row0 + row) * p.dbeta_ld + h] = (T)v;
+        }
+        // pairs of tokens
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            if (w + t * NW >= 10) continue;
+            int it, jt;
+            triangle(w + t * NW, it, jt);
+            f32x4 kk = {0, 0, 0, 0}, qk = {0, 0, 0, 0}, pair;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const typename Frag<T>::type b = get_frag<T>(keys + (jt * KS + s) * kFrag<T>, lane);
+                kk = mma(get_frag<T>(keys + (it * KS + s) * kFrag<T>, lane), b, kk);
+                qk = mma(get_frag<T>(keys + ((4 + it) * KS + s) * kFrag<T>, lane), b, qk);
+            }
+            const int j = 16 * jt + l16;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * it + q4 + r;
+                const float decay = i >= j ? expf((float)(sh.cum[i] - sh.cum[j])) : 0.0f;
+                const float lo = i >= j ? dm[t][r] * (decay * p.scale) : 0.0f, be = i > j ? wm[t][r] * decay : 0.0f;
+                pair[r] = i > j ? lo * qk[r] - be * kk[r] : 0.0f;      // a token's pair with itself crosses no decay
+                put_terms(sh.low, i * ML + j, lo);
+                if (i >= j) {
+                    put_terms(sh.sym, i * ML + j, -be);
+                    put_terms(sh.sym, j * ML + i, -be);
+                }
+            }
+            const double sum = row_sum4<double>(pair, lane);
+            if ((l16 & 3) == 0) sh.row[jt][16 * it + q4 + (l16 >> 2)] = sum;
+            double down = ((double)pair[0] + (double)pair[1]) + ((double)pair[2] + (double)pair[3]);
+            down += __shfl_xor(down, 16);
+            down += __shfl_xor(down, 32);
+            if (q == 0) sh.col[it][j] = down;
+        }
+        // what the states in front and behind give, and its part in dg
+        double front[4], behind[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            front[t] = behind[t] = 0.0;
+            const f32x4 grow = *reinterpret_cast<const f32x4 *>(sh.from_start + 16 * t + q4);
+            const f32x4 fade = *reinterpret_cast<const f32x4 *>(sh.to_end + 16 * t + q4);
+#pragma unroll
+            for (int x = 0; x < CT; ++x) {
+                by[x][t] = by[x][t] * (grow * p.scale);
+                old[x][t] = old[x][t] * grow;
+                nw[x][t] = nw[x][t] * fade;
+                const typename Frag<T>::type kf = get_frag<T>(kt + ((w * CT + x) * 2 + (t >> 1)) * kFrag<T>, lane);
+                const typename Frag<T>::type qf = get_frag<T>(qt + ((w * CT + x) * 2 + (t >> 1)) * kFrag<T>, lane);
+                f32x4 a, b;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float kv = frag_get(kf, 4 * (t & 1) + r), qv = frag_get(qf, 4 * (t & 1) + r);
+                    a[r] = by[x][t][r] * qv - old[x][t][r] * kv;
+                    b[r] = nw[x][t][r] * kv;
+                }
+                front[t] += row_sum4<double>(a, lane);
+                behind[t] += row_sum4<double>(b, lane);
+                dq[x][t] = dq[x][t] + by[x][t];
+                dk[x][t] = dk[x][t] + (nw[x][t] - old[x][t]);
+            }
+            if ((l16 & 3) == 0) {
+                sh.front[w][16 * t + q4 + (l16 >> 2)] = front[t];
+                sh.behind[w][16 * t + q4 + (l16 >> 2)] = behind[t];
+            }
+        }
+        for (int o = 32; o > 0; o >>= 1) across += __shfl_xor(across, o);
+        if (lane == 0) sh.across[w] = across;
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < CT; ++x)
+#pragma unroll
+            for (int P = 0; P < 2; ++P) {
+                Split<T, 1> kf, qf;
+                kf.f[0] = get_frag<T>(kt + ((w * CT + x) * 2 + P) * kFrag<T>, lane);
+                qf.f[0] = get_frag<T>(qt + ((w * CT + x) * 2 + P) * kFrag<T>, lane);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+#pragma unroll
+                    for (int e = 0; e < NL; ++e) {
+                        if (P <= t / 2) dq[x][t] = mma(read_rows_stacked(sh.low[e], ML, 16 * t, 32 * P, lane), kf.f[0], dq[x][t]);
+                        dk[x][t] = mma(read_rows_stacked(sh.sym[e], ML, 16 * t, 32 * P, lane), kf.f[0], dk[x][t]);
+                        if (P >= t / 2) dk[x][t] = mma(read_cols_stacked(sh.low[e], ML, 32 * P, 16 * t, lane), qf.f[0], dk[x][t]);
+                    }
+                }
+            }
+        if (w == 0) {
+            double d = 0.0, b = 0.0, whole = 0.0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (e <= lane >> 4) d += sh.row[e][lane];
+                if (e >= lane >> 4) d -= sh.col[e][lane];
+            }
+#pragma unroll
+            for (int e = 0; e < NW; ++e) d += sh.front[e][lane], b += sh.behind[e][lane], whole += sh.across[e];
+            if (lane >= live) d = b = 0.0;
+            const double upto = wave_prefix(d), sum = wave_last(upto), before = wave_prefix(b) - b;
+            const double dg = (sum - upto + d) + before + (double)sh.from_start[kDQ - 1] * whole;
+            const double step = lane > 0 ? sh.cum[lane] - sh.cum[lane - 1] : sh.cum[0];
+            // no gradient by a decay that is zero
+            if (lane < live) p.dg[(row0 + lane) * p.dg_ld + h] = expf((float)step) == 0.0f ? 0.0f : (float)dg;
+        }
+    }
+    // dq and dk: of this call, or of a slice's heads
+#pragma unroll
+    for (int x = 0; x < CT; ++x) {
+        const int b = w * CT + x, key = 32 * (b >> 1) + 4 * (b & 1) + key0;
+        if (key >= p.S) continue;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * t + q4 + r;
+                if (row >= all) continue;
+                const float vq = row < live ? dq[x][t][r] : 0.0f, vk = row < live ? dk[x][t][r] : 0.0f;
+                if (p.slices == 1) {
+                    ((T *)p.dq)[(row0 + row) * p.dq_ld + (int64_t)grp * p.S + key] = (T)vq;
+                    ((T *)p.dk)[(row0 + row) * p.dk_ld + (int64_t)grp * p.S + key] = (T)vk;
+                } else {
+                    const int64_t at = (((int64_t)slice * p.N * p.L + row0 + row) * p.G + grp) * p.S + key;
+                    p.part[0][at] = vq;
+                    p.part[1][at] = vk;
+                }
+            }
+    }
+}
+
+// dq and dk from the slices' sums, always in the same order
+template <typename T> __global__ void __launch_bounds__(256) delta_reduce_kernel(DeltaParams p)
+{
+    const int64_t rows = (int64_t)p.N * p.L, width = (int64_t)p.G * p.S, e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= rows * width) return;
+    const int64_t row = e / width, col = e - row * width;
+    float q = 0.0f, k = 0.0f;
+    for (int s = 0; s < p.slices; ++s) {
+        q += p.part[0][s * rows * width + e];
+        k += p.part[1][s * rows * width + e];
+    }
+    ((T *)p.dq)[row * p.dq_ld + col] = (T)q;
+    ((T *)p.dk)[row * p.dk_ld + col] = (T)k;
 }
 
 // ---- one token -----------------------------------------------------------------------

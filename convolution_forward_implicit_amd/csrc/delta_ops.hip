@@ -16,6 +16,8 @@ struct conv_delta_plan {
     int SP, K, blocks;                   // padded keys, chunks, blocks of 16 channels of a head
     int slices, heads_per_slice;         // of a group's heads, for what a chunk does without its state
     int64_t ws_bytes, o_heads;
+    int PP, grad_slices, grad_heads;     // the gradient's padded channels, and its slices of a group's heads
+    int64_t bwd_ws_bytes, o_bwd_heads, o_bound[2], o_rows[2], o_part[2];
     char text[256];
 };
 
@@ -48,12 +50,44 @@ template <typename T, int SP> void launch_fwd(const DeltaParams &p, int64_t unit
     hipLaunchKernelGGL((delta_fwd_kernel<T, SP>), dim3((unsigned)state_grid(units)), dim3(64), 0, s, p);
 }
 
-template <typename T> void launch_delta(int SP, const DeltaParams &p, int64_t units, hipStream_t s)
+// The gradient: what chunks do without their states, both passes over the states,
+// the gradients of the chunks and, where a group's heads are sliced, their sums.
+template <typename T, int SP> void launch_bwd(DeltaParams p, const conv_delta_plan &pl, hipStream_t s)
 {
-    if (SP == 32) return launch_fwd<T, 32>(p, units, s);
-    if (SP == 64) return launch_fwd<T, 64>(p, units, s);
-    if (SP == 128) return launch_fwd<T, 128>(p, units, s);
-    return launch_fwd<T, 256>(p, units, s);
+    const int64_t chunks = (int64_t)p.N * p.K * p.G, units = (int64_t)p.N * p.H * p.blocks;
+    if (p.K > 0)
+        hipLaunchKernelGGL((delta_prepare_kernel<T, SP, true>), dim3((unsigned)(chunks * p.slices)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((delta_states_kernel<T, SP>), dim3((unsigned)(2 * state_grid(units))), dim3(64), 0, s, p);
+    if (p.K == 0) return;
+    p.slices = pl.grad_slices;
+    p.heads_per_slice = pl.grad_heads;
+    hipLaunchKernelGGL((delta_grad_kernel<T, SP>), dim3((unsigned)(chunks * p.slices)), dim3(64 * GradShape<T, SP>::NW), 0, s, p);
+    if (p.slices > 1) {
+        const int64_t grid = ((int64_t)p.N * p.L * p.G * p.S + 255) / 256;
+        hipLaunchKernelGGL((delta_reduce_kernel<T>), dim3((unsigned)grid), dim3(256), 0, s, p);
+    }
+}
+
+template <typename T, int SP> void launch_delta(const DeltaParams &p, const conv_delta_plan &pl, bool grad, hipStream_t s)
+{
+    if (grad) launch_bwd<T, SP>(p, pl, s);
+    else launch_fwd<T, SP>(p, (int64_t)p.N * p.H * p.blocks, s);
+}
+
+template <typename T> void launch_delta(const DeltaParams &p, const conv_delta_plan &pl, bool grad, hipStream_t s)
+{
+    if (pl.SP == 32) return launch_delta<T, 32>(p, pl, grad, s);
+    if (pl.SP == 64) return launch_delta<T, 64>(p, pl, grad, s);
+    if (pl.SP == 128) return launch_delta<T, 128>(p, pl, grad, s);
+    return launch_delta<T, 256>(p, pl, grad, s);
+}
+
+// Slices of a group's `heads` so that `groups` of them give about `want` workgroups.
+void slice_heads(int64_t groups, int64_t heads, int64_t want, int *slices, int *per)
+{
+    const int64_t n = std::max<int64_t>(1, std::min(heads, want / std::max<int64_t>(1, groups)));
+    *per = (int)((heads + n - 1) / n);
+    *slices = (int)((heads + *per - 1) / *per);
 }
 
 // A step's lanes for the keys of a channel, and workgroups for the channels of a head.
@@ -117,17 +151,30 @@ conv_status_t conv_delta_create(const conv_delta_desc_t *desc, conv_delta_plan_t
         delete pl;
         return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
     }
-    const int64_t wgs = std::max<int64_t>(1, d.N * pl->K * d.G), hpg = d.H / d.G;
-    // two workgroups of the preparation fit a compute unit
-    const int64_t want = std::max<int64_t>(1, std::min(hpg, 512 / wgs));
-    pl->heads_per_slice = (int)((hpg + want - 1) / want);
-    pl->slices = (int)((hpg + pl->heads_per_slice - 1) / pl->heads_per_slice);
+    // two workgroups of the preparation fit a compute unit, one of the gradient's
+    const int64_t groups = d.N * pl->K * d.G, hpg = d.H / d.G;
+    slice_heads(groups, hpg, 512, &pl->slices, &pl->heads_per_slice);
+    slice_heads(groups, hpg, 256, &pl->grad_slices, &pl->grad_heads);
     pl->o_heads = up(d.N * pl->K * d.G * keys_of(d, pl->SP, false));
     pl->ws_bytes = pl->o_heads + up(d.N * pl->K * d.H * head_of(d, false));
+    pl->PP = (int)((d.P + 31) / 32 * 32);
+    int64_t o = up(groups * keys_of(d, pl->SP, true));
+    pl->o_bwd_heads = o;
+    o += up(d.N * pl->K * d.H * head_of(d, true));
+    const int64_t states = up(d.N * d.H * pl->K * pl->PP * pl->SP * 4), tokens = up(d.N * d.H * pl->K * kDQ * pl->PP * 4);
+    const int64_t part = pl->grad_slices > 1 ? up((int64_t)pl->grad_slices * d.N * d.L * d.G * d.S * 4) : 0;
+    for (int k = 0; k < 2; ++k) {
+        pl->o_bound[k] = o + k * states;
+        pl->o_rows[k] = o + 2 * states + k * tokens;
+        pl->o_part[k] = o + 2 * states + 2 * tokens + k * part;
+    }
+    pl->bwd_ws_bytes = o + 2 * (states + tokens + part);
     snprintf(pl->text, sizeof(pl->text),
-             "delta %s N=%lld L=%lld H=%lld P=%lld G=%lld S=%lld(%d), %d chunks of %d, %d slices of %d heads",
+             "delta %s N=%lld L=%lld H=%lld P=%lld G=%lld S=%lld(%d), %d chunks of %d, %d slices of %d heads; "
+             "gradient: %d slices of %d heads",
              d.dtype == CONV_DT_BF16 ? "bf16" : "f32", (long long)d.N, (long long)d.L, (long long)d.H, (long long)d.P,
-             (long long)d.G, (long long)d.S, pl->SP, pl->K, kDQ, pl->slices, pl->heads_per_slice);
+             (long long)d.G, (long long)d.S, pl->SP, pl->K, kDQ, pl->slices, pl->heads_per_slice,
+             pl->grad_slices, pl->grad_heads);
     if (getenv("CONVFWD_LOG")) fprintf(stderr, "convfwd: %s\n", pl->text);
     *plan = pl;
     return CONV_OK;
@@ -137,6 +184,13 @@ conv_status_t conv_delta_workspace_bytes(const conv_delta_plan_t *plan, int64_t 
 {
     if (!plan || !bytes) return fail(CONV_ERR_INVALID_ARG, "plan or bytes is NULL");
     *bytes = plan->ws_bytes;
+    return CONV_OK;
+}
+
+conv_status_t conv_delta_bwd_workspace_bytes(const conv_delta_plan_t *plan, int64_t *bytes)
+{
+    if (!plan || !bytes) return fail(CONV_ERR_INVALID_ARG, "plan or bytes is NULL");
+    *bytes = plan->bwd_ws_bytes;
     return CONV_OK;
 }
 
@@ -206,11 +260,11 @@ static conv_status_t delta_forward_call(const conv_delta_plan_t *plan, const con
     p.heads = (char *)ws + plan->o_heads;
     const Rows vec[] = {in[0], in[1]};
     p.vec = delta_vector(*plan, vec, 2);
-    const int64_t units = d.N * d.H * plan->blocks;
-    if (!one_launch((double)state_grid(units), 64) || !one_launch((double)d.N * plan->K * d.G * plan->slices, 256))
+    if (!one_launch((double)state_grid(d.N * d.H * plan->blocks), 64) ||
+        !one_launch((double)d.N * plan->K * d.G * plan->slices, 256))
         return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
-    if (d.dtype == CONV_DT_BF16) launch_delta<bf16_t>(plan->SP, p, units, s);
-    else launch_delta<float>(plan->SP, p, units, s);
+    if (d.dtype == CONV_DT_BF16) launch_delta<bf16_t>(p, *plan, false, s);
+    else launch_delta<float>(p, *plan, false, s);
     return launched();
 }
 
@@ -223,6 +277,71 @@ conv_status_t conv_delta_run(const conv_delta_plan_t *plan, const conv_delta_arg
 conv_status_t conv_delta_step(const conv_delta_plan_t *plan, const conv_delta_args_t *args, void *stream)
 {
     return delta_forward_call(plan, args, true, nullptr, 0, stream);
+}
+
+conv_status_t conv_delta_bwd_run(const conv_delta_plan_t *plan, const conv_delta_bwd_args_t *a, void *workspace,
+                                 int64_t workspace_bytes, void *stream)
+{
+    if (!plan || !a) return fail(CONV_ERR_INVALID_ARG, "plan or args is NULL");
+    const conv_delta_desc_t &d = plan->desc;
+    const int64_t e = plan->esz, rows = d.N * d.L, hp = d.H * d.P, gs = d.G * d.S, states = d.N * hp * d.S;
+    if (a->dstate && !a->state) return fail(CONV_ERR_INVALID_ARG, "dstate without a state");
+    const Rows in[] = {{"dy", a->dy, rows, hp, or_packed(a->dy_ld, hp), e},
+                       {"q", a->q, rows, gs, or_packed(a->q_ld, gs), e},
+                       {"k", a->k, rows, gs, or_packed(a->k_ld, gs), e},
+                       {"v", a->v, rows, hp, or_packed(a->v_ld, hp), e},
+                       {"g", a->g, rows, d.H, or_packed(a->g_ld, d.H), 4},
+                       {"beta", a->beta, rows, d.H, or_packed(a->beta_ld, d.H), e},
+                       {"lengths", a->lengths, 1, d.N, std::max<int64_t>(1, d.N), 4},
+                       {"state", a->state, 1, states, states, 4},
+                       {"dstate_out", a->dstate_out, 1, states, states, 4}};
+    const int64_t need = plan->bwd_ws_bytes;
+    const Rows out[] = {{"dq", a->dq, rows, gs, or_packed(a->dq_ld, gs), e},
+                        {"dk", a->dk, rows, gs, or_packed(a->dk_ld, gs), e},
+                        {"dv", a->dv, rows, hp, or_packed(a->dv_ld, hp), e},
+                        {"dg", a->dg, rows, d.H, or_packed(a->dg_ld, d.H), 4},
+                        {"dbeta", a->dbeta, rows, d.H, or_packed(a->dbeta_ld, d.H), e},
+                        {"dstate", a->dstate, 1, states, states, 4},
+                        {"workspace", workspace, 1, need, std::max<int64_t>(1, need), 1}};
+    conv_status_t st = check_rows(in, 9);
+    if (st == CONV_OK) st = check_rows(out, 6);
+    if (st != CONV_OK) return st;
+    if (d.N == 0) return CONV_OK;
+    if (rows > 0 && (!a->dy || !a->q || !a->k || !a->v || !a->g || !a->beta || !a->dq || !a->dk || !a->dv || !a->dg || !a->dbeta))
+        return fail(CONV_ERR_INVALID_ARG, "dy, q, k, v, g, beta, dq, dk, dv, dg or dbeta is NULL");
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != CONV_OK) return st;
+    if ((st = check_overlap(out, 7, in, 9)) != CONV_OK) return st;
+    if (rows == 0 && !a->dstate) return CONV_OK;
+    DeltaParams p;
+    delta_params(*plan, &p);
+    p.q = a->q; p.k = a->k; p.v = a->v; p.g = a->g; p.beta = a->beta; p.state = a->state; p.lengths = a->lengths;
+    p.dy = a->dy; p.dstate_out = a->dstate_out; p.dq = a->dq; p.dk = a->dk; p.dv = a->dv; p.dg = a->dg; p.dbeta = a->dbeta;
+    p.dstate = a->dstate;
+    p.dy_ld = stride(in[0]); p.q_ld = stride(in[1]); p.k_ld = stride(in[2]); p.v_ld = stride(in[3]); p.g_ld = stride(in[4]);
+    p.beta_ld = stride(in[5]);
+    p.dq_ld = stride(out[0]); p.dk_ld = stride(out[1]); p.dv_ld = stride(out[2]); p.dg_ld = stride(out[3]);
+    p.dbeta_ld = stride(out[4]);
+    p.PP = plan->PP;
+    p.blocks = plan->PP / 16;
+    char *ws = (char *)workspace;
+    p.keys = ws;
+    p.heads = ws + plan->o_bwd_heads;
+    for (int k = 0; k < 2; ++k) {
+        p.bound[k] = (float *)(ws + plan->o_bound[k]);
+        p.rows[k] = (float *)(ws + plan->o_rows[k]);
+        p.part[k] = (float *)(ws + plan->o_part[k]);
+    }
+    const Rows vec[] = {in[1], in[2]};
+    p.vec = delta_vector(*plan, vec, 2);
+    const double groups = (double)d.N * plan->K * d.G;
+    if (!one_launch(2.0 * (double)state_grid(d.N * d.H * p.blocks), 64) || !one_launch(groups * plan->slices, 256) ||
+        !one_launch(groups * plan->grad_slices, 512) || !one_launch((double)rows * (double)gs / 256 + 1, 256))
+        return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
+    hipStream_t s = (hipStream_t)stream;
+    (void)hipGetLastError();
+    if (d.dtype == CONV_DT_BF16) launch_delta<bf16_t>(p, *plan, true, s);
+    else launch_delta<float>(p, *plan, true, s);
+    return launched();
 }
 
 void conv_delta_destroy(conv_delta_plan_t *plan) { delete plan; }

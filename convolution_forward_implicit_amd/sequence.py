@@ -338,6 +338,7 @@ class DeltaRule(_Plan):
         self.g_shape = (N, L, H)
         self.state_shape = (N, H, P, S)
         self.workspace_bytes = capi.conv_delta_workspace_bytes(self._plan)
+        self.bwd_workspace_bytes = capi.conv_delta_bwd_workspace_bytes(self._plan)
 
     def _state(self, v, name, torch, dev):
         return None if v is None else self._dense(v, self.state_shape, torch.float32, dev, name)
@@ -389,6 +390,34 @@ class DeltaRule(_Plan):
             with away:
                 capi.conv_delta_step(self._plan, byref(args), stream)
         return out
+
+    def backward(self, dy, q, k, v, g, beta, state=None, lengths=None, dstate_out=None, out=None, stream=None):
+        """Gradients of <y, dy> + <state_out, dstate_out> as a dict of "dq",
+        "dk", "dv", "dg", "dbeta" and "dstate" (None without a state).  out: a dict
+        of tensors to write some of them into, which may be column ranges."""
+        import torch
+        t, dev, f32 = self._type(torch), v.device, torch.float32
+        stream, away = self._on(torch, dev, stream)
+        shapes = {"dq": self.q_shape, "dk": self.q_shape, "dv": self.v_shape, "dg": self.g_shape, "dbeta": self.g_shape,
+                  "dstate": None if state is None else self.state_shape}
+        got = dict.fromkeys(shapes)
+        _given(got, out, shapes)
+        for name, shape in shapes.items():
+            if shape is not None and got[name] is None:
+                got[name] = self._new(torch, {"dg": g, "dstate": state}.get(name, v), shape, away)
+        lead, gs, hp, hh = self.v_shape[:2], self.q_shape[2:], self.v_shape[2:], self.g_shape[2:]
+        dyp, dy_ld = self._rows(dy, lead, hp, t, dev, "dy")
+        rows = self._inputs(torch, dev, lead, q, k, v, g, beta)
+        outs = [self._rows(got[name], lead, inner, dt, dev, name) for name, inner, dt in (
+            ("dq", gs, t), ("dk", gs, t), ("dv", hp, t), ("dg", hh, f32), ("dbeta", hh, t))]
+        args = capi.conv_delta_bwd_args_t(
+            dyp, *(a for a, _ in rows), self._state(state, "state", torch, dev),
+            None if lengths is None else self._dense(lengths, self.v_shape[:1], torch.int32, dev, "lengths"),
+            self._state(dstate_out, "dstate_out", torch, dev), *(a for a, _ in outs),
+            self._state(got["dstate"], "dstate", torch, dev), dy_ld, *(ld for _, ld in rows), *(ld for _, ld in outs))
+        _with_workspace(torch, self.bwd_workspace_bytes, dev, away, lambda ws, n: capi.conv_delta_bwd_run(
+            self._plan, byref(args), ws, n, stream))
+        return got
 
 
 def _dtype(dtype):

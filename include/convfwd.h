@@ -556,6 +556,23 @@ typedef struct {
     int64_t q_ld, k_ld, v_ld, g_ld, beta_ld, y_ld;
 } conv_delta_args_t;
 
+/* Gradients of <y, dy> + <state_out, dstate_out> (dstate_out optional).  dstate
+ * is NULL unless state is given (optional then).  dq and dk are the sums over a
+ * group's heads; a decay of zero has no gradient. */
+typedef struct {
+    const void *dy, *q, *k, *v;
+    const float *g;
+    const void *beta;
+    const float *state;
+    const int32_t *lengths;
+    const float *dstate_out;
+    void *dq, *dk, *dv;
+    float *dg;
+    void *dbeta;
+    float *dstate;
+    int64_t dy_ld, q_ld, k_ld, v_ld, g_ld, beta_ld, dq_ld, dk_ld, dv_ld, dg_ld, dbeta_ld;
+} conv_delta_bwd_args_t;
+
 typedef struct conv_delta_plan conv_delta_plan_t;   /* opaque */
 conv_status_t conv_delta_create(const conv_delta_desc_t *desc, conv_delta_plan_t **plan);
 conv_status_t conv_delta_workspace_bytes(const conv_delta_plan_t *plan, int64_t *bytes);
@@ -565,6 +582,9 @@ conv_status_t conv_delta_run(const conv_delta_plan_t *plan, const conv_delta_arg
  * rows n of q, k, v, g, beta, y at n times their ld.  state and state_out are
  * required and may be the same buffer; lengths must be NULL. */
 conv_status_t conv_delta_step(const conv_delta_plan_t *plan, const conv_delta_args_t *args, void *stream);
+conv_status_t conv_delta_bwd_workspace_bytes(const conv_delta_plan_t *plan, int64_t *bytes);
+conv_status_t conv_delta_bwd_run(const conv_delta_plan_t *plan, const conv_delta_bwd_args_t *args, void *workspace,
+                                 int64_t workspace_bytes, void *stream);
 void conv_delta_destroy(conv_delta_plan_t *plan);
 const char *conv_delta_describe(const conv_delta_plan_t *plan);
 

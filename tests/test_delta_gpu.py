@@ -177,3 +177,109 @@ def test_prompt_then_tokens_is_the_whole_sequence(dtype):
     _near(torch.cat(ys, 1), want, my, HALF[dtype], C, "y")
     _near(y, want, my, HALF[dtype], C, "whole y")
     _near(state, last, ms, HALF["f32"], C, "state")
+
+
+# ---- the gradient ----------------------------------------------------------------
+# It chains two products of what the forward pass and the pass behind it leave: twice the
+# forward's error of terms that are products of both scales.  A decay's gradient sums, over
+# the chunk, terms of the tokens on both sides: its scale is taken from the 127 tokens around.
+CG = 2.0 ** -13
+
+
+def _around(v):
+    """Sums over the 127 tokens around each, [N, L, H]."""
+    if v.shape[1] == 0:
+        return v
+    c = torch.nn.functional.pad(v.cumsum(1), (0, 0, 1, 0))
+    t = torch.arange(v.shape[1])
+    return c[:, (t + 64).clamp(max=v.shape[1])] - c[:, (t - 63).clamp(min=0)]
+
+
+def _check_gradient(got, want, mag, dtype, what=""):
+    mag = dict(mag, dg=mag["dg"] + _around(mag["dbeta"]))
+    for k, t in got.items():
+        if t is not None:
+            _near(t, want[k], mag[k], HALF["f32" if k in ("dg", "dstate") else dtype], CG, what + k)
+
+
+@pytest.mark.parametrize("keys", ["random", "same", "few"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("case", CASES + [(1, 70, 12, 16, 1, 24, True, None)], ids=str)
+def test_gradient(case, dtype, keys):
+    N, L, H, P, G, S, state, lengths = case
+    a, s0, n = _case(N, L, H, P, G, S, dtype, state, lengths, 23 + L, keys)
+    g = torch.Generator().manual_seed(L)
+    dy = torch.randn(N, L, H, P, generator=g).to(TYPE[dtype])
+    dlast = torch.randn(N, H, P, S, generator=g) if state else None
+    p = _plan(N, L, H, P, G, S, dtype)
+    want, mag = ref.delta_grad(dy, **a, scale=S ** -0.5, state=s0, lengths=n, dstate_out=dlast)
+    put = lambda t: None if t is None else t.to(DEV)
+    got = p.backward(dy.to(DEV), **_gpu(a), state=put(s0), lengths=put(n), dstate_out=put(dlast))
+    assert (got["dstate"] is not None) == state
+    _check_gradient(got, want, mag, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradient_in_column_ranges_and_behind_lengths(dtype):
+    """dq, dk and dv into columns of one tensor, odd ones too; NaN behind the lengths reaches nothing."""
+    N, L, H, P, G, S = 3, 130, 4, 24, 2, 20
+    a, s0, _ = _case(N, L, H, P, G, S, dtype, True, None, 9)
+    g = torch.Generator().manual_seed(1)
+    dy = torch.randn(N, L, H, P, generator=g).to(TYPE[dtype])
+    n = torch.tensor([130, 0, 37], dtype=torch.int32)
+    p = _plan(N, L, H, P, G, S, dtype)
+    kw = dict(state=s0.to(DEV), lengths=n.to(DEV))
+    want = p.backward(dy.to(DEV), **_gpu(a), **kw)
+    for i in range(N):
+        for k in a:
+            a[k][i, n[i]:] = float("nan")
+        dy[i, n[i]:] = float("nan")
+        for k in ("dq", "dk", "dv", "dg", "dbeta"):
+            assert (want[k][i, n[i]:] == 0).all(), k
+    width = 2 * G * S + H * P
+    for extra in (0, 3):
+        u = torch.full((N, L, width + 2 * extra), 5.0, dtype=TYPE[dtype], device=DEV)
+        q, k, v = u[..., extra:extra + width].split([G * S, G * S, H * P], -1)
+        out = {"dq": q.unflatten(-1, (G, S)), "dk": k.unflatten(-1, (G, S)), "dv": v.unflatten(-1, (H, P))}
+        got = p.backward(dy.to(DEV), **_gpu(a), **kw, out=out)
+        for name, t in want.items():
+            assert torch.equal(got[name], t), name
+        assert (u[..., :extra] == 5).all() and (u[..., extra + width:] == 5).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradient_of_decays_that_clear_the_state(dtype):
+    """A decay of zero has no gradient and lets none through."""
+    N, L, H, P, G, S = 1, 150, 3, 16, 1, 32
+    a, s0, _ = _case(N, L, H, P, G, S, dtype, True, None, 3)
+    a["g"][:, 70, 0], a["g"][:, 70, 1], a["g"][:, :, 2] = -float("inf"), -1e30, -50.0
+    dy = torch.randn(N, L, H, P, generator=torch.Generator().manual_seed(2)).to(TYPE[dtype])
+    dlast = torch.randn(N, H, P, S, generator=torch.Generator().manual_seed(3))
+    want, mag = ref.delta_grad(dy, **a, scale=S ** -0.5, state=s0, dstate_out=dlast)
+    got = _plan(N, L, H, P, G, S, dtype).backward(dy.to(DEV), **_gpu(a), state=s0.to(DEV), dstate_out=dlast.to(DEV))
+    _check_gradient(got, want, mag, dtype)
+    assert (got["dg"][:, 70, :2] == 0).all()
+
+
+def test_gradient_against_differences():
+    """In fp32, along random directions, the gradients are the slope of the loss, which the reference evaluates in
+    double precision on both sides of the point."""
+    N, L, H, P, G, S = 2, 70, 4, 24, 2, 20
+    a, s0, _ = _case(N, L, H, P, G, S, "f32", True, None, 4)
+    g = torch.Generator().manual_seed(8)
+    dy, dlast = torch.randn(N, L, H, P, generator=g), torch.randn(N, H, P, S, generator=g)
+    got = _plan(N, L, H, P, G, S, "f32").backward(dy.to(DEV), **_gpu(a), state=s0.to(DEV), dstate_out=dlast.to(DEV))
+    grad = {k: got["d" + k].cpu().double() for k in ("q", "k", "v", "g", "beta", "state")}
+    v = {k: t.double() for k, t in dict(a, state=s0).items()}
+
+    def loss(s, way):
+        y, last, _, _ = ref.delta(**{k: t + s * way[k] for k, t in v.items()}, scale=S ** -0.5)
+        return float((y * dy.double()).sum() + (last * dlast.double()).sum())
+
+    eps = 1e-5
+    for k in v:
+        way = {j: torch.randn(t.shape, generator=g, dtype=torch.float64) * (j == k) for j, t in v.items()}
+        slope = (loss(eps, way) - loss(-eps, way)) / (2 * eps)
+        # fp32 gradients: 2^-13 of sums of terms that in norm are about the gradient's own
+        scale = float(grad[k].norm() * way[k].norm())
+        assert abs(float((grad[k] * way[k]).sum()) - slope) <= 2.0 ** -13 * scale + 1e-6 * abs(slope), (k, slope)
