@@ -22,16 +22,22 @@ ConvBwdData(problem, dtype) is the input gradient of a forward problem,
 ConvBwdWeight(problem) its weight gradient (bf16).
 
 CausalConv(problem, dtype, has_bias, silu) is the short causal depthwise
-convolution of a sequence model and SelectiveScan(problem, dtype) the state
-space scan behind it; both run over prompts (ragged batches, states in and
-out), token by token (.step) and backwards (.backward).
+convolution of a sequence model; SelectiveScan(problem, dtype) the state space
+scan and DeltaRule(problem, dtype) the gated delta rule behind it.  All run over
+prompts (ragged batches, states in and out), token by token (.step) and
+backwards (.backward).
+
+GroupNorm(problem, dtype, act, ...) normalises channels-innermost tensors: behind
+a convolution over a sample's pixels, around a mixer each head of each token,
+with an activation or a gate.
 """
 from . import capi
 from .capi import ConvError  # noqa: F401
+from .norm import GroupNorm  # noqa: F401
 from .sequence import CausalConv, DeltaRule, SelectiveScan  # noqa: F401
 
 __all__ = ["ConvFwd", "ConvChain", "ConvBwdData", "ConvBwdWeight", "CausalConv", "SelectiveScan",
-           "DeltaRule", "ConvError", "capi", "desc_from_problem"]
+           "DeltaRule", "GroupNorm", "ConvError", "capi", "desc_from_problem"]
 
 
 def _ndim(p):

@@ -13,7 +13,7 @@ from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("conv_fwd.hip", "seq_ops.hip", "delta_ops.hip")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("conv_fwd.hip", "seq_ops.hip", "delta_ops.hip", "norm_ops.hip")]
 LIB = os.path.join(HERE, "libconvfwd.so")
 # peak-rate probes (measured roofline denominators for the benchmark)
 PROBE_SOURCES = [os.path.join(HERE, "csrc", "peak_probe.hip")]

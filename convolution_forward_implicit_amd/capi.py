@@ -46,6 +46,11 @@ SEQUENCE_EXPORTED = ["conv_causal_create", "conv_causal_run", "conv_causal_step"
 DELTA_EXPORTED = ["conv_delta_create", "conv_delta_workspace_bytes", "conv_delta_run", "conv_delta_step",
                   "conv_delta_bwd_workspace_bytes", "conv_delta_bwd_run", "conv_delta_destroy", "conv_delta_describe"]
 
+# the group norm
+GNORM_EXPORTED = ["conv_gnorm_create", "conv_gnorm_workspace_bytes", "conv_gnorm_run", "conv_gnorm_bwd_workspace_bytes",
+                  "conv_gnorm_bwd_run", "conv_gnorm_destroy", "conv_gnorm_describe"]
+NORM_ACTS = {"none": 0, "silu": 1, "gelu": 2}
+
 
 class conv_fwd_desc_t(ctypes.Structure):
     _fields_ = [("ndim", ctypes.c_int32), ("dtype", ctypes.c_int32),
@@ -106,6 +111,21 @@ class conv_delta_bwd_args_t(ctypes.Structure):
                                                   "dq", "dk", "dv", "dg", "dbeta", "dstate")] +
                 [(n, ctypes.c_int64) for n in ("dy_ld", "q_ld", "k_ld", "v_ld", "g_ld", "beta_ld",
                                                  "dq_ld", "dk_ld", "dv_ld", "dg_ld", "dbeta_ld")])
+
+
+class conv_gnorm_desc_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("dtype", "act", "has_bias", "gated", "center", "per_token")] +
+                [(n, ctypes.c_int64) for n in ("N", "L", "G", "C")] + [("eps", ctypes.c_double)])
+
+
+class conv_gnorm_args_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "w", "bias", "gate", "lengths", "y")] +
+                [(n, ctypes.c_int64) for n in ("x_ld", "gate_ld", "y_ld")])
+
+
+class conv_gnorm_bwd_args_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("dy", "x", "w", "bias", "gate", "lengths", "dx", "dw", "dbias", "dgate")] +
+                [(n, ctypes.c_int64) for n in ("dy_ld", "x_ld", "gate_ld", "dx_ld", "dgate_ld")])
 
 
 class ConvError(RuntimeError):
@@ -220,16 +240,17 @@ def lib():
             f("describe").argtypes = [P]
             f("describe").restype = ctypes.c_char_p
         L.conv_scan_workspace_bytes.argtypes = [P, ctypes.POINTER(I64)]
-        L.conv_delta_create.argtypes = [ctypes.POINTER(conv_delta_desc_t), ctypes.POINTER(P)]
-        L.conv_delta_workspace_bytes.argtypes = [P, ctypes.POINTER(I64)]
-        L.conv_delta_run.argtypes = [P, ctypes.POINTER(conv_delta_args_t), P, I64, P]
+        for name, desc, args, bwd in (("delta", conv_delta_desc_t, conv_delta_args_t, conv_delta_bwd_args_t),
+                                      ("gnorm", conv_gnorm_desc_t, conv_gnorm_args_t, conv_gnorm_bwd_args_t)):
+            f = lambda what: getattr(L, "conv_%s_%s" % (name, what))
+            f("create").argtypes = [ctypes.POINTER(desc), ctypes.POINTER(P)]
+            f("workspace_bytes").argtypes = f("bwd_workspace_bytes").argtypes = [P, ctypes.POINTER(I64)]
+            f("run").argtypes = [P, ctypes.POINTER(args), P, I64, P]
+            f("bwd_run").argtypes = [P, ctypes.POINTER(bwd), P, I64, P]
+            f("destroy").argtypes = f("describe").argtypes = [P]
+            f("destroy").restype = None
+            f("describe").restype = ctypes.c_char_p
         L.conv_delta_step.argtypes = [P, ctypes.POINTER(conv_delta_args_t), P]
-        L.conv_delta_bwd_workspace_bytes.argtypes = [P, ctypes.POINTER(I64)]
-        L.conv_delta_bwd_run.argtypes = [P, ctypes.POINTER(conv_delta_bwd_args_t), P, I64, P]
-        L.conv_delta_destroy.argtypes = [P]
-        L.conv_delta_destroy.restype = None
-        L.conv_delta_describe.argtypes = [P]
-        L.conv_delta_describe.restype = ctypes.c_char_p
         _lib = L
     return _lib
 
@@ -593,3 +614,38 @@ def conv_delta_destroy(plan):
 
 def conv_delta_describe(plan):
     return lib().conv_delta_describe(plan).decode()
+
+
+# ---- the group norm ------------------------------------------------------------
+def conv_gnorm_create(desc):
+    plan = ctypes.c_void_p()
+    _check(lib().conv_gnorm_create(ctypes.byref(desc), ctypes.byref(plan)))
+    return plan.value
+
+
+def conv_gnorm_workspace_bytes(plan):
+    n = ctypes.c_int64()
+    _check(lib().conv_gnorm_workspace_bytes(plan, ctypes.byref(n)))
+    return n.value
+
+
+def conv_gnorm_run(plan, args, workspace, workspace_bytes, stream=0):
+    _check(lib().conv_gnorm_run(plan, args, workspace, workspace_bytes, stream))
+
+
+def conv_gnorm_bwd_workspace_bytes(plan):
+    n = ctypes.c_int64()
+    _check(lib().conv_gnorm_bwd_workspace_bytes(plan, ctypes.byref(n)))
+    return n.value
+
+
+def conv_gnorm_bwd_run(plan, args, workspace, workspace_bytes, stream=0):
+    _check(lib().conv_gnorm_bwd_run(plan, args, workspace, workspace_bytes, stream))
+
+
+def conv_gnorm_destroy(plan):
+    lib().conv_gnorm_destroy(plan)
+
+
+def conv_gnorm_describe(plan):
+    return lib().conv_gnorm_describe(plan).decode()

@@ -588,6 +588,72 @@ conv_status_t conv_delta_bwd_run(const conv_delta_plan_t *plan, const conv_delta
 void conv_delta_destroy(conv_delta_plan_t *plan);
 const char *conv_delta_describe(const conv_delta_plan_t *plan);
 
+/* ---- Group norm with an activation ------------------------------------------
+ * Channels innermost, as the convolutions leave them: x is N x L x G x C, L the
+ * pixels or tokens of a sample, G groups of C channels.  Statistics are those of
+ * a group's channels over all the sample's rows (per_token = 0), or of each row by
+ * itself (per_token = 1: a head's channels behind a mixer, keys and queries in front
+ * of one).
+ *
+ *   xhat = (x - mean) / sqrt(var + eps)   var the mean of (x - mean)^2    (center = 1)
+ *   xhat =  x         / sqrt(ms + eps)    ms the mean of x^2              (center = 0)
+ *   v    = w[g,c] * xhat + bias[g,c]
+ *   y    = act(v)    or, with a gate,    v * act(gate)
+ *
+ * act: none, v * sigmoid(v), or v * Phi(v) (the erf form).  x, gate and y have *_ld
+ * elements from row to row (0 = G * C) and L times that from sample to sample; w and
+ * bias are G x C; all in the descriptor's dtype.  lengths as conv_causal: rows
+ * behind a sample's length are not read and count for nothing, their y and gradients
+ * are zeros.  Statistics and sums are fp32 and more, squares are summed around a
+ * mean, the result is rounded once.  A NaN or an infinity reaches its whole group.
+ *
+ * Partial sums go through a caller-owned device workspace (16-byte aligned; the
+ * size may be 0, then it may be NULL) and are added in a fixed order.  Calls that
+ * overlap in time need workspaces of their own.  Alignment, overlap, ownership,
+ * threading, asynchrony and errors as conv_causal. */
+enum { CONV_NORM_ACT_NONE = 0, CONV_NORM_ACT_SILU = 1, CONV_NORM_ACT_GELU = 2 };
+
+typedef struct {
+    int32_t dtype;         /* conv_dtype_t                                     */
+    int32_t act;           /* CONV_NORM_ACT_*                                  */
+    int32_t has_bias;      /* 0 or 1                                           */
+    int32_t gated;         /* 0 or 1                                           */
+    int32_t center;        /* 0 or 1                                           */
+    int32_t per_token;     /* 0 or 1                                           */
+    int64_t N;             /* samples, >= 0                                    */
+    int64_t L;             /* rows of a sample, >= 0                           */
+    int64_t G;             /* groups, >= 1                                     */
+    int64_t C;             /* channels of a group, >= 1                        */
+    double eps;            /* finite, >= 0                                     */
+} conv_gnorm_desc_t;
+
+typedef struct {
+    const void *x, *w, *bias, *gate;    /* bias, gate NULL iff the plan has none */
+    const int32_t *lengths;             /* optional                            */
+    void *y;
+    int64_t x_ld, gate_ld, y_ld;
+} conv_gnorm_args_t;
+
+/* Gradients of <y, dy>; dw and dbias are the sums over all rows, in the
+ * descriptor's dtype.  dbias and dgate NULL iff the plan has none. */
+typedef struct {
+    const void *dy, *x, *w, *bias, *gate;
+    const int32_t *lengths;
+    void *dx, *dw, *dbias, *dgate;
+    int64_t dy_ld, x_ld, gate_ld, dx_ld, dgate_ld;
+} conv_gnorm_bwd_args_t;
+
+typedef struct conv_gnorm_plan conv_gnorm_plan_t;   /* opaque */
+conv_status_t conv_gnorm_create(const conv_gnorm_desc_t *desc, conv_gnorm_plan_t **plan);
+conv_status_t conv_gnorm_workspace_bytes(const conv_gnorm_plan_t *plan, int64_t *bytes);
+conv_status_t conv_gnorm_run(const conv_gnorm_plan_t *plan, const conv_gnorm_args_t *args, void *workspace,
+                             int64_t workspace_bytes, void *stream);
+conv_status_t conv_gnorm_bwd_workspace_bytes(const conv_gnorm_plan_t *plan, int64_t *bytes);
+conv_status_t conv_gnorm_bwd_run(const conv_gnorm_plan_t *plan, const conv_gnorm_bwd_args_t *args, void *workspace,
+                                 int64_t workspace_bytes, void *stream);
+void conv_gnorm_destroy(conv_gnorm_plan_t *plan);
+const char *conv_gnorm_describe(const conv_gnorm_plan_t *plan);
+
 /* Message of the last failed call on this thread ("" if none). */
 const char *conv_fwd_last_error(void);
 
