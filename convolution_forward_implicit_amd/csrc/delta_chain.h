@@ -1,0 +1,406 @@
+// The passes of the gated delta rule that go from chunk to chunk: the states with y,
+// the states for a gradient, and the states' gradient.
+//
+// A chunk's state follows from the one before it by three products, each of which needs
+// all of the one before: K S0^T gives Z, N (beta Z) gives Y, K^T U the new state.  With few
+// heads this chain is what takes the time, so a workgroup has 16 channels of one head
+// only and its four waves share every product: wave t has the tokens 16 t .. of the
+// first two and, of the third, the keys 32 t .. (and 128 on), whose state it holds.  What
+// each leaves goes to the others through LDS, split into its terms once, with a
+// barrier behind each product.  y needs nothing that a wave has not read anyway: Q S0^T
+// fills the wait behind Z, M U that behind the state.  Two more waves bring K and N
+// into LDS a chunk ahead; Q and M have one reader each and go to its registers.
+#pragma once
+
+#include "delta_kernels.h"
+#include "igemm_dma.h"
+
+namespace convfwd {
+
+enum ChainMode { CHAIN_Y, CHAIN_STATES, CHAIN_BACK };
+
+constexpr int kLoaders = 2;
+
+template <typename T, int SP, ChainMode MODE> struct ChainShared {
+    static constexpr int KS = SP / 32, NT = kN<T>, NM = kM<T>;
+    static constexpr int KEYS = 4 * KS * kFrag<T>, TRI = kTri * NT * kFrag<T>, OPS = KEYS + kRows + TRI;
+    struct Exchange {
+        char s[NT * KS * kFrag<T>];     // the state (its gradient)
+        char a[NT * 2 * kFrag<T>];      // Z (dU)
+        char b[NT * 2 * kFrag<T>];      // e^{c_Q - c} U (e^c dV)
+        char y[(MODE == CHAIN_Y ? NM : 1) * 2 * kFrag<T>];      // Y (dO)
+        char x[(MODE == CHAIN_BACK ? NT : 0) * 2 * kFrag<T> + 16];      // (scale e^c dO)
+    };
+    static constexpr int NB = 2 * OPS + (int)sizeof(Exchange) <= 160 * 1024 ? 2 : 1;     // chunks of K and N
+    __align__(16) char ops[NB][OPS];
+    __align__(16) Exchange x;
+};
+
+// KB kilobytes of memory to LDS, by the loaders.  The loads are written out: the
+// compiler, which cannot see what they write, would wait for them before any read of
+// LDS.
+template <int KB> SEQ_DEV void fetch(const char *from, char *to, int wave, int lane)
+{
+    const i32x4_t buf = uniform_rsrc(buffer_rsrc(from, KB * 1024));
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)to);
+#pragma unroll
+    for (int e = 0; e < KB; e += kLoaders) {
+        const uint32_t b = (uint32_t)(e + wave) * 1024;
+        uint32_t saved;
+        if (KB % kLoaders == 0 || e + wave < KB)
+            asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds\n\ts_mov_b32 m0, %0"
+                         : "=&s"(saved) : "s"(at + b), "v"(lane * 16), "s"(buf), "s"(b) : "memory");
+    }
+}
+// The workgroup's waves meet; LDS writes are done, loads may be under way.
+SEQ_DEV void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// The four rows 4q + r of a column that a lane of a result holds, of `rows` rows of a
+// tensor from row `first`: rows behind and columns at P and behind come as zeros and are
+// not written.
+template <typename T> struct LaneRows {
+    __amdgpu_buffer_rsrc_t buf;
+    uint32_t at, step;
+    SEQ_DEV LaneRows(const void *g, int64_t ld, int64_t first, int rows, int P, int ch, int lane)
+    {
+        const int64_t bytes = rows > 0 ? ((int64_t)(rows - 1) * ld + P) * (int64_t)sizeof(T) : 0;
+        buf = __builtin_amdgcn_make_buffer_rsrc((T *)const_cast<void *>(g) + first * ld, 0, (int)bytes, 0x00020000);
+        step = (uint32_t)ld * (uint32_t)sizeof(T);
+        at = ch < P ? (uint32_t)((lane >> 4) * 4) * step + (uint32_t)ch * (uint32_t)sizeof(T) : 0x80000000u;
+    }
+    SEQ_DEV uint32_t bits(int r) const      // an element's, as a float's
+    {
+        if constexpr (sizeof(T) == 4) return __builtin_amdgcn_raw_buffer_load_b32(buf, at + (uint32_t)r * step, 0, 0);
+        else return (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(buf, at + (uint32_t)r * step, 0, 0) << 16;
+    }
+    SEQ_DEV void put(int r, float v) const
+    {
+        if constexpr (sizeof(T) == 4)
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), buf, at + (uint32_t)r * step, 0, kStream);
+        else
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)v), buf, at + (uint32_t)r * step, 0, kStream);
+    }
+};
+
+// A result of the tokens 16 t .. as terms of an operand over the tokens: half of the 32
+template <typename T, int NS> SEQ_DEV void put_half(char *at, int t, int lane, f32x4 v)
+{
+    if constexpr (sizeof(T) == 4) {
+        reinterpret_cast<f32x4 *>(at + (t >> 1) * kFrag<T> + (t & 1) * 1024)[lane] = v;
+    } else {
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+            float a = v[0], b = v[1], c = v[2], d = v[3];
+            const uint32_t lo = take_pair(a, b), hi = take_pair(c, d);
+            v = f32x4{a, b, c, d};
+            *reinterpret_cast<uint64_t *>(at + (k * 2 + (t >> 1)) * kFrag<T> + lane * 16 + (t & 1) * 8) = (uint64_t)hi << 32 | lo;
+        }
+    }
+}
+template <typename T, int NS> SEQ_DEV void get_split(const char *at, int apart, int lane, Split<T, NS> &s)
+{
+#pragma unroll
+    for (int e = 0; e < NS; ++e) s.f[e] = get_frag<T>(at + e * apart, lane);
+}
+// K^T's operand of the keys 32 s + 8 (r / 4) + 4 a + r % 4 (row r) and the tokens 32 P + 4q ..,
+// 32 P + 16 + 4q .. from K's in LDS, [4][KS]
+template <int KS> SEQ_DEV bf16x8 get_transposed(const char *at, int P, int s, int a, int lane, bf16_t)
+{
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
+    const int i = lane & 15;
+    const char *p = at + (2 * P * KS + s) * 1024 + ((i & 3) * 16 + (lane >> 4) * 4 + (i >> 2)) * 16 + 8 * a;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + KS * 1024));
+    return __builtin_bit_cast(bf16x8, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+template <int KS> SEQ_DEV Frag<float>::type get_transposed(const char *at, int P, int s, int a, int lane, float)
+{
+    const int r = lane & 15;
+    // key 8 (r / 4) + 4 a + r % 4 of token row: lane group r / 4, vector a, element r % 4
+    const float *p = reinterpret_cast<const float *>(at + (2 * P * KS + s) * 2048 + a * 1024 + ((r >> 2) * 16 + (lane >> 4) * 4) * 16) + (r & 3);
+    Frag<float>::type f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f.v[e] = p[e * 4], f.v[4 + e] = p[KS * 512 + e * 4];
+    return f;
+}
+
+template <typename T, int SP, ChainMode MODE>
+SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, MODE> &sh)
+{
+    typedef ChainShared<T, SP, MODE> Shared;
+    constexpr bool GRAD = MODE != CHAIN_Y, BACK = MODE == CHAIN_BACK;
+    constexpr int KS = SP / 32, NT = kN<T>, NM = kM<T>, NB = Shared::NB, KEYS = Shared::KEYS, F = kFrag<T>;
+    constexpr int OWN = (KS + 3) / 4;                   // key blocks that a wave may hold
+    const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q4 = (lane >> 4) * 4;
+    const int64_t nh = unit / p.blocks, n = nh / p.H;
+    const int h = (int)(nh - n * p.H), grp = h / (p.H / p.G), ch = (int)(unit - nh * p.blocks) * 16 + l16;
+    const int64_t len = seq_len(p.lengths, n, p.L);
+    const int live = (int)((len + kDQ - 1) / kDQ);
+    const char *keys = p.keys + (n * p.K * p.G + grp) * keys_bytes<T, SP>(GRAD), *heads = p.heads + (n * p.K * p.H + h) * head_bytes<T>(GRAD);
+    const int64_t keys_step = p.G * keys_bytes<T, SP>(GRAD), head_step = p.H * head_bytes<T>(GRAD);
+    constexpr int64_t tri = (GRAD ? (int64_t)sizeof(ChunkScalars) : kRows) + (BACK ? Shared::TRI : 0);      // N, or its transpose
+    auto chunk = [&](int i) { return BACK ? live - 1 - i : i; };
+    if (w >= 4) {
+        auto load = [&](int i) {
+            const char *k = keys + chunk(i) * keys_step, *a = heads + chunk(i) * head_step;
+            fetch<KEYS / 1024>(k, sh.ops[i % NB], w - 4, lane);
+            fetch<kRows / 1024>(a, sh.ops[i % NB] + KEYS, w - 4, lane);
+            fetch<Shared::TRI / 1024>(a + tri, sh.ops[i % NB] + KEYS + kRows, w - 4, lane);
+        };
+        if (NB == 2 && live > 0) load(0);
+        for (int i = 0; i < live; ++i) {
+            if (NB == 1) {
+                meet();
+                load(i);
+            }
+            wait_vmcnt<0>();
+            meet();
+            if (NB == 2 && i + 1 < live) load(i + 1);
+            meet();
+            meet();
+        }
+        return;
+    }
+    f32x4 st[OWN][2];
+    auto state_at = [&](int o, int a, int r) { return 32 * (w + 4 * o) + 2 * q4 + 4 * a + r; };      // the key
+    {
+        const float *from = BACK ? p.dstate_out : p.state;
+        const float *g = from + (nh * p.P + ch) * p.S;
+#pragma unroll
+        for (int o = 0; o < OWN; ++o)
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) st[o][a][r] = from && ch < p.P && state_at(o, a, r) < p.S ? g[state_at(o, a, r)] : 0.0f;
+    }
+    auto put_state = [&]() {
+#pragma unroll
+        for (int o = 0; o < OWN; ++o) {
+            if (w + 4 * o >= KS) continue;
+            Split<T, NT> s;
+            stack(st[o][0], st[o][1], s);
+#pragma unroll
+            for (int e = 0; e < NT; ++e) put_frag(sh.x.s + (e * KS + w + 4 * o) * F, lane, s.f[e]);
+        }
+    };
+    // what this wave alone reads: Q and M; going back M^T and Q^T
+    constexpr int NQ = BACK ? 4 * OWN : MODE == CHAIN_Y ? KS : 0, TM = BACK ? NT : MODE == CHAIN_Y ? NM : 0;
+    typename Frag<T>::type qf[NQ + 1];
+    Split<T, TM + 1> mf[2];
+    uint32_t vb[4];                     // v, or dO, of the next chunk
+    auto load_q = [&](int i) {
+        const char *k = keys + chunk(i) * keys_step;
+#pragma unroll
+        for (int s = 0; s < NQ; ++s) {
+            if (!BACK) qf[s] = get_frag<T>(k + ((4 + w) * KS + s) * F, lane);
+            else if (w + 4 * (s >> 2) < KS) qf[s] = get_frag<T>(k + (12 * KS + (w + 4 * (s >> 2)) * 4 + (s & 3)) * F, lane);
+        }
+    };
+    auto load_m = [&](int i) {
+        const char *m = heads + chunk(i) * head_step + tri + Shared::TRI;
+#pragma unroll
+        for (int P = 0; P < 2; ++P)
+            if (BACK ? P >= w / 2 : P <= w / 2) {
+#pragma unroll
+                for (int e = 0; e < TM; ++e)
+                    mf[P].f[e] = get_frag<T>(m + (BACK ? upper(w, P) * NT + e : lower(w, P) * NM + e) * F, lane);
+            }
+    };
+    auto rows_of = [&](const void *t, int64_t ld, int i) {
+        const int64_t t0 = (int64_t)chunk(i) * kDQ + 16 * w;
+        return LaneRows<T>((const T *)t + (int64_t)h * p.P, ld, n * p.L + t0, (int)(len - t0 < 16 ? len - t0 : 16), p.P, ch, lane);
+    };
+    auto load_v = [&](int i) {
+        const LaneRows<T> rows = BACK ? rows_of(p.dy, p.dy_ld, i) : rows_of(p.v, p.v_ld, i);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) vb[r] = rows.bits(r);
+    };
+    if (live > 0) {
+        load_q(0);
+        load_m(0);
+        load_v(0);
+        put_state();
+    }
+    for (int i = 0; i < live; ++i) {
+        const char *ops = sh.ops[i % NB], *tr = ops + KEYS + kRows;
+        const ChunkScalars *cs = reinterpret_cast<const ChunkScalars *>(ops + KEYS);
+        const int64_t at = nh * p.K + chunk(i);
+        f32x4 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint32_t b = vb[r];
+            v[r] = __builtin_bit_cast(float, b);
+        }
+        if constexpr (BACK) put_half<T, 1>(sh.x.y, w, lane, v);
+        if (i + 1 < live) load_v(i + 1);
+        if constexpr (GRAD) {
+            float *b = p.bound[BACK] + (at * p.PP + ch) * SP + 2 * q4;
+#pragma unroll
+            for (int o = 0; o < OWN; ++o)
+                if (w + 4 * o < KS)
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) *reinterpret_cast<f32x4 *>(b + 32 * (w + 4 * o) + 4 * a) = st[o][a];
+        }
+        if (NB == 1) meet();
+        meet();
+        // K S0^T, a sum of each term by itself
+        Split<T, NT> sp[KS];
+        typename Frag<T>::type kf[KS];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            kf[s] = get_frag<T>(ops + (w * KS + s) * F, lane);
+            get_split(sh.x.s + s * F, KS * F, lane, sp[s]);
+        }
+        const f32x4 grow = *reinterpret_cast<const f32x4 *>(cs->from_start + 16 * w + q4);
+        const f32x4 fade = *reinterpret_cast<const f32x4 *>(cs->to_end + 16 * w + q4);
+        const f32x4 beta = *reinterpret_cast<const f32x4 *>(cs->beta + 16 * w + q4);
+        const float total = cs->from_start[kDQ - 1];
+        f32x4 r[NT];
+#pragma unroll
+        for (int e = 0; e < NT; ++e) r[e] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int e = 0; e < NT; ++e) r[e] = mma(kf[s], sp[s].f[e], r[e]);
+#pragma unroll
+        for (int e = NT - 1; e > 0; --e) r[e - 1] = r[e - 1] + r[e];
+        f32x4 z;
+        if constexpr (BACK) {
+            z = r[0] * fade;
+#pragma unroll
+            for (int P = 0; P < 2; ++P)
+                if (P >= w / 2) {
+                    const typename Frag<T>::type d = get_frag<T>(sh.x.y + P * F, lane);
+#pragma unroll
+                    for (int e = NT - 1; e >= 0; --e) z = mma(mf[P].f[e], d, z);         // dU
+                }
+            if (i + 1 < live) load_m(i + 1);
+        } else {
+            z = v - grow * r[0];
+        }
+        put_half<T, NT>(sh.x.a, w, lane, z);
+        f32x4 y = {0, 0, 0, 0};
+        if constexpr (MODE == CHAIN_Y) {
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int e = 0; e < NM; ++e) y = mma(qf[s], sp[s].f[e], y);
+            y = y * (grow * p.scale);
+            if (i + 1 < live) load_q(i + 1);
+        }
+        if constexpr (BACK) put_half<T, NT>(sh.x.x, w, lane, v * (grow * p.scale));
+        Split<T, NT> nf[2];
+#pragma unroll
+        for (int P = 0; P < 2; ++P)
+            if (BACK ? P >= w / 2 : P <= w / 2) get_split(tr + (BACK ? upper(w, P) : lower(w, P)) * NT * F, F, lane, nf[P]);
+        meet();
+        // N (beta Z)
+#pragma unroll
+        for (int P = 0; P < 2; ++P)
+            if (BACK ? P >= w / 2 : P <= w / 2) {
+                Split<T, NT> b;
+                get_split(sh.x.a + P * F, 2 * F, lane, b);
+                z = mma_terms(nf[P], b, z);
+            }
+        put_half<T, NT>(sh.x.b, w, lane, z * (BACK ? beta * grow * -1.0f : beta * fade));
+        if constexpr (MODE == CHAIN_Y) put_half<T, NM>(sh.x.y, w, lane, z);
+        if constexpr (GRAD) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p.rows[BACK][(at * kDQ + 16 * w + q4 + e) * p.PP + ch] = z[e];
+        }
+        typename Frag<T>::type kt[OWN][2][2];
+#pragma unroll
+        for (int o = 0; o < OWN; ++o)
+            if (w + 4 * o < KS)
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+#pragma unroll
+                    for (int P = 0; P < 2; ++P) kt[o][a][P] = get_transposed<KS>(ops, P, w + 4 * o, a, lane, T());
+        meet();
+        // the state behind the chunk
+        if (w < KS) {
+            Split<T, NT> u[2], x[2];
+#pragma unroll
+            for (int P = 0; P < 2; ++P) {
+                get_split(sh.x.b + P * F, 2 * F, lane, u[P]);
+                if constexpr (BACK) get_split(sh.x.x + P * F, 2 * F, lane, x[P]);
+            }
+#pragma unroll
+            for (int o = 0; o < OWN; ++o) {
+                if (w + 4 * o >= KS) continue;
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    f32x4 s = st[o][a] * total;
+#pragma unroll
+                    for (int P = 0; P < 2; ++P)
+#pragma unroll
+                        for (int e = NT - 1; e >= 0; --e) {
+                            s = mma(kt[o][a][P], u[P].f[e], s);
+                            if constexpr (BACK) s = mma(qf[4 * o + 2 * a + P], x[P].f[e], s);
+                        }
+                    st[o][a] = s;
+                }
+            }
+            put_state();
+        }
+        if constexpr (BACK) {
+            if (i + 1 < live) load_q(i + 1);
+        }
+        if constexpr (MODE == CHAIN_Y) {
+#pragma unroll
+            for (int P = 0; P < 2; ++P)
+                if (P <= w / 2) {
+                    Split<T, NM> b;
+                    get_split(sh.x.y + P * F, 2 * F, lane, b);
+#pragma unroll
+                    for (int e = 0; e < NM; ++e)
+#pragma unroll
+                        for (int k = 0; k < NM - e; ++k) y = mma(mf[P].f[e], b.f[k], y);
+                }
+            if (i + 1 < live) load_m(i + 1);
+            const LaneRows<T> rows = rows_of(p.y, p.y_ld, i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) rows.put(e, y[e]);
+        }
+    }
+    float *to = BACK ? p.dstate : p.state_out;
+    if (to && ch < p.P)
+#pragma unroll
+        for (int o = 0; o < OWN; ++o)
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (w + 4 * o < KS && state_at(o, a, r) < p.S) to[(nh * p.P + ch) * p.S + state_at(o, a, r)] = st[o][a][r];
+    if (MODE == CHAIN_Y && ch < p.P)
+        for (int64_t t = len + 4 * w + (lane >> 4); t < p.L; t += 16) ((T *)p.y)[(n * p.L + t) * p.y_ld + (int64_t)h * p.P + ch] = (T)0.0f;
+}
+
+constexpr int kChainThreads = 64 * (4 + kLoaders);
+
+template <typename T, int SP> __global__ void __launch_bounds__(kChainThreads) delta_y_kernel(DeltaParams p)
+{
+    __shared__ ChainShared<T, SP, CHAIN_Y> sh;
+    const int64_t units = (int64_t)p.N * p.H * p.blocks, unit = unit_of(blockIdx.x, units);
+    if (unit < units) delta_chain<T, SP, CHAIN_Y>(p, unit, sh);
+}
+
+// The two passes over the states of a gradient, which do not depend on each other.
+template <typename T, int SP> __global__ void __launch_bounds__(kChainThreads) delta_states_kernel(DeltaParams p)
+{
+    __shared__ union Both {
+        ChainShared<T, SP, CHAIN_STATES> ahead;
+        ChainShared<T, SP, CHAIN_BACK> back;
+        SEQ_DEV Both() {}
+    } sh;
+    const int64_t units = (int64_t)p.N * p.H * p.blocks, half = gridDim.x / 2;
+    const bool back = blockIdx.x < half;
+    const int64_t unit = unit_of(back ? blockIdx.x : blockIdx.x - half, units);
+    if (unit >= units) return;
+    if (back) delta_chain<T, SP, CHAIN_BACK>(p, unit, sh.back);
+    else delta_chain<T, SP, CHAIN_STATES>(p, unit, sh.ahead);
+}
+
+}  // namespace convfwd

@@ -70,20 +70,25 @@ struct DeltaParams {
 
 // ---- operands in the workspace -------------------------------------------------
 template <typename T> constexpr int kFrag = 64 * 8 * (int)sizeof(T);
-// K (4 x SP/32), Q (the same), K^T and, for the gradient, Q^T (SP/16 x 2)
-template <typename T, int SP> constexpr int64_t keys_bytes(bool grad) { return (int64_t)(grad ? 4 : 3) * (SP / 8) * kFrag<T>; }
-// what a head adds: -N beta of three terms, M of two, c; gradient: -N beta, (-N beta')^T and M^T of three terms
+// K (4 x SP/32), Q (the same) and, for the gradient, K^T and Q^T (SP/16 x 2)
+template <typename T, int SP> constexpr int64_t keys_bytes(bool grad) { return (int64_t)(grad ? 4 : 2) * (SP / 8) * kFrag<T>; }
+// what a head adds: -N beta of three terms, M beta of two; gradient: -N beta, (-beta N)^T and M^T of three terms
 template <typename T> constexpr int kN = 3;
 template <> constexpr int kN<float> = 1;
 template <typename T> constexpr int kM = 2;
 template <> constexpr int kM<float> = 1;
 struct ChunkScalars {
-    float from_start[kDQ], to_end[kDQ], beta[kDQ];
-    double cum[kDQ];
+    float from_start[kDQ];      // e^{c_i}
+    float beta[kDQ];
+    float to_end[kDQ];          // e^{c_Q - c_i}
+    float pad[kDQ];             // one load of 1 KB
+    double cum[kDQ];            // c_i; the gradient's
 };
+constexpr int kRows = 1024;     // bytes of ChunkScalars that the passes over the states read
+// forward: ChunkScalars' first kilobyte, N, M; gradient: ChunkScalars, N, N^T, M^T
 template <typename T> constexpr int64_t head_bytes(bool grad)
 {
-    return (int64_t)(grad ? 3 * kN<T> : kN<T> + kM<T>) * kTri * kFrag<T> + (int64_t)sizeof(ChunkScalars);
+    return grad ? (int64_t)sizeof(ChunkScalars) + 3 * kN<T> * kTri * kFrag<T> : kRows + (int64_t)(kN<T> + kM<T>) * kTri * kFrag<T>;
 }
 
 SEQ_DEV void put_frag(char *at, int lane, bf16x8 f) { reinterpret_cast<bf16x8 *>(at)[lane] = f; }
@@ -199,9 +204,9 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaParams p)
             put_frag(at + (4 * KS + w * KS + s) * kFrag<T>, lane, read_rows(sh.q, LD, 16 * w, 32 * s, lane));
         }
         at += 8 * KS * kFrag<T>;
-        for (int f = w; f < 4 * KS; f += 4) {       // (s, a, pair of token tiles)
+        for (int f = w; f < (GRAD ? 4 * KS : 0); f += 4) {       // (s, a, pair of token tiles)
             put_frag(at + f * kFrag<T>, lane, read_keys(sh.k, LD, 32 * (f & 1), f >> 2, f >> 1 & 1, lane));
-            if (GRAD) put_frag(at + (4 * KS + f) * kFrag<T>, lane, read_keys(sh.q, LD, 32 * (f & 1), f >> 2, f >> 1 & 1, lane));
+            put_frag(at + (4 * KS + f) * kFrag<T>, lane, read_keys(sh.q, LD, 32 * (f & 1), f >> 2, f >> 1 & 1, lane));
         }
     }
     // k_j . k_i and k_j . q_i: rows j of tile J, columns i of tile w
@@ -229,12 +234,13 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaParams p)
             const double cum = wave_prefix((double)(g < -1e5f ? -1e5f : g)), end = wave_last(cum);
             sh.cum[lane] = cum;
             sh.beta[lane] = beta;
-            ChunkScalars *cs = reinterpret_cast<ChunkScalars *>(at + head_bytes<T>(GRAD) - sizeof(ChunkScalars));
+            ChunkScalars *cs = reinterpret_cast<ChunkScalars *>(at);
             cs->from_start[lane] = expf((float)cum);
             cs->to_end[lane] = expf((float)(end - cum));
             cs->beta[lane] = beta;
-            cs->cum[lane] = cum;
+            if (GRAD) cs->cum[lane] = cum;
         }
+        at += GRAD ? (int64_t)sizeof(ChunkScalars) : kRows;
         __syncthreads();
         f32x4 tt[4], mm[4], beta[4];
         const double ci = sh.cum[i];
@@ -342,266 +348,6 @@ SEQ_DEV int64_t unit_of(int64_t block, int64_t units)
 {
     const int64_t per = (units + 7) / 8;
     return (block & 7) * per + (block >> 3);
-}
-
-// A state tile pair s: key 32 s + 8q + 4a + r in register [2s + a][r] of channel lane % 16
-template <int SP> SEQ_DEV void load_state(const float *state, bool have, int S, int lane, f32x4 (&st)[SP / 16])
-{
-    const int q8 = (lane >> 4) * 8;
-#pragma unroll
-    for (int i = 0; i < SP / 16; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int key = 32 * (i >> 1) + q8 + 4 * (i & 1) + r;
-            st[i][r] = have && key < S ? state[key] : 0.0f;
-        }
-}
-template <int SP> SEQ_DEV void store_state(float *state, bool have, int S, int lane, const f32x4 (&st)[SP / 16])
-{
-    const int q8 = (lane >> 4) * 8;
-#pragma unroll
-    for (int i = 0; i < SP / 16; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int key = 32 * (i >> 1) + q8 + 4 * (i & 1) + r;
-            if (have && key < S) state[key] = st[i][r];
-        }
-}
-
-// The forward pass (OUT: y and the last state) or the gradient's pass over the
-// states (the state in front of every chunk, and Y).
-template <typename T, int SP, bool OUT> SEQ_DEV void delta_forward(const DeltaParams &p, int64_t unit, int lane)
-{
-    constexpr int KS = SP / 32, NT = OUT ? kM<T> : 1;
-    const int l16 = lane & 15, q4 = (lane >> 4) * 4;
-    const int64_t nh = unit / p.blocks, n = nh / p.H;
-    const int h = (int)(nh - n * p.H), grp = h / (p.H / p.G), ch = (int)(unit - nh * p.blocks) * 16 + l16;
-    const bool mine = ch < p.P;
-    const int64_t len = seq_len(p.lengths, n, p.L);
-    const T *vg = (const T *)p.v + n * p.L * p.v_ld + (int64_t)h * p.P + ch;
-    T *yg = (T *)p.y + n * p.L * p.y_ld + (int64_t)h * p.P + ch;
-    f32x4 st[SP / 16];
-    load_state<SP>(p.state + (nh * p.P + ch) * p.S, p.state && mine, p.S, lane, st);
-    const int live = (int)((len + kDQ - 1) / kDQ);
-    for (int c = 0; c < live; ++c) {
-        const char *keys = p.keys + ((n * p.K + c) * p.G + grp) * keys_bytes<T, SP>(!OUT);
-        const char *head = p.heads + ((n * p.K + c) * p.H + h) * head_bytes<T>(!OUT);
-        const ChunkScalars *cs = reinterpret_cast<const ChunkScalars *>(head + head_bytes<T>(!OUT) - sizeof(ChunkScalars));
-        const int64_t t0 = (int64_t)c * kDQ;
-        const int rows = (int)(len - t0 < kDQ ? len - t0 : kDQ);
-        if constexpr (!OUT) {
-            float *b = p.bound[0] + ((nh * p.K + c) * p.PP + ch) * SP + (lane >> 4) * 8;
-#pragma unroll
-            for (int i = 0; i < SP / 16; ++i) *reinterpret_cast<f32x4 *>(b + 32 * (i >> 1) + 4 * (i & 1)) = st[i];
-        }
-        Split<T, kN<T>> sp[KS];
-#pragma unroll
-        for (int s = 0; s < KS; ++s) stack(st[2 * s], st[2 * s + 1], sp[s]);
-        f32x4 z[4], grow[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            grow[t] = *reinterpret_cast<const f32x4 *>(cs->from_start + 16 * t + q4);
-            f32x4 acc = {0, 0, 0, 0};
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                Split<T, 1> a;
-                a.f[0] = get_frag<T>(keys + (t * KS + s) * kFrag<T>, lane);
-                acc = mma_terms(a, sp[s], acc);
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * t + q4 + r;
-                const float v = mine && row < rows ? (float)vg[(t0 + row) * p.v_ld] : 0.0f;
-                z[t][r] = fmaf(-grow[t][r], acc[r], v);
-            }
-        }
-        Split<T, kN<T>> zs[2];
-        stack(z[0], z[1], zs[0]);
-        stack(z[2], z[3], zs[1]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int P = 0; P <= t / 2; ++P) {
-                Split<T, kN<T>> a;
-#pragma unroll
-                for (int e = 0; e < kN<T>; ++e) a.f[e] = get_frag<T>(head + (lower(t, P) * kN<T> + e) * kFrag<T>, lane);
-                z[t] = mma_terms(a, zs[P], z[t]);        // Y
-            }
-        if constexpr (OUT) {
-            Split<T, NT> ys[2];
-            stack(z[0], z[1], ys[0]);
-            stack(z[2], z[3], ys[1]);
-            const char *qs = keys + 4 * KS * kFrag<T>, *ms = head + kTri * kN<T> * kFrag<T>;
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                f32x4 acc = {0, 0, 0, 0};
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const typename Frag<T>::type a = get_frag<T>(qs + (t * KS + s) * kFrag<T>, lane);
-#pragma unroll
-                    for (int e = 0; e < NT; ++e) acc = mma(a, sp[s].f[e], acc);
-                }
-                acc = acc * (grow[t] * p.scale);
-#pragma unroll
-                for (int P = 0; P <= t / 2; ++P) {
-                    Split<T, NT> a;
-#pragma unroll
-                    for (int e = 0; e < NT; ++e) a.f[e] = get_frag<T>(ms + (lower(t, P) * NT + e) * kFrag<T>, lane);
-                    acc = mma_terms(a, ys[P], acc);
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * t + q4 + r;
-                    if (mine && row < rows) yg[(t0 + row) * p.y_ld] = (T)acc[r];
-                }
-            }
-        } else {
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    p.rows[0][((nh * p.K + c) * kDQ + 16 * t + q4 + r) * p.PP + ch] = z[t][r];
-        }
-        Split<T, kN<T>> us[2];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-            z[t] = z[t] * (*reinterpret_cast<const f32x4 *>(cs->beta + 16 * t + q4) *
-                           *reinterpret_cast<const f32x4 *>(cs->to_end + 16 * t + q4));
-        stack(z[0], z[1], us[0]);
-        stack(z[2], z[3], us[1]);
-        const float total = cs->from_start[kDQ - 1];
-        const char *kt = keys + 8 * KS * kFrag<T>;
-#pragma unroll
-        for (int i = 0; i < SP / 16; ++i) {
-            st[i] = st[i] * total;
-#pragma unroll
-            for (int P = 0; P < 2; ++P) {
-                Split<T, 1> a;
-                a.f[0] = get_frag<T>(kt + (i * 2 + P) * kFrag<T>, lane);
-                st[i] = mma_terms(a, us[P], st[i]);
-            }
-        }
-    }
-    if constexpr (OUT) {
-        if (mine)
-            for (int64_t t = len + (lane >> 4); t < p.L; t += 4) yg[t * p.y_ld] = (T)0.0f;
-        store_state<SP>(p.state_out + (nh * p.P + ch) * p.S, p.state_out && mine, p.S, lane, st);
-    }
-}
-
-template <typename T, int SP> __global__ void __launch_bounds__(64) delta_fwd_kernel(DeltaParams p)
-{
-    const int64_t units = (int64_t)p.N * p.H * p.blocks, unit = unit_of(blockIdx.x, units);
-    if (unit < units) delta_forward<T, SP, true>(p, unit, threadIdx.x);
-}
-
-// The gradient of the state, from the last chunk to the first: that of the state
-// behind every chunk, and E.
-template <typename T, int SP> SEQ_DEV void delta_backward(const DeltaParams &p, int64_t unit, int lane)
-{
-    constexpr int KS = SP / 32;
-    const int l16 = lane & 15, q4 = (lane >> 4) * 4;
-    const int64_t nh = unit / p.blocks, n = nh / p.H;
-    const int h = (int)(nh - n * p.H), grp = h / (p.H / p.G), ch = (int)(unit - nh * p.blocks) * 16 + l16;
-    const bool mine = ch < p.P;
-    const int64_t len = seq_len(p.lengths, n, p.L);
-    const T *dyg = (const T *)p.dy + n * p.L * p.dy_ld + (int64_t)h * p.P + ch;
-    f32x4 st[SP / 16];
-    load_state<SP>(p.dstate_out + (nh * p.P + ch) * p.S, p.dstate_out && mine, p.S, lane, st);
-    for (int c = (int)((len + kDQ - 1) / kDQ) - 1; c >= 0; --c) {
-        const char *keys = p.keys + ((n * p.K + c) * p.G + grp) * keys_bytes<T, SP>(true);
-        const char *head = p.heads + ((n * p.K + c) * p.H + h) * head_bytes<T>(true);
-        const ChunkScalars *cs = reinterpret_cast<const ChunkScalars *>(head + head_bytes<T>(true) - sizeof(ChunkScalars));
-        const int64_t t0 = (int64_t)c * kDQ;
-        const int rows = (int)(len - t0 < kDQ ? len - t0 : kDQ);
-        float *b = p.bound[1] + ((nh * p.K + c) * p.PP + ch) * SP + (lane >> 4) * 8;
-#pragma unroll
-        for (int i = 0; i < SP / 16; ++i) *reinterpret_cast<f32x4 *>(b + 32 * (i >> 1) + 4 * (i & 1)) = st[i];
-        Split<T, kN<T>> sp[KS];
-#pragma unroll
-        for (int s = 0; s < KS; ++s) stack(st[2 * s], st[2 * s + 1], sp[s]);
-        f32x4 z[4], dy[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            f32x4 acc = {0, 0, 0, 0};
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                Split<T, 1> a;
-                a.f[0] = get_frag<T>(keys + (t * KS + s) * kFrag<T>, lane);
-                acc = mma_terms(a, sp[s], acc);
-            }
-            z[t] = acc * *reinterpret_cast<const f32x4 *>(cs->to_end + 16 * t + q4);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * t + q4 + r;
-                dy[t][r] = mine && row < rows ? (float)dyg[(t0 + row) * p.dy_ld] : 0.0f;
-            }
-        }
-        const char *nt = head + kTri * kN<T> * kFrag<T>, *mt = nt + kTri * kN<T> * kFrag<T>;
-        Split<T, 1> ds[2];
-        stack(dy[0], dy[1], ds[0]);
-        stack(dy[2], dy[3], ds[1]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int P = t / 2; P < 2; ++P) {
-                Split<T, kN<T>> a;
-#pragma unroll
-                for (int e = 0; e < kN<T>; ++e) a.f[e] = get_frag<T>(mt + (upper(t, P) * kN<T> + e) * kFrag<T>, lane);
-                z[t] = mma_terms(a, ds[P], z[t]);        // dU
-            }
-        Split<T, kN<T>> zs[2];
-        stack(z[0], z[1], zs[0]);
-        stack(z[2], z[3], zs[1]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int P = t / 2; P < 2; ++P) {
-                Split<T, kN<T>> a;
-#pragma unroll
-                for (int e = 0; e < kN<T>; ++e) a.f[e] = get_frag<T>(nt + (upper(t, P) * kN<T> + e) * kFrag<T>, lane);
-                z[t] = mma_terms(a, zs[P], z[t]);        // E
-            }
-        Split<T, kN<T>> us[2], xs[2];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const f32x4 grow = *reinterpret_cast<const f32x4 *>(cs->from_start + 16 * t + q4);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) p.rows[1][((nh * p.K + c) * kDQ + 16 * t + q4 + r) * p.PP + ch] = z[t][r];
-            z[t] = z[t] * (grow * *reinterpret_cast<const f32x4 *>(cs->beta + 16 * t + q4)) * -1.0f;
-            dy[t] = dy[t] * (grow * p.scale);
-        }
-        stack(z[0], z[1], us[0]);
-        stack(z[2], z[3], us[1]);
-        stack(dy[0], dy[1], xs[0]);
-        stack(dy[2], dy[3], xs[1]);
-        const float total = cs->from_start[kDQ - 1];
-        const char *kt = keys + 8 * KS * kFrag<T>, *qt = kt + 4 * KS * kFrag<T>;
-#pragma unroll
-        for (int i = 0; i < SP / 16; ++i) {
-            st[i] = st[i] * total;
-#pragma unroll
-            for (int P = 0; P < 2; ++P) {
-                Split<T, 1> a, q;
-                a.f[0] = get_frag<T>(kt + (i * 2 + P) * kFrag<T>, lane);
-                q.f[0] = get_frag<T>(qt + (i * 2 + P) * kFrag<T>, lane);
-                st[i] = mma_terms(a, us[P], st[i]);
-                st[i] = mma_terms(q, xs[P], st[i]);
-            }
-        }
-    }
-    store_state<SP>(p.dstate + (nh * p.P + ch) * p.S, p.dstate && mine, p.S, lane, st);
-}
-
-// The two passes over the states of a gradient, which do not depend on each other.
-template <typename T, int SP> __global__ void __launch_bounds__(64) delta_states_kernel(DeltaParams p)
-{
-    const int64_t units = (int64_t)p.N * p.H * p.blocks, half = gridDim.x / 2;
-    const bool back = blockIdx.x < half;
-    const int64_t unit = unit_of(back ? blockIdx.x : blockIdx.x - half, units);
-    if (unit >= units) return;
-    if (back) delta_backward<T, SP>(p, unit, threadIdx.x);
-    else delta_forward<T, SP, false>(p, unit, threadIdx.x);
 }
 
 // ---- the gradient of a chunk ---------------------------------------------------------
@@ -716,7 +462,7 @@ __global__ void __launch_bounds__(64 * (SP == 32 ? 2 : SP == 256 ? 8 : 4)) delta
     for (int h = h0; h < (live > 0 ? h1 : h0); ++h) {
         const int64_t nh = n * p.H + h;
         const char *head = p.heads + (chunk * p.H + h) * head_bytes<T>(true);
-        const ChunkScalars *cs = reinterpret_cast<const ChunkScalars *>(head + head_bytes<T>(true) - sizeof(ChunkScalars));
+        const ChunkScalars *cs = reinterpret_cast<const ChunkScalars *>(head);
         __syncthreads();
         if (w == 0) {
             sh.from_start[lane] = cs->from_start[lane];

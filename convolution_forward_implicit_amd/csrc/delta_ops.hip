@@ -6,7 +6,7 @@
 #include <new>
 
 #include "../../include/convfwd.h"
-#include "delta_fwd.h"
+#include "delta_chain.h"
 #include "seq_host.h"
 #include "status.h"
 
@@ -28,8 +28,6 @@ int64_t up(int64_t v) { return (v + 255) / 256 * 256; }
 
 template <typename T> int64_t keys_of(int SP, bool grad)
 {
-    if (!grad)
-        return 2 * (SP == 32 ? kKeysBytes<T, 32> : SP == 64 ? kKeysBytes<T, 64> : SP == 128 ? kKeysBytes<T, 128> : kKeysBytes<T, 256>);
     return SP == 32 ? keys_bytes<T, 32>(grad) : SP == 64 ? keys_bytes<T, 64>(grad)
          : SP == 128 ? keys_bytes<T, 128>(grad) : keys_bytes<T, 256>(grad);
 }
@@ -39,31 +37,17 @@ int64_t keys_of(const conv_delta_desc_t &d, int SP, bool grad)
 }
 int64_t head_of(const conv_delta_desc_t &d, bool grad)
 {
-    if (!grad) return d.dtype == CONV_DT_BF16 ? kHeadBytes<bf16_t> : kHeadBytes<float>;
     return d.dtype == CONV_DT_BF16 ? head_bytes<bf16_t>(grad) : head_bytes<float>(grad);
 }
 
 int64_t state_grid(int64_t units) { return (units + 7) / 8 * 8; }
 
-// The forward pass: what chunks do without their states, then the states, with as many
-// channels of a head in a workgroup as leave one for every compute unit.
-template <typename T, int SP, int NS> bool launch_states(const DeltaParams &p, hipStream_t s)
-{
-    if constexpr (sizeof(StateShared<T, SP, NS>) <= 160 * 1024) {
-        const int64_t units = (int64_t)p.N * p.H * ((p.blocks + NS - 1) / NS);
-        hipLaunchKernelGGL((delta_state_kernel<T, SP, NS>), dim3((unsigned)state_grid(units)), dim3(128 * NS), 0, s, p);
-        return true;
-    }
-    return false;
-}
-
 template <typename T, int SP> void launch_fwd(const DeltaParams &p, int64_t units, hipStream_t s)
 {
     if (p.K > 0)
-        hipLaunchKernelGGL((delta_chunks_kernel<T, SP>), dim3((unsigned)((int64_t)p.N * p.K * p.G * p.slices)), dim3(256), 0, s, p);
-    if (units >= 4 * 256 && p.blocks % 4 == 0 && launch_states<T, SP, 4>(p, s)) return;
-    if (units >= 2 * 256 && p.blocks % 2 == 0 && launch_states<T, SP, 2>(p, s)) return;
-    launch_states<T, SP, 1>(p, s);
+        hipLaunchKernelGGL((delta_prepare_kernel<T, SP, false>), dim3((unsigned)((int64_t)p.N * p.K * p.G * p.slices)), dim3(256),
+                           0, s, p);
+    hipLaunchKernelGGL((delta_y_kernel<T, SP>), dim3((unsigned)state_grid(units)), dim3(kChainThreads), 0, s, p);
 }
 
 // The gradient: what chunks do without their states, both passes over the states,
@@ -73,7 +57,7 @@ template <typename T, int SP> void launch_bwd(DeltaParams p, const conv_delta_pl
     const int64_t chunks = (int64_t)p.N * p.K * p.G, units = (int64_t)p.N * p.H * p.blocks;
     if (p.K > 0)
         hipLaunchKernelGGL((delta_prepare_kernel<T, SP, true>), dim3((unsigned)(chunks * p.slices)), dim3(256), 0, s, p);
-    hipLaunchKernelGGL((delta_states_kernel<T, SP>), dim3((unsigned)(2 * state_grid(units))), dim3(64), 0, s, p);
+    hipLaunchKernelGGL((delta_states_kernel<T, SP>), dim3((unsigned)(2 * state_grid(units))), dim3(kChainThreads), 0, s, p);
     if (p.K == 0) return;
     p.slices = pl.grad_slices;
     p.heads_per_slice = pl.grad_heads;
@@ -163,7 +147,7 @@ conv_status_t conv_delta_create(const conv_delta_desc_t *desc, conv_delta_plan_t
     const double units = (double)d.N * d.H * pl->blocks, chunks = (double)d.N * pl->K;
     const double ws = chunks * ((double)d.G * keys_of(d, pl->SP, true) + (double)d.H * head_of(d, true)) +
                       2.0 * (double)d.N * d.H * pl->K * (d.P + 31.0) * (pl->SP + kDQ) * 4.0;
-    if ((!one_launch(units, 128) && !one_launch((double)d.N * d.H * step_shape(d).blocks, 256)) || ws >= kMaxBytes) {
+    if ((!one_launch(units, kChainThreads) && !one_launch((double)d.N * d.H * step_shape(d).blocks, 256)) || ws >= kMaxBytes) {
         delete pl;
         return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
     }
@@ -276,7 +260,7 @@ static conv_status_t delta_forward_call(const conv_delta_plan_t *plan, const con
     p.heads = (char *)ws + plan->o_heads;
     const Rows vec[] = {in[0], in[1]};
     p.vec = delta_vector(*plan, vec, 2);
-    if (!one_launch((double)state_grid(d.N * d.H * plan->blocks), 128) ||
+    if (!one_launch((double)state_grid(d.N * d.H * plan->blocks), kChainThreads) ||
         !one_launch((double)d.N * plan->K * d.G * plan->slices, 256))
         return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
     if (d.dtype == CONV_DT_BF16) launch_delta<bf16_t>(p, *plan, false, s);
@@ -350,7 +334,7 @@ conv_status_t conv_delta_bwd_run(const conv_delta_plan_t *plan, const conv_delta
     const Rows vec[] = {in[1], in[2]};
     p.vec = delta_vector(*plan, vec, 2);
     const double groups = (double)d.N * plan->K * d.G;
-    if (!one_launch(2.0 * (double)state_grid(d.N * d.H * p.blocks), 64) || !one_launch(groups * plan->slices, 256) ||
+    if (!one_launch(2.0 * (double)state_grid(d.N * d.H * p.blocks), kChainThreads) || !one_launch(groups * plan->slices, 256) ||
         !one_launch(groups * plan->grad_slices, 512) || !one_launch((double)rows * (double)gs / 256 + 1, 256))
         return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
     hipStream_t s = (hipStream_t)stream;
