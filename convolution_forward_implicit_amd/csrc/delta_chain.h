@@ -7,9 +7,10 @@
 // only and its four waves share every product: wave t has the tokens 16 t .. of the
 // first two and, of the third, the keys 32 t .. (and 128 on), whose state it holds.  What
 // each leaves goes to the others through LDS, split into its terms once, with a
-// barrier behind each product.  y needs nothing that a wave has not read anyway: Q S0^T
-// fills the wait behind Z, M U that behind the state.  Two more waves bring K and N
-// into LDS a chunk ahead; Q and M have one reader each and go to its registers.
+// barrier behind each product.  Four more waves do what the chain does not wait for:
+// they bring K and N into LDS a chunk ahead and compute y or, going back, what M^T dO
+// and Q^T dO add; their own operands (Q and M) have one reader each and go to its
+// registers.
 #pragma once
 
 #include "delta_kernels.h"
@@ -19,7 +20,7 @@ namespace convfwd {
 
 enum ChainMode { CHAIN_Y, CHAIN_STATES, CHAIN_BACK };
 
-constexpr int kLoaders = 2;
+constexpr int kHelpers = 4;
 
 template <typename T, int SP, ChainMode MODE> struct ChainShared {
     static constexpr int KS = SP / 32, NT = kN<T>, NM = kM<T>;
@@ -28,15 +29,16 @@ template <typename T, int SP, ChainMode MODE> struct ChainShared {
         char s[NT * KS * kFrag<T>];     // the state (its gradient)
         char a[NT * 2 * kFrag<T>];      // Z (dU)
         char b[NT * 2 * kFrag<T>];      // e^{c_Q - c} U (e^c dV)
-        char y[(MODE == CHAIN_Y ? NM : 1) * 2 * kFrag<T>];      // Y (dO)
-        char x[(MODE == CHAIN_BACK ? NT : 0) * 2 * kFrag<T> + 16];      // (scale e^c dO)
+        char y[(MODE == CHAIN_Y ? NM : 0) * 2 * kFrag<T> + 16];         // Y
+        f32x4 du[MODE == CHAIN_BACK ? 2 : 0][4][64];                    // M^T dO of this chunk and the next
+        f32x4 ds[MODE == CHAIN_BACK ? SP / 16 : 0][64];                 // scale (e^c dO)^T Q
     };
     static constexpr int NB = 2 * OPS + (int)sizeof(Exchange) <= 160 * 1024 ? 2 : 1;     // chunks of K and N
     __align__(16) char ops[NB][OPS];
     __align__(16) Exchange x;
 };
 
-// KB kilobytes of memory to LDS, by the loaders.  The loads are written out: the
+// KB kilobytes of memory to LDS, by the helpers.  The loads are written out: the
 // compiler, which cannot see what they write, would wait for them before any read of
 // LDS.
 template <int KB> SEQ_DEV void fetch(const char *from, char *to, int wave, int lane)
@@ -44,10 +46,10 @@ template <int KB> SEQ_DEV void fetch(const char *from, char *to, int wave, int l
     const i32x4_t buf = uniform_rsrc(buffer_rsrc(from, KB * 1024));
     const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)to);
 #pragma unroll
-    for (int e = 0; e < KB; e += kLoaders) {
+    for (int e = 0; e < KB; e += kHelpers) {
         const uint32_t b = (uint32_t)(e + wave) * 1024;
         uint32_t saved;
-        if (KB % kLoaders == 0 || e + wave < KB)
+        if (KB % kHelpers == 0 || e + wave < KB)
             asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds\n\ts_mov_b32 m0, %0"
                          : "=&s"(saved) : "s"(at + b), "v"(lane * 16), "s"(buf), "s"(b) : "memory");
     }
@@ -142,29 +144,172 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
     const int64_t keys_step = p.G * keys_bytes<T, SP>(GRAD), head_step = p.H * head_bytes<T>(GRAD);
     constexpr int64_t tri = (GRAD ? (int64_t)sizeof(ChunkScalars) : kRows) + (BACK ? Shared::TRI : 0);      // N, or its transpose
     auto chunk = [&](int i) { return BACK ? live - 1 - i : i; };
+    const int t = w & 3;
+    // rows 16 t .. of this chunk
+    auto rows_of = [&](const void *x, int64_t ld, int i, int tile) {
+        const int64_t t0 = (int64_t)chunk(i) * kDQ + 16 * tile;
+        return LaneRows<T>((const T *)x + (int64_t)h * p.P, ld, n * p.L + t0, (int)(len - t0 < 16 ? len - t0 : 16), p.P, ch, lane);
+    };
     if (w >= 4) {
         auto load = [&](int i) {
             const char *k = keys + chunk(i) * keys_step, *a = heads + chunk(i) * head_step;
-            fetch<KEYS / 1024>(k, sh.ops[i % NB], w - 4, lane);
-            fetch<kRows / 1024>(a, sh.ops[i % NB] + KEYS, w - 4, lane);
-            fetch<Shared::TRI / 1024>(a + tri, sh.ops[i % NB] + KEYS + kRows, w - 4, lane);
+            fetch<KEYS / 1024>(k, sh.ops[i % NB], t, lane);
+            fetch<kRows / 1024>(a, sh.ops[i % NB] + KEYS, t, lane);
+            fetch<Shared::TRI / 1024>(a + tri, sh.ops[i % NB] + KEYS + kRows, t, lane);
+        };
+        constexpr int NQ = BACK ? 4 * OWN : MODE == CHAIN_Y ? KS : 0, TM = BACK ? NT : MODE == CHAIN_Y ? NM : 0;
+        typename Frag<T>::type qf[NQ + 1];
+        Split<T, TM + 1> mf[2];
+        uint32_t vb[16];
+        auto load_q = [&](int i) {
+            const char *k = keys + chunk(i) * keys_step;
+#pragma unroll
+            for (int s = 0; s < NQ; ++s) {
+                if (!BACK) qf[s] = get_frag<T>(k + ((4 + t) * KS + s) * F, lane);
+                else if (t + 4 * (s >> 2) < KS) qf[s] = get_frag<T>(k + (12 * KS + (t + 4 * (s >> 2)) * 4 + (s & 3)) * F, lane);
+            }
+        };
+        auto load_m = [&](int i) {
+            const char *m = heads + chunk(i) * head_step + tri + Shared::TRI;
+#pragma unroll
+            for (int P = 0; P < 2; ++P)
+                if (BACK ? P >= t / 2 : P <= t / 2) {
+#pragma unroll
+                    for (int e = 0; e < TM; ++e)
+                        mf[P].f[e] = get_frag<T>(m + (BACK ? upper(t, P) * NT + e : lower(t, P) * NM + e) * F, lane);
+                }
+        };
+        f32x4 dy[4];
+        auto load_dy = [&](int i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const LaneRows<T> rows = rows_of(p.dy, p.dy_ld, i, e);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) vb[4 * e + r] = rows.bits(r);
+            }
+        };
+        auto take_dy = [&]() {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const uint32_t b = vb[e];
+                dy[e / 4][e % 4] = __builtin_bit_cast(float, b);
+            }
+        };
+        auto put_du = [&](int i) {      // M^T dO of chunk i, whose dO is in dy
+            Split<T, 1> d[2];
+            stack(dy[0], dy[1], d[0]);
+            stack(dy[2], dy[3], d[1]);
+            f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+#pragma unroll
+            for (int P = 0; P < 2; ++P)
+                if (P >= t / 2) {
+#pragma unroll
+                    for (int e = TM - 1; e >= 0; --e) acc[P] = mma(mf[P].f[e], d[P].f[0], acc[P]);
+                }
+            if constexpr (BACK) sh.x.du[i & 1][t][lane] = acc[0] + acc[1];
+        };
+        // y's part by the chunk's own tokens, and its rows
+        auto put_y = [&](int i, f32x4 y) {
+            f32x4 acc[2] = {y, f32x4{0, 0, 0, 0}};
+#pragma unroll
+            for (int P = 0; P < 2; ++P)
+                if (P <= t / 2) {
+                    Split<T, NM> b;
+                    get_split(sh.x.y + P * F, 2 * F, lane, b);
+#pragma unroll
+                    for (int e = 0; e < NM; ++e)
+#pragma unroll
+                        for (int k = 0; k < NM - e; ++k) acc[P] = mma(mf[P].f[e], b.f[k], acc[P]);
+                }
+            const LaneRows<T> rows = rows_of(p.y, p.y_ld, i, t);
+            y = acc[0] + acc[1];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) rows.put(e, y[e]);
         };
         if (NB == 2 && live > 0) load(0);
+        if (live > 0) {
+            load_q(0);
+            if constexpr (BACK) {
+                load_m(0);
+                load_dy(0);
+                take_dy();
+                put_du(0);
+                if (live > 1) load_dy(1), load_m(1);
+            }
+        }
+        f32x4 y = {0, 0, 0, 0};
         for (int i = 0; i < live; ++i) {
+            const ChunkScalars *cs = reinterpret_cast<const ChunkScalars *>(sh.ops[i % NB] + KEYS);
             if (NB == 1) {
                 meet();
                 load(i);
             }
             wait_vmcnt<0>();
             meet();
-            if (NB == 2 && i + 1 < live) load(i + 1);
-            meet();
-            meet();
+            // the buffer of the chunk before is free; a chunk's y is finished while the next one's Z comes about
+            if constexpr (MODE == CHAIN_Y) {
+                const f32x4 last = y;
+                const f32x4 grow = *reinterpret_cast<const f32x4 *>(cs->from_start + 16 * t + q4);
+                f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    Split<T, NM> b;
+                    get_split(sh.x.s + s * F, KS * F, lane, b);
+#pragma unroll
+                    for (int e = 0; e < NM; ++e) acc[s & 1] = mma(qf[s], b.f[e], acc[s & 1]);
+                }
+                y = (acc[0] + acc[1]) * (grow * p.scale);
+                if (i > 0) put_y(i - 1, last);
+                meet();
+                if (i + 1 < live) load_q(i + 1);
+                load_m(i);
+                if (NB == 2 && i + 1 < live) load(i + 1);
+                meet();
+            } else {
+                if (NB == 2 && i + 1 < live) load(i + 1);
+            }
+            if constexpr (BACK) {
+                // (scale e^c dO)^T Q for the states of wave t
+                Split<T, NT> x[2];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    dy[e] = dy[e] * (*reinterpret_cast<const f32x4 *>(cs->from_start + 16 * e + q4) * p.scale);
+                stack(dy[0], dy[1], x[0]);
+                stack(dy[2], dy[3], x[1]);
+#pragma unroll
+                for (int o = 0; o < OWN; ++o) {
+                    if (t + 4 * o >= KS) continue;
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+#pragma unroll
+                        for (int e = NT - 1; e >= 0; --e)
+#pragma unroll
+                            for (int P = 0; P < 2; ++P) acc[P] = mma(qf[4 * o + 2 * a + P], x[P].f[e], acc[P]);
+                        sh.x.ds[2 * (t + 4 * o) + a][lane] = acc[0] + acc[1];
+                    }
+                }
+                if (i + 1 < live) load_q(i + 1);
+                meet();
+                if (i + 1 < live) {
+                    take_dy();
+                    put_du(i + 1);
+                }
+                if (i + 2 < live) load_m(i + 2), load_dy(i + 2);
+                meet();
+            }
+            if constexpr (MODE == CHAIN_STATES) {
+                meet();
+                meet();
+            }
         }
+        if (MODE == CHAIN_Y && live > 0) put_y(live - 1, y);
+        if (MODE == CHAIN_Y && ch < p.P)
+            for (int64_t r = len + 4 * t + (lane >> 4); r < p.L; r += 16) ((T *)p.y)[(n * p.L + r) * p.y_ld + (int64_t)h * p.P + ch] = (T)0.0f;
         return;
     }
     f32x4 st[OWN][2];
-    auto state_at = [&](int o, int a, int r) { return 32 * (w + 4 * o) + 2 * q4 + 4 * a + r; };      // the key
+    auto state_at = [&](int o, int a, int r) { return 32 * (t + 4 * o) + 2 * q4 + 4 * a + r; };      // the key
     {
         const float *from = BACK ? p.dstate_out : p.state;
         const float *g = from + (nh * p.P + ch) * p.S;
@@ -178,71 +323,27 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
     auto put_state = [&]() {
 #pragma unroll
         for (int o = 0; o < OWN; ++o) {
-            if (w + 4 * o >= KS) continue;
+            if (t + 4 * o >= KS) continue;
             Split<T, NT> s;
             stack(st[o][0], st[o][1], s);
 #pragma unroll
-            for (int e = 0; e < NT; ++e) put_frag(sh.x.s + (e * KS + w + 4 * o) * F, lane, s.f[e]);
+            for (int e = 0; e < NT; ++e) put_frag(sh.x.s + (e * KS + t + 4 * o) * F, lane, s.f[e]);
         }
     };
-    // what this wave alone reads: Q and M; going back M^T and Q^T
-    constexpr int NQ = BACK ? 4 * OWN : MODE == CHAIN_Y ? KS : 0, TM = BACK ? NT : MODE == CHAIN_Y ? NM : 0;
-    typename Frag<T>::type qf[NQ + 1];
-    Split<T, TM + 1> mf[2];
-    uint32_t vb[4];                     // v, or dO, of the next chunk
-    auto load_q = [&](int i) {
-        const char *k = keys + chunk(i) * keys_step;
-#pragma unroll
-        for (int s = 0; s < NQ; ++s) {
-            if (!BACK) qf[s] = get_frag<T>(k + ((4 + w) * KS + s) * F, lane);
-            else if (w + 4 * (s >> 2) < KS) qf[s] = get_frag<T>(k + (12 * KS + (w + 4 * (s >> 2)) * 4 + (s & 3)) * F, lane);
-        }
-    };
-    auto load_m = [&](int i) {
-        const char *m = heads + chunk(i) * head_step + tri + Shared::TRI;
-#pragma unroll
-        for (int P = 0; P < 2; ++P)
-            if (BACK ? P >= w / 2 : P <= w / 2) {
-#pragma unroll
-                for (int e = 0; e < TM; ++e)
-                    mf[P].f[e] = get_frag<T>(m + (BACK ? upper(w, P) * NT + e : lower(w, P) * NM + e) * F, lane);
-            }
-    };
-    auto rows_of = [&](const void *t, int64_t ld, int i) {
-        const int64_t t0 = (int64_t)chunk(i) * kDQ + 16 * w;
-        return LaneRows<T>((const T *)t + (int64_t)h * p.P, ld, n * p.L + t0, (int)(len - t0 < 16 ? len - t0 : 16), p.P, ch, lane);
-    };
+    uint32_t vb[4];                     // v of the next chunk
     auto load_v = [&](int i) {
-        const LaneRows<T> rows = BACK ? rows_of(p.dy, p.dy_ld, i) : rows_of(p.v, p.v_ld, i);
+        const LaneRows<T> rows = rows_of(p.v, p.v_ld, i, t);
 #pragma unroll
         for (int r = 0; r < 4; ++r) vb[r] = rows.bits(r);
     };
     if (live > 0) {
-        load_q(0);
-        load_m(0);
-        load_v(0);
+        if (!BACK) load_v(0);
         put_state();
     }
     for (int i = 0; i < live; ++i) {
         const char *ops = sh.ops[i % NB], *tr = ops + KEYS + kRows;
         const ChunkScalars *cs = reinterpret_cast<const ChunkScalars *>(ops + KEYS);
         const int64_t at = nh * p.K + chunk(i);
-        f32x4 v;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const uint32_t b = vb[r];
-            v[r] = __builtin_bit_cast(float, b);
-        }
-        if constexpr (BACK) put_half<T, 1>(sh.x.y, w, lane, v);
-        if (i + 1 < live) load_v(i + 1);
-        if constexpr (GRAD) {
-            float *b = p.bound[BACK] + (at * p.PP + ch) * SP + 2 * q4;
-#pragma unroll
-            for (int o = 0; o < OWN; ++o)
-                if (w + 4 * o < KS)
-#pragma unroll
-                    for (int a = 0; a < 2; ++a) *reinterpret_cast<f32x4 *>(b + 32 * (w + 4 * o) + 4 * a) = st[o][a];
-        }
         if (NB == 1) meet();
         meet();
         // K S0^T, a sum of each term by itself
@@ -250,14 +351,14 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
         typename Frag<T>::type kf[KS];
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            kf[s] = get_frag<T>(ops + (w * KS + s) * F, lane);
+            kf[s] = get_frag<T>(ops + (t * KS + s) * F, lane);
             get_split(sh.x.s + s * F, KS * F, lane, sp[s]);
         }
-        const f32x4 grow = *reinterpret_cast<const f32x4 *>(cs->from_start + 16 * w + q4);
-        const f32x4 fade = *reinterpret_cast<const f32x4 *>(cs->to_end + 16 * w + q4);
-        const f32x4 beta = *reinterpret_cast<const f32x4 *>(cs->beta + 16 * w + q4);
+        const f32x4 grow = *reinterpret_cast<const f32x4 *>(cs->from_start + 16 * t + q4);
+        const f32x4 fade = *reinterpret_cast<const f32x4 *>(cs->to_end + 16 * t + q4);
+        const f32x4 beta = *reinterpret_cast<const f32x4 *>(cs->beta + 16 * t + q4);
         const float total = cs->from_start[kDQ - 1];
-        f32x4 r[NT];
+        f32x4 r[NT], z;
 #pragma unroll
         for (int e = 0; e < NT; ++e) r[e] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -266,104 +367,90 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
             for (int e = 0; e < NT; ++e) r[e] = mma(kf[s], sp[s].f[e], r[e]);
 #pragma unroll
         for (int e = NT - 1; e > 0; --e) r[e - 1] = r[e - 1] + r[e];
-        f32x4 z;
         if constexpr (BACK) {
-            z = r[0] * fade;
-#pragma unroll
-            for (int P = 0; P < 2; ++P)
-                if (P >= w / 2) {
-                    const typename Frag<T>::type d = get_frag<T>(sh.x.y + P * F, lane);
-#pragma unroll
-                    for (int e = NT - 1; e >= 0; --e) z = mma(mf[P].f[e], d, z);         // dU
-                }
-            if (i + 1 < live) load_m(i + 1);
+            z = sh.x.du[i & 1][t][lane] + r[0] * fade;           // dU
         } else {
-            z = v - grow * r[0];
-        }
-        put_half<T, NT>(sh.x.a, w, lane, z);
-        f32x4 y = {0, 0, 0, 0};
-        if constexpr (MODE == CHAIN_Y) {
 #pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int e = 0; e < NM; ++e) y = mma(qf[s], sp[s].f[e], y);
-            y = y * (grow * p.scale);
-            if (i + 1 < live) load_q(i + 1);
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t b = vb[e];
+                z[e] = fmaf(-grow[e], r[0][e], __builtin_bit_cast(float, b));
+            }
         }
-        if constexpr (BACK) put_half<T, NT>(sh.x.x, w, lane, v * (grow * p.scale));
+        put_half<T, NT>(sh.x.a, t, lane, z);
         Split<T, NT> nf[2];
 #pragma unroll
         for (int P = 0; P < 2; ++P)
-            if (BACK ? P >= w / 2 : P <= w / 2) get_split(tr + (BACK ? upper(w, P) : lower(w, P)) * NT * F, F, lane, nf[P]);
+            if (BACK ? P >= t / 2 : P <= t / 2) get_split(tr + (BACK ? upper(t, P) : lower(t, P)) * NT * F, F, lane, nf[P]);
+        if constexpr (GRAD) {
+            float *b = p.bound[BACK] + (at * p.PP + ch) * SP + 2 * q4;
+#pragma unroll
+            for (int o = 0; o < OWN; ++o)
+                if (t + 4 * o < KS)
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) *reinterpret_cast<f32x4 *>(b + 32 * (t + 4 * o) + 4 * a) = st[o][a];
+        }
         meet();
-        // N (beta Z)
+        // N (beta Z); sums that do not wait for each other
+        f32x4 acc[3] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}, z};
 #pragma unroll
         for (int P = 0; P < 2; ++P)
-            if (BACK ? P >= w / 2 : P <= w / 2) {
+            if (BACK ? P >= t / 2 : P <= t / 2) {
                 Split<T, NT> b;
                 get_split(sh.x.a + P * F, 2 * F, lane, b);
-                z = mma_terms(nf[P], b, z);
-            }
-        put_half<T, NT>(sh.x.b, w, lane, z * (BACK ? beta * grow * -1.0f : beta * fade));
-        if constexpr (MODE == CHAIN_Y) put_half<T, NM>(sh.x.y, w, lane, z);
-        if constexpr (GRAD) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) p.rows[BACK][(at * kDQ + 16 * w + q4 + e) * p.PP + ch] = z[e];
-        }
+                for (int e = NT - 1; e >= 0; --e)
+#pragma unroll
+                    for (int k = 0; k < NT - e; ++k) acc[NT - 1 - e - k > 0 ? e % 2 : 2] = mma(nf[P].f[e], b.f[k], acc[NT - 1 - e - k > 0 ? e % 2 : 2]);
+            }
+        z = acc[2] + (acc[1] + acc[0]);
+        put_half<T, NT>(sh.x.b, t, lane, z * (BACK ? beta * grow * -1.0f : beta * fade));
+        if constexpr (MODE == CHAIN_Y) put_half<T, NM>(sh.x.y, t, lane, z);
         typename Frag<T>::type kt[OWN][2][2];
 #pragma unroll
         for (int o = 0; o < OWN; ++o)
-            if (w + 4 * o < KS)
+            if (t + 4 * o < KS)
 #pragma unroll
                 for (int a = 0; a < 2; ++a)
 #pragma unroll
-                    for (int P = 0; P < 2; ++P) kt[o][a][P] = get_transposed<KS>(ops, P, w + 4 * o, a, lane, T());
+                    for (int P = 0; P < 2; ++P) kt[o][a][P] = get_transposed<KS>(ops, P, t + 4 * o, a, lane, T());
         meet();
         // the state behind the chunk
-        if (w < KS) {
-            Split<T, NT> u[2], x[2];
+        if (t < KS) {
+            Split<T, NT> u[2];
 #pragma unroll
-            for (int P = 0; P < 2; ++P) {
-                get_split(sh.x.b + P * F, 2 * F, lane, u[P]);
-                if constexpr (BACK) get_split(sh.x.x + P * F, 2 * F, lane, x[P]);
-            }
+            for (int P = 0; P < 2; ++P) get_split(sh.x.b + P * F, 2 * F, lane, u[P]);
+            f32x4 sums[OWN][2][2];
 #pragma unroll
-            for (int o = 0; o < OWN; ++o) {
-                if (w + 4 * o >= KS) continue;
+            for (int o = 0; o < OWN; ++o)
 #pragma unroll
                 for (int a = 0; a < 2; ++a) {
-                    f32x4 s = st[o][a] * total;
-#pragma unroll
-                    for (int P = 0; P < 2; ++P)
-#pragma unroll
-                        for (int e = NT - 1; e >= 0; --e) {
-                            s = mma(kt[o][a][P], u[P].f[e], s);
-                            if constexpr (BACK) s = mma(qf[4 * o + 2 * a + P], x[P].f[e], s);
-                        }
-                    st[o][a] = s;
+                    sums[o][a][0] = st[o][a] * total;
+                    sums[o][a][1] = f32x4{0, 0, 0, 0};
+                    if constexpr (BACK) {
+                        if (t + 4 * o < KS) sums[o][a][1] = sh.x.ds[2 * (t + 4 * o) + a][lane];
+                    }
                 }
-            }
+#pragma unroll
+            for (int e = NT - 1; e >= 0; --e)
+#pragma unroll
+                for (int P = 0; P < 2; ++P)
+#pragma unroll
+                    for (int o = 0; o < OWN; ++o) {
+                        if (t + 4 * o >= KS) continue;
+#pragma unroll
+                        for (int a = 0; a < 2; ++a) sums[o][a][1 - P] = mma(kt[o][a][P], u[P].f[e], sums[o][a][1 - P]);
+                    }
+#pragma unroll
+            for (int o = 0; o < OWN; ++o)
+#pragma unroll
+                for (int a = 0; a < 2; ++a) st[o][a] = sums[o][a][0] + sums[o][a][1];
             put_state();
         }
-        if constexpr (BACK) {
-            if (i + 1 < live) load_q(i + 1);
+        if constexpr (GRAD) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p.rows[BACK][(at * kDQ + 16 * t + q4 + e) * p.PP + ch] = z[e];
         }
-        if constexpr (MODE == CHAIN_Y) {
-#pragma unroll
-            for (int P = 0; P < 2; ++P)
-                if (P <= w / 2) {
-                    Split<T, NM> b;
-                    get_split(sh.x.y + P * F, 2 * F, lane, b);
-#pragma unroll
-                    for (int e = 0; e < NM; ++e)
-#pragma unroll
-                        for (int k = 0; k < NM - e; ++k) y = mma(mf[P].f[e], b.f[k], y);
-                }
-            if (i + 1 < live) load_m(i + 1);
-            const LaneRows<T> rows = rows_of(p.y, p.y_ld, i);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) rows.put(e, y[e]);
-        }
+        if (!BACK && i + 1 < live) load_v(i + 1);
     }
     float *to = BACK ? p.dstate : p.state_out;
     if (to && ch < p.P)
@@ -372,13 +459,11 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
 #pragma unroll
             for (int a = 0; a < 2; ++a)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (w + 4 * o < KS && state_at(o, a, r) < p.S) to[(nh * p.P + ch) * p.S + state_at(o, a, r)] = st[o][a][r];
-    if (MODE == CHAIN_Y && ch < p.P)
-        for (int64_t t = len + 4 * w + (lane >> 4); t < p.L; t += 16) ((T *)p.y)[(n * p.L + t) * p.y_ld + (int64_t)h * p.P + ch] = (T)0.0f;
+                for (int e = 0; e < 4; ++e)
+                    if (t + 4 * o < KS && state_at(o, a, e) < p.S) to[(nh * p.P + ch) * p.S + state_at(o, a, e)] = st[o][a][e];
 }
 
-constexpr int kChainThreads = 64 * (4 + kLoaders);
+constexpr int kChainThreads = 64 * (4 + kHelpers);
 
 template <typename T, int SP> __global__ void __launch_bounds__(kChainThreads) delta_y_kernel(DeltaParams p)
 {
