@@ -8,7 +8,7 @@
 // first two and, of the third, the keys 32 t .. (and 128 on), whose state it holds.  What
 // each leaves goes to the others through LDS, split into its terms once, with a
 // barrier behind each product.  Four more waves do what the chain does not wait for:
-// they bring K and N into LDS a chunk ahead and compute y or, going back, what M^T dO
+// they bring K and N into LDS two chunks ahead and compute y or, going back, what M^T dO
 // and Q^T dO add; their own operands (Q and M) have one reader each and go to its
 // registers.
 #pragma once
@@ -29,11 +29,13 @@ template <typename T, int SP, ChainMode MODE> struct ChainShared {
         char s[NT * KS * kFrag<T>];     // the state (its gradient)
         char a[NT * 2 * kFrag<T>];      // Z (dU)
         char b[NT * 2 * kFrag<T>];      // e^{c_Q - c} U (e^c dV)
-        char y[(MODE == CHAIN_Y ? NM : 0) * 2 * kFrag<T> + 16];         // Y
-        f32x4 du[MODE == CHAIN_BACK ? 2 : 0][4][64];                    // M^T dO of this chunk and the next
+        char y[2][(MODE == CHAIN_Y ? NM : 0) * 2 * kFrag<T> + 16];      // Y of this chunk and the last
+        f32x4 in[2][4][64];             // V (M^T dO) of this chunk and the next
         f32x4 ds[MODE == CHAIN_BACK ? SP / 16 : 0][64];                 // scale (e^c dO)^T Q
     };
-    static constexpr int NB = 2 * OPS + (int)sizeof(Exchange) <= 160 * 1024 ? 2 : 1;     // chunks of K and N
+    // chunks of K and N: the one in use and those under way
+    static constexpr int NB = (160 * 1024 - (int)sizeof(Exchange)) / OPS >= 3 ? 3 : (160 * 1024 - (int)sizeof(Exchange)) / OPS;
+    static constexpr int LEAST = KEYS / 1024 / kHelpers + TRI / 1024 / kHelpers;     // loads of a chunk that every helper starts
     __align__(16) char ops[NB][OPS];
     __align__(16) Exchange x;
 };
@@ -160,7 +162,7 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
         constexpr int NQ = BACK ? 4 * OWN : MODE == CHAIN_Y ? KS : 0, TM = BACK ? NT : MODE == CHAIN_Y ? NM : 0;
         typename Frag<T>::type qf[NQ + 1];
         Split<T, TM + 1> mf[2];
-        uint32_t vb[16];
+        uint32_t vb[16];                // the next dO, or v
         auto load_q = [&](int i) {
             const char *k = keys + chunk(i) * keys_step;
 #pragma unroll
@@ -178,6 +180,20 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
                     for (int e = 0; e < TM; ++e)
                         mf[P].f[e] = get_frag<T>(m + (BACK ? upper(t, P) * NT + e : lower(t, P) * NM + e) * F, lane);
                 }
+        };
+        auto load_v = [&](int i) {
+            const LaneRows<T> rows = rows_of(p.v, p.v_ld, i, t);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) vb[r] = rows.bits(r);
+        };
+        auto put_v = [&](int i) {
+            f32x4 v;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const uint32_t b = vb[r];
+                v[r] = __builtin_bit_cast(float, b);
+            }
+            sh.x.in[i & 1][t][lane] = v;
         };
         f32x4 dy[4];
         auto load_dy = [&](int i) {
@@ -206,7 +222,7 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
 #pragma unroll
                     for (int e = TM - 1; e >= 0; --e) acc[P] = mma(mf[P].f[e], d[P].f[0], acc[P]);
                 }
-            if constexpr (BACK) sh.x.du[i & 1][t][lane] = acc[0] + acc[1];
+            sh.x.in[i & 1][t][lane] = acc[0] + acc[1];
         };
         // y's part by the chunk's own tokens, and its rows
         auto put_y = [&](int i, f32x4 y) {
@@ -215,7 +231,7 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
             for (int P = 0; P < 2; ++P)
                 if (P <= t / 2) {
                     Split<T, NM> b;
-                    get_split(sh.x.y + P * F, 2 * F, lane, b);
+                    get_split(sh.x.y[i & 1] + P * F, 2 * F, lane, b);
 #pragma unroll
                     for (int e = 0; e < NM; ++e)
 #pragma unroll
@@ -226,7 +242,8 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
 #pragma unroll
             for (int e = 0; e < 4; ++e) rows.put(e, y[e]);
         };
-        if (NB == 2 && live > 0) load(0);
+        if (NB > 1 && live > 0) load(0);
+        if (NB > 2 && live > 1) load(1);
         if (live > 0) {
             load_q(0);
             if constexpr (BACK) {
@@ -235,6 +252,10 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
                 take_dy();
                 put_du(0);
                 if (live > 1) load_dy(1), load_m(1);
+            } else {
+                load_v(0);
+                put_v(0);
+                if (live > 1) load_v(1);
             }
         }
         f32x4 y = {0, 0, 0, 0};
@@ -244,9 +265,13 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
                 meet();
                 load(i);
             }
-            wait_vmcnt<0>();
+            // This chunk's K and N are there.  Behind their loads came those of the next one's and, at least, Q, v and
+            // a block of M (going back a block of M^T and dO), which may be under way.
+            if (NB < 3 || i == 0 || i + 1 >= live) wait_vmcnt<0>();
+            else wait_vmcnt<(MODE == CHAIN_Y ? NQ + TM + 4 : BACK ? TM + 16 : 4) + Shared::LEAST>();
             meet();
-            // the buffer of the chunk before is free; a chunk's y is finished while the next one's Z comes about
+            if (NB == 2 && i + 1 < live) load(i + 1);
+            // a chunk's y is finished while the next one is under way
             if constexpr (MODE == CHAIN_Y) {
                 const f32x4 last = y;
                 const f32x4 grow = *reinterpret_cast<const f32x4 *>(cs->from_start + 16 * t + q4);
@@ -259,14 +284,14 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
                     for (int e = 0; e < NM; ++e) acc[s & 1] = mma(qf[s], b.f[e], acc[s & 1]);
                 }
                 y = (acc[0] + acc[1]) * (grow * p.scale);
-                if (i > 0) put_y(i - 1, last);
-                meet();
                 if (i + 1 < live) load_q(i + 1);
-                load_m(i);
-                if (NB == 2 && i + 1 < live) load(i + 1);
                 meet();
-            } else {
-                if (NB == 2 && i + 1 < live) load(i + 1);
+                if (i + 1 < live) put_v(i + 1);
+                load_v(i + 2 < live ? i + 2 : i);
+                if (i > 0) put_y(i - 1, last);
+                load_m(i);
+                meet();
+                if (NB == 3 && i + 2 < live) load(i + 2);
             }
             if constexpr (BACK) {
                 // (scale e^c dO)^T Q for the states of wave t
@@ -297,10 +322,14 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
                 }
                 if (i + 2 < live) load_m(i + 2), load_dy(i + 2);
                 meet();
+                if (NB == 3 && i + 2 < live) load(i + 2);
             }
             if constexpr (MODE == CHAIN_STATES) {
                 meet();
+                if (i + 1 < live) put_v(i + 1);
+                load_v(i + 2 < live ? i + 2 : i);
                 meet();
+                if (NB == 3 && i + 2 < live) load(i + 2);
             }
         }
         if (MODE == CHAIN_Y && live > 0) put_y(live - 1, y);
@@ -330,16 +359,7 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
             for (int e = 0; e < NT; ++e) put_frag(sh.x.s + (e * KS + t + 4 * o) * F, lane, s.f[e]);
         }
     };
-    uint32_t vb[4];                     // v of the next chunk
-    auto load_v = [&](int i) {
-        const LaneRows<T> rows = rows_of(p.v, p.v_ld, i, t);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) vb[r] = rows.bits(r);
-    };
-    if (live > 0) {
-        if (!BACK) load_v(0);
-        put_state();
-    }
+    if (live > 0) put_state();
     for (int i = 0; i < live; ++i) {
         const char *ops = sh.ops[i % NB], *tr = ops + KEYS + kRows;
         const ChunkScalars *cs = reinterpret_cast<const ChunkScalars *>(ops + KEYS);
@@ -358,6 +378,20 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
         const f32x4 fade = *reinterpret_cast<const f32x4 *>(cs->to_end + 16 * t + q4);
         const f32x4 beta = *reinterpret_cast<const f32x4 *>(cs->beta + 16 * t + q4);
         const float total = cs->from_start[kDQ - 1];
+        const f32x4 in = sh.x.in[i & 1][t][lane];
+        // what the next products read of K and N, so that no wait for it stands in front of a barrier
+        Split<T, NT> nf[2];
+#pragma unroll
+        for (int P = 0; P < 2; ++P)
+            if (BACK ? P >= t / 2 : P <= t / 2) get_split(tr + (BACK ? upper(t, P) : lower(t, P)) * NT * F, F, lane, nf[P]);
+        typename Frag<T>::type kt[OWN][2][2];
+#pragma unroll
+        for (int o = 0; o < OWN; ++o)
+            if (t + 4 * o < KS)
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+#pragma unroll
+                    for (int P = 0; P < 2; ++P) kt[o][a][P] = get_transposed<KS>(ops, P, t + 4 * o, a, lane, T());
         f32x4 r[NT], z;
 #pragma unroll
         for (int e = 0; e < NT; ++e) r[e] = f32x4{0, 0, 0, 0};
@@ -367,20 +401,8 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
             for (int e = 0; e < NT; ++e) r[e] = mma(kf[s], sp[s].f[e], r[e]);
 #pragma unroll
         for (int e = NT - 1; e > 0; --e) r[e - 1] = r[e - 1] + r[e];
-        if constexpr (BACK) {
-            z = sh.x.du[i & 1][t][lane] + r[0] * fade;           // dU
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t b = vb[e];
-                z[e] = fmaf(-grow[e], r[0][e], __builtin_bit_cast(float, b));
-            }
-        }
+        z = BACK ? in + r[0] * fade : in - grow * r[0];         // dU, Z
         put_half<T, NT>(sh.x.a, t, lane, z);
-        Split<T, NT> nf[2];
-#pragma unroll
-        for (int P = 0; P < 2; ++P)
-            if (BACK ? P >= t / 2 : P <= t / 2) get_split(tr + (BACK ? upper(t, P) : lower(t, P)) * NT * F, F, lane, nf[P]);
         if constexpr (GRAD) {
             float *b = p.bound[BACK] + (at * p.PP + ch) * SP + 2 * q4;
 #pragma unroll
@@ -391,7 +413,7 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
         }
         meet();
         // N (beta Z); sums that do not wait for each other
-        f32x4 acc[3] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}, z};
+        f32x4 acc[2][2] = {{z, f32x4{0, 0, 0, 0}}, {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}}};
 #pragma unroll
         for (int P = 0; P < 2; ++P)
             if (BACK ? P >= t / 2 : P <= t / 2) {
@@ -400,19 +422,11 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
 #pragma unroll
                 for (int e = NT - 1; e >= 0; --e)
 #pragma unroll
-                    for (int k = 0; k < NT - e; ++k) acc[NT - 1 - e - k > 0 ? e % 2 : 2] = mma(nf[P].f[e], b.f[k], acc[NT - 1 - e - k > 0 ? e % 2 : 2]);
+                    for (int k = 0; k < NT - e; ++k) acc[P][e + k < NT - 1] = mma(nf[P].f[e], b.f[k], acc[P][e + k < NT - 1]);
             }
-        z = acc[2] + (acc[1] + acc[0]);
+        z = (acc[0][0] + acc[1][0]) + (acc[0][1] + acc[1][1]);
         put_half<T, NT>(sh.x.b, t, lane, z * (BACK ? beta * grow * -1.0f : beta * fade));
-        if constexpr (MODE == CHAIN_Y) put_half<T, NM>(sh.x.y, t, lane, z);
-        typename Frag<T>::type kt[OWN][2][2];
-#pragma unroll
-        for (int o = 0; o < OWN; ++o)
-            if (t + 4 * o < KS)
-#pragma unroll
-                for (int a = 0; a < 2; ++a)
-#pragma unroll
-                    for (int P = 0; P < 2; ++P) kt[o][a][P] = get_transposed<KS>(ops, P, t + 4 * o, a, lane, T());
+        if constexpr (MODE == CHAIN_Y) put_half<T, NM>(sh.x.y[i & 1], t, lane, z);
         meet();
         // the state behind the chunk
         if (t < KS) {
@@ -450,7 +464,6 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
 #pragma unroll
             for (int e = 0; e < 4; ++e) p.rows[BACK][(at * kDQ + 16 * t + q4 + e) * p.PP + ch] = z[e];
         }
-        if (!BACK && i + 1 < live) load_v(i + 1);
     }
     float *to = BACK ? p.dstate : p.state_out;
     if (to && ch < p.P)
