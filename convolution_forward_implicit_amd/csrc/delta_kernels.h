@@ -20,7 +20,7 @@
 //
 // and the rest from S_0, R, Y and E of each chunk by itself (delta_grad_kernel).
 // All exponents are differences of sums, at most 0 for g <= 0.  The sums are
-// added in fp64; a g below -1e5 counts as that.
+// added in fp64, in powers of two; a g below -1e5 counts as that.
 //
 // Numbers.  As in the scan, q, k and dO enter the bf16 matrix instructions as
 // they are and what is computed on the way (states, Z, U, N) as the sum of three
@@ -53,7 +53,7 @@ struct DeltaParams {
     int64_t q_ld, k_ld, v_ld, g_ld, beta_ld, y_ld;
     int64_t L;
     int N, H, P, G, S, K;       // K: chunks of a sequence
-    int vec, slices, heads_per_slice, blocks;   // blocks: of 16 channels of a head
+    int vec, direct, slices, heads_per_slice, blocks;       // blocks: of 16 channels of a head
     float scale;
     char *keys, *heads;         // workspace: operands of a group's keys and of a head, by chunk
     // gradient
@@ -82,7 +82,7 @@ struct ChunkScalars {
     float beta[kDQ];
     float to_end[kDQ];          // e^{c_Q - c_i}
     float pad[kDQ];             // one load of 1 KB
-    double cum[kDQ];            // c_i; the gradient's
+    double cum[kDQ];            // c_i in powers of two; the gradient's
 };
 constexpr int kRows = 1024;     // bytes of ChunkScalars that the passes over the states read
 // forward: ChunkScalars' first kilobyte, N, M; gradient: ChunkScalars, N, N^T, M^T
@@ -160,14 +160,20 @@ SEQ_DEV Frag<float>::type read_keys(const float *t, int ld, int t0, int s, int a
 }
 
 // ---- what a chunk can do without its state ---------------------------------------
-template <typename T, int SP> struct PrepareShared {
+template <typename T, int SP, bool GRAD> struct PrepareShared {
     static constexpr int LD = Tile<T, kDQ, SP>::LD;
     static constexpr int TL = kDQ + 4;
-    T k[kDQ * LD], q[kDQ * LD];
-    float t[kDQ * TL];          // [j][i]: T transposed; gradient: N and M, transposed, in turn
-    float inv[4][16][20];       // [block][j][m]: the inverse of a block of 1 + beta T on the diagonal, transposed
-    float beta[kDQ];
-    double cum[kDQ];
+    struct Rows {
+        T k[kDQ * LD], q[kDQ * LD];
+    };
+    struct Solve {              // when the rows have been read
+        float t[GRAD ? 2 : 1][kDQ * TL];        // [j][i]: T transposed; gradient: then N and M, transposed
+        float inv[4][16][20];   // [block][j][m]: the inverse of a block of 1 + beta T on the diagonal, transposed
+    };
+    static constexpr int BYTES = sizeof(Rows) > sizeof(Solve) ? sizeof(Rows) : sizeof(Solve);
+    __align__(16) char at[BYTES];
+    double cum[4][kDQ];         // every wave's own
+    float beta[4][kDQ];
 };
 
 // One chunk of one group: 4 waves, wave I owns the rows 16 I .. of T, N and M.
@@ -177,87 +183,109 @@ template <typename T, int SP> struct PrepareShared {
 // do not depend on each other, N_IJ = (T_IJ - sum_{J<M<=I} N_IM beta T_MJ) (1 +
 // beta T_JJ)^-1, on the fp32 matrix instructions.
 template <typename T, int SP, bool GRAD>
-__global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaParams p)
+__global__ void __launch_bounds__(256, SP <= 128 ? 2 : 1) delta_prepare_kernel(DeltaParams p)
 {
-    typedef PrepareShared<T, SP> Shared;
+    typedef PrepareShared<T, SP, GRAD> Shared;
     constexpr int LD = Shared::LD, TL = Shared::TL, KS = SP / 32;
-    __shared__ __align__(16) Shared sh;
+    __shared__ Shared sh;
+    typename Shared::Rows &in = *reinterpret_cast<typename Shared::Rows *>(sh.at);
+    typename Shared::Solve &so = *reinterpret_cast<typename Shared::Solve *>(sh.at);
     const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q4 = (lane >> 4) * 4;
     const int64_t chunk = blockIdx.x / ((int64_t)p.G * p.slices);        // n K + c
     const int gs = (int)(blockIdx.x - chunk * p.G * p.slices), grp = gs / p.slices, slice = gs - grp * p.slices;
     const int64_t n = chunk / p.K, t0 = (chunk - n * p.K) * kDQ, len = seq_len(p.lengths, n, p.L);
     if (t0 >= len) return;
     const int live = (int)(len - t0 < kDQ ? len - t0 : kDQ);
+    const int per = p.H / p.G, h0 = grp * per + slice * p.heads_per_slice;
+    const int h1 = min(h0 + p.heads_per_slice, (grp + 1) * per);
+    const int64_t row = n * p.L + t0 + (lane < live ? lane : 0);
+    float g = p.g[row * p.g_ld + h0], rate = (float)((const T *)p.beta)[row * p.beta_ld + h0];
     {
         Tile<T, kDQ, SP> a, b;
         a.load((const T *)p.k + (n * p.L + t0) * p.k_ld + (int64_t)grp * p.S, p.k_ld, live, p.S, p.vec);
         b.load((const T *)p.q + (n * p.L + t0) * p.q_ld + (int64_t)grp * p.S, p.q_ld, live, p.S, p.vec);
-        a.store(sh.k);
-        b.store(sh.q);
+        a.store(in.k);
+        b.store(in.q);
     }
     __syncthreads();
-    if (slice == 0) {
-        char *at = p.keys + (chunk * p.G + grp) * keys_bytes<T, SP>(GRAD);
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            put_frag(at + (w * KS + s) * kFrag<T>, lane, read_rows(sh.k, LD, 16 * w, 32 * s, lane));
-            put_frag(at + (4 * KS + w * KS + s) * kFrag<T>, lane, read_rows(sh.q, LD, 16 * w, 32 * s, lane));
-        }
-        at += 8 * KS * kFrag<T>;
-        for (int f = w; f < (GRAD ? 4 * KS : 0); f += 4) {       // (s, a, pair of token tiles)
-            put_frag(at + f * kFrag<T>, lane, read_keys(sh.k, LD, 32 * (f & 1), f >> 2, f >> 1 & 1, lane));
-            put_frag(at + (4 * KS + f) * kFrag<T>, lane, read_keys(sh.q, LD, 32 * (f & 1), f >> 2, f >> 1 & 1, lane));
-        }
-    }
     // k_j . k_i and k_j . q_i: rows j of tile J, columns i of tile w
     f32x4 kk[4], kq[4];
 #pragma unroll
-    for (int J = 0; J < 4; ++J) {
-        kk[J] = kq[J] = f32x4{0, 0, 0, 0};
-        if (J > w) continue;
+    for (int J = 0; J < 4; ++J) kk[J] = kq[J] = f32x4{0, 0, 0, 0};
+    char *out = p.keys + (chunk * p.G + grp) * keys_bytes<T, SP>(GRAD);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const typename Frag<T>::type a = read_rows(sh.k, LD, 16 * J, 32 * s, lane);
-            kk[J] = mma(a, read_rows(sh.k, LD, 16 * w, 32 * s, lane), kk[J]);
-            kq[J] = mma(a, read_rows(sh.q, LD, 16 * w, 32 * s, lane), kq[J]);
+    for (int s = 0; s < KS; ++s) {
+        const typename Frag<T>::type bk = read_rows(in.k, LD, 16 * w, 32 * s, lane), bq = read_rows(in.q, LD, 16 * w, 32 * s, lane);
+        if (slice == 0 && !p.direct) {
+            put_frag(out + (w * KS + s) * kFrag<T>, lane, bk);
+            put_frag(out + (4 * KS + w * KS + s) * kFrag<T>, lane, bq);
+        }
+#pragma unroll
+        for (int J = 0; J < 4; ++J) {
+            if (J > w) continue;
+            const typename Frag<T>::type a = read_rows(in.k, LD, 16 * J, 32 * s, lane);
+            kk[J] = mma(a, bk, kk[J]);
+            kq[J] = mma(a, bq, kq[J]);
         }
     }
-    const int per = p.H / p.G, h0 = grp * per + slice * p.heads_per_slice;
-    const int h1 = min(h0 + p.heads_per_slice, (grp + 1) * per);
+    if (GRAD && slice == 0)
+        for (int f = w; f < 4 * KS; f += 4) {       // (s, a, pair of token tiles)
+            put_frag(out + (8 * KS + f) * kFrag<T>, lane, read_keys(in.k, LD, 32 * (f & 1), f >> 2, f >> 1 & 1, lane));
+            put_frag(out + (12 * KS + f) * kFrag<T>, lane, read_keys(in.q, LD, 32 * (f & 1), f >> 2, f >> 1 & 1, lane));
+        }
     const int i = 16 * w + l16;
     for (int h = h0; h < h1; ++h) {
         char *at = p.heads + (chunk * p.H + h) * head_bytes<T>(GRAD);
-        if (w == 0) {
-            const int64_t row = n * p.L + t0 + lane;
-            const float g = lane < live ? p.g[row * p.g_ld + h] : 0.0f;
-            const float beta = lane < live ? (float)((const T *)p.beta)[row * p.beta_ld + h] : 0.0f;
-            const double cum = wave_prefix((double)(g < -1e5f ? -1e5f : g)), end = wave_last(cum);
-            sh.cum[lane] = cum;
-            sh.beta[lane] = beta;
-            ChunkScalars *cs = reinterpret_cast<ChunkScalars *>(at);
-            cs->from_start[lane] = expf((float)cum);
-            cs->to_end[lane] = expf((float)(end - cum));
-            cs->beta[lane] = beta;
-            if (GRAD) cs->cum[lane] = cum;
-        }
-        at += GRAD ? (int64_t)sizeof(ChunkScalars) : kRows;
-        __syncthreads();
-        f32x4 tt[4], mm[4], beta[4];
-        const double ci = sh.cum[i];
-#pragma unroll
-        for (int J = 0; J < 4; ++J) {
-            beta[J] = *reinterpret_cast<const f32x4 *>(sh.beta + 16 * J + q4);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int j = 16 * J + q4 + r;
-                const float decay = j <= i ? expf((float)(ci - sh.cum[j])) : 0.0f;
-                tt[J][r] = j < i ? kk[J][r] * decay : 0.0f;
-                mm[J][r] = j <= i ? kq[J][r] * decay * p.scale : 0.0f;
-                sh.t[j * TL + i] = tt[J][r];
+        {
+            const bool on = lane < live;
+            const double step = (double)(g < -1e5f ? -1e5f : g) * 1.4426950408889634074;
+            const float beta = on ? rate : 0.0f;
+            const double cum = wave_prefix(on ? step : 0.0), end = wave_last(cum);
+            if (h + 1 < h1) {       // the next head's
+                g = p.g[row * p.g_ld + h + 1];
+                rate = (float)((const T *)p.beta)[row * p.beta_ld + h + 1];
+            }
+            sh.cum[w][lane] = cum;
+            sh.beta[w][lane] = beta;
+            if (w == 0) {
+                ChunkScalars *cs = reinterpret_cast<ChunkScalars *>(at);
+                cs->from_start[lane] = exp2_fast((float)cum);
+                cs->to_end[lane] = exp2_fast((float)(end - cum));
+                cs->beta[lane] = beta;
+                if (GRAD) cs->cum[lane] = cum;
             }
         }
-        __syncthreads();
-        // column l16 of (1 + beta T_ww)^-1, by forward substitution
+        at += GRAD ? (int64_t)sizeof(ChunkScalars) : kRows;
+        __syncthreads();        // the rows, or the last head's T, have been read
+        f32x4 tt[4], mm[4];
+        {
+            const double ci = sh.cum[w][i];
+#pragma unroll
+            for (int J = 0; J < 4; ++J) {
+                tt[J] = mm[J] = f32x4{0, 0, 0, 0};
+                if (J > w) continue;
+                const f32x4 beta = *reinterpret_cast<const f32x4 *>(&sh.beta[w][16 * J + q4]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int j = 16 * J + q4 + r;
+                    const float decay = j <= i ? exp2_fast((float)(ci - sh.cum[w][j])) : 0.0f;
+                    tt[J][r] = j < i ? kk[J][r] * decay : 0.0f;
+                    mm[J][r] = j <= i ? kq[J][r] * decay * p.scale * (GRAD ? 1.0f : beta[r]) : 0.0f;
+                    so.t[0][j * TL + i] = tt[J][r];
+                }
+            }
+        }
+        if constexpr (!GRAD) {
+#pragma unroll
+            for (int P = 0; P < 2; ++P) {
+                if (2 * P > w) continue;
+                Split<T, kM<T>> s;
+                stack(mm[2 * P], mm[2 * P + 1], s);
+#pragma unroll
+                for (int e = 0; e < kM<T>; ++e) put_frag(at + (kTri * kN<T> + lower(w, P) * kM<T> + e) * kFrag<T>, lane, s.f[e]);
+            }
+        }
+        // column l16 of (1 + beta T_ww)^-1, by forward substitution in this wave's own block
         {
             float x[16];
 #pragma unroll
@@ -265,13 +293,18 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaParams p)
 #pragma unroll
             for (int l = 0; l < 15; ++l) {
 #pragma unroll
-                for (int m = l + 1; m < 16; ++m)
-                    x[m] = fmaf(-sh.t[(16 * w + l) * TL + 16 * w + m] * sh.beta[16 * w + m], x[l], x[m]);
+                for (int m4 = (l + 1) / 4 * 4; m4 < 16; m4 += 4) {
+                    const f32x4 col = *reinterpret_cast<const f32x4 *>(&so.t[0][(16 * w + l) * TL + 16 * w + m4]) *
+                                      *reinterpret_cast<const f32x4 *>(&sh.beta[w][16 * w + m4]);
+#pragma unroll
+                    for (int m = m4; m < m4 + 4; ++m)
+                        if (m > l) x[m] = fmaf(-col[m - m4], x[l], x[m]);
+                }
             }
             if (lane < 16) {
 #pragma unroll
                 for (int m = 0; m < 16; m += 4)
-                    *reinterpret_cast<f32x4 *>(&sh.inv[w][l16][m]) = f32x4{x[m], x[m + 1], x[m + 2], x[m + 3]};
+                    *reinterpret_cast<f32x4 *>(&so.inv[w][l16][m]) = f32x4{x[m], x[m + 1], x[m + 2], x[m + 3]};
             }
         }
         __syncthreads();
@@ -284,15 +317,14 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaParams p)
 #pragma unroll
             for (int M = 3; M > J; --M) {
                 if (M > w) continue;
-                const f32x4 a = *reinterpret_cast<const f32x4 *>(sh.t + (16 * J + l16) * TL + 16 * M + q4);
+                const f32x4 a = *reinterpret_cast<const f32x4 *>(&so.t[0][(16 * J + l16) * TL + 16 * M + q4]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) rhs = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], nb[M][r], rhs, 0, 0, 0);
             }
-            const f32x4 a = *reinterpret_cast<const f32x4 *>(&sh.inv[J][l16][q4]);
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(&so.inv[J][l16][q4]);
 #pragma unroll
             for (int r = 0; r < 4; ++r) nn[J] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], rhs[r], nn[J], 0, 0, 0);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) nb[J][r] = -beta[J][r] * nn[J][r];
+            nb[J] = nn[J] * *reinterpret_cast<const f32x4 *>(&sh.beta[w][16 * J + q4]) * -1.0f;
         }
 #pragma unroll
         for (int P = 0; P < 2; ++P) {
@@ -302,33 +334,27 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaParams p)
 #pragma unroll
             for (int e = 0; e < kN<T>; ++e) put_frag(at + (lower(w, P) * kN<T> + e) * kFrag<T>, lane, s.f[e]);
         }
-        at += kTri * kN<T> * kFrag<T>;
-        if constexpr (!GRAD) {
+        if constexpr (GRAD) {
+            at += kTri * kN<T> * kFrag<T>;
+            __syncthreads();
 #pragma unroll
-            for (int P = 0; P < 2; ++P) {
-                if (2 * P > w) continue;
-                Split<T, kM<T>> s;
-                stack(mm[2 * P] * beta[2 * P], mm[2 * P + 1] * beta[2 * P + 1], s);
+            for (int J = 0; J < 4; ++J)
 #pragma unroll
-                for (int e = 0; e < kM<T>; ++e) put_frag(at + (lower(w, P) * kM<T> + e) * kFrag<T>, lane, s.f[e]);
-            }
-        } else {
+                for (int r = 0; r < 4; ++r) {
+                    so.t[0][(16 * J + q4 + r) * TL + i] = nn[J][r];
+                    so.t[1][(16 * J + q4 + r) * TL + i] = mm[J][r];
+                }
+            __syncthreads();
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
-                __syncthreads();
-#pragma unroll
-                for (int J = 0; J < 4; ++J)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) sh.t[(16 * J + q4 + r) * TL + i] = which ? mm[J][r] : nn[J][r];
-                __syncthreads();
 #pragma unroll
                 for (int P = 0; P < 2; ++P) {
                     if (2 * P + 1 < w) continue;
                     f32x4 v[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        v[e] = *reinterpret_cast<const f32x4 *>(sh.t + i * TL + 32 * P + 16 * e + q4);
-                        if (!which) v[e] = v[e] * -beta[2 * P + e];
+                        v[e] = *reinterpret_cast<const f32x4 *>(&so.t[which][i * TL + 32 * P + 16 * e + q4]);
+                        if (!which) v[e] = v[e] * *reinterpret_cast<const f32x4 *>(&sh.beta[w][32 * P + 16 * e + q4]) * -1.0f;
                     }
                     Split<T, kN<T>> s;
                     stack(v[0], v[1], s);
@@ -338,7 +364,6 @@ __global__ void __launch_bounds__(256) delta_prepare_kernel(DeltaParams p)
                 at += kTri * kN<T> * kFrag<T>;
             }
         }
-        __syncthreads();        // cum, beta and t are the next head's
     }
 }
 
@@ -587,7 +612,7 @@ __global__ void __launch_bounds__(64 * (SP == 32 ? 2 : SP == 256 ? 8 : 4)) delta
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int i = 16 * it + q4 + r;
-                const float decay = i >= j ? expf((float)(sh.cum[i] - sh.cum[j])) : 0.0f;
+                const float decay = i >= j ? exp2_fast((float)(sh.cum[i] - sh.cum[j])) : 0.0f;
                 const float lo = i >= j ? dm[t][r] * (decay * p.scale) : 0.0f, be = i > j ? wm[t][r] * decay : 0.0f;
                 pair[r] = i > j ? lo * qk[r] - be * kk[r] : 0.0f;      // a token's pair with itself crosses no decay
                 put_terms(sh.low, i * ML + j, lo);
@@ -668,7 +693,7 @@ __global__ void __launch_bounds__(64 * (SP == 32 ? 2 : SP == 256 ? 8 : 4)) delta
             const double dg = (sum - upto + d) + before + (double)sh.from_start[kDQ - 1] * whole;
             const double step = lane > 0 ? sh.cum[lane] - sh.cum[lane - 1] : sh.cum[0];
             // no gradient by a decay that is zero
-            if (lane < live) p.dg[(row0 + lane) * p.dg_ld + h] = expf((float)step) == 0.0f ? 0.0f : (float)dg;
+            if (lane < live) p.dg[(row0 + lane) * p.dg_ld + h] = exp2_fast((float)step) == 0.0f ? 0.0f : (float)dg;
         }
     }
     // dq and dk: of this call, or of a slice's heads
