@@ -388,11 +388,12 @@ SEQ_DEV int64_t unit_of(int64_t block, int64_t units)
 // (every path of dg_t crosses the decay of token t; a pair counts as its row less
 // its column, the same number in fp64 twice, so that what cancels leaves nothing).
 // One workgroup takes one chunk of a slice of a group's heads; a wave owns CT
-// blocks of 16 keys, in the order of K^T's operands, and reads S and R itself: no
-// other wave needs them.  dO, dV and U go through LDS, split into their terms once.
+// blocks of 16 keys, in the order of K^T's operands, and reads S and R itself, a step
+// ahead: no other wave needs them.  dO, dV and U go through LDS, split into their terms
+// once, their rows fetched a block of channels ahead.
 template <typename T, int SP> struct GradShape {
-    static constexpr int NW = SP == 32 ? 2 : SP == 256 ? 8 : 4;      // waves
-    static constexpr int CT = SP / 16 / NW;
+    static constexpr int NW = SP <= 64 ? 4 : 8;                      // waves
+    static constexpr int CT = SP / 16 < NW ? 1 : SP / 16 / NW;
     static constexpr int PB = 64;                                    // channels at a time
     static constexpr int TT = (10 + NW - 1) / NW;                    // triangular tiles of a wave
     static constexpr int LD = PB + Frag<T>::PAD, ML = kDQ + Frag<T>::PAD;
@@ -434,6 +435,13 @@ SEQ_DEV Frag<float>::type read_cols_stacked(const float *t, int ld, int k0, int 
     return f;
 }
 
+// an element a lane's number of bytes from an address that all lanes share: no
+// register pairs for addresses
+template <typename X> SEQ_DEV X *lane_at(X *base, uint32_t bytes)
+{
+    return reinterpret_cast<X *>(reinterpret_cast<uintptr_t>(base) + bytes);
+}
+
 // element (row, col) of a matrix held as terms
 template <typename T, int NS, int ALL> SEQ_DEV void put_terms(T (&m)[NS][ALL], int at, float v)
 {
@@ -445,14 +453,19 @@ template <typename T, int NS, int ALL> SEQ_DEV void put_terms(T (&m)[NS][ALL], i
     }
 }
 
-template <typename T, int SP>
-__global__ void __launch_bounds__(64 * (SP == 32 ? 2 : SP == 256 ? 8 : 4)) delta_grad_kernel(DeltaParams p)
+template <typename T, int SP> __global__ void __launch_bounds__(SP <= 64 ? 256 : 512) delta_grad_kernel(DeltaParams p)
 {
     typedef GradShape<T, SP> G;
     constexpr int NW = G::NW, CT = G::CT, PB = G::PB, TT = G::TT, LD = G::LD, ML = G::ML, NL = G::NL, KS = SP / 32;
     constexpr int kRowsAtOnce = NW * 4, RI = kDQ / kRowsAtOnce;     // 16 threads take a row of PB channels
     __shared__ __align__(16) GradShared<T, SP> sh;
-    const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q = lane >> 4, q4 = q * 4;
+    const int lane0 = threadIdx.x & 63, w = wave_id();
+    const int lane = lane0, l16 = lane & 15, q = lane >> 4, q4 = q * 4;
+    // a phase takes its lane anew, so that its LDS addresses (beyond an instruction's offset) are not all computed
+    // before the loop over the heads and held
+#define NEW_LANE const int lane = fresh_vector(lane0), l16 = lane & 15, q = lane >> 4, q4 = q * 4; (void)lane, (void)l16, (void)q, (void)q4
+    const bool cols = w * CT < SP / 16;                                  // a wave that has keys
+    const int tri = NW - 1 - w;                                          // the others first
     const int64_t chunk = blockIdx.x / ((int64_t)p.G * p.slices);        // n K + c
     const int gs = (int)(blockIdx.x - chunk * p.G * p.slices), grp = gs / p.slices, slice = gs - grp * p.slices;
     const int64_t n = chunk / p.K, c = chunk - n * p.K, t0 = c * kDQ, len = seq_len(p.lengths, n, p.L);
@@ -484,8 +497,61 @@ __global__ void __launch_bounds__(64 * (SP == 32 ? 2 : SP == 256 ? 8 : 4)) delta
     for (int e = threadIdx.x; e < kDQ * ML; e += NW * 64)
 #pragma unroll
         for (int x = 0; x < NL; ++x) sh.low[x][e] = (T)0.0f;
+    // k_i . k_j and q_i . k_j are all heads'
+    f32x4 kk[TT], qk[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        kk[t] = qk[t] = f32x4{0, 0, 0, 0};
+        if (live == 0 || tri + t * NW >= 10) continue;
+        int it, jt;
+        triangle(tri + t * NW, it, jt);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const typename Frag<T>::type b = get_frag<T>(keys + (jt * KS + s) * kFrag<T>, lane);
+            kk[t] = mma(get_frag<T>(keys + (it * KS + s) * kFrag<T>, lane), b, kk[t]);
+            qk[t] = mma(get_frag<T>(keys + ((4 + it) * KS + s) * kFrag<T>, lane), b, qk[t]);
+        }
+    }
+    const int my_row = threadIdx.x >> 4;
+    const uint32_t dy_step = (uint32_t)p.dy_ld * (uint32_t)sizeof(T), dv_step = (uint32_t)p.dv_ld * (uint32_t)sizeof(T);
+    f32x4 ry[RI], re[RI], rd[RI];       // the next block of channels: Y, E, dO
+    auto load_rows = [&](int h, int p0) {
+        const int pc = p0 + 4 * l16;
+        const int64_t at = ((n * p.H + h) * p.K + c) * kDQ * p.PP;
+        const float *gy = p.rows[0] + at, *ge = p.rows[1] + at;
+        const T *gd = (const T *)p.dy + row0 * p.dy_ld + (int64_t)h * p.P;
+#pragma unroll
+        for (int e = 0; e < RI; ++e) {
+            const int row = my_row + e * kRowsAtOnce;
+            ry[e] = re[e] = rd[e] = f32x4{0, 0, 0, 0};
+            if (row < live && pc < p.PP) {
+                const uint32_t o = (uint32_t)(row * p.PP + pc) * 4, d = (uint32_t)row * dy_step + (uint32_t)pc * (uint32_t)sizeof(T);
+                ry[e] = *reinterpret_cast<const f32x4 *>(lane_at(gy, o));
+                re[e] = *reinterpret_cast<const f32x4 *>(lane_at(ge, o));
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (pc + i < p.P) rd[e][i] = (float)lane_at(gd, d)[i];
+            }
+        }
+    };
+    float sv[CT][8], rv[CT][8];         // the next 32 channels of S and R
+    auto load_states = [&](int h, int p0) {
+        if (!cols) return;
+        const int64_t at = (((n * p.H + h) * p.K + c) * p.PP + p0) * SP;
+#pragma unroll
+        for (int x = 0; x < CT; ++x) {
+            const int b = w * CT + x;
+            const uint32_t o = (uint32_t)(8 * q * SP + 32 * (b >> 1) + 4 * (b & 1) + key0) * 4;
+            const float *gs = lane_at(p.bound[0] + at, o), *gr = lane_at(p.bound[1] + at, o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sv[x][i] = gs[i * SP], rv[x][i] = gr[i * SP];
+        }
+    };
+    if (live > 0) {
+        load_rows(h0, 0);
+        load_states(h0, 0);
+    }
     for (int h = h0; h < (live > 0 ? h1 : h0); ++h) {
-        const int64_t nh = n * p.H + h;
         const char *head = p.heads + (chunk * p.H + h) * head_bytes<T>(true);
         const ChunkScalars *cs = reinterpret_cast<const ChunkScalars *>(head);
         __syncthreads();
@@ -507,73 +573,70 @@ __global__ void __launch_bounds__(64 * (SP == 32 ? 2 : SP == 256 ? 8 : 4)) delta
         for (int e = 0; e < RI; ++e) db[e] = 0.0f;
         double across = 0.0;
         for (int p0 = 0; p0 < p.PP; p0 += PB) {
+            NEW_LANE;
+            const int my_row = 4 * w + q;
             __syncthreads();
-            const int pc = p0 + 4 * (threadIdx.x & 15);
 #pragma unroll
             for (int e = 0; e < RI; ++e) {
-                const int row = (threadIdx.x >> 4) + e * kRowsAtOnce;
-                f32x4 y = {0, 0, 0, 0}, ee = {0, 0, 0, 0}, dy = {0, 0, 0, 0};
-                if (row < live && pc < p.PP) {
-                    const int64_t at = ((nh * p.K + c) * kDQ + row) * p.PP + pc;
-                    y = *reinterpret_cast<const f32x4 *>(p.rows[0] + at);
-                    ee = *reinterpret_cast<const f32x4 *>(p.rows[1] + at);
-                    const T *g = (const T *)p.dy + (row0 + row) * p.dy_ld + (int64_t)h * p.P + pc;
-                    T *d = (T *)p.dv + (row0 + row) * p.dv_ld + (int64_t)h * p.P + pc;
+                const int row = my_row + e * kRowsAtOnce, pc = p0 + 4 * l16;
+                const float beta = sh.beta[row];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        db[e] = fmaf(ee[i], y[i], db[e]);
-                        if (pc + i < p.P) {
-                            dy[i] = (float)g[i];
-                            d[i] = (T)(sh.beta[row] * ee[i]);
-                        }
-                    }
-                    ee = ee * sh.beta[row];
-                    y = y * sh.beta[row];
+                for (int i = 0; i < 4; ++i) db[e] = fmaf(re[e][i], ry[e][i], db[e]);
+                const f32x4 dv = re[e] * beta;
+                if (row < live) {
+                    T *d = lane_at((T *)p.dv + row0 * p.dv_ld + (int64_t)h * p.P, (uint32_t)row * dv_step + (uint32_t)pc * (uint32_t)sizeof(T));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (pc + i < p.P) d[i] = (T)dv[i];
                 }
-                const int at = row * LD + 4 * (threadIdx.x & 15);
-                write_split4<1>(sh.dy + at, 0, dy);
-                write_split4<kN<T>>(sh.dv[0] + at, kDQ * LD, ee);
-                write_split4<kN<T>>(sh.u[0] + at, kDQ * LD, y);
+                const int at = row * LD + 4 * l16;
+                write_split4<1>(sh.dy + at, 0, rd[e]);
+                write_split4<kN<T>>(sh.dv[0] + at, kDQ * LD, dv);
+                write_split4<kN<T>>(sh.u[0] + at, kDQ * LD, ry[e] * beta);
             }
+            if (p0 + PB < p.PP) load_rows(h, p0 + PB);
+            else if (h + 1 < h1) load_rows(h + 1, 0);
             __syncthreads();
-#pragma unroll
+            // one step after the other, and one row tile: all of their reads at once leave no registers
+#pragma unroll 1
             for (int s = 0; s < PB / 32; ++s) {
                 if (p0 + 32 * s >= p.PP) break;
-                Split<T, kN<T>> ss[CT], rs[CT];
-#pragma unroll
-                for (int x = 0; x < CT; ++x) {
-                    const int b = w * CT + x;
-                    const int64_t at = ((nh * p.K + c) * p.PP + p0 + 32 * s + 8 * q) * SP + 32 * (b >> 1) + 4 * (b & 1) + key0;
-                    float sv[8], rv[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) sv[i] = p.bound[0][at + i * SP], rv[i] = p.bound[1][at + i * SP];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) across = fma((double)sv[i], (double)rv[i], across);
-                    make_split(sv, ss[x]);
-                    make_split(rv, rs[x]);
-                }
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    Split<T, 1> a;
-                    Split<T, kN<T>> d, u;
-                    a.f[0] = read_rows(sh.dy, LD, 16 * t, 32 * s, lane);
-#pragma unroll
-                    for (int e = 0; e < kN<T>; ++e) {
-                        d.f[e] = read_rows(sh.dv[e], LD, 16 * t, 32 * s, lane);
-                        u.f[e] = read_rows(sh.u[e], LD, 16 * t, 32 * s, lane);
-                    }
+                NEW_LANE;
+                if (cols) {
+                    Split<T, kN<T>> ss[CT], rs[CT];
 #pragma unroll
                     for (int x = 0; x < CT; ++x) {
-                        by[x][t] = mma_terms(a, ss[x], by[x][t]);
-                        old[x][t] = mma_terms(d, ss[x], old[x][t]);
-                        nw[x][t] = mma_terms(u, rs[x], nw[x][t]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) across = fma((double)sv[x][i], (double)rv[x][i], across);
+                        make_split(sv[x], ss[x]);
+                        make_split(rv[x], rs[x]);
+                    }
+                    if (p0 + 32 * (s + 1) < p.PP) load_states(h, p0 + 32 * (s + 1));
+                    else if (h + 1 < h1) load_states(h + 1, 0);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        Split<T, 1> a;
+                        Split<T, kN<T>> d, u;
+                        a.f[0] = read_rows(sh.dy, LD, 16 * t, 32 * s, lane);
+#pragma unroll
+                        for (int e = 0; e < kN<T>; ++e) {
+                            d.f[e] = read_rows(sh.dv[e], LD, 16 * t, 32 * s, lane);
+                            u.f[e] = read_rows(sh.u[e], LD, 16 * t, 32 * s, lane);
+                        }
+#pragma unroll
+                        for (int x = 0; x < CT; ++x) {
+                            by[x][t] = mma_terms(a, ss[x], by[x][t]);
+                            old[x][t] = mma_terms(d, ss[x], old[x][t]);
+                            nw[x][t] = mma_terms(u, rs[x], nw[x][t]);
+                        }
+                        in_order();
                     }
                 }
 #pragma unroll
                 for (int t = 0; t < TT; ++t) {
-                    if (w + t * NW >= 10) continue;
+                    if (tri + t * NW >= 10) continue;
                     int it, jt;
-                    triangle(w + t * NW, it, jt);
+                    triangle(tri + t * NW, it, jt);
                     Split<T, 1> a;
                     Split<T, kN<T>> d, u;
                     a.f[0] = read_rows(sh.dy, LD, 16 * it, 32 * s, lane);
@@ -584,37 +647,36 @@ __global__ void __launch_bounds__(64 * (SP == 32 ? 2 : SP == 256 ? 8 : 4)) delta
                     }
                     dm[t] = mma_terms(a, u, dm[t]);
                     wm[t] = mma_terms(d, u, wm[t]);
+                    in_order();
                 }
             }
         }
         // dbeta: the 16 threads of a row
 #pragma unroll
         for (int e = 0; e < RI; ++e) {
+            NEW_LANE;
+            const int my_row = 4 * w + q;
             float v = db[e];
             for (int o = 8; o > 0; o >>= 1) v += __shfl_xor(v, o);
-            const int row = (threadIdx.x >> 4) + e * kRowsAtOnce;
-            if (l16 == 0 && row < live) ((T *)p.dbeta)[(row0 + row) * p.dbeta_ld + h] = (T)v;
+            const int row = my_row + e * kRowsAtOnce;
+            if (l16 == 0 && row < live)
+                *lane_at((T *)p.dbeta + row0 * p.dbeta_ld + h, (uint32_t)row * (uint32_t)p.dbeta_ld * (uint32_t)sizeof(T)) = (T)v;
         }
         // pairs of tokens
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            if (w + t * NW >= 10) continue;
+            if (tri + t * NW >= 10) continue;
+            NEW_LANE;
             int it, jt;
-            triangle(w + t * NW, it, jt);
-            f32x4 kk = {0, 0, 0, 0}, qk = {0, 0, 0, 0}, pair;
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                const typename Frag<T>::type b = get_frag<T>(keys + (jt * KS + s) * kFrag<T>, lane);
-                kk = mma(get_frag<T>(keys + (it * KS + s) * kFrag<T>, lane), b, kk);
-                qk = mma(get_frag<T>(keys + ((4 + it) * KS + s) * kFrag<T>, lane), b, qk);
-            }
+            triangle(tri + t * NW, it, jt);
+            f32x4 pair;
             const int j = 16 * jt + l16;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int i = 16 * it + q4 + r;
                 const float decay = i >= j ? exp2_fast((float)(sh.cum[i] - sh.cum[j])) : 0.0f;
                 const float lo = i >= j ? dm[t][r] * (decay * p.scale) : 0.0f, be = i > j ? wm[t][r] * decay : 0.0f;
-                pair[r] = i > j ? lo * qk[r] - be * kk[r] : 0.0f;      // a token's pair with itself crosses no decay
+                pair[r] = i > j ? lo * qk[t][r] - be * kk[t][r] : 0.0f;      // a token's pair with itself crosses no decay
                 put_terms(sh.low, i * ML + j, lo);
                 if (i >= j) {
                     put_terms(sh.sym, i * ML + j, -be);
@@ -627,12 +689,14 @@ __global__ void __launch_bounds__(64 * (SP == 32 ? 2 : SP == 256 ? 8 : 4)) delta
             down += __shfl_xor(down, 16);
             down += __shfl_xor(down, 32);
             if (q == 0) sh.col[it][j] = down;
+            in_order();
         }
         // what the states in front and behind give, and its part in dg
-        double front[4], behind[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            front[t] = behind[t] = 0.0;
+            if (!cols) break;
+            NEW_LANE;
+            double front = 0.0, behind = 0.0;
             const f32x4 grow = *reinterpret_cast<const f32x4 *>(sh.from_start + 16 * t + q4);
             const f32x4 fade = *reinterpret_cast<const f32x4 *>(sh.to_end + 16 * t + q4);
 #pragma unroll
@@ -649,14 +713,15 @@ __global__ void __launch_bounds__(64 * (SP == 32 ? 2 : SP == 256 ? 8 : 4)) delta
                     a[r] = by[x][t][r] * qv - old[x][t][r] * kv;
                     b[r] = nw[x][t][r] * kv;
                 }
-                front[t] += row_sum4<double>(a, lane);
-                behind[t] += row_sum4<double>(b, lane);
+                front += row_sum4<double>(a, lane);
+                behind += row_sum4<double>(b, lane);
                 dq[x][t] = dq[x][t] + by[x][t];
                 dk[x][t] = dk[x][t] + (nw[x][t] - old[x][t]);
+                in_order();
             }
             if ((l16 & 3) == 0) {
-                sh.front[w][16 * t + q4 + (l16 >> 2)] = front[t];
-                sh.behind[w][16 * t + q4 + (l16 >> 2)] = behind[t];
+                sh.front[w][16 * t + q4 + (l16 >> 2)] = front;
+                sh.behind[w][16 * t + q4 + (l16 >> 2)] = behind;
             }
         }
         for (int o = 32; o > 0; o >>= 1) across += __shfl_xor(across, o);
@@ -666,6 +731,8 @@ __global__ void __launch_bounds__(64 * (SP == 32 ? 2 : SP == 256 ? 8 : 4)) delta
         for (int x = 0; x < CT; ++x)
 #pragma unroll
             for (int P = 0; P < 2; ++P) {
+                if (!cols) continue;
+                NEW_LANE;
                 Split<T, 1> kf, qf;
                 kf.f[0] = get_frag<T>(kt + ((w * CT + x) * 2 + P) * kFrag<T>, lane);
                 qf.f[0] = get_frag<T>(qt + ((w * CT + x) * 2 + P) * kFrag<T>, lane);
@@ -677,9 +744,11 @@ __global__ void __launch_bounds__(64 * (SP == 32 ? 2 : SP == 256 ? 8 : 4)) delta
                         dk[x][t] = mma(read_rows_stacked(sh.sym[e], ML, 16 * t, 32 * P, lane), kf.f[0], dk[x][t]);
                         if (P >= t / 2) dk[x][t] = mma(read_cols_stacked(sh.low[e], ML, 32 * P, 16 * t, lane), qf.f[0], dk[x][t]);
                     }
+                    in_order();
                 }
             }
         if (w == 0) {
+            NEW_LANE;
             double d = 0.0, b = 0.0, whole = 0.0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -687,7 +756,8 @@ __global__ void __launch_bounds__(64 * (SP == 32 ? 2 : SP == 256 ? 8 : 4)) delta
                 if (e >= lane >> 4) d -= sh.col[e][lane];
             }
 #pragma unroll
-            for (int e = 0; e < NW; ++e) d += sh.front[e][lane], b += sh.behind[e][lane], whole += sh.across[e];
+            for (int e = 0; e < NW; ++e)
+                if (e * CT < SP / 16) d += sh.front[e][lane], b += sh.behind[e][lane], whole += sh.across[e];
             if (lane >= live) d = b = 0.0;
             const double upto = wave_prefix(d), sum = wave_last(upto), before = wave_prefix(b) - b;
             const double dg = (sum - upto + d) + before + (double)sh.from_start[kDQ - 1] * whole;
@@ -697,10 +767,12 @@ __global__ void __launch_bounds__(64 * (SP == 32 ? 2 : SP == 256 ? 8 : 4)) delta
         }
     }
     // dq and dk: of this call, or of a slice's heads
+    const int64_t part = (((int64_t)slice * p.N * p.L + row0) * p.G + grp) * p.S;
+    const uint32_t part_step = (uint32_t)(p.G * p.S) * 4;
 #pragma unroll
     for (int x = 0; x < CT; ++x) {
         const int b = w * CT + x, key = 32 * (b >> 1) + 4 * (b & 1) + key0;
-        if (key >= p.S) continue;
+        if (!cols || key >= p.S) continue;
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -709,16 +781,17 @@ __global__ void __launch_bounds__(64 * (SP == 32 ? 2 : SP == 256 ? 8 : 4)) delta
                 if (row >= all) continue;
                 const float vq = row < live ? dq[x][t][r] : 0.0f, vk = row < live ? dk[x][t][r] : 0.0f;
                 if (p.slices == 1) {
-                    ((T *)p.dq)[(row0 + row) * p.dq_ld + (int64_t)grp * p.S + key] = (T)vq;
-                    ((T *)p.dk)[(row0 + row) * p.dk_ld + (int64_t)grp * p.S + key] = (T)vk;
+                    const uint32_t k = (uint32_t)key * (uint32_t)sizeof(T);
+                    *lane_at((T *)p.dq + row0 * p.dq_ld + (int64_t)grp * p.S, (uint32_t)row * (uint32_t)p.dq_ld * (uint32_t)sizeof(T) + k) = (T)vq;
+                    *lane_at((T *)p.dk + row0 * p.dk_ld + (int64_t)grp * p.S, (uint32_t)row * (uint32_t)p.dk_ld * (uint32_t)sizeof(T) + k) = (T)vk;
                 } else {
-                    const int64_t at = (((int64_t)slice * p.N * p.L + row0 + row) * p.G + grp) * p.S + key;
-                    p.part[0][at] = vq;
-                    p.part[1][at] = vk;
+                    *lane_at(p.part[0] + part, (uint32_t)row * part_step + (uint32_t)key * 4) = vq;
+                    *lane_at(p.part[1] + part, (uint32_t)row * part_step + (uint32_t)key * 4) = vk;
                 }
             }
     }
 }
+#undef NEW_LANE
 
 // dq and dk from the slices' sums, always in the same order
 template <typename T> __global__ void __launch_bounds__(256) delta_reduce_kernel(DeltaParams p)
