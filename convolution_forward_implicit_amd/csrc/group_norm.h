@@ -15,9 +15,11 @@
 // Over pixels (gnorm_stats, _apply, _sums, _grad): a workgroup takes a slab of a
 // sample's rows by whole groups; a thread owns V neighbouring channels, whose
 // weights it loads once, and steps over the slab's rows.  The first pass leaves each
-// slab's mean and sum of squares around it; whoever needs a group's joins the slabs'
-// itself, which saves a launch.  The gradient's second pass leaves sum d and sum d
-// xhat of every channel of a slab: dw, db and both of a group's sums come from these.
+// slab's mean and sum of squares around it, which gnorm_join makes a group's: a launch
+// more, but joined by every workgroup of the next pass they took longer than its rows
+// (8 x 3136 x 256 channels: 14 us where 6 are left).  The gradient's second pass leaves
+// sum d and sum d xhat of every channel of a slab: dw, db and both of a group's sums
+// come from these.
 //
 // Of each token by itself (gnorm_token, gnorm_token_grad): `lanes` lanes hold a group
 // in registers, so everything is read once.
@@ -49,6 +51,7 @@ struct NormParams {
     float *stats;                   // [sample][slab][G][2]: mean, sum of squares around it
     float *sums;                    // [sample][slab][2][G C]: sum d, sum d xhat
     float *group;                   // [sample][slab][G][2]: the same times w, of a group
+    float *moments, *pulls;         // [sample][G][2]: mean and r; sum d w / n, sum d w xhat / n
     int64_t reduce_from;            // workgroups from here on add up dw and dbias
 };
 
@@ -123,16 +126,16 @@ SEQ_DEV int64_t norm_rows(const NormParams &p, int64_t n)
 // `wide` of rows r0, r0 + step, ..
 struct NormShare {
     int64_t n, slab, row0;      // sample, its slab, first row of the sample's
-    int64_t live, last;         // end of the slab's rows: those that count, all
+    int64_t first, live, last;  // of the slab's rows: the first, the end of those that count, of all
     int g0, ng, cv, wide, step, col, r0;
 };
-template <int V> SEQ_DEV NormShare norm_share(const NormParams &p, int64_t block)
+template <int V> SEQ_DEV NormShare norm_share(const NormParams &p, uint32_t block)
 {
     NormShare s;
-    const int64_t slab = block / p.blocks;
-    s.n = slab / p.slabs;
-    s.slab = slab - s.n * p.slabs;
-    s.g0 = (int)(block - slab * p.blocks) * p.groups;
+    const uint32_t slab = block / (uint32_t)p.blocks, n = slab / (uint32_t)p.slabs;      // fewer than 2^32 workgroups
+    s.n = n;
+    s.slab = slab - n * (uint32_t)p.slabs;
+    s.g0 = (int)(block - slab * (uint32_t)p.blocks) * p.groups;
     s.ng = min(p.groups, p.G - s.g0);
     s.cv = p.C / V;
     s.wide = s.ng * s.cv;
@@ -141,41 +144,43 @@ template <int V> SEQ_DEV NormShare norm_share(const NormParams &p, int64_t block
     s.col = s.wide <= 256 ? (int)threadIdx.x - s.r0 * s.wide : (int)threadIdx.x;
     if (s.r0 >= s.step) s.col = s.wide;
     s.row0 = s.n * p.rows;
-    s.last = (s.slab + 1) * p.slab < p.rows ? (s.slab + 1) * p.slab : p.rows;
+    s.first = s.slab * p.slab;
+    s.last = s.first + p.slab < p.rows ? s.first + p.slab : p.rows;
     const int64_t rows = norm_rows(p, s.n);
     s.live = s.last < rows ? s.last : rows;
     return s;
 }
 
-SEQ_DEV double row16_sum(double v)
+// (count, mean, squares) of `n` parts that get(i, cnt, mean, m2) names, by LANES lanes:
+// in fp64, around the first part's mean, which is near the whole's.
+template <int LANES> SEQ_DEV double lanes_sum64(double v)
 {
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
     return v;
 }
-
-// (count, mean, squares) of `n` parts that get(i, cnt, mean, m2) names, by the 16 lanes of a row
-template <typename F> SEQ_DEV void join_parts(int64_t n, F &&get, double &mean, double &m2)
+template <int LANES, typename F> SEQ_DEV void join_parts(int n, F &&get, double &cnt, double &mean, double &m2)
 {
-    const int l = threadIdx.x & 15;
-    double cnt = 0.0, sum = 0.0;
-    for (int64_t i = l; i < n; i += 16) {
+    const int l = threadIdx.x & (LANES - 1);
+    float c0, mean0, s0;
+    get(0, c0, mean0, s0);
+    double sum = 0.0, sq = 0.0;
+    cnt = 0.0;
+#pragma unroll 4
+    for (int i = l; i < n; i += LANES) {
         float c, m, s;
         get(i, c, m, s);
+        const double d = c > 0.0f ? (double)m - (double)mean0 : 0.0, cd = (double)c * d;
         cnt += (double)c;
-        sum += (double)c * (double)m;
+        sum += cd;
+        sq += c > 0.0f ? fma(cd, d, (double)s) : 0.0;
     }
-    cnt = row16_sum(cnt);
-    sum = row16_sum(sum);
-    mean = cnt > 0.0 ? sum / cnt : 0.0;
-    m2 = 0.0;
-    for (int64_t i = l; i < n; i += 16) {
-        float c, m, s;
-        get(i, c, m, s);
-        const double d = (double)m - mean;
-        m2 += c > 0.0f ? (double)s + (double)c * d * d : 0.0;
-    }
-    m2 = row16_sum(m2);
+    cnt = lanes_sum64<LANES>(cnt);
+    sum = lanes_sum64<LANES>(sum);
+    sq = lanes_sum64<LANES>(sq);
+    const double off = cnt > 0.0 ? sum / cnt : 0.0, left = fma(-off, sum, sq);
+    mean = (double)mean0 + off;
+    m2 = left < 0.0 ? 0.0 : left;       // a NaN stays one
 }
 
 // (count, mean, squares) joined with a batch of `b` values of mean bm and squares bs
@@ -188,12 +193,13 @@ SEQ_DEV void join_batch(float &cnt, float &mean, float &m2, float b, float bm, f
 }
 
 constexpr int kNormBatch = 4;       // rows that a thread has under way
+constexpr int kReduceThreads = 1024;    // 16 channels' slabs, by 64 threads each
 
 template <typename T, int V> __global__ void __launch_bounds__(256) gnorm_stats_kernel(NormParams p)
 {
     __shared__ float part[3][256];
     const NormShare s = norm_share<V>(p, blockIdx.x);
-    const int64_t first = s.slab * p.slab;
+    const int64_t first = s.first;
     float cnt = 0.0f, mean = 0.0f, m2 = 0.0f;
     for (int col = s.col; col < s.wide; col += 256) {
         const T *x = (const T *)p.x + s.row0 * p.x_ld + (int64_t)s.g0 * p.C + col * V;
@@ -235,11 +241,11 @@ template <typename T, int V> __global__ void __launch_bounds__(256) gnorm_stats_
     // threads that hold parts of group g: all 256 where a row is wider than that
     for (int g = threadIdx.x >> 4; g < s.ng; g += 16) {
         const int cols = s.wide <= 256 ? s.cv : 256, n = s.wide <= 256 ? s.cv * s.step : 256;
-        double mean_g, m2_g;
-        join_parts(n, [&](int64_t i, float &c, float &m, float &q) {
-            const int t = (int)i / cols * s.wide + (s.wide <= 256 ? g * s.cv : 0) + (int)i % cols;
+        double cnt_g, mean_g, m2_g;
+        join_parts<16>(n, [&](int i, float &c, float &m, float &q) {
+            const int t = i / cols * s.wide + (s.wide <= 256 ? g * s.cv : 0) + i % cols;
             c = part[0][t], m = part[1][t], q = part[2][t];
-        }, mean_g, m2_g);
+        }, cnt_g, mean_g, m2_g);
         if ((threadIdx.x & 15) == 0) {
             float *o = p.stats + ((s.n * p.slabs + s.slab) * p.G + s.g0 + g) * 2;
             o[0] = (float)mean_g;
@@ -248,26 +254,45 @@ template <typename T, int V> __global__ void __launch_bounds__(256) gnorm_stats_
     }
 }
 
-// mean and r of the groups of this workgroup, from all slabs of the sample
-SEQ_DEV void norm_statistics(const NormParams &p, const NormShare &s, float *mean, float *rstd)
+// A group's mean and r from its slabs', or (GRAD) what its gradients are taken off by: a wave each
+template <bool GRAD> SEQ_DEV void norm_join(const NormParams &p, uint32_t block)
 {
-    const int64_t rows = norm_rows(p, s.n);
-    const double n = (double)rows * p.C;
-    for (int g = threadIdx.x >> 4; g < s.ng; g += 16) {
-        double m, m2;
-        join_parts(p.slabs, [&](int64_t i, float &c, float &mm, float &q) {
-            const float *o = p.stats + ((s.n * p.slabs + i) * p.G + s.g0 + g) * 2;
+    const uint32_t at = block * (GRAD ? kReduceThreads / 64 : 4) + (threadIdx.x >> 6), sample = at / (uint32_t)p.G;
+    const int g = (int)(at - sample * (uint32_t)p.G), lane = threadIdx.x & 63;
+    const int64_t n = sample;
+    if (n >= p.samples) return;
+    const int64_t rows = norm_rows(p, n);
+    if constexpr (GRAD) {
+        const double count = (double)rows * p.C;
+        double a = 0.0, b = 0.0;
+#pragma unroll 4
+        for (int i = lane; i < (int)p.slabs; i += 64) {
+            const float *o = p.group + ((n * p.slabs + i) * p.G + g) * 2;
+            a += (double)o[0];
+            b += (double)o[1];
+        }
+        a = lanes_sum64<64>(a);
+        b = lanes_sum64<64>(b);
+        if (lane == 0) {
+            p.pulls[(int64_t)at * 2] = p.center && count > 0.0 ? (float)(a / count) : 0.0f;
+            p.pulls[(int64_t)at * 2 + 1] = count > 0.0 ? (float)(b / count) : 0.0f;
+        }
+    } else {
+        double count, m, m2;
+        join_parts<64>((int)p.slabs, [&](int i, float &c, float &mm, float &q) {
+            const float *o = p.stats + ((n * p.slabs + i) * p.G + g) * 2;
             const int64_t have = rows - i * p.slab;
             c = (float)((have < 0 ? 0 : have < p.slab ? have : p.slab) * p.C);
             mm = o[0], q = o[1];
-        }, m, m2);
-        if ((threadIdx.x & 15) == 0) {
-            const double var = n > 0.0 ? m2 / n + (p.center ? 0.0 : m * m) : 0.0;
-            mean[g] = p.center ? (float)m : 0.0f;
-            rstd[g] = (float)(1.0 / sqrt(var + (double)p.eps));
+        }, count, m, m2);
+        if (lane == 0) {
+            const double var = count > 0.0 ? m2 / count + (p.center ? 0.0 : m * m) : 0.0;
+            p.moments[(int64_t)at * 2] = p.center ? (float)m : 0.0f;
+            p.moments[(int64_t)at * 2 + 1] = (float)(1.0 / sqrt(var + (double)p.eps));
         }
     }
 }
+__global__ void __launch_bounds__(256) gnorm_join_kernel(NormParams p) { norm_join<false>(p, blockIdx.x); }
 
 // V weights and biases of a thread's channels
 template <typename T, int V> SEQ_DEV void norm_weights(const NormParams &p, int64_t at, float (&w)[V], float (&b)[V])
@@ -289,40 +314,52 @@ template <typename T, int V> SEQ_DEV void norm_out(const NormParams &p, const fl
     }
 }
 
+// Rows row, row + step, .. of a thread's channels, as they are; in place of those that do not count a row that is
+// there: without a branch the loads are all under way at once.
+template <typename T, int V> struct Batch {
+    typename Pack<T, V>::type q[kNormBatch];
+    SEQ_DEV void load(const T *x, int64_t ld, int64_t row, int step, int64_t live)
+    {
+        const int last = live > 0 ? (int)live - 1 : 0;
+#pragma unroll
+        for (int e = 0; e < kNormBatch; ++e) {
+            const int r = (int)row + e * step;
+            q[e] = *reinterpret_cast<const typename Pack<T, V>::type *>(x + (int64_t)(r < last ? r : last) * ld);
+        }
+    }
+    SEQ_DEV void get(int e, float (&v)[V]) const
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = pack_get<T, V>(q[e], i);
+    }
+};
+
 template <typename T, int V> __global__ void __launch_bounds__(256) gnorm_apply_kernel(NormParams p)
 {
-    __shared__ float mean[256], rstd[256];
     const NormShare s = norm_share<V>(p, blockIdx.x);
-    norm_statistics(p, s, mean, rstd);
-    __syncthreads();
-    const int64_t first = s.slab * p.slab;
+    const int64_t first = s.first + s.r0;
+    Batch<T, V> vb, zb;
     for (int col = s.col; col < s.wide; col += 256) {
         const int64_t at = (int64_t)s.g0 * p.C + col * V;
-        const float m = mean[col / s.cv], r = rstd[col / s.cv];
+        const float *mo = p.moments + (s.n * p.G + s.g0 + col / s.cv) * 2;
+        const float m = mo[0], r = mo[1];
         float w[V], b[V];
         norm_weights<T, V>(p, at, w, b);
         const T *x = (const T *)p.x + s.row0 * p.x_ld + at, *zg = (const T *)p.gate + s.row0 * p.gate_ld + at;
         T *yg = (T *)p.y + s.row0 * p.y_ld + at;
-        for (int64_t row = first + s.r0; row < s.last; row += kNormBatch * s.step) {
-            float v[kNormBatch][V], z[kNormBatch][V];
-#pragma unroll
-            for (int e = 0; e < kNormBatch; ++e) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) v[e][i] = z[e][i] = 0.0f;
-                const int64_t at_row = row + e * s.step;
-                if (at_row < s.live) {
-                    load_f32<T, V>(x + at_row * p.x_ld, v[e]);
-                    if (p.gate) load_f32<T, V>(zg + at_row * p.gate_ld, z[e]);
-                }
-            }
+        for (int64_t row = first; row < s.last; row += kNormBatch * s.step) {
+            vb.load(x, p.x_ld, row, s.step, s.live);
+            if (p.gate) zb.load(zg, p.gate_ld, row, s.step, s.live);
 #pragma unroll
             for (int e = 0; e < kNormBatch; ++e) {
                 const int64_t at_row = row + e * s.step;
                 if (at_row >= s.last) continue;
-                float y[V];
+                float v[V], z[V], y[V];
+                vb.get(e, v);
+                if (p.gate) zb.get(e, z);
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[e][i] = fmaf((v[e][i] - m) * r, w[i], b[i]);
-                norm_out<T, V>(p, v[e], z[e], y);
+                for (int i = 0; i < V; ++i) v[i] = fmaf((v[i] - m) * r, w[i], b[i]);
+                norm_out<T, V>(p, v, z, y);
                 if (at_row >= s.live)
 #pragma unroll
                     for (int i = 0; i < V; ++i) y[i] = 0.0f;
@@ -353,11 +390,11 @@ SEQ_DEV void norm_back(const NormParams &p, const float (&xhat)[V], const float 
 
 template <typename T, int V> __global__ void __launch_bounds__(256) gnorm_sums_kernel(NormParams p)
 {
-    __shared__ float mean[256], rstd[256], part[2][256 * V];
+    __shared__ float part[2][256 * V];
     const NormShare s = norm_share<V>(p, blockIdx.x);
-    norm_statistics(p, s, mean, rstd);
-    __syncthreads();
-    const int64_t first = s.slab * p.slab, W = (int64_t)p.G * p.C;
+    const int64_t first = s.first + s.r0;
+    Batch<T, V> vb, zb, db;
+    const int64_t W = (int64_t)p.G * p.C;
     float *out = p.sums + (s.n * p.slabs + s.slab) * 2 * W + (int64_t)s.g0 * p.C;
     double whole[2] = {0.0, 0.0};           // of the one group of a wide row
     const int turns = s.wide <= 256 ? 1 : (s.wide + 255) / 256;
@@ -368,34 +405,29 @@ template <typename T, int V> __global__ void __launch_bounds__(256) gnorm_sums_k
 #pragma unroll
         for (int i = 0; i < V; ++i) sd[i] = sx[i] = w[i] = 0.0f;
         if (col < s.wide) {
-            const float m = mean[col / s.cv], r = rstd[col / s.cv];
+            const float *mo = p.moments + (s.n * p.G + s.g0 + col / s.cv) * 2;
+            const float m = mo[0], r = mo[1];
             norm_weights<T, V>(p, at, w, b);
             const T *x = (const T *)p.x + s.row0 * p.x_ld + at, *zg = (const T *)p.gate + s.row0 * p.gate_ld + at;
             const T *dg = (const T *)p.dy + s.row0 * p.dy_ld + at;
-            for (int64_t row = first + s.r0; row < s.live; row += kNormBatch * s.step) {
-                float v[kNormBatch][V], z[kNormBatch][V], dy[kNormBatch][V];
-#pragma unroll
-                for (int e = 0; e < kNormBatch; ++e) {
-                    const int64_t at_row = row + e * s.step;
-#pragma unroll
-                    for (int i = 0; i < V; ++i) v[e][i] = z[e][i] = dy[e][i] = 0.0f;
-                    if (at_row < s.live) {
-                        load_f32<T, V>(x + at_row * p.x_ld, v[e]);
-                        load_f32<T, V>(dg + at_row * p.dy_ld, dy[e]);
-                        if (p.gate) load_f32<T, V>(zg + at_row * p.gate_ld, z[e]);
-                    }
-                }
+            for (int64_t row = first; row < s.live; row += kNormBatch * s.step) {
+                vb.load(x, p.x_ld, row, s.step, s.live);
+                db.load(dg, p.dy_ld, row, s.step, s.live);
+                if (p.gate) zb.load(zg, p.gate_ld, row, s.step, s.live);
 #pragma unroll
                 for (int e = 0; e < kNormBatch; ++e) {
                     if (row + e * s.step >= s.live) continue;
-                    float d[V], dz[V];
+                    float v[V], z[V], dy[V], d[V], dz[V];
+                    vb.get(e, v);
+                    db.get(e, dy);
+                    if (p.gate) zb.get(e, z);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) v[e][i] = (v[e][i] - m) * r;
-                    norm_back<T, V>(p, v[e], w, b, z[e], dy[e], d, dz);
+                    for (int i = 0; i < V; ++i) v[i] = (v[i] - m) * r;
+                    norm_back<T, V>(p, v, w, b, z, dy, d, dz);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         sd[i] += d[i];
-                        sx[i] = fmaf(d[i], v[e][i], sx[i]);
+                        sx[i] = fmaf(d[i], v[i], sx[i]);
                     }
                 }
             }
@@ -440,8 +472,8 @@ template <typename T, int V> __global__ void __launch_bounds__(256) gnorm_sums_k
         for (int g = threadIdx.x >> 4; g < s.ng; g += 16) {
             double a = 0.0, b = 0.0;
             for (int i = threadIdx.x & 15; i < p.C; i += 16) a += (double)part[0][g * p.C + i], b += (double)part[1][g * p.C + i];
-            a = row16_sum(a);
-            b = row16_sum(b);
+            a = lanes_sum64<16>(a);
+            b = lanes_sum64<16>(b);
             if ((threadIdx.x & 15) == 0) group[2 * g] = (float)a, group[2 * g + 1] = (float)b;
         }
     } else {                                // one group
@@ -452,94 +484,82 @@ template <typename T, int V> __global__ void __launch_bounds__(256) gnorm_sums_k
         if (threadIdx.x < 16) {
             double a = 0.0, b = 0.0;
             for (int i = threadIdx.x; i < 256; i += 16) a += both[0][i], b += both[1][i];
-            a = row16_sum(a);
-            b = row16_sum(b);
+            a = lanes_sum64<16>(a);
+            b = lanes_sum64<16>(b);
             if (threadIdx.x == 0) group[0] = (float)a, group[1] = (float)b;
         }
     }
 }
 
-// dw and dbias of 16 channels: the sums of `n` slabs, by 16 threads each
+// dw and dbias of 16 channels: the sums of `n` slabs
 template <typename T> SEQ_DEV void norm_reduce(const NormParams &p, int64_t block, int64_t n)
 {
-    __shared__ double part[2][16][17];
+    constexpr int ROWS = kReduceThreads / 16;
+    __shared__ double part[2][ROWS][17];
     const int c = threadIdx.x & 15, l = threadIdx.x >> 4;
     const int64_t W = (int64_t)p.G * p.C, ch = block * 16 + c;
     double d = 0.0, x = 0.0;
-    if (ch < W)
-        for (int64_t i = l; i < n; i += 16) {
-            d += (double)p.sums[i * 2 * W + ch];
-            x += (double)p.sums[(i * 2 + 1) * W + ch];
+    if (ch < W) {
+        const float *sums = p.sums + ch;
+#pragma unroll 4
+        for (int64_t i = l; i < n; i += ROWS) {
+            d += (double)sums[i * 2 * W];
+            x += (double)sums[(i * 2 + 1) * W];
         }
+    }
     part[0][l][c] = d;
     part[1][l][c] = x;
     __syncthreads();
-    if (l == 0 && ch < W) {
-        d = x = 0.0;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) d += part[0][e][c], x += part[1][e][c];
-        ((T *)p.dw)[ch] = (T)(float)x;
-        if (p.dbias) ((T *)p.dbias)[ch] = (T)(float)d;
+    for (int half = ROWS / 2; half > 0; half >>= 1) {
+        if (l < half) {
+            part[0][l][c] += part[0][l + half][c];
+            part[1][l][c] += part[1][l + half][c];
+        }
+        __syncthreads();
     }
+    if (l == 0 && ch < W) {
+        ((T *)p.dw)[ch] = (T)(float)part[1][0][c];
+        if (p.dbias) ((T *)p.dbias)[ch] = (T)(float)part[0][0][c];
+    }
+}
+
+// what the slabs' sums make: of the groups, and dw and dbias
+template <typename T> __global__ void __launch_bounds__(kReduceThreads) gnorm_join_sums_kernel(NormParams p)
+{
+    if (blockIdx.x >= p.reduce_from) norm_reduce<T>(p, blockIdx.x - p.reduce_from, p.samples * p.slabs);
+    else norm_join<true>(p, blockIdx.x);
 }
 
 template <typename T, int V> __global__ void __launch_bounds__(256) gnorm_grad_kernel(NormParams p)
 {
-    __shared__ float mean[256], rstd[256], m1[256], m2[256];
-    if (blockIdx.x >= p.reduce_from) return norm_reduce<T>(p, blockIdx.x - p.reduce_from, p.samples * p.slabs);
     const NormShare s = norm_share<V>(p, blockIdx.x);
-    norm_statistics(p, s, mean, rstd);
-    {
-        const double n = (double)norm_rows(p, s.n) * p.C;
-        for (int g = threadIdx.x >> 4; g < s.ng; g += 16) {
-            double a = 0.0, b = 0.0;
-            for (int64_t i = threadIdx.x & 15; i < p.slabs; i += 16) {
-                const float *o = p.group + ((s.n * p.slabs + i) * p.G + s.g0 + g) * 2;
-                a += (double)o[0];
-                b += (double)o[1];
-            }
-            a = row16_sum(a);
-            b = row16_sum(b);
-            if ((threadIdx.x & 15) == 0) {
-                m1[g] = p.center && n > 0.0 ? (float)(a / n) : 0.0f;
-                m2[g] = n > 0.0 ? (float)(b / n) : 0.0f;
-            }
-        }
-    }
-    __syncthreads();
-    const int64_t first = s.slab * p.slab;
+    const int64_t first = s.first + s.r0;
+    Batch<T, V> vb, zb, db;
     for (int col = s.col; col < s.wide; col += 256) {
-        const int64_t at = (int64_t)s.g0 * p.C + col * V;
-        const int g = col / s.cv;
-        const float m = mean[g], r = rstd[g], a1 = m1[g], a2 = m2[g];
+        const int64_t at = (int64_t)s.g0 * p.C + col * V, g = s.n * p.G + s.g0 + col / s.cv;
+        const float m = p.moments[g * 2], r = p.moments[g * 2 + 1], a1 = p.pulls[g * 2], a2 = p.pulls[g * 2 + 1];
         float w[V], b[V];
         norm_weights<T, V>(p, at, w, b);
         const T *x = (const T *)p.x + s.row0 * p.x_ld + at, *zg = (const T *)p.gate + s.row0 * p.gate_ld + at;
         const T *dg = (const T *)p.dy + s.row0 * p.dy_ld + at;
         T *dx = (T *)p.dx + s.row0 * p.dx_ld + at, *dzg = (T *)p.dgate + s.row0 * p.dgate_ld + at;
-        for (int64_t row = first + s.r0; row < s.last; row += kNormBatch * s.step) {
-            float v[kNormBatch][V], z[kNormBatch][V], dy[kNormBatch][V];
-#pragma unroll
-            for (int e = 0; e < kNormBatch; ++e) {
-                const int64_t at_row = row + e * s.step;
-#pragma unroll
-                for (int i = 0; i < V; ++i) v[e][i] = z[e][i] = dy[e][i] = 0.0f;
-                if (at_row < s.live) {
-                    load_f32<T, V>(x + at_row * p.x_ld, v[e]);
-                    load_f32<T, V>(dg + at_row * p.dy_ld, dy[e]);
-                    if (p.gate) load_f32<T, V>(zg + at_row * p.gate_ld, z[e]);
-                }
-            }
+        for (int64_t row = first; row < s.last; row += kNormBatch * s.step) {
+            vb.load(x, p.x_ld, row, s.step, s.live);
+            db.load(dg, p.dy_ld, row, s.step, s.live);
+            if (p.gate) zb.load(zg, p.gate_ld, row, s.step, s.live);
 #pragma unroll
             for (int e = 0; e < kNormBatch; ++e) {
                 const int64_t at_row = row + e * s.step;
                 if (at_row >= s.last) continue;
-                float d[V], dz[V];
+                float v[V], z[V], dy[V], d[V], dz[V];
+                vb.get(e, v);
+                db.get(e, dy);
+                if (p.gate) zb.get(e, z);
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[e][i] = (v[e][i] - m) * r;
-                norm_back<T, V>(p, v[e], w, b, z[e], dy[e], d, dz);
+                for (int i = 0; i < V; ++i) v[i] = (v[i] - m) * r;
+                norm_back<T, V>(p, v, w, b, z, dy, d, dz);
 #pragma unroll
-                for (int i = 0; i < V; ++i) d[i] = r * (fmaf(d[i], w[i], -a1) - v[e][i] * a2);
+                for (int i = 0; i < V; ++i) d[i] = r * (fmaf(d[i], w[i], -a1) - v[i] * a2);
                 if (at_row >= s.live)
 #pragma unroll
                     for (int i = 0; i < V; ++i) d[i] = dz[i] = 0.0f;
@@ -764,7 +784,7 @@ template <typename T, int V, int R> __global__ void __launch_bounds__(256) gnorm
     }
 }
 
-template <typename T> __global__ void __launch_bounds__(256) gnorm_reduce_kernel(NormParams p)
+template <typename T> __global__ void __launch_bounds__(kReduceThreads) gnorm_reduce_kernel(NormParams p)
 {
     norm_reduce<T>(p, blockIdx.x, p.slabs);
 }
