@@ -485,54 +485,66 @@ template <typename T, int SP> __global__ void __launch_bounds__(SP <= 64 ? 256 :
         const int64_t wide = (int64_t)(h1 - h0) * p.P;
         for (int64_t e = threadIdx.x; e < (all - live) * wide; e += NW * 64)
             ((T *)p.dv)[(row0 + live + e / wide) * p.dv_ld + (int64_t)h0 * p.P + e % wide] = (T)0.0f;
+        for (int e = threadIdx.x; e < (all - live) * p.S; e += NW * 64) {
+            const int64_t row = row0 + live + e / p.S;
+            const int key = e % p.S;
+            if (p.slices == 1) {
+                ((T *)p.dq)[row * p.dq_ld + (int64_t)grp * p.S + key] = (T)0.0f;
+                ((T *)p.dk)[row * p.dk_ld + (int64_t)grp * p.S + key] = (T)0.0f;
+            } else {
+                const int64_t at = (((int64_t)slice * p.N * p.L + row) * p.G + grp) * p.S + key;
+                p.part[0][at] = p.part[1][at] = 0.0f;
+            }
+        }
     }
-    f32x4 dq[CT][4], dk[CT][4];
-#pragma unroll
-    for (int x = 0; x < CT; ++x)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) dq[x][t] = dk[x][t] = f32x4{0, 0, 0, 0};
+    const int64_t part = (((int64_t)slice * p.N * p.L + row0) * p.G + grp) * p.S;
+    const uint32_t part_step = (uint32_t)(p.G * p.S) * 4;
     const char *keys = p.keys + (chunk * p.G + grp) * keys_bytes<T, SP>(true);
     const char *kt = keys + 8 * KS * kFrag<T>, *qt = kt + 4 * KS * kFrag<T>;
     // the upper triangles stay zero
     for (int e = threadIdx.x; e < kDQ * ML; e += NW * 64)
 #pragma unroll
         for (int x = 0; x < NL; ++x) sh.low[x][e] = (T)0.0f;
-    // k_i . k_j and q_i . k_j are all heads'
-    f32x4 kk[TT], qk[TT];
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-        kk[t] = qk[t] = f32x4{0, 0, 0, 0};
-        if (live == 0 || tri + t * NW >= 10) continue;
-        int it, jt;
-        triangle(tri + t * NW, it, jt);
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const typename Frag<T>::type b = get_frag<T>(keys + (jt * KS + s) * kFrag<T>, lane);
-            kk[t] = mma(get_frag<T>(keys + (it * KS + s) * kFrag<T>, lane), b, kk[t]);
-            qk[t] = mma(get_frag<T>(keys + ((4 + it) * KS + s) * kFrag<T>, lane), b, qk[t]);
-        }
-    }
     const int my_row = threadIdx.x >> 4;
     const uint32_t dy_step = (uint32_t)p.dy_ld * (uint32_t)sizeof(T), dv_step = (uint32_t)p.dv_ld * (uint32_t)sizeof(T);
-    f32x4 ry[RI], re[RI], rd[RI];       // the next block of channels: Y, E, dO
+    // The next block of channels: Y, E and dO's bits.  Rows and channels that there are none of lie behind the buffers'
+    // ends and come as zeros: a load under a branch would be waited for in it.
+    constexpr uint32_t NOWHERE = 0x80000000u;
+    f32x4 ry[RI], re[RI];
+    uint32_t rd[RI][4];
+    auto rows_of = [&](const void *t, int64_t ld, int h) {
+        return __builtin_amdgcn_make_buffer_rsrc((T *)const_cast<void *>(t) + row0 * ld + (int64_t)h * p.P, 0,
+                                                 (int)(((live - 1) * ld + p.P) * (int64_t)sizeof(T)), 0x00020000);
+    };
     auto load_rows = [&](int h, int p0) {
         const int pc = p0 + 4 * l16;
         const int64_t at = ((n * p.H + h) * p.K + c) * kDQ * p.PP;
-        const float *gy = p.rows[0] + at, *ge = p.rows[1] + at;
-        const T *gd = (const T *)p.dy + row0 * p.dy_ld + (int64_t)h * p.P;
+        const __amdgpu_buffer_rsrc_t gy = __builtin_amdgcn_make_buffer_rsrc(p.rows[0] + at, 0, live * p.PP * 4, 0x00020000);
+        const __amdgpu_buffer_rsrc_t ge = __builtin_amdgcn_make_buffer_rsrc(p.rows[1] + at, 0, live * p.PP * 4, 0x00020000);
+        const __amdgpu_buffer_rsrc_t gd = rows_of(p.dy, p.dy_ld, h);
 #pragma unroll
         for (int e = 0; e < RI; ++e) {
             const int row = my_row + e * kRowsAtOnce;
-            ry[e] = re[e] = rd[e] = f32x4{0, 0, 0, 0};
-            if (row < live && pc < p.PP) {
-                const uint32_t o = (uint32_t)(row * p.PP + pc) * 4, d = (uint32_t)row * dy_step + (uint32_t)pc * (uint32_t)sizeof(T);
-                ry[e] = *reinterpret_cast<const f32x4 *>(lane_at(gy, o));
-                re[e] = *reinterpret_cast<const f32x4 *>(lane_at(ge, o));
+            const uint32_t o = pc < p.PP ? (uint32_t)(row * p.PP + pc) * 4 : NOWHERE;
+            ry[e] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(gy, o, 0, 0));
+            re[e] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ge, o, 0, 0));
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (pc + i < p.P) rd[e][i] = (float)lane_at(gd, d)[i];
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t d = pc + i < p.P ? (uint32_t)row * dy_step + (uint32_t)(pc + i) * (uint32_t)sizeof(T) : NOWHERE;
+                if constexpr (sizeof(T) == 4) rd[e][i] = __builtin_amdgcn_raw_buffer_load_b32(gd, d, 0, 0);
+                else rd[e][i] = __builtin_amdgcn_raw_buffer_load_b16(gd, d, 0, 0);
             }
         }
+    };
+    // a head's factors of token `lane`; the first wave gives them to the others
+    float grow_of, fade_of, beta_of;
+    double cum_of;
+    auto load_scalars = [&](int h) {
+        const ChunkScalars *cs = reinterpret_cast<const ChunkScalars *>(p.heads + (chunk * p.H + h) * head_bytes<T>(true));
+        grow_of = cs->from_start[lane];
+        fade_of = cs->to_end[lane];
+        beta_of = cs->beta[lane];
+        cum_of = cs->cum[lane];
     };
     float sv[CT][8], rv[CT][8];         // the next 32 channels of S and R
     auto load_states = [&](int h, int p0) {
@@ -548,19 +560,35 @@ template <typename T, int SP> __global__ void __launch_bounds__(SP <= 64 ? 256 :
         }
     };
     if (live > 0) {
+        load_scalars(h0);
         load_rows(h0, 0);
         load_states(h0, 0);
     }
+    // k_i . k_j and q_i . k_j are all heads'
+    f32x4 kk[TT], qk[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        kk[t] = qk[t] = f32x4{0, 0, 0, 0};
+        if (live == 0 || tri + t * NW >= 10) continue;
+        int it, jt;
+        triangle(tri + t * NW, it, jt);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const typename Frag<T>::type b = get_frag<T>(keys + (jt * KS + s) * kFrag<T>, lane);
+            kk[t] = mma(get_frag<T>(keys + (it * KS + s) * kFrag<T>, lane), b, kk[t]);
+            qk[t] = mma(get_frag<T>(keys + ((4 + it) * KS + s) * kFrag<T>, lane), b, qk[t]);
+        }
+    }
     for (int h = h0; h < (live > 0 ? h1 : h0); ++h) {
-        const char *head = p.heads + (chunk * p.H + h) * head_bytes<T>(true);
-        const ChunkScalars *cs = reinterpret_cast<const ChunkScalars *>(head);
         __syncthreads();
         if (w == 0) {
-            sh.from_start[lane] = cs->from_start[lane];
-            sh.to_end[lane] = cs->to_end[lane];
-            sh.beta[lane] = cs->beta[lane];
-            sh.cum[lane] = cs->cum[lane];
+            sh.from_start[lane] = grow_of;
+            sh.to_end[lane] = fade_of;
+            sh.beta[lane] = beta_of;
+            sh.cum[lane] = cum_of;
         }
+        if (h + 1 < h1) load_scalars(h + 1);
+        const __amdgpu_buffer_rsrc_t gv = rows_of(p.dv, p.dv_ld, h);
         f32x4 by[CT][4], old[CT][4], nw[CT][4], dm[TT], wm[TT];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
@@ -583,14 +611,19 @@ template <typename T, int SP> __global__ void __launch_bounds__(SP <= 64 ? 256 :
 #pragma unroll
                 for (int i = 0; i < 4; ++i) db[e] = fmaf(re[e][i], ry[e][i], db[e]);
                 const f32x4 dv = re[e] * beta;
-                if (row < live) {
-                    T *d = lane_at((T *)p.dv + row0 * p.dv_ld + (int64_t)h * p.P, (uint32_t)row * dv_step + (uint32_t)pc * (uint32_t)sizeof(T));
+                f32x4 dy;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (pc + i < p.P) d[i] = (T)dv[i];
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t to = pc + i < p.P ? (uint32_t)row * dv_step + (uint32_t)(pc + i) * (uint32_t)sizeof(T) : NOWHERE;
+                    const uint32_t bits = sizeof(T) == 4 ? rd[e][i] : rd[e][i] << 16;
+                    dy[i] = __builtin_bit_cast(float, bits);
+                    if constexpr (sizeof(T) == 4)
+                        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, (float)dv[i]), gv, to, 0, 0);
+                    else
+                        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)dv[i]), gv, to, 0, 0);
                 }
                 const int at = row * LD + 4 * l16;
-                write_split4<1>(sh.dy + at, 0, rd[e]);
+                write_split4<1>(sh.dy + at, 0, dy);
                 write_split4<kN<T>>(sh.dv[0] + at, kDQ * LD, dv);
                 write_split4<kN<T>>(sh.u[0] + at, kDQ * LD, ry[e] * beta);
             }
@@ -651,6 +684,19 @@ template <typename T, int SP> __global__ void __launch_bounds__(SP <= 64 ? 256 :
                 }
             }
         }
+        // K^T and Q^T, under way while the pairs are summed
+        typename Frag<T>::type kf[CT][2], qf[CT][2];
+        if (cols) {
+            NEW_LANE;
+#pragma unroll
+            for (int x = 0; x < CT; ++x)
+#pragma unroll
+                for (int P = 0; P < 2; ++P) {
+                    kf[x][P] = get_frag<T>(kt + ((w * CT + x) * 2 + P) * kFrag<T>, lane);
+                    qf[x][P] = get_frag<T>(qt + ((w * CT + x) * 2 + P) * kFrag<T>, lane);
+                }
+            in_order();
+        }
         // dbeta: the 16 threads of a row
 #pragma unroll
         for (int e = 0; e < RI; ++e) {
@@ -691,7 +737,8 @@ template <typename T, int SP> __global__ void __launch_bounds__(SP <= 64 ? 256 :
             if (q == 0) sh.col[it][j] = down;
             in_order();
         }
-        // what the states in front and behind give, and its part in dg
+        // what the states in front and behind give (dq and dk stand where by and old did), and its part in dg
+        auto &dq = by, &dk = old;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             if (!cols) break;
@@ -704,19 +751,16 @@ template <typename T, int SP> __global__ void __launch_bounds__(SP <= 64 ? 256 :
                 by[x][t] = by[x][t] * (grow * p.scale);
                 old[x][t] = old[x][t] * grow;
                 nw[x][t] = nw[x][t] * fade;
-                const typename Frag<T>::type kf = get_frag<T>(kt + ((w * CT + x) * 2 + (t >> 1)) * kFrag<T>, lane);
-                const typename Frag<T>::type qf = get_frag<T>(qt + ((w * CT + x) * 2 + (t >> 1)) * kFrag<T>, lane);
                 f32x4 a, b;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float kv = frag_get(kf, 4 * (t & 1) + r), qv = frag_get(qf, 4 * (t & 1) + r);
+                    const float kv = frag_get(kf[x][t >> 1], 4 * (t & 1) + r), qv = frag_get(qf[x][t >> 1], 4 * (t & 1) + r);
                     a[r] = by[x][t][r] * qv - old[x][t][r] * kv;
                     b[r] = nw[x][t][r] * kv;
                 }
                 front += row_sum4<double>(a, lane);
                 behind += row_sum4<double>(b, lane);
-                dq[x][t] = dq[x][t] + by[x][t];
-                dk[x][t] = dk[x][t] + (nw[x][t] - old[x][t]);
+                dk[x][t] = nw[x][t] - old[x][t];
                 in_order();
             }
             if ((l16 & 3) == 0) {
@@ -733,16 +777,13 @@ template <typename T, int SP> __global__ void __launch_bounds__(SP <= 64 ? 256 :
             for (int P = 0; P < 2; ++P) {
                 if (!cols) continue;
                 NEW_LANE;
-                Split<T, 1> kf, qf;
-                kf.f[0] = get_frag<T>(kt + ((w * CT + x) * 2 + P) * kFrag<T>, lane);
-                qf.f[0] = get_frag<T>(qt + ((w * CT + x) * 2 + P) * kFrag<T>, lane);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
 #pragma unroll
                     for (int e = 0; e < NL; ++e) {
-                        if (P <= t / 2) dq[x][t] = mma(read_rows_stacked(sh.low[e], ML, 16 * t, 32 * P, lane), kf.f[0], dq[x][t]);
-                        dk[x][t] = mma(read_rows_stacked(sh.sym[e], ML, 16 * t, 32 * P, lane), kf.f[0], dk[x][t]);
-                        if (P >= t / 2) dk[x][t] = mma(read_cols_stacked(sh.low[e], ML, 32 * P, 16 * t, lane), qf.f[0], dk[x][t]);
+                        if (P <= t / 2) dq[x][t] = mma(read_rows_stacked(sh.low[e], ML, 16 * t, 32 * P, lane), kf[x][P], dq[x][t]);
+                        dk[x][t] = mma(read_rows_stacked(sh.sym[e], ML, 16 * t, 32 * P, lane), kf[x][P], dk[x][t]);
+                        if (P >= t / 2) dk[x][t] = mma(read_cols_stacked(sh.low[e], ML, 32 * P, 16 * t, lane), qf[x][P], dk[x][t]);
                     }
                     in_order();
                 }
@@ -765,30 +806,34 @@ template <typename T, int SP> __global__ void __launch_bounds__(SP <= 64 ? 256 :
             // no gradient by a decay that is zero
             if (lane < live) p.dg[(row0 + lane) * p.dg_ld + h] = exp2_fast((float)step) == 0.0f ? 0.0f : (float)dg;
         }
-    }
-    // dq and dk: of this call, or of a slice's heads
-    const int64_t part = (((int64_t)slice * p.N * p.L + row0) * p.G + grp) * p.S;
-    const uint32_t part_step = (uint32_t)(p.G * p.S) * 4;
+        // dq and dk: the sums over the slice's heads wait in the workspace, where a lane finds its own again (held in
+        // registers they would leave the products above too few), and behind the last head go to the outputs, or stay
+        // for the sum over the slices
+        const bool out = h + 1 == h1 && p.slices == 1;
 #pragma unroll
-    for (int x = 0; x < CT; ++x) {
-        const int b = w * CT + x, key = 32 * (b >> 1) + 4 * (b & 1) + key0;
-        if (!cols || key >= p.S) continue;
+        for (int x = 0; x < CT; ++x) {
+            NEW_LANE;
+            const int b = w * CT + x, key = 32 * (b >> 1) + 4 * (b & 1) + 8 * (l16 >> 2) + (l16 & 3);
+            if (!cols || key >= p.S) continue;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * t + q4 + r;
-                if (row >= all) continue;
-                const float vq = row < live ? dq[x][t][r] : 0.0f, vk = row < live ? dk[x][t][r] : 0.0f;
-                if (p.slices == 1) {
-                    const uint32_t k = (uint32_t)key * (uint32_t)sizeof(T);
-                    *lane_at((T *)p.dq + row0 * p.dq_ld + (int64_t)grp * p.S, (uint32_t)row * (uint32_t)p.dq_ld * (uint32_t)sizeof(T) + k) = (T)vq;
-                    *lane_at((T *)p.dk + row0 * p.dk_ld + (int64_t)grp * p.S, (uint32_t)row * (uint32_t)p.dk_ld * (uint32_t)sizeof(T) + k) = (T)vk;
-                } else {
-                    *lane_at(p.part[0] + part, (uint32_t)row * part_step + (uint32_t)key * 4) = vq;
-                    *lane_at(p.part[1] + part, (uint32_t)row * part_step + (uint32_t)key * 4) = vk;
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * t + q4 + r;
+                    if (row >= live) continue;
+                    float *sq = lane_at(p.part[0] + part, (uint32_t)row * part_step + (uint32_t)key * 4);
+                    float *sk = lane_at(p.part[1] + part, (uint32_t)row * part_step + (uint32_t)key * 4);
+                    const float vq = dq[x][t][r] + (h > h0 ? *sq : 0.0f), vk = dk[x][t][r] + (h > h0 ? *sk : 0.0f);
+                    if (out) {
+                        const uint32_t k = (uint32_t)key * (uint32_t)sizeof(T);
+                        *lane_at((T *)p.dq + row0 * p.dq_ld + (int64_t)grp * p.S, (uint32_t)row * (uint32_t)p.dq_ld * (uint32_t)sizeof(T) + k) = (T)vq;
+                        *lane_at((T *)p.dk + row0 * p.dk_ld + (int64_t)grp * p.S, (uint32_t)row * (uint32_t)p.dk_ld * (uint32_t)sizeof(T) + k) = (T)vk;
+                    } else {
+                        *sq = vq;
+                        *sk = vk;
+                    }
                 }
-            }
+        }
     }
 }
 #undef NEW_LANE

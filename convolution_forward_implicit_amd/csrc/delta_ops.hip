@@ -162,7 +162,7 @@ conv_status_t conv_delta_create(const conv_delta_desc_t *desc, conv_delta_plan_t
     pl->o_bwd_heads = o;
     o += up(d.N * pl->K * d.H * head_of(d, true));
     const int64_t states = up(d.N * d.H * pl->K * pl->PP * pl->SP * 4), tokens = up(d.N * d.H * pl->K * kDQ * pl->PP * 4);
-    const int64_t part = pl->grad_slices > 1 ? up((int64_t)pl->grad_slices * d.N * d.L * d.G * d.S * 4) : 0;
+    const int64_t part = hpg > 1 ? up((int64_t)pl->grad_slices * d.N * d.L * d.G * d.S * 4) : 0;
     for (int k = 0; k < 2; ++k) {
         pl->o_bound[k] = o + k * states;
         pl->o_rows[k] = o + 2 * states + k * tokens;
