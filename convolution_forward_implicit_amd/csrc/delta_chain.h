@@ -22,7 +22,7 @@ enum ChainMode { CHAIN_Y, CHAIN_STATES, CHAIN_BACK };
 
 constexpr int kHelpers = 4;
 
-template <typename T, int SP, ChainMode MODE> struct ChainShared {
+template <typename T, int SP, ChainMode MODE, int CB> struct ChainShared {
     static constexpr int KS = SP / 32, NT = kN<T>, NM = kM<T>;
     static constexpr int KEYS = 4 * KS * kFrag<T>, TRI = kTri * NT * kFrag<T>, OPS = KEYS + kRows + TRI;
     struct Exchange {
@@ -33,11 +33,12 @@ template <typename T, int SP, ChainMode MODE> struct ChainShared {
         f32x4 in[2][4][64];             // V (M^T dO) of this chunk and the next
         f32x4 ds[MODE == CHAIN_BACK ? SP / 16 : 0][64];                 // scale (e^c dO)^T Q
     };
+    static constexpr int LEFT = 160 * 1024 - CB * (int)sizeof(Exchange);
     // chunks of K and N: the one in use and those under way
-    static constexpr int NB = (160 * 1024 - (int)sizeof(Exchange)) / OPS >= 3 ? 3 : (160 * 1024 - (int)sizeof(Exchange)) / OPS;
+    static constexpr int NB = LEFT / OPS >= 3 ? 3 : LEFT / OPS;
     static constexpr int LEAST = KEYS / 1024 / kHelpers + TRI / 1024 / kHelpers;     // loads of a chunk that every helper starts
     __align__(16) char ops[NB][OPS];
-    __align__(16) Exchange x;
+    __align__(16) Exchange x[CB];
 };
 
 // KB kilobytes of memory to LDS, by the helpers.  The loads are written out: the
@@ -149,16 +150,16 @@ template <int KS> SEQ_DEV Frag<float>::type get_transposed(const char *at, int P
     return f;
 }
 
-template <typename T, int SP, ChainMode MODE>
-SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, MODE> &sh)
+template <typename T, int SP, ChainMode MODE, int CB>
+SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, MODE, CB> &sh)
 {
-    typedef ChainShared<T, SP, MODE> Shared;
+    typedef ChainShared<T, SP, MODE, CB> Shared;
     constexpr bool GRAD = MODE != CHAIN_Y, BACK = MODE == CHAIN_BACK;
     constexpr int KS = SP / 32, NT = kN<T>, NM = kM<T>, NB = Shared::NB, KEYS = Shared::KEYS, F = kFrag<T>;
     constexpr int OWN = (KS + 3) / 4;                   // key blocks that a wave may hold
     const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q4 = (lane >> 4) * 4;
     const int64_t nh = unit / p.blocks, n = nh / p.H;
-    const int h = (int)(nh - n * p.H), grp = h / (p.H / p.G), ch = (int)(unit - nh * p.blocks) * 16 + l16;
+    const int h = (int)(nh - n * p.H), grp = h / (p.H / p.G), ch0 = (int)(unit - nh * p.blocks) * 16 * CB + l16;
     const int64_t len = seq_len(p.lengths, n, p.L);
     const int live = (int)((len + kDQ - 1) / kDQ);
     const char *keys = p.keys + (n * p.K * p.G + grp) * keys_bytes<T, SP>(GRAD), *heads = p.heads + (n * p.K * p.H + h) * head_bytes<T>(GRAD);
@@ -167,9 +168,9 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
     auto chunk = [&](int i) { return BACK ? live - 1 - i : i; };
     const int t = w & 3;
     // rows 16 t .. of this chunk
-    auto rows_of = [&](const void *x, int64_t ld, int i, int tile) {
+    auto rows_of = [&](const void *x, int64_t ld, int i, int tile, int c) {
         const int64_t t0 = (int64_t)chunk(i) * kDQ + 16 * tile;
-        return LaneRows<T>((const T *)x + (int64_t)h * p.P, ld, n * p.L + t0, (int)(len - t0 < 16 ? len - t0 : 16), p.P, ch, lane);
+        return LaneRows<T>((const T *)x + (int64_t)h * p.P, ld, n * p.L + t0, (int)(len - t0 < 16 ? len - t0 : 16), p.P, ch0 + 16 * c, lane);
     };
     if (w >= 4) {
         auto load = [&](int i) {
@@ -185,7 +186,7 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
         constexpr int NQ = BACK ? 4 * OWN : MODE == CHAIN_Y ? KS : 0, TM = BACK ? NT : MODE == CHAIN_Y ? NM : 0;
         typename Frag<T>::type qf[NQ + 1];
         Split<T, TM + 1> mf[2];
-        uint32_t vb[16];                // the next dO, or v
+        uint32_t vb[CB][16];            // the next dO, or v
         auto load_q = [&](int i) {
             const char *k = keys + chunk(i) * keys_step;
             if (MODE == CHAIN_Y && p.direct) {
@@ -223,65 +224,81 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
                 }
         };
         auto load_v = [&](int i) {
-            const LaneRows<T> rows = rows_of(p.v, p.v_ld, i, t);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) vb[r] = rows.bits(r);
+            for (int c = 0; c < CB; ++c) {
+                const LaneRows<T> rows = rows_of(p.v, p.v_ld, i, t, c);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) vb[c][r] = rows.bits(r);
+            }
         };
         auto put_v = [&](int i) {
-            f32x4 v;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const uint32_t b = vb[r];
-                v[r] = __builtin_bit_cast(float, b);
+            for (int c = 0; c < CB; ++c) {
+                f32x4 v;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint32_t b = vb[c][r];
+                    v[r] = __builtin_bit_cast(float, b);
+                }
+                sh.x[c].in[i & 1][t][lane] = v;
             }
-            sh.x.in[i & 1][t][lane] = v;
         };
-        f32x4 dy[4];
+        f32x4 dy[CB][4];
         auto load_dy = [&](int i) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const LaneRows<T> rows = rows_of(p.dy, p.dy_ld, i, e);
+            for (int c = 0; c < CB; ++c)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) vb[4 * e + r] = rows.bits(r);
-            }
+                for (int e = 0; e < 4; ++e) {
+                    const LaneRows<T> rows = rows_of(p.dy, p.dy_ld, i, e, c);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) vb[c][4 * e + r] = rows.bits(r);
+                }
         };
         auto take_dy = [&]() {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const uint32_t b = vb[e];
-                dy[e / 4][e % 4] = __builtin_bit_cast(float, b);
-            }
+            for (int c = 0; c < CB; ++c)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const uint32_t b = vb[c][e];
+                    dy[c][e / 4][e % 4] = __builtin_bit_cast(float, b);
+                }
         };
         auto put_du = [&](int i) {      // M^T dO of chunk i, whose dO is in dy
-            Split<T, 1> d[2];
-            stack(dy[0], dy[1], d[0]);
-            stack(dy[2], dy[3], d[1]);
-            f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
 #pragma unroll
-            for (int P = 0; P < 2; ++P)
-                if (P >= t / 2) {
+            for (int c = 0; c < CB; ++c) {
+                Split<T, 1> d[2];
+                stack(dy[c][0], dy[c][1], d[0]);
+                stack(dy[c][2], dy[c][3], d[1]);
+                f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
 #pragma unroll
-                    for (int e = TM - 1; e >= 0; --e) acc[P] = mma(mf[P].f[e], d[P].f[0], acc[P]);
-                }
-            sh.x.in[i & 1][t][lane] = acc[0] + acc[1];
+                for (int P = 0; P < 2; ++P)
+                    if (P >= t / 2) {
+#pragma unroll
+                        for (int e = TM - 1; e >= 0; --e) acc[P] = mma(mf[P].f[e], d[P].f[0], acc[P]);
+                    }
+                sh.x[c].in[i & 1][t][lane] = acc[0] + acc[1];
+            }
         };
         // y's part by the chunk's own tokens, and its rows
-        auto put_y = [&](int i, f32x4 y) {
-            f32x4 acc[2] = {y, f32x4{0, 0, 0, 0}};
+        auto put_y = [&](int i, const f32x4 (&y)[CB]) {
 #pragma unroll
-            for (int P = 0; P < 2; ++P)
-                if (P <= t / 2) {
-                    Split<T, NM> b;
-                    get_split(sh.x.y[i & 1] + P * F, 2 * F, lane, b);
+            for (int c = 0; c < CB; ++c) {
+                f32x4 acc[2] = {y[c], f32x4{0, 0, 0, 0}};
 #pragma unroll
-                    for (int e = 0; e < NM; ++e)
+                for (int P = 0; P < 2; ++P)
+                    if (P <= t / 2) {
+                        Split<T, NM> b;
+                        get_split(sh.x[c].y[i & 1] + P * F, 2 * F, lane, b);
 #pragma unroll
-                        for (int k = 0; k < NM - e; ++k) acc[P] = mma(mf[P].f[e], b.f[k], acc[P]);
-                }
-            const LaneRows<T> rows = rows_of(p.y, p.y_ld, i, t);
-            y = acc[0] + acc[1];
+                        for (int e = 0; e < NM; ++e)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) rows.put(e, y[e]);
+                            for (int k = 0; k < NM - e; ++k) acc[P] = mma(mf[P].f[e], b.f[k], acc[P]);
+                    }
+                const LaneRows<T> rows = rows_of(p.y, p.y_ld, i, t, c);
+                const f32x4 sum = acc[0] + acc[1];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) rows.put(e, sum[e]);
+            }
         };
         if (NB > 1 && live > 0) load(0);
         if (NB > 2 && live > 1) load(1);
@@ -299,7 +316,7 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
                 if (live > 1) load_v(1);
             }
         }
-        f32x4 y = {0, 0, 0, 0};
+        f32x4 y[CB], last[CB];
         for (int i = 0; i < live; ++i) {
             const ChunkScalars *cs = reinterpret_cast<const ChunkScalars *>(sh.ops[i % NB] + KEYS);
             if (NB == 1) {
@@ -309,22 +326,25 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
             // This chunk's K and N are there.  Behind their loads came those of the next one's and, at least, Q, v and
             // a block of M (going back a block of M^T and dO), which may be under way.
             if (NB < 3 || i == 0 || i + 1 >= live) wait_vmcnt<0>();
-            else wait_vmcnt<(MODE == CHAIN_Y ? NQ + TM + 4 : BACK ? TM + 16 : 4) + Shared::LEAST>();
+            else wait_vmcnt<(MODE == CHAIN_Y ? NQ + TM + 4 * CB : BACK ? TM + 16 * CB : 4 * CB) + Shared::LEAST>();
             meet();
             if (NB == 2 && i + 1 < live) load(i + 1);
             // a chunk's y is finished while the next one is under way
             if constexpr (MODE == CHAIN_Y) {
-                const f32x4 last = y;
                 const f32x4 grow = *reinterpret_cast<const f32x4 *>(cs->from_start + 16 * t + q4);
-                f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    Split<T, NM> b;
-                    get_split(sh.x.s + s * F, KS * F, lane, b);
+                for (int c = 0; c < CB; ++c) {
+                    last[c] = y[c];
+                    f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
 #pragma unroll
-                    for (int e = 0; e < NM; ++e) acc[s & 1] = mma(qf[s], b.f[e], acc[s & 1]);
+                    for (int s = 0; s < KS; ++s) {
+                        Split<T, NM> b;
+                        get_split(sh.x[c].s + s * F, KS * F, lane, b);
+#pragma unroll
+                        for (int e = 0; e < NM; ++e) acc[s & 1] = mma(qf[s], b.f[e], acc[s & 1]);
+                    }
+                    y[c] = (acc[0] + acc[1]) * (grow * p.scale);
                 }
-                y = (acc[0] + acc[1]) * (grow * p.scale);
                 if (i + 1 < live) load_q(i + 1);
                 meet();
                 if (i + 1 < live) put_v(i + 1);
@@ -336,23 +356,26 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
             }
             if constexpr (BACK) {
                 // (scale e^c dO)^T Q for the states of wave t
-                Split<T, NT> x[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    dy[e] = dy[e] * (*reinterpret_cast<const f32x4 *>(cs->from_start + 16 * e + q4) * p.scale);
-                stack(dy[0], dy[1], x[0]);
-                stack(dy[2], dy[3], x[1]);
+                for (int c = 0; c < CB; ++c) {
+                    Split<T, NT> x[2];
 #pragma unroll
-                for (int o = 0; o < OWN; ++o) {
-                    if (t + 4 * o >= KS) continue;
+                    for (int e = 0; e < 4; ++e)
+                        dy[c][e] = dy[c][e] * (*reinterpret_cast<const f32x4 *>(cs->from_start + 16 * e + q4) * p.scale);
+                    stack(dy[c][0], dy[c][1], x[0]);
+                    stack(dy[c][2], dy[c][3], x[1]);
 #pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+                    for (int o = 0; o < OWN; ++o) {
+                        if (t + 4 * o >= KS) continue;
 #pragma unroll
-                        for (int e = NT - 1; e >= 0; --e)
+                        for (int a = 0; a < 2; ++a) {
+                            f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
 #pragma unroll
-                            for (int P = 0; P < 2; ++P) acc[P] = mma(qf[4 * o + 2 * a + P], x[P].f[e], acc[P]);
-                        sh.x.ds[2 * (t + 4 * o) + a][lane] = acc[0] + acc[1];
+                            for (int e = NT - 1; e >= 0; --e)
+#pragma unroll
+                                for (int P = 0; P < 2; ++P) acc[P] = mma(qf[4 * o + 2 * a + P], x[P].f[e], acc[P]);
+                            sh.x[c].ds[2 * (t + 4 * o) + a][lane] = acc[0] + acc[1];
+                        }
                     }
                 }
                 if (i + 1 < live) load_q(i + 1);
@@ -374,115 +397,129 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
             }
         }
         if (MODE == CHAIN_Y && live > 0) put_y(live - 1, y);
-        if (MODE == CHAIN_Y && ch < p.P)
+        for (int ch = ch0; MODE == CHAIN_Y && ch < p.P && ch < ch0 + 16 * CB; ch += 16)
             for (int64_t r = len + 4 * t + (lane >> 4); r < p.L; r += 16) ((T *)p.y)[(n * p.L + r) * p.y_ld + (int64_t)h * p.P + ch] = (T)0.0f;
         return;
     }
-    f32x4 st[OWN][2];
+    f32x4 st[CB][OWN][2];
     auto state_at = [&](int o, int a, int r) { return 32 * (t + 4 * o) + 2 * q4 + 4 * a + r; };      // the key
-    {
-        const float *from = BACK ? p.dstate_out : p.state;
-        const float *g = from + (nh * p.P + ch) * p.S;
+    const float *from = BACK ? p.dstate_out : p.state;
+#pragma unroll
+    for (int c = 0; c < CB; ++c) {
+        const float *g = from + (nh * p.P + ch0 + 16 * c) * p.S;
 #pragma unroll
         for (int o = 0; o < OWN; ++o)
 #pragma unroll
             for (int a = 0; a < 2; ++a)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) st[o][a][r] = from && ch < p.P && state_at(o, a, r) < p.S ? g[state_at(o, a, r)] : 0.0f;
+                for (int r = 0; r < 4; ++r)
+                    st[c][o][a][r] = from && ch0 + 16 * c < p.P && state_at(o, a, r) < p.S ? g[state_at(o, a, r)] : 0.0f;
     }
-    auto put_state = [&]() {
+    auto put_state = [&](int c) {
 #pragma unroll
         for (int o = 0; o < OWN; ++o) {
             if (t + 4 * o >= KS) continue;
             Split<T, NT> s;
-            stack(st[o][0], st[o][1], s);
+            stack(st[c][o][0], st[c][o][1], s);
 #pragma unroll
-            for (int e = 0; e < NT; ++e) put_frag(sh.x.s + (e * KS + t + 4 * o) * F, lane, s.f[e]);
+            for (int e = 0; e < NT; ++e) put_frag(sh.x[c].s + (e * KS + t + 4 * o) * F, lane, s.f[e]);
         }
     };
-    if (live > 0) put_state();
+    if (live > 0)
+#pragma unroll
+        for (int c = 0; c < CB; ++c) put_state(c);
     for (int i = 0; i < live; ++i) {
         const char *ops = sh.ops[i % NB], *tr = ops + KEYS + kRows;
         const ChunkScalars *cs = reinterpret_cast<const ChunkScalars *>(ops + KEYS);
         const int64_t at = nh * p.K + chunk(i);
         if (NB == 1) meet();
         meet();
-        // K S0^T, a sum of each term by itself
-        Split<T, NT> sp[KS];
-        typename Frag<T>::type kf[KS];
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            kf[s] = get_frag<T>(ops + (t * KS + s) * F, lane);
-            get_split(sh.x.s + s * F, KS * F, lane, sp[s]);
-        }
         const f32x4 grow = *reinterpret_cast<const f32x4 *>(cs->from_start + 16 * t + q4);
         const f32x4 fade = *reinterpret_cast<const f32x4 *>(cs->to_end + 16 * t + q4);
         const f32x4 beta = *reinterpret_cast<const f32x4 *>(cs->beta + 16 * t + q4);
         const float total = cs->from_start[kDQ - 1];
-        const f32x4 in = sh.x.in[i & 1][t][lane];
-        // what the next products read of K and N, so that no wait for it stands in front of a barrier
+        typename Frag<T>::type kf[KS];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) kf[s] = get_frag<T>(ops + (t * KS + s) * F, lane);
         Split<T, NT> nf[2];
-#pragma unroll
-        for (int P = 0; P < 2; ++P)
-            if (BACK ? P >= t / 2 : P <= t / 2) get_split(tr + (BACK ? upper(t, P) : lower(t, P)) * NT * F, F, lane, nf[P]);
         typename Frag<T>::type kt[OWN][2][2];
+        f32x4 z[CB];
 #pragma unroll
-        for (int o = 0; o < OWN; ++o)
-            if (t + 4 * o < KS)
+        for (int c = 0; c < CB; ++c) {
+            // K S0^T, a sum of each term by itself
+            Split<T, NT> sp[KS];
 #pragma unroll
-                for (int a = 0; a < 2; ++a)
+            for (int s = 0; s < KS; ++s) get_split(sh.x[c].s + s * F, KS * F, lane, sp[s]);
+            const f32x4 in = sh.x[c].in[i & 1][t][lane];
+            if (c == 0) {
+                // what the next products read of K and N, so that no wait for it stands in front of a barrier
 #pragma unroll
-                    for (int P = 0; P < 2; ++P) kt[o][a][P] = get_transposed<KS>(ops, P, t + 4 * o, a, lane, T());
-        f32x4 r[NT], z;
+                for (int P = 0; P < 2; ++P)
+                    if (BACK ? P >= t / 2 : P <= t / 2) get_split(tr + (BACK ? upper(t, P) : lower(t, P)) * NT * F, F, lane, nf[P]);
 #pragma unroll
-        for (int e = 0; e < NT; ++e) r[e] = f32x4{0, 0, 0, 0};
+                for (int o = 0; o < OWN; ++o)
+                    if (t + 4 * o < KS)
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
+                        for (int a = 0; a < 2; ++a)
 #pragma unroll
-            for (int e = 0; e < NT; ++e) r[e] = mma(kf[s], sp[s].f[e], r[e]);
+                            for (int P = 0; P < 2; ++P) kt[o][a][P] = get_transposed<KS>(ops, P, t + 4 * o, a, lane, T());
+            }
+            f32x4 r[NT];
 #pragma unroll
-        for (int e = NT - 1; e > 0; --e) r[e - 1] = r[e - 1] + r[e];
-        z = BACK ? in + r[0] * fade : in - grow * r[0];         // dU, Z
-        put_half<T, NT>(sh.x.a, t, lane, z);
-        if constexpr (GRAD) {
-            float *b = p.bound[BACK] + (at * p.PP + ch) * SP + 2 * q4;
+            for (int e = 0; e < NT; ++e) r[e] = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int o = 0; o < OWN; ++o)
-                if (t + 4 * o < KS)
+            for (int s = 0; s < KS; ++s)
 #pragma unroll
-                    for (int a = 0; a < 2; ++a) *reinterpret_cast<f32x4 *>(b + 32 * (t + 4 * o) + 4 * a) = st[o][a];
+                for (int e = 0; e < NT; ++e) r[e] = mma(kf[s], sp[s].f[e], r[e]);
+#pragma unroll
+            for (int e = NT - 1; e > 0; --e) r[e - 1] = r[e - 1] + r[e];
+            z[c] = BACK ? in + r[0] * fade : in - grow * r[0];          // dU, Z
+            put_half<T, NT>(sh.x[c].a, t, lane, z[c]);
+            if constexpr (GRAD) {
+                float *b = p.bound[BACK] + (at * p.PP + ch0 + 16 * c) * SP + 2 * q4;
+#pragma unroll
+                for (int o = 0; o < OWN; ++o)
+                    if (t + 4 * o < KS)
+#pragma unroll
+                        for (int a = 0; a < 2; ++a) *reinterpret_cast<f32x4 *>(b + 32 * (t + 4 * o) + 4 * a) = st[c][o][a];
+            }
         }
         meet();
-        // N (beta Z); sums that do not wait for each other
-        f32x4 acc[2][2] = {{z, f32x4{0, 0, 0, 0}}, {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}}};
 #pragma unroll
-        for (int P = 0; P < 2; ++P)
-            if (BACK ? P >= t / 2 : P <= t / 2) {
-                Split<T, NT> b;
-                get_split(sh.x.a + P * F, 2 * F, lane, b);
+        for (int c = 0; c < CB; ++c) {
+            // N (beta Z); sums that do not wait for each other
+            f32x4 acc[2][2] = {{z[c], f32x4{0, 0, 0, 0}}, {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}}};
 #pragma unroll
-                for (int e = NT - 1; e >= 0; --e)
+            for (int P = 0; P < 2; ++P)
+                if (BACK ? P >= t / 2 : P <= t / 2) {
+                    Split<T, NT> b;
+                    get_split(sh.x[c].a + P * F, 2 * F, lane, b);
 #pragma unroll
-                    for (int k = 0; k < NT - e; ++k) acc[P][e + k < NT - 1] = mma(nf[P].f[e], b.f[k], acc[P][e + k < NT - 1]);
-            }
-        z = (acc[0][0] + acc[1][0]) + (acc[0][1] + acc[1][1]);
-        put_half<T, NT>(sh.x.b, t, lane, z * (BACK ? beta * grow * -1.0f : beta * fade));
-        if constexpr (MODE == CHAIN_Y) put_half<T, NM>(sh.x.y[i & 1], t, lane, z);
+                    for (int e = NT - 1; e >= 0; --e)
+#pragma unroll
+                        for (int k = 0; k < NT - e; ++k) acc[P][e + k < NT - 1] = mma(nf[P].f[e], b.f[k], acc[P][e + k < NT - 1]);
+                }
+            z[c] = (acc[0][0] + acc[1][0]) + (acc[0][1] + acc[1][1]);
+            put_half<T, NT>(sh.x[c].b, t, lane, z[c] * (BACK ? beta * grow * -1.0f : beta * fade));
+            if constexpr (MODE == CHAIN_Y) put_half<T, NM>(sh.x[c].y[i & 1], t, lane, z[c]);
+        }
         meet();
         // the state behind the chunk
-        if (t < KS) {
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+            if (t >= KS) break;
             Split<T, NT> u[2];
 #pragma unroll
-            for (int P = 0; P < 2; ++P) get_split(sh.x.b + P * F, 2 * F, lane, u[P]);
+            for (int P = 0; P < 2; ++P) get_split(sh.x[c].b + P * F, 2 * F, lane, u[P]);
             f32x4 sums[OWN][2][2];
 #pragma unroll
             for (int o = 0; o < OWN; ++o)
 #pragma unroll
                 for (int a = 0; a < 2; ++a) {
-                    sums[o][a][0] = st[o][a] * total;
+                    sums[o][a][0] = st[c][o][a] * total;
                     sums[o][a][1] = f32x4{0, 0, 0, 0};
                     if constexpr (BACK) {
-                        if (t + 4 * o < KS) sums[o][a][1] = sh.x.ds[2 * (t + 4 * o) + a][lane];
+                        if (t + 4 * o < KS) sums[o][a][1] = sh.x[c].ds[2 * (t + 4 * o) + a][lane];
                     }
                 }
 #pragma unroll
@@ -498,48 +535,57 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
 #pragma unroll
             for (int o = 0; o < OWN; ++o)
 #pragma unroll
-                for (int a = 0; a < 2; ++a) st[o][a] = sums[o][a][0] + sums[o][a][1];
-            put_state();
+                for (int a = 0; a < 2; ++a) st[c][o][a] = sums[o][a][0] + sums[o][a][1];
+            put_state(c);
         }
         if constexpr (GRAD) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) p.rows[BACK][(at * kDQ + 16 * t + q4 + e) * p.PP + ch] = z[e];
+            for (int c = 0; c < CB; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p.rows[BACK][(at * kDQ + 16 * t + q4 + e) * p.PP + ch0 + 16 * c] = z[c][e];
         }
     }
     float *to = BACK ? p.dstate : p.state_out;
-    if (to && ch < p.P)
 #pragma unroll
-        for (int o = 0; o < OWN; ++o)
+    for (int c = 0; c < CB; ++c)
+        if (to && ch0 + 16 * c < p.P)
 #pragma unroll
-            for (int a = 0; a < 2; ++a)
+            for (int o = 0; o < OWN; ++o)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (t + 4 * o < KS && state_at(o, a, e) < p.S) to[(nh * p.P + ch) * p.S + state_at(o, a, e)] = st[o][a][e];
+                for (int a = 0; a < 2; ++a)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (t + 4 * o < KS && state_at(o, a, e) < p.S)
+                            to[(nh * p.P + ch0 + 16 * c) * p.S + state_at(o, a, e)] = st[c][o][a][e];
 }
 
 constexpr int kChainThreads = 64 * (4 + kHelpers);
 
-template <typename T, int SP> __global__ void __launch_bounds__(kChainThreads) delta_y_kernel(DeltaParams p)
+// Blocks of 16 channels that a workgroup may have: two where the exchange of both leaves
+// room for a chunk of K and N.
+template <typename T, int SP> constexpr int kMostBlocks = SP <= 128 ? 2 : 1;
+
+template <typename T, int SP, int CB> __global__ void __launch_bounds__(kChainThreads) delta_y_kernel(DeltaParams p)
 {
-    __shared__ ChainShared<T, SP, CHAIN_Y> sh;
+    __shared__ ChainShared<T, SP, CHAIN_Y, CB> sh;
     const int64_t units = (int64_t)p.N * p.H * p.blocks, unit = unit_of(blockIdx.x, units);
-    if (unit < units) delta_chain<T, SP, CHAIN_Y>(p, unit, sh);
+    if (unit < units) delta_chain<T, SP, CHAIN_Y, CB>(p, unit, sh);
 }
 
 // The two passes over the states of a gradient, which do not depend on each other.
-template <typename T, int SP> __global__ void __launch_bounds__(kChainThreads) delta_states_kernel(DeltaParams p)
+template <typename T, int SP, int CB> __global__ void __launch_bounds__(kChainThreads) delta_states_kernel(DeltaParams p)
 {
     __shared__ union Both {
-        ChainShared<T, SP, CHAIN_STATES> ahead;
-        ChainShared<T, SP, CHAIN_BACK> back;
+        ChainShared<T, SP, CHAIN_STATES, CB> ahead;
+        ChainShared<T, SP, CHAIN_BACK, CB> back;
         SEQ_DEV Both() {}
     } sh;
     const int64_t units = (int64_t)p.N * p.H * p.blocks, half = gridDim.x / 2;
     const bool back = blockIdx.x < half;
     const int64_t unit = unit_of(back ? blockIdx.x : blockIdx.x - half, units);
     if (unit >= units) return;
-    if (back) delta_chain<T, SP, CHAIN_BACK>(p, unit, sh.back);
-    else delta_chain<T, SP, CHAIN_STATES>(p, unit, sh.ahead);
+    if (back) delta_chain<T, SP, CHAIN_BACK, CB>(p, unit, sh.back);
+    else delta_chain<T, SP, CHAIN_STATES, CB>(p, unit, sh.ahead);
 }
 
 }  // namespace convfwd

@@ -460,7 +460,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(SP <= 64 ? 256 :
     constexpr int kRowsAtOnce = NW * 4, RI = kDQ / kRowsAtOnce;     // 16 threads take a row of PB channels
     __shared__ __align__(16) GradShared<T, SP> sh;
     const int lane0 = threadIdx.x & 63, w = wave_id();
-    const int lane = lane0, l16 = lane & 15, q = lane >> 4, q4 = q * 4;
+    const int lane = lane0, l16 = lane & 15, q = lane >> 4;
     // a phase takes its lane anew, so that its LDS addresses (beyond an instruction's offset) are not all computed
     // before the loop over the heads and held
 #define NEW_LANE const int lane = fresh_vector(lane0), l16 = lane & 15, q = lane >> 4, q4 = q * 4; (void)lane, (void)l16, (void)q, (void)q4

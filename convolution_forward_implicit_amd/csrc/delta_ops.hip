@@ -4,6 +4,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <new>
+#include <type_traits>
 
 #include "../../include/convfwd.h"
 #include "delta_chain.h"
@@ -42,22 +43,44 @@ int64_t head_of(const conv_delta_desc_t &d, bool grad)
 
 int64_t state_grid(int64_t units) { return (units + 7) / 8 * 8; }
 
-template <typename T, int SP> void launch_fwd(const DeltaParams &p, int64_t units, hipStream_t s)
+// A workgroup takes one block of 16 channels, or two where there would be more
+// workgroups than compute units, each of which holds one: both blocks go through the
+// chunk's barriers and share its loads of K and N.  bf16, 128 keys: 512 blocks of
+// 4096 tokens 254 -> 190 us, both directions of 256 blocks of 2048 153 -> 131; where there
+// are compute units for every block one takes 127 us, half as many workgroups 190.
+template <typename T, int SP, typename F> void paired(DeltaParams &p, int directions, F launch)
+{
+    if constexpr (kMostBlocks<T, SP> == 2) {
+        if ((double)directions * p.N * p.H * p.blocks > 256) {
+            p.blocks = (p.blocks + 1) / 2;
+            return launch(std::integral_constant<int, 2>());
+        }
+    }
+    launch(std::integral_constant<int, 1>());
+}
+
+template <typename T, int SP> void launch_fwd(DeltaParams p, hipStream_t s)
 {
     if (p.K > 0)
         hipLaunchKernelGGL((delta_prepare_kernel<T, SP, false>), dim3((unsigned)((int64_t)p.N * p.K * p.G * p.slices)), dim3(256),
                            0, s, p);
-    hipLaunchKernelGGL((delta_y_kernel<T, SP>), dim3((unsigned)state_grid(units)), dim3(kChainThreads), 0, s, p);
+    paired<T, SP>(p, 1, [&](auto cb) {
+        hipLaunchKernelGGL((delta_y_kernel<T, SP, decltype(cb)::value>), dim3((unsigned)state_grid((int64_t)p.N * p.H * p.blocks)),
+                           dim3(kChainThreads), 0, s, p);
+    });
 }
 
 // The gradient: what chunks do without their states, both passes over the states,
 // the gradients of the chunks and, where a group's heads are sliced, their sums.
 template <typename T, int SP> void launch_bwd(DeltaParams p, const conv_delta_plan &pl, hipStream_t s)
 {
-    const int64_t chunks = (int64_t)p.N * p.K * p.G, units = (int64_t)p.N * p.H * p.blocks;
+    const int64_t chunks = (int64_t)p.N * p.K * p.G;
     if (p.K > 0)
         hipLaunchKernelGGL((delta_prepare_kernel<T, SP, true>), dim3((unsigned)(chunks * p.slices)), dim3(256), 0, s, p);
-    hipLaunchKernelGGL((delta_states_kernel<T, SP>), dim3((unsigned)(2 * state_grid(units))), dim3(kChainThreads), 0, s, p);
+    paired<T, SP>(p, 2, [&](auto cb) {
+        hipLaunchKernelGGL((delta_states_kernel<T, SP, decltype(cb)::value>),
+                           dim3((unsigned)(2 * state_grid((int64_t)p.N * p.H * p.blocks))), dim3(kChainThreads), 0, s, p);
+    });
     if (p.K == 0) return;
     p.slices = pl.grad_slices;
     p.heads_per_slice = pl.grad_heads;
@@ -71,7 +94,7 @@ template <typename T, int SP> void launch_bwd(DeltaParams p, const conv_delta_pl
 template <typename T, int SP> void launch_delta(const DeltaParams &p, const conv_delta_plan &pl, bool grad, hipStream_t s)
 {
     if (grad) launch_bwd<T, SP>(p, pl, s);
-    else launch_fwd<T, SP>(p, (int64_t)p.N * p.H * p.blocks, s);
+    else launch_fwd<T, SP>(p, s);
 }
 
 template <typename T> void launch_delta(const DeltaParams &p, const conv_delta_plan &pl, bool grad, hipStream_t s)
