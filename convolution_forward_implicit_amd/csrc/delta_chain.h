@@ -43,7 +43,9 @@ template <typename T, int SP, ChainMode MODE, int CB> struct ChainShared {
 
 // KB kilobytes of memory to LDS, by the helpers.  The loads are written out: the
 // compiler, which cannot see what they write, would wait for them before any read of
-// LDS.
+// LDS.  K and Q come as the preparation laid them out: from their rows, 64 bytes of
+// each at a time, y took 128 us instead of 110 (32 heads, 4096 tokens) and the
+// preparation 31 instead of 32.
 template <int KB> SEQ_DEV void fetch(const char *from, char *to, int wave, int lane)
 {
     const i32x4_t buf = uniform_rsrc(buffer_rsrc(from, KB * 1024));
@@ -55,25 +57,6 @@ template <int KB> SEQ_DEV void fetch(const char *from, char *to, int wave, int l
         if (KB % kHelpers == 0 || e + wave < KB)
             asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds\n\ts_mov_b32 m0, %0"
                          : "=&s"(saved) : "s"(at + b), "v"(lane * 16), "s"(buf), "s"(b) : "memory");
-    }
-}
-// K's operands from its rows in memory, of a group's 64 x SP keys: rows at `rows` and
-// behind come as zeros.
-template <typename T, int SP> SEQ_DEV void fetch_keys(const T *from, int64_t ld, int rows, char *to, int wave, int lane)
-{
-    constexpr int KS = SP / 32, HALVES = sizeof(T) / 2;      // loads of an operand
-    const uint32_t step = (uint32_t)ld * (uint32_t)sizeof(T);
-    const i32x4_t buf = uniform_rsrc(buffer_rsrc(from, (uint32_t)((rows - 1) * (int)step + SP * (int)sizeof(T))));
-    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)to);
-    const uint32_t mine = (uint32_t)(lane & 15) * step + (uint32_t)(lane >> 4) * 8 * sizeof(T);
-#pragma unroll
-    for (int e = 0; e < 4 * KS * HALVES; e += kHelpers) {
-        const uint32_t b = (uint32_t)(e + wave), op = b / HALVES;
-        uint32_t saved;
-        asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
-                     : "=&s"(saved)
-                     : "s"(at + b * 1024), "v"(mine + op / KS * 16 * step + op % KS * 32 * (uint32_t)sizeof(T) + b % HALVES * 16), "s"(buf)
-                     : "memory");
     }
 }
 // The workgroup's waves meet; LDS writes are done, loads may be under way.
@@ -175,11 +158,7 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
     if (w >= 4) {
         auto load = [&](int i) {
             const char *k = keys + chunk(i) * keys_step, *a = heads + chunk(i) * head_step;
-            if (!GRAD && p.direct)
-                fetch_keys<T, SP>((const T *)p.k + (n * p.L + (int64_t)chunk(i) * kDQ) * p.k_ld + (int64_t)grp * p.S, p.k_ld,
-                                  (int)(len - (int64_t)chunk(i) * kDQ < kDQ ? len - (int64_t)chunk(i) * kDQ : kDQ), sh.ops[i % NB], t, lane);
-            else
-                fetch<KEYS / 1024>(k, sh.ops[i % NB], t, lane);
+            fetch<KEYS / 1024>(k, sh.ops[i % NB], t, lane);
             fetch<kRows / 1024>(a, sh.ops[i % NB] + KEYS, t, lane);
             fetch<Shared::TRI / 1024>(a + tri, sh.ops[i % NB] + KEYS + kRows, t, lane);
         };
@@ -189,24 +168,6 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
         uint32_t vb[CB][16];            // the next dO, or v
         auto load_q = [&](int i) {
             const char *k = keys + chunk(i) * keys_step;
-            if (MODE == CHAIN_Y && p.direct) {
-                const int64_t t0 = (int64_t)i * kDQ + 16 * t;
-                const uint32_t step = (uint32_t)p.q_ld * (uint32_t)sizeof(T);
-                const int left = (int)(len - t0 < 16 ? len - t0 : 16);
-                const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(
-                    (T *)const_cast<void *>(p.q) + (n * p.L + t0) * p.q_ld + (int64_t)grp * p.S, 0,
-                    left > 0 ? (left - 1) * (int)step + SP * (int)sizeof(T) : 0, 0x00020000);
-                const uint32_t at = (uint32_t)l16 * step + (uint32_t)(lane >> 4) * 8 * (uint32_t)sizeof(T);
-#pragma unroll
-                for (int s = 0; s < NQ; ++s) {
-                    u32x4 v[sizeof(T) / 2];
-#pragma unroll
-                    for (int e = 0; e < (int)sizeof(T) / 2; ++e)
-                        v[e] = __builtin_amdgcn_raw_buffer_load_b128(buf, at + (uint32_t)(s * 32 * (int)sizeof(T) + 16 * e), 0, 0);
-                    qf[s] = __builtin_bit_cast(typename Frag<T>::type, v);
-                }
-                return;
-            }
 #pragma unroll
             for (int s = 0; s < NQ; ++s) {
                 if (!BACK) qf[s] = get_frag<T>(k + ((4 + t) * KS + s) * F, lane);

@@ -53,7 +53,7 @@ struct DeltaParams {
     int64_t q_ld, k_ld, v_ld, g_ld, beta_ld, y_ld;
     int64_t L;
     int N, H, P, G, S, K;       // K: chunks of a sequence
-    int vec, direct, slices, heads_per_slice, blocks;       // blocks: of 16 channels of a head
+    int vec, slices, heads_per_slice, blocks;       // blocks: of 16 channels of a head
     float scale;
     char *keys, *heads;         // workspace: operands of a group's keys and of a head, by chunk
     // gradient
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(256, SP <= 128 ? 2 : 1) delta_prepare_kernel(D
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
         const typename Frag<T>::type bk = read_rows(in.k, LD, 16 * w, 32 * s, lane), bq = read_rows(in.q, LD, 16 * w, 32 * s, lane);
-        if (slice == 0 && !p.direct) {
+        if (slice == 0) {
             put_frag(out + (w * KS + s) * kFrag<T>, lane, bk);
             put_frag(out + (4 * KS + w * KS + s) * kFrag<T>, lane, bq);
         }

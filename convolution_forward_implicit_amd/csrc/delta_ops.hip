@@ -283,7 +283,6 @@ static conv_status_t delta_forward_call(const conv_delta_plan_t *plan, const con
     p.heads = (char *)ws + plan->o_heads;
     const Rows vec[] = {in[0], in[1]};
     p.vec = delta_vector(*plan, vec, 2);
-    p.direct = p.vec && d.S == plan->SP;
     if (!one_launch((double)state_grid(d.N * d.H * plan->blocks), kChainThreads) ||
         !one_launch((double)d.N * plan->K * d.G * plan->slices, 256))
         return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");

@@ -1,6 +1,6 @@
 """The gated delta rule on the GPU at the sizes that take its other forms: more blocks of
-channels than compute units, rows of keys read where they lie, several heads of a
-group in a workgroup, offsets past 32 bits, two calls at a time.  Reference and
+channels than compute units, keys as wide as their operands, several heads of a group
+in a workgroup, offsets past 32 bits, two calls at a time.  Reference and
 tolerances are those of the tests of the smaller sizes.
 """
 import pytest
@@ -49,9 +49,9 @@ def test_gradient_of_shared_keys(case, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("S", [32, 64, 128, 256])
-def test_keys_where_they_lie(S, dtype):
-    """Keys as wide as their operands and aligned, as columns of one tensor, against the same with a key fewer of
-    zeros; NaN behind the lengths."""
+def test_aligned_keys(S, dtype):
+    """Keys as wide as their operands, as columns of one tensor, aligned and not: the same numbers; NaN behind the
+    lengths."""
     N, L, H, P, G = 3, 150, 4, 24, 2
     a, s0, _ = _case(N, L, H, P, G, S, dtype, True, None, 3 + S)
     n = torch.tensor([150, 0, 71], dtype=torch.int32)
@@ -66,7 +66,6 @@ def test_keys_where_they_lie(S, dtype):
     got = _plan(N, L, H, P, G, S, dtype)(**v, state=s0.to(DEV), lengths=n.to(DEV), state_out=out)
     _near(got, y, my, HALF[dtype], C, "y")
     _near(out, last, ms, HALF["f32"], C, "state_out")
-    # not aligned: through the copies of the operands, the same numbers
     w = torch.cat([torch.zeros(N, L, 1, dtype=TYPE[dtype], device=DEV), u], -1)
     v["q"], v["k"] = (t.unflatten(-1, (G, S)) for t in w[..., 1:].split([G * S, G * S], -1))
     assert torch.equal(got, _plan(N, L, H, P, G, S, dtype)(**v, state=s0.to(DEV), lengths=n.to(DEV)))
