@@ -29,12 +29,15 @@
 //
 // delta_prepare_kernel does what a chunk can do without its state and leaves the
 // operands of the matrix instructions in the workspace, each as the 64 lanes
-// load it.  delta_state_kernel then carries 16 channels of one head's state
-// through the sequence: one wave, nothing shared, no barrier.  The results of
+// load it; the passes over the chunks follow in delta_chain.h.  The results of
 // one product are the operand of the next as they stand: two results of 16 rows
 // are an operand of a reduction over 32 (tokens 4q..4q+3 and 16+4q..16+4q+3 of
 // lane group q), and the rows of K^T are taken in such an order that the states
 // come out as 8 consecutive keys, which K's and Q's rows hold.
+//
+// Measured in bf16, heads of 128 channels and 128 keys, 4096 tokens: preparation 32 us
+// (32 heads on 16 of keys; 95 MB, 3 TB/s, two workgroups a compute unit), y 110 us, 1.7 us
+// a chunk; gradient (16 heads) preparation 35, states 138, chunks 150 us.
 #pragma once
 
 #include "seq_frags.h"
@@ -391,6 +394,12 @@ SEQ_DEV int64_t unit_of(int64_t block, int64_t units)
 // blocks of 16 keys, in the order of K^T's operands, and reads S and R itself, a step
 // ahead: no other wave needs them.  dO, dV and U go through LDS, split into their terms
 // once, their rows fetched a block of channels ahead.
+//
+// 1024 chunks of 128 channels and keys in bf16 take 150 us: 320 KB a chunk, 2.2 TB/s.  With
+// one workgroup of eight waves a compute unit (256 registers a thread, 126 KB of LDS) the
+// first loads of a chunk, 15 of its 37 us, run beside nothing; with 256 keys the sums
+// of three products leave too few registers and some 600 bytes a lane go to scratch
+// memory.
 template <typename T, int SP> struct GradShape {
     static constexpr int NW = SP <= 64 ? 4 : 8;                      // waves
     static constexpr int CT = SP / 16 < NW ? 1 : SP / 16 / NW;
@@ -856,7 +865,8 @@ template <typename T> __global__ void __launch_bounds__(256) delta_reduce_kernel
 // ---- one token -----------------------------------------------------------------------
 // With s = S k, o = S q of the old state and d = k . q, all in one pass over it:
 // y = v - e^g s, the output scale (e^g o + beta d y), the new state e^g S + beta y k^T.
-// A lane holds four keys of kDeltaRows channels; `lpr` lanes share a channel.
+// A lane holds four keys of kDeltaRows channels; `lpr` lanes share a channel.  64 sequences
+// of 32 heads, 128 x 128: 56 us, 4.8 TB/s of states read and written.
 constexpr int kDeltaRows = 4;
 
 template <typename T, bool VEC> __global__ void __launch_bounds__(256) delta_step_kernel(DeltaParams p, int lpr, int blocks)

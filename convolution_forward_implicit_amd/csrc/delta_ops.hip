@@ -46,8 +46,8 @@ int64_t state_grid(int64_t units) { return (units + 7) / 8 * 8; }
 // A workgroup takes one block of 16 channels, or two where there would be more
 // workgroups than compute units, each of which holds one: both blocks go through the
 // chunk's barriers and share its loads of K and N.  bf16, 128 keys: 512 blocks of
-// 4096 tokens 254 -> 190 us, both directions of 256 blocks of 2048 153 -> 131; where there
-// are compute units for every block one takes 127 us, half as many workgroups 190.
+// 4096 tokens 243 -> 181 us, both directions of 256 blocks of 2048 157 -> 138; where there
+// are compute units for every block a block each takes 110 us, two blocks each 181.
 template <typename T, int SP, typename F> void paired(DeltaParams &p, int directions, F launch)
 {
     if constexpr (kMostBlocks<T, SP> == 2) {

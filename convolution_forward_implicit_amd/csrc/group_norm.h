@@ -17,12 +17,14 @@
 // weights it loads once, and steps over the slab's rows.  The first pass leaves each
 // slab's mean and sum of squares around it, which gnorm_join makes a group's: a launch
 // more, but joined by every workgroup of the next pass they took longer than its rows
-// (8 x 3136 x 256 channels: 14 us where 6 are left).  The gradient's second pass leaves
+// (8 x 3136 x 256 channels in bf16: 14 us where 7.5 are left; in all 6.4 + 3.5 + 7.5, a pass over
+// 26 MB at the rate of a large copy 5.2).  The gradient's second pass leaves
 // sum d and sum d xhat of every channel of a slab: dw, db and both of a group's sums
 // come from these.
 //
 // Of each token by itself (gnorm_token, gnorm_token_grad): `lanes` lanes hold a group
-// in registers, so everything is read once.
+// in registers, so everything is read once: 4096 x 32 heads of 128 with a gate in bf16,
+// 101 MB in 20.4 us, 4.9 TB/s, a large copy's rate.
 //
 // Numbers.  Squares are summed around a mean that is near theirs, never as mean of
 // squares less square of mean: a thread takes the mean of a batch of values it holds
