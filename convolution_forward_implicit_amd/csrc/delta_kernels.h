@@ -37,7 +37,7 @@
 //
 // Measured in bf16, heads of 128 channels and 128 keys, 4096 tokens: preparation 32 us
 // (32 heads on 16 of keys; 95 MB, 3 TB/s, two workgroups a compute unit), y 110 us, 1.7 us
-// a chunk; gradient (16 heads) preparation 35, states 138, chunks 150 us.
+// a chunk; gradient (16 heads) preparation 38, states 140, chunks 139 us.
 #pragma once
 
 #include "seq_frags.h"
@@ -73,8 +73,12 @@ struct DeltaParams {
 
 // ---- operands in the workspace -------------------------------------------------
 template <typename T> constexpr int kFrag = 64 * 8 * (int)sizeof(T);
-// K (4 x SP/32), Q (the same) and, for the gradient, K^T and Q^T (SP/16 x 2)
-template <typename T, int SP> constexpr int64_t keys_bytes(bool grad) { return (int64_t)(grad ? 4 : 2) * (SP / 8) * kFrag<T>; }
+// K (4 x SP/32), Q (the same) and, for the gradient, K^T and Q^T (SP/16 x 2), k_i . k_j and q_i . k_j in fp32
+template <typename T, int SP> constexpr int64_t frags_bytes(bool grad) { return (int64_t)(grad ? 4 : 2) * (SP / 8) * kFrag<T>; }
+template <typename T, int SP> constexpr int64_t keys_bytes(bool grad)
+{
+    return frags_bytes<T, SP>(grad) + (grad ? 2 * kDQ * kDQ * 4 : 0);
+}
 // what a head adds: -N beta of three terms, M beta of two; gradient: -N beta, (-beta N)^T and M^T of three terms
 template <typename T> constexpr int kN = 3;
 template <> constexpr int kN<float> = 1;
@@ -237,6 +241,12 @@ __global__ void __launch_bounds__(256, SP <= 128 ? 2 : 1) delta_prepare_kernel(D
             put_frag(out + (12 * KS + f) * kFrag<T>, lane, read_keys(in.q, LD, 32 * (f & 1), f >> 2, f >> 1 & 1, lane));
         }
     const int i = 16 * w + l16;
+    if (GRAD && slice == 0) {
+        f32x4 *dots = reinterpret_cast<f32x4 *>(out + frags_bytes<T, SP>(true)) + i * (kDQ / 4) + (lane >> 4);
+#pragma unroll
+        for (int J = 0; J < 4; ++J)
+            if (J <= w) dots[4 * J] = kk[J], dots[kDQ * kDQ / 4 + 4 * J] = kq[J];
+    }
     for (int h = h0; h < h1; ++h) {
         char *at = p.heads + (chunk * p.H + h) * head_bytes<T>(GRAD);
         {
@@ -395,11 +405,13 @@ SEQ_DEV int64_t unit_of(int64_t block, int64_t units)
 // ahead: no other wave needs them.  dO, dV and U go through LDS, split into their terms
 // once, their rows fetched a block of channels ahead.
 //
-// 1024 chunks of 128 channels and keys in bf16 take 150 us: 320 KB a chunk, 2.2 TB/s.  With
-// one workgroup of eight waves a compute unit (256 registers a thread, 126 KB of LDS) the
-// first loads of a chunk, 15 of its 37 us, run beside nothing; with 256 keys the sums
-// of three products leave too few registers and some 600 bytes a lane go to scratch
-// memory.
+// 1024 chunks of 128 channels and keys in bf16 take 139 us: 290 KB a chunk, 2.1 TB/s.  One
+// workgroup of eight waves fits a compute unit (256 registers a thread, 126 KB of LDS).
+// A workgroup that went from chunk to chunk and loaded the next one's first rows beside
+// the last phases of this one took 147 us, its registers spilled; the products of keys
+// and queries, taken here once a chunk instead of from the preparation, 150.  With 256 keys
+// the sums of three products leave too few registers and some 650 bytes a lane go to
+// scratch memory.
 template <typename T, int SP> struct GradShape {
     static constexpr int NW = SP <= 64 ? 4 : 8;                      // waves
     static constexpr int CT = SP / 16 < NW ? 1 : SP / 16 / NW;
@@ -573,21 +585,6 @@ template <typename T, int SP> __global__ void __launch_bounds__(SP <= 64 ? 256 :
         load_rows(h0, 0);
         load_states(h0, 0);
     }
-    // k_i . k_j and q_i . k_j are all heads'
-    f32x4 kk[TT], qk[TT];
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-        kk[t] = qk[t] = f32x4{0, 0, 0, 0};
-        if (live == 0 || tri + t * NW >= 10) continue;
-        int it, jt;
-        triangle(tri + t * NW, it, jt);
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const typename Frag<T>::type b = get_frag<T>(keys + (jt * KS + s) * kFrag<T>, lane);
-            kk[t] = mma(get_frag<T>(keys + (it * KS + s) * kFrag<T>, lane), b, kk[t]);
-            qk[t] = mma(get_frag<T>(keys + ((4 + it) * KS + s) * kFrag<T>, lane), b, qk[t]);
-        }
-    }
     for (int h = h0; h < (live > 0 ? h1 : h0); ++h) {
         __syncthreads();
         if (w == 0) {
@@ -704,8 +701,21 @@ template <typename T, int SP> __global__ void __launch_bounds__(SP <= 64 ? 256 :
                     kf[x][P] = get_frag<T>(kt + ((w * CT + x) * 2 + P) * kFrag<T>, lane);
                     qf[x][P] = get_frag<T>(qt + ((w * CT + x) * 2 + P) * kFrag<T>, lane);
                 }
-            in_order();
         }
+        // and k_i . k_j, q_i . k_j
+        f32x4 kk[TT], qk[TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            if (tri + t * NW >= 10) continue;
+            NEW_LANE;
+            int it, jt;
+            triangle(tri + t * NW, it, jt);
+            const float *dots = lane_at(reinterpret_cast<const float *>(keys + frags_bytes<T, SP>(true)),
+                                        (uint32_t)((16 * it + q4) * kDQ + 16 * jt + l16) * 4);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) kk[t][r] = dots[r * kDQ], qk[t][r] = dots[kDQ * kDQ + r * kDQ];
+        }
+        in_order();
         // dbeta: the 16 threads of a row
 #pragma unroll
         for (int e = 0; e < RI; ++e) {

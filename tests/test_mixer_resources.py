@@ -28,7 +28,7 @@ KERNELS = [
     ("delta_grad_kernel<bf16_t, 64>", "DeltaParams", 0, 1),
     ("delta_grad_kernel<bf16_t, 128>", "DeltaParams", 64, 1),
     ("delta_grad_kernel<float, 128>", "DeltaParams", 96, 1),
-    ("delta_grad_kernel<bf16_t, 256>", "DeltaParams", 640, 1),
+    ("delta_grad_kernel<bf16_t, 256>", "DeltaParams", 672, 1),
     ("delta_step_kernel<bf16_t, true>", "DeltaParams, int, int", 0, 1),
     ("gnorm_sums_kernel<bf16_t, 8>", "NormParams", 0, 2),
     ("gnorm_grad_kernel<bf16_t, 8>", "NormParams", 0, 2),
