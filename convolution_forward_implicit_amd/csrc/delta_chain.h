@@ -444,7 +444,7 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
             z[c] = BACK ? in + r[0] * fade : in - grow * r[0];          // dU, Z
             put_half<T, NT>(sh.x[c].a, t, lane, z[c]);
             if constexpr (GRAD) {
-                float *b = p.bound[BACK] + (at * p.PP + ch0 + 16 * c) * SP + 2 * q4;
+                float *b = p.bound[BACK] + at * states_floats(p.PP, SP) + (int64_t)(ch0 + 16 * c) * SP + 2 * q4;
 #pragma unroll
                 for (int o = 0; o < OWN; ++o)
                     if (t + 4 * o < KS)
@@ -510,7 +510,7 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
 #pragma unroll
             for (int c = 0; c < CB; ++c)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p.rows[BACK][(at * kDQ + 16 * t + q4 + e) * p.PP + ch0 + 16 * c] = z[c][e];
+                for (int e = 0; e < 4; ++e) p.rows[BACK][at * rows_floats(p.PP) + (16 * t + q4 + e) * p.PP + ch0 + 16 * c] = z[c][e];
         }
     }
     float *to = BACK ? p.dstate : p.state_out;

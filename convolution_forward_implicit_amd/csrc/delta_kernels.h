@@ -37,7 +37,7 @@
 //
 // Measured in bf16, heads of 128 channels and 128 keys, 4096 tokens: preparation 32 us
 // (32 heads on 16 of keys; 95 MB, 3 TB/s, two workgroups a compute unit), y 110 us, 1.7 us
-// a chunk; gradient (16 heads) preparation 38, states 140, chunks 139 us.
+// a chunk; gradient (16 heads) preparation 38, states 140, chunks 135 us.
 #pragma once
 
 #include "seq_frags.h"
@@ -97,6 +97,13 @@ template <typename T> constexpr int64_t head_bytes(bool grad)
 {
     return grad ? (int64_t)sizeof(ChunkScalars) + 3 * kN<T> * kTri * kFrag<T> : kRows + (int64_t)(kN<T> + kM<T>) * kTri * kFrag<T>;
 }
+
+// The states of a chunk, and its rows, with 4 KB and 256 bytes between those of two
+// chunks: workgroups that start together would all begin in the same memory channels
+// (the gradient's chunks 140 -> 135 us).
+constexpr int kApart = 1088;
+constexpr int64_t states_floats(int PP, int SP) { return (int64_t)PP * SP + kApart; }
+constexpr int64_t rows_floats(int PP) { return (int64_t)kDQ * PP + kApart; }
 
 SEQ_DEV void put_frag(char *at, int lane, bf16x8 f) { reinterpret_cast<bf16x8 *>(at)[lane] = f; }
 SEQ_DEV void put_frag(char *at, int lane, const Frag<float>::type &f)
@@ -405,7 +412,7 @@ SEQ_DEV int64_t unit_of(int64_t block, int64_t units)
 // ahead: no other wave needs them.  dO, dV and U go through LDS, split into their terms
 // once, their rows fetched a block of channels ahead.
 //
-// 1024 chunks of 128 channels and keys in bf16 take 139 us: 290 KB a chunk, 2.1 TB/s.  One
+// 1024 chunks of 128 channels and keys in bf16 take 135 us: 290 KB a chunk, 2.2 TB/s.  One
 // workgroup of eight waves fits a compute unit (256 registers a thread, 126 KB of LDS).
 // A workgroup that went from chunk to chunk and loaded the next one's first rows beside
 // the last phases of this one took 147 us, its registers spilled; the products of keys
@@ -539,7 +546,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(SP <= 64 ? 256 :
     };
     auto load_rows = [&](int h, int p0) {
         const int pc = p0 + 4 * l16;
-        const int64_t at = ((n * p.H + h) * p.K + c) * kDQ * p.PP;
+        const int64_t at = ((n * p.H + h) * p.K + c) * rows_floats(p.PP);
         const __amdgpu_buffer_rsrc_t gy = __builtin_amdgcn_make_buffer_rsrc(p.rows[0] + at, 0, live * p.PP * 4, 0x00020000);
         const __amdgpu_buffer_rsrc_t ge = __builtin_amdgcn_make_buffer_rsrc(p.rows[1] + at, 0, live * p.PP * 4, 0x00020000);
         const __amdgpu_buffer_rsrc_t gd = rows_of(p.dy, p.dy_ld, h);
@@ -570,7 +577,7 @@ template <typename T, int SP> __global__ void __launch_bounds__(SP <= 64 ? 256 :
     float sv[CT][8], rv[CT][8];         // the next 32 channels of S and R
     auto load_states = [&](int h, int p0) {
         if (!cols) return;
-        const int64_t at = (((n * p.H + h) * p.K + c) * p.PP + p0) * SP;
+        const int64_t at = ((n * p.H + h) * p.K + c) * states_floats(p.PP, SP) + (int64_t)p0 * SP;
 #pragma unroll
         for (int x = 0; x < CT; ++x) {
             const int b = w * CT + x;

@@ -169,7 +169,7 @@ conv_status_t conv_delta_create(const conv_delta_desc_t *desc, conv_delta_plan_t
     // What neither a prompt nor a step could launch; every call checks its own form.
     const double units = (double)d.N * d.H * pl->blocks, chunks = (double)d.N * pl->K;
     const double ws = chunks * ((double)d.G * keys_of(d, pl->SP, true) + (double)d.H * head_of(d, true)) +
-                      2.0 * (double)d.N * d.H * pl->K * (d.P + 31.0) * (pl->SP + kDQ) * 4.0;
+                      2.0 * (double)d.N * d.H * pl->K * ((d.P + 31.0) * (pl->SP + kDQ) + 2.0 * kApart) * 4.0;
     if ((!one_launch(units, kChainThreads) && !one_launch((double)d.N * d.H * step_shape(d).blocks, 256)) || ws >= kMaxBytes) {
         delete pl;
         return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
@@ -184,7 +184,7 @@ conv_status_t conv_delta_create(const conv_delta_desc_t *desc, conv_delta_plan_t
     int64_t o = up(groups * keys_of(d, pl->SP, true));
     pl->o_bwd_heads = o;
     o += up(d.N * pl->K * d.H * head_of(d, true));
-    const int64_t states = up(d.N * d.H * pl->K * pl->PP * pl->SP * 4), tokens = up(d.N * d.H * pl->K * kDQ * pl->PP * 4);
+    const int64_t states = up(d.N * d.H * pl->K * states_floats(pl->PP, pl->SP) * 4), tokens = up(d.N * d.H * pl->K * rows_floats(pl->PP) * 4);
     const int64_t part = hpg > 1 ? up((int64_t)pl->grad_slices * d.N * d.L * d.G * d.S * 4) : 0;
     for (int k = 0; k < 2; ++k) {
         pl->o_bound[k] = o + k * states;
