@@ -131,7 +131,10 @@ conv_status_t run_norm(const conv_gnorm_plan &pl, NormParams &p, const Rows *vec
     p.pulls = (float *)(ws + pl.o_pulls);
     const double grid = (double)sl.count * sh.blocks * (tokens ? 1.0 : (double)pl.samples);
     const int64_t reduce = grad ? ceil_div(d.G * d.C, 16) : 0;
-    if (!one_launch(grid, 256) || !one_launch((double)reduce, kReduceThreads)) return fail(CONV_ERR_UNSUPPORTED, "N x L x G x C is too large for one launch");
+    // the sums of dw share their launch with those of the samples' groups
+    const double joins = grad && !tokens ? (double)pl.samples * d.G / (kReduceThreads / 64) + 1 : 0.0;
+    if (!one_launch(grid, 256) || !one_launch((double)reduce + joins, kReduceThreads))
+        return fail(CONV_ERR_UNSUPPORTED, "N x L x G x C is too large for one launch");
     (void)hipGetLastError();
     if (d.dtype == CONV_DT_BF16) {
         if (V == 8) launch_norm<bf16_t, 8>(p, tokens ? sh.R : 0, grad, (int64_t)grid, reduce, s);
