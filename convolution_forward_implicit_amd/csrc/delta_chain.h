@@ -13,7 +13,7 @@
 // M^T dO and Q^T dO add; their own operands (Q and M) have one reader each and go to its
 // registers.
 //
-// A chunk of 128 keys takes 1.7 us: a third of it the three splits and their way through
+// A chunk of 128 keys takes 1.85 us: a third of it the three splits and their way through
 // LDS, a quarter the matrix instructions (33 of a wave one behind the other), the rest
 // barriers and reads of LDS.  K S0^T by the keys whose state a wave holds, summed through
 // LDS instead of the state's terms read by all, took 5% less with 128 keys and 10 to 20%
@@ -30,13 +30,13 @@ enum ChainMode { CHAIN_Y, CHAIN_STATES, CHAIN_BACK };
 constexpr int kHelpers = 4;
 
 template <typename T, int SP, ChainMode MODE, int CB> struct ChainShared {
-    static constexpr int KS = SP / 32, NT = kN<T>, NM = kM<T>;
+    static constexpr int KS = SP / 32, NT = kN<T>;
     static constexpr int KEYS = 4 * KS * kFrag<T>, TRI = kTri * NT * kFrag<T>, OPS = KEYS + kRows + TRI;
     struct Exchange {
         char s[NT * KS * kFrag<T>];     // the state (its gradient)
         char a[NT * 2 * kFrag<T>];      // Z (dU)
         char b[NT * 2 * kFrag<T>];      // e^{c_Q - c} U (e^c dV)
-        char y[2][(MODE == CHAIN_Y ? NM : 0) * 2 * kFrag<T> + 16];      // Y of this chunk and the last
+        char y[2][(MODE == CHAIN_Y ? NT : 0) * 2 * kFrag<T> + 16];      // Y of this chunk and the last
         f32x4 in[2][4][64];             // V (M^T dO) of this chunk and the next
         f32x4 ds[MODE == CHAIN_BACK ? SP / 16 : 0][64];                 // scale (e^c dO)^T Q
     };
@@ -145,7 +145,7 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
 {
     typedef ChainShared<T, SP, MODE, CB> Shared;
     constexpr bool GRAD = MODE != CHAIN_Y, BACK = MODE == CHAIN_BACK;
-    constexpr int KS = SP / 32, NT = kN<T>, NM = kM<T>, NB = Shared::NB, KEYS = Shared::KEYS, F = kFrag<T>;
+    constexpr int KS = SP / 32, NT = kN<T>, NB = Shared::NB, KEYS = Shared::KEYS, F = kFrag<T>;
     constexpr int OWN = (KS + 3) / 4;                   // key blocks that a wave may hold
     const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q4 = (lane >> 4) * 4;
     const int64_t nh = unit / p.blocks, n = nh / p.H;
@@ -169,7 +169,7 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
             fetch<kRows / 1024>(a, sh.ops[i % NB] + KEYS, t, lane);
             fetch<Shared::TRI / 1024>(a + tri, sh.ops[i % NB] + KEYS + kRows, t, lane);
         };
-        constexpr int NQ = BACK ? 4 * OWN : MODE == CHAIN_Y ? KS : 0, TM = BACK ? NT : MODE == CHAIN_Y ? NM : 0;
+        constexpr int NQ = BACK ? 4 * OWN : MODE == CHAIN_Y ? KS : 0, TM = MODE == CHAIN_STATES ? 0 : NT;
         typename Frag<T>::type qf[NQ + 1];
         Split<T, TM + 1> mf[2];
         uint32_t vb[CB][16];            // the next dO, or v
@@ -188,7 +188,7 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
                 if (BACK ? P >= t / 2 : P <= t / 2) {
 #pragma unroll
                     for (int e = 0; e < TM; ++e)
-                        mf[P].f[e] = get_frag<T>(m + (BACK ? upper(t, P) * NT + e : lower(t, P) * NM + e) * F, lane);
+                        mf[P].f[e] = get_frag<T>(m + ((BACK ? upper(t, P) : lower(t, P)) * NT + e) * F, lane);
                 }
         };
         auto load_v = [&](int i) {
@@ -255,12 +255,12 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
 #pragma unroll
                 for (int P = 0; P < 2; ++P)
                     if (P <= t / 2) {
-                        Split<T, NM> b;
+                        Split<T, NT> b;
                         get_split(sh.x[c].y[i & 1] + P * F, 2 * F, lane, b);
 #pragma unroll
-                        for (int e = 0; e < NM; ++e)
+                        for (int e = 0; e < NT; ++e)
 #pragma unroll
-                            for (int k = 0; k < NM - e; ++k) acc[P] = mma(mf[P].f[e], b.f[k], acc[P]);
+                            for (int k = 0; k < NT - e; ++k) acc[P] = mma(mf[P].f[e], b.f[k], acc[P]);
                     }
                 const LaneRows<T> rows = rows_of(p.y, p.y_ld, i, t, c);
                 const f32x4 sum = acc[0] + acc[1];
@@ -297,7 +297,8 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
             else wait_vmcnt<(MODE == CHAIN_Y ? NQ + TM + 4 * CB : BACK ? TM + 16 * CB : 4 * CB) + Shared::LEAST>();
             meet();
             if (NB == 2 && i + 1 < live) load(i + 1);
-            // a chunk's y is finished while the next one is under way
+            // A chunk's y is finished while the next one is under way: beside its second product, the shortest of the
+            // three; beside the third, which all of the chain waits for, the pass took 131 us instead of 119.
             if constexpr (MODE == CHAIN_Y) {
                 const f32x4 grow = *reinterpret_cast<const f32x4 *>(cs->from_start + 16 * t + q4);
 #pragma unroll
@@ -306,10 +307,10 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
                     f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
 #pragma unroll
                     for (int s = 0; s < KS; ++s) {
-                        Split<T, NM> b;
+                        Split<T, NT> b;
                         get_split(sh.x[c].s + s * F, KS * F, lane, b);
 #pragma unroll
-                        for (int e = 0; e < NM; ++e) acc[s & 1] = mma(qf[s], b.f[e], acc[s & 1]);
+                        for (int e = 0; e < NT; ++e) acc[s & 1] = mma(qf[s], b.f[e], acc[s & 1]);
                     }
                     y[c] = (acc[0] + acc[1]) * (grow * p.scale);
                 }
@@ -469,7 +470,7 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
                 }
             z[c] = (acc[0][0] + acc[1][0]) + (acc[0][1] + acc[1][1]);
             put_half<T, NT>(sh.x[c].b, t, lane, z[c] * (BACK ? beta * grow * -1.0f : beta * fade));
-            if constexpr (MODE == CHAIN_Y) put_half<T, NM>(sh.x[c].y[i & 1], t, lane, z[c]);
+            if constexpr (MODE == CHAIN_Y) put_half<T, NT>(sh.x[c].y[i & 1], t, lane, z[c]);
         }
         meet();
         // the state behind the chunk

@@ -23,9 +23,10 @@
 // added in fp64, in powers of two; a g below -1e5 counts as that.
 //
 // Numbers.  As in the scan, q, k and dO enter the bf16 matrix instructions as
-// they are and what is computed on the way (states, Z, U, N) as the sum of three
-// bf16 numbers: states come out with fp32's digits.  fp32 calls run on the fp32
-// matrix instructions.
+// they are and what is computed on the way (states, Z, U, N, M) as the sum of three
+// bf16 numbers: states come out with fp32's digits, and y with its own where its terms
+// cancel.  (Two terms of what only y reads took 7% less of a prompt's time.)  fp32 calls
+// run on the fp32 matrix instructions.
 //
 // delta_prepare_kernel does what a chunk can do without its state and leaves the
 // operands of the matrix instructions in the workspace, each as the 64 lanes
@@ -36,8 +37,8 @@
 // come out as 8 consecutive keys, which K's and Q's rows hold.
 //
 // Measured in bf16, heads of 128 channels and 128 keys, 4096 tokens: preparation 32 us
-// (32 heads on 16 of keys; 95 MB, 3 TB/s, two workgroups a compute unit), y 110 us, 1.7 us
-// a chunk; gradient (16 heads) preparation 38, states 140, chunks 135 us.
+// (32 heads on 16 of keys; 95 MB, 3 TB/s, two workgroups a compute unit), y 119 us, 1.85
+// us a chunk; gradient (16 heads) preparation 38, states 140, chunks 138 us.
 #pragma once
 
 #include "seq_frags.h"
@@ -79,11 +80,9 @@ template <typename T, int SP> constexpr int64_t keys_bytes(bool grad)
 {
     return frags_bytes<T, SP>(grad) + (grad ? 2 * kDQ * kDQ * 4 : 0);
 }
-// what a head adds: -N beta of three terms, M beta of two; gradient: -N beta, (-beta N)^T and M^T of three terms
+// what a head adds, in terms: -N beta and M beta; gradient: -N beta, (-beta N)^T and M^T
 template <typename T> constexpr int kN = 3;
 template <> constexpr int kN<float> = 1;
-template <typename T> constexpr int kM = 2;
-template <> constexpr int kM<float> = 1;
 struct ChunkScalars {
     float from_start[kDQ];      // e^{c_i}
     float beta[kDQ];
@@ -95,7 +94,7 @@ constexpr int kRows = 1024;     // bytes of ChunkScalars that the passes over th
 // forward: ChunkScalars' first kilobyte, N, M; gradient: ChunkScalars, N, N^T, M^T
 template <typename T> constexpr int64_t head_bytes(bool grad)
 {
-    return grad ? (int64_t)sizeof(ChunkScalars) + 3 * kN<T> * kTri * kFrag<T> : kRows + (int64_t)(kN<T> + kM<T>) * kTri * kFrag<T>;
+    return grad ? (int64_t)sizeof(ChunkScalars) + 3 * kN<T> * kTri * kFrag<T> : kRows + (int64_t)2 * kN<T> * kTri * kFrag<T>;
 }
 
 // The states of a chunk, and its rows, with 4 KB and 256 bytes between those of two
@@ -299,10 +298,10 @@ __global__ void __launch_bounds__(256, SP <= 128 ? 2 : 1) delta_prepare_kernel(D
 #pragma unroll
             for (int P = 0; P < 2; ++P) {
                 if (2 * P > w) continue;
-                Split<T, kM<T>> s;
+                Split<T, kN<T>> s;
                 stack(mm[2 * P], mm[2 * P + 1], s);
 #pragma unroll
-                for (int e = 0; e < kM<T>; ++e) put_frag(at + (kTri * kN<T> + lower(w, P) * kM<T> + e) * kFrag<T>, lane, s.f[e]);
+                for (int e = 0; e < kN<T>; ++e) put_frag(at + (kTri * kN<T> + lower(w, P) * kN<T> + e) * kFrag<T>, lane, s.f[e]);
             }
         }
         // column l16 of (1 + beta T_ww)^-1, by forward substitution in this wave's own block
@@ -412,8 +411,8 @@ SEQ_DEV int64_t unit_of(int64_t block, int64_t units)
 // ahead: no other wave needs them.  dO, dV and U go through LDS, split into their terms
 // once, their rows fetched a block of channels ahead.
 //
-// 1024 chunks of 128 channels and keys in bf16 take 135 us: 290 KB a chunk, 2.2 TB/s.  One
-// workgroup of eight waves fits a compute unit (256 registers a thread, 126 KB of LDS).
+// 1024 chunks of 128 channels and keys in bf16 take 138 us: 290 KB a chunk, 2.1 TB/s.  One
+// workgroup of eight waves fits a compute unit (256 registers a thread, 147 KB of LDS).
 // A workgroup that went from chunk to chunk and loaded the next one's first rows beside
 // the last phases of this one took 147 us, its registers spilled; the products of keys
 // and queries, taken here once a chunk instead of from the preparation, 150.  With 256 keys
@@ -425,7 +424,7 @@ template <typename T, int SP> struct GradShape {
     static constexpr int PB = 64;                                    // channels at a time
     static constexpr int TT = (10 + NW - 1) / NW;                    // triangular tiles of a wave
     static constexpr int LD = PB + Frag<T>::PAD, ML = kDQ + Frag<T>::PAD;
-    static constexpr int NL = kM<T>;                                 // terms of D o Gamma and W o Gamma
+    static constexpr int NL = kN<T>;                                 // terms of D o Gamma and W o Gamma
 };
 template <typename T, int SP> struct GradShared {
     typedef GradShape<T, SP> G;

@@ -5,8 +5,7 @@ ragged and strided batches, keys that repeat, decays that clear the state.
 Tolerances.  A result of type T is rounded once: half a step, 2^-8 (bf16) or
 2^-24 (fp32) of its value.  Before that an error is at most c times the scale that
 the reference gives (norms of what the tokens add): operands computed on the way
-are off by 2^-16 at most (two bf16 terms, where y is rounded to bf16 itself) or
-2^-23 (three); sums over 256 keys, 64 tokens and the chunk's triangular system
+are off by 2^-16 at most (two bf16 terms; the kernels have three, 2^-23); sums over 256 keys, 64 tokens and the chunk's triangular system
 add (256 + 64 + 64) 2^-24 < 2^-15; a decay is the exponential of a rounded
 difference, 2^-24 of itself up to 2^7, two of them 2^-16.  Together under 2^-14.
 """
