@@ -51,8 +51,8 @@ template <typename T, int SP, ChainMode MODE, int CB> struct ChainShared {
 // KB kilobytes of memory to LDS, by the helpers.  The loads are written out: the
 // compiler, which cannot see what they write, would wait for them before any read of
 // LDS.  K and Q come as the preparation laid them out: from their rows, 64 bytes of
-// each at a time, y took 128 us instead of 110 (32 heads, 4096 tokens) and the
-// preparation 31 instead of 32.
+// each at a time, y took 18 us of 110 more (32 heads, 4096 tokens) and the preparation
+// 1 of 32 less.
 template <int KB> SEQ_DEV void fetch(const char *from, char *to, int wave, int lane)
 {
     const i32x4_t buf = uniform_rsrc(buffer_rsrc(from, KB * 1024));

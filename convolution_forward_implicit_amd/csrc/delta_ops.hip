@@ -47,7 +47,8 @@ int64_t state_grid(int64_t units) { return (units + 7) / 8 * 8; }
 // workgroups than compute units, each of which holds one: both blocks go through the
 // chunk's barriers and share its loads of K and N.  bf16, 128 keys: 512 blocks of
 // 4096 tokens 243 -> 181 us, both directions of 256 blocks of 2048 157 -> 138; where there
-// are compute units for every block a block each takes 110 us, two blocks each 181.
+// are compute units for every block a block each takes 110 us, two blocks each 181 (what
+// y alone reads in two terms).
 template <typename T, int SP, typename F> void paired(DeltaParams &p, int directions, F launch)
 {
     if constexpr (kMostBlocks<T, SP> == 2) {
