@@ -72,19 +72,15 @@ def test_aligned_keys(S, dtype):
 
 
 def test_offsets_past_32_bits():
-    """Sequences 2^31 elements apart: the last one's rows, and the step's."""
-    N, L, H, P, G, S = 3, 5, 2, 32, 1, 32
-    far = 1 << 23                                   # a row's stride; rows of a sequence are L of them apart
-    p = _plan(N, 64 * 3, H, P, G, S, "bf16")
-    L = 64 * 3
+    """Rows 16 MB apart, all in one tensor: those of the last sequence lie past the 2^32nd element."""
+    N, L, H, P, G, S = 3, 192, 2, 32, 1, 32
+    far = 1 << 23
     a, _, _ = _case(N, L, H, P, G, S, "bf16", False, None, 2)
     v = _gpu(a)
+    p = _plan(N, L, H, P, G, S, "bf16")
     want = p(**v)
-    base = torch.zeros(N * L * far, dtype=torch.bfloat16, device=DEV)       # 9.7 GB
-    assert base.numel() > 2 ** 32
-    wide = base.view(N, L, far)
-    q, k, x = wide[..., :S], wide[..., S:2 * S], wide[..., 2 * S:2 * S + H * P]
-    y = wide[..., 512:512 + H * P]
+    wide = torch.zeros(N * L * far, dtype=torch.bfloat16, device=DEV).view(N, L, far)       # 9.7 GB
+    q, k, x, y = wide[..., :S], wide[..., S:2 * S], wide[..., 2 * S:2 * S + H * P], wide[..., 512:512 + H * P]
     q.copy_(v["q"].flatten(2)), k.copy_(v["k"].flatten(2)), x.copy_(v["v"].flatten(2))
     got = p(q.unflatten(-1, (G, S)), k.unflatten(-1, (G, S)), x.unflatten(-1, (H, P)), v["g"], v["beta"],
             out=y.unflatten(-1, (H, P)))
