@@ -185,12 +185,13 @@ template <int LANES, typename F> SEQ_DEV void join_parts(int n, F &&get, double 
     m2 = left < 0.0 ? 0.0 : left;       // a NaN stays one
 }
 
-// (count, mean, squares) joined with a batch of `b` values of mean bm and squares bs
+// (count, mean, squares) joined with a batch of `b` values of mean bm and squares bs.  d is a mean itself while the
+// count is 0: squared it may be infinite, and infinity times 0 no number.
 SEQ_DEV void join_batch(float &cnt, float &mean, float &m2, float b, float bm, float bs)
 {
     const float all = cnt + b, d = bm - mean, f = all > 0.0f ? b / all : 0.0f;
     mean = fmaf(d, f, mean);
-    m2 += fmaf(d * d, cnt * f, bs);
+    m2 += fmaf(d * (cnt * f), d, bs);
     cnt = all;
 }
 

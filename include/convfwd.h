@@ -606,6 +606,8 @@ const char *conv_delta_describe(const conv_delta_plan_t *plan);
  * behind a sample's length are not read and count for nothing, their y and gradients
  * are zeros.  Statistics and sums are fp32 and more, squares are summed around a
  * mean, the result is rounded once.  A NaN or an infinity reaches its whole group.
+ * Sums of squares have fp32's range: those of x - mean (center = 0, each token by
+ * itself: of x) must stay below 2^128, which values up to 2^48 do in any number.
  *
  * Partial sums go through a caller-owned device workspace (16-byte aligned; the
  * size may be 0, then it may be NULL) and are added in a fixed order.  Calls that

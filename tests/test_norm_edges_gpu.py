@@ -1,0 +1,36 @@
+"""The group norm on the GPU at the ends of its range: means whose square is no fp32 number,
+sums of thousands of equal terms a thread.  Reference: oracle/norm.py.
+"""
+import pytest
+import torch
+
+from oracle import norm as ref
+from test_norm_gpu import C, CG, DEV, HALF, TYPE, _gpu, _near, _plan
+
+pytestmark = pytest.mark.gpu
+
+
+# N, L, G, C, per_token: several batches a thread, a row wider than a workgroup, one row, tokens in registers, tokens
+# that are samples of their own
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("mean", [2e19, -2e19])
+@pytest.mark.parametrize("case", [(2, 300, 3, 40, False), (1, 9, 1, 2050, False), (3, 1, 2, 64, False), (2, 5, 2, 64, True),
+                                  (1, 3, 1, 4100, True)], ids=str)
+def test_means_whose_square_overflows(case, mean, dtype):
+    """Only what is left of the mean is squared: 2e19 squared is beyond fp32, half of 2^-7 of it squared is 6e33 and
+    12000 of these 7e37.  Both types hold the two values."""
+    N, L, G, Ch, per_token = case
+    g = torch.Generator().manual_seed(L)
+    t = TYPE[dtype]
+    a = dict(x=(mean * (1 + 2.0 ** -7 * torch.randint(0, 2, (N, L, G, Ch), generator=g))).to(t),
+             w=(1 + 0.3 * torch.randn(G, Ch, generator=g)).to(t), bias=torch.randn(G, Ch, generator=g).to(t), gate=None,
+             lengths=None)
+    dy = torch.randn(N, L, G, Ch, generator=g).to(t)
+    kw = dict(act="silu", per_token=per_token)
+    p = _plan(N, L, G, Ch, dtype, a, **kw)
+    y, my = ref.norm(**a, **kw)
+    _near(p(**_gpu(a)), y, my, HALF[dtype], C, "y")
+    want, mag = ref.norm_grad(dy, **a, **kw)
+    for k, got in p.backward(dy.to(DEV), **_gpu(a)).items():
+        if got is not None:
+            _near(got, want[k], mag[k], HALF[dtype], CG, k)
