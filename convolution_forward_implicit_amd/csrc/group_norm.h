@@ -32,7 +32,7 @@
 // fp64, always in the same order.
 #pragma once
 
-#include "seq_frags.h"
+#include "seq_common.h"
 
 namespace convfwd {
 
@@ -317,13 +317,23 @@ template <typename T, int V> SEQ_DEV void norm_out(const NormParams &p, const fl
     }
 }
 
-// Rows row, row + step, .. of a thread's channels, as they are; in place of those that do not count a row that is
-// there: without a branch the loads are all under way at once.
+// Zeros in a slab's rows of a sample none of whose rows count: there is none that a Batch could read instead.
+template <typename T, int V> SEQ_DEV void norm_clear(const NormParams &p, const NormShare &s, void *out, int64_t ld)
+{
+    const float zeros[V] = {};
+    for (int col = s.col; col < s.wide; col += 256) {
+        T *g = (T *)out + s.row0 * ld + (int64_t)s.g0 * p.C + col * V;
+        for (int64_t row = s.first + s.r0; row < s.last; row += s.step) stream_f32<T, V>(g + row * ld, zeros);
+    }
+}
+
+// Rows row, row + step, .. of a thread's channels, as they are; in place of those that do not count the last that
+// does (live > 0): without a branch the loads are all under way at once.
 template <typename T, int V> struct Batch {
     typename Pack<T, V>::type q[kNormBatch];
     SEQ_DEV void load(const T *x, int64_t ld, int64_t row, int step, int64_t live)
     {
-        const int last = live > 0 ? (int)live - 1 : 0;
+        const int last = (int)live - 1;
 #pragma unroll
         for (int e = 0; e < kNormBatch; ++e) {
             const int r = (int)row + e * step;
@@ -341,6 +351,7 @@ template <typename T, int V> __global__ void __launch_bounds__(256) gnorm_apply_
 {
     const NormShare s = norm_share<V>(p, blockIdx.x);
     const int64_t first = s.first + s.r0;
+    if (s.live <= 0) return norm_clear<T, V>(p, s, p.y, p.y_ld);
     Batch<T, V> vb, zb;
     for (int col = s.col; col < s.wide; col += 256) {
         const int64_t at = (int64_t)s.g0 * p.C + col * V;
@@ -537,6 +548,11 @@ template <typename T, int V> __global__ void __launch_bounds__(256) gnorm_grad_k
 {
     const NormShare s = norm_share<V>(p, blockIdx.x);
     const int64_t first = s.first + s.r0;
+    if (s.live <= 0) {
+        norm_clear<T, V>(p, s, p.dx, p.dx_ld);
+        if (p.gate) norm_clear<T, V>(p, s, p.dgate, p.dgate_ld);
+        return;
+    }
     Batch<T, V> vb, zb, db;
     for (int col = s.col; col < s.wide; col += 256) {
         const int64_t at = (int64_t)s.g0 * p.C + col * V, g = s.n * p.G + s.g0 + col / s.cv;
