@@ -20,6 +20,7 @@ struct conv_gnorm_plan {
     int64_t esz;
     int64_t samples, rows;               // that share statistics: N of L rows, or N L of one
     NormSlabs slabs, token_fwd, token_bwd;
+    bool by_slabs;                       // the passes over slabs can be launched
     int64_t ws_bytes, bwd_ws_bytes, o_moments, o_sums, o_group, o_pulls;
     char text[256];
 };
@@ -133,7 +134,7 @@ conv_status_t run_norm(const conv_gnorm_plan &pl, NormParams &p, const Rows *vec
     const int64_t reduce = grad ? ceil_div(d.G * d.C, 16) : 0;
     // the sums of dw share their launch with those of the samples' groups
     const double joins = grad && !tokens ? (double)pl.samples * d.G / (kReduceThreads / 64) + 1 : 0.0;
-    if (!one_launch(grid, 256) || !one_launch((double)reduce + joins, kReduceThreads))
+    if ((!tokens && !pl.by_slabs) || !one_launch(grid, 256) || !one_launch((double)reduce + joins, kReduceThreads))
         return fail(CONV_ERR_UNSUPPORTED, "N x L x G x C is too large for one launch");
     (void)hipGetLastError();
     if (d.dtype == CONV_DT_BF16) {
@@ -175,6 +176,8 @@ conv_status_t conv_gnorm_create(const conv_gnorm_desc_t *desc, conv_gnorm_plan_t
     const int64_t esz = d.dtype == CONV_DT_BF16 ? 2 : 4;
     const int V = widest(d.C, esz, [](int) { return true; });
     const int64_t tokens = d.N * d.L;
+    if ((double)tokens * d.G * d.C * 8 >= kMaxBytes)
+        return fail(CONV_ERR_UNSUPPORTED, "N x L x G x C is too large for one launch");
     conv_gnorm_plan pl{};
     pl.desc = d;
     pl.esz = esz;
@@ -186,14 +189,15 @@ conv_status_t conv_gnorm_create(const conv_gnorm_desc_t *desc, conv_gnorm_plan_t
     pl.slabs = split_rows(pl.samples, pl.rows, rows.blocks, rows.step, 512);
     pl.token_fwd = split_rows(1, tokens, tok.blocks, tok.step * (tok.R == 1 ? 4 : 2), 2048);
     pl.token_bwd = split_rows(1, tokens, tok.blocks, tok.step * (tok.R == 1 ? 2 : 1), 512);
-    const double parts = (double)pl.samples * pl.slabs.count, W = (double)d.G * d.C;
-    if (parts * W * 8 >= kMaxBytes || !one_launch(parts, 256) ||
-        !one_launch((double)pl.samples * d.G, 64))
+    // Tokens whose groups stay in registers need no slabs: their plan is made also where a launch over slabs could not
+    // take their number, and a call whose tensors do not allow the vectors for it is refused.
+    pl.by_slabs = one_launch((double)pl.samples * pl.slabs.count, 256) && one_launch((double)pl.samples * d.G, 64);
+    if (!pl.by_slabs && !in_registers(d, V))
         return fail(CONV_ERR_UNSUPPORTED, "N x L x G x C is too large for one launch");
     // What a call needs goes by the vectors that its tensors allow: a token's group in registers needs the sums of its
     // slabs only.
     const bool narrow = in_registers(d, 1);
-    const int64_t n = narrow ? 0 : pl.samples * pl.slabs.count;
+    const int64_t n = narrow || !pl.by_slabs ? 0 : pl.samples * pl.slabs.count;
     const int64_t sums = std::max(n, in_registers(d, V) ? pl.token_bwd.count : 0);
     const int64_t each = n > 0 ? up(pl.samples * d.G * 8) : 0;      // two numbers of every sample's groups
     pl.o_moments = up(n * d.G * 8);

@@ -34,3 +34,29 @@ def test_means_whose_square_overflows(case, mean, dtype):
     for k, got in p.backward(dy.to(DEV), **_gpu(a)).items():
         if got is not None:
             _near(got, want[k], mag[k], HALF[dtype], CG, k)
+
+
+@pytest.mark.parametrize("dims", [(1, (1 << 21) + 5, 32, 4), (3, (1 << 23) + 7, 1, 8)], ids=str)
+def test_more_tokens_than_samples_could_be(dims):
+    """Each token by itself: the first and the last tokens as in a call of their own, forward and gradient, padded too;
+    dw and dbias as the sums of the terms.  bf16 tensors of one sign in dy."""
+    N, L, G, Ch = dims
+    n = 300
+    g = torch.Generator(DEV).manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV).to(torch.bfloat16)
+    x, dy, w, b = r(N, L, G, Ch), r(N, L, G, Ch).abs(), r(G, Ch), r(G, Ch)
+    lengths = torch.full((N,), L, dtype=torch.int32, device=DEV)
+    lengths[-1] = L - 100
+    a = dict(bias=0, gate=None)
+    p, q = (_plan(N, m, G, Ch, "bf16", a, per_token=True) for m in (L, n))
+    y, got = p(x, w, b, lengths=lengths), p.backward(dy, x, w, b, lengths=lengths)
+    for lo in (0, L - n):
+        part = slice(lo, lo + n)
+        short = (lengths - lo).clamp(max=n)
+        cut, cdy = x[:, part].contiguous(), dy[:, part].contiguous()
+        assert torch.equal(y[:, part], q(cut, w, b, lengths=short))
+        assert torch.equal(got["dx"][:, part], q.backward(cdy, cut, w, b, lengths=short)["dx"])
+    # the terms are dy, at most 512 of a thread in fp32: 2^-15 of their sum, and the result's rounding
+    keep = torch.arange(L, device=DEV) < lengths[:, None]
+    db = sum((dy[i].double() * keep[i, :, None, None]).sum(0) for i in range(N))
+    assert ((got["dbias"].double() - db).abs() <= (2.0 ** -8 * (1 + 2 ** -8) + 2.0 ** -15) * db).all()
