@@ -196,6 +196,31 @@ SEQ_DEV void join_batch(float &cnt, float &mean, float &m2, float b, float bm, f
 }
 
 constexpr int kNormBatch = 4;       // rows that a thread has under way
+// Rows of a slab that a thread may have: it adds their terms up in fp32, and equal terms are rounded the same way every
+// time (4096 of 1 + 2^-13 lost 6e-5 of their sum, 16384 equal rows 4e-5 of their squares).  Slabs, and a thread's
+// columns of a row wider than a workgroup, are joined in fp64.
+constexpr int kNormChain = 64;
+
+// (count, mean, squares) of several columns of a thread, around the first one's mean
+struct NormColumns {
+    float mean0;
+    double cnt = 0.0, sum = 0.0, sq = 0.0;
+    SEQ_DEV void add(float c, float mean, float m2)
+    {
+        if (cnt == 0.0) mean0 = mean;
+        const double d = (double)mean - (double)mean0, cd = (double)c * d;
+        cnt += (double)c;
+        sum += cd;
+        sq += fma(cd, d, (double)m2);
+    }
+    SEQ_DEV void get(float &c, float &mean, float &m2) const
+    {
+        const double off = sum / cnt, left = fma(-off, sum, sq);
+        c = (float)cnt;
+        mean = (float)((double)mean0 + off);
+        m2 = left < 0.0 ? 0.0f : (float)left;       // a NaN stays one
+    }
+};
 constexpr int kReduceThreads = 1024;    // 16 channels' slabs, by 64 threads each
 
 template <typename T, int V> __global__ void __launch_bounds__(256) gnorm_stats_kernel(NormParams p)
@@ -204,6 +229,7 @@ template <typename T, int V> __global__ void __launch_bounds__(256) gnorm_stats_
     const NormShare s = norm_share<V>(p, blockIdx.x);
     const int64_t first = s.first;
     float cnt = 0.0f, mean = 0.0f, m2 = 0.0f;
+    NormColumns all;
     for (int col = s.col; col < s.wide; col += 256) {
         const T *x = (const T *)p.x + s.row0 * p.x_ld + (int64_t)s.g0 * p.C + col * V;
         for (int64_t r = first + s.r0; r < s.live; r += kNormBatch * s.step) {
@@ -236,7 +262,12 @@ template <typename T, int V> __global__ void __launch_bounds__(256) gnorm_stats_
             }
             join_batch(cnt, mean, m2, n, bm, sq);
         }
+        if (s.wide > 256 && cnt > 0.0f) {
+            all.add(cnt, mean, m2);
+            cnt = mean = m2 = 0.0f;
+        }
     }
+    if (all.cnt > 0.0) all.get(cnt, mean, m2);
     part[0][threadIdx.x] = cnt;
     part[1][threadIdx.x] = mean;
     part[2][threadIdx.x] = m2;

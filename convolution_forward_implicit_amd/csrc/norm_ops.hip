@@ -19,7 +19,7 @@ struct conv_gnorm_plan {
     conv_gnorm_desc_t desc;
     int64_t esz;
     int64_t samples, rows;               // that share statistics: N of L rows, or N L of one
-    NormSlabs slabs, token_fwd, token_bwd;
+    NormSlabs token_fwd;                 // of each token in registers, forward
     bool by_slabs;                       // the passes over slabs can be launched
     int64_t ws_bytes, bwd_ws_bytes, o_moments, o_sums, o_group, o_pulls;
     char text[256];
@@ -65,13 +65,27 @@ Share over_tokens(const conv_gnorm_desc_t &d, int V)
     return {lanes, R <= 2 ? R : 4, (int)groups, (int)ceil_div(d.G, groups), (int)(slots / groups)};
 }
 
-// `rows` rows of each of `samples` so that there are about `want` workgroups of `unit` rows and more.
-NormSlabs split_rows(int64_t samples, int64_t rows, int64_t blocks, int64_t unit, int64_t want)
+// `rows` rows of each of `samples` so that there are about `want` workgroups of `unit` rows and more, but not more rows
+// than `most`.
+NormSlabs split_rows(int64_t samples, int64_t rows, int64_t blocks, int64_t unit, int64_t want, int64_t most)
 {
     if (samples == 0 || rows == 0) return {0, 1};
     const int64_t n = std::max<int64_t>(1, want / std::max<int64_t>(1, samples * blocks));
-    const int64_t each = ceil_div(ceil_div(rows, n), unit) * unit;
+    const int64_t each = std::min(ceil_div(ceil_div(rows, n), unit) * unit, most);
     return {ceil_div(rows, each), each};
+}
+// The slabs of a call in vectors of V: of its samples' rows, or, of a gradient whose groups are in registers, of its
+// tokens; a thread has kNormChain rows of one at most.  Up to that there are two workgroups a compute unit for a pass
+// over rows (8 x 3136 x 256 channels, forward and gradient: 17 and 34 us; with one 19 and 37, with four 18 and 40).
+NormSlabs row_slabs(const conv_gnorm_desc_t &d, int V)
+{
+    const Share s = over_rows(d, V);
+    return split_rows(d.per_token ? d.N * d.L : d.N, d.per_token ? 1 : d.L, s.blocks, s.step, 512, kNormChain * s.step);
+}
+NormSlabs token_slabs(const conv_gnorm_desc_t &d, int V)
+{
+    const Share s = over_tokens(d, V);
+    return split_rows(1, d.N * d.L, s.blocks, s.step * (s.R == 1 ? 2 : 1), 512, kNormChain * s.step);
 }
 
 template <typename T, int V> void launch_rows(NormParams p, bool grad, int64_t grid, int64_t reduce, hipStream_t s)
@@ -120,7 +134,7 @@ conv_status_t run_norm(const conv_gnorm_plan &pl, NormParams &p, const Rows *vec
     });
     const bool tokens = in_registers(d, V);
     const Share sh = tokens ? over_tokens(d, V) : over_rows(d, V);
-    const NormSlabs sl = !tokens ? pl.slabs : grad ? pl.token_bwd : pl.token_fwd;
+    const NormSlabs sl = !tokens ? row_slabs(d, V) : grad ? token_slabs(d, V) : pl.token_fwd;
     p.samples = pl.samples; p.rows = pl.rows; p.L = d.L; p.tokens = d.N * d.L;
     p.G = (int)d.G; p.C = (int)d.C; p.act = d.act; p.center = d.center; p.eps = (float)d.eps;
     p.slabs = sl.count; p.slab = sl.rows;
@@ -183,22 +197,22 @@ conv_status_t conv_gnorm_create(const conv_gnorm_desc_t *desc, conv_gnorm_plan_t
     pl.esz = esz;
     pl.samples = d.per_token ? tokens : d.N;
     pl.rows = d.per_token ? 1 : d.L;
-    // Two workgroups a compute unit for a pass over rows (8 x 3136 x 256 channels, forward and gradient: 17 and 34 us;
-    // with one 19 and 37, with four 18 and 40).
-    const Share rows = over_rows(d, V), tok = over_tokens(d, V);
-    pl.slabs = split_rows(pl.samples, pl.rows, rows.blocks, rows.step, 512);
-    pl.token_fwd = split_rows(1, tokens, tok.blocks, tok.step * (tok.R == 1 ? 4 : 2), 2048);
-    pl.token_bwd = split_rows(1, tokens, tok.blocks, tok.step * (tok.R == 1 ? 2 : 1), 512);
+    const Share tok = over_tokens(d, V);
+    pl.token_fwd = split_rows(1, tokens, tok.blocks, tok.step * (tok.R == 1 ? 4 : 2), 2048, tokens);
+    const NormSlabs slabs = row_slabs(d, V);
     // Tokens whose groups stay in registers need no slabs: their plan is made also where a launch over slabs could not
     // take their number, and a call whose tensors do not allow the vectors for it is refused.
-    pl.by_slabs = one_launch((double)pl.samples * pl.slabs.count, 256) && one_launch((double)pl.samples * d.G, 64);
+    pl.by_slabs = one_launch((double)pl.samples * slabs.count, 256) && one_launch((double)pl.samples * d.G, 64);
     if (!pl.by_slabs && !in_registers(d, V))
         return fail(CONV_ERR_UNSUPPORTED, "N x L x G x C is too large for one launch");
     // What a call needs goes by the vectors that its tensors allow: a token's group in registers needs the sums of its
     // slabs only.
-    const bool narrow = in_registers(d, 1);
-    const int64_t n = narrow || !pl.by_slabs ? 0 : pl.samples * pl.slabs.count;
-    const int64_t sums = std::max(n, in_registers(d, V) ? pl.token_bwd.count : 0);
+    int64_t n = 0, sums = 0;
+    for (int v = V; v >= 1; v /= 2) {
+        if (in_registers(d, v)) sums = std::max(sums, token_slabs(d, v).count);
+        else if (pl.by_slabs) n = std::max(n, pl.samples * row_slabs(d, v).count);
+    }
+    sums = std::max(sums, n);
     const int64_t each = n > 0 ? up(pl.samples * d.G * 8) : 0;      // two numbers of every sample's groups
     pl.o_moments = up(n * d.G * 8);
     pl.ws_bytes = pl.o_moments + each;
@@ -210,7 +224,7 @@ conv_status_t conv_gnorm_create(const conv_gnorm_desc_t *desc, conv_gnorm_plan_t
              d.dtype == CONV_DT_BF16 ? "bf16" : "f32", (long long)d.N, (long long)d.L, (long long)d.G, (long long)d.C,
              d.has_bias ? " bias" : "", d.act == CONV_NORM_ACT_SILU ? " silu" : d.act == CONV_NORM_ACT_GELU ? " gelu" : "",
              d.gated ? " gated" : "", d.center ? "" : " uncentered", d.per_token ? "each token" : "each sample",
-             (long long)(d.per_token ? pl.token_fwd : pl.slabs).count, (long long)(d.per_token ? pl.token_fwd : pl.slabs).rows);
+             (long long)(d.per_token ? pl.token_fwd : slabs).count, (long long)(d.per_token ? pl.token_fwd : slabs).rows);
     conv_gnorm_plan *made = new (std::nothrow) conv_gnorm_plan(pl);
     if (!made) return fail(CONV_ERR_NOMEM, "plan allocation failed");
     if (getenv("CONVFWD_LOG")) fprintf(stderr, "convfwd: %s\n", made->text);
