@@ -357,9 +357,10 @@ conv_status_t conv_delta_bwd_run(const conv_delta_plan_t *plan, const conv_delta
     }
     const Rows vec[] = {in[1], in[2]};
     p.vec = delta_vector(*plan, vec, 2);
+    // the sums over slices fit any launch: there are some only where N K G is at most 128
     const double groups = (double)d.N * plan->K * d.G;
     if (!one_launch(2.0 * (double)state_grid(d.N * d.H * p.blocks), kChainThreads) || !one_launch(groups * plan->slices, 256) ||
-        !one_launch(groups * plan->grad_slices, 512) || !one_launch((double)rows * (double)gs / 256 + 1, 256))
+        !one_launch(groups * plan->grad_slices, 512))
         return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
     hipStream_t s = (hipStream_t)stream;
     (void)hipGetLastError();
