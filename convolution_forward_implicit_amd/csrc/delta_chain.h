@@ -530,9 +530,9 @@ SEQ_DEV void delta_chain(const DeltaParams &p, int64_t unit, ChainShared<T, SP, 
 
 constexpr int kChainThreads = 64 * (4 + kHelpers);
 
-// Blocks of 16 channels that a workgroup may have: two where the exchange of both leaves
-// room for a chunk of K and N.
-template <typename T, int SP> constexpr int kMostBlocks = SP <= 128 ? 2 : 1;
+// Keys up to which a workgroup may have two blocks of 16 channels: the exchange of both
+// leaves room for a chunk of K and N.
+constexpr int kMostPaired = 128;
 
 template <typename T, int SP, int CB> __global__ void __launch_bounds__(kChainThreads) delta_y_kernel(DeltaParams p)
 {

@@ -48,11 +48,20 @@ int64_t state_grid(int64_t units) { return (units + 7) / 8 * 8; }
 // chunk's barriers and share its loads of K and N.  bf16, 128 keys: 512 blocks of
 // 4096 tokens 243 -> 181 us, both directions of 256 blocks of 2048 157 -> 138; where there
 // are compute units for every block a block each takes 110 us, two blocks each 181 (what
-// y alone reads in two terms).
+// y alone reads in two terms).  Above 128 keys there is no room for two.
+bool two_blocks(int SP, double units) { return SP <= kMostPaired && units > 256; }
+
+// Workgroups of a pass over the states of N H heads of `blocks` blocks in so many directions.
+double chain_grid(int SP, int directions, int64_t heads, int64_t blocks)
+{
+    if (two_blocks(SP, (double)directions * heads * blocks)) blocks = (blocks + 1) / 2;
+    return (double)directions * state_grid(heads * blocks);
+}
+
 template <typename T, int SP, typename F> void paired(DeltaParams &p, int directions, F launch)
 {
-    if constexpr (kMostBlocks<T, SP> == 2) {
-        if ((double)directions * p.N * p.H * p.blocks > 256) {
+    if constexpr (SP <= kMostPaired) {
+        if (two_blocks(SP, (double)directions * p.N * p.H * p.blocks)) {
             p.blocks = (p.blocks + 1) / 2;
             return launch(std::integral_constant<int, 2>());
         }
@@ -168,10 +177,11 @@ conv_status_t conv_delta_create(const conv_delta_desc_t *desc, conv_delta_plan_t
     pl->K = (int)((d.L + kDQ - 1) / kDQ);
     pl->blocks = (int)((d.P + 15) / 16);
     // What neither a prompt nor a step could launch; every call checks its own form.
-    const double units = (double)d.N * d.H * pl->blocks, chunks = (double)d.N * pl->K;
+    const double chunks = (double)d.N * pl->K;
     const double ws = chunks * ((double)d.G * keys_of(d, pl->SP, true) + (double)d.H * head_of(d, true)) +
                       2.0 * (double)d.N * d.H * pl->K * ((d.P + 31.0) * (pl->SP + kDQ) + 2.0 * kApart) * 4.0;
-    if ((!one_launch(units, kChainThreads) && !one_launch((double)d.N * d.H * step_shape(d).blocks, 256)) || ws >= kMaxBytes) {
+    if ((!one_launch(chain_grid(pl->SP, 1, d.N * d.H, pl->blocks), kChainThreads) &&
+         !one_launch((double)d.N * d.H * step_shape(d).blocks, 256)) || ws >= kMaxBytes) {
         delete pl;
         return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
     }
@@ -284,7 +294,7 @@ static conv_status_t delta_forward_call(const conv_delta_plan_t *plan, const con
     p.heads = (char *)ws + plan->o_heads;
     const Rows vec[] = {in[0], in[1]};
     p.vec = delta_vector(*plan, vec, 2);
-    if (!one_launch((double)state_grid(d.N * d.H * plan->blocks), kChainThreads) ||
+    if (!one_launch(chain_grid(plan->SP, 1, d.N * d.H, plan->blocks), kChainThreads) ||
         !one_launch((double)d.N * plan->K * d.G * plan->slices, 256))
         return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
     if (d.dtype == CONV_DT_BF16) launch_delta<bf16_t>(p, *plan, false, s);
@@ -359,7 +369,7 @@ conv_status_t conv_delta_bwd_run(const conv_delta_plan_t *plan, const conv_delta
     p.vec = delta_vector(*plan, vec, 2);
     // the sums over slices fit any launch: there are some only where N K G is at most 128
     const double groups = (double)d.N * plan->K * d.G;
-    if (!one_launch(2.0 * (double)state_grid(d.N * d.H * p.blocks), kChainThreads) || !one_launch(groups * plan->slices, 256) ||
+    if (!one_launch(chain_grid(plan->SP, 2, d.N * d.H, p.blocks), kChainThreads) || !one_launch(groups * plan->slices, 256) ||
         !one_launch(groups * plan->grad_slices, 512))
         return fail(CONV_ERR_UNSUPPORTED, "N x L x H x P is too large for one launch");
     hipStream_t s = (hipStream_t)stream;

@@ -42,3 +42,13 @@ def _ends(call, dims, dtype, status):
 def test_a_gradient_without_slices_sums_none(dtype, dims):
     """The sums of dq and dk over slices of a group's heads take no launch where there is one slice."""
     _ends(_bwd, dims, dtype, capi.CONV_ERR_HIP)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("call,N", [(_run, (1 << 19) - 1), (_bwd, (1 << 18) - 1)], ids=["prompt", "gradient"])
+def test_two_blocks_a_workgroup_are_one(call, N, dtype):
+    """Up to 128 keys a workgroup takes 32 channels where there are many, and only half as many are launched."""
+    dims = dict(N=N, L=1, H=16, P=32, G=1, S=32)
+    _ends(call, dims, dtype, capi.CONV_ERR_HIP)
+    _ends(call, dict(dims, N=N + 1), dtype, capi.CONV_ERR_UNSUPPORTED)
+    _ends(call, dict(dims, S=129), dtype, capi.CONV_ERR_UNSUPPORTED)
