@@ -4,7 +4,10 @@ only): the definition, token after token, and its gradient written out by hand.
 Next to every result stands what its rounding errors are proportional to.  With
 g <= 0 and beta |k|^2 <= 2 a step takes no norm of the state up, so an error made
 at one token reaches later ones at most as large as it was made: the norms of
-what the tokens add, faded like the state, bound the sum of all of them.
+what the tokens add, faded like the state, bound the sum of all of them.  The same
+holds going back: a token takes the gradient R of the state to e^g (R - beta R k k^T),
+no larger in norm, and its own rounding adds beta |k|^2 |R|.  A product is off by
+either factor's error times the other's norm.
 """
 import torch
 
@@ -66,25 +69,29 @@ def delta_grad(dy, q, k, v, g, beta, scale, state=None, lengths=None, dstate_out
     for t in reversed(range(L)):
         faded, e, S, ms = steps[t]
         on = live[:, t, None].to(F64)
-        kn, qn, vn, b = _norm(k[:, t]), _norm(q[:, t]), _norm(v[:, t]), beta[:, t]
+        kn, qn, vn, b = _norm(k[:, t]), _norm(q[:, t]), _norm(v[:, t]), beta[:, t].abs()
         d["dq"][:, t] = (S * dy[:, t, ..., None]).sum(-2)
         mag["dq"][:, t] = _norm(dy[:, t]) * ms
         R = R + dy[:, t, ..., None] * q[:, t, :, None]
+        # R's own norm and that of its error (what was added so far), e's, the faded state's
         mr = mr + on * _norm(dy[:, t]) * qn
+        rn, en, sn, me = _norm(R, 2), _norm(e), _norm(faded, 2), vn + kn * ms
         rk = (R * k[:, t, :, None]).sum(-1)
         d["dbeta"][:, t] = on * (rk * e).sum(-1)
-        mag["dbeta"][:, t] = on * mr * kn * (vn + kn * ms)
-        d["dv"][:, t] = on[..., None] * b[..., None] * rk
-        mag["dv"][:, t] = on * b.abs() * kn * mr
-        u = b[..., None] * e
+        mag["dbeta"][:, t] = on * kn * (mr * en + rn * me)
+        d["dv"][:, t] = on[..., None] * beta[:, t][..., None] * rk
+        mag["dv"][:, t] = on * b * kn * mr
+        u = beta[:, t][..., None] * e
         d["dk"][:, t] = on[..., None] * ((R * u[..., None]).sum(-2) - (faded * d["dv"][:, t, ..., None]).sum(-2))
-        mag["dk"][:, t] = on * mr * b.abs() * (vn + 2 * kn * ms)
+        mag["dk"][:, t] = on * b * (mr * (en + kn * sn) + rn * (me + kn * ms))
         back = R - d["dv"][:, t, ..., None] * k[:, t, :, None]
         d["dg"][:, t] = on * (back * faded).sum((-1, -2))
-        mag["dg"][:, t] = on * mr * (steps[t - 1][3] if t else m0)
+        # besides, the terms that cross the token's decay are summed: what is added behind it times what was added in
+        # front, which may cancel.  They take the roundings of their own products and decays, an eighth of a state's.
+        mag["dg"][:, t] = on * (mr * sn + rn * ms + mr * ms / 8)
         live4 = live[:, t, None, None, None]
         R = torch.where(live4, back * g[:, t].exp()[..., None, None], R)
-        mr = torch.where(live[:, t, None], (mr + on * b.abs() * kn * kn * mr) * g[:, t].exp(), mr)
+        mr = torch.where(live[:, t, None], (mr + b * kn * kn * rn) * g[:, t].exp(), mr)
     group = lambda x: x.unflatten(2, (G, H // G)).sum(3)
     d["dq"], d["dk"] = group(d["dq"]), group(d["dk"])
     mag["dq"], mag["dk"] = group(mag["dq"])[..., None], group(mag["dk"])[..., None]
