@@ -60,3 +60,51 @@ def test_more_tokens_than_samples_could_be(dims):
     keep = torch.arange(L, device=DEV) < lengths[:, None]
     db = sum((dy[i].double() * keep[i, :, None, None]).sum(0) for i in range(N))
     assert ((got["dbias"].double() - db).abs() <= (2.0 ** -8 * (1 + 2 ** -8) + 2.0 ** -15) * db).all()
+
+
+@pytest.mark.parametrize("dtype,Ch", [("bf16", 520), ("bf16", 2048), ("f32", 260), ("f32", 1024)])
+def test_tokens_in_registers_and_columns_that_are_not(dtype, Ch):
+    """The same plan over aligned tensors, whose groups stay in registers, and over columns from an odd one on, which
+    go through slabs: forward and gradient, the rest of the rows as it was."""
+    N, L, G = 2, 21, 3
+    W, t = G * Ch, TYPE[dtype]
+    g = torch.Generator().manual_seed(Ch)
+    r = lambda *s: torch.randn(*s, generator=g)
+    a = dict(x=r(N, L, G, Ch).to(t), w=(1 + 0.3 * r(G, Ch)).to(t), bias=r(G, Ch).to(t), gate=r(N, L, G, Ch).to(t),
+             lengths=torch.tensor([L, 9], dtype=torch.int32))
+    dy = r(N, L, G, Ch).to(t)
+    kw = dict(act="silu", per_token=True)
+    p = _plan(N, L, G, Ch, dtype, a, **kw)
+    y, my = ref.norm(**a, **kw)
+    want, mag = ref.norm_grad(dy, **a, **kw)
+    v = _gpu(a)
+    _near(p(**v), y, my, HALF[dtype], C, "y")
+    wide = torch.full((N, L, 2 * W + 1), 5.0, dtype=t, device=DEV)
+    x, out = (wide[..., i:i + W].unflatten(-1, (G, Ch)) for i in (1, W + 1))
+    x.copy_(v["x"])
+    _near(p(**dict(v, x=x), out=out), y, my, HALF[dtype], C, "y")
+    for got in (p.backward(dy.to(DEV), **v), p.backward(dy.to(DEV), **dict(v, x=x), out={"dx": out})):
+        for k in want:
+            _near(got[k], want[k], mag[k], HALF[dtype], CG, k)
+    assert (wide[..., 0] == 5).all() and torch.equal(x, v["x"])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("per_token,Ch", [(False, 24), (True, 24), (True, 520)])
+def test_what_is_no_number_reaches_its_group_and_no_other(per_token, Ch, bad):
+    """All of its group's y and dx are NaN; every other group's are what they are without it, to the bit."""
+    N, L, G = 2, 37, 3
+    g = torch.Generator().manual_seed(Ch)
+    x, dy, w = torch.randn(N, L, G, Ch, generator=g), torch.randn(N, L, G, Ch, generator=g).to(DEV), torch.ones(G, Ch, device=DEV)
+    p = _plan(N, L, G, Ch, "f32", dict(bias=None, gate=None), per_token=per_token)
+    out = []
+    for value in (float(x[1, 5, 1, 7]), bad):
+        x[1, 5, 1, 7] = value
+        d = x.to(DEV)
+        out.append((p(d, w), p.backward(dy, d, w)["dx"]))
+    for clean, got in zip(*out):
+        mine = torch.zeros(N, L, G, Ch, dtype=torch.bool, device=DEV)
+        mine[1, 5:6, 1] = True
+        if not per_token:
+            mine[1, :, 1] = True
+        assert torch.isnan(got[mine]).all() and torch.equal(got[~mine], clean[~mine])
