@@ -20,7 +20,10 @@
 //
 // and the rest from S_0, R, Y and E of each chunk by itself (delta_grad_kernel).
 // All exponents are differences of sums, at most 0 for g <= 0.  The sums are
-// added in fp64, in powers of two; a g below -1e5 counts as that.
+// added in fp64, in powers of two; a g below -1e5 counts as that.  A difference is
+// rounded to fp32 for its exponential, which is off by |c_i - c_j| 2^-24 of itself: 2^-20
+// of a decay of e^-11, and less of the largest decay the further one has faded.  (fp32
+// calls are 2.3e-7 off in 2-norm; plain fp32 operations with exponents in 64 bits 1.8e-7.)
 //
 // Numbers.  As in the scan, q, k and dO enter the bf16 matrix instructions as
 // they are and what is computed on the way (states, Z, U, N, M) as the sum of three
@@ -38,7 +41,8 @@
 //
 // Measured in bf16, heads of 128 channels and 128 keys, 4096 tokens: preparation 32 us
 // (32 heads on 16 of keys; 95 MB, 3 TB/s, two workgroups a compute unit), y 119 us, 1.85
-// us a chunk; gradient (16 heads) preparation 38, states 140, chunks 138 us.
+// us a chunk; gradient (16 heads) preparation 39, states 147, chunks 151 us (medians of a
+// trace; the least 36, 139, 140).
 #pragma once
 
 #include "seq_frags.h"
@@ -411,13 +415,13 @@ SEQ_DEV int64_t unit_of(int64_t block, int64_t units)
 // ahead: no other wave needs them.  dO, dV and U go through LDS, split into their terms
 // once, their rows fetched a block of channels ahead.
 //
-// 1024 chunks of 128 channels and keys in bf16 take 138 us: 290 KB a chunk, 2.1 TB/s.  One
+// 1024 chunks of 128 channels and keys in bf16 take 140 us and more: 290 KB a chunk, 2.1 TB/s.  One
 // workgroup of eight waves fits a compute unit (256 registers a thread, 147 KB of LDS).
 // A workgroup that went from chunk to chunk and loaded the next one's first rows beside
 // the last phases of this one took 147 us, its registers spilled; the products of keys
-// and queries, taken here once a chunk instead of from the preparation, 150.  With 256 keys
-// the sums of three products leave too few registers and some 650 bytes a lane go to
-// scratch memory.
+// and queries, taken here once a chunk instead of from the preparation, 150 (against 139 in turn).
+// 128 keys put 12 bytes a lane in scratch memory (fp32 76); with 256 the sums of three products
+// leave too few registers and it is some 650.
 template <typename T, int SP> struct GradShape {
     static constexpr int NW = SP <= 64 ? 4 : 8;                      // waves
     static constexpr int CT = SP / 16 < NW ? 1 : SP / 16 / NW;

@@ -45,10 +45,17 @@ int64_t state_grid(int64_t units) { return (units + 7) / 8 * 8; }
 
 // A workgroup takes one block of 16 channels, or two where there would be more
 // workgroups than compute units, each of which holds one: both blocks go through the
-// chunk's barriers and share its loads of K and N.  bf16, 128 keys: 512 blocks of
-// 4096 tokens 243 -> 181 us, both directions of 256 blocks of 2048 157 -> 138; where there
-// are compute units for every block a block each takes 110 us, two blocks each 181 (what
-// y alone reads in two terms).  Above 128 keys there is no room for two.
+// chunk's barriers and share its loads of K and N.  Above 128 keys there is no room for
+// two.  Whole calls of 2048 tokens in us, a block each | two:
+//
+//   blocks       bf16, 32 keys   64          128         fp32, 32    64          128
+//   256            67 |  92       71 |  91    81 | 105    82 | 118    97 | 139   132 | 186
+//   264           104 |  92      109 |  94   129 | 107   142 | 123   162 | 141   218 | 189
+//   512           115 | 102      126 | 107   148 | 125   154 | 135   182 | 163   256 | 227
+//   gradient, 256 234 | 230      260 | 254   319 | 304   284 | 292   335 | 337   423 | 414
+//   gradient, 512 512 | 446      577 | 498   682 | 590   585 | 529   690 | 615   849 | 751
+//
+// (A gradient's 256 blocks are 512 units, both directions.)
 bool two_blocks(int SP, double units) { return SP <= kMostPaired && units > 256; }
 
 // Workgroups of a pass over the states of N H heads of `blocks` blocks in so many directions.
